@@ -393,6 +393,110 @@ int fa3_decode_attn_gqa_paged(const int8_t* q, const int8_t* k, const int8_t* v,
                               float softmax_scale, void* workspace, size_t workspace_bytes,
                               int32_t* dev_err, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Attention input: per-head RMS norm and position rotation.  FA3 calibrates and
+ * quantizes q and k as attention sees them (msModelSlim FA3量化, 原理 / 算法流程:
+ * the attention activations), that is after a model's per-head norm and its
+ * rotary position embedding; the pages leave those two steps to the model.
+ * For one head row x of D values at position p:
+ *   a = x * (mean(x^2) + eps)^-1/2 * weight        (weight NULL: a = x)
+ *   y1 = a1 * c - a2 * s,  y2 = a2 * c + a1 * s    for each pair (a1, a2) i of the
+ *        first rot_dim values, c = cos_sin[p][i], s = cos_sin[p][rot_dim / 2 + i]
+ *   y  = a for the values from rot_dim on.
+ * Pairs: (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved is non-zero.
+ * cos_sin  float32 [table_len][rot_dim], or NULL: no rotation.
+ * weight   bf16 [D].
+ * Supported: D % 8 == 0, D <= 256; rot_dim % 8 == 0, rot_dim <= D; eps >= 0;
+ *            strides multiples of 4 elements, rows 8-byte aligned; cos_sin
+ *            16-byte aligned.
+ * ------------------------------------------------------------------------ */
+
+/* Norm and rotation to bf16 (out_f32 = 0) or float32 (out_f32 = 1), computed in
+ * float32 and rounded once: the activations that calibration looks at.
+ * q        bf16, row (b, s, h) of q[b*q_sb + s*q_ss + h*q_sh + d], b < B, s < S,
+ *          h < Hq; k likewise with Hkv heads, or NULL (with k_out NULL, Hkv 0).
+ * q_out, k_out  rows by their own strides (for example [B][H][S][D], the layout
+ *          fa3_calibrate_perhead takes), 16-byte aligned, strides multiples of 4;
+ *          q_out may be q itself (bf16, the same strides), k_out k.
+ * pos      int32 [B*S], the position of token (b, s); outside [0, table_len) the
+ *          token is skipped and FA3_DEVERR_POS is set.  May be NULL without a table.
+ * q_weight and k_weight are both given or both NULL (when k is given). */
+int fa3_norm_rope(const uint16_t* q, const uint16_t* k, const uint16_t* q_weight, const uint16_t* k_weight,
+                  float eps, const float* cos_sin, int table_len, int rot_dim, int interleaved, const int32_t* pos,
+                  void* q_out, void* k_out, int out_f32, int B, int S, int Hq, int Hkv, int D,
+                  int64_t q_sb, int64_t q_ss, int64_t q_sh, int64_t k_sb, int64_t k_ss, int64_t k_sh,
+                  int64_t qo_sb, int64_t qo_ss, int64_t qo_sh, int64_t ko_sb, int64_t ko_ss, int64_t ko_sh,
+                  int32_t* dev_err, void* stream);
+
+/* The same on the way into the paged INT8 cache (layout above), in one launch: k is
+ * normed, rotated and quantized, v quantized (fa3_quantize_append's codes), each
+ * appended to its pool, and q, if given, normed, rotated and quantized to q_out.
+ * The new rows of all sequences are packed: rows q_start[b] .. q_start[b+1] - 1
+ * of q, k and v belong to sequence b, and are the last tokens of its context of
+ * kv_lens[b] tokens: row q_start[b] + i has position kv_lens[b] - n_b + i, in the
+ * cache and in cos_sin, n_b = q_start[b+1] - q_start[b].
+ *   code = clamp(round_half_even(y / scale[h]), -127, 127)      (scale 0 -> 0)
+ * of q and k is decided as if y and y / scale were computed in float64.
+ * q        bf16 [n][Hq][D], row stride q_stride elements (heads contiguous), or NULL
+ *          (with q_out and q_weight NULL); k, v  bf16 [n][Hkv][D], row strides k_stride, v_stride.
+ * q_out    int8 [n][Hq][D];  k_cache, v_cache  int8 [num_pages][page_size][Hkv][D].
+ * q_start  int32 [B+1], non-decreasing, within [0, n];  kv_lens  int32 [B], n_b <=
+ *          kv_lens[b] <= max_pages * page_size; otherwise FA3_DEVERR_LENS is set
+ *          and the sequence is skipped.  Rows outside [q_start[0], q_start[B])
+ *          are not read and their q_out is left as it was.
+ * A position past the table sets FA3_DEVERR_POS and skips the row; a block-table
+ * entry outside the pool sets FA3_DEVERR_PAGE and skips its k and v (q_out is
+ * written).  Supported: any page_size >= 1; q_out, k_cache, v_cache 8-byte aligned. */
+int fa3_rope_append_gqa_paged(const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                              const uint16_t* q_weight, const uint16_t* k_weight, float eps,
+                              const float* cos_sin, int table_len, int rot_dim, int interleaved,
+                              const float* q_scale, const float* k_scale, const float* v_scale,
+                              int8_t* q_out, int8_t* k_cache, int8_t* v_cache,
+                              const int32_t* block_table, const int32_t* q_start, const int32_t* kv_lens,
+                              int n, int B, int Hq, int Hkv, int D,
+                              int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                              int num_pages, int page_size, int max_pages, int32_t* dev_err, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Attention of packed new rows with INT8 q, k and v (fa3_prefill_attn_gqa's
+ * arithmetic).  q_start packs the new rows of all sequences as above: from one
+ * row a sequence (a decode step) to whole prompts, in one batch.  Query head h
+ * reads KV head g = h / (Hq / Hkv):
+ *   s[t] = (q[row, h] . k[t, g]) * q_scale[h] * k_scale[g] * softmax_scale
+ *   out[row, h, :] = bf16( v_scale[g] * sum_t softmax(s)_t * v[t, g, :] )
+ * q        int8 [n][Hq][D];  out  bf16 [n][Hq][D].  Rows outside
+ *          [q_start[0], q_start[B]) and those of a sequence with bad lengths
+ *          (FA3_DEVERR_LENS) are left as they were.
+ * Supported: D = 128, Hq / Hkv <= 128; q, k, v, out 16-byte aligned.
+ * workspace  fa3_chunk_workspace_size(n, B, Hq, Hkv, D) bytes, 16-byte aligned
+ *          (partial results of row blocks whose keys are shared out); its
+ *          contents need no initialisation.
+ * ------------------------------------------------------------------------ */
+size_t fa3_chunk_workspace_size(int n, int B, int Hq, int Hkv, int D);
+
+/* A chunk of new tokens over a paged cache that holds them already: row
+ * q_start[b] + i of sequence b attends causally to t <= kv_lens[b] - n_b + i.
+ * kv_lens as for fa3_rope_append_gqa_paged; k, v the pools.  An entry outside the
+ * pool sets FA3_DEVERR_PAGE and reads as zeros (that sequence's output is not valid).
+ * Supported: any page_size >= 1. */
+int fa3_prefill_attn_gqa_paged(const int8_t* q, const int8_t* k, const int8_t* v,
+                               const float* q_scale, const float* k_scale, const float* v_scale,
+                               const int32_t* q_start, const int32_t* kv_lens, const int32_t* block_table,
+                               uint16_t* out, int n, int B, int Hq, int Hkv, int D,
+                               int num_pages, int page_size, int max_pages, float softmax_scale,
+                               void* workspace, size_t workspace_bytes, int32_t* dev_err, void* stream);
+
+/* Cross attention to an encoder's states of another length: every row of sequence b
+ * attends to all of t < enc_lens[b], 0 <= enc_lens[b] <= T (else FA3_DEVERR_LENS);
+ * no states at all gives zero rows.
+ * k, v     int8 [B][T][Hkv][D] (rows t >= enc_lens[b] are not read), as
+ *          fa3_quantize_append writes them. */
+int fa3_cross_attn_gqa(const int8_t* q, const int8_t* k, const int8_t* v,
+                       const float* q_scale, const float* k_scale, const float* v_scale,
+                       const int32_t* q_start, const int32_t* enc_lens, uint16_t* out,
+                       int n, int B, int T, int Hq, int Hkv, int D, float softmax_scale,
+                       void* workspace, size_t workspace_bytes, int32_t* dev_err, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -63,6 +63,13 @@ _SIGS = {
                                        _P, _P]),
     "fa3_decode_attn_gqa_paged": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P,
                                        _SZ, _P, _P]),
+    "fa3_norm_rope": (_I, [_P] * 4 + [_F, _P, _I, _I, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I] + [_I64] * 12
+                      + [_P, _P]),
+    "fa3_rope_append_gqa_paged": (_I, [_P] * 5 + [_F, _P, _I, _I, _I] + [_P] * 9 + [_I] * 5 + [_I64] * 3 + [_I] * 3
+                                  + [_P, _P]),
+    "fa3_chunk_workspace_size": (_SZ, [_I] * 5),
+    "fa3_prefill_attn_gqa_paged": (_I, [_P] * 10 + [_I] * 8 + [_F, _P, _SZ, _P, _P]),
+    "fa3_cross_attn_gqa": (_I, [_P] * 9 + [_I] * 6 + [_F, _P, _SZ, _P, _P]),
 }
 
 
@@ -563,3 +570,314 @@ def decode_attn_gqa_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_s
                                          _stream(stream))
     _check("fa3_decode_attn_gqa_paged", st)
     return out
+
+
+# ------------------------------------- attention input and packed new rows
+def rope_table(n_pos: int, rot_dim: int, base: float = 10000.0, device="cuda",
+               inv_freq: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """float32 [n_pos][rot_dim] of cos, then sin, of position * inv_freq, computed in
+    float64 (angles of far positions lose their fraction in float32); inv_freq
+    [rot_dim / 2] defaults to base^(-2i / rot_dim)."""
+    if n_pos <= 0 or rot_dim <= 0 or rot_dim % 2:
+        raise ValueError("n_pos must be positive and rot_dim positive and even")
+    if inv_freq is None:
+        inv_freq = float(base) ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    elif inv_freq.numel() != rot_dim // 2:
+        raise ValueError("inv_freq must hold rot_dim / 2 values")
+    a = torch.arange(n_pos, dtype=torch.float64, device=device)[:, None] * inv_freq.to(device, torch.float64)[None]
+    return torch.cat([a.cos(), a.sin()], 1).float().contiguous()
+
+
+def _on_device(t: torch.Tensor, *others) -> int:
+    """The device index of t, which the other tensors (None allowed) have to share."""
+    dev = t.get_device()
+    for o in others:
+        if o is not None and o.get_device() != dev:
+            raise ValueError("all tensors must be on one device")
+    return dev
+
+
+class _Here:
+    """Launches on a tensor's device and, for outputs allocated inside, on the call's stream."""
+
+    __slots__ = ("ctx",)
+
+    def __init__(self, dev: int, stream=None):
+        if stream is not None:
+            if stream.device_index != dev:
+                raise ValueError("stream must be on the tensors' device")
+            self.ctx = torch.cuda.stream(stream)
+        else:
+            self.ctx = torch.cuda.device(dev) if torch.cuda.current_device() != dev else None
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *a):
+        if self.ctx is not None:
+            self.ctx.__exit__(*a)
+
+
+def _opt(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _dev_err(t: Optional[torch.Tensor]) -> None:
+    if t is not None:
+        _need_contig(t, torch.int32, "dev_err")
+        if t.numel() < 1:
+            raise ValueError("dev_err must hold one value")
+
+
+def _rot_table(cos_sin: Optional[torch.Tensor], D: int):
+    if cos_sin is None:
+        return 0, 0
+    _need_contig(cos_sin, torch.float32, "cos_sin")
+    if cos_sin.dim() != 2 or cos_sin.shape[1] > D:
+        raise ValueError("cos_sin must be [table_len][rot_dim] with rot_dim <= D")
+    return cos_sin.shape
+
+
+def _weight(w: Optional[torch.Tensor], D: int, name: str) -> None:
+    if w is not None:
+        _need_contig(w, torch.bfloat16, name)
+        if w.numel() != D:
+            raise ValueError(f"{name} must hold D values")
+
+
+def _rows4(t: torch.Tensor, name: str, out: bool = False):
+    """(B, S, H, D) and the strides (b, s, h) of head rows [B][S][H][D] or [n][H][D]."""
+    if t.dim() == 3:
+        t = t.unsqueeze(0)
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be [B][S][H][D] or [n][H][D]")
+    if t.stride(3) != 1 and t.shape[3] > 1:
+        raise ValueError(f"{name} must have contiguous head rows")
+    st = [0 if t.shape[i] == 1 else t.stride(i) for i in range(3)]
+    if out and any(s == 0 and t.shape[i] > 1 for i, s in enumerate(st)):
+        raise ValueError(f"{name} must not be an expanded tensor")
+    return t.shape, st
+
+
+def norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], cos_sin: Optional[torch.Tensor],
+              pos: Optional[torch.Tensor], q_weight: Optional[torch.Tensor] = None,
+              k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = False,
+              q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+              out_dtype: torch.dtype = torch.bfloat16, dev_err: Optional[torch.Tensor] = None, stream=None):
+    """Per-head RMS norm (with q_weight / k_weight bf16 [D]) and position rotation of q and k in one pass.
+
+    q bf16 [B][S][Hq][D] or [n][Hq][D] and k likewise with Hkv heads (or None): any strides
+    with contiguous head rows, so slices of one projection need no copy.  cos_sin float32
+    [table_len][rot_dim] (rope_table; None: no rotation), pos int32 of one position a token.
+    Results are bf16 or float32: contiguous, or in q_out / k_out of q's / k's shape and any
+    such strides (a transposed view lays them out (B, H, S, D) for calibrate_perhead; q and
+    k themselves are allowed).  Returns (q_out, k_out)."""
+    _need(q, torch.bfloat16, "q")
+    (B, S, Hq, D), qs = _rows4(q, "q")
+    Hkv, ks, kos = 0, (0, 0, 0), (0, 0, 0)
+    if k is not None:
+        _need(k, torch.bfloat16, "k")
+        (kB, kS, Hkv, kD), ks = _rows4(k, "k")
+        if (kB, kS, kD) != (B, S, D) or k.dim() != q.dim():
+            raise ValueError("k must have q's tokens and head size")
+        if (q_weight is None) != (k_weight is None):
+            raise ValueError("q_weight and k_weight go together")
+    elif k_out is not None or k_weight is not None:
+        raise ValueError("k_out and k_weight need k")
+    table_len, rot = _rot_table(cos_sin, D)
+    if cos_sin is not None:
+        if pos is None:
+            raise ValueError("pos must be given with cos_sin")
+        _need_contig(pos, torch.int32, "pos")
+        if pos.numel() != B * S:
+            raise ValueError("pos must hold one position for each token")
+    _weight(q_weight, D, "q_weight")
+    _weight(k_weight, D, "k_weight")
+    _dev_err(dev_err)
+    dev = _on_device(q, k, cos_sin, pos, q_weight, k_weight, q_out, k_out, dev_err)
+    with _Here(dev, stream):
+        t = out_dtype if q_out is None else q_out.dtype
+        if t not in (torch.bfloat16, torch.float32):
+            raise TypeError("results are bfloat16 or float32")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=t, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=t, device=q.device)
+        for o, x, n in ((q_out, q, "q_out"), (k_out, k, "k_out")):
+            if x is not None and (o.dtype != t or o.shape != x.shape):
+                raise ValueError(f"{n} must have the input's shape and the results' one type")
+        qos = _rows4(q_out, "q_out", out=True)[1]
+        if k is not None:
+            kos = _rows4(k_out, "k_out", out=True)[1]
+        if q.numel():
+            st = lib().fa3_norm_rope(q.data_ptr(), _opt(k), _opt(q_weight), _opt(k_weight), eps, _opt(cos_sin),
+                                     table_len, rot, int(interleaved), _opt(pos), q_out.data_ptr(), _opt(k_out),
+                                     int(t == torch.float32), B, S, Hq, Hkv, D, *qs, *ks, *qos, *kos, _opt(dev_err),
+                                     _stream(stream))
+            _check("fa3_norm_rope", st)
+    return q_out, k_out
+
+
+def _packed(q_start: torch.Tensor, lens: torch.Tensor, lens_name: str) -> int:
+    _need_contig(q_start, torch.int32, "q_start")
+    _need_contig(lens, torch.int32, lens_name)
+    B = lens.numel()
+    if q_start.numel() != B + 1 or B == 0:
+        raise ValueError(f"q_start must hold one value more than {lens_name}")
+    return B
+
+
+def _packed_rows(t: torch.Tensor, H: int, D: int, n: int, name: str) -> int:
+    """Row stride of packed rows [n][H][D] with contiguous rows of heads."""
+    _need(t, torch.bfloat16, name)
+    if t.dim() != 3 or t.shape != (n, H, D):
+        raise ValueError(f"{name} must be [n][H][D]")
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"{name} must have contiguous rows of heads")
+    return 0 if n == 1 else t.stride(0)
+
+
+def _scale(t: torch.Tensor, H: int, name: str) -> None:
+    _need_contig(t, torch.float32, name)
+    if t.numel() != H:
+        raise ValueError(f"{name} must hold one value for each head")
+
+
+def _pools(k: torch.Tensor, v: torch.Tensor):
+    _need_contig(k, torch.int8, "k_cache")
+    _need_contig(v, torch.int8, "v_cache")
+    if k.dim() != 4 or k.shape != v.shape:
+        raise ValueError("the k and v pools must both be [num_pages][page_size][Hkv][D]")
+    return k.shape
+
+
+def rope_append_gqa_paged(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+                          cos_sin: Optional[torch.Tensor], q_scale: Optional[torch.Tensor], k_scale: torch.Tensor,
+                          v_scale: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                          block_table: torch.Tensor, q_start: torch.Tensor, kv_lens: torch.Tensor,
+                          q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                          eps: float = 1e-6, interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+                          dev_err: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """The input step of a GQA layer over the paged INT8 cache, in one launch: k (normed if k_weight is
+    given, and rotated) and v are quantized into their pools; q (or None) likewise to INT8 codes.
+
+    q bf16 [n][Hq][D], k, v bf16 [n][Hkv][D] with any row stride (slices of one projection): rows
+    q_start[b] .. q_start[b+1] - 1 are the last tokens of sequence b's kv_lens[b]-token context.
+    k_cache, v_cache int8 [num_pages][page_size][Hkv][D].  Returns the query's codes int8
+    [n][Hq][D] (zero outside the sequences' rows when allocated here)."""
+    num_pages, page_size, Hkv, D = _pools(k_cache, v_cache)
+    B = _packed(q_start, kv_lens, "kv_lens")
+    n = k.shape[0]
+    ks, vs = _packed_rows(k, Hkv, D, n, "k"), _packed_rows(v, Hkv, D, n, "v")
+    _scale(k_scale, Hkv, "k_scale")
+    _scale(v_scale, Hkv, "v_scale")
+    _weight(q_weight, D, "q_weight")
+    _weight(k_weight, D, "k_weight")
+    table_len, rot = _rot_table(cos_sin, D)
+    max_pages = _block_table(block_table, B)
+    _dev_err(dev_err)
+    Hq, qs = 0, 0
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must be [n][H][D]")
+        Hq = q.shape[1]
+        qs = _packed_rows(q, Hq, D, n, "q")
+        _scale(q_scale, Hq, "q_scale")
+    elif q_out is not None or q_weight is not None:
+        raise ValueError("q_out and q_weight need q")
+    dev = _on_device(k, q, v, cos_sin, q_scale, k_scale, v_scale, k_cache, v_cache, block_table, q_start, kv_lens,
+                     q_weight, k_weight, q_out, dev_err)
+    with _Here(dev, stream):
+        if q is not None:
+            if q_out is None:
+                q_out = torch.zeros(n, Hq, D, dtype=torch.int8, device=q.device)
+            _need_contig(q_out, torch.int8, "q_out")
+            if q_out.shape != (n, Hq, D):
+                raise ValueError("q_out must be [n][Hq][D]")
+        if n:
+            st = lib().fa3_rope_append_gqa_paged(
+                _opt(q), k.data_ptr(), v.data_ptr(), _opt(q_weight), _opt(k_weight), eps, _opt(cos_sin), table_len,
+                rot, int(interleaved), _opt(q_scale) if Hq else None, k_scale.data_ptr(), v_scale.data_ptr(),
+                _opt(q_out), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), q_start.data_ptr(),
+                kv_lens.data_ptr(), n, B, Hq, Hkv, D, qs, ks, vs, num_pages, page_size, max_pages, _opt(dev_err),
+                _stream(stream))
+            _check("fa3_rope_append_gqa_paged", st)
+    return q_out
+
+
+def chunk_workspace_size(n: int, B: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(lib().fa3_chunk_workspace_size(n, B, Hq, Hkv, D))
+
+
+def _chunk_workspace(nbytes: int, device, stream):
+    # A captured call takes its buffer from the graph's own pool: replays of two graphs
+    # (or of a graph and eager calls) then never share one.
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    return _workspace("chunk", nbytes, device, stream=stream)
+
+
+def _packed_attn(name: str, q, k, v, q_scale, k_scale, v_scale, q_start, lens, softmax_scale, out, workspace, dev_err,
+                 stream, B, Hkv, extra, table=None):
+    for t, m in ((q, "q"), (k, "k"), (v, "v")):
+        _need_contig(t, torch.int8, m)
+    if q.dim() != 3 or q.shape[2] != k.shape[3]:
+        raise ValueError("q must be [n][Hq][D] with k's head size")
+    n, Hq, D = q.shape
+    _scale(q_scale, Hq, "q_scale")
+    _scale(k_scale, Hkv, "k_scale")
+    _scale(v_scale, Hkv, "v_scale")
+    _dev_err(dev_err)
+    dev = _on_device(q, k, v, q_scale, k_scale, v_scale, q_start, lens, table, out, workspace, dev_err)
+    with _Here(dev, stream):
+        if out is None:
+            out = torch.zeros(n, Hq, D, dtype=torch.bfloat16, device=q.device)
+        _need_contig(out, torch.bfloat16, "out")
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+        if n:
+            L = lib()
+            if workspace is None:
+                nbytes = L.fa3_chunk_workspace_size(n, B, Hq, Hkv, D)
+                workspace = _chunk_workspace(nbytes, q.device, stream) if nbytes else None
+            ptrs = [q.data_ptr(), k.data_ptr(), v.data_ptr(), q_scale.data_ptr(), k_scale.data_ptr(),
+                    v_scale.data_ptr(), q_start.data_ptr(), lens.data_ptr()]
+            if table is not None:
+                ptrs.append(table.data_ptr())
+            st = getattr(L, name)(*ptrs, out.data_ptr(), n, B, *extra(Hq, Hkv, D), softmax_scale, _opt(workspace),
+                                  0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                  _opt(dev_err), _stream(stream))
+            _check(name, st)
+    return out
+
+
+def prefill_attn_gqa_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_scale: torch.Tensor,
+                           k_scale: torch.Tensor, v_scale: torch.Tensor, q_start: torch.Tensor, kv_lens: torch.Tensor,
+                           block_table: torch.Tensor, softmax_scale: float, out: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None, dev_err: Optional[torch.Tensor] = None,
+                           stream=None) -> torch.Tensor:
+    """Causal attention of a chunk of new tokens over page pools: q int8 [n][Hq][D] packed by q_start,
+    k/v int8 [num_pages][page_size][Hkv][D] (holding the new tokens already) -> bf16 [n][Hq][D].
+
+    Rows outside the sequences are left as they were (zero when ``out`` is allocated here)."""
+    num_pages, page_size, Hkv, _ = _pools(k, v)
+    B = _packed(q_start, kv_lens, "kv_lens")
+    max_pages = _block_table(block_table, B)
+    return _packed_attn("fa3_prefill_attn_gqa_paged", q, k, v, q_scale, k_scale, v_scale, q_start, kv_lens,
+                        softmax_scale, out, workspace, dev_err, stream, B, Hkv,
+                        lambda Hq, Hk, D: (Hq, Hk, D, num_pages, page_size, max_pages), table=block_table)
+
+
+def cross_attn_gqa(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_scale: torch.Tensor, k_scale: torch.Tensor,
+                   v_scale: torch.Tensor, q_start: torch.Tensor, enc_lens: torch.Tensor, softmax_scale: float,
+                   out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   dev_err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of q int8 [n][Hq][D] (packed by q_start) to all enc_lens[b] encoder states k/v int8
+    [B][T][Hkv][D] of its sequence -> bf16 [n][Hq][D]; zero rows where there is no state."""
+    B = _packed(q_start, enc_lens, "enc_lens")
+    if k.dim() != 4 or k.shape != v.shape or k.shape[0] != B:
+        raise ValueError("k and v must both be [B][T][Hkv][D]")
+    T, Hkv = k.shape[1], k.shape[2]
+    return _packed_attn("fa3_cross_attn_gqa", q, k, v, q_scale, k_scale, v_scale, q_start, enc_lens, softmax_scale,
+                        out, workspace, dev_err, stream, B, Hkv, lambda Hq, Hk, D: (T, Hq, Hk, D))

@@ -540,3 +540,92 @@ def gqa_decode_float(q: np.ndarray, k: np.ndarray, v: np.ndarray, lens: np.ndarr
             s = (np.asarray(k[b, :n, g], np.float64) @ np.asarray(q[b, h], np.float64)) * float(softmax_scale)
             out[b, h] = _softmax_weights(s) @ np.asarray(v[b, :n, g], np.float64)
     return out
+
+
+# ---------------------------------------------------------------------------
+# Attention input (per-head RMS norm, position rotation) and attention of packed
+# new rows: the model steps between a projection and the INT8 cache, and the
+# chunk / cross attention over it.  The pages leave norm and rotation to the model.
+# ---------------------------------------------------------------------------
+def norm_rope(x: np.ndarray, weight, eps: float, cos_sin, pos: np.ndarray, interleaved: bool):
+    """x [n, H, D] at positions pos [n] -> (y, m) float64, m = |a1 c| + |a2 s|, the size of the terms
+    of each value (what a float32 evaluation rounds relative to)."""
+    a = np.asarray(x, np.float64).copy()
+    if weight is not None:
+        ms = np.mean(a * a, axis=-1, keepdims=True)
+        a = a / np.sqrt(ms + np.float64(np.float32(eps))) * np.asarray(weight, np.float64)
+    y, m = a.copy(), np.abs(a)
+    if cos_sin is None:
+        return y, m
+    rot = cos_sin.shape[1]
+    half = rot // 2
+    for i in range(half):
+        d1, d2 = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
+        c = cos_sin[pos, i].astype(np.float64)[:, None]
+        s = cos_sin[pos, half + i].astype(np.float64)[:, None]
+        y[..., d1] = a[..., d1] * c - a[..., d2] * s
+        y[..., d2] = a[..., d2] * c + a[..., d1] * s
+        m[..., d1] = np.abs(a[..., d1] * c) + np.abs(a[..., d2] * s)
+        m[..., d2] = np.abs(a[..., d2] * c) + np.abs(a[..., d1] * s)
+    return y, m
+
+
+def quantize64(y: np.ndarray, scale: np.ndarray) -> np.ndarray:
+    """clamp(round_half_even(y / scale[h]), -127, 127) in float64; y [n, H, D]."""
+    s = np.asarray(scale, np.float64)[None, :, None]
+    r = np.where(s == 0, 0.0, np.asarray(y, np.float64) / np.where(s == 0, 1.0, s))
+    return np.clip(np.rint(r), -127, 127).astype(np.int8)
+
+
+def packed_rows(q_start: np.ndarray, kv_lens: np.ndarray):
+    """(sequence, position) of every packed row, in order of rows."""
+    for b in range(len(kv_lens)):
+        n = int(q_start[b + 1]) - int(q_start[b])
+        for i in range(n):
+            yield b, int(kv_lens[b]) - n + i
+
+
+def rope_append_paged(q, k, v, q_weight, k_weight, eps, cos_sin, interleaved, q_scale, k_scale, v_scale, q_out,
+                      k_pool, v_pool, block_table, q_start, kv_lens):
+    """New copies of (q_out, k_pool, v_pool) after the append; q may be None."""
+    rows = list(packed_rows(q_start, kv_lens))
+    r0 = int(q_start[0])
+    pos = np.array([p for _, p in rows], np.int64)
+    sel = slice(r0, r0 + len(rows))
+    q_out = None if q is None else q_out.copy()
+    k_pool, v_pool = k_pool.copy(), v_pool.copy()
+    if not rows:
+        return q_out, k_pool, v_pool
+    ps = k_pool.shape[1]
+    if q is not None:
+        q_out[sel] = quantize64(norm_rope(q[sel], q_weight, eps, cos_sin, pos, interleaved)[0], q_scale)
+    k8 = quantize64(norm_rope(k[sel], k_weight, eps, cos_sin, pos, interleaved)[0], k_scale)
+    v8 = quantize(v[sel], np.asarray(v_scale, np.float32)[None, :, None])
+    for j, (b, p) in enumerate(rows):
+        page = block_table[b, p // ps]
+        k_pool[page, p % ps] = k8[j]
+        v_pool[page, p % ps] = v8[j]
+    return q_out, k_pool, v_pool
+
+
+def packed_attention(q8, keys, values, q_scale, k_scale, v_scale, q_start, lens, softmax_scale, causal, out):
+    """Attention of packed rows, float64: keys[b], values[b] are int8 [len_b, Hkv, D] (lens[b] of them).
+    Returns a float64 copy of out with the sequences' rows filled in."""
+    out = np.array(out, np.float64)
+    Hq = q8.shape[1]
+    G = Hq // keys[0].shape[1]
+    for b in range(len(lens)):
+        n, T = int(q_start[b + 1]) - int(q_start[b]), int(lens[b])
+        for i in range(n):
+            row = int(q_start[b]) + i
+            T_i = T - n + i + 1 if causal else T
+            for h in range(Hq):
+                g = h // G
+                if T_i == 0:
+                    out[row, h] = 0.0
+                    continue
+                s = keys[b][:T_i, g].astype(np.float64) @ q8[row, h].astype(np.float64)
+                s = s * (float(q_scale[h]) * float(k_scale[g]) * float(softmax_scale))
+                w = np.exp(s - s.max())
+                out[row, h] = float(v_scale[g]) * (w @ values[b][:T_i, g].astype(np.float64)) / w.sum()
+    return out

@@ -1,0 +1,378 @@
+"""GPU parity of attention over packed new rows (chunks over a paged cache, cross attention) against the
+float64 oracle."""
+import numpy as np
+import pytest
+import torch
+
+import workloads as W
+from helpers import bf16_dev, fa3
+from oracle import fa3_oracle as O
+
+pytestmark = pytest.mark.gpu
+SM = 128 ** -0.5
+KEEP = 3.0                                       # what rows of no sequence hold before and after
+
+
+def _t(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def _case(rng, Hq, Hkv, q_lens, kv_lens, page=None, lead=0, behind=1):
+    B = len(q_lens)
+    q_start = (lead + np.concatenate([[0], np.cumsum(q_lens)])).astype(np.int32)
+    n = int(q_start[-1]) + behind
+    code = lambda *s: np.clip(np.rint(rng.standard_t(5, s) * 30), -127, 127).astype(np.int8)  # noqa: E731
+    c = dict(q=code(n, Hq, 128), q_start=q_start, lens=np.asarray(kv_lens, np.int32), page=page,
+             qs=(W.log_uniform(rng, 0.5, 2, Hq) / 30).astype(np.float32),
+             ks=(W.log_uniform(rng, 0.5, 2, Hkv) / 30).astype(np.float32),
+             vs=(W.log_uniform(rng, 0.5, 2, Hkv) / 30).astype(np.float32))
+    T = max(max(kv_lens), 1)
+    if page is None:
+        c["k"], c["v"] = code(B, T, Hkv, 128), code(B, T, Hkv, 128)
+    else:
+        mp = -(-T // page) + 1
+        num = B * mp + 2
+        c["table"] = rng.permutation(num)[:B * mp].reshape(B, mp).astype(np.int32)
+        for b, kv in enumerate(kv_lens):
+            c["table"][b, -(-kv // page):] = num + 5                          # past the context: never read
+        c["k"], c["v"] = code(num, page, Hkv, 128), code(num, page, Hkv, 128)
+    return c
+
+
+def _run(F, c, err=None, out=None, **kw):
+    if out is None:
+        out = torch.full(c["q"].shape, KEEP, dtype=torch.bfloat16, device="cuda")
+    a = [_t(c[k]) for k in ("q", "k", "v", "qs", "ks", "vs", "q_start", "lens")]
+    if c["page"] is None:
+        o = F.cross_attn_gqa(*a, SM, out=out, dev_err=err, **kw)
+    else:
+        o = F.prefill_attn_gqa_paged(*a, _t(c["table"]), SM, out=out, dev_err=err, **kw)
+    torch.cuda.synchronize()
+    return o.float().cpu().numpy()
+
+
+def _ref(c):
+    lens = np.where(np.diff(c["q_start"]) > 0, c["lens"], 0)
+    if c["page"] is None:
+        kv = [[x[b, :n] for b, n in enumerate(lens)] for x in (c["k"], c["v"])]
+    else:
+        kv = [[x[c["table"][b, np.arange(n) // c["page"]], np.arange(n) % c["page"]] for b, n in enumerate(lens)]
+              for x in (c["k"], c["v"])]
+    return O.packed_attention(c["q"], *kv, c["qs"], c["ks"], c["vs"], c["q_start"], lens, SM, c["page"] is not None,
+                              np.full(c["q"].shape, KEEP))
+
+
+def _gate(got, ref, c, what):
+    """|got - ref| within what the arithmetic can be off.  The output rounds by half a step, 2^-8 of the value
+    (with one key the output is bf16(v), so this alone can be the whole error, and a relative-RMS gate below 2^-8
+    cannot hold for few distinct values).  Before that the output is a mean of v with weights off by: fp16 rounding
+    2^-11 of a weight, twice (sum and product); at most 2^-25 for each of the T weights below fp16's normal range,
+    twice, where the largest weight is at least 1; and the float32 score, |s| log2 units rounded about four times,
+    2^-22 |s| (a relative error of the weight)."""
+    T = max(1, int(c["lens"].max()))
+    s = 128.0 * np.abs(c["q"].astype(np.int32)).max() * np.abs(c["k"].astype(np.int32)).max() * float(c["qs"].max()) \
+        * float(c["ks"].max()) * SM * 1.4427
+    v = 127.0 * float(c["vs"].max())
+    tol = 2.0 ** -8 * np.abs(ref) * (1 + 2.0 ** -8) + (2.0 ** -10 + T * 2.0 ** -24 + 2.0 ** -22 * s) * v + 1e-30
+    d = np.abs(np.asarray(got, np.float64) - ref)
+    assert np.all(np.isfinite(got)), f"{what}: non-finite output"
+    print(f"{what}: {float((d / tol).max()):.3f} of the tolerance")
+    assert np.all(d <= tol), f"{what}: {float((d / tol).max()):.3f} of the tolerance"
+
+
+def _check(F, c, what):
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got, ref = _run(F, c, err), _ref(c)
+    assert int(err.item()) == 0
+    s, e = c["q_start"][0], c["q_start"][-1]
+    assert np.all(got[:s] == KEEP) and np.all(got[e:] == KEEP), f"{what}: rows of no sequence written"
+    _gate(got[s:e], ref[s:e], c, what)
+    return got
+
+
+@pytest.mark.parametrize("Hq,Hkv,page", [(8, 1, 64), (4, 4, 16), (6, 2, 24), (10, 2, 7), (14, 2, 100), (16, 1, 128),
+                                         (2, 1, 1), (128, 1, 48), (36, 3, 256)])
+def test_ragged_chunks(Hq, Hkv, page):
+    # group sizes 8, 1, 3, 5, 7, 16, 2, 128, 12; a sequence without new rows; single tokens; pages inside tiles
+    F = fa3()
+    rng = np.random.default_rng([Hq, Hkv, page])
+    c = _case(rng, Hq, Hkv, [1, 40, 0, 3, 70], [300, 40, 7, 129, 200], page, lead=2)
+    _check(F, c, f"chunk G={Hq // Hkv} page={page}")
+
+
+@pytest.mark.parametrize("kv", [1, 2, 127, 128, 129, 255, 256, 257, 1023])
+def test_single_tokens_at_key_tile_edges(kv):
+    F = fa3()
+    c = _case(np.random.default_rng(kv), 8, 2, [1, 1, 1], [kv, 1, max(1, kv - 1)], 32)
+    _check(F, c, f"one token, {kv} keys")
+
+
+@pytest.mark.parametrize("n", [15, 16, 17, 31, 32, 33, 64, 65, 129])
+def test_row_block_edges(n):
+    # 16 positions fill a tile of 128 rows at 8 heads, 32 a row block
+    F = fa3()
+    c = _case(np.random.default_rng(n), 8, 1, [n, n], [n, n + 130], 64)
+    _check(F, c, f"{n} rows")
+
+
+def test_many_sequences():
+    F = fa3()
+    rng = np.random.default_rng(3)
+    ql = rng.integers(0, 4, 150)
+    c = _case(rng, 4, 2, list(ql), list(ql + rng.integers(0, 60, 150)), 16)
+    _check(F, c, "150 sequences")
+
+
+def test_long_context_of_one_sequence():
+    # one row block of each KV head: its keys are shared out over the whole GPU
+    F = fa3()
+    for q in (1, 5, 20):
+        c = _case(np.random.default_rng(q), 16, 2, [q], [9001], 48)
+        _check(F, c, f"{q} rows over 9001 keys")
+
+
+def test_mixed_long_and_single():
+    F = fa3()
+    c = _case(np.random.default_rng(4), 16, 2, [1, 260, 1, 1], [3000, 1300, 2, 700], 64)
+    _check(F, c, "mixed batch")
+
+
+def test_growing_scores_force_rescales():
+    F = fa3()
+    c = _case(np.random.default_rng(5), 8, 1, [40, 1], [600, 1500], 64)
+    sign = np.where(np.arange(128) % 3 == 0, -1, 1)
+    T = 1500
+    ramp = np.clip(np.arange(T) / T * 127, 1, 127)
+    for b, n in enumerate(c["lens"]):
+        for t in range(n):
+            c["k"][c["table"][b, t // 64], t % 64] = np.rint(sign * ramp[t]).astype(np.int8)
+    c["q"][:] = (sign * 100).astype(np.int8)
+    c["qs"][:] = c["ks"][:] = 0.02
+    _check(F, c, "growing scores")
+
+
+def test_extreme_codes_and_zero_scales():
+    F = fa3()
+    c = _case(np.random.default_rng(6), 4, 2, [18, 1], [140, 400], 16)
+    c["q"][:] = np.where(c["q"] > 0, 127, -127)
+    c["k"][:] = np.where(c["k"] > 0, 127, -127)
+    c["qs"][:] = c["ks"][:] = 1.0                                             # one key takes all the weight
+    c["qs"][1] = 0.0                                                          # equal weights
+    c["vs"][1] = 0.0
+    _check(F, c, "extreme codes")
+
+
+def test_bad_lengths_leave_their_rows():
+    F = fa3()
+    for page, bads in ((16, [3, -1, 4000]), (None, [-1, 4000])):
+        for bad in bads:
+            c = _case(np.random.default_rng(7), 8, 2, [4, 5, 30], [50, 60, 70], page)
+            ref = _ref(c)
+            c["lens"][1] = bad
+            err = torch.zeros(1, dtype=torch.int32, device="cuda")
+            got = _run(F, c, err)
+            assert int(err.item()) == F.FA3_DEVERR_LENS
+            assert np.all(got[4:9] == KEEP)
+            for r in (slice(0, 4), slice(9, 39)):
+                _gate(got[r], ref[r], c, f"beside lens {bad}")
+
+
+@pytest.mark.parametrize("start", [[0, 9, 4, 39], [-3, 4, 9, 39], [0, 4, 9, 4000]])
+def test_bad_q_start_is_reported(start):
+    F = fa3()
+    c = _case(np.random.default_rng(8), 8, 2, [4, 5, 30], [50, 60, 70], 16)
+    c["q_start"] = np.asarray(start, np.int32)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = _run(F, c, err)
+    assert int(err.item()) == F.FA3_DEVERR_LENS
+    assert np.all(np.isfinite(got))
+
+
+def test_bad_page_is_reported():
+    F = fa3()
+    c = _case(np.random.default_rng(9), 8, 2, [4, 5, 30], [50, 60, 70], 16)
+    ref = _ref(c)
+    for bad in (-1, c["k"].shape[0]):
+        keep, c["table"][1, 2] = c["table"][1, 2], bad
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = _run(F, c, err)
+        c["table"][1, 2] = keep
+        assert int(err.item()) == F.FA3_DEVERR_PAGE
+        for r in (slice(0, 4), slice(9, 39)):
+            _gate(got[r], ref[r], c, "beside a bad page")
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(8, 1), (4, 4), (12, 4), (5, 1)])
+def test_cross_ragged(Hq, Hkv):
+    # states: none, one, inside a tile, several tiles; rows: none, one, many
+    F = fa3()
+    rng = np.random.default_rng([Hq, Hkv])
+    c = _case(rng, Hq, Hkv, [3, 1, 0, 70, 1, 33], [0, 1, 9, 200, 515, 128], None, lead=1)
+    got = _check(F, c, f"cross G={Hq // Hkv}")
+    assert not got[1:4].any()                                                 # no states: zero rows
+
+
+def test_cross_all_empty():
+    F = fa3()
+    c = _case(np.random.default_rng(10), 4, 2, [2, 40], [0, 0], None)
+    got = _check(F, c, "no states")
+    assert not got[:42].any()
+
+
+def test_agrees_with_the_decode_and_prefill_calls():
+    # the same cache through the calls that were there: all within the gate of one oracle
+    F = fa3()
+    rng = np.random.default_rng(11)
+    c = _case(rng, 16, 2, [1, 1, 1], [400, 33, 1], 16, behind=0)
+    a = [_t(c[k]) for k in ("q", "k", "v", "qs", "ks", "vs", "lens")]
+    ref = _ref(c)
+    _gate(_run(F, c), ref, c, "chunk")
+    _gate(F.decode_attn_gqa_paged(*a, _t(c["table"]), SM).float().cpu().numpy(), ref, c, "decode")
+    c = _case(rng, 16, 2, [90], [90], 16, behind=0)
+    ref = _ref(c)
+    _gate(_run(F, c), ref, c, "chunk")
+    k, v = (x[c["table"][0, np.arange(90) // 16], np.arange(90) % 16][None] for x in (c["k"], c["v"]))
+    one = _t(np.array([90], np.int32))
+    pre = F.prefill_attn_gqa(_t(c["q"][None]), _t(k), _t(v), _t(c["qs"]), _t(c["ks"]), _t(c["vs"]), one, one, SM)
+    _gate(pre[0].float().cpu().numpy(), ref, c, "prefill")
+
+
+def test_results_repeat_bit_for_bit():
+    F = fa3()
+    c = _case(np.random.default_rng(12), 16, 2, [1, 100, 7], [2500, 1300, 900], 64)
+    first = _run(F, c)
+    for _ in range(3):
+        assert np.array_equal(first, _run(F, c))
+
+
+def test_streams_and_graphs():
+    # a side stream of its own; a captured call replayed on changed contents; two graphs replayed in turn
+    F = fa3()
+    rng = np.random.default_rng(13)
+    c = _case(rng, 16, 2, [1, 37, 1], [2000, 700, 90], 64)
+    d = _case(rng, 16, 2, [1, 37, 1], [1500, 64, 1999], 64)
+    d["table"], d["k"], d["v"] = c["table"].copy(), c["k"], c["v"]
+    full = np.random.default_rng(14).permutation(c["k"].shape[0])[:c["table"].size].reshape(c["table"].shape)
+    c["table"] = full.astype(np.int32)
+    d["table"] = full.astype(np.int32)
+    want_c, want_d = _run(F, c), _run(F, d)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = _run(F, c, stream=s)
+    assert np.array_equal(got, want_c)
+    g, bufs = [], []
+    for k in range(2):
+        a = [_t(c[x]) for x in ("q", "k", "v", "qs", "ks", "vs", "q_start", "lens")] + [_t(c["table"])]
+        out = torch.full(c["q"].shape, KEEP, dtype=torch.bfloat16, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            F.prefill_attn_gqa_paged(*a, SM, out=out)
+        g.append(graph)
+        bufs.append((a, out))
+    for k, x in ((0, c), (1, d), (0, d), (1, c)):
+        a, out = bufs[k]
+        for t, name in zip(a, ("q", "k", "v", "qs", "ks", "vs", "q_start", "lens")):
+            t.copy_(_t(x[name]))
+        out.fill_(KEEP)
+        g[k].replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(out.float().cpu().numpy(), want_c if x is c else want_d)
+    # both graphs at once on two streams
+    s2 = torch.cuda.Stream()
+    for a, out in bufs:
+        out.fill_(KEEP)
+    torch.cuda.synchronize()
+    for st, graph in ((s, g[0]), (s2, g[1])):
+        with torch.cuda.stream(st):
+            graph.replay()
+    torch.cuda.synchronize()
+    assert np.array_equal(bufs[0][1].float().cpu().numpy(), want_d)
+    assert np.array_equal(bufs[1][1].float().cpu().numpy(), want_c)
+
+
+def test_two_streams_at_once():
+    F = fa3()
+    rng = np.random.default_rng(15)
+    cs = [_case(rng, 16, 2, [1, 20], [3000, 900], 64) for _ in range(2)]
+    want = [_run(F, c) for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    args = [[_t(c[k]) for k in ("q", "k", "v", "qs", "ks", "vs", "q_start", "lens")] + [_t(c["table"])] for c in cs]
+    outs = [torch.full(c["q"].shape, KEEP, dtype=torch.bfloat16, device="cuda") for c in cs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, a, o in zip(streams, args, outs):
+            F.prefill_attn_gqa_paged(*a, SM, out=o, stream=s)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert np.array_equal(o.float().cpu().numpy(), w)
+
+
+def test_pool_past_32_bit_offsets():
+    F = fa3()
+    c = _case(np.random.default_rng(16), 8, 8, [2], [100], 64, behind=0)
+    num = (1 << 32) // (8 * 128 * 64) + 40
+    big = [torch.zeros(num, 64, 8, 128, dtype=torch.int8, device="cuda") for _ in range(2)]
+    table = np.array([[num - 1, num - 7, 0]], np.int32)
+    for p, x in zip(big, (c["k"], c["v"])):
+        p[num - 1], p[num - 7] = _t(x[c["table"][0, 0]]), _t(x[c["table"][0, 1]])
+    out = F.prefill_attn_gqa_paged(_t(c["q"]), *big, _t(c["qs"]), _t(c["ks"]), _t(c["vs"]), _t(c["q_start"]),
+                                   _t(c["lens"]), _t(table), SM)
+    _gate(out.float().cpu().numpy(), _ref(c), c, "large pool")
+
+
+def test_a_layer_as_it_is_served():
+    """Calibrate on norm_rope's activations, append a prompt and then single tokens to the paged cache, attend
+    to it, and cross-attend: every step against the oracle on the codes the step before left."""
+    F = fa3()
+    rng = np.random.default_rng(17)
+    Hq, Hkv, D, page, eps = 8, 2, 128, 16, 1e-6
+    prompts, steps = [40, 9], 3
+    cs = F.rope_table(64, D)
+    inv = 10000.0 ** (-np.arange(0, D, 2) / D)
+    ang = np.arange(64)[:, None] * inv
+    np.testing.assert_allclose(cs.cpu().numpy(), np.concatenate([np.cos(ang), np.sin(ang)], 1), atol=2.0 ** -24)
+    w = [W.bf16_round(1 + 0.2 * rng.standard_normal(D).astype(np.float32)) for _ in range(2)]
+    act = lambda n: W.bf16_round(W.student_t(rng, (n, Hq + 2 * Hkv, D), 4, 1.0))  # noqa: E731
+    # calibration
+    x = act(64)
+    q, k = F.norm_rope(bf16_dev(x[:, :Hq]), bf16_dev(x[:, Hq:Hq + Hkv]), cs, torch.arange(64, dtype=torch.int32).cuda(),
+                       bf16_dev(w[0]), bf16_dev(w[1]), eps)
+    scales = []
+    for y, H in ((q, Hq), (k, Hkv), (bf16_dev(x[:, Hq + Hkv:]), Hkv)):
+        mn, mx = (torch.full((H,), s * float("inf"), device="cuda") for s in (1, -1))
+        F.calibrate_perhead(y.transpose(0, 1).contiguous().reshape(H, -1), 0.9999, mn, mx)
+        scales.append(F.qparams(mn, mx))
+    num = 12
+    pools = [torch.zeros(num, page, Hkv, D, dtype=torch.int8, device="cuda") for _ in range(2)]
+    table = torch.from_numpy(rng.permutation(num)[:8].reshape(2, 4).astype(np.int32)).cuda()
+    have = [0, 0]
+    for ql in [prompts] + [[1, 1]] * steps:
+        q_start = np.concatenate([[0], np.cumsum(ql)]).astype(np.int32)
+        have = [h + n for h, n in zip(have, ql)]
+        lens = np.array(have, np.int32)
+        x = act(int(q_start[-1]))
+        xd, before = bf16_dev(x), [p.cpu().numpy() for p in pools]
+        q8 = F.rope_append_gqa_paged(xd[:, :Hq], xd[:, Hq:Hq + Hkv], xd[:, Hq + Hkv:], cs, *scales, *pools, table,
+                                     _t(q_start), _t(lens), bf16_dev(w[0]), bf16_dev(w[1]), eps)
+        out = F.prefill_attn_gqa_paged(q8, *pools, *scales, _t(q_start), _t(lens), table, SM)
+        sc = [s.cpu().numpy() for s in scales]
+        rq, rk, rv = O.rope_append_paged(x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], *w, eps, cs.cpu().numpy(), False,
+                                         *sc, np.zeros((len(x), Hq, D), np.int8), *before, table.cpu().numpy(),
+                                         q_start, lens)
+        assert np.array_equal(q8.cpu().numpy(), rq)
+        assert all(np.array_equal(p.cpu().numpy(), r) for p, r in zip(pools, (rk, rv)))
+        kv = [[O.gather_paged(r, table.cpu().numpy(), page, lens)[b, :n] for b, n in enumerate(lens)] for r in (rk, rv)]
+        ref = O.packed_attention(rq, *kv, *sc, q_start, lens, SM, True, np.zeros(rq.shape))
+        case = dict(q=rq, k=rk, qs=sc[0], ks=sc[1], vs=sc[2], lens=lens)
+        _gate(out.float().cpu().numpy(), ref, case, f"layer step {ql}")
+    # cross attention of the last rows to states written by quantize_append
+    states = W.bf16_round(W.student_t(rng, (2, 25, Hkv, D), 4, 1.0))
+    ck, cv = (torch.zeros(2, 25, Hkv, D, dtype=torch.int8, device="cuda") for _ in range(2))
+    for cache, s in ((ck, scales[1]), (cv, scales[2])):
+        F.quantize_append(bf16_dev(states), s, cache, torch.zeros(2, dtype=torch.int32, device="cuda"))
+    enc = np.array([25, 11], np.int32)
+    out = F.cross_attn_gqa(q8, ck, cv, *scales, _t(q_start), _t(enc), SM)
+    kv = [[x.cpu().numpy()[b, :n] for b, n in enumerate(enc)] for x in (ck, cv)]
+    ref = O.packed_attention(rq, *kv, *sc, q_start, enc, SM, False, np.zeros(rq.shape))
+    case = dict(q=rq, k=ck.cpu().numpy(), qs=sc[0], ks=sc[1], vs=sc[2], lens=enc)
+    _gate(out.float().cpu().numpy(), ref, case, "cross step")

@@ -1,0 +1,318 @@
+"""GPU parity of the attention-input calls: norm_rope (bf16 / float32 results) and rope_append_gqa_paged
+(INT8 codes into the paged cache), against the float64 oracle."""
+import numpy as np
+import pytest
+import torch
+
+import workloads as W
+from helpers import bf16_dev, fa3
+from oracle import fa3_oracle as O
+
+pytestmark = pytest.mark.gpu
+EPS = 1e-6
+
+
+def _t(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def _table(n, rot):
+    inv = 10000.0 ** (-np.arange(0, rot, 2) / rot)
+    a = np.arange(n)[:, None] * inv
+    return np.concatenate([np.cos(a), np.sin(a)], 1).astype(np.float32)
+
+
+def _values(rng, shape):
+    # heavy-tailed values of mixed head magnitudes, bf16-exact
+    x = W.student_t(rng, shape, 4, W.log_uniform(rng, 0.05, 5.0, shape[:-2] + (shape[-2], 1)))
+    return W.bf16_round(x)
+
+
+def _check(got, y, m, f32):
+    # float32 arithmetic: the sum of squares is at most 13 roundings deep (halved by the root), then mean, eps,
+    # root, reciprocal, two products, one rotation product and one fma: below 16 * 2^-24 of the terms; a bf16
+    # result adds half a step, 2^-8 of the value.
+    tol = 2.0 ** -20 * m + (0 if f32 else 2.0 ** -8 * np.abs(y)) + 1e-38
+    d = np.abs(got.double().cpu().numpy() - y)
+    assert np.all(np.isfinite(d))
+    assert np.all(d <= tol), float((d / tol).max())
+
+
+@pytest.mark.parametrize("D,rot,interleaved", [(128, 128, False), (128, 64, True), (64, 64, True), (80, 32, False),
+                                               (96, 96, True), (192, 64, False), (256, 256, False), (8, 8, True),
+                                               (128, 8, False), (72, 56, False)])
+@pytest.mark.parametrize("norm,f32", [(True, False), (False, True)])
+def test_norm_rope(D, rot, interleaved, norm, f32):
+    F = fa3()
+    rng = np.random.default_rng([D, rot])
+    n, Hq, Hkv, L = 37, 5, 3, 501
+    x = _values(rng, (n, Hq + 2 * Hkv, D))
+    wq, wk = (W.bf16_round(1 + 0.3 * rng.standard_normal(D).astype(np.float32)) for _ in range(2))
+    pos = rng.integers(0, L, n).astype(np.int32)
+    pos[:3] = [0, L - 1, 0]
+    cs = _table(L, rot)
+    xd = bf16_dev(x)
+    q, k = F.norm_rope(xd[:, :Hq], xd[:, Hq:Hq + Hkv], _t(cs), _t(pos), bf16_dev(wq) if norm else None,
+                       bf16_dev(wk) if norm else None, EPS, interleaved,
+                       out_dtype=torch.float32 if f32 else torch.bfloat16)
+    for got, sl, w in ((q, slice(0, Hq), wq), (k, slice(Hq, Hq + Hkv), wk)):
+        _check(got, *O.norm_rope(x[:, sl], w if norm else None, EPS, cs, pos, interleaved), f32)
+
+
+@pytest.mark.parametrize("what", ["norm_only", "rope_only", "q_only", "copy"])
+def test_parts_of_the_pass(what):
+    F = fa3()
+    rng = np.random.default_rng(5)
+    x = _values(rng, (9, 4, 128))
+    w = W.bf16_round(1 + 0.3 * rng.standard_normal(128).astype(np.float32))
+    pos = rng.integers(0, 64, 9).astype(np.int32)
+    cs = _table(64, 128)
+    use_w, use_t = what in ("norm_only", "q_only"), what in ("rope_only", "q_only")
+    xd, wd = bf16_dev(x), bf16_dev(w)
+    k = None if what == "q_only" else xd[:, 3:]
+    q, ko = F.norm_rope(xd[:, :3], k, _t(cs) if use_t else None, _t(pos) if use_t else None, wd if use_w else None,
+                        wd if use_w and k is not None else None, EPS)
+    assert (ko is None) == (k is None)
+    for got, sl in ((q, slice(0, 3)), (ko, slice(3, 4))):
+        if got is not None:
+            _check(got, *O.norm_rope(x[:, sl], w if use_w else None, EPS, cs if use_t else None, pos, False), False)
+            if what == "copy":
+                assert torch.equal(got, xd[:, sl])
+
+
+def test_strided_transposed_and_in_place():
+    F = fa3()
+    rng = np.random.default_rng(6)
+    B, S, H, D = 3, 21, 4, 128
+    x = _values(rng, (B, S, H, D))
+    pos = np.stack([np.arange(S) + 7 * b for b in range(B)]).astype(np.int32)
+    cs = _table(64, 128)
+    y, m = O.norm_rope(x.reshape(B * S, H, D), None, EPS, cs, pos.ravel(), False)
+    xd = bf16_dev(x)
+    out = torch.zeros(B, H, S, D, dtype=torch.bfloat16, device="cuda")
+    F.norm_rope(xd, None, _t(cs), _t(pos), q_out=out.transpose(1, 2))
+    _check(out.transpose(1, 2).reshape(B * S, H, D), y, m, False)
+    heads_first = xd.transpose(1, 2).contiguous().transpose(1, 2)          # strided input
+    q, _ = F.norm_rope(heads_first, None, _t(cs), _t(pos))
+    assert torch.equal(q, out.transpose(1, 2))
+    F.norm_rope(xd, None, _t(cs), _t(pos), q_out=xd)                        # in place
+    assert torch.equal(xd, out.transpose(1, 2))
+    # rotating the rope part alone of wider rows (an absorbed MLA query), the rest untouched
+    wide = bf16_dev(np.concatenate([x, x], -1))
+    keep = wide.clone()
+    F.norm_rope(wide[..., D:], None, _t(cs), _t(pos), q_out=wide[..., D:])
+    assert torch.equal(wide[..., :D], keep[..., :D]) and torch.equal(wide[..., D:], out.transpose(1, 2))
+
+
+def test_bad_positions_skip_the_token():
+    F = fa3()
+    rng = np.random.default_rng(7)
+    x = _values(rng, (4, 2, 64))
+    cs = _table(10, 64)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full((4, 2, 64), 9.0, dtype=torch.bfloat16, device="cuda")
+    pos = np.array([3, 10, -1, 9], np.int32)
+    F.norm_rope(bf16_dev(x), None, _t(cs), _t(pos), q_out=out, dev_err=err)
+    assert int(err.item()) == F.FA3_DEVERR_POS
+    assert bool((out[1:3] == 9.0).all())
+    y, m = O.norm_rope(x[[0, 3]], None, EPS, cs, pos[[0, 3]], False)
+    _check(out[[0, 3]], y, m, False)
+
+
+def test_calibrate_takes_what_norm_rope_lays_out():
+    # norm_rope -> (B, H, S, D) -> calibrate -> qparams: the range of the very values it wrote
+    F = fa3()
+    rng = np.random.default_rng(8)
+    B, S, H, D = 2, 40, 3, 128
+    x = _values(rng, (B, S, H, D))
+    w = W.bf16_round(1 + 0.3 * rng.standard_normal(D).astype(np.float32))
+    pos = np.tile(np.arange(S, dtype=np.int32), (B, 1))
+    out = torch.empty(B, H, S, D, dtype=torch.bfloat16, device="cuda")
+    F.norm_rope(bf16_dev(x), None, _t(_table(S, D)), _t(pos), bf16_dev(w), q_out=out.transpose(1, 2))
+    mn, mx = (torch.full((H,), s * float("inf"), device="cuda") for s in (1, -1))
+    F.calibrate_perhead(out, 0.9999, mn, mx)
+    scale = F.qparams(mn, mx).cpu().numpy()
+    ref = O.qparams(*O.calibrate([out.float().cpu().numpy()], 0.9999))
+    assert np.array_equal(scale, ref)
+
+
+# --------------------------------------------------------------------- append
+def _append_case(rng, Hq, Hkv, D, rot, page, q_lens, kv_lens, norm, lead=0, behind=2):
+    B = len(q_lens)
+    q_start = (lead + np.concatenate([[0], np.cumsum(q_lens)])).astype(np.int32)
+    n = int(q_start[-1]) + behind
+    mp = -(-max(kv_lens) // page) + 1
+    num = B * mp + 3
+    table = rng.permutation(num)[:B * mp].reshape(B, mp).astype(np.int32)
+    for b, kv in enumerate(kv_lens):
+        table[b, -(-kv // page):] = -1                                      # past the context: never read
+    x = _values(rng, (n, Hq + 2 * Hkv, D))
+    sc = (np.abs(x).max(axis=(0, 2)) / 127 * rng.uniform(0.3, 1.0, Hq + 2 * Hkv)).astype(np.float32)
+    if norm:
+        sc[:Hq + Hkv] = np.float32(4.0 / 127)
+    if Hq:
+        sc[0] = 0.0                                                         # an all-zero head's scale
+    pools = [rng.integers(-127, 128, (num, page, Hkv, D)).astype(np.int8) for _ in range(2)]
+    w = [W.bf16_round(1 + 0.3 * rng.standard_normal(D).astype(np.float32)) if norm else None for _ in range(2)]
+    return dict(x=x, Hq=Hq, Hkv=Hkv, D=D, cs=_table(max(kv_lens) + 1, rot) if rot else None, q_start=q_start,
+                kv_lens=np.asarray(kv_lens, np.int32), table=table, sc=sc, pools=pools, w=w, n=n)
+
+
+def _run_append(F, c, interleaved, err=None, q=True):
+    Hq, Hkv = c["Hq"], c["Hkv"]
+    xd = bf16_dev(c["x"])
+    kp, vp = (_t(p) for p in c["pools"])
+    q_out = torch.full((c["n"], Hq, c["D"]), 77, dtype=torch.int8, device="cuda") if q else None
+    w = [None if a is None else bf16_dev(a) for a in c["w"]]
+    sc = _t(c["sc"])
+    F.rope_append_gqa_paged(xd[:, :Hq] if q else None, xd[:, Hq:Hq + Hkv], xd[:, Hq + Hkv:],
+                            None if c["cs"] is None else _t(c["cs"]), sc[:Hq].clone() if q else None,
+                            sc[Hq:Hq + Hkv].clone(), sc[Hq + Hkv:].clone(), kp, vp, _t(c["table"]), _t(c["q_start"]),
+                            _t(c["kv_lens"]), w[0] if q else None, w[1], EPS, interleaved, q_out=q_out, dev_err=err)
+    torch.cuda.synchronize()
+    return [None if a is None else a.cpu().numpy() for a in (q_out, kp, vp)]
+
+
+def _ref_append(c, interleaved, q=True):
+    Hq, Hkv, x, sc = c["Hq"], c["Hkv"], c["x"], c["sc"]
+    q_out = np.full((c["n"], Hq, c["D"]), 77, np.int8)
+    return O.rope_append_paged(x[:, :Hq] if q else None, x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], c["w"][0], c["w"][1], EPS,
+                               c["cs"], interleaved, sc[:Hq], sc[Hq:Hq + Hkv], sc[Hq + Hkv:], q_out, *c["pools"],
+                               c["table"], c["q_start"], c["kv_lens"])
+
+
+def _same(got, ref):
+    for g, r, name in zip(got, ref, ("q", "k", "v")):
+        if r is not None:
+            assert np.array_equal(g, r), f"{name}: {(g != r).sum()} of {g.size} codes differ"
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,rot,page,interleaved,norm", [
+    (8, 2, 128, 128, 64, False, True), (8, 2, 128, 128, 64, False, False), (5, 1, 128, 64, 7, True, True),
+    (3, 3, 80, 32, 1, True, False), (6, 2, 256, 256, 16, False, True), (1, 1, 64, 64, 24, True, False),
+    (7, 5, 96, 96, 100, False, True), (4, 4, 128, 0, 16, False, False), (4, 4, 192, 0, 16, False, True)])
+def test_append_bit_exact(Hq, Hkv, D, rot, page, interleaved, norm):
+    F = fa3()
+    rng = np.random.default_rng([Hq, D, page])
+    c = _append_case(rng, Hq, Hkv, D, rot, page, [1, 0, 37, 5, 1], [130, 9, 37, 64, 1], norm, lead=1)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    _same(_run_append(F, c, interleaved, err), _ref_append(c, interleaved))
+    assert int(err.item()) == 0
+
+
+def test_append_without_q():
+    F = fa3()
+    c = _append_case(np.random.default_rng(11), 2, 3, 128, 128, 16, [3, 20], [50, 20], True)
+    c["w"][0] = None
+    _same(_run_append(F, c, False, q=False), _ref_append(c, False, q=False))
+
+
+def test_append_ties_and_clamps():
+    # power-of-two scales put many quotients exactly on half steps (position 0 turns nothing), far values clamp
+    F = fa3()
+    rng = np.random.default_rng(12)
+    c = _append_case(rng, 4, 2, 128, 128, 16, [1, 1, 30], [1, 1, 30], False)
+    c["x"] = W.bf16_round((rng.integers(-400, 401, c["x"].shape) / 64).astype(np.float32))
+    c["x"][2, 0, :] = np.float32(2.0 ** 100)
+    c["sc"][:] = np.float32(1 / 32)
+    c["sc"][1] = np.float32(2.0 ** -120)                                    # beyond the exact-product range
+    c["sc"][2] = np.float32(1e-41)                                          # a subnormal scale
+    _same(_run_append(F, c, False), _ref_append(c, False))
+
+
+def test_append_near_ties_are_decided_exactly():
+    # 2.6 million rotated and normed codes: a few of them lie within float32 rounding of a half step
+    F = fa3()
+    rng = np.random.default_rng(13)
+    for norm in (False, True):
+        c = _append_case(rng, 16, 4, 128, 128, 64, [500, 41], [500, 600], norm)
+        _same(_run_append(F, c, norm), _ref_append(c, norm))
+
+
+def test_append_many_sequences():
+    # more sequences than one 32-way step, then than two, finds
+    F = fa3()
+    for B in (33, 1100):
+        rng = np.random.default_rng(B)
+        ql = rng.integers(0, 3, B)
+        ql[-1] = 1
+        c = _append_case(rng, 1, 1, 64, 64, 4, list(ql), list(ql + rng.integers(1, 9, B)), False)
+        _same(_run_append(F, c, False), _ref_append(c, False))
+
+
+def test_append_errors_skip_what_is_wrong():
+    F = fa3()
+    rng = np.random.default_rng(14)
+    c = _append_case(rng, 4, 2, 128, 128, 16, [3, 4, 2, 5], [20, 30, 40, 16], True)
+    ref = list(_ref_append(c, False))
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def untouched(ref, b):
+        s, e = c["q_start"][b], c["q_start"][b + 1]
+        ref[0][s:e] = 77
+        for j in (1, 2):
+            for p in range(c["kv_lens"][b] - (e - s), c["kv_lens"][b]):
+                at = (c["table"][b, p // 16], p % 16)
+                ref[j][at] = c["pools"][j - 1][at]
+
+    good = c["kv_lens"].copy()
+    for bad in (2, 100000, -5):                                              # fewer than the new rows; past T_max
+        c["kv_lens"][1] = bad
+        got = _run_append(F, c, False, err)
+        assert int(err.item()) == F.FA3_DEVERR_LENS
+        err.zero_()
+        r = [a.copy() for a in ref]
+        c["kv_lens"] = good.copy()
+        untouched(r, 1)
+        _same(got, r)
+    table = c["table"].copy()
+    c["table"][2, 39 // 16] = c["pools"][0].shape[0]                         # both new tokens of sequence 2
+    got = _run_append(F, c, False, err)
+    assert int(err.item()) == F.FA3_DEVERR_PAGE
+    c["table"] = table
+    r = [a.copy() for a in ref]
+    untouched(r, 2)
+    r[0] = ref[0]
+    _same(got, r)
+    err.zero_()
+    c["cs"] = c["cs"][:39]                                                   # sequence 2's last position has no angle
+    got = _run_append(F, c, False, err)
+    assert int(err.item()) == F.FA3_DEVERR_POS
+    r = [a.copy() for a in ref]
+    row, at = c["q_start"][3] - 1, (c["table"][2, 39 // 16], 39 % 16)
+    r[0][row] = 77
+    for j in (1, 2):
+        r[j][at] = c["pools"][j - 1][at]
+    _same(got, r)
+
+
+def test_v_codes_are_those_of_quantize_append_paged():
+    F = fa3()
+    rng = np.random.default_rng(15)
+    x = _values(rng, (2, 6, 3, 128))
+    sc = _t((np.abs(x).max(axis=(0, 1, 3)) / 127).astype(np.float32))
+    table = _t(np.array([[2, 0], [1, 3]], np.int32))
+    a, b, k = (torch.zeros(4, 8, 3, 128, dtype=torch.int8, device="cuda") for _ in range(3))
+    F.quantize_append_paged(bf16_dev(x), sc, a, table, _t(np.array([4, 10], np.int32)))
+    xd = bf16_dev(x).reshape(12, 3, 128)
+    F.rope_append_gqa_paged(None, xd, xd, None, None, sc, sc, k, b, table, _t(np.array([0, 6, 12], np.int32)),
+                            _t(np.array([10, 16], np.int32)))
+    assert torch.equal(a, b) and torch.equal(a, k)
+
+
+def test_append_past_32_bit_offsets():
+    # a pool of more than 2^32 bytes, written near its end
+    F = fa3()
+    Hkv, D, page = 8, 128, 64
+    num = (1 << 32) // (Hkv * D * page) + 40
+    kp, vp = (torch.zeros(num, page, Hkv, D, dtype=torch.int8, device="cuda") for _ in range(2))
+    rng = np.random.default_rng(16)
+    x = _values(rng, (2, Hkv, D))
+    sc = (np.abs(x).max(axis=(0, 2)) / 127).astype(np.float32)
+    xd = bf16_dev(x)
+    F.rope_append_gqa_paged(None, xd, xd, None, None, _t(sc), _t(sc), kp, vp, _t(np.array([[num - 1]], np.int32)),
+                            _t(np.array([0, 2], np.int32)), _t(np.array([page], np.int32)))
+    ref = O.quantize(x, sc[None, :, None])
+    for p in (kp, vp):
+        assert np.array_equal(p[num - 1, page - 2:].cpu().numpy(), ref)
+        assert not p[:num - 1].any() and not p[num - 1, :page - 2].any()
