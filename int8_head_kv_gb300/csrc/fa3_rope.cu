@@ -25,7 +25,7 @@
 namespace fa3 {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 constexpr int kRopeWarps = kRopeThreads / 32;
 
 // One tensor of head rows: row (b, s, h) starts at x + b * sb + s * ss + h * sh.
@@ -35,10 +35,16 @@ struct HeadRows {
   int64_t sb, ss, sh;
 };
 
+struct HeadOut {
+  void* y;
+  int64_t sb, ss, sh;
+};
+
 struct RotArgs {
   const float* cos_sin;     // [table_len][rot], or nullptr: no rotation
   int table_len, rot, interleaved, D;
-  float eps;
+  float eps, inv_D;
+  double inv_D64;
 };
 
 // A lane's eight values of a row: two groups of four at o1 and o2.
@@ -64,77 +70,122 @@ __device__ __forceinline__ void bf16x4(uint2 v, float* f) {
 }
 __device__ __forceinline__ uint2 load4(const uint16_t* p) { return *reinterpret_cast<const uint2*>(p); }
 
-// f[0..7] = values at o1, o2 -> pair members a[e], b[e] (and back).
-template <typename T>
-__device__ __forceinline__ void to_pairs(const T* f, bool inter, T* a, T* b) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    a[e] = inter ? f[2 * e] : f[e];
-    b[e] = inter ? f[2 * e + 1] : f[4 + e];
-  }
-}
-template <typename T>
-__device__ __forceinline__ void from_pairs(const T* a, const T* b, bool inter, T* f) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (inter) {
-      f[2 * e] = a[e];
-      f[2 * e + 1] = b[e];
-    } else {
-      f[e] = a[e];
-      f[4 + e] = b[e];
-    }
-  }
+// The pair e of a lane's eight values is (f[first(e)], f[second(e)]).
+template <bool INTER>
+__device__ __forceinline__ constexpr int first(int e) { return INTER ? 2 * e : e; }
+template <bool INTER>
+__device__ __forceinline__ constexpr int second(int e) { return INTER ? 2 * e + 1 : 4 + e; }
+
+using f2 = unsigned long long;          // two floats for the packed instructions
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
-// Sum over the lanes of a row (row_lanes a power of two).
-template <typename T>
-__device__ __forceinline__ T row_sum(T v, int row_lanes) {
-  for (int o = row_lanes >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+__device__ __forceinline__ float rsqrt_approx(float x) {          // relative 2^-22.9
+  float r;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {  // a NaN is dropped
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Two 16-bit codes clamped to [-127, 127].
+__device__ __forceinline__ uint32_t clamp_code2(uint32_t v) {
+  uint32_t r;
+  asm("{\n.reg .b32 x;\nmax.s16x2 x, %1, %2;\nmin.s16x2 %0, x, %3;\n}" : "=r"(r) : "r"(v), "r"(0xff81ff81u), "r"(0x007f007fu));
+  return r;
+}
+
+// Sum over the LANES lanes of a row.
+template <int LANES, typename T>
+__device__ __forceinline__ T row_sum(T v) {
+#pragma unroll
+  for (int o = LANES / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// The transform in type T; x and w are the lane's values of the row and its weight.
-template <typename T>
-__device__ __forceinline__ void transform(const float (&x)[8], const float (&w)[8], bool norm, const Lane8& p,
-                                          const RotArgs& r, float4 c4, float4 s4, int row_lanes, T (&y)[8]) {
-  T f[8];
+// A lane's values of a row as packed pair members: a[j] = (a_2j, a_2j+1), b likewise.
+struct Pairs {
+  f2 a[2], b[2];
+};
+template <bool INTER>
+__device__ __forceinline__ Pairs unpack_pairs(uint2 lo, uint2 hi) {
+  float f[8];
+  bf16x4(lo, f);
+  bf16x4(hi, f + 4);
+  Pairs p;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = (T)x[e];
-  if (norm) {
-    T ss = (T)0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ss += f[e] * f[e];
-    const T rstd = (T)1 / sqrt(row_sum(ss, row_lanes) / (T)r.D + (T)r.eps);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = f[e] * rstd * (T)w[e];
+  for (int j = 0; j < 2; ++j) {
+    p.a[j] = f32x2_pack(f[first<INTER>(2 * j)], f[first<INTER>(2 * j + 1)]);
+    p.b[j] = f32x2_pack(f[second<INTER>(2 * j)], f[second<INTER>(2 * j + 1)]);
+  }
+  return p;
+}
+
+// The row's sum of squares: squares of bf16 values are exact in float32, the sum is eight
+// to ten roundings deep.
+template <int LANES>
+__device__ __forceinline__ float row_squares(const Pairs& p) {
+  f2 acc = mul2(p.a[0], p.a[0]);
+  acc = f32x2_fma(p.a[1], p.a[1], acc);
+  acc = f32x2_fma(p.b[0], p.b[0], acc);
+  acc = f32x2_fma(p.b[1], p.b[1], acc);
+  float lo, hi;
+  f32x2_unpack(acc, lo, hi);
+  return row_sum<LANES>(lo + hi);
+}
+
+// What a token and a weight multiply a lane's pairs by: y_a = a * ac - b * bs,
+// y_b = b * bc + a * as, times the row's 1 / rms.  The products of weight and angle are
+// taken once for all heads of the task (one rounding).
+struct Turn {
+  f2 ac[2], nbs[2], bc[2], as[2];
+};
+template <bool INTER>
+__device__ __forceinline__ Turn make_turn(const Lane8& p, const RotArgs& r, int pos, const uint16_t* weight, int i) {
+  float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+  float4 c4 = make_float4(1.f, 1.f, 1.f, 1.f), s4 = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (weight && p.in) {
+    bf16x4(load4(weight + p.o1), w);
+    bf16x4(load4(weight + p.o2), w + 4);
   }
   if (p.rotated) {
-    T a[4], b[4], ya[4], yb[4];
-    to_pairs(f, r.interleaved != 0, a, b);
-    const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      ya[e] = a[e] * (T)c[e] - b[e] * (T)s[e];
-      yb[e] = b[e] * (T)c[e] + a[e] * (T)s[e];
-    }
-    from_pairs(ya, yb, r.interleaved != 0, y);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = f[e];
+    const float* row = r.cos_sin + (int64_t)pos * r.rot + 4 * i;
+    c4 = *reinterpret_cast<const float4*>(row);
+    s4 = *reinterpret_cast<const float4*>(row + r.rot / 2);
   }
+  const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+  Turn t;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int e = 2 * j;
+    const float wa0 = w[first<INTER>(e)], wa1 = w[first<INTER>(e + 1)];
+    const float wb0 = w[second<INTER>(e)], wb1 = w[second<INTER>(e + 1)];
+    t.ac[j] = f32x2_pack(wa0 * c[e], wa1 * c[e + 1]);
+    t.as[j] = f32x2_pack(wa0 * s[e], wa1 * s[e + 1]);
+    t.bc[j] = f32x2_pack(wb0 * c[e], wb1 * c[e + 1]);
+    t.nbs[j] = f32x2_pack(-wb0 * s[e], -wb1 * s[e + 1]);
+  }
+  return t;
 }
 
 // ------------------------------------------------------------------- norm_rope
 struct NormRopeArgs {
   HeadRows q, k;
-  void *q_out, *k_out;
-  int64_t qo_sb, qo_ss, qo_sh, ko_sb, ko_ss, ko_sh;
+  HeadOut qo, ko;
   RotArgs r;
   const int32_t* pos;       // [B * S]
   int S, Hq, Hkv;
-  uint32_t tokens, chunks, per_chunk;   // head rows per warp task
-  int row_lanes;
+  uint32_t tokens, chunks, q_chunks, per_chunk;   // a warp's task: per_chunk heads of a token
   DivU32 div_chunks, div_S;
   int32_t* err;
 };
@@ -152,54 +203,83 @@ __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* dst, const 
       make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
-template <typename OUT>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const NormRopeArgs a) {
-  pdl_wait();
-  pdl_launch_dependents();
+// Tasks of a token: chunks of per_chunk heads that lie within q or within k, so that
+// pointers, strides and weights are the warp's.  Two passes (32 / LANES rows each) are
+// loaded while the two before them are worked on.
+template <typename OUT, int LANES, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads, 8) norm_rope_kernel(const NormRopeArgs a) {
+  constexpr int rows = 32 / LANES;
   const int lane = threadIdx.x & 31;
-  const int i = lane & (a.row_lanes - 1), sub = lane / a.row_lanes, rows = 32 / a.row_lanes;
+  const int i = lane % LANES, sub = lane / LANES;
   const Lane8 p = lane_place(i, a.r);
   const uint32_t nt = a.tokens * a.chunks;
+  pdl_wait();
+  pdl_launch_dependents();
   for (uint32_t t = blockIdx.x * kRopeWarps + (threadIdx.x >> 5); t < nt; t += gridDim.x * kRopeWarps) {
     const uint32_t tok = divu32(t, a.div_chunks), chunk = t - tok * a.chunks;
     const uint32_t b = divu32(tok, a.div_S), s = tok - b * (uint32_t)a.S;
-    float4 c4 = make_float4(1.f, 1.f, 1.f, 1.f), s4 = make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool is_q = chunk < a.q_chunks;
+    const HeadRows T = is_q ? a.q : a.k;
+    const int h_first = (int)((is_q ? chunk : chunk - a.q_chunks) * a.per_chunk);
+    const int n = min((int)a.per_chunk, (is_q ? a.Hq : a.Hkv) - h_first) - sub;   // rows from this half on
+    const uint16_t* x = T.x + b * T.sb + s * T.ss + (h_first + sub) * T.sh;
+    const int64_t step = rows * T.sh;
+    uint2 cur[2][2], nxt[2][2];
+    auto fetch = [&](uint2 (&d)[2][2], int h, const uint16_t* at) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        d[u][0] = d[u][1] = make_uint2(0u, 0u);
+        if (h + u * rows < n && p.in) {
+          d[u][0] = load4(at + u * step + p.o1);
+          d[u][1] = load4(at + u * step + p.o2);
+        }
+      }
+    };
+    fetch(cur, 0, x);
+    int pos = 0;
     if (a.r.cos_sin) {
-      const int pos = a.pos[tok];
+      pos = a.pos[tok];
       if (pos < 0 || pos >= a.r.table_len) {
         if (lane == 0) set_dev_err(a.err, FA3_DEVERR_POS);
         continue;
       }
-      if (p.rotated) {
-        const float* row = a.r.cos_sin + (int64_t)pos * a.r.rot + 4 * i;
-        c4 = *reinterpret_cast<const float4*>(row);
-        s4 = *reinterpret_cast<const float4*>(row + a.r.rot / 2);
-      }
     }
-    const int h_end = min((int)((chunk + 1) * a.per_chunk), a.Hq + a.Hkv);
-    for (int h0 = chunk * a.per_chunk; h0 < h_end; h0 += rows) {
-      const int hh = h0 + sub;
-      const bool live = hh < h_end && p.in;
-      const bool is_q = hh < a.Hq;
-      const int h = is_q ? hh : hh - a.Hq;
-      const HeadRows& T = is_q ? a.q : a.k;
-      float x[8] = {}, w[8] = {}, y[8];
-      if (live) {
-        const uint16_t* xr = T.x + b * T.sb + s * T.ss + h * T.sh;
-        bf16x4(load4(xr + p.o1), x);
-        bf16x4(load4(xr + p.o2), x + 4);
+    const Turn w = make_turn<INTER>(p, a.r, pos, T.weight, i);
+    const HeadOut O = is_q ? a.qo : a.ko;
+    OUT* y = (OUT*)O.y + b * O.sb + s * O.ss + (h_first + sub) * O.sh;
+    for (int h = 0; h < n + sub; h += 2 * rows) {                      // n + sub: the same for the whole warp
+      x += 2 * step;
+      fetch(nxt, h + 2 * rows, x);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (u && h + rows >= n + sub) break;
+        const Pairs v = unpack_pairs<INTER>(cur[u][0], cur[u][1]);
+        f2 r2 = 0;
         if (T.weight) {
-          bf16x4(load4(T.weight + p.o1), w);
-          bf16x4(load4(T.weight + p.o2), w + 4);
+          const float rstd = rsqrtf(row_squares<LANES>(v) * a.r.inv_D + a.r.eps);
+          r2 = f32x2_pack(rstd, rstd);
+        }
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          // values that pass stay apart from their neighbours: 0 * inf is no 0
+          f2 ya = p.rotated ? f32x2_fma(v.a[j], w.ac[j], mul2(v.b[j], w.nbs[j])) : mul2(v.a[j], w.ac[j]);
+          f2 yb = p.rotated ? f32x2_fma(v.b[j], w.bc[j], mul2(v.a[j], w.as[j])) : mul2(v.b[j], w.bc[j]);
+          if (T.weight) {
+            ya = mul2(ya, r2);
+            yb = mul2(yb, r2);
+          }
+          f32x2_unpack(ya, f[first<INTER>(2 * j)], f[first<INTER>(2 * j + 1)]);
+          f32x2_unpack(yb, f[second<INTER>(2 * j)], f[second<INTER>(2 * j + 1)]);
+        }
+        if (h + u * rows < n && p.in) {
+          store4(y + u * rows * O.sh + p.o1, f);
+          store4(y + u * rows * O.sh + p.o2, f + 4);
         }
       }
-      transform<float>(x, w, a.q.weight != nullptr || a.k.weight != nullptr, p, a.r, c4, s4, a.row_lanes, y);
-      if (live) {
-        OUT* yr = is_q ? (OUT*)a.q_out + b * a.qo_sb + s * a.qo_ss + h * a.qo_sh
-                       : (OUT*)a.k_out + b * a.ko_sb + s * a.ko_ss + h * a.ko_sh;
-        store4(yr + p.o1, y);
-        store4(yr + p.o2, y + 4);
-      }
+      y += 2 * rows * O.sh;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) cur[u][0] = nxt[u][0], cur[u][1] = nxt[u][1];
     }
   }
 }
@@ -212,8 +292,7 @@ struct RopeAppendArgs {
   RotArgs r;
   const int32_t *block_table, *q_start, *kv_lens;
   int n, B, Hq, Hkv, num_pages, page_size, max_pages, T_max;
-  uint32_t chunks, per_chunk;
-  int row_lanes;
+  uint32_t chunks, q_chunks, k_chunks, per_chunk;   // a warp's task: per_chunk heads of q, k or v of a token
   DivU32 div_chunks, div_ps;
   int32_t* err;
 };
@@ -235,112 +314,284 @@ __device__ __forceinline__ int find_sequence(const int32_t* q_start, int B, int 
   return lo;
 }
 
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeAppendArgs a) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int i = lane & (a.row_lanes - 1), sub = lane / a.row_lanes, rows = 32 / a.row_lanes;
-  const Lane8 p = lane_place(i, a.r);
-  const Lane8 pass = {8 * i, 8 * i + 4, p.in, false};
-  const uint32_t nt = (uint32_t)a.n * a.chunks;
-  const int heads = a.Hq + 2 * a.Hkv;
-  for (uint32_t t = blockIdx.x * kRopeWarps + (threadIdx.x >> 5); t < nt; t += gridDim.x * kRopeWarps) {
-    const int row = (int)divu32(t, a.div_chunks);
-    const int chunk = (int)(t - (uint32_t)row * a.chunks);
-    const int b = find_sequence(a.q_start, a.B, row, lane);
-    if (b < 0 || b >= a.B) continue;                       // behind the last sequence
-    const int q0 = a.q_start[b], q1 = a.q_start[b + 1], kv = a.kv_lens[b];
-    if (q0 < 0 || q1 <= row || q1 > a.n || kv < q1 - q0 || kv > a.T_max) {
-      if (lane == 0) set_dev_err(a.err, FA3_DEVERR_LENS);
-      continue;
+// Codes in float32, and where that cannot decide, in float64.
+//
+// Fast path: with f = 1 / (rms s), t = y f by one fma onto 1.5 * 2^23, which rounds half
+// to even in the low mantissa bits; d is what the rounding left.  In units of u = 2^-24
+// and relative to m = |a ac| + |b bs|, t is off by: product and fma 2, reciprocal of s
+// 1.65, and with the norm ten roundings of the sum, mean and eps halved by the root 6,
+// rsqrtf 4, f 1, weight times angle 1; together 3.7 (15.7).  A t whose half step is
+// nearer than 8 (20) u (|a| + |b|) max(|ac|, |bs|, |bc|, |as|) is decided again: one or
+// two values in 10^4 of normal data.
+//
+// Again, by the whole warp because the row's sum of squares is needed: sum and products
+// in float64, 1 / sqrt by one Newton step on rsqrtf (relative 1e-13), and the sign of
+// y - h s for the half step h next to t (h s is exact).  What float32 cannot carry (a scale
+// outside [2^-100, 2^100], a sum of squares outside [2^-100, 2^100], infinities and NaN)
+// ends there too.  The codes are those of float64 arithmetic.
+constexpr float kTieNorm = 20.f / 16777216.f, kTiePlain = 8.f / 16777216.f;
+
+__device__ __forceinline__ int code64(double y, double s) {
+  if (s == 0.0) return 0;
+  return __double2int_rn(fmin(fmax(y / s, -127.0), 127.0));
+}
+
+// Value e of a lane's eight, decided in float64 (x: the values, w: the weights, c and sn
+// the angles of its four pairs).
+template <bool INTER>
+__device__ __forceinline__ int decide64(const float (&x)[8], const float (&w)[8], const float (&c)[4],
+                                        const float (&sn)[4], int e, double rstd, bool norm, bool turn, bool exact,
+                                        float s, float rs) {
+  const int pe = INTER ? e / 2 : e % 4;
+  const bool sec = INTER ? (e & 1) != 0 : e >= 4;
+  const int o = sec ? first<INTER>(pe) : second<INTER>(pe);
+  const double mine = (double)x[e] * rstd * (norm ? (double)w[e] : 1.0);
+  double y = mine;
+  if (turn) {
+    const double other = (double)x[o] * rstd * (norm ? (double)w[o] : 1.0);
+    y = sec ? mine * (double)c[pe] + other * (double)sn[pe] : mine * (double)c[pe] - other * (double)sn[pe];
+  }
+  if (!exact) return code64(y, (double)s);
+  const float lo = floorf((float)y * rs), h = lo + 0.5f;       // the half step next to y / s
+  const double over = y - (double)h * (double)s;
+  const int code = (int)(over > 0.0 ? lo + 1.f : over < 0.0 ? lo : rintf(h));
+  return max(-127, min(127, code));
+}
+
+// (hi, lo) += v with hi + lo exact but for lo's own roundings.
+__device__ __forceinline__ void add_exact(float& hi, float& lo, float v) {
+  const float s = __fadd_rn(hi, v), t = __fsub_rn(s, hi);
+  lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(v, t)));
+  hi = s;
+}
+
+// The lane's codes with those of `again` (a bit each) decided in float64; every lane of
+// the warp calls it.  Out of line: it is rare, and its registers are not the loop's.
+template <int LANES, bool INTER>
+__device__ __noinline__ uint2 decide_row(const RotArgs& r, const uint16_t* weight, uint2 x1, uint2 x2, float s,
+                                         uint2 codes, uint32_t again, bool sound, bool is_v, int pos, int i) {
+  const Lane8 p = lane_place(i, r);
+  float x[8], w[8] = {}, c[4] = {}, sn[4] = {};
+  bf16x4(x1, x);
+  bf16x4(x2, x + 4);
+  double rstd = 1.0;
+  if (weight) {
+    // The sum of squares as an unevaluated pair of float32 (Knuth's exact sum of two numbers;
+    // the squares are exact): float64 arithmetic is 32 times slower here, so it starts at the
+    // row's one sum.
+    float hi = 0.f, lo = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) add_exact(hi, lo, x[e] * x[e]);
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) {
+      const float h2 = __shfl_xor_sync(0xffffffffu, hi, o), l2 = __shfl_xor_sync(0xffffffffu, lo, o);
+      add_exact(hi, lo, h2);
+      lo = __fadd_rn(lo, l2);
     }
-    const int pos = kv - (q1 - row);
-    float4 c4 = make_float4(1.f, 1.f, 1.f, 1.f), s4 = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (a.r.cos_sin) {
-      if (pos >= a.r.table_len) {
-        if (lane == 0) set_dev_err(a.err, FA3_DEVERR_POS);
-        continue;
-      }
-      if (p.rotated) {
-        const float* tr = a.r.cos_sin + (int64_t)pos * a.r.rot + 4 * i;
-        c4 = *reinterpret_cast<const float4*>(tr);
-        s4 = *reinterpret_cast<const float4*>(tr + a.r.rot / 2);
-      }
+    double ms;
+    if (sound) {
+      ms = ((double)hi + (double)lo) * r.inv_D64 + (double)r.eps;
+      const double r0 = (double)rsqrtf((float)ms);
+      rstd = r0 * fma(-0.5 * ms * r0, r0, 1.5);
     }
-    const uint32_t pi = divu32((uint32_t)pos, a.div_ps);
-    const int pg = a.block_table[(int64_t)b * a.max_pages + pi];
-    const bool page_ok = pg >= 0 && pg < a.num_pages;
-    if (!page_ok && lane == 0) set_dev_err(a.err, FA3_DEVERR_PAGE);
-    const int64_t pool_row = (int64_t)pg * a.page_size + (pos - (int)pi * a.page_size);
-    const int h_end = min((chunk + 1) * (int)a.per_chunk, heads);
-    for (int h0 = chunk * (int)a.per_chunk; h0 < h_end; h0 += rows) {
-      const int hh = h0 + sub;
-      const int kind = hh < a.Hq ? 0 : hh < a.Hq + a.Hkv ? 1 : 2;
-      const int h = kind == 0 ? hh : kind == 1 ? hh - a.Hq : hh - a.Hq - a.Hkv;
-      const bool live = hh < h_end && p.in && (kind == 0 ? a.q_out != nullptr : page_ok);
-      const HeadRows& T = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
-      const Lane8 pl = kind == 2 ? pass : p;
-      float x[8] = {}, w[8] = {};
-      float sc = 0.f;
-      if (live) {
-        const uint16_t* xr = T.x + row * T.ss + h * T.sh;
-        bf16x4(load4(xr + pl.o1), x);
-        bf16x4(load4(xr + pl.o2), x + 4);
-        if (T.weight) {
-          bf16x4(load4(T.weight + pl.o1), w);
-          bf16x4(load4(T.weight + pl.o2), w + 4);
-        }
-        sc = (kind == 0 ? a.q_scale : kind == 1 ? a.k_scale : a.v_scale)[h];
-      }
-      const bool norm = kind < 2 && T.weight != nullptr;
-      double y[8];
-      {
-        double f[8], ss = 0.0;
+    if (__any_sync(0xffffffffu, !sound)) {                   // squares that float32 does not hold
+      double sd = 0.0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          f[e] = (double)x[e];
-          ss += f[e] * f[e];
-        }
-        ss = row_sum(ss, a.row_lanes);
-        if (norm) {
-          const double rstd = 1.0 / sqrt(ss / (double)a.r.D + (double)a.r.eps);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = f[e] * rstd * (double)w[e];
-        }
-        if (pl.rotated) {
-          double pa[4], pb[4], ya[4], yb[4];
-          to_pairs(f, a.r.interleaved != 0, pa, pb);
-          const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            ya[e] = pa[e] * (double)c[e] - pb[e] * (double)s[e];
-            yb[e] = pb[e] * (double)c[e] + pa[e] * (double)s[e];
-          }
-          from_pairs(ya, yb, a.r.interleaved != 0, y);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = f[e];
-        }
-      }
-      if (live) {
-        uint32_t packed[2] = {0u, 0u};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          int code = 0;
-          if (kind == 2) {
-            code = quant_code(x[e], sc);
-          } else if (sc != 0.f) {
-            code = __double2int_rn(fmin(fmax(y[e] / (double)sc, -127.0), 127.0));
-          }
-          packed[e >> 2] |= ((uint32_t)code & 0xffu) << (8 * (e & 3));
-        }
-        int8_t* dst = kind == 0 ? a.q_out + ((int64_t)row * a.Hq + h) * a.r.D
-                                : (kind == 1 ? a.k_cache : a.v_cache) + (pool_row * a.Hkv + h) * a.r.D;
-        *reinterpret_cast<uint32_t*>(dst + pl.o1) = packed[0];
-        *reinterpret_cast<uint32_t*>(dst + pl.o2) = packed[1];
-      }
+      for (int e = 0; e < 8; ++e) sd = fma((double)x[e], (double)x[e], sd);
+      ms = row_sum<LANES>(sd) / (double)r.D + (double)r.eps;
+      if (!sound) rstd = 1.0 / sqrt(ms);
     }
   }
+  if (!again) return codes;
+  if (weight) {
+    bf16x4(load4(weight + p.o1), w);
+    bf16x4(load4(weight + p.o2), w + 4);
+  }
+  if (p.rotated) {
+    const float* tr = r.cos_sin + (int64_t)pos * r.rot + 4 * i;
+    const float4 c4 = *reinterpret_cast<const float4*>(tr), s4 = *reinterpret_cast<const float4*>(tr + r.rot / 2);
+    c[0] = c4.x, c[1] = c4.y, c[2] = c4.z, c[3] = c4.w;
+    sn[0] = s4.x, sn[1] = s4.y, sn[2] = s4.z, sn[3] = s4.w;
+  }
+  uint32_t q[2] = {codes.x, codes.y};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (again >> e & 1u) {
+      const int code = is_v ? quant_code(x[e], s) : decide64<INTER>(x, w, c, sn, e, rstd, weight != nullptr, p.rotated, sound, s, rcp_approx(s));
+      q[e / 4] = (q[e / 4] & ~(0xffu << (8 * (e % 4)))) | (((uint32_t)code & 0xffu) << (8 * (e % 4)));
+    }
+  return make_uint2(q[0], q[1]);
+}
+
+// Where a packed row goes: its position and the pool row.
+struct Place {
+  int pos;
+  int64_t pool_row;          // -1: the page lies outside the pool
+  bool ok;
+};
+__device__ __forceinline__ Place place_row(const RopeAppendArgs& a, int row, int lane) {
+  Place pl = {0, -1, false};
+  const int b = find_sequence(a.q_start, a.B, row, lane);
+  if (b < 0 || b >= a.B) return pl;                        // behind the last sequence
+  const int q0 = a.q_start[b], q1 = a.q_start[b + 1], kv = a.kv_lens[b];
+  if (q0 < 0 || q1 <= row || q1 > a.n || kv < q1 - q0 || kv > a.T_max) {
+    if (lane == 0) set_dev_err(a.err, FA3_DEVERR_LENS);
+    return pl;
+  }
+  pl.pos = kv - (q1 - row);
+  if (a.r.cos_sin && pl.pos >= a.r.table_len) {
+    if (lane == 0) set_dev_err(a.err, FA3_DEVERR_POS);
+    return pl;
+  }
+  pl.ok = true;
+  const uint32_t pi = divu32((uint32_t)pl.pos, a.div_ps);
+  const int pg = a.block_table[(int64_t)b * a.max_pages + pi];
+  if (pg >= 0 && pg < a.num_pages)
+    pl.pool_row = (int64_t)pg * a.page_size + (pl.pos - (int)pi * a.page_size);
+  else if (lane == 0)
+    set_dev_err(a.err, FA3_DEVERR_PAGE);
+  return pl;
+}
+
+template <int LANES, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeAppendArgs a) {
+  constexpr int rows = 32 / LANES;
+  const int lane = threadIdx.x & 31;
+  const int i = lane % LANES, sub = lane / LANES;
+  const Lane8 p = lane_place(i, a.r);
+  const uint32_t nt = (uint32_t)a.n * a.chunks;
+  pdl_wait();
+  pdl_launch_dependents();
+  for (uint32_t t = blockIdx.x * kRopeWarps + (threadIdx.x >> 5); t < nt; t += gridDim.x * kRopeWarps) {
+    const int row = (int)divu32(t, a.div_chunks);
+    uint32_t chunk = t - (uint32_t)row * a.chunks;
+    const bool is_q = chunk < a.q_chunks;
+    if (!is_q) chunk -= a.q_chunks;
+    const bool is_v = !is_q && chunk >= a.k_chunks;
+    if (is_v) chunk -= a.k_chunks;
+    const HeadRows T = is_q ? a.q : is_v ? a.v : a.k;
+    const float* scale = is_q ? a.q_scale : is_v ? a.v_scale : a.k_scale;
+    const int H = is_q ? a.Hq : a.Hkv;
+    const int h_first = (int)(chunk * a.per_chunk) + sub;
+    const int n_all = min((int)a.per_chunk, H - (h_first - sub));      // the task's rows
+    const int n_in = p.in ? n_all - sub : 0;                           // as this lane counts them
+    const int64_t step = (int64_t)rows * T.sh;
+    const uint16_t* x1 = T.x + row * T.ss + (int64_t)h_first * T.sh + p.o1;
+    const int gap = p.o2 - p.o1;
+    const float* sp = scale + h_first;
+    // Two passes (rows rows each) are loaded while the two before them are worked on; the
+    // first ones' loads go out before the look-ups of the token's place.
+    uint2 cur[2][2], nxt[2][2];
+    float s_cur[2], s_nxt[2];
+    auto fetch = [&](uint2 (&d)[2][2], float (&sc)[2], int h) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        d[u][0] = d[u][1] = make_uint2(0u, 0u);
+        sc[u] = 1.f;
+        if (h + u * rows < n_in) {
+          d[u][0] = load4(x1 + u * step);
+          d[u][1] = load4(x1 + u * step + gap);
+          sc[u] = sp[u * rows];
+        }
+      }
+      x1 += 2 * step;
+      sp += 2 * rows;
+    };
+    fetch(cur, s_cur, 0);
+    const Place pl = place_row(a, row, lane);
+    if (!pl.ok || (!is_q && pl.pool_row < 0)) continue;
+    int8_t* y1 = (is_q ? a.q_out + (int64_t)row * a.Hq * a.r.D
+                       : (is_v ? a.v_cache : a.k_cache) + pl.pool_row * a.Hkv * a.r.D) + (int64_t)h_first * a.r.D + p.o1;
+    const int y_step = rows * a.r.D;
+    const bool norm = T.weight != nullptr;
+    Lane8 pt = p;
+    pt.rotated = p.rotated && !is_v;                        // v: multiplied by 1 and 0
+    const Turn w = make_turn<INTER>(pt, a.r, pl.pos, T.weight, i);
+    float band = 0.f;                                       // the largest factor, times the tie band
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float g0, g1, g2, g3;
+      f32x2_unpack(w.ac[j], g0, g1);
+      f32x2_unpack(w.nbs[j], g2, g3);
+      band = fmaxf(band, fmaxf(fmaxf(fabsf(g0), fabsf(g1)), fmaxf(fabsf(g2), fabsf(g3))));
+      f32x2_unpack(w.bc[j], g0, g1);
+      f32x2_unpack(w.as[j], g2, g3);
+      band = fmaxf(band, fmaxf(fmaxf(fabsf(g0), fabsf(g1)), fmaxf(fabsf(g2), fabsf(g3))));
+    }
+    band *= norm ? kTieNorm : kTiePlain;
+    const float lim_min = 0.5f - 32768.f * (norm ? kTieNorm : kTiePlain);
+    const f2 magic = f32x2_pack(kCodeMagic, kCodeMagic);
+    for (int h = 0; h < n_all; h += 2 * rows) {
+      fetch(nxt, s_nxt, h + 2 * rows);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (u && h + rows >= n_all) break;
+        const float s = s_cur[u];
+        const Pairs v = unpack_pairs<INTER>(cur[u][0], cur[u][1]);
+        float f = rcp_approx(s);
+        bool sound = exact_scale(s);
+        if (norm) {
+          const float ss = row_squares<LANES>(v);
+          sound = sound & (ss >= 7.8886e-31f) & (ss <= 1.2676e30f);
+          f *= rsqrt_approx(fmaf(ss, a.r.inv_D, a.r.eps));
+        }
+        const f2 ff = f32x2_pack(f, f);
+        uint32_t t[8];
+        float d[8], m = 0.f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const f2 ya = f32x2_fma(v.a[j], w.ac[j], mul2(v.b[j], w.nbs[j]));
+          const f2 yb = f32x2_fma(v.b[j], w.bc[j], mul2(v.a[j], w.as[j]));
+          const f2 ta = f32x2_fma(ya, ff, magic), tb = f32x2_fma(yb, ff, magic);          // magic + RNE(t)
+          const f2 da = f32x2_fma(ya, ff, f32x2_sub(magic, ta)), db = f32x2_fma(yb, ff, f32x2_sub(magic, tb));
+          const int at[4] = {first<INTER>(2 * j), first<INTER>(2 * j + 1), second<INTER>(2 * j), second<INTER>(2 * j + 1)};
+          float t0, t1, t2, t3, a0, a1, b0, b1;
+          f32x2_unpack(ta, t0, t1);
+          f32x2_unpack(tb, t2, t3);
+          t[at[0]] = __float_as_uint(t0), t[at[1]] = __float_as_uint(t1);
+          t[at[2]] = __float_as_uint(t2), t[at[3]] = __float_as_uint(t3);
+          f32x2_unpack(da, d[at[0]], d[at[1]]);
+          f32x2_unpack(db, d[at[2]], d[at[3]]);
+          f32x2_unpack(v.a[j], a0, a1);
+          f32x2_unpack(v.b[j], b0, b1);
+          m = max3_nan(m, fabsf(a0) + fabsf(b0), fabsf(a1) + fabsf(b1));
+        }
+        // codes: the low 16 bits of t, clamped in pairs, then the low bytes
+        uint2 code;
+        code.x = __byte_perm(clamp_code2(__byte_perm(t[0], t[1], 0x5410)), clamp_code2(__byte_perm(t[2], t[3], 0x5410)), 0x6420);
+        code.y = __byte_perm(clamp_code2(__byte_perm(t[4], t[5], 0x5410)), clamp_code2(__byte_perm(t[6], t[7], 0x5410)), 0x6420);
+        const float lim = fmaf(-m * band, f, 0.5f);
+        const float dm = max3(max3(fabsf(d[0]), fabsf(d[1]), fabsf(d[2])), max3(fabsf(d[3]), fabsf(d[4]), fabsf(d[5])),
+                              fmaxf(fabsf(d[6]), fabsf(d[7])));
+        const bool sure = sound & (dm <= lim) & (lim >= lim_min);
+        const bool live = h + u * rows < n_in;
+        if (__any_sync(0xffffffffu, live & !sure)) {
+          uint32_t again = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (live & (!sound | !(lim >= lim_min) | !(fabsf(d[e]) <= lim))) again |= 1u << e;
+          code = decide_row<LANES, INTER>(a.r, T.weight, cur[u][0], cur[u][1], s, code, again, sound, is_v, pl.pos, i);
+        }
+        if (live) {
+          *reinterpret_cast<uint32_t*>(y1 + u * y_step) = code.x;
+          *reinterpret_cast<uint32_t*>(y1 + u * y_step + gap) = code.y;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) cur[u][0] = nxt[u][0], cur[u][1] = nxt[u][1], s_cur[u] = s_nxt[u];
+      y1 += 2 * y_step;
+    }
+  }
+}
+
+template <int LANES>
+auto append_kernel(bool inter) {
+  return inter ? rope_append_kernel<LANES, true> : rope_append_kernel<LANES, false>;
+}
+template <int LANES>
+auto norm_kernel(bool inter, bool f32) {
+  return f32 ? (inter ? norm_rope_kernel<float, LANES, true> : norm_rope_kernel<float, LANES, false>)
+             : (inter ? norm_rope_kernel<__nv_bfloat16, LANES, true> : norm_rope_kernel<__nv_bfloat16, LANES, false>);
 }
 
 inline bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
@@ -356,7 +607,7 @@ int rot_args(const float* cos_sin, int table_len, int rot_dim, int interleaved, 
     rot_dim = 0;
     table_len = 0;
   }
-  *r = RotArgs{cos_sin, table_len, rot_dim, interleaved ? 1 : 0, D, eps};
+  *r = RotArgs{cos_sin, table_len, rot_dim, interleaved ? 1 : 0, D, eps, 1.f / (float)D, 1.0 / (double)D};
   return FA3_OK;
 }
 
@@ -366,7 +617,7 @@ int lanes_per_row(int D) { return D <= 64 ? 8 : D <= 128 ? 16 : 32; }
 // longer tasks, which read a token's table row and place once for more heads.
 int heads_per_task(int64_t tokens, int heads, int rows, int sms) {
   const int64_t passes = tokens * ((heads + rows - 1) / rows);
-  const int64_t per = std::max<int64_t>(1, std::min<int64_t>(8, passes / ((int64_t)sms * 64)));
+  const int64_t per = std::max<int64_t>(1, std::min<int64_t>(8, passes / ((int64_t)sms * 24)));
   return (int)per * rows;
 }
 
@@ -400,22 +651,24 @@ FA3_API int fa3_norm_rope(const uint16_t* q, const uint16_t* k, const uint16_t* 
   if (st != FA3_OK) return st;
   a.q = HeadRows{q, q_weight, q_sb, q_ss, q_sh};
   a.k = HeadRows{k, k_weight, k_sb, k_ss, k_sh};
-  a.q_out = q_out; a.k_out = k_out;
-  a.qo_sb = qo_sb; a.qo_ss = qo_ss; a.qo_sh = qo_sh; a.ko_sb = ko_sb; a.ko_ss = ko_ss; a.ko_sh = ko_sh;
+  a.qo = HeadOut{q_out, qo_sb, qo_ss, qo_sh};
+  a.ko = HeadOut{k_out, ko_sb, ko_ss, ko_sh};
   a.pos = pos; a.S = S; a.Hq = Hq; a.Hkv = Hkv; a.err = dev_err;
-  a.row_lanes = lanes_per_row(D);
-  const int rows = 32 / a.row_lanes, heads = Hq + Hkv;
+  const int lanes = lanes_per_row(D), rows = 32 / lanes, heads = Hq + Hkv;
   a.tokens = (uint32_t)((int64_t)B * S);
   a.per_chunk = (uint32_t)heads_per_task(a.tokens, heads, rows, sms);
-  a.chunks = (heads + a.per_chunk - 1) / a.per_chunk;
+  a.q_chunks = (Hq + a.per_chunk - 1) / a.per_chunk;
+  a.chunks = a.q_chunks + (Hkv + a.per_chunk - 1) / a.per_chunk;
   const int64_t tasks = (int64_t)a.tokens * a.chunks;
   if (tasks >= ((int64_t)1 << 31)) return FA3_ERANGE;
   a.div_chunks = make_divu32(a.chunks);
   a.div_S = make_divu32((uint32_t)S);
   const int64_t blocks = std::min<int64_t>((tasks + kRopeWarps - 1) / kRopeWarps, (int64_t)sms * 8);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return cuda_status(launch_pdl(out_f32 ? norm_rope_kernel<float> : norm_rope_kernel<__nv_bfloat16>,
-                                dim3((unsigned)blocks), dim3(kRopeThreads), 0, s, a));
+  const bool inter = a.r.interleaved != 0, f32 = out_f32 != 0;
+  auto* kernel = lanes == 8 ? norm_kernel<8>(inter, f32) : lanes == 16 ? norm_kernel<16>(inter, f32)
+                                                                       : norm_kernel<32>(inter, f32);
+  return cuda_status(launch_pdl(kernel, dim3((unsigned)blocks), dim3(kRopeThreads), 0, s, a));
 }
 
 FA3_API int fa3_rope_append_gqa_paged(const uint16_t* q, const uint16_t* k, const uint16_t* v,
@@ -453,15 +706,19 @@ FA3_API int fa3_rope_append_gqa_paged(const uint16_t* q, const uint16_t* k, cons
   a.block_table = block_table; a.q_start = q_start; a.kv_lens = kv_lens;
   a.n = n; a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.num_pages = num_pages; a.page_size = page_size; a.max_pages = max_pages;
   a.T_max = max_pages * page_size; a.err = dev_err;
-  a.row_lanes = lanes_per_row(D);
-  const int rows = 32 / a.row_lanes, heads = Hq + 2 * Hkv;
+  const int lanes = lanes_per_row(D), rows = 32 / lanes, heads = Hq + 2 * Hkv;
   a.per_chunk = (uint32_t)heads_per_task(n, heads, rows, sms);
-  a.chunks = (heads + a.per_chunk - 1) / a.per_chunk;
+  a.q_chunks = (Hq + a.per_chunk - 1) / a.per_chunk;
+  a.k_chunks = (Hkv + a.per_chunk - 1) / a.per_chunk;
+  a.chunks = a.q_chunks + 2 * a.k_chunks;
   const int64_t tasks = (int64_t)n * a.chunks;
   if (tasks >= ((int64_t)1 << 31)) return FA3_ERANGE;
   a.div_chunks = make_divu32(a.chunks);
   a.div_ps = make_divu32((uint32_t)page_size);
   const int64_t blocks = std::min<int64_t>((tasks + kRopeWarps - 1) / kRopeWarps, (int64_t)sms * 8);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return cuda_status(launch_pdl(rope_append_kernel, dim3((unsigned)blocks), dim3(kRopeThreads), 0, s, a));
+  const bool inter = a.r.interleaved != 0;
+  auto* kernel = lanes == 8 ? append_kernel<8>(inter) : lanes == 16 ? append_kernel<16>(inter)
+                                                                    : append_kernel<32>(inter);
+  return cuda_status(launch_pdl(kernel, dim3((unsigned)blocks), dim3(kRopeThreads), 0, s, a));
 }
