@@ -9,10 +9,29 @@
 //   out[i, h] = bf16( v_scale[g] * sum_t softmax(s)_t * v8[t, g] )
 //   t <= kv_len_b - n_b + i  (chunk)      t < kv_len_b  (cross)
 //
-// A row block of a KV head is 2 x P positions x the group's G heads, P = 128 / G: two
-// tiles of 128 TMEM lanes that share every converted key tile.  int8 codes are exact in
-// fp16 and a 128-term sum of their products stays below 2^24, so kind::f16 MMAs with
-// fp32 accumulation give the exact integer score.
+// Work.  A unit is a row block of one sequence and KV head: up to 2 x P positions x the
+// group's G heads (P = 128 / G), so that a converted K/V tile of 128 keys feeds up to 256
+// rows.  The pipe works in steps, Q.K^T and P.V of 128 rows and 128 keys:
+//   * two row tiles: each key tile is two steps, of tile 0 and of tile 1;
+//   * one row tile (up to P positions left, a decode token or a short draft): the key tiles
+//     alternate between the two score and accumulator buffers, and the two results are
+//     merged in the CTA.  Either way step t works on buffer t & 1, and while a buffer's
+//     softmax runs the tensor pipe has the other buffer's step.
+// All steps of all units, plus a unit's fixed cost in steps, lie on one line that is cut into equal
+// parts, one per SM: a CTA takes whole units and at most one part of a unit at either
+// end.  A cut unit's parts leave unnormalised O, maximum and sum in the workspace, and
+// chunk_combine_kernel merges them, so one long sequence and a ragged batch both fill the GPU.
+//
+// Roles in the CTA (384 threads): warp 0 issues the MMAs; warps 1-3 look keys up in the
+// block table, load int8 K and V tiles one tile ahead into registers and write them as fp16
+// core matrices into one of two stages; warps 4-7 and 8-11 (one row each) run the softmax of
+// buffers 0 and 1.  int8 codes are exact in fp16 and a 128-term sum of their products
+// stays below 2^24, so kind::f16 MMAs with fp32 accumulation give the exact integer
+// score (sm_103a has no integer tcgen05 kind).  P (fp16, relative to a lazily moved row
+// maximum) is written over its scores in TMEM and is the A operand of P.V; the row sum is
+// float32 over the unrounded weights.  TMEM: O_0, O_1, S_0, S_1, 128 columns each.
+// Every wait is bounded; on time-out the kernel sets FA3_DEVERR_TIMEOUT, drains its
+// MMAs, frees its TMEM and returns.
 #include "fa3_common.cuh"
 #include "fa3_tc.cuh"
 
@@ -20,6 +39,7 @@
 #include <cuda_fp16.h>
 #include <math_constants.h>
 
+#include <algorithm>
 #include <cmath>
 
 namespace fa3 {
@@ -27,28 +47,35 @@ namespace {
 
 constexpr int kD = 128;            // head dim
 constexpr int kKeys = 128;         // keys per tile
-constexpr int kRowsP = 128;        // rows (TMEM lanes) per query tile
-constexpr int kThreadsP = 384;     // warp 0: MMA, warps 1-3: converters, 4-7: softmax A, 8-11: softmax B
-constexpr int kConvP = 96;
-constexpr uint32_t TMP_O = 0, TMP_S = 256;                 // O_x [128x, +128), S_x [256 + 128x, +128)
+constexpr int kRows = 128;         // rows (TMEM lanes) per row tile
+constexpr int kThreadsC = 384;     // warp 0: MMA, warps 1-3: converters, 4-7 / 8-11: softmax of buffer 0 / 1
+constexpr int kConv = 96;
+constexpr uint32_t TM_O = 0, TM_S = 256;                   // O_x [128x, +128), S_x [256 + 128x, +128)
 constexpr uint32_t KV_TILE = kKeys * kD * 2;               // 32 KB of fp16
-constexpr uint32_t Q_TILE = kRowsP * kD * 2;               // 32 KB of fp16
-constexpr uint32_t OFFP_Q = 0;                             // 2 x fp16 query rows, K-major
-constexpr uint32_t OFFP_K = OFFP_Q + 2 * Q_TILE;           // 2 stages
-constexpr uint32_t OFFP_V = OFFP_K + 2 * KV_TILE;          // 2 stages
-constexpr uint32_t OFFP_BAR = OFFP_V + 2 * KV_TILE;
+constexpr uint32_t Q_TILE = kRows * kD * 2;                // 32 KB of fp16
+constexpr uint32_t OFF_Q = 0;                              // 2 x fp16 query rows, K-major
+constexpr uint32_t OFF_K = OFF_Q + 2 * Q_TILE;             // 2 stages
+constexpr uint32_t OFF_V = OFF_K + 2 * KV_TILE;            // 2 stages
+constexpr uint32_t OFF_ML = OFF_V + 2 * KV_TILE;           // [2][128] float2: (m, l) of a single row tile's halves
+constexpr uint32_t OFF_BAR = OFF_ML + 2 * kRows * 8;
 enum {
-  PB_K_FULL = 0, PB_K_EMPTY = 2, PB_V_FULL = 4, PB_V_EMPTY = 6,
-  PB_S_FULL = 8,                   // [2]: tile x's scores of the current key tile
-  PB_P_FULL = 10,                  // [2]: tile x's P written over its S
-  PB_PV_DONE = 12,                 // [2]: P_x.V done (O_x holds it; S_x free)
-  PB_Q_READY = 14, PB_DRAIN, PB_N
+  B_K_FULL = 0, B_K_EMPTY = 2, B_V_FULL = 4, B_V_EMPTY = 6,
+  B_S_FULL = 8,                    // [2]: buffer x's scores of its next step
+  B_P_FULL = 10,                   // [2]: P written over S_x
+  B_PV_DONE = 12,                  // [2]: P_x.V done (O_x holds it; S_x free)
+  B_ML = 14,                       // [2]: buffer x's (m, l) of a single row tile written
+  B_READ = 16,                     // [2]: warps of buffer x have read both O of a single row tile
+  B_Q_READY = 18, B_DRAIN, B_N
 };
-constexpr uint32_t OFFP_TSLOT = OFFP_BAR + 8 * PB_N;
-constexpr uint32_t OFFP_ABORT = OFFP_TSLOT + 4;
-constexpr uint32_t SMEM_PREFILL = OFFP_BAR + 256 + 1024;   // + alignment slack
-static_assert(OFFP_ABORT + 4 <= OFFP_BAR + 256, "barrier area");
-static_assert(SMEM_PREFILL <= 232448, "shared memory");
+constexpr uint32_t OFF_TSLOT = OFF_BAR + 8 * B_N;
+constexpr uint32_t OFF_ABORT = OFF_TSLOT + 4;
+constexpr uint32_t SMEM_CHUNK = OFF_BAR + 256 + 1024;      // + alignment slack
+static_assert(OFF_ABORT + 4 <= OFF_BAR + 256, "barrier area");
+static_assert(SMEM_CHUNK <= 232448, "shared memory");
+
+// A unit's cost beside its steps (its query rows, pipeline fill and epilogue), in steps, and
+// the least part of the line a CTA takes.
+constexpr int kUnitCost = 2, kLeastPart = 6;
 
 struct ChunkParams {
   const int8_t* q;              // [n][Hq][128]
@@ -61,357 +88,609 @@ struct ChunkParams {
   const int32_t* kv_lens;       // [B]
   const int32_t* block_table;   // [B][max_pages], or nullptr: sequence b's keys are rows b*T ..
   uint16_t* out;                // bf16 [n][Hq][128]
+  float4* part_o;               // [2 * CTAs][32][rows_max]: O of a cut unit's part, column group by row
+  float2* part_ml;              // [2 * CTAs][rows_max]
   int32_t* err;
-  int n, B, T, Hq, Hkv, G, P, causal;
+  int n, B, T, Hq, Hkv, G, P, causal, ctas, rows_max;
   int page_size, max_pages, num_pages;
   DivU32 div_ps;                // / page_size
   float sm_log2;                // softmax_scale * log2(e)
 };
 
-// The new rows and keys of sequence b; false for an empty or invalid sequence.
-__device__ __forceinline__ bool sequence_of(const ChunkParams& p, int b, int& q0, int& nq, int& nkv, bool report) {
-  q0 = p.q_start[b];
+// ------------------------------------------------------------------ the line of steps
+struct Seq {
+  int q0, nq, nkv;
+};
+// The new rows and keys of sequence b; nq = 0 for an empty or invalid sequence.
+__device__ __forceinline__ Seq sequence_of(const ChunkParams& p, int b, bool report) {
+  Seq s;
+  s.q0 = p.q_start[b];
   const int q1 = p.q_start[b + 1];
-  nkv = p.kv_lens[b];
-  nq = q1 - q0;
-  if (q0 < 0 || q1 < q0 || q1 > p.n || (nq > 0 && (nkv < (p.causal ? nq : 0) || nkv > p.T))) {
+  s.nkv = p.kv_lens[b];
+  s.nq = q1 - s.q0;
+  if (s.q0 < 0 || q1 < s.q0 || q1 > p.n || (s.nq > 0 && (s.nkv < (p.causal ? s.nq : 0) || s.nkv > p.T))) {
     if (report) set_dev_err(p.err, FA3_DEVERR_LENS);
-    return false;
+    s.nq = 0;
   }
-  return nq > 0;
+  return s;
+}
+__device__ __forceinline__ int blocks_of(const ChunkParams& p, const Seq& s) { return (s.nq + 2 * p.P - 1) / (2 * p.P); }
+// Key tiles of row block rb, and its cost.
+__device__ __forceinline__ int tiles_of(const ChunkParams& p, const Seq& s, int rb) {
+  const int keys = p.causal ? s.nkv - s.nq + min(s.nq, (rb + 1) * 2 * p.P) : s.nkv;
+  return (keys + kKeys - 1) / kKeys;
+}
+__device__ __forceinline__ bool is_dual(const ChunkParams& p, const Seq& s, int rb) { return s.nq - rb * 2 * p.P > p.P; }
+__device__ __forceinline__ int cost_of(const ChunkParams& p, const Seq& s, int rb) {
+  return kUnitCost + tiles_of(p, s, rb) * (is_dual(p, s, rb) ? 2 : 1);
+}
+// Cost of all row blocks of one KV head of the sequence.
+__device__ __forceinline__ int64_t sequence_cost(const ChunkParams& p, const Seq& s) {
+  const int nb = blocks_of(p, s);
+  if (nb == 0) return 0;
+  int64_t c = cost_of(p, s, nb - 1) + (int64_t)(nb - 1) * kUnitCost;
+  if (p.causal) {
+    int64_t t = 0;
+    int keys = s.nkv - s.nq + 2 * p.P + kKeys - 1;
+    for (int rb = 0; rb < nb - 1; ++rb, keys += 2 * p.P) t += keys / kKeys;
+    c += 2 * t;
+  } else {
+    c += 2 * (int64_t)(nb - 1) * ((s.nkv + kKeys - 1) / kKeys);
+  }
+  return c;
 }
 
-__global__ void __launch_bounds__(kThreadsP, 1) gqa_chunk_kernel(const __grid_constant__ ChunkParams p) {
+__device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {     // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  return v;
+}
+
+// Cost of the whole batch (the warp together).
+__device__ __forceinline__ int64_t total_cost(const ChunkParams& p, int lane, bool report) {
+  int64_t sum = 0;
+  for (int b = lane; b < p.B; b += 32) sum += sequence_cost(p, sequence_of(p, b, report));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum * p.Hkv;
+}
+// CTAs that take part, and where CTA c's part of the line begins.
+__device__ __forceinline__ int parts_of(const ChunkParams& p, int64_t total) {
+  const int64_t most = total / kLeastPart;
+  return (int)(most < 1 ? 1 : most < p.ctas ? most : p.ctas);
+}
+__device__ __forceinline__ int64_t part_begin(int64_t total, int parts, int c) { return total * c / parts; }
+
+// A position on the line: unit (b, g, rb) and the offset into it.
+struct Cursor {
+  int b, g, rb;
+  Seq s;
+  int64_t off;
+};
+// First sequence from b on with new rows (the warp together); b = B when there is none.
+__device__ __forceinline__ void to_sequence(const ChunkParams& p, Cursor& c, int b, int lane) {
+  for (; b < p.B; b += 32) {
+    Seq s = {0, 0, 0};
+    if (b + lane < p.B) s = sequence_of(p, b + lane, false);
+    const unsigned have = __ballot_sync(0xffffffffu, s.nq > 0);
+    if (have) {
+      const int l = __ffs(have) - 1;
+      c.b = b + l;
+      c.s.q0 = __shfl_sync(0xffffffffu, s.q0, l);
+      c.s.nq = __shfl_sync(0xffffffffu, s.nq, l);
+      c.s.nkv = __shfl_sync(0xffffffffu, s.nkv, l);
+      return;
+    }
+  }
+  c.b = p.B;
+  c.s = Seq{0, 0, 0};
+}
+// The unit that holds position x of the line (x < total).
+__device__ __forceinline__ Cursor seek(const ChunkParams& p, int64_t x, int lane) {
+  Cursor c = {p.B, 0, 0, {0, 0, 0}, 0};
+  for (int base = 0; base < p.B; base += 32) {
+    Seq s = {0, 0, 0};
+    if (base + lane < p.B) s = sequence_of(p, base + lane, false);
+    const int64_t mine = sequence_cost(p, s), inc = warp_scan(mine * p.Hkv, lane);
+    const unsigned beyond = __ballot_sync(0xffffffffu, inc > x);
+    if (beyond) {
+      const int l = __ffs(beyond) - 1;
+      const int64_t per_head = __shfl_sync(0xffffffffu, mine, l);
+      x -= __shfl_sync(0xffffffffu, inc, l) - per_head * p.Hkv;
+      c.b = base + l;
+      c.s.q0 = __shfl_sync(0xffffffffu, s.q0, l);
+      c.s.nq = __shfl_sync(0xffffffffu, s.nq, l);
+      c.s.nkv = __shfl_sync(0xffffffffu, s.nkv, l);
+      c.g = (int)(x / per_head);
+      x -= c.g * per_head;
+      break;
+    }
+    x -= __shfl_sync(0xffffffffu, inc, 31);
+  }
+  const int nb = blocks_of(p, c.s);
+  for (int base = 0; base < nb; base += 32) {
+    const int64_t mine = base + lane < nb ? cost_of(p, c.s, base + lane) : 0, inc = warp_scan(mine, lane);
+    const unsigned beyond = __ballot_sync(0xffffffffu, inc > x);
+    if (beyond) {
+      const int l = __ffs(beyond) - 1;
+      c.rb = base + l;
+      c.off = x - __shfl_sync(0xffffffffu, inc - mine, l);
+      break;
+    }
+    x -= __shfl_sync(0xffffffffu, inc, 31);
+  }
+  return c;
+}
+
+// Key tile at which a part that begins `off` into a unit begins.
+__device__ __forceinline__ int tile_at(int64_t off, bool dual, int nt) {
+  const int64_t t = off <= kUnitCost ? 0 : (off - kUnitCost) >> (dual ? 1 : 0);
+  return (int)(t < nt ? t : nt);
+}
+
+// What a CTA does of a unit: key tiles [t0, t1) of nt, for row block rb.
+struct Part {
+  int b, g, rb, q0, nq, nkv, t0, t1, nt;
+  bool dual, first;                 // first: the part holds the unit's begin
+  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == nt; }
+};
+
+// A CTA's parts in order; every warp walks them by itself.
+struct Walk {
+  Cursor c;
+  int64_t left;
+  __device__ __forceinline__ void begin(const ChunkParams& p, int64_t total, int parts, int cta, int lane) {
+    const int64_t x = part_begin(total, parts, cta);
+    left = part_begin(total, parts, cta + 1) - x;
+    if (left > 0) c = seek(p, x, lane);
+  }
+  __device__ __forceinline__ bool next(const ChunkParams& p, Part& u, int lane) {
+    while (left > 0) {
+      const int nt = tiles_of(p, c.s, c.rb);
+      const bool dual = is_dual(p, c.s, c.rb);
+      const int64_t cost = kUnitCost + (int64_t)nt * (dual ? 2 : 1);
+      const int64_t take = cost - c.off < left ? cost - c.off : left;
+      u = Part{c.b, c.g, c.rb, c.s.q0, c.s.nq, c.s.nkv, tile_at(c.off, dual, nt), tile_at(c.off + take, dual, nt), nt,
+               dual, c.off == 0};
+      if (c.off + take == cost) u.t1 = nt;
+      left -= take;
+      c.off = 0;
+      if (++c.rb == blocks_of(p, c.s)) {
+        c.rb = 0;
+        if (++c.g == p.Hkv) {
+          c.g = 0;
+          if (left > 0) to_sequence(p, c, c.b + 1, lane);
+        }
+      }
+      if (u.t0 < u.t1 || (nt == 0 && u.first)) return true;
+    }
+    return false;
+  }
+};
+
+// Cache row of key t of sequence b, or -1 for a block-table entry outside the pool.
+__device__ __forceinline__ int64_t key_row(const ChunkParams& p, int b, int t) {
+  if (!p.block_table) return (int64_t)b * p.T + t;
+  const uint32_t pi = divu32((uint32_t)t, p.div_ps);
+  const int pg = __ldg(p.block_table + (int64_t)b * p.max_pages + pi);
+  if (pg < 0 || pg >= p.num_pages) {
+    set_dev_err(p.err, FA3_DEVERR_PAGE);
+    return -1;
+  }
+  return (int64_t)pg * p.page_size + (t - (int)pi * p.page_size);
+}
+
+// The wait for this thread's TMEM loads, which also orders the uses of v behind it.
+__device__ __forceinline__ void wait_ld32(uint32_t* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                 "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                 "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+               :: "memory");
+}
+
+__global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_constant__ ChunkParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = blockIdx.y;
-  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + OFFP_ABORT);
-  auto bar = [&](int i) { return sbase + OFFP_BAR + 8u * (uint32_t)i; };
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + OFF_ABORT);
+  auto bar = [&](int i) { return sbase + OFF_BAR + 8u * (uint32_t)i; };
   pdl_wait();
   pdl_launch_dependents();
 
-  // Row block blockIdx.x: the sequences' counts of row blocks, 32 sequences at a time.
-  int b = -1, rb = 0, q0 = 0, nq = 0, nkv = 0;
-  for (int base = 0, seen = 0; base < p.B; base += 32) {
-    int c = 0, s0, sq, sk;
-    if (base + lane < p.B && sequence_of(p, base + lane, s0, sq, sk, g == 0 && warp == 0))
-      c = (sq + 2 * p.P - 1) / (2 * p.P);
-    int inc = c;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
-    const unsigned beyond = __ballot_sync(0xffffffffu, seen + inc > (int)blockIdx.x);
-    if (beyond) {
-      const int l = __ffs(beyond) - 1;
-      b = base + l;
-      rb = (int)blockIdx.x - seen - __shfl_sync(0xffffffffu, inc - c, l);
-      break;
-    }
-    seen += __shfl_sync(0xffffffffu, inc, 31);
-  }
-  if (b < 0) return;
-  sequence_of(p, b, q0, nq, nkv, false);
-  const int i0 = rb * 2 * p.P;                             // first position of tile A; tile B follows
-  const int prefix = nkv - nq;
-  const int n_keys = p.causal ? prefix + min(nq, i0 + 2 * p.P) : nkv;
-  const int nt = (n_keys + kKeys - 1) / kKeys;
+  const int64_t total = total_cost(p, lane, blockIdx.x == 0 && warp == 0);
+  const int parts = parts_of(p, total);
+  if ((int)blockIdx.x >= parts || total == 0) return;
+  Walk walk;
+  walk.begin(p, total, parts, blockIdx.x, lane);
 
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(bar(PB_K_FULL + s), kConvP);
-      mbar_init(bar(PB_K_EMPTY + s), 1);
-      mbar_init(bar(PB_V_FULL + s), kConvP);
-      mbar_init(bar(PB_V_EMPTY + s), 1);
-      mbar_init(bar(PB_S_FULL + s), 1);
-      mbar_init(bar(PB_P_FULL + s), 4);
-      mbar_init(bar(PB_PV_DONE + s), 1);
+      mbar_init(bar(B_K_FULL + s), kConv);
+      mbar_init(bar(B_K_EMPTY + s), 1);
+      mbar_init(bar(B_V_FULL + s), kConv);
+      mbar_init(bar(B_V_EMPTY + s), 1);
+      mbar_init(bar(B_S_FULL + s), 1);
+      mbar_init(bar(B_P_FULL + s), 4);
+      mbar_init(bar(B_PV_DONE + s), 1);
+      mbar_init(bar(B_ML + s), 4);
+      mbar_init(bar(B_READ + s), 4);
     }
-    mbar_init(bar(PB_Q_READY), 8);
-    mbar_init(bar(PB_DRAIN), 1);
+    mbar_init(bar(B_Q_READY), 8);
+    mbar_init(bar(B_DRAIN), 1);
     *abort_flag = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-                 ::"r"(sbase + OFFP_TSLOT), "r"(512) : "memory");
+                 ::"r"(sbase + OFF_TSLOT), "r"(512) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFFP_TSLOT);
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TSLOT);
 
   if (warp == 0) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      const uint32_t id_qk = idesc_f16(kRowsP, kKeys, false, false);
-      const uint32_t id_pv = idesc_f16(kRowsP, kD, false, true);
-      bool ok = wait_bar(bar(PB_Q_READY), 0, abort_flag, p.err);
-      // S_x = Q_x . K_j^T: Q_x the K-major A operand in shared memory (8-row core
-      // groups 128 B apart, 8-wide d groups 2048 B apart), K the K-major B operand.
-      // S_x holds the P of key tile j - 1 until P_x.V(j - 1) is done.
-      auto issue_qk = [&](int j, int x) -> bool {
-        const int s = j & 1;
-        if (!wait_bar(bar(PB_K_FULL + s), (uint32_t)(j >> 1) & 1u, abort_flag, p.err)) return false;
-        if (j > 0 && !wait_bar(bar(PB_PV_DONE + x), (uint32_t)(j - 1) & 1u, abort_flag, p.err)) return false;
-        tc_fence_after();
+    const uint32_t id_qk = idesc_f16(kRows, kKeys, false, false);
+    const uint32_t id_pv = idesc_f16(kRows, kD, false, true);
+    uint32_t kc = 0, done[2] = {0, 0}, units = 0;             // key tiles, steps of each buffer, units so far
+    bool ok = true;
+    Part u;
+    while (ok && walk.next(p, u, lane)) {
+      if (u.nt == 0) continue;
+      const int nk = u.t1 - u.t0, steps = u.dual ? 2 * nk : nk;
+      if (lane == 0) {
+        ok = wait_bar(bar(B_Q_READY), units & 1u, abort_flag, p.err);
+        // S_x = Q.K^T: the row tile's K-major A operand in shared memory (8-row core groups 128 B
+        // apart, 8-wide d groups 2048 B apart), K the K-major B operand.
+        auto issue_qk = [&](int t) -> bool {
+          const int x = t & 1;
+          const uint32_t kt = kc + (uint32_t)(u.dual ? t >> 1 : t), s = kt & 1u;
+          if (!wait_bar(bar(B_K_FULL + s), (kt >> 1) & 1u, abort_flag, p.err)) return false;
+          // S_x holds the P of step t - 2 until its P.V is done
+          if (t >= 2 && !wait_bar(bar(B_PV_DONE + x), (done[x] + (uint32_t)(t >> 1) - 1u) & 1u, abort_flag, p.err))
+            return false;
+          tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < kD / 16; ++kk) {
-          const uint64_t a = sdesc(sbase + OFFP_Q + x * Q_TILE + kk * 4096, 2048, 128);
-          const uint64_t bd = sdesc(sbase + OFFP_K + s * KV_TILE + kk * 4096, 2048, 128);
-          mma_f16(tmem + TMP_S + x * 128, a, bd, id_qk, kk > 0 ? 1u : 0u);
-        }
-        mma_commit(bar(PB_S_FULL + x));
-        if (x == 1) mma_commit(bar(PB_K_EMPTY + s));         // both tiles are done with K_j
-        return true;
-      };
-      // O_x += P_x . V_j: P_x (fp16, written over S_x: column k holds keys 2k, 2k + 1)
-      // is the A operand in TMEM, V the MN-major B operand (token groups 128 B apart,
-      // d groups 2048 B apart).
-      auto issue_pv = [&](int j, int x) -> bool {
-        const int s = j & 1;
-        if (!wait_bar(bar(PB_P_FULL + x), (uint32_t)j & 1u, abort_flag, p.err)) return false;
-        if (x == 0 && !wait_bar(bar(PB_V_FULL + s), (uint32_t)(j >> 1) & 1u, abort_flag, p.err)) return false;
-        tc_fence_after();
+          for (int kk = 0; kk < kD / 16; ++kk) {
+            const uint64_t a = sdesc(sbase + OFF_Q + (u.dual ? x : 0) * Q_TILE + kk * 4096, 2048, 128);
+            const uint64_t bd = sdesc(sbase + OFF_K + s * KV_TILE + kk * 4096, 2048, 128);
+            mma_f16(tmem + TM_S + x * 128, a, bd, id_qk, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(bar(B_S_FULL + x));
+          if (!u.dual || x == 1) mma_commit(bar(B_K_EMPTY + s));    // all steps of this key tile have it
+          return true;
+        };
+        // O_x += P_x.V: P_x (fp16, over S_x: column k holds keys 2k, 2k + 1) is the A operand in
+        // TMEM, V the MN-major B operand (token groups 128 B apart, d groups 2048 B apart).
+        auto issue_pv = [&](int t) -> bool {
+          const int x = t & 1;
+          const uint32_t kt = kc + (uint32_t)(u.dual ? t >> 1 : t), s = kt & 1u;
+          if (!wait_bar(bar(B_P_FULL + x), (done[x] + (uint32_t)(t >> 1)) & 1u, abort_flag, p.err)) return false;
+          if (!wait_bar(bar(B_V_FULL + s), (kt >> 1) & 1u, abort_flag, p.err)) return false;
+          tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk) {
-          const uint64_t bd = sdesc(sbase + OFFP_V + s * KV_TILE + kk * 256, 128, 2048);
-          mma_f16_ts(tmem + TMP_O + x * 128, tmem + TMP_S + x * 128 + kk * 8, bd, id_pv,
-                     (j > 0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < kKeys / 16; ++kk) {
+            const uint64_t bd = sdesc(sbase + OFF_V + s * KV_TILE + kk * 256, 128, 2048);
+            mma_f16_ts(tmem + TM_O + x * 128, tmem + TM_S + x * 128 + kk * 8, bd, id_pv, (t >= 2 || kk > 0) ? 1u : 0u);
+          }
+          mma_commit(bar(B_PV_DONE + x));
+          if (!u.dual || x == 1) mma_commit(bar(B_V_EMPTY + s));
+          return true;
+        };
+        for (int t = 0; t < 2 && t < steps && ok; ++t) ok = issue_qk(t);
+        for (int t = 0; t < steps && ok; ++t) {
+          ok = issue_pv(t);
+          if (ok && t + 2 < steps) ok = issue_qk(t + 2);
         }
-        mma_commit(bar(PB_PV_DONE + x));
-        if (x == 1) mma_commit(bar(PB_V_EMPTY + s));          // both tiles are done with V_j
-        return true;
-      };
-      ok = ok && nt > 0 && issue_qk(0, 0) && issue_qk(0, 1);
-      for (int j = 0; j < nt && ok; ++j) {
-        ok = issue_pv(j, 0) && issue_pv(j, 1);
-        if (ok && j + 1 < nt) ok = issue_qk(j + 1, 0) && issue_qk(j + 1, 1);
       }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      kc += (uint32_t)nk;
+      done[0] += (uint32_t)(steps + 1) / 2;
+      done[1] += (uint32_t)steps / 2;
+      ++units;
+    }
+    if (lane == 0) {
       // Drain: every MMA issued has completed before TMEM is freed.
-      mma_commit(bar(PB_DRAIN));
-      wait_bar(bar(PB_DRAIN), 0, abort_flag, p.err);
+      mma_commit(bar(B_DRAIN));
+      wait_bar(bar(B_DRAIN), 0, abort_flag, p.err);
     }
   } else if (warp < 4) {
     // ------------------------------------------------------ int8 -> fp16 converters
-    // A tile is 2 x 128 rows x 8 chunks of 16 bytes (K, then V).  Each group of 32
-    // consecutive units is 16 tokens x 2 chunks, lane l taking token l % 16 and
-    // chunk l / 16: a warp loads 16 full 32-byte sectors and its fp16 stores hit
-    // every bank once per 128 bytes.  fp16 element (token n, d) lands at
-    // (d / 8) * 2048 + n * 16 + (d % 8) * 2.  K(j) may be written once both
-    // Q.K^T of tile j - 2 are done, V(j) once both P.V of tile j - 2 are.
-    constexpr int kUnits = 2 * kKeys * (kD / 16);                 // 2048
-    constexpr int kPer = (kUnits + kConvP - 1) / kConvP;           // 22
-    const int ct = tid - 32;
+    // A tile of K or V is 32 items of 16 tokens x 2 chunks of 16 bytes, lane l taking token l % 16
+    // and chunk l / 16 of its item: a warp loads 16 full 32-byte sectors and its fp16 stores hit
+    // every bank once per 128 bytes.  fp16 element (token n, d) lands at (d / 8) * 2048 + n * 16 +
+    // (d % 8) * 2.  The next tile's loads go out as soon as this one's registers are written.
+    const int w3 = warp - 1;
+    constexpr int kItems = 11;                               // of 32, every third
     const int64_t row_stride = (int64_t)p.Hkv * kD;
-    const int8_t* kb = p.k + (int64_t)g * kD;
-    const int8_t* vb = p.v + (int64_t)g * kD;
-    // cache row of key t, or -1 for a block-table entry outside the pool
-    auto key_row = [&](int t) -> int64_t {
-      if (!p.block_table) return (int64_t)b * p.T + t;
-      const uint32_t pi = divu32((uint32_t)t, p.div_ps);
-      const int pg = __ldg(p.block_table + (int64_t)b * p.max_pages + pi);
-      if (pg < 0 || pg >= p.num_pages) {
-        set_dev_err(p.err, FA3_DEVERR_PAGE);
-        return -1;
+    Part u = {};
+    bool more = true;
+    int j = 0, n_keys = 0;                                   // next tile to load, of u
+    int64_t rows[8];                                         // cache rows of this lane's tokens, -1: none
+    auto next_tile = [&]() {                                 // false: nothing left
+      while (j >= u.t1) {
+        if (!walk.next(p, u, lane)) return false;
+        j = u.t0;
+        n_keys = p.causal ? u.nkv - u.nq + min(u.nq, (u.rb + 1) * 2 * p.P) : u.nkv;
       }
-      return (int64_t)pg * p.page_size + (t - (int)pi * p.page_size);
-    };
-    auto unit = [&](int i, int& kv, int& n, int& cc) {
-      const int u = ct + kConvP * i;
-      const int grp = u >> 5, l = u & 31;                          // grp < 64 for u < kUnits
-      kv = grp >> 5;
-      n = (grp & 7) * 16 + (l & 15);
-      cc = ((grp >> 3) & 3) * 2 + (l >> 4);
-      return u < kUnits;
-    };
-    for (int j = 0; j < nt; ++j) {
-      const int s = j & 1;
-      const uint32_t par = ((uint32_t)(j >> 1) & 1u) ^ 1u;
-      uint4 w[kPer];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        int kv, n, cc;
-        const bool in = unit(i, kv, n, cc);
-        const int t = j * kKeys + n;
-        w[i] = make_uint4(0u, 0u, 0u, 0u);
-        const int64_t kr = in && t < n_keys ? key_row(t) : -1;
-        if (kr >= 0) w[i] = __ldg(reinterpret_cast<const uint4*>((kv ? vb : kb) + kr * row_stride) + cc);
+      for (int tg = 0; tg < 8; ++tg) {
+        const int t = j * kKeys + tg * 16 + (lane & 15);
+        rows[tg] = t < n_keys ? key_row(p, u.b, t) : -1;
       }
-      bool ok = true;
+      ++j;
+      return true;
+    };
+    uint4 kr[kItems], vr[kItems];
+    auto load = [&](const int8_t* base, uint4 (&r)[kItems]) {
 #pragma unroll
-      for (int half = 0; half < 2 && ok; ++half) {
-        if (!wait_bar(bar((half ? PB_V_EMPTY : PB_K_EMPTY) + s), par, abort_flag, p.err)) { ok = false; break; }
-        uint8_t* dst = smem + (half ? OFFP_V : OFFP_K) + s * KV_TILE;
+      for (int i = 0; i < kItems; ++i) {
+        r[i] = make_uint4(0u, 0u, 0u, 0u);
+        // item w3 + 3 i; rows[] is indexed by a constant: each i meets at most two token groups
+        const int lo = (3 * i) >> 2, hi = (3 * i + 2) >> 2 < 8 ? (3 * i + 2) >> 2 : 7;
+        const int item = w3 + 3 * i;
+        const int64_t kr_ = (item >> 2) == lo ? rows[lo] : rows[hi];
+        if (item < 32 && kr_ >= 0)
+          r[i] = __ldg(reinterpret_cast<const uint4*>(base + kr_ * row_stride) + (item & 3) * 2 + (lane >> 4));
+      }
+    };
+    auto store = [&](uint8_t* dst, const uint4 (&r)[kItems]) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          int kv, n, cc;
-          if (unit(i, kv, n, cc) && kv == half) {
-            uint4 o0, o1;
-            i8x4_to_f16x4(w[i].x, o0.x, o0.y);
-            i8x4_to_f16x4(w[i].y, o0.z, o0.w);
-            i8x4_to_f16x4(w[i].z, o1.x, o1.y);
-            i8x4_to_f16x4(w[i].w, o1.z, o1.w);
-            *reinterpret_cast<uint4*>(dst + (2 * cc) * 2048 + n * 16) = o0;
-            *reinterpret_cast<uint4*>(dst + (2 * cc + 1) * 2048 + n * 16) = o1;
-          }
+      for (int i = 0; i < kItems; ++i) {
+        const int item = w3 + 3 * i;
+        if (item < 32) {
+          const int n = (item >> 2) * 16 + (lane & 15), cc = (item & 3) * 2 + (lane >> 4);
+          uint4 o0, o1;
+          i8x4_to_f16x4(r[i].x, o0.x, o0.y);
+          i8x4_to_f16x4(r[i].y, o0.z, o0.w);
+          i8x4_to_f16x4(r[i].z, o1.x, o1.y);
+          i8x4_to_f16x4(r[i].w, o1.z, o1.w);
+          *reinterpret_cast<uint4*>(dst + (2 * cc) * 2048 + n * 16) = o0;
+          *reinterpret_cast<uint4*>(dst + (2 * cc + 1) * 2048 + n * 16) = o1;
         }
-        fence_proxy_async();
-        mbar_arrive(bar((half ? PB_V_FULL : PB_K_FULL) + s));
       }
-      if (!ok) break;
+      fence_proxy_async();
+    };
+    more = next_tile();
+    if (more) {
+      load(p.k + (int64_t)u.g * kD, kr);
+      load(p.v + (int64_t)u.g * kD, vr);
+    }
+    for (uint32_t kc = 0; more; ++kc) {
+      const uint32_t s = kc & 1u, par = ((kc >> 1) & 1u) ^ 1u;
+      if (!warp_all(wait_bar(bar(B_K_EMPTY + s), par, abort_flag, p.err))) break;
+      store(smem + OFF_K + s * KV_TILE, kr);
+      mbar_arrive(bar(B_K_FULL + s));
+      more = next_tile();
+      if (more) load(p.k + (int64_t)u.g * kD, kr);
+      if (!warp_all(wait_bar(bar(B_V_EMPTY + s), par, abort_flag, p.err))) break;
+      store(smem + OFF_V + s * KV_TILE, vr);
+      mbar_arrive(bar(B_V_FULL + s));
+      if (more) load(p.v + (int64_t)u.g * kD, vr);
     }
   } else {
     // ------------------------------------------------------------ softmax warps
-    const int x = (warp - 4) >> 2;                          // query tile: 0 = A, 1 = B
+    const int x = (warp - 4) >> 2;                          // buffer
     const int r = ((warp - 4) & 3) * 32 + lane;             // row == TMEM lane
     const uint32_t lane_base = (uint32_t)(((warp - 4) & 3) * 32) << 16;
-    const int i = i0 + x * p.P + r / p.G, h = g * p.G + r % p.G;
-    const bool active = r < p.P * p.G && i < nq;
-    const int pos = !active ? -1 : p.causal ? prefix + i : nkv - 1;   // last key this row sees
-    // an inactive row masks every key (its scale stays finite so that -inf * c is -inf)
-    const float c = active ? p.q_scale[h] * p.k_scale[g] * p.sm_log2 : 1.f;
-    const int pos_min = p.causal ? prefix + i0 + x * p.P : nkv - 1;   // the tile's first row's last key
-    const bool ragged = i0 + (x + 1) * p.P > nq || p.P * p.G < kRowsP;   // the tile has inactive rows
-    const uint32_t o_col = tmem + lane_base + TMP_O + x * 128;
-    const uint32_t scol = tmem + lane_base + TMP_S + x * 128;
+    const uint32_t o_col = tmem + lane_base + TM_O + x * 128;
+    const uint32_t scol = tmem + lane_base + TM_S + x * 128;
+    float2* ml = reinterpret_cast<float2*>(smem + OFF_ML);
     auto warp_arrive = [&](int which) {
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(which));
     };
-    // The row's query codes as fp16 into tile x's K-major A operand (chunk of 8 d at
-    // (d / 8) * 2048 + row * 16).
-    {
-      const int8_t* qrow = p.q + ((int64_t)(q0 + (active ? i : 0)) * p.Hq + h) * kD;
-      uint8_t* qdst = smem + OFFP_Q + x * Q_TILE + r * 16;
-#pragma unroll
-      for (int c16 = 0; c16 < 8; ++c16) {
-        uint4 xq = make_uint4(0u, 0u, 0u, 0u);
-        if (active) xq = *reinterpret_cast<const uint4*>(qrow + 16 * c16);
-        uint4 o0, o1;
-        i8x4_to_f16x4(xq.x, o0.x, o0.y);
-        i8x4_to_f16x4(xq.y, o0.z, o0.w);
-        i8x4_to_f16x4(xq.z, o1.x, o1.y);
-        i8x4_to_f16x4(xq.w, o1.z, o1.w);
-        *reinterpret_cast<uint4*>(qdst + (2 * c16) * 2048) = o0;
-        *reinterpret_cast<uint4*>(qdst + (2 * c16 + 1) * 2048) = o1;
-      }
-      fence_proxy_async();
-      warp_arrive(PB_Q_READY);
-    }
-    float m_run = -CUDART_INF_F, l_run = 0.f;
+    uint32_t done = 0, done_other = 0, merges = 0;          // steps of this buffer and the other, merged units
     bool ok = true;
-    for (int j = 0; j < nt && ok; ++j) {
-      if (!warp_all(wait_bar(bar(PB_S_FULL + x), (uint32_t)j & 1u, abort_flag, p.err))) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      const int t0 = j * kKeys;
-      // keys of this tile beyond some row's position (the diagonal) or inactive rows
-      const bool masked = ragged || t0 + kKeys - 1 > pos_min;
-      // pass 1: the tile's row maximum of the raw integer scores, then scaled (c > 0)
-      float mx = -CUDART_INF_F;
-#pragma unroll 1
-      for (int c4 = 0; c4 < 4; ++c4) {
-        uint32_t v[32];
-        FA3_TMEM_LD32(scol + c4 * 32, v);
-        tmem_wait_ld();
-        if (masked) {
+    Part u;
+    while (ok && walk.next(p, u, lane)) {
+      const int nk = u.t1 - u.t0, steps = u.dual ? 2 * nk : nk, mine = (steps + 1 - x) / 2;
+      const int pl = r / p.G, hh = u.g * p.G + r - pl * p.G;  // position in the row tile, query head
+      const int i = u.rb * 2 * p.P + (u.dual ? x * p.P : 0) + pl;
+      const bool active = pl < p.P && i < u.nq;
+      const bool warp_active = __any_sync(0xffffffffu, active);
+      const int64_t orow = (int64_t)(u.q0 + (active ? i : 0)) * p.Hq + hh;   // row of q and out
+      if (u.nt == 0) {                                        // no key at all: zero rows
+        if (active && (u.dual || x == 0)) {
+          uint4* o = reinterpret_cast<uint4*>(p.out + orow * kD);
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            mx = fmaxf(mx, t0 + c4 * 32 + e <= pos ? __uint_as_float(v[e]) : -CUDART_INF_F);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) mx = max3(mx, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+          for (int c8 = 0; c8 < kD / 8; ++c8) o[c8] = make_uint4(0u, 0u, 0u, 0u);
         }
+        continue;                                             // the MMA warp passes over it as well
       }
-      mx *= c;
-      const float m_new = fmaxf(m_run, mx);
-      // Lazy rescale: the reference maximum moves only when the row maximum grew by
-      // more than 8; then O (holding P.V up to key tile j - 1) is scaled in place.
-      const bool grow = m_new != -CUDART_INF_F && (m_run == -CUDART_INF_F || m_new > m_run + 8.f);
-      if (__any_sync(0xffffffffu, grow && m_run != -CUDART_INF_F)) {
-        if (!warp_all(wait_bar(bar(PB_PV_DONE + x), (uint32_t)(j - 1) & 1u, abort_flag, p.err))) {
+      // The row's query codes as fp16 into the row tile's K-major A operand (chunk of 8 d at
+      // (d / 8) * 2048 + row * 16).
+      if (u.dual || x == 0) {
+        const int8_t* qrow = p.q + orow * kD;
+        uint8_t* qdst = smem + OFF_Q + (u.dual ? x : 0) * Q_TILE + r * 16;
+#pragma unroll
+        for (int c16 = 0; c16 < 8; ++c16) {
+          uint4 xq = make_uint4(0u, 0u, 0u, 0u);
+          if (active) xq = __ldg(reinterpret_cast<const uint4*>(qrow + 16 * c16));
+          uint4 o0, o1;
+          i8x4_to_f16x4(xq.x, o0.x, o0.y);
+          i8x4_to_f16x4(xq.y, o0.z, o0.w);
+          i8x4_to_f16x4(xq.z, o1.x, o1.y);
+          i8x4_to_f16x4(xq.w, o1.z, o1.w);
+          *reinterpret_cast<uint4*>(qdst + (2 * c16) * 2048) = o0;
+          *reinterpret_cast<uint4*>(qdst + (2 * c16 + 1) * 2048) = o1;
+        }
+        fence_proxy_async();
+      }
+      warp_arrive(B_Q_READY);
+      const int pos = !active ? -1 : p.causal ? u.nkv - u.nq + i : u.nkv - 1;   // last key this row sees
+      const int pos_min = __reduce_min_sync(0xffffffffu, active ? pos : 0x7fffffff);
+      const float c = active ? p.q_scale[hh] * p.k_scale[u.g] * p.sm_log2 : 0.f;
+      float m_run = -CUDART_INF_F, l_run = 0.f;
+      for (int st = 0; st < mine && ok; ++st) {
+        const uint32_t ph = done + (uint32_t)st;
+        if (!warp_all(wait_bar(bar(B_S_FULL + x), ph & 1u, abort_flag, p.err))) {
           ok = false;
           break;
         }
-        tc_fence_after();
-        const float f = (grow && m_run != -CUDART_INF_F) ? ex2_approx(m_run - m_new) : 1.f;
-#pragma unroll 1
-        for (int c4 = 0; c4 < 4; ++c4) {
-          uint32_t v[32];
-          FA3_TMEM_LD32(o_col + c4 * 32, v);
-          tmem_wait_ld();
+        if (warp_active) {
+          tc_fence_after();
+          const int t0 = (u.t0 + (u.dual ? st : 2 * st + x)) * kKeys;
+          const bool masked = t0 + kKeys - 1 > pos_min;       // some active row of the warp does not see all keys
+          const int last = pos - t0;                          // this row's last key of the tile
+          // the row's maximum of the integer scores; a masked score counts as -inf
+          uint32_t v[2][32];
+          float mx = -CUDART_INF_F, mx1 = -CUDART_INF_F;
+          FA3_TMEM_LD32(scol, v[0]);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-          FA3_TMEM_ST32(o_col + c4 * 32, v);
-        }
-      }
-      if (grow) {
-        l_run = m_run == -CUDART_INF_F ? 0.f : l_run * ex2_approx(m_run - m_new);
-        m_run = m_new;
-      }
-      const float mc = m_run == -CUDART_INF_F ? 0.f : m_run;
-      // pass 2: P = exp2(s c - m) as fp16 pairs over the S columns already read
-      // (keys 32 c4 .. 32 c4 + 31 go to columns 16 c4 .. 16 c4 + 15); the row sum
-      // takes the same fp16 weights, so the output is a weighted mean of V.
-#pragma unroll 1
-      for (int c4 = 0; c4 < 4; ++c4) {
-        uint32_t v[32];
-        FA3_TMEM_LD32(scol + c4 * 32, v);
-        tmem_wait_ld();
-        uint32_t pk[16];
+          for (int c4 = 0; c4 < 4; ++c4) {
+            uint32_t* w = v[c4 & 1];
+            wait_ld32(w);
+            if (c4 < 3) FA3_TMEM_LD32(scol + (c4 + 1) * 32, v[(c4 + 1) & 1]);
+            if (masked) {
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const int t = t0 + c4 * 32 + e;
-          float p0 = ex2_approx(fmaf(__uint_as_float(v[e]), c, -mc));
-          float p1 = ex2_approx(fmaf(__uint_as_float(v[e + 1]), c, -mc));
-          if (masked) {
-            p0 = t <= pos ? p0 : 0.f;
-            p1 = t + 1 <= pos ? p1 : 0.f;
+              for (int e = 0; e < 32; ++e) w[e] = 32 * c4 + e <= last ? w[e] : 0xff800000u;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              mx = max3(mx, __uint_as_float(w[e]), __uint_as_float(w[e + 1]));
+              mx1 = max3(mx1, __uint_as_float(w[e + 2]), __uint_as_float(w[e + 3]));
+            }
           }
-          pk[e / 2] = pack_f16x2(p0, p1);
-          const float2 pr = __half22float2(*reinterpret_cast<const __half2*>(&pk[e / 2]));
-          l_run += pr.x + pr.y;
+          FA3_TMEM_LD32(scol, v[0]);
+          mx = fmaxf(mx, mx1);
+          mx = mx == -CUDART_INF_F ? mx : mx * c;
+          // Lazy rescale: the reference maximum moves only when the row maximum grew by more than 8
+          // (log2 units); then O (P.V up to this buffer's step before) is scaled in place.
+          const bool grow = mx > m_run + 8.f || (m_run == -CUDART_INF_F && mx != -CUDART_INF_F);
+          const bool scale_o = grow && m_run != -CUDART_INF_F;
+          if (__any_sync(0xffffffffu, scale_o)) {
+            if (!warp_all(wait_bar(bar(B_PV_DONE + x), (ph - 1u) & 1u, abort_flag, p.err))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const float f = scale_o ? ex2_approx(m_run - mx) : 1.f;
+#pragma unroll 1
+            for (int c16 = 0; c16 < 8; ++c16) {
+              uint32_t w[16];
+              FA3_TMEM_LD16(o_col + c16 * 16, w);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
+              FA3_TMEM_ST16(o_col + c16 * 16, w);
+            }
+          }
+          if (grow) {
+            l_run = m_run == -CUDART_INF_F ? 0.f : l_run * ex2_approx(m_run - mx);
+            m_run = mx;
+          }
+          const float mc = m_run == -CUDART_INF_F ? 0.f : -m_run;
+          // P = exp2(s c - m) as fp16 pairs over the S columns (keys 32 c4 .. 32 c4 + 31 go to columns
+          // 16 c4 .. 16 c4 + 15); the row sum takes the weights before the rounding.
+          float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+          for (int c4 = 0; c4 < 4; ++c4) {
+            uint32_t pk[16];
+            uint32_t* w = v[c4 & 1];
+            wait_ld32(w);
+            if (c4 < 3) FA3_TMEM_LD32(scol + (c4 + 1) * 32, v[(c4 + 1) & 1]);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float p0, p1;
+              fma2(p0, p1, __uint_as_float(w[e]), __uint_as_float(w[e + 1]), c, c, mc, mc);
+              p0 = ex2_approx(p0);
+              p1 = ex2_approx(p1);
+              if (masked) {
+                p0 = 32 * c4 + e <= last ? p0 : 0.f;
+                p1 = 32 * c4 + e + 1 <= last ? p1 : 0.f;
+              }
+              add2(l0, l1, l0, l1, p0, p1);
+              pk[e / 2] = pack_f16x2(p0, p1);
+            }
+            FA3_TMEM_ST16(scol + c4 * 16, pk);
+          }
+          l_run += l0 + l1;
+          tmem_wait_st();
+          tc_fence_before();
         }
-        FA3_TMEM_ST16(scol + c4 * 16, pk);
+        warp_arrive(B_P_FULL + x);
       }
-      tmem_wait_st();
-      tc_fence_before();
-      warp_arrive(PB_P_FULL + x);
-    }
-    // epilogue: out = v_scale * O / l
-    if (nt == 0) {                                          // no key at all: zero rows
-      if (active) {
-        uint4* orow = reinterpret_cast<uint4*>(p.out + ((int64_t)(q0 + i) * p.Hq + h) * kD);
-        for (int c8 = 0; c8 < kD / 8; ++c8) orow[c8] = make_uint4(0u, 0u, 0u, 0u);
+      if (!ok) break;
+      done += (uint32_t)mine;
+      done_other += (uint32_t)(steps - mine);
+      // ---------------------------------------------------------- epilogue
+      // O_x is complete when the buffer's last P.V is.  A single row tile has both buffers' results for
+      // the same rows: both warpgroups read both and write half of the columns each.
+      if (mine > 0) ok = warp_all(wait_bar(bar(B_PV_DONE + x), (done - 1u) & 1u, abort_flag, p.err));
+      float f_mine = 1.f, f_other = 0.f;
+      bool both = false;
+      if (!u.dual) {
+        ml[x * kRows + r] = make_float2(m_run, l_run);
+        warp_arrive(B_ML + x);
+        ok = ok && warp_all(wait_bar(bar(B_ML + (x ^ 1)), merges & 1u, abort_flag, p.err));
+        both = steps > mine;
+        if (ok && both) ok = warp_all(wait_bar(bar(B_PV_DONE + (x ^ 1)), (done_other - 1u) & 1u, abort_flag, p.err));
+        if (!ok) break;
+        const float2 o = ml[(x ^ 1) * kRows + r];
+        const float m = fmaxf(m_run, o.x);
+        f_mine = m_run == -CUDART_INF_F ? 0.f : ex2_approx(m_run - m);
+        f_other = o.x == -CUDART_INF_F ? 0.f : ex2_approx(o.x - m);
+        l_run = l_run * f_mine + o.y * f_other;
+        m_run = m;
+        ++merges;
       }
-    } else if (ok && warp_all(wait_bar(bar(PB_PV_DONE + x), (uint32_t)(nt - 1) & 1u, abort_flag, p.err))) {
+      if (!ok) break;
       tc_fence_after();
-      const float inv = (active && l_run > 0.f) ? p.v_scale[g] / l_run : 0.f;
-      uint16_t* orow = p.out + ((int64_t)(q0 + (active ? i : 0)) * p.Hq + h) * kD;
+      if (warp_active) {
+        const bool whole = u.whole();
+        const float inv = !whole ? 1.f : l_run > 0.f ? p.v_scale[u.g] / l_run : 0.f;
+        f_mine *= inv;
+        f_other *= inv;
+        const int slot = 2 * (int)blockIdx.x + (u.first ? 1 : 0);
+        const int prow = (u.dual ? x * kRows : 0) + r;
+        float4* po = p.part_o + (int64_t)slot * (kD / 4) * p.rows_max + prow;
+        const int c_begin = u.dual ? 0 : x * 4, c_end = u.dual ? 8 : c_begin + 4;      // groups of 16 columns
 #pragma unroll 1
-      for (int c4 = 0; c4 < 4; ++c4) {
-        uint32_t v[32];
-        FA3_TMEM_LD32(o_col + c4 * 32, v);
-        tmem_wait_ld();
-        if (active) {
-          uint32_t w[16];
+        for (int c16 = c_begin; c16 < c_end; ++c16) {
+          uint32_t a[16], b2[16];
+          if (mine > 0) FA3_TMEM_LD16(o_col + c16 * 16, a);
+          if (both) FA3_TMEM_LD16(tmem + lane_base + TM_O + (x ^ 1) * 128 + c16 * 16, b2);
+          tmem_wait_ld();
+          float f[16];
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const __nv_bfloat162 bb =
-                __floats2bfloat162_rn(__uint_as_float(v[e]) * inv, __uint_as_float(v[e + 1]) * inv);
-            w[e / 2] = *reinterpret_cast<const uint32_t*>(&bb);
+          for (int e = 0; e < 16; ++e) {
+            f[e] = f_mine == 0.f || mine == 0 ? 0.f : __uint_as_float(a[e]) * f_mine;
+            if (both && f_other != 0.f) f[e] = fmaf(__uint_as_float(b2[e]), f_other, f[e]);
           }
+          if (active) {
+            if (whole) {
+              uint32_t w[8];
 #pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4)
-            *reinterpret_cast<uint4*>(orow + c4 * 32 + q4 * 8) =
-                make_uint4(w[4 * q4], w[4 * q4 + 1], w[4 * q4 + 2], w[4 * q4 + 3]);
+              for (int e = 0; e < 16; e += 2) {
+                const __nv_bfloat162 bb = __floats2bfloat162_rn(f[e], f[e + 1]);
+                w[e / 2] = *reinterpret_cast<const uint32_t*>(&bb);
+              }
+              uint4* o = reinterpret_cast<uint4*>(p.out + orow * kD + c16 * 16);
+              o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+              o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            } else {
+#pragma unroll
+              for (int q4 = 0; q4 < 4; ++q4)
+                po[(int64_t)(c16 * 4 + q4) * p.rows_max] = make_float4(f[4 * q4], f[4 * q4 + 1], f[4 * q4 + 2], f[4 * q4 + 3]);
+            }
+          }
         }
+        if (!whole && active && (u.dual || x == 0)) p.part_ml[(int64_t)slot * p.rows_max + prow] = make_float2(m_run, l_run);
+      }
+      if (!u.dual) {
+        // the other warpgroup's next P.V may overwrite what this one reads, and this one's that one's
+        tc_fence_before();
+        warp_arrive(B_READ + x);
+        ok = warp_all(wait_bar(bar(B_READ + (x ^ 1)), (merges - 1u) & 1u, abort_flag, p.err));
       }
     }
   }
@@ -424,31 +703,129 @@ __global__ void __launch_bounds__(kThreadsP, 1) gqa_chunk_kernel(const __grid_co
   }
 }
 
+// Merges the parts of cut units.  Block (c - 1, rows): the cut between CTAs c - 1 and c, if it is
+// the first in its unit; rows 32 blockIdx.y .. + 31.  A lane has a row, a warp 16 columns.
+__global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constant__ ChunkParams p) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cut = blockIdx.x + 1;
+  // The lengths were written before the kernel that launched this one ahead of its end, so the
+  // plan need not wait for that kernel; its results do.
+  const int64_t total = total_cost(p, lane, false);
+  const int parts = parts_of(p, total);
+  bool work = cut < parts;
+  Cursor c;
+  int nt = 0, owner = 0;
+  int64_t cost = 0, begin = 0;
+  bool dual = false;
+  if (work) {
+    const int64_t x = part_begin(total, parts, cut);
+    c = seek(p, x, lane);
+    nt = tiles_of(p, c.s, c.rb);
+    dual = is_dual(p, c.s, c.rb);
+    cost = kUnitCost + (int64_t)nt * (dual ? 2 : 1);
+    begin = x - c.off;                                       // of the unit, on the line
+    owner = (int)(((begin + 1) * parts - 1) / total);        // CTA of the unit's begin
+    work = c.off > 0 && owner == cut - 1;
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  if (!work) return;
+  const int prow = blockIdx.y * 32 + lane;                   // row tile x 128 + row
+  const int r = prow & (kRows - 1), pl = r / p.G, h = c.g * p.G + r - pl * p.G;
+  const int i = c.rb * 2 * p.P + (prow >= kRows ? p.P : 0) + pl;
+  if (prow >= kRows && !dual) return;
+  const bool active = pl < p.P && i < c.s.nq;
+  auto range = [&](int cta, int& t0, int& t1) {              // the key tiles of a CTA's part
+    const int64_t b = part_begin(total, parts, cta) - begin, e = part_begin(total, parts, cta + 1) - begin;
+    t0 = b <= 0 ? 0 : tile_at(b, dual, nt);
+    t1 = e >= cost ? nt : tile_at(e, dual, nt);
+    return t0 < t1;
+  };
+  int last = owner, have = 0, t0, t1;
+  for (int k = owner; k < parts && part_begin(total, parts, k) < begin + cost; ++k) {
+    last = k;
+    have += range(k, t0, t1) ? 1 : 0;
+  }
+  if (have < 2 || !active) return;                           // one CTA has all the keys after all
+  auto slot_of = [&](int cta) { return 2 * (int64_t)cta + (cta == owner ? 1 : 0); };
+  float m = -CUDART_INF_F;
+  for (int k = owner; k <= last; ++k)
+    if (range(k, t0, t1)) m = fmaxf(m, p.part_ml[slot_of(k) * p.rows_max + prow].x);
+  float l = 0.f, o[16] = {};
+  for (int k = owner; k <= last; ++k) {
+    if (!range(k, t0, t1)) continue;
+    const float2 ml = p.part_ml[slot_of(k) * p.rows_max + prow];
+    if (ml.x == -CUDART_INF_F) continue;
+    const float f = ex2_approx(ml.x - m);
+    l = fmaf(ml.y, f, l);
+    const float4* po = p.part_o + slot_of(k) * (kD / 4) * p.rows_max + prow;
+#pragma unroll
+    for (int q4 = 0; q4 < 4; ++q4) {
+      const float4 a = po[(int64_t)(warp * 4 + q4) * p.rows_max];
+      o[4 * q4] = fmaf(a.x, f, o[4 * q4]);
+      o[4 * q4 + 1] = fmaf(a.y, f, o[4 * q4 + 1]);
+      o[4 * q4 + 2] = fmaf(a.z, f, o[4 * q4 + 2]);
+      o[4 * q4 + 3] = fmaf(a.w, f, o[4 * q4 + 3]);
+    }
+  }
+  const float inv = l > 0.f ? p.v_scale[c.g] / l : 0.f;
+  uint32_t w[8];
+#pragma unroll
+  for (int e = 0; e < 16; e += 2) {
+    const __nv_bfloat162 bb = __floats2bfloat162_rn(o[e] * inv, o[e + 1] * inv);
+    w[e / 2] = *reinterpret_cast<const uint32_t*>(&bb);
+  }
+  uint4* out = reinterpret_cast<uint4*>(p.out + ((int64_t)(c.s.q0 + i) * p.Hq + h) * kD + warp * 16);
+  out[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+// Rows of a unit's partial result: one row tile when no sequence can fill more.
+int rows_max_of(int n, int G) { return n > kRows / G ? 2 * kRows : kRows; }
+
+size_t workspace_bytes_of(int ctas, int rows_max) {
+  return (size_t)2 * ctas * rows_max * (kD * sizeof(float) + sizeof(float2));
+}
+
 }  // namespace
 }  // namespace fa3
 
 using namespace fa3;
 
+FA3_API size_t fa3_chunk_workspace_size(int n, int B, int Hq, int Hkv, int D) {
+  if (n <= 0 || B <= 0 || Hq <= 0 || Hkv <= 0 || D != kD || Hq % Hkv != 0 || Hq / Hkv > kRows) return 0;
+  int sms = 0;
+  if (check_device(&sms) != FA3_OK) sms = 152;
+  return workspace_bytes_of(sms, rows_max_of(n, Hq / Hkv));
+}
+
 namespace {
-int chunk_attn(ChunkParams& p, int D, float softmax_scale, void* stream) {
+int chunk_attn(ChunkParams& p, int D, float softmax_scale, void* workspace, size_t workspace_bytes, void* stream) {
   if (!p.q || !p.k || !p.v || !p.q_scale || !p.k_scale || !p.v_scale || !p.q_start || !p.kv_lens || !p.out)
     return FA3_EINVAL;
   if (p.n <= 0 || p.B <= 0 || p.T <= 0 || p.Hq <= 0 || p.Hkv <= 0 || D <= 0 || p.Hq % p.Hkv != 0) return FA3_EINVAL;
   if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale)) return FA3_EINVAL;
   p.G = p.Hq / p.Hkv;
-  if (D != kD || p.G > kRowsP || p.B > 65535 || p.Hkv > 65535) return FA3_ERANGE;
+  if (D != kD || p.G > kRows) return FA3_ERANGE;
   if (!aligned16(p.q) || !aligned16(p.k) || !aligned16(p.v) || !aligned16(p.out)) return FA3_ERANGE;
-  p.P = kRowsP / p.G;
+  p.P = kRows / p.G;
   p.sm_log2 = softmax_scale * 1.4426950408889634f;
   int sms = 0;
   const int st = check_device(&sms);
   if (st != FA3_OK) return st;
+  p.ctas = sms;
+  p.rows_max = rows_max_of(p.n, p.G);
+  if (!workspace || workspace_bytes < workspace_bytes_of(sms, p.rows_max) || !aligned16(workspace)) return FA3_EWORKSPACE;
+  p.part_o = static_cast<float4*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)2 * sms * (kD / 4) * p.rows_max);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaFuncSetAttribute(gqa_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_PREFILL) != cudaSuccess)
+  if (cudaFuncSetAttribute(gqa_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_CHUNK) != cudaSuccess)
     return FA3_ECUDA;
-  // at most n / 2P + B row blocks; one more block, which sees every sequence, reports the bad ones
-  const dim3 grid((unsigned)(p.n / (2 * p.P) + p.B + 1), (unsigned)p.Hkv);
-  return cuda_status(launch_pdl(gqa_chunk_kernel, grid, dim3(kThreadsP), SMEM_PREFILL, s, p));
+  if (launch_pdl(gqa_chunk_kernel, dim3((unsigned)sms), dim3(kThreadsC), SMEM_CHUNK, s, p) != cudaSuccess)
+    return FA3_ECUDA;
+  if (sms > 1 && launch_pdl(chunk_combine_kernel, dim3((unsigned)(sms - 1), (unsigned)(p.rows_max / 32)), dim3(256), 0, s,
+                            p) != cudaSuccess)
+    return FA3_ECUDA;
+  return FA3_OK;
 }
 }  // namespace
 
@@ -466,7 +843,7 @@ FA3_API int fa3_prefill_attn_gqa_paged(const int8_t* q, const int8_t* k, const i
   p.n = n; p.B = B; p.T = max_pages * page_size; p.Hq = Hq; p.Hkv = Hkv; p.causal = 1;
   p.page_size = page_size; p.max_pages = max_pages; p.num_pages = num_pages;
   p.div_ps = make_divu32((uint32_t)page_size);
-  return chunk_attn(p, D, softmax_scale, stream);
+  return chunk_attn(p, D, softmax_scale, workspace, workspace_bytes, stream);
 }
 
 FA3_API int fa3_cross_attn_gqa(const int8_t* q, const int8_t* k, const int8_t* v, const float* q_scale,
@@ -478,7 +855,5 @@ FA3_API int fa3_cross_attn_gqa(const int8_t* q, const int8_t* k, const int8_t* v
   p.q = q; p.k = k; p.v = v; p.q_scale = q_scale; p.k_scale = k_scale; p.v_scale = v_scale; p.q_start = q_start;
   p.kv_lens = enc_lens; p.out = out; p.err = dev_err;
   p.n = n; p.B = B; p.T = T; p.Hq = Hq; p.Hkv = Hkv; p.causal = 0;
-  return chunk_attn(p, D, softmax_scale, stream);
+  return chunk_attn(p, D, softmax_scale, workspace, workspace_bytes, stream);
 }
-
-FA3_API size_t fa3_chunk_workspace_size(int n, int B, int Hq, int Hkv, int D) { return 0; }

@@ -219,6 +219,16 @@ def test_cross_all_empty():
     assert not got[:42].any()
 
 
+def test_cross_many_empty_between_full():
+    # a CTA's run of several units without keys beside units with keys, one and two row tiles
+    F = fa3()
+    rng = np.random.default_rng(18)
+    lens = [0] * 90 + [300, 0, 0, 140] + [0] * 60
+    rows = [1] * 90 + [1, 2, 1, 40] + list(rng.integers(0, 40, 60))
+    c = _case(rng, 8, 2, rows, lens, None)
+    _check(F, c, "many empty states")
+
+
 def test_agrees_with_the_decode_and_prefill_calls():
     # the same cache through the calls that were there: all within the gate of one oracle
     F = fa3()
