@@ -477,8 +477,8 @@ size_t fa3_chunk_workspace_size(int n, int B, int Hq, int Hkv, int D);
 /* A chunk of new tokens over a paged cache that holds them already: row
  * q_start[b] + i of sequence b attends causally to t <= kv_lens[b] - n_b + i.
  * kv_lens as for fa3_rope_append_gqa_paged; k, v the pools.  An entry outside the
- * pool sets FA3_DEVERR_PAGE and reads as zeros (that sequence's output is not valid).
- * Supported: any page_size >= 1. */
+ * pool sets FA3_DEVERR_PAGE and reads another page (that sequence's output is not valid).
+ * Supported: any page_size >= 1, num_pages * page_size < 2^31. */
 int fa3_prefill_attn_gqa_paged(const int8_t* q, const int8_t* k, const int8_t* v,
                                const float* q_scale, const float* k_scale, const float* v_scale,
                                const int32_t* q_start, const int32_t* kv_lens, const int32_t* block_table,
@@ -490,7 +490,7 @@ int fa3_prefill_attn_gqa_paged(const int8_t* q, const int8_t* k, const int8_t* v
  * attends to all of t < enc_lens[b], 0 <= enc_lens[b] <= T (else FA3_DEVERR_LENS);
  * no states at all gives zero rows.
  * k, v     int8 [B][T][Hkv][D] (rows t >= enc_lens[b] are not read), as
- *          fa3_quantize_append writes them. */
+ *          fa3_quantize_append writes them; B * T < 2^31. */
 int fa3_cross_attn_gqa(const int8_t* q, const int8_t* k, const int8_t* v,
                        const float* q_scale, const float* k_scale, const float* v_scale,
                        const int32_t* q_start, const int32_t* enc_lens, uint16_t* out,

@@ -22,10 +22,10 @@
 // end.  A cut unit's parts leave unnormalised O, maximum and sum in the workspace, and
 // chunk_combine_kernel merges them, so one long sequence and a ragged batch both fill the GPU.
 //
-// Roles in the CTA (384 threads): warp 0 issues the MMAs; warps 1-3 look keys up in the
+// Roles in the CTA (416 threads): warp 0 issues the MMAs; warps 1-3 and 12 look keys up in the
 // block table, load int8 K and V tiles one tile ahead into registers and write them as fp16
-// core matrices into one of two stages; warps 4-7 and 8-11 (one row each) run the softmax of
-// buffers 0 and 1.  int8 codes are exact in fp16 and a 128-term sum of their products
+// into one of two stages; warps 4-7 and 8-11 (a row a lane) run the softmax of buffers 0
+// and 1.  int8 codes are exact in fp16 and a 128-term sum of their products
 // stays below 2^24, so kind::f16 MMAs with fp32 accumulation give the exact integer
 // score (sm_103a has no integer tcgen05 kind).  P (fp16, relative to a lazily moved row
 // maximum) is written over its scores in TMEM and is the A operand of P.V; the row sum is
@@ -48,16 +48,17 @@ namespace {
 constexpr int kD = 128;            // head dim
 constexpr int kKeys = 128;         // keys per tile
 constexpr int kRows = 128;         // rows (TMEM lanes) per row tile
-constexpr int kThreadsC = 384;     // warp 0: MMA, warps 1-3: converters, 4-7 / 8-11: softmax of buffer 0 / 1
-constexpr int kConv = 96;
+constexpr int kThreadsC = 416;     // warp 0: MMA; 4-7 / 8-11: softmax of buffer 0 / 1; 1-3 and 12: converters
 constexpr uint32_t TM_O = 0, TM_S = 256;                   // O_x [128x, +128), S_x [256 + 128x, +128)
 constexpr uint32_t KV_TILE = kKeys * kD * 2;               // 32 KB of fp16
+constexpr uint32_t KV_HALF = KV_TILE / 2;                  // 64 values of d: 128 keys x 128 B, 128-byte swizzle
 constexpr uint32_t Q_TILE = kRows * kD * 2;                // 32 KB of fp16
 constexpr uint32_t OFF_Q = 0;                              // 2 x fp16 query rows, K-major
 constexpr uint32_t OFF_K = OFF_Q + 2 * Q_TILE;             // 2 stages
 constexpr uint32_t OFF_V = OFF_K + 2 * KV_TILE;            // 2 stages
 constexpr uint32_t OFF_ML = OFF_V + 2 * KV_TILE;           // [2][128] float2: (m, l) of a single row tile's halves
-constexpr uint32_t OFF_BAR = OFF_ML + 2 * kRows * 8;
+constexpr uint32_t OFF_WALK = OFF_ML + 2 * kRows * 8;      // a Walk a warp
+constexpr uint32_t OFF_BAR = OFF_WALK + 13 * 64;
 enum {
   B_K_FULL = 0, B_K_EMPTY = 2, B_V_FULL = 4, B_V_EMPTY = 6,
   B_S_FULL = 8,                    // [2]: buffer x's scores of its next step
@@ -238,49 +239,77 @@ struct Part {
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == nt; }
 };
 
-// A CTA's parts in order; every warp walks them by itself.
+// A CTA's parts in order.  Every warp walks them by itself, its place kept in shared memory (it is looked at
+// once a part, and its registers are wanted elsewhere).
 struct Walk {
   Cursor c;
   int64_t left;
-  __device__ __forceinline__ void begin(const ChunkParams& p, int64_t total, int parts, int cta, int lane) {
-    const int64_t x = part_begin(total, parts, cta);
-    left = part_begin(total, parts, cta + 1) - x;
-    if (left > 0) c = seek(p, x, lane);
-  }
-  __device__ __forceinline__ bool next(const ChunkParams& p, Part& u, int lane) {
-    while (left > 0) {
-      const int nt = tiles_of(p, c.s, c.rb);
-      const bool dual = is_dual(p, c.s, c.rb);
-      const int64_t cost = kUnitCost + (int64_t)nt * (dual ? 2 : 1);
-      const int64_t take = cost - c.off < left ? cost - c.off : left;
-      u = Part{c.b, c.g, c.rb, c.s.q0, c.s.nq, c.s.nkv, tile_at(c.off, dual, nt), tile_at(c.off + take, dual, nt), nt,
-               dual, c.off == 0};
-      if (c.off + take == cost) u.t1 = nt;
-      left -= take;
-      c.off = 0;
-      if (++c.rb == blocks_of(p, c.s)) {
-        c.rb = 0;
-        if (++c.g == p.Hkv) {
-          c.g = 0;
-          if (left > 0) to_sequence(p, c, c.b + 1, lane);
-        }
-      }
-      if (u.t0 < u.t1 || (nt == 0 && u.first)) return true;
-    }
-    return false;
-  }
 };
-
-// Cache row of key t of sequence b, or -1 for a block-table entry outside the pool.
-__device__ __forceinline__ int64_t key_row(const ChunkParams& p, int b, int t) {
-  if (!p.block_table) return (int64_t)b * p.T + t;
-  const uint32_t pi = divu32((uint32_t)t, p.div_ps);
-  const int pg = __ldg(p.block_table + (int64_t)b * p.max_pages + pi);
-  if (pg < 0 || pg >= p.num_pages) {
-    set_dev_err(p.err, FA3_DEVERR_PAGE);
-    return -1;
+static_assert(sizeof(Walk) <= 64, "walk area");
+__device__ __forceinline__ void walk_begin(const ChunkParams& p, Walk* at, int64_t total, int parts, int cta, int lane) {
+  const int64_t x = part_begin(total, parts, cta);
+  Walk w;
+  w.left = part_begin(total, parts, cta + 1) - x;
+  w.c = Cursor{p.B, 0, 0, {0, 0, 0}, 0};
+  if (w.left > 0) w.c = seek(p, x, lane);
+  if (lane == 0) *at = w;
+  __syncwarp();
+}
+__device__ __noinline__ bool walk_next(const ChunkParams& p, Walk* at, Part& u, int lane) {
+  Walk w = *at;
+  bool got = false;
+  while (w.left > 0 && !got) {
+    Cursor& c = w.c;
+    const int nt = tiles_of(p, c.s, c.rb);
+    const bool dual = is_dual(p, c.s, c.rb);
+    const int64_t cost = kUnitCost + (int64_t)nt * (dual ? 2 : 1);
+    const int64_t take = cost - c.off < w.left ? cost - c.off : w.left;
+    u = Part{c.b, c.g, c.rb, c.s.q0, c.s.nq, c.s.nkv, tile_at(c.off, dual, nt), tile_at(c.off + take, dual, nt), nt,
+             dual, c.off == 0};
+    if (c.off + take == cost) u.t1 = nt;
+    w.left -= take;
+    c.off = 0;
+    if (++c.rb == blocks_of(p, c.s)) {
+      c.rb = 0;
+      if (++c.g == p.Hkv) {
+        c.g = 0;
+        if (w.left > 0) to_sequence(p, c, c.b + 1, lane);
+      }
+    }
+    got = u.t0 < u.t1 || (nt == 0 && u.first);
   }
-  return (int64_t)pg * p.page_size + (t - (int)pi * p.page_size);
+  __syncwarp();
+  if (lane == 0) *at = w;
+  __syncwarp();
+  return got;
+}
+
+// wait_bar with its loop out of line: the roles' code has to fit the instruction cache together.  The test
+// suspends the thread by itself for a while, and the clock and the abort flag are looked at now and then.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, int32_t* err) {
+  const uint64_t t0 = global_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (global_ns() - t0 > kWaitNs) break;
+  }
+  *abort_flag = 1u;
+  set_dev_err(err, FA3_DEVERR_TIMEOUT);
+  return false;
+}
+__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, int32_t* err) {
+  return mbar_try(bar, parity) || wait_on(bar, parity, abort_flag, err);
+}
+
+// One lane of the warp waits for all: a test by 32 lanes takes the shared-memory pipe 32 times as long,
+// and the waiting warps' tests would crowd out the loads and stores of the working ones.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int lane, volatile uint32_t* abort_flag,
+                                          int32_t* err) {
+  bool ok = true;
+  if (lane == 0) ok = wait_long(bar, parity, abort_flag, err);
+  return __shfl_sync(0xffffffffu, ok, 0);
 }
 
 // The wait for this thread's TMEM loads, which also orders the uses of v behind it.
@@ -291,6 +320,37 @@ __device__ __forceinline__ void wait_ld32(uint32_t* v) {
                  "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
                  "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
                :: "memory");
+}
+
+// 16 bytes that this SM reads once: the L1 (what shared memory leaves of it) is passed by.
+__device__ __forceinline__ uint4 load_once(const int8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// MMAs on descriptors given by their low words (address and leading stride; the step along the contraction
+// is one 32-bit addition): the issuing thread is one warp's worth of instructions, so each one counts.
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo, bool swizzle) { return (sbo >> 4) | (1u << 14) | (swizzle ? 2u << 29 : 0u); }
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4) | ((lbo >> 4) << 16); }
+template <uint32_t HI_A, uint32_t HI_B>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n.reg .pred p;\n.reg .b64 a, b;\nmov.b64 a, {%1, %5};\nmov.b64 b, {%2, %6};\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n"
+      ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"((uint32_t)acc), "n"(HI_A), "n"(HI_B) : "memory");
+}
+template <uint32_t HI>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n.reg .pred p;\n.reg .b64 b;\nmov.b64 b, {%2, %5};\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n"
+      ::"r"(d), "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"((uint32_t)acc), "n"(HI) : "memory");
 }
 
 __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_constant__ ChunkParams p) {
@@ -306,14 +366,14 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
   const int64_t total = total_cost(p, lane, blockIdx.x == 0 && warp == 0);
   const int parts = parts_of(p, total);
   if ((int)blockIdx.x >= parts || total == 0) return;
-  Walk walk;
-  walk.begin(p, total, parts, blockIdx.x, lane);
+  Walk* walk = reinterpret_cast<Walk*>(smem + OFF_WALK) + warp;
+  walk_begin(p, walk, total, parts, blockIdx.x, lane);
 
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(bar(B_K_FULL + s), kConv);
+      mbar_init(bar(B_K_FULL + s), 4);
       mbar_init(bar(B_K_EMPTY + s), 1);
-      mbar_init(bar(B_V_FULL + s), kConv);
+      mbar_init(bar(B_V_FULL + s), 4);
       mbar_init(bar(B_V_EMPTY + s), 1);
       mbar_init(bar(B_S_FULL + s), 1);
       mbar_init(bar(B_P_FULL + s), 4);
@@ -340,141 +400,152 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
     // ------------------------------------------------------------ MMA issuer
     const uint32_t id_qk = idesc_f16(kRows, kKeys, false, false);
     const uint32_t id_pv = idesc_f16(kRows, kD, false, true);
-    uint32_t kc = 0, done[2] = {0, 0}, units = 0;             // key tiles, steps of each buffer, units so far
+    uint32_t kc = 0, done0 = 0, done1 = 0, units = 0;         // key tiles, steps of each buffer, units so far
     bool ok = true;
     Part u;
-    while (ok && walk.next(p, u, lane)) {
+    while (ok && walk_next(p, walk, u, lane)) {
       if (u.nt == 0) continue;
       const int nk = u.t1 - u.t0, steps = u.dual ? 2 * nk : nk;
       if (lane == 0) {
-        ok = wait_bar(bar(B_Q_READY), units & 1u, abort_flag, p.err);
+        ok = wait_long(bar(B_Q_READY), units & 1u, abort_flag, p.err);
         // S_x = Q.K^T: the row tile's K-major A operand in shared memory (8-row core groups 128 B
-        // apart, 8-wide d groups 2048 B apart), K the K-major B operand.
-        auto issue_qk = [&](int t) -> bool {
-          const int x = t & 1;
-          const uint32_t kt = kc + (uint32_t)(u.dual ? t >> 1 : t), s = kt & 1u;
-          if (!wait_bar(bar(B_K_FULL + s), (kt >> 1) & 1u, abort_flag, p.err)) return false;
-          // S_x holds the P of step t - 2 until its P.V is done
-          if (t >= 2 && !wait_bar(bar(B_PV_DONE + x), (done[x] + (uint32_t)(t >> 1) - 1u) & 1u, abort_flag, p.err))
-            return false;
+        // apart, 8-wide d groups 2048 B apart), K the K-major B operand (128-byte swizzle: 8-key groups
+        // 1024 B apart, 16 values of d 32 B apart within a half).  S_x holds the P of the buffer's step
+        // before until its P.V is done (d: the buffer's steps before this one, any: in this unit).
+        auto issue_qk = [&](const int x, uint32_t kt, uint32_t d, bool any) -> bool {
+          const uint32_t s = kt & 1u;
+          if (!wait_long(bar(B_K_FULL) + 8u * s, (kt >> 1) & 1u, abort_flag, p.err)) return false;
+          if (any && !wait_long(bar(B_PV_DONE + x), (d - 1u) & 1u, abort_flag, p.err)) return false;
           tc_fence_after();
+          const uint32_t a = desc_lo(sbase + OFF_Q + (u.dual ? x : 0) * Q_TILE, 2048);
+          const uint32_t bd = desc_lo(sbase + OFF_K + s * KV_TILE, 16);
 #pragma unroll
-          for (int kk = 0; kk < kD / 16; ++kk) {
-            const uint64_t a = sdesc(sbase + OFF_Q + (u.dual ? x : 0) * Q_TILE + kk * 4096, 2048, 128);
-            const uint64_t bd = sdesc(sbase + OFF_K + s * KV_TILE + kk * 4096, 2048, 128);
-            mma_f16(tmem + TM_S + x * 128, a, bd, id_qk, kk > 0 ? 1u : 0u);
-          }
+          for (int kk = 0; kk < kD / 16; ++kk)
+            mma_ss<desc_hi(128, false), desc_hi(1024, true)>(
+                tmem + TM_S + x * 128, a + kk * (4096 >> 4), bd + (kk / 4) * (KV_HALF >> 4) + (kk % 4) * (32 >> 4), id_qk,
+                kk > 0);
           mma_commit(bar(B_S_FULL + x));
-          if (!u.dual || x == 1) mma_commit(bar(B_K_EMPTY + s));    // all steps of this key tile have it
+          if (!u.dual || x == 1) mma_commit(bar(B_K_EMPTY) + 8u * s);    // all steps of this key tile have it
           return true;
         };
         // O_x += P_x.V: P_x (fp16, over S_x: column k holds keys 2k, 2k + 1) is the A operand in
-        // TMEM, V the MN-major B operand (token groups 128 B apart, d groups 2048 B apart).
-        auto issue_pv = [&](int t) -> bool {
-          const int x = t & 1;
-          const uint32_t kt = kc + (uint32_t)(u.dual ? t >> 1 : t), s = kt & 1u;
-          if (!wait_bar(bar(B_P_FULL + x), (done[x] + (uint32_t)(t >> 1)) & 1u, abort_flag, p.err)) return false;
-          if (!wait_bar(bar(B_V_FULL + s), (kt >> 1) & 1u, abort_flag, p.err)) return false;
+        // TMEM, V the MN-major B operand (128-byte swizzle: 8-key groups 1024 B apart, halves of d 16 KB).
+        auto issue_pv = [&](const int x, uint32_t kt, uint32_t d, bool any) -> bool {
+          const uint32_t s = kt & 1u;
+          if (!wait_long(bar(B_V_FULL) + 8u * s, (kt >> 1) & 1u, abort_flag, p.err)) return false;
+          if (!wait_long(bar(B_P_FULL + x), d & 1u, abort_flag, p.err)) return false;
           tc_fence_after();
+          const uint32_t bd = desc_lo(sbase + OFF_V + s * KV_TILE, KV_HALF);
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk) {
-            const uint64_t bd = sdesc(sbase + OFF_V + s * KV_TILE + kk * 256, 128, 2048);
-            mma_f16_ts(tmem + TM_O + x * 128, tmem + TM_S + x * 128 + kk * 8, bd, id_pv, (t >= 2 || kk > 0) ? 1u : 0u);
-          }
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            mma_ts<desc_hi(1024, true)>(tmem + TM_O + x * 128, tmem + TM_S + x * 128 + kk * 8, bd + kk * (2048 >> 4), id_pv,
+                                        any || kk > 0);
           mma_commit(bar(B_PV_DONE + x));
-          if (!u.dual || x == 1) mma_commit(bar(B_V_EMPTY + s));
+          if (!u.dual || x == 1) mma_commit(bar(B_V_EMPTY) + 8u * s);
           return true;
         };
-        for (int t = 0; t < 2 && t < steps && ok; ++t) ok = issue_qk(t);
-        for (int t = 0; t < steps && ok; ++t) {
-          ok = issue_pv(t);
-          if (ok && t + 2 < steps) ok = issue_qk(t + 2);
+        // Steps t and t + 1 of buffers 0 and 1: P.V of step t, then Q.K^T of step t + 2.
+        const uint32_t per = u.dual ? 1u : 2u, odd = u.dual ? 0u : 1u;   // key tiles a pair of steps, of its second
+        uint32_t kt = kc - per, i = 0xffffffffu;                         // the pair's first key tile, its number
+#pragma unroll 1
+        for (int t = -2; t < steps && ok; t += 2, kt += per, ++i) {
+          const bool any = (int32_t)i > 0;
+          if (t >= 0) ok = issue_pv(0, kt, done0 + i, any);
+          if (ok && t + 2 < steps) ok = issue_qk(0, kt + per, done0 + i + 1u, t >= 0);
+          if (ok && t >= 0 && t + 1 < steps) ok = issue_pv(1, kt + odd, done1 + i, any);
+          if (ok && t + 3 < steps) ok = issue_qk(1, kt + per + odd, done1 + i + 1u, t >= 0);
         }
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
       kc += (uint32_t)nk;
-      done[0] += (uint32_t)(steps + 1) / 2;
-      done[1] += (uint32_t)steps / 2;
+      done0 += (uint32_t)(steps + 1) / 2;
+      done1 += (uint32_t)steps / 2;
       ++units;
     }
     if (lane == 0) {
       // Drain: every MMA issued has completed before TMEM is freed.
       mma_commit(bar(B_DRAIN));
-      wait_bar(bar(B_DRAIN), 0, abort_flag, p.err);
+      wait_long(bar(B_DRAIN), 0, abort_flag, p.err);
     }
-  } else if (warp < 4) {
+  } else if (warp < 4 || warp == 12) {
     // ------------------------------------------------------ int8 -> fp16 converters
-    // A tile of K or V is 32 items of 16 tokens x 2 chunks of 16 bytes, lane l taking token l % 16
-    // and chunk l / 16 of its item: a warp loads 16 full 32-byte sectors and its fp16 stores hit
-    // every bank once per 128 bytes.  fp16 element (token n, d) lands at (d / 8) * 2048 + n * 16 +
-    // (d % 8) * 2.  The next tile's loads go out as soon as this one's registers are written.
-    const int w3 = warp - 1;
-    constexpr int kItems = 11;                               // of 32, every third
-    const int64_t row_stride = (int64_t)p.Hkv * kD;
+    // A warp has 32 keys of a tile.  A load takes four whole rows of 128 bytes, so that every line is
+    // asked for once: lane l has bytes 16 (l % 8) .. of row l / 8, and lanes l % 8 >= 4 that of the row's
+    // neighbour (l / 8) ^ 1.  The two 16-byte fp16 chunks a lane gets go to chunks 2c and 2c + 1 of the key's
+    // swizzled row; the neighbour's row has the other parity, so the eight lanes of a store hit different
+    // banks.  A lane looks one key up in the block table, the others get its row by shuffles.  Keys past the
+    // end are the last key again: their weights are zero.  The next tile's loads go out as soon as this one's
+    // registers are written.
+    const int cw = warp < 4 ? warp - 1 : 3, cl = lane & 7, rl = (lane >> 3) ^ (cl >> 2);
+    const int row_stride = p.Hkv * kD;
     Part u = {};
     bool more = true;
     int j = 0, n_keys = 0;                                   // next tile to load, of u
-    int64_t rows[8];                                         // cache rows of this lane's tokens, -1: none
+    int row[8];                                              // cache rows of the lane's eight loads
     auto next_tile = [&]() {                                 // false: nothing left
       while (j >= u.t1) {
-        if (!walk.next(p, u, lane)) return false;
+        if (!walk_next(p, walk, u, lane)) return false;
         j = u.t0;
         n_keys = p.causal ? u.nkv - u.nq + min(u.nq, (u.rb + 1) * 2 * p.P) : u.nkv;
       }
-#pragma unroll
-      for (int tg = 0; tg < 8; ++tg) {
-        const int t = j * kKeys + tg * 16 + (lane & 15);
-        rows[tg] = t < n_keys ? key_row(p, u.b, t) : -1;
+      const uint32_t t = (uint32_t)min(j * kKeys + 32 * cw + lane, n_keys - 1);
+      int mine;
+      if (p.block_table) {
+        const uint32_t pi = divu32(t, p.div_ps);
+        int pg = __ldg(p.block_table + (int64_t)u.b * p.max_pages + pi);
+        if ((uint32_t)pg >= (uint32_t)p.num_pages) {         // outside the pool: any row of it
+          set_dev_err(p.err, FA3_DEVERR_PAGE);
+          pg = 0;
+        }
+        mine = pg * p.page_size + (int)(t - pi * (uint32_t)p.page_size);
+      } else {
+        mine = u.b * p.T + (int)t;
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) row[i] = __shfl_sync(0xffffffffu, mine, 4 * i + rl);
       ++j;
       return true;
     };
-    uint4 kr[kItems], vr[kItems];
-    auto load = [&](const int8_t* base, uint4 (&r)[kItems]) {
+    uint4 kr[8], vr[8];
+    auto load = [&](const int8_t* base, uint4 (&r)[8]) {
 #pragma unroll
-      for (int i = 0; i < kItems; ++i) {
-        r[i] = make_uint4(0u, 0u, 0u, 0u);
-        // item w3 + 3 i; rows[] is indexed by a constant: each i meets at most two token groups
-        const int lo = (3 * i) >> 2, hi = (3 * i + 2) >> 2 < 8 ? (3 * i + 2) >> 2 : 7;
-        const int item = w3 + 3 * i;
-        const int64_t kr_ = (item >> 2) == lo ? rows[lo] : rows[hi];
-        if (item < 32 && kr_ >= 0)
-          r[i] = __ldg(reinterpret_cast<const uint4*>(base + kr_ * row_stride) + (item & 3) * 2 + (lane >> 4));
-      }
+      for (int i = 0; i < 8; ++i) r[i] = load_once(base + (int64_t)row[i] * row_stride);
     };
-    auto store = [&](uint8_t* dst, const uint4 (&r)[kItems]) {
+    // chunk 2 cl (and 2 cl + 1) of key n: half cl / 4, row n, chunk ((2 cl) % 8) ^ (n % 8)
+    const uint32_t dst0 = sbase + (uint32_t)(cl >> 2) * KV_HALF + (uint32_t)(32 * cw + rl) * 128;
+    const uint32_t at0 = ((uint32_t)(2 * cl & 7) ^ (uint32_t)rl) * 16;   // n % 8 = rl, or rl + 4 for odd i
+    auto store = [&](uint32_t tile, const uint4 (&r)[8]) {
 #pragma unroll
-      for (int i = 0; i < kItems; ++i) {
-        const int item = w3 + 3 * i;
-        if (item < 32) {
-          const int n = (item >> 2) * 16 + (lane & 15), cc = (item & 3) * 2 + (lane >> 4);
-          uint4 o0, o1;
-          i8x4_to_f16x4(r[i].x, o0.x, o0.y);
-          i8x4_to_f16x4(r[i].y, o0.z, o0.w);
-          i8x4_to_f16x4(r[i].z, o1.x, o1.y);
-          i8x4_to_f16x4(r[i].w, o1.z, o1.w);
-          *reinterpret_cast<uint4*>(dst + (2 * cc) * 2048 + n * 16) = o0;
-          *reinterpret_cast<uint4*>(dst + (2 * cc + 1) * 2048 + n * 16) = o1;
-        }
+      for (int i = 0; i < 8; ++i) {
+        uint4 o0, o1;
+        i8x4_to_f16x4(r[i].x, o0.x, o0.y);
+        i8x4_to_f16x4(r[i].y, o0.z, o0.w);
+        i8x4_to_f16x4(r[i].z, o1.x, o1.y);
+        i8x4_to_f16x4(r[i].w, o1.z, o1.w);
+        const uint32_t at = at0 ^ ((i & 1) ? 64u : 0u);
+        sts128(tile + dst0 + 4 * i * 128 + at, o0);
+        sts128(tile + dst0 + 4 * i * 128 + (at ^ 16u), o1);
       }
       fence_proxy_async();
     };
     more = next_tile();
     if (more) {
-      load(p.k + (int64_t)u.g * kD, kr);
-      load(p.v + (int64_t)u.g * kD, vr);
+      load(p.k + (int64_t)u.g * kD + cl * 16, kr);
+      load(p.v + (int64_t)u.g * kD + cl * 16, vr);
     }
     for (uint32_t kc = 0; more; ++kc) {
       const uint32_t s = kc & 1u, par = ((kc >> 1) & 1u) ^ 1u;
-      if (!warp_all(wait_bar(bar(B_K_EMPTY + s), par, abort_flag, p.err))) break;
-      store(smem + OFF_K + s * KV_TILE, kr);
-      mbar_arrive(bar(B_K_FULL + s));
+      if (!warp_wait(bar(B_K_EMPTY + s), par, lane, abort_flag, p.err)) break;
+      store(OFF_K + s * KV_TILE, kr);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_K_FULL + s));
       more = next_tile();
-      if (more) load(p.k + (int64_t)u.g * kD, kr);
-      if (!warp_all(wait_bar(bar(B_V_EMPTY + s), par, abort_flag, p.err))) break;
-      store(smem + OFF_V + s * KV_TILE, vr);
-      mbar_arrive(bar(B_V_FULL + s));
-      if (more) load(p.v + (int64_t)u.g * kD, vr);
+      if (more) load(p.k + (int64_t)u.g * kD + cl * 16, kr);
+      if (!warp_wait(bar(B_V_EMPTY + s), par, lane, abort_flag, p.err)) break;
+      store(OFF_V + s * KV_TILE, vr);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_V_FULL + s));
+      if (more) load(p.v + (int64_t)u.g * kD + cl * 16, vr);
     }
   } else {
     // ------------------------------------------------------------ softmax warps
@@ -491,7 +562,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
     uint32_t done = 0, done_other = 0, merges = 0;          // steps of this buffer and the other, merged units
     bool ok = true;
     Part u;
-    while (ok && walk.next(p, u, lane)) {
+    while (ok && walk_next(p, walk, u, lane)) {
       const int nk = u.t1 - u.t0, steps = u.dual ? 2 * nk : nk, mine = (steps + 1 - x) / 2;
       const int pl = r / p.G, hh = u.g * p.G + r - pl * p.G;  // position in the row tile, query head
       const int i = u.rb * 2 * p.P + (u.dual ? x * p.P : 0) + pl;
@@ -528,47 +599,62 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
       warp_arrive(B_Q_READY);
       const int pos = !active ? -1 : p.causal ? u.nkv - u.nq + i : u.nkv - 1;   // last key this row sees
       const int pos_min = __reduce_min_sync(0xffffffffu, active ? pos : 0x7fffffff);
-      const float c = active ? p.q_scale[hh] * p.k_scale[u.g] * p.sm_log2 : 0.f;
+      // positive, so that -inf * c stays -inf; with a scale of zero every score still rounds to weight 1
+      const float c = active ? fmaxf(p.q_scale[hh] * p.k_scale[u.g] * p.sm_log2, 1e-37f) : 1.f;
       float m_run = -CUDART_INF_F, l_run = 0.f;
       for (int st = 0; st < mine && ok; ++st) {
         const uint32_t ph = done + (uint32_t)st;
-        if (!warp_all(wait_bar(bar(B_S_FULL + x), ph & 1u, abort_flag, p.err))) {
+        if (!warp_wait(bar(B_S_FULL + x), ph & 1u, lane, abort_flag, p.err)) {
           ok = false;
           break;
         }
         if (warp_active) {
           tc_fence_after();
-          const int t0 = (u.t0 + (u.dual ? st : 2 * st + x)) * kKeys;
-          const bool masked = t0 + kKeys - 1 > pos_min;       // some active row of the warp does not see all keys
-          const int last = pos - t0;                          // this row's last key of the tile
-          // the row's maximum of the integer scores; a masked score counts as -inf
-          uint32_t v[2][32];
-          float mx = -CUDART_INF_F, mx1 = -CUDART_INF_F;
-          FA3_TMEM_LD32(scol, v[0]);
+          const int t0 = (u.t0 + (u.dual ? st : 2 * st + x)) * kKeys;   // the tile's first key
+          if (t0 + kKeys - 1 > pos_min) {
+            // some active row of the warp does not see all keys: their scores become -inf
+            const int last = pos - t0;
+#pragma unroll 1
+            for (int c16 = 0; c16 < 8; ++c16) {
+              uint32_t w[16];
+              FA3_TMEM_LD16(scol + c16 * 16, w);
+              tmem_wait_ld();
 #pragma unroll
-          for (int c4 = 0; c4 < 4; ++c4) {
-            uint32_t* w = v[c4 & 1];
-            wait_ld32(w);
-            if (c4 < 3) FA3_TMEM_LD32(scol + (c4 + 1) * 32, v[(c4 + 1) & 1]);
-            if (masked) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) w[e] = 32 * c4 + e <= last ? w[e] : 0xff800000u;
+              for (int e = 0; e < 16; ++e) w[e] = 16 * c16 + e <= last ? w[e] : 0xff800000u;
+              FA3_TMEM_ST16(scol + c16 * 16, w);
             }
+            tmem_wait_st();
+          }
+          // The row's maximum of the integer scores.  The loops over the columns stay rolled: the roles'
+          // code has to fit the instruction cache together.
+          uint32_t v0[32], v1[32];
+          float mx = -CUDART_INF_F, mx1 = -CUDART_INF_F;
+          FA3_TMEM_LD32(scol, v0);
+#pragma unroll 1
+          for (int c2 = 0; c2 < 2; ++c2) {
+            wait_ld32(v0);
+            FA3_TMEM_LD32(scol + c2 * 64 + 32, v1);
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
-              mx = max3(mx, __uint_as_float(w[e]), __uint_as_float(w[e + 1]));
-              mx1 = max3(mx1, __uint_as_float(w[e + 2]), __uint_as_float(w[e + 3]));
+              mx = max3(mx, __uint_as_float(v0[e]), __uint_as_float(v0[e + 1]));
+              mx1 = max3(mx1, __uint_as_float(v0[e + 2]), __uint_as_float(v0[e + 3]));
+            }
+            wait_ld32(v1);
+            FA3_TMEM_LD32(scol + (c2 ? 0 : 64), v0);           // the next half, then the first again
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              mx = max3(mx, __uint_as_float(v1[e]), __uint_as_float(v1[e + 1]));
+              mx1 = max3(mx1, __uint_as_float(v1[e + 2]), __uint_as_float(v1[e + 3]));
             }
           }
-          FA3_TMEM_LD32(scol, v[0]);
           mx = fmaxf(mx, mx1);
-          mx = mx == -CUDART_INF_F ? mx : mx * c;
+          mx *= c;
           // Lazy rescale: the reference maximum moves only when the row maximum grew by more than 8
           // (log2 units); then O (P.V up to this buffer's step before) is scaled in place.
           const bool grow = mx > m_run + 8.f || (m_run == -CUDART_INF_F && mx != -CUDART_INF_F);
           const bool scale_o = grow && m_run != -CUDART_INF_F;
           if (__any_sync(0xffffffffu, scale_o)) {
-            if (!warp_all(wait_bar(bar(B_PV_DONE + x), (ph - 1u) & 1u, abort_flag, p.err))) {
+            if (!warp_wait(bar(B_PV_DONE + x), (ph - 1u) & 1u, lane, abort_flag, p.err)) {
               ok = false;
               break;
             }
@@ -592,26 +678,27 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
           // P = exp2(s c - m) as fp16 pairs over the S columns (keys 32 c4 .. 32 c4 + 31 go to columns
           // 16 c4 .. 16 c4 + 15); the row sum takes the weights before the rounding.
           float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-          for (int c4 = 0; c4 < 4; ++c4) {
+          auto weigh = [&](const uint32_t (&w)[32], uint32_t col) {
             uint32_t pk[16];
-            uint32_t* w = v[c4 & 1];
-            wait_ld32(w);
-            if (c4 < 3) FA3_TMEM_LD32(scol + (c4 + 1) * 32, v[(c4 + 1) & 1]);
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
               float p0, p1;
               fma2(p0, p1, __uint_as_float(w[e]), __uint_as_float(w[e + 1]), c, c, mc, mc);
               p0 = ex2_approx(p0);
               p1 = ex2_approx(p1);
-              if (masked) {
-                p0 = 32 * c4 + e <= last ? p0 : 0.f;
-                p1 = 32 * c4 + e + 1 <= last ? p1 : 0.f;
-              }
               add2(l0, l1, l0, l1, p0, p1);
               pk[e / 2] = pack_f16x2(p0, p1);
             }
-            FA3_TMEM_ST16(scol + c4 * 16, pk);
+            FA3_TMEM_ST16(col, pk);
+          };
+#pragma unroll 1
+          for (int c2 = 0; c2 < 2; ++c2) {
+            wait_ld32(v0);
+            FA3_TMEM_LD32(scol + c2 * 64 + 32, v1);
+            weigh(v0, scol + c2 * 32);
+            wait_ld32(v1);
+            if (c2 == 0) FA3_TMEM_LD32(scol + 64, v0);
+            weigh(v1, scol + c2 * 32 + 16);
           }
           l_run += l0 + l1;
           tmem_wait_st();
@@ -625,15 +712,15 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
       // ---------------------------------------------------------- epilogue
       // O_x is complete when the buffer's last P.V is.  A single row tile has both buffers' results for
       // the same rows: both warpgroups read both and write half of the columns each.
-      if (mine > 0) ok = warp_all(wait_bar(bar(B_PV_DONE + x), (done - 1u) & 1u, abort_flag, p.err));
+      if (mine > 0) ok = warp_wait(bar(B_PV_DONE + x), (done - 1u) & 1u, lane, abort_flag, p.err);
       float f_mine = 1.f, f_other = 0.f;
       bool both = false;
       if (!u.dual) {
         ml[x * kRows + r] = make_float2(m_run, l_run);
         warp_arrive(B_ML + x);
-        ok = ok && warp_all(wait_bar(bar(B_ML + (x ^ 1)), merges & 1u, abort_flag, p.err));
+        ok = ok && warp_wait(bar(B_ML + (x ^ 1)), merges & 1u, lane, abort_flag, p.err);
         both = steps > mine;
-        if (ok && both) ok = warp_all(wait_bar(bar(B_PV_DONE + (x ^ 1)), (done_other - 1u) & 1u, abort_flag, p.err));
+        if (ok && both) ok = warp_wait(bar(B_PV_DONE + (x ^ 1)), (done_other - 1u) & 1u, lane, abort_flag, p.err);
         if (!ok) break;
         const float2 o = ml[(x ^ 1) * kRows + r];
         const float m = fmaxf(m_run, o.x);
@@ -690,7 +777,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
         // the other warpgroup's next P.V may overwrite what this one reads, and this one's that one's
         tc_fence_before();
         warp_arrive(B_READ + x);
-        ok = warp_all(wait_bar(bar(B_READ + (x ^ 1)), (merges - 1u) & 1u, abort_flag, p.err));
+        ok = warp_wait(bar(B_READ + (x ^ 1)), (merges - 1u) & 1u, lane, abort_flag, p.err);
       }
     }
   }
@@ -805,7 +892,8 @@ int chunk_attn(ChunkParams& p, int D, float softmax_scale, void* workspace, size
   if (p.n <= 0 || p.B <= 0 || p.T <= 0 || p.Hq <= 0 || p.Hkv <= 0 || D <= 0 || p.Hq % p.Hkv != 0) return FA3_EINVAL;
   if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale)) return FA3_EINVAL;
   p.G = p.Hq / p.Hkv;
-  if (D != kD || p.G > kRows) return FA3_ERANGE;
+  if (D != kD || p.G > kRows || p.Hkv > 65535) return FA3_ERANGE;
+  if ((p.block_table ? (int64_t)p.num_pages * p.page_size : (int64_t)p.B * p.T) >= ((int64_t)1 << 31)) return FA3_ERANGE;
   if (!aligned16(p.q) || !aligned16(p.k) || !aligned16(p.v) || !aligned16(p.out)) return FA3_ERANGE;
   p.P = kRows / p.G;
   p.sm_log2 = softmax_scale * 1.4426950408889634f;
