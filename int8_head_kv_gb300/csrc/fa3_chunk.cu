@@ -22,7 +22,7 @@
 // end.  A cut unit's parts leave unnormalised O, maximum and sum in the workspace, and
 // chunk_combine_kernel merges them, so one long sequence and a ragged batch both fill the GPU.
 //
-// Roles in the CTA (416 threads): warp 0 issues the MMAs; warps 1-3 and 12 look keys up in the
+// Roles in the CTA (512 threads): warp 0 issues the MMAs; warps 12-15 look keys up in the
 // block table, load int8 K and V tiles one tile ahead into registers and write them as fp16
 // into one of two stages; warps 4-7 and 8-11 (a row a lane) run the softmax of buffers 0
 // and 1.  int8 codes are exact in fp16 and a 128-term sum of their products
@@ -48,7 +48,11 @@ namespace {
 constexpr int kD = 128;            // head dim
 constexpr int kKeys = 128;         // keys per tile
 constexpr int kRows = 128;         // rows (TMEM lanes) per row tile
-constexpr int kThreadsC = 416;     // warp 0: MMA; 4-7 / 8-11: softmax of buffer 0 / 1; 1-3 and 12: converters
+constexpr int kThreadsC = 512;     // warp 0: MMA; 4-7 / 8-11: softmax of buffer 0 / 1; 12-15: converters
+// Registers a thread of each warpgroup (launched with 128 each, 512 in all).  Nothing in the loops may spill: local
+// memory goes to L2, since shared memory leaves no L1 to speak of.
+constexpr int kRegsIssue = 72, kRegsSoftmax = 152, kRegsConvert = 136;
+static_assert(kRegsIssue + 2 * kRegsSoftmax + kRegsConvert <= 512, "register file");
 constexpr uint32_t TM_O = 0, TM_S = 256;                   // O_x [128x, +128), S_x [256 + 128x, +128)
 constexpr uint32_t KV_TILE = kKeys * kD * 2;               // 32 KB of fp16
 constexpr uint32_t KV_HALF = KV_TILE / 2;                  // 64 values of d: 128 keys x 128 B, 128-byte swizzle
@@ -58,7 +62,7 @@ constexpr uint32_t OFF_K = OFF_Q + 2 * Q_TILE;             // 2 stages
 constexpr uint32_t OFF_V = OFF_K + 2 * KV_TILE;            // 2 stages
 constexpr uint32_t OFF_ML = OFF_V + 2 * KV_TILE;           // [2][128] float2: (m, l) of a single row tile's halves
 constexpr uint32_t OFF_WALK = OFF_ML + 2 * kRows * 8;      // a Walk a warp
-constexpr uint32_t OFF_BAR = OFF_WALK + 13 * 64;
+constexpr uint32_t OFF_BAR = OFF_WALK + 16 * 128;
 enum {
   B_K_FULL = 0, B_K_EMPTY = 2, B_V_FULL = 4, B_V_EMPTY = 6,
   B_S_FULL = 8,                    // [2]: buffer x's scores of its next step
@@ -239,54 +243,64 @@ struct Part {
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == nt; }
 };
 
-// A CTA's parts in order.  Every warp walks them by itself, its place kept in shared memory (it is looked at
-// once a part, and its registers are wanted elsewhere).
+// A CTA's parts in order.  Every warp walks them by itself; its place and the part it is at lie in shared
+// memory: they are looked at once a part, their registers are wanted elsewhere, and local memory is far away
+// (shared memory leaves no L1 to speak of).
 struct Walk {
   Cursor c;
   int64_t left;
+  Part u;
 };
-static_assert(sizeof(Walk) <= 64, "walk area");
+static_assert(sizeof(Walk) <= 128, "walk area");
 __device__ __forceinline__ void walk_begin(const ChunkParams& p, Walk* at, int64_t total, int parts, int cta, int lane) {
   const int64_t x = part_begin(total, parts, cta);
-  Walk w;
-  w.left = part_begin(total, parts, cta + 1) - x;
-  w.c = Cursor{p.B, 0, 0, {0, 0, 0}, 0};
-  if (w.left > 0) w.c = seek(p, x, lane);
-  if (lane == 0) *at = w;
+  const int64_t left = part_begin(total, parts, cta + 1) - x;
+  Cursor c = {p.B, 0, 0, {0, 0, 0}, 0};
+  if (left > 0) c = seek(p, x, lane);
+  if (lane == 0) {
+    at->c = c;
+    at->left = left;
+  }
   __syncwarp();
 }
-__device__ __noinline__ bool walk_next(const ChunkParams& p, Walk* at, Part& u, int lane) {
-  Walk w = *at;
+// Moves to the next part, at->u; false: there is none.
+__device__ __forceinline__ bool walk_next(const ChunkParams& p, Walk* at, int lane) {
+  Cursor c = at->c;
+  int64_t left = at->left;
+  Part u = {};
   bool got = false;
-  while (w.left > 0 && !got) {
-    Cursor& c = w.c;
+  while (left > 0 && !got) {
     const int nt = tiles_of(p, c.s, c.rb);
     const bool dual = is_dual(p, c.s, c.rb);
     const int64_t cost = kUnitCost + (int64_t)nt * (dual ? 2 : 1);
-    const int64_t take = cost - c.off < w.left ? cost - c.off : w.left;
+    const int64_t take = cost - c.off < left ? cost - c.off : left;
     u = Part{c.b, c.g, c.rb, c.s.q0, c.s.nq, c.s.nkv, tile_at(c.off, dual, nt), tile_at(c.off + take, dual, nt), nt,
              dual, c.off == 0};
     if (c.off + take == cost) u.t1 = nt;
-    w.left -= take;
+    left -= take;
     c.off = 0;
     if (++c.rb == blocks_of(p, c.s)) {
       c.rb = 0;
       if (++c.g == p.Hkv) {
         c.g = 0;
-        if (w.left > 0) to_sequence(p, c, c.b + 1, lane);
+        if (left > 0) to_sequence(p, c, c.b + 1, lane);
       }
     }
     got = u.t0 < u.t1 || (nt == 0 && u.first);
   }
   __syncwarp();
-  if (lane == 0) *at = w;
+  if (lane == 0) {
+    at->c = c;
+    at->left = left;
+    at->u = u;
+  }
   __syncwarp();
   return got;
 }
 
-// wait_bar with its loop out of line: the roles' code has to fit the instruction cache together.  The test
-// suspends the thread by itself for a while, and the clock and the abort flag are looked at now and then.
-__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, int32_t* err) {
+// wait_bar for waits that last: the test suspends the thread by itself for a while, and the clock and the
+// abort flag are looked at now and then only.
+__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, int32_t* err) {
   const uint64_t t0 = global_ns();
   for (;;) {
 #pragma unroll 1
@@ -330,27 +344,44 @@ __device__ __forceinline__ uint4 load_once(const int8_t* p) {
   return v;
 }
 
+template <int N>
+__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
 // MMAs on descriptors given by their low words (address and leading stride; the step along the contraction
-// is one 32-bit addition): the issuing thread is one warp's worth of instructions, so each one counts.
+// is one 32-bit addition).  The whole warp runs the issuing code, converged, so that its addresses stay in
+// uniform registers, and the elected lane's predicate guards the instruction itself.
 __host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo, bool swizzle) { return (sbo >> 4) | (1u << 14) | (swizzle ? 2u << 29 : 0u); }
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4) | ((lbo >> 4) << 16); }
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+  return e;
+}
 template <uint32_t HI_A, uint32_t HI_B>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n.reg .pred p;\n.reg .b64 a, b;\nmov.b64 a, {%1, %5};\nmov.b64 b, {%2, %6};\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n"
-      ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"((uint32_t)acc), "n"(HI_A), "n"(HI_B) : "memory");
+      "{\n.reg .pred p, e;\n.reg .b64 a, b;\nsetp.ne.b32 e, %0, 0;\nsetp.ne.b32 p, %5, 0;\n"
+      "mov.b64 a, {%2, %6};\nmov.b64 b, {%3, %7};\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%1], a, b, %4, p;\n}\n"
+      ::"r"(lead), "r"(d), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "n"(HI_A), "n"(HI_B) : "memory");
 }
 template <uint32_t HI>
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n.reg .pred p;\n.reg .b64 b;\nmov.b64 b, {%2, %5};\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n"
-      ::"r"(d), "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"((uint32_t)acc), "n"(HI) : "memory");
+      "{\n.reg .pred p, e;\n.reg .b64 b;\nsetp.ne.b32 e, %0, 0;\nsetp.ne.b32 p, %5, 0;\nmov.b64 b, {%3, %6};\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], b, %4, p;\n}\n"
+      ::"r"(lead), "r"(d), "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(acc), "n"(HI) : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n.reg .pred e;\nsetp.ne.b32 e, %1, 0;\n"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar), "r"(lead)
+      : "memory");
 }
 
 __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_constant__ ChunkParams p) {
@@ -396,52 +427,60 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TSLOT);
 
+  if (warp < 4) {
+    reg_dec<kRegsIssue>();
+  } else if (warp < 12) {
+    reg_inc<kRegsSoftmax>();
+  } else {
+    reg_inc<kRegsConvert>();
+  }
   if (warp == 0) {
     // ------------------------------------------------------------ MMA issuer
     const uint32_t id_qk = idesc_f16(kRows, kKeys, false, false);
     const uint32_t id_pv = idesc_f16(kRows, kD, false, true);
     uint32_t kc = 0, done0 = 0, done1 = 0, units = 0;         // key tiles, steps of each buffer, units so far
     bool ok = true;
-    Part u;
-    while (ok && walk_next(p, walk, u, lane)) {
+    const uint32_t lead = elect_one();
+    while (ok && walk_next(p, walk, lane)) {
+      struct { int t0, t1, nt; bool dual; } u = {walk->u.t0, walk->u.t1, walk->u.nt, walk->u.dual};
       if (u.nt == 0) continue;
       const int nk = u.t1 - u.t0, steps = u.dual ? 2 * nk : nk;
-      if (lane == 0) {
-        ok = wait_long(bar(B_Q_READY), units & 1u, abort_flag, p.err);
+      {
+        ok = warp_all(wait_long(bar(B_Q_READY), units & 1u, abort_flag, p.err));
         // S_x = Q.K^T: the row tile's K-major A operand in shared memory (8-row core groups 128 B
         // apart, 8-wide d groups 2048 B apart), K the K-major B operand (128-byte swizzle: 8-key groups
         // 1024 B apart, 16 values of d 32 B apart within a half).  S_x holds the P of the buffer's step
         // before until its P.V is done (d: the buffer's steps before this one, any: in this unit).
         auto issue_qk = [&](const int x, uint32_t kt, uint32_t d, bool any) -> bool {
           const uint32_t s = kt & 1u;
-          if (!wait_long(bar(B_K_FULL) + 8u * s, (kt >> 1) & 1u, abort_flag, p.err)) return false;
-          if (any && !wait_long(bar(B_PV_DONE + x), (d - 1u) & 1u, abort_flag, p.err)) return false;
+          if (!warp_all(wait_long(bar(B_K_FULL) + 8u * s, (kt >> 1) & 1u, abort_flag, p.err))) return false;
+          if (any && !warp_all(wait_long(bar(B_PV_DONE + x), (d - 1u) & 1u, abort_flag, p.err))) return false;
           tc_fence_after();
           const uint32_t a = desc_lo(sbase + OFF_Q + (u.dual ? x : 0) * Q_TILE, 2048);
           const uint32_t bd = desc_lo(sbase + OFF_K + s * KV_TILE, 16);
 #pragma unroll
           for (int kk = 0; kk < kD / 16; ++kk)
             mma_ss<desc_hi(128, false), desc_hi(1024, true)>(
-                tmem + TM_S + x * 128, a + kk * (4096 >> 4), bd + (kk / 4) * (KV_HALF >> 4) + (kk % 4) * (32 >> 4), id_qk,
-                kk > 0);
-          mma_commit(bar(B_S_FULL + x));
-          if (!u.dual || x == 1) mma_commit(bar(B_K_EMPTY) + 8u * s);    // all steps of this key tile have it
+                lead, tmem + TM_S + x * 128, a + kk * (4096 >> 4), bd + (kk / 4) * (KV_HALF >> 4) + (kk % 4) * (32 >> 4), id_qk,
+                kk > 0 ? 1u : 0u);
+          commit_if(lead, bar(B_S_FULL + x));
+          if (!u.dual || x == 1) commit_if(lead, bar(B_K_EMPTY) + 8u * s);    // all steps of this key tile have it
           return true;
         };
         // O_x += P_x.V: P_x (fp16, over S_x: column k holds keys 2k, 2k + 1) is the A operand in
         // TMEM, V the MN-major B operand (128-byte swizzle: 8-key groups 1024 B apart, halves of d 16 KB).
         auto issue_pv = [&](const int x, uint32_t kt, uint32_t d, bool any) -> bool {
           const uint32_t s = kt & 1u;
-          if (!wait_long(bar(B_V_FULL) + 8u * s, (kt >> 1) & 1u, abort_flag, p.err)) return false;
-          if (!wait_long(bar(B_P_FULL + x), d & 1u, abort_flag, p.err)) return false;
+          if (!warp_all(wait_long(bar(B_V_FULL) + 8u * s, (kt >> 1) & 1u, abort_flag, p.err))) return false;
+          if (!warp_all(wait_long(bar(B_P_FULL + x), d & 1u, abort_flag, p.err))) return false;
           tc_fence_after();
           const uint32_t bd = desc_lo(sbase + OFF_V + s * KV_TILE, KV_HALF);
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma_ts<desc_hi(1024, true)>(tmem + TM_O + x * 128, tmem + TM_S + x * 128 + kk * 8, bd + kk * (2048 >> 4), id_pv,
-                                        any || kk > 0);
-          mma_commit(bar(B_PV_DONE + x));
-          if (!u.dual || x == 1) mma_commit(bar(B_V_EMPTY) + 8u * s);
+            mma_ts<desc_hi(1024, true)>(lead, tmem + TM_O + x * 128, tmem + TM_S + x * 128 + kk * 8, bd + kk * (2048 >> 4), id_pv,
+                                        any || kk > 0 ? 1u : 0u);
+          commit_if(lead, bar(B_PV_DONE + x));
+          if (!u.dual || x == 1) commit_if(lead, bar(B_V_EMPTY) + 8u * s);
           return true;
         };
         // Steps t and t + 1 of buffers 0 and 1: P.V of step t, then Q.K^T of step t + 2.
@@ -456,18 +495,15 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
           if (ok && t + 3 < steps) ok = issue_qk(1, kt + per + odd, done1 + i + 1u, t >= 0);
         }
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
       kc += (uint32_t)nk;
       done0 += (uint32_t)(steps + 1) / 2;
       done1 += (uint32_t)steps / 2;
       ++units;
     }
-    if (lane == 0) {
-      // Drain: every MMA issued has completed before TMEM is freed.
-      mma_commit(bar(B_DRAIN));
-      wait_long(bar(B_DRAIN), 0, abort_flag, p.err);
-    }
-  } else if (warp < 4 || warp == 12) {
+    // Drain: every MMA issued has completed before TMEM is freed.
+    commit_if(lead, bar(B_DRAIN));
+    wait_long(bar(B_DRAIN), 0, abort_flag, p.err);
+  } else if (warp >= 12) {
     // ------------------------------------------------------ int8 -> fp16 converters
     // A warp has 32 keys of a tile.  A load takes four whole rows of 128 bytes, so that every line is
     // asked for once: lane l has bytes 16 (l % 8) .. of row l / 8, and lanes l % 8 >= 4 that of the row's
@@ -476,30 +512,34 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
     // banks.  A lane looks one key up in the block table, the others get its row by shuffles.  Keys past the
     // end are the last key again: their weights are zero.  The next tile's loads go out as soon as this one's
     // registers are written.
-    const int cw = warp < 4 ? warp - 1 : 3, cl = lane & 7, rl = (lane >> 3) ^ (cl >> 2);
+    const int cw = warp - 12, cl = lane & 7, rl = (lane >> 3) ^ (cl >> 2);
     const int row_stride = p.Hkv * kD;
-    Part u = {};
     bool more = true;
-    int j = 0, n_keys = 0;                                   // next tile to load, of u
+    int j = 0, t_end = 0, n_keys = 0, b = 0;                 // next tile to load, of sequence b
+    int64_t head = 0;                                        // offset of the KV head in a row
     int row[8];                                              // cache rows of the lane's eight loads
     auto next_tile = [&]() {                                 // false: nothing left
-      while (j >= u.t1) {
-        if (!walk_next(p, walk, u, lane)) return false;
+      while (j >= t_end) {
+        if (!walk_next(p, walk, lane)) return false;
+        const Part& u = walk->u;
         j = u.t0;
+        t_end = u.t1;
+        b = u.b;
+        head = u.g * kD + cl * 16;
         n_keys = p.causal ? u.nkv - u.nq + min(u.nq, (u.rb + 1) * 2 * p.P) : u.nkv;
       }
       const uint32_t t = (uint32_t)min(j * kKeys + 32 * cw + lane, n_keys - 1);
       int mine;
       if (p.block_table) {
         const uint32_t pi = divu32(t, p.div_ps);
-        int pg = __ldg(p.block_table + (int64_t)u.b * p.max_pages + pi);
+        int pg = __ldg(p.block_table + (int64_t)b * p.max_pages + pi);
         if ((uint32_t)pg >= (uint32_t)p.num_pages) {         // outside the pool: any row of it
           set_dev_err(p.err, FA3_DEVERR_PAGE);
           pg = 0;
         }
         mine = pg * p.page_size + (int)(t - pi * (uint32_t)p.page_size);
       } else {
-        mine = u.b * p.T + (int)t;
+        mine = b * p.T + (int)t;
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) row[i] = __shfl_sync(0xffffffffu, mine, 4 * i + rl);
@@ -530,8 +570,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
     };
     more = next_tile();
     if (more) {
-      load(p.k + (int64_t)u.g * kD + cl * 16, kr);
-      load(p.v + (int64_t)u.g * kD + cl * 16, vr);
+      load(p.k + head, kr);
+      load(p.v + head, vr);
     }
     for (uint32_t kc = 0; more; ++kc) {
       const uint32_t s = kc & 1u, par = ((kc >> 1) & 1u) ^ 1u;
@@ -540,14 +580,14 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_K_FULL + s));
       more = next_tile();
-      if (more) load(p.k + (int64_t)u.g * kD + cl * 16, kr);
+      if (more) load(p.k + head, kr);
       if (!warp_wait(bar(B_V_EMPTY + s), par, lane, abort_flag, p.err)) break;
       store(OFF_V + s * KV_TILE, vr);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_V_FULL + s));
-      if (more) load(p.v + (int64_t)u.g * kD + cl * 16, vr);
+      if (more) load(p.v + head, vr);
     }
-  } else {
+  } else if (warp >= 4) {
     // ------------------------------------------------------------ softmax warps
     const int x = (warp - 4) >> 2;                          // buffer
     const int r = ((warp - 4) & 3) * 32 + lane;             // row == TMEM lane
@@ -561,8 +601,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
     };
     uint32_t done = 0, done_other = 0, merges = 0;          // steps of this buffer and the other, merged units
     bool ok = true;
-    Part u;
-    while (ok && walk_next(p, walk, u, lane)) {
+    while (ok && walk_next(p, walk, lane)) {
+      const Part u = walk->u;
       const int nk = u.t1 - u.t0, steps = u.dual ? 2 * nk : nk, mine = (steps + 1 - x) / 2;
       const int pl = r / p.G, hh = u.g * p.G + r - pl * p.G;  // position in the row tile, query head
       const int i = u.rb * 2 * p.P + (u.dual ? x * p.P : 0) + pl;
