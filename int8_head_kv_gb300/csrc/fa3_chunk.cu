@@ -344,6 +344,7 @@ __device__ __forceinline__ uint4 load_once(const int8_t* p) {
   return v;
 }
 
+__device__ __forceinline__ void prefetch_line(const int8_t* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 template <int N>
 __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -514,36 +515,50 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
     // registers are written.
     const int cw = warp - 12, cl = lane & 7, rl = (lane >> 3) ^ (cl >> 2);
     const int row_stride = p.Hkv * kD;
-    bool more = true;
-    int j = 0, t_end = 0, n_keys = 0, b = 0;                 // next tile to load, of sequence b
-    int64_t head = 0;                                        // offset of the KV head in a row
-    int row[8];                                              // cache rows of the lane's eight loads
-    auto next_tile = [&]() {                                 // false: nothing left
+    // Two tiles ahead of the one being written: its keys' block-table entries are on their way (pg); one tile
+    // ahead: its rows are known, asked of HBM into L2 and then loaded.
+    bool more = true, ahead = true;
+    int j = 0, t_end = 0, n_keys = 0, b = 0;                 // the tile after the one looked up, of sequence b
+    int g = 0, pg = 0, in_page = 0;                          // the tile looked up: KV head, entry and row in the page
+    int64_t head = 0;                                        // the tile to load: offset of this lane's bytes in a row
+    int row[8];                                              // and the cache rows of the lane's eight loads
+    auto look_up = [&]() {                                   // false: nothing left
       while (j >= t_end) {
         if (!walk_next(p, walk, lane)) return false;
         const Part& u = walk->u;
         j = u.t0;
         t_end = u.t1;
         b = u.b;
-        head = u.g * kD + cl * 16;
+        g = u.g;
         n_keys = p.causal ? u.nkv - u.nq + min(u.nq, (u.rb + 1) * 2 * p.P) : u.nkv;
       }
       const uint32_t t = (uint32_t)min(j * kKeys + 32 * cw + lane, n_keys - 1);
-      int mine;
       if (p.block_table) {
         const uint32_t pi = divu32(t, p.div_ps);
-        int pg = __ldg(p.block_table + (int64_t)b * p.max_pages + pi);
+        pg = __ldg(p.block_table + (int64_t)b * p.max_pages + pi);
+        in_page = (int)(t - pi * (uint32_t)p.page_size);
+      } else {
+        in_page = b * p.T + (int)t;
+      }
+      ++j;
+      return true;
+    };
+    auto next_tile = [&]() {                                 // false: nothing left
+      if (!ahead) return false;
+      int mine = in_page;
+      if (p.block_table) {
         if ((uint32_t)pg >= (uint32_t)p.num_pages) {         // outside the pool: any row of it
           set_dev_err(p.err, FA3_DEVERR_PAGE);
           pg = 0;
         }
-        mine = pg * p.page_size + (int)(t - pi * (uint32_t)p.page_size);
-      } else {
-        mine = b * p.T + (int)t;
+        mine += pg * p.page_size;
       }
+      head = g * kD + cl * 16;
+      prefetch_line(p.k + (int64_t)mine * row_stride + g * kD);
+      prefetch_line(p.v + (int64_t)mine * row_stride + g * kD);
 #pragma unroll
       for (int i = 0; i < 8; ++i) row[i] = __shfl_sync(0xffffffffu, mine, 4 * i + rl);
-      ++j;
+      ahead = look_up();
       return true;
     };
     uint4 kr[8], vr[8];
@@ -568,6 +583,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
       }
       fence_proxy_async();
     };
+    ahead = look_up();
     more = next_tile();
     if (more) {
       load(p.k + head, kr);
