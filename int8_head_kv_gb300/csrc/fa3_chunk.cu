@@ -40,6 +40,7 @@
 #include <math_constants.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 namespace fa3 {
@@ -962,8 +963,14 @@ int chunk_attn(ChunkParams& p, int D, float softmax_scale, void* workspace, size
   p.part_o = static_cast<float4*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)2 * sms * (kD / 4) * p.rows_max);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaFuncSetAttribute(gqa_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_CHUNK) != cudaSuccess)
-    return FA3_ECUDA;
+  static std::atomic<bool> set[64];                          // the kernel's attribute, once a device
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return FA3_ECUDA;
+  if (dev >= 64 || !set[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(gqa_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_CHUNK) != cudaSuccess)
+      return FA3_ECUDA;
+    if (dev < 64) set[dev].store(true, std::memory_order_release);
+  }
   if (launch_pdl(gqa_chunk_kernel, dim3((unsigned)sms), dim3(kThreadsC), SMEM_CHUNK, s, p) != cudaSuccess)
     return FA3_ECUDA;
   if (sms > 1 && launch_pdl(chunk_combine_kernel, dim3((unsigned)(sms - 1), (unsigned)(p.rows_max / 32)), dim3(256), 0, s,

@@ -8,6 +8,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 
 namespace fa3 {
 
@@ -22,16 +23,24 @@ void timing_end(cudaStream_t s) {
   if (g_timing_start && g_timing_stop) cudaEventRecord(g_timing_stop, s);
 }
 
+// The attributes of a device do not change: looked up once each (atomic slots: two host threads may both look
+// them up, and both store the same value).  Value: SM count, or -status.
 int check_device(int* num_sms) {
+  static std::atomic<int> known[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return FA3_ECUDA;
-  int major = 0, minor = 0, sms = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return FA3_ECUDA;
-  if (major != 10 || minor != 3) return FA3_EDEVICE;
-  if (num_sms) *num_sms = sms;
+  int v = dev >= 0 && dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (v == 0) {
+    int major = 0, minor = 0, sms = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return FA3_ECUDA;
+    v = major != 10 || minor != 3 ? -FA3_EDEVICE : sms;
+    if (dev >= 0 && dev < 64) known[dev].store(v, std::memory_order_relaxed);
+  }
+  if (v < 0) return -v;
+  if (num_sms) *num_sms = v;
   return FA3_OK;
 }
 

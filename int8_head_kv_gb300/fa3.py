@@ -573,6 +573,9 @@ def decode_attn_gqa_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_s
 
 
 # ------------------------------------- attention input and packed new rows
+_BF16, _F32, _I32, _I8 = torch.bfloat16, torch.float32, torch.int32, torch.int8
+
+
 def rope_table(n_pos: int, rot_dim: int, base: float = 10000.0, device="cuda",
                inv_freq: Optional[torch.Tensor] = None) -> torch.Tensor:
     """float32 [n_pos][rot_dim] of cos, then sin, of position * inv_freq, computed in
@@ -588,76 +591,37 @@ def rope_table(n_pos: int, rot_dim: int, base: float = 10000.0, device="cuda",
     return torch.cat([a.cos(), a.sin()], 1).float().contiguous()
 
 
-def _on_device(t: torch.Tensor, *others) -> int:
-    """The device index of t, which the other tensors (None allowed) have to share."""
-    dev = t.get_device()
-    for o in others:
-        if o is not None and o.get_device() != dev:
-            raise ValueError("all tensors must be on one device")
-    return dev
+# The calls below are made once a layer and step with little work behind them, so their checks are one
+# expression each; what is wrong is worked out only when something is.
+def _wrong(t, dtype, name: str):
+    _need_contig(t, dtype, name)
+    raise ValueError("all tensors must be on one device")
 
 
-class _Here:
-    """Launches on a tensor's device and, for outputs allocated inside, on the call's stream."""
-
-    __slots__ = ("ctx",)
-
-    def __init__(self, dev: int, stream=None):
-        if stream is not None:
-            if stream.device_index != dev:
-                raise ValueError("stream must be on the tensors' device")
-            self.ctx = torch.cuda.stream(stream)
-        else:
-            self.ctx = torch.cuda.device(dev) if torch.cuda.current_device() != dev else None
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-
-    def __exit__(self, *a):
-        if self.ctx is not None:
-            self.ctx.__exit__(*a)
-
-
-def _opt(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
-def _dev_err(t: Optional[torch.Tensor]) -> None:
-    if t is not None:
-        _need_contig(t, torch.int32, "dev_err")
-        if t.numel() < 1:
-            raise ValueError("dev_err must hold one value")
-
-
-def _rot_table(cos_sin: Optional[torch.Tensor], D: int):
-    if cos_sin is None:
-        return 0, 0
-    _need_contig(cos_sin, torch.float32, "cos_sin")
-    if cos_sin.dim() != 2 or cos_sin.shape[1] > D:
-        raise ValueError("cos_sin must be [table_len][rot_dim] with rot_dim <= D")
-    return cos_sin.shape
-
-
-def _weight(w: Optional[torch.Tensor], D: int, name: str) -> None:
-    if w is not None:
-        _need_contig(w, torch.bfloat16, name)
-        if w.numel() != D:
-            raise ValueError(f"{name} must hold D values")
+def _here(dev: int, stream):
+    """(raw stream of the call, context to enter for its launches and allocations or None)."""
+    if stream is not None:
+        if stream.device_index != dev:
+            raise ValueError("stream must be on the tensors' device")
+        return stream.cuda_stream, torch.cuda.stream(stream)
+    ctx = torch.cuda.device(dev) if torch.cuda.current_device() != dev else None
+    return torch._C._cuda_getCurrentRawStream(dev), ctx
 
 
 def _rows4(t: torch.Tensor, name: str, out: bool = False):
-    """(B, S, H, D) and the strides (b, s, h) of head rows [B][S][H][D] or [n][H][D]."""
-    if t.dim() == 3:
-        t = t.unsqueeze(0)
-    if t.dim() != 4:
+    """Strides (b, s, h) of head rows [B][S][H][D] or [n][H][D]; 0 where there is one index."""
+    st = t.stride()
+    sh = t.shape
+    if len(sh) == 3:
+        st, sh = (0,) + st, (1,) + tuple(sh)
+    if len(sh) != 4:
         raise ValueError(f"{name} must be [B][S][H][D] or [n][H][D]")
-    if t.stride(3) != 1 and t.shape[3] > 1:
+    if st[3] != 1 and sh[3] > 1:
         raise ValueError(f"{name} must have contiguous head rows")
-    st = [0 if t.shape[i] == 1 else t.stride(i) for i in range(3)]
-    if out and any(s == 0 and t.shape[i] > 1 for i, s in enumerate(st)):
+    sb, ss, hs = st[0] if sh[0] > 1 else 0, st[1] if sh[1] > 1 else 0, st[2] if sh[2] > 1 else 0
+    if out and ((sb == 0 and sh[0] > 1) or (ss == 0 and sh[1] > 1) or (hs == 0 and sh[2] > 1)):
         raise ValueError(f"{name} must not be an expanded tensor")
-    return t.shape, st
+    return sb, ss, hs
 
 
 def norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], cos_sin: Optional[torch.Tensor],
@@ -673,83 +637,139 @@ def norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], cos_sin: Optional[torc
     Results are bf16 or float32: contiguous, or in q_out / k_out of q's / k's shape and any
     such strides (a transposed view lays them out (B, H, S, D) for calibrate_perhead; q and
     k themselves are allowed).  Returns (q_out, k_out)."""
-    _need(q, torch.bfloat16, "q")
-    (B, S, Hq, D), qs = _rows4(q, "q")
-    Hkv, ks, kos = 0, (0, 0, 0), (0, 0, 0)
+    _need(q, _BF16, "q")
+    sh = q.shape
+    qs = _rows4(q, "q")
+    B, S, Hq, D = sh if len(sh) == 4 else (1,) + tuple(sh)
+    dev = q.get_device()
+    Hkv, ks, kos, kp, kop = 0, (0, 0, 0), (0, 0, 0), None, None
     if k is not None:
-        _need(k, torch.bfloat16, "k")
-        (kB, kS, Hkv, kD), ks = _rows4(k, "k")
-        if (kB, kS, kD) != (B, S, D) or k.dim() != q.dim():
+        _need(k, _BF16, "k")
+        ks = _rows4(k, "k")
+        ksh = k.shape
+        Hkv = ksh[-2]
+        if len(ksh) != len(sh) or ksh[:-2] != sh[:-2] or ksh[-1] != D:
             raise ValueError("k must have q's tokens and head size")
         if (q_weight is None) != (k_weight is None):
             raise ValueError("q_weight and k_weight go together")
+        kp = k.data_ptr()
     elif k_out is not None or k_weight is not None:
         raise ValueError("k_out and k_weight need k")
-    table_len, rot = _rot_table(cos_sin, D)
+    table_len, rot, cp, pp = 0, 0, None, None
     if cos_sin is not None:
+        table_len, rot, cp = _table(cos_sin, D, dev)
         if pos is None:
             raise ValueError("pos must be given with cos_sin")
-        _need_contig(pos, torch.int32, "pos")
+        if not (pos.dtype is _I32 and pos.get_device() == dev and pos.is_contiguous()):
+            _wrong(pos, _I32, "pos")
         if pos.numel() != B * S:
             raise ValueError("pos must hold one position for each token")
-    _weight(q_weight, D, "q_weight")
-    _weight(k_weight, D, "k_weight")
-    _dev_err(dev_err)
-    dev = _on_device(q, k, cos_sin, pos, q_weight, k_weight, q_out, k_out, dev_err)
-    with _Here(dev, stream):
+        pp = pos.data_ptr()
+    qw, kw = _vector(q_weight, D, _BF16, "q_weight", dev), _vector(k_weight, D, _BF16, "k_weight", dev)
+    ep = _error_word(dev_err, dev)
+    if k is not None and k.get_device() != dev:
+        raise ValueError("all tensors must be on one device")
+    raw, ctx = _here(dev, stream)
+    if ctx is not None:
+        ctx.__enter__()
+    try:
         t = out_dtype if q_out is None else q_out.dtype
-        if t not in (torch.bfloat16, torch.float32):
+        if t is not _BF16 and t is not _F32:
             raise TypeError("results are bfloat16 or float32")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=t, device=q.device)
-        if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=t, device=q.device)
-        for o, x, n in ((q_out, q, "q_out"), (k_out, k, "k_out")):
-            if x is not None and (o.dtype != t or o.shape != x.shape):
-                raise ValueError(f"{n} must have the input's shape and the results' one type")
-        qos = _rows4(q_out, "q_out", out=True)[1]
+            q_out = torch.empty(sh, dtype=t, device=q.device)
+        elif q_out.shape != sh or q_out.get_device() != dev:
+            raise ValueError("q_out must have the input's shape and device")
+        qos = _rows4(q_out, "q_out", True)
         if k is not None:
-            kos = _rows4(k_out, "k_out", out=True)[1]
-        if q.numel():
-            st = lib().fa3_norm_rope(q.data_ptr(), _opt(k), _opt(q_weight), _opt(k_weight), eps, _opt(cos_sin),
-                                     table_len, rot, int(interleaved), _opt(pos), q_out.data_ptr(), _opt(k_out),
-                                     int(t == torch.float32), B, S, Hq, Hkv, D, *qs, *ks, *qos, *kos, _opt(dev_err),
-                                     _stream(stream))
-            _check("fa3_norm_rope", st)
+            if k_out is None:
+                k_out = torch.empty(ksh, dtype=t, device=q.device)
+            elif k_out.dtype is not t or k_out.shape != ksh or k_out.get_device() != dev:
+                raise ValueError("k_out must have the input's shape and device and q_out's type")
+            kos, kop = _rows4(k_out, "k_out", True), k_out.data_ptr()
+        if B * S and Hq and D:
+            st = lib().fa3_norm_rope(q.data_ptr(), kp, qw, kw, eps, cp, table_len, rot, interleaved, pp,
+                                     q_out.data_ptr(), kop, t is _F32, B, S, Hq, Hkv, D, *qs, *ks, *qos, *kos, ep, raw)
+            if st:
+                raise FA3Error("fa3_norm_rope", st)
+    finally:
+        if ctx is not None:
+            ctx.__exit__(None, None, None)
     return q_out, k_out
 
 
-def _packed(q_start: torch.Tensor, lens: torch.Tensor, lens_name: str) -> int:
-    _need_contig(q_start, torch.int32, "q_start")
-    _need_contig(lens, torch.int32, lens_name)
+def _table(cos_sin: torch.Tensor, D: int, dev: int):
+    if not (cos_sin.dtype is _F32 and cos_sin.get_device() == dev and cos_sin.is_contiguous()):
+        _wrong(cos_sin, _F32, "cos_sin")
+    sh = cos_sin.shape
+    if len(sh) != 2 or sh[1] > D:
+        raise ValueError("cos_sin must be [table_len][rot_dim] with rot_dim <= D")
+    return sh[0], sh[1], cos_sin.data_ptr()
+
+
+def _vector(t: Optional[torch.Tensor], n: int, dtype, name: str, dev: int):
+    """The address of n contiguous values, or None."""
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()):
+        _wrong(t, dtype, name)
+    if t.numel() != n:
+        raise ValueError(f"{name} must hold {n} values")
+    return t.data_ptr()
+
+
+def _error_word(t: Optional[torch.Tensor], dev: int):
+    if t is None:
+        return None
+    if not (t.dtype is _I32 and t.get_device() == dev and t.numel() >= 1):
+        _need(t, _I32, "dev_err")
+        raise ValueError("dev_err must hold one value on the tensors' device")
+    return t.data_ptr()
+
+
+def _lens(q_start: torch.Tensor, lens: torch.Tensor, lens_name: str, dev: int) -> int:
+    if not (lens.dtype is _I32 and lens.get_device() == dev and lens.is_contiguous()):
+        _wrong(lens, _I32, lens_name)
     B = lens.numel()
-    if q_start.numel() != B + 1 or B == 0:
+    if B == 0:
+        raise ValueError(f"{lens_name} must not be empty")
+    if not (q_start.dtype is _I32 and q_start.get_device() == dev and q_start.is_contiguous()):
+        _wrong(q_start, _I32, "q_start")
+    if q_start.numel() != B + 1:
         raise ValueError(f"q_start must hold one value more than {lens_name}")
     return B
 
 
-def _packed_rows(t: torch.Tensor, H: int, D: int, n: int, name: str) -> int:
+def _packed_rows(t: torch.Tensor, H: int, D: int, n: int, name: str, dev: int) -> int:
     """Row stride of packed rows [n][H][D] with contiguous rows of heads."""
-    _need(t, torch.bfloat16, name)
-    if t.dim() != 3 or t.shape != (n, H, D):
+    if not (t.dtype is _BF16 and t.get_device() == dev):
+        _need(t, _BF16, name)
+        raise ValueError("all tensors must be on one device")
+    if t.shape != (n, H, D):
         raise ValueError(f"{name} must be [n][H][D]")
-    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+    st = t.stride()
+    if (D > 1 and st[2] != 1) or (H > 1 and st[1] != D):
         raise ValueError(f"{name} must have contiguous rows of heads")
-    return 0 if n == 1 else t.stride(0)
+    return 0 if n == 1 else st[0]
 
 
-def _scale(t: torch.Tensor, H: int, name: str) -> None:
-    _need_contig(t, torch.float32, name)
-    if t.numel() != H:
-        raise ValueError(f"{name} must hold one value for each head")
-
-
-def _pools(k: torch.Tensor, v: torch.Tensor):
-    _need_contig(k, torch.int8, "k_cache")
-    _need_contig(v, torch.int8, "v_cache")
-    if k.dim() != 4 or k.shape != v.shape:
+def _pool_shape(k: torch.Tensor, v: torch.Tensor, dev: int):
+    for t, name in ((k, "the k pool"), (v, "the v pool")):
+        if not (t.dtype is _I8 and t.get_device() == dev and t.is_contiguous()):
+            _wrong(t, _I8, name)
+    sh = k.shape
+    if len(sh) != 4 or sh != v.shape:
         raise ValueError("the k and v pools must both be [num_pages][page_size][Hkv][D]")
-    return k.shape
+    return sh
+
+
+def _pages(block_table: torch.Tensor, B: int, dev: int) -> int:
+    if not (block_table.dtype is _I32 and block_table.get_device() == dev and block_table.is_contiguous()):
+        _wrong(block_table, _I32, "block_table")
+    sh = block_table.shape
+    if len(sh) != 2 or sh[0] != B:
+        raise ValueError("block_table must be [B][max_pages]")
+    return sh[1]
 
 
 def rope_append_gqa_paged(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
@@ -766,43 +786,47 @@ def rope_append_gqa_paged(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.T
     q_start[b] .. q_start[b+1] - 1 are the last tokens of sequence b's kv_lens[b]-token context.
     k_cache, v_cache int8 [num_pages][page_size][Hkv][D].  Returns the query's codes int8
     [n][Hq][D] (zero outside the sequences' rows when allocated here)."""
-    num_pages, page_size, Hkv, D = _pools(k_cache, v_cache)
-    B = _packed(q_start, kv_lens, "kv_lens")
+    _need(k, _BF16, "k")
+    dev = k.get_device()
+    num_pages, page_size, Hkv, D = _pool_shape(k_cache, v_cache, dev)
+    B = _lens(q_start, kv_lens, "kv_lens", dev)
     n = k.shape[0]
-    ks, vs = _packed_rows(k, Hkv, D, n, "k"), _packed_rows(v, Hkv, D, n, "v")
-    _scale(k_scale, Hkv, "k_scale")
-    _scale(v_scale, Hkv, "v_scale")
-    _weight(q_weight, D, "q_weight")
-    _weight(k_weight, D, "k_weight")
-    table_len, rot = _rot_table(cos_sin, D)
-    max_pages = _block_table(block_table, B)
-    _dev_err(dev_err)
-    Hq, qs = 0, 0
+    ks, vs = _packed_rows(k, Hkv, D, n, "k", dev), _packed_rows(v, Hkv, D, n, "v", dev)
+    ksc, vsc = _vector(k_scale, Hkv, _F32, "k_scale", dev), _vector(v_scale, Hkv, _F32, "v_scale", dev)
+    qw, kw = _vector(q_weight, D, _BF16, "q_weight", dev), _vector(k_weight, D, _BF16, "k_weight", dev)
+    table_len, rot, cp = _table(cos_sin, D, dev) if cos_sin is not None else (0, 0, None)
+    max_pages = _pages(block_table, B, dev)
+    ep = _error_word(dev_err, dev)
+    Hq, qs, qsc, qp, qop = 0, 0, None, None, None
     if q is not None:
         if q.dim() != 3:
             raise ValueError("q must be [n][H][D]")
         Hq = q.shape[1]
-        qs = _packed_rows(q, Hq, D, n, "q")
-        _scale(q_scale, Hq, "q_scale")
+        qs, qsc, qp = _packed_rows(q, Hq, D, n, "q", dev), _vector(q_scale, Hq, _F32, "q_scale", dev), q.data_ptr()
     elif q_out is not None or q_weight is not None:
         raise ValueError("q_out and q_weight need q")
-    dev = _on_device(k, q, v, cos_sin, q_scale, k_scale, v_scale, k_cache, v_cache, block_table, q_start, kv_lens,
-                     q_weight, k_weight, q_out, dev_err)
-    with _Here(dev, stream):
+    raw, ctx = _here(dev, stream)
+    if ctx is not None:
+        ctx.__enter__()
+    try:
         if q is not None:
             if q_out is None:
-                q_out = torch.zeros(n, Hq, D, dtype=torch.int8, device=q.device)
-            _need_contig(q_out, torch.int8, "q_out")
-            if q_out.shape != (n, Hq, D):
+                q_out = torch.zeros(n, Hq, D, dtype=_I8, device=q.device)
+            elif not (q_out.dtype is _I8 and q_out.get_device() == dev and q_out.is_contiguous()):
+                _wrong(q_out, _I8, "q_out")
+            elif q_out.shape != (n, Hq, D):
                 raise ValueError("q_out must be [n][Hq][D]")
+            qop = q_out.data_ptr()
         if n:
             st = lib().fa3_rope_append_gqa_paged(
-                _opt(q), k.data_ptr(), v.data_ptr(), _opt(q_weight), _opt(k_weight), eps, _opt(cos_sin), table_len,
-                rot, int(interleaved), _opt(q_scale) if Hq else None, k_scale.data_ptr(), v_scale.data_ptr(),
-                _opt(q_out), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), q_start.data_ptr(),
-                kv_lens.data_ptr(), n, B, Hq, Hkv, D, qs, ks, vs, num_pages, page_size, max_pages, _opt(dev_err),
-                _stream(stream))
-            _check("fa3_rope_append_gqa_paged", st)
+                qp, k.data_ptr(), v.data_ptr(), qw, kw, eps, cp, table_len, rot, interleaved, qsc, ksc, vsc, qop,
+                k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), q_start.data_ptr(),
+                kv_lens.data_ptr(), n, B, Hq, Hkv, D, qs, ks, vs, num_pages, page_size, max_pages, ep, raw)
+            if st:
+                raise FA3Error("fa3_rope_append_gqa_paged", st)
+    finally:
+        if ctx is not None:
+            ctx.__exit__(None, None, None)
     return q_out
 
 
@@ -814,41 +838,49 @@ def _chunk_workspace(nbytes: int, device, stream):
     # A captured call takes its buffer from the graph's own pool: replays of two graphs
     # (or of a graph and eager calls) then never share one.
     if torch.cuda.is_current_stream_capturing():
-        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
     return _workspace("chunk", nbytes, device, stream=stream)
 
 
-def _packed_attn(name: str, q, k, v, q_scale, k_scale, v_scale, q_start, lens, softmax_scale, out, workspace, dev_err,
-                 stream, B, Hkv, extra, table=None):
-    for t, m in ((q, "q"), (k, "k"), (v, "v")):
-        _need_contig(t, torch.int8, m)
-    if q.dim() != 3 or q.shape[2] != k.shape[3]:
+def _packed_attn(name, q, k, v, q_scale, k_scale, v_scale, q_start, lens, B, Hkv, sizes, table, softmax_scale, out,
+                 workspace, dev_err, stream, dev):
+    if not (q.dtype is _I8 and q.get_device() == dev and q.is_contiguous()):
+        _wrong(q, _I8, "q")
+    sh = q.shape
+    D = k.shape[3]
+    if len(sh) != 3 or sh[2] != D:
         raise ValueError("q must be [n][Hq][D] with k's head size")
-    n, Hq, D = q.shape
-    _scale(q_scale, Hq, "q_scale")
-    _scale(k_scale, Hkv, "k_scale")
-    _scale(v_scale, Hkv, "v_scale")
-    _dev_err(dev_err)
-    dev = _on_device(q, k, v, q_scale, k_scale, v_scale, q_start, lens, table, out, workspace, dev_err)
-    with _Here(dev, stream):
+    n, Hq = sh[0], sh[1]
+    qsc = _vector(q_scale, Hq, _F32, "q_scale", dev)
+    ksc, vsc = _vector(k_scale, Hkv, _F32, "k_scale", dev), _vector(v_scale, Hkv, _F32, "v_scale", dev)
+    ep = _error_word(dev_err, dev)
+    raw, ctx = _here(dev, stream)
+    if ctx is not None:
+        ctx.__enter__()
+    try:
         if out is None:
-            out = torch.zeros(n, Hq, D, dtype=torch.bfloat16, device=q.device)
-        _need_contig(out, torch.bfloat16, "out")
-        if out.shape != q.shape:
+            out = torch.zeros(sh, dtype=_BF16, device=q.device)
+        elif not (out.dtype is _BF16 and out.get_device() == dev and out.is_contiguous()):
+            _wrong(out, _BF16, "out")
+        elif out.shape != sh:
             raise ValueError("out must have q's shape")
         if n:
             L = lib()
             if workspace is None:
                 nbytes = L.fa3_chunk_workspace_size(n, B, Hq, Hkv, D)
                 workspace = _chunk_workspace(nbytes, q.device, stream) if nbytes else None
-            ptrs = [q.data_ptr(), k.data_ptr(), v.data_ptr(), q_scale.data_ptr(), k_scale.data_ptr(),
-                    v_scale.data_ptr(), q_start.data_ptr(), lens.data_ptr()]
-            if table is not None:
-                ptrs.append(table.data_ptr())
-            st = getattr(L, name)(*ptrs, out.data_ptr(), n, B, *extra(Hq, Hkv, D), softmax_scale, _opt(workspace),
-                                  0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                  _opt(dev_err), _stream(stream))
-            _check(name, st)
+            elif workspace.get_device() != dev or not workspace.is_contiguous():
+                raise ValueError("workspace must be contiguous and on the tensors' device")
+            wp, wn = (None, 0) if workspace is None else (workspace.data_ptr(),
+                                                          workspace.numel() * workspace.element_size())
+            st = getattr(L, name)(q.data_ptr(), k.data_ptr(), v.data_ptr(), qsc, ksc, vsc, q_start.data_ptr(),
+                                  lens.data_ptr(), *table, out.data_ptr(), n, B, *sizes(Hq), softmax_scale, wp, wn, ep,
+                                  raw)
+            if st:
+                raise FA3Error(name, st)
+    finally:
+        if ctx is not None:
+            ctx.__exit__(None, None, None)
     return out
 
 
@@ -861,12 +893,14 @@ def prefill_attn_gqa_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_
     k/v int8 [num_pages][page_size][Hkv][D] (holding the new tokens already) -> bf16 [n][Hq][D].
 
     Rows outside the sequences are left as they were (zero when ``out`` is allocated here)."""
-    num_pages, page_size, Hkv, _ = _pools(k, v)
-    B = _packed(q_start, kv_lens, "kv_lens")
-    max_pages = _block_table(block_table, B)
-    return _packed_attn("fa3_prefill_attn_gqa_paged", q, k, v, q_scale, k_scale, v_scale, q_start, kv_lens,
-                        softmax_scale, out, workspace, dev_err, stream, B, Hkv,
-                        lambda Hq, Hk, D: (Hq, Hk, D, num_pages, page_size, max_pages), table=block_table)
+    _need(k, _I8, "k")
+    dev = k.get_device()
+    num_pages, page_size, Hkv, D = _pool_shape(k, v, dev)
+    B = _lens(q_start, kv_lens, "kv_lens", dev)
+    max_pages = _pages(block_table, B, dev)
+    return _packed_attn("fa3_prefill_attn_gqa_paged", q, k, v, q_scale, k_scale, v_scale, q_start, kv_lens, B, Hkv,
+                        lambda Hq: (Hq, Hkv, D, num_pages, page_size, max_pages), (block_table.data_ptr(),),
+                        softmax_scale, out, workspace, dev_err, stream, dev)
 
 
 def cross_attn_gqa(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_scale: torch.Tensor, k_scale: torch.Tensor,
@@ -875,9 +909,14 @@ def cross_attn_gqa(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_scale: t
                    dev_err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Attention of q int8 [n][Hq][D] (packed by q_start) to all enc_lens[b] encoder states k/v int8
     [B][T][Hkv][D] of its sequence -> bf16 [n][Hq][D]; zero rows where there is no state."""
-    B = _packed(q_start, enc_lens, "enc_lens")
-    if k.dim() != 4 or k.shape != v.shape or k.shape[0] != B:
+    _need_contig(k, _I8, "k")
+    dev = k.get_device()
+    if not (v.dtype is _I8 and v.get_device() == dev and v.is_contiguous()):
+        _wrong(v, _I8, "v")
+    B = _lens(q_start, enc_lens, "enc_lens", dev)
+    sh = k.shape
+    if len(sh) != 4 or sh != v.shape or sh[0] != B:
         raise ValueError("k and v must both be [B][T][Hkv][D]")
-    T, Hkv = k.shape[1], k.shape[2]
-    return _packed_attn("fa3_cross_attn_gqa", q, k, v, q_scale, k_scale, v_scale, q_start, enc_lens, softmax_scale,
-                        out, workspace, dev_err, stream, B, Hkv, lambda Hq, Hk, D: (T, Hq, Hk, D))
+    T, Hkv, D = sh[1], sh[2], sh[3]
+    return _packed_attn("fa3_cross_attn_gqa", q, k, v, q_scale, k_scale, v_scale, q_start, enc_lens, B, Hkv,
+                        lambda Hq: (T, Hq, Hkv, D), (), softmax_scale, out, workspace, dev_err, stream, dev)
