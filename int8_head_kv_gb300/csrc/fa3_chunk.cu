@@ -22,10 +22,9 @@
 // end.  A cut unit's parts leave unnormalised O, maximum and sum in the workspace, and
 // chunk_combine_kernel merges them, so one long sequence and a ragged batch both fill the GPU.
 //
-// Roles in the CTA (512 threads): warp 0 issues the MMAs; warps 12-15 look keys up in the
-// block table, load int8 K and V tiles one tile ahead into registers and write them as fp16
-// into one of two stages; warps 4-7 and 8-11 (a row a lane) run the softmax of buffers 0
-// and 1.  int8 codes are exact in fp16 and a 128-term sum of their products
+// Roles in the CTA (512 threads): warp 0 issues the MMAs; warp 1 looks pages up in the block
+// table and brings int8 K and V tiles to shared memory by TMA; warps 12-15 write them as fp16
+// into one of two stages; warps 4-7 and 8-11 (a row a lane) run the softmax of buffers 0 and 1.  int8 codes are exact in fp16 and a 128-term sum of their products
 // stays below 2^24, so kind::f16 MMAs with fp32 accumulation give the exact integer
 // score (sm_103a has no integer tcgen05 kind).  P (fp16, relative to a lazily moved row
 // maximum) is written over its scores in TMEM and is the A operand of P.V; the row sum is
@@ -49,10 +48,10 @@ namespace {
 constexpr int kD = 128;            // head dim
 constexpr int kKeys = 128;         // keys per tile
 constexpr int kRows = 128;         // rows (TMEM lanes) per row tile
-constexpr int kThreadsC = 512;     // warp 0: MMA; 4-7 / 8-11: softmax of buffer 0 / 1; 12-15: converters
+constexpr int kThreadsC = 512;     // warp 0: MMA; 1: TMA; 4-7 / 8-11: softmax of buffer 0 / 1; 12-15: converters
 // Registers a thread of each warpgroup (launched with 128 each, 512 in all).  Nothing in the loops may spill: local
 // memory goes to L2, since shared memory leaves no L1 to speak of.
-constexpr int kRegsIssue = 72, kRegsSoftmax = 152, kRegsConvert = 136;
+constexpr int kRegsIssue = 112, kRegsSoftmax = 152, kRegsConvert = 96;
 static_assert(kRegsIssue + 2 * kRegsSoftmax + kRegsConvert <= 512, "register file");
 constexpr uint32_t TM_O = 0, TM_S = 256;                   // O_x [128x, +128), S_x [256 + 128x, +128)
 constexpr uint32_t KV_TILE = kKeys * kD * 2;               // 32 KB of fp16
@@ -61,9 +60,13 @@ constexpr uint32_t Q_TILE = kRows * kD * 2;                // 32 KB of fp16
 constexpr uint32_t OFF_Q = 0;                              // 2 x fp16 query rows, K-major
 constexpr uint32_t OFF_K = OFF_Q + 2 * Q_TILE;             // 2 stages
 constexpr uint32_t OFF_V = OFF_K + 2 * KV_TILE;            // 2 stages
-constexpr uint32_t OFF_ML = OFF_V + 2 * KV_TILE;           // [2][128] float2: (m, l) of a single row tile's halves
-constexpr uint32_t OFF_WALK = OFF_ML + 2 * kRows * 8;      // a Walk a warp
-constexpr uint32_t OFF_BAR = OFF_WALK + 16 * 128;
+constexpr uint32_t OFF_RAW = OFF_V + 2 * KV_TILE;          // int8 K and V tile on their way: 128 keys x 128 B each
+constexpr uint32_t RAW_TILE = kKeys * kD;
+constexpr uint32_t OFF_ML = OFF_Q + Q_TILE;                // [2][128] float2: (m, l) of a single row tile's halves,
+                                                           // in the second row tile's place
+constexpr uint32_t kWalkBytes = 96;
+constexpr uint32_t OFF_WALK = OFF_RAW + 2 * RAW_TILE;      // a Walk a warp
+constexpr uint32_t OFF_BAR = OFF_WALK + 16 * kWalkBytes;
 enum {
   B_K_FULL = 0, B_K_EMPTY = 2, B_V_FULL = 4, B_V_EMPTY = 6,
   B_S_FULL = 8,                    // [2]: buffer x's scores of its next step
@@ -71,7 +74,9 @@ enum {
   B_PV_DONE = 12,                  // [2]: P_x.V done (O_x holds it; S_x free)
   B_ML = 14,                       // [2]: buffer x's (m, l) of a single row tile written
   B_READ = 16,                     // [2]: warps of buffer x have read both O of a single row tile
-  B_Q_READY = 18, B_DRAIN, B_N
+  B_RAW_FULL = 18,                 // [2]: int8 K, V tile arrived
+  B_RAW_EMPTY = 20,                // [2]: int8 K, V tile taken into registers
+  B_Q_READY = 22, B_DRAIN, B_N
 };
 constexpr uint32_t OFF_TSLOT = OFF_BAR + 8 * B_N;
 constexpr uint32_t OFF_ABORT = OFF_TSLOT + 4;
@@ -101,7 +106,15 @@ struct ChunkParams {
   int page_size, max_pages, num_pages;
   DivU32 div_ps;                // / page_size
   float sm_log2;                // softmax_scale * log2(e)
+  int box;                      // rows of a TMA box; 0: pages too ragged for boxes, loads through registers
+  CUtensorMap map_k, map_v;     // [cache rows][Hkv * 128] in boxes of [box][128]
 };
+
+// Keys come in boxes of consecutive cache rows, the largest power of two that divides the page size
+// (and the tile), from 8 rows on.  A box of 8 rows or more keeps the TMA unit fast enough (one row a copy took 31
+// cycles a row, 126 us for the 16 x 4096-key decode against 67 through registers); smaller powers go through
+// registers.
+constexpr int kLeastBox = 8;
 
 // ------------------------------------------------------------------ the line of steps
 struct Seq {
@@ -252,8 +265,8 @@ struct Walk {
   int64_t left;
   Part u;
 };
-static_assert(sizeof(Walk) <= 128, "walk area");
-__device__ __forceinline__ void walk_begin(const ChunkParams& p, Walk* at, int64_t total, int parts, int cta, int lane) {
+static_assert(sizeof(Walk) <= kWalkBytes, "walk area");
+__device__ __noinline__ void walk_begin(const ChunkParams& p, Walk* at, int64_t total, int parts, int cta, int lane) {
   const int64_t x = part_begin(total, parts, cta);
   const int64_t left = part_begin(total, parts, cta + 1) - x;
   Cursor c = {p.B, 0, 0, {0, 0, 0}, 0};
@@ -265,7 +278,7 @@ __device__ __forceinline__ void walk_begin(const ChunkParams& p, Walk* at, int64
   __syncwarp();
 }
 // Moves to the next part, at->u; false: there is none.
-__device__ __forceinline__ bool walk_next(const ChunkParams& p, Walk* at, int lane) {
+__device__ __noinline__ bool walk_next(const ChunkParams& p, Walk* at, int lane) {
   Cursor c = at->c;
   int64_t left = at->left;
   Part u = {};
@@ -299,41 +312,31 @@ __device__ __forceinline__ bool walk_next(const ChunkParams& p, Walk* at, int la
   return got;
 }
 
-// wait_bar for waits that last: the test suspends the thread by itself for a while, and the clock and the
-// abort flag are looked at now and then only.
-__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, int32_t* err) {
-  const uint64_t t0 = global_ns();
-  for (;;) {
+// wait_bar for short waits.  Reading the global timer takes longer than most of them last, so the limit is a
+// number of tests (2^25, about a second: a test suspends the thread for a while by itself), and the abort flag is
+// looked at every 256.
+constexpr uint32_t kMostTests = 1u << 25;
+__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, int32_t* err) {
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if (global_ns() - t0 > kWaitNs) break;
+  for (uint32_t i = 0; i < kMostTests; ++i) {
+    if (mbar_try(bar, parity)) return true;
+    if ((i & 255u) == 255u && *abort_flag) return false;
   }
   *abort_flag = 1u;
   set_dev_err(err, FA3_DEVERR_TIMEOUT);
   return false;
 }
-__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, int32_t* err) {
-  return mbar_try(bar, parity) || wait_on(bar, parity, abort_flag, err);
-}
-
-// One lane of the warp waits for all: a test by 32 lanes takes the shared-memory pipe 32 times as long,
-// and the waiting warps' tests would crowd out the loads and stores of the working ones.
+// The same for a warp, whose lanes have to agree.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int lane, volatile uint32_t* abort_flag,
                                           int32_t* err) {
-  bool ok = true;
-  if (lane == 0) ok = wait_long(bar, parity, abort_flag, err);
-  return __shfl_sync(0xffffffffu, ok, 0);
+  return warp_all(wait_long(bar, parity, abort_flag, err));
 }
 
 // The wait for this thread's TMEM loads, which also orders the uses of v behind it.
-__device__ __forceinline__ void wait_ld32(uint32_t* v) {
+__device__ __forceinline__ void wait_ld16(uint32_t* v) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
-                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
-                 "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
-                 "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
                :: "memory");
 }
 
@@ -345,6 +348,20 @@ __device__ __forceinline__ uint4 load_once(const int8_t* p) {
   return v;
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* tm, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
+}
 __device__ __forceinline__ void prefetch_line(const int8_t* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 template <int N>
 __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -399,7 +416,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
   const int64_t total = total_cost(p, lane, blockIdx.x == 0 && warp == 0);
   const int parts = parts_of(p, total);
   if ((int)blockIdx.x >= parts || total == 0) return;
-  Walk* walk = reinterpret_cast<Walk*>(smem + OFF_WALK) + warp;
+  Walk* walk = reinterpret_cast<Walk*>(smem + OFF_WALK + warp * kWalkBytes);
   walk_begin(p, walk, total, parts, blockIdx.x, lane);
 
   if (tid == 0) {
@@ -413,6 +430,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
       mbar_init(bar(B_PV_DONE + s), 1);
       mbar_init(bar(B_ML + s), 4);
       mbar_init(bar(B_READ + s), 4);
+      mbar_init(bar(B_RAW_FULL + s), 1);
+      mbar_init(bar(B_RAW_EMPTY + s), 4);
     }
     mbar_init(bar(B_Q_READY), 8);
     mbar_init(bar(B_DRAIN), 1);
@@ -429,13 +448,6 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TSLOT);
 
-  if (warp < 4) {
-    reg_dec<kRegsIssue>();
-  } else if (warp < 12) {
-    reg_inc<kRegsSoftmax>();
-  } else {
-    reg_inc<kRegsConvert>();
-  }
   if (warp == 0) {
     // ------------------------------------------------------------ MMA issuer
     const uint32_t id_qk = idesc_f16(kRows, kKeys, false, false);
@@ -447,54 +459,55 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
       struct { int t0, t1, nt; bool dual; } u = {walk->u.t0, walk->u.t1, walk->u.nt, walk->u.dual};
       if (u.nt == 0) continue;
       const int nk = u.t1 - u.t0, steps = u.dual ? 2 * nk : nk;
-      {
-        ok = warp_all(wait_long(bar(B_Q_READY), units & 1u, abort_flag, p.err));
-        // S_x = Q.K^T: the row tile's K-major A operand in shared memory (8-row core groups 128 B
-        // apart, 8-wide d groups 2048 B apart), K the K-major B operand (128-byte swizzle: 8-key groups
-        // 1024 B apart, 16 values of d 32 B apart within a half).  S_x holds the P of the buffer's step
-        // before until its P.V is done (d: the buffer's steps before this one, any: in this unit).
-        auto issue_qk = [&](const int x, uint32_t kt, uint32_t d, bool any) -> bool {
-          const uint32_t s = kt & 1u;
-          if (!warp_all(wait_long(bar(B_K_FULL) + 8u * s, (kt >> 1) & 1u, abort_flag, p.err))) return false;
-          if (any && !warp_all(wait_long(bar(B_PV_DONE + x), (d - 1u) & 1u, abort_flag, p.err))) return false;
-          tc_fence_after();
-          const uint32_t a = desc_lo(sbase + OFF_Q + (u.dual ? x : 0) * Q_TILE, 2048);
-          const uint32_t bd = desc_lo(sbase + OFF_K + s * KV_TILE, 16);
-#pragma unroll
-          for (int kk = 0; kk < kD / 16; ++kk)
-            mma_ss<desc_hi(128, false), desc_hi(1024, true)>(
-                lead, tmem + TM_S + x * 128, a + kk * (4096 >> 4), bd + (kk / 4) * (KV_HALF >> 4) + (kk % 4) * (32 >> 4), id_qk,
-                kk > 0 ? 1u : 0u);
-          commit_if(lead, bar(B_S_FULL + x));
-          if (!u.dual || x == 1) commit_if(lead, bar(B_K_EMPTY) + 8u * s);    // all steps of this key tile have it
-          return true;
-        };
-        // O_x += P_x.V: P_x (fp16, over S_x: column k holds keys 2k, 2k + 1) is the A operand in
-        // TMEM, V the MN-major B operand (128-byte swizzle: 8-key groups 1024 B apart, halves of d 16 KB).
-        auto issue_pv = [&](const int x, uint32_t kt, uint32_t d, bool any) -> bool {
-          const uint32_t s = kt & 1u;
-          if (!warp_all(wait_long(bar(B_V_FULL) + 8u * s, (kt >> 1) & 1u, abort_flag, p.err))) return false;
-          if (!warp_all(wait_long(bar(B_P_FULL + x), d & 1u, abort_flag, p.err))) return false;
-          tc_fence_after();
-          const uint32_t bd = desc_lo(sbase + OFF_V + s * KV_TILE, KV_HALF);
-#pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma_ts<desc_hi(1024, true)>(lead, tmem + TM_O + x * 128, tmem + TM_S + x * 128 + kk * 8, bd + kk * (2048 >> 4), id_pv,
-                                        any || kk > 0 ? 1u : 0u);
-          commit_if(lead, bar(B_PV_DONE + x));
-          if (!u.dual || x == 1) commit_if(lead, bar(B_V_EMPTY) + 8u * s);
-          return true;
-        };
-        // Steps t and t + 1 of buffers 0 and 1: P.V of step t, then Q.K^T of step t + 2.
-        const uint32_t per = u.dual ? 1u : 2u, odd = u.dual ? 0u : 1u;   // key tiles a pair of steps, of its second
-        uint32_t kt = kc - per, i = 0xffffffffu;                         // the pair's first key tile, its number
+      ok = warp_all(wait_long(bar(B_Q_READY), units & 1u, abort_flag, p.err));
+      // Step t: buffer t & 1, key tile t (or t / 2 with two row tiles).  P.V of step t, then Q.K^T of step t + 2.
+      // All roles' loops are kept rolled: together they have to stay in the SM's instruction cache, and an MMA lasts
+      // longer than an iteration.
+      const uint32_t per = u.dual ? 1u : 0u;
 #pragma unroll 1
-        for (int t = -2; t < steps && ok; t += 2, kt += per, ++i) {
-          const bool any = (int32_t)i > 0;
-          if (t >= 0) ok = issue_pv(0, kt, done0 + i, any);
-          if (ok && t + 2 < steps) ok = issue_qk(0, kt + per, done0 + i + 1u, t >= 0);
-          if (ok && t >= 0 && t + 1 < steps) ok = issue_pv(1, kt + odd, done1 + i, any);
-          if (ok && t + 3 < steps) ok = issue_qk(1, kt + per + odd, done1 + i + 1u, t >= 0);
+      for (int t = -2; t < steps && ok; ++t) {
+        const uint32_t x = (uint32_t)t & 1u;
+        if (t >= 0) {
+          // O_x += P_x.V: P_x (fp16, over S_x: column k holds keys 2k, 2k + 1) is the A operand in
+          // TMEM, V the MN-major B operand (128-byte swizzle: 8-key groups 1024 B apart, halves of d 16 KB).
+          const uint32_t kt = kc + ((uint32_t)t >> per), s = kt & 1u, d = (x ? done1 : done0) + ((uint32_t)t >> 1);
+          ok = warp_all(wait_long(bar(B_V_FULL) + 8u * s, (kt >> 1) & 1u, abort_flag, p.err)) &&
+               warp_all(wait_long(bar(B_P_FULL) + 8u * x, d & 1u, abort_flag, p.err));
+          if (!ok) break;
+          tc_fence_after();
+          uint32_t bd = desc_lo(sbase + OFF_V + s * KV_TILE, KV_HALF), ap = tmem + TM_S + x * 128;
+          uint32_t acc = t >= 2 ? 1u : 0u;
+#pragma unroll 1
+          for (int kk = 0; kk < kKeys / 16; ++kk) {
+            mma_ts<desc_hi(1024, true)>(lead, tmem + TM_O + x * 128, ap, bd, id_pv, acc);
+            bd += 2048 >> 4;
+            ap += 8;
+            acc = 1u;
+          }
+          commit_if(lead, bar(B_PV_DONE) + 8u * x);
+          if (!u.dual || x) commit_if(lead, bar(B_V_EMPTY) + 8u * s);
+        }
+        if (t + 2 < steps) {
+          // S_x = Q.K^T: the row tile's K-major A operand in shared memory (8-row core groups 128 B
+          // apart, 8-wide d groups 2048 B apart), K the K-major B operand (128-byte swizzle: 8-key groups
+          // 1024 B apart, 16 values of d 32 B apart within a half).  S_x holds the P of step t until its P.V is done.
+          const uint32_t t2 = (uint32_t)(t + 2), kt = kc + (t2 >> per), s = kt & 1u;
+          ok = warp_all(wait_long(bar(B_K_FULL) + 8u * s, (kt >> 1) & 1u, abort_flag, p.err));
+          if (ok && t >= 0)
+            ok = warp_all(wait_long(bar(B_PV_DONE) + 8u * x, ((x ? done1 : done0) + ((uint32_t)t >> 1)) & 1u, abort_flag, p.err));
+          if (!ok) break;
+          tc_fence_after();
+          uint32_t a = desc_lo(sbase + OFF_Q + (u.dual ? x : 0u) * Q_TILE, 2048), bd = desc_lo(sbase + OFF_K + s * KV_TILE, 16);
+          uint32_t acc = 0u;
+#pragma unroll 1
+          for (int kk = 0; kk < kD / 16; ++kk) {
+            mma_ss<desc_hi(128, false), desc_hi(1024, true)>(lead, tmem + TM_S + x * 128, a, bd, id_qk, acc);
+            a += 4096 >> 4;
+            bd += kk == 3 ? (KV_HALF >> 4) - 3 * (32 >> 4) : 32 >> 4;
+            acc = 1u;
+          }
+          commit_if(lead, bar(B_S_FULL) + 8u * x);
+          if (!u.dual || x) commit_if(lead, bar(B_K_EMPTY) + 8u * s);    // all steps of this key tile have it
         }
       }
       kc += (uint32_t)nk;
@@ -505,24 +518,80 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
     // Drain: every MMA issued has completed before TMEM is freed.
     commit_if(lead, bar(B_DRAIN));
     wait_long(bar(B_DRAIN), 0, abort_flag, p.err);
+  } else if (warp == 1) {
+    // ------------------------------------------------------ TMA: int8 tiles of K and V
+    // Lanes 0 .. 15 have a box of K each, lanes 16 .. 31 of V (fewer boxes: fewer lanes).  A lane looks up the
+    // page of its box's first key one tile ahead.  Boxes past the end are the last box again.
+    if (p.box) {
+      const int kv = lane >> 4, boxes = kKeys / p.box, i = lane & 15;
+      const bool mine = i < boxes;
+      int j = 0, t_end = 0, n_keys = 0, b = 0, g = 0;        // the tile to look up next
+      int pg = 0, at = 0, g_at = 0;                          // the tile looked up
+      auto look_up = [&]() {                                 // false: nothing left
+        while (j >= t_end) {
+          if (!walk_next(p, walk, lane)) return false;
+          const Part& u = walk->u;
+          j = u.t0;
+          t_end = u.t1;
+          b = u.b;
+          g = u.g;
+          n_keys = p.causal ? u.nkv - u.nq + min(u.nq, (u.rb + 1) * 2 * p.P) : u.nkv;
+        }
+        const uint32_t t = (uint32_t)min(j * kKeys + i * p.box, (n_keys - 1) & ~(p.box - 1));
+        if (p.block_table) {
+          const uint32_t pi = divu32(t, p.div_ps);
+          pg = mine ? __ldg(p.block_table + (int64_t)b * p.max_pages + pi) : 0;
+          at = (int)(t - pi * (uint32_t)p.page_size);
+        } else {
+          at = b * p.T + (int)t;
+        }
+        g_at = g;
+        ++j;
+        return true;
+      };
+      const CUtensorMap* map = kv ? &p.map_v : &p.map_k;
+      const uint32_t dst = sbase + OFF_RAW + kv * RAW_TILE + (uint32_t)(i * p.box) * kD;
+      bool more = look_up(), ok = true;
+      uint32_t kc = 0;
+      for (; more && ok; ++kc) {
+        if ((uint32_t)pg >= (uint32_t)p.num_pages && p.block_table) {   // outside the pool: any page of it
+          set_dev_err(p.err, FA3_DEVERR_PAGE);
+          pg = 0;
+        }
+        const int row = at + (p.block_table ? pg * p.page_size : 0), col = g_at * kD;
+        more = look_up();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          ok = ok && warp_wait(bar(B_RAW_EMPTY + h), (kc & 1u) ^ 1u, lane, abort_flag, p.err);
+          if (!ok) break;
+          if (lane == 0) mbar_expect_tx(bar(B_RAW_FULL + h), RAW_TILE);
+          __syncwarp();
+          if (kv == h && mine) tma_2d(dst, map, col, row, bar(B_RAW_FULL + h));
+        }
+      }
+      // What was sent off lands before the block ends, also after a time-out elsewhere (a bounded wait; of the
+      // last tile K alone may be on its way, then V's last is the one before).
+      if (lane < 2 && kc > 0) {
+        const uint64_t t0 = global_ns();
+        for (uint32_t back = 1; back <= (ok ? 1u : 2u) && back <= kc; ++back)
+          while (!mbar_try(bar(B_RAW_FULL + lane), (kc - back) & 1u) && global_ns() - t0 < kWaitNs / 50) {}
+      }
+    }
   } else if (warp >= 12) {
     // ------------------------------------------------------ int8 -> fp16 converters
-    // A warp has 32 keys of a tile.  A load takes four whole rows of 128 bytes, so that every line is
-    // asked for once: lane l has bytes 16 (l % 8) .. of row l / 8, and lanes l % 8 >= 4 that of the row's
-    // neighbour (l / 8) ^ 1.  The two 16-byte fp16 chunks a lane gets go to chunks 2c and 2c + 1 of the key's
-    // swizzled row; the neighbour's row has the other parity, so the eight lanes of a store hit different
-    // banks.  A lane looks one key up in the block table, the others get its row by shuffles.  Keys past the
-    // end are the last key again: their weights are zero.  The next tile's loads go out as soon as this one's
-    // registers are written.
+    // A warp has 32 keys of a tile, a lane 16 bytes of eight of them: bytes 16 (l % 8) .. of row l / 8, lanes
+    // l % 8 >= 4 of the row's neighbour (l / 8) ^ 1.  The two 16-byte fp16 chunks they become go to chunks 2c and
+    // 2c + 1 of the key's swizzled row; the neighbour's row has the other parity, so the eight lanes of a
+    // store hit different banks.  Without boxes the bytes come from the cache itself: a lane looks one key up, the
+    // others get its row by shuffles, and the rows of the next tile are asked of HBM into L2 a tile ahead.
     const int cw = warp - 12, cl = lane & 7, rl = (lane >> 3) ^ (cl >> 2);
+    const uint32_t src0 = sbase + OFF_RAW + (uint32_t)(32 * cw + rl) * kD + cl * 16;
+    // chunk 2 cl (and 2 cl + 1) of key n: half cl / 4, row n, chunk ((2 cl) % 8) ^ (n % 8)
+    const uint32_t dst0 = sbase + (uint32_t)(cl >> 2) * KV_HALF + (uint32_t)(32 * cw + rl) * 128;
+    const uint32_t at0 = ((uint32_t)(2 * cl & 7) ^ (uint32_t)rl) * 16;   // n % 8 = rl, or rl + 4 for odd i
     const int row_stride = p.Hkv * kD;
-    // Two tiles ahead of the one being written: its keys' block-table entries are on their way (pg); one tile
-    // ahead: its rows are known, asked of HBM into L2 and then loaded.
-    bool more = true, ahead = true;
-    int j = 0, t_end = 0, n_keys = 0, b = 0;                 // the tile after the one looked up, of sequence b
-    int g = 0, pg = 0, in_page = 0;                          // the tile looked up: KV head, entry and row in the page
-    int64_t head = 0;                                        // the tile to load: offset of this lane's bytes in a row
-    int row[8];                                              // and the cache rows of the lane's eight loads
+    int j = 0, t_end = 0, n_keys = 0, b = 0, g = 0;          // the tile to look up next
+    int mine = 0, head = 0, head_next = 0;                   // the tile looked up: this lane's row, offset of the KV head
     auto look_up = [&]() {                                   // false: nothing left
       while (j >= t_end) {
         if (!walk_next(p, walk, lane)) return false;
@@ -533,76 +602,68 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
         g = u.g;
         n_keys = p.causal ? u.nkv - u.nq + min(u.nq, (u.rb + 1) * 2 * p.P) : u.nkv;
       }
-      const uint32_t t = (uint32_t)min(j * kKeys + 32 * cw + lane, n_keys - 1);
-      if (p.block_table) {
-        const uint32_t pi = divu32(t, p.div_ps);
-        pg = __ldg(p.block_table + (int64_t)b * p.max_pages + pi);
-        in_page = (int)(t - pi * (uint32_t)p.page_size);
-      } else {
-        in_page = b * p.T + (int)t;
+      if (!p.box) {
+        const uint32_t t = (uint32_t)min(j * kKeys + 32 * cw + lane, n_keys - 1), pi = divu32(t, p.div_ps);
+        int pg = __ldg(p.block_table + (int64_t)b * p.max_pages + pi);
+        if ((uint32_t)pg >= (uint32_t)p.num_pages) {         // outside the pool: any page of it
+          set_dev_err(p.err, FA3_DEVERR_PAGE);
+          pg = 0;
+        }
+        mine = pg * p.page_size + (int)(t - pi * (uint32_t)p.page_size);
+        head_next = g * kD;
+        prefetch_line(p.k + (int64_t)mine * row_stride + head_next);
+        prefetch_line(p.v + (int64_t)mine * row_stride + head_next);
       }
       ++j;
       return true;
     };
-    auto next_tile = [&]() {                                 // false: nothing left
-      if (!ahead) return false;
-      int mine = in_page;
-      if (p.block_table) {
-        if ((uint32_t)pg >= (uint32_t)p.num_pages) {         // outside the pool: any row of it
-          set_dev_err(p.err, FA3_DEVERR_PAGE);
-          pg = 0;
-        }
-        mine += pg * p.page_size;
-      }
-      head = g * kD + cl * 16;
-      prefetch_line(p.k + (int64_t)mine * row_stride + g * kD);
-      prefetch_line(p.v + (int64_t)mine * row_stride + g * kD);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) row[i] = __shfl_sync(0xffffffffu, mine, 4 * i + rl);
-      ahead = look_up();
-      return true;
-    };
-    uint4 kr[8], vr[8];
-    auto load = [&](const int8_t* base, uint4 (&r)[8]) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) r[i] = load_once(base + (int64_t)row[i] * row_stride);
-    };
-    // chunk 2 cl (and 2 cl + 1) of key n: half cl / 4, row n, chunk ((2 cl) % 8) ^ (n % 8)
-    const uint32_t dst0 = sbase + (uint32_t)(cl >> 2) * KV_HALF + (uint32_t)(32 * cw + rl) * 128;
-    const uint32_t at0 = ((uint32_t)(2 * cl & 7) ^ (uint32_t)rl) * 16;   // n % 8 = rl, or rl + 4 for odd i
-    auto store = [&](uint32_t tile, const uint4 (&r)[8]) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint4 o0, o1;
-        i8x4_to_f16x4(r[i].x, o0.x, o0.y);
-        i8x4_to_f16x4(r[i].y, o0.z, o0.w);
-        i8x4_to_f16x4(r[i].z, o1.x, o1.y);
-        i8x4_to_f16x4(r[i].w, o1.z, o1.w);
-        const uint32_t at = at0 ^ ((i & 1) ? 64u : 0u);
-        sts128(tile + dst0 + 4 * i * 128 + at, o0);
-        sts128(tile + dst0 + 4 * i * 128 + (at ^ 16u), o1);
-      }
-      fence_proxy_async();
-    };
-    ahead = look_up();
-    more = next_tile();
-    if (more) {
-      load(p.k + head, kr);
-      load(p.v + head, vr);
-    }
-    for (uint32_t kc = 0; more; ++kc) {
+    bool more = look_up(), ok = true;
+    for (uint32_t kc = 0; more && ok; ++kc) {
       const uint32_t s = kc & 1u, par = ((kc >> 1) & 1u) ^ 1u;
-      if (!warp_wait(bar(B_K_EMPTY + s), par, lane, abort_flag, p.err)) break;
-      store(OFF_K + s * KV_TILE, kr);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_K_FULL + s));
-      more = next_tile();
-      if (more) load(p.k + head, kr);
-      if (!warp_wait(bar(B_V_EMPTY + s), par, lane, abort_flag, p.err)) break;
-      store(OFF_V + s * KV_TILE, vr);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_V_FULL + s));
-      if (more) load(p.v + head, vr);
+      const int rows = mine;                                 // of this tile
+      head = head_next;
+      more = look_up();
+#pragma unroll 1
+      for (uint32_t kv = 0; kv < 2 && ok; ++kv) {
+        const uint32_t dst = dst0 + OFF_K + (OFF_V - OFF_K) * kv + s * KV_TILE;
+        auto write = [&](const uint4& r, int i) {
+          uint4 o0, o1;
+          i8x4_to_f16x4(r.x, o0.x, o0.y);
+          i8x4_to_f16x4(r.y, o0.z, o0.w);
+          i8x4_to_f16x4(r.z, o1.x, o1.y);
+          i8x4_to_f16x4(r.w, o1.z, o1.w);
+          const uint32_t at = at0 ^ ((uint32_t)(i & 1) << 6);
+          sts128(dst + 4 * i * 128 + at, o0);
+          sts128(dst + 4 * i * 128 + (at ^ 16u), o1);
+        };
+        if (p.box) {
+          ok = warp_wait(bar(B_RAW_FULL) + 8u * kv, kc & 1u, lane, abort_flag, p.err) &&
+               warp_wait(bar(B_K_EMPTY) + 8u * (s + (B_V_EMPTY - B_K_EMPTY) * kv), par, lane, abort_flag, p.err);
+          if (!ok) break;
+          const uint32_t src = src0 + kv * RAW_TILE;
+#pragma unroll 1
+          for (int i = 0; i < 8; i += 2) {
+            const uint4 r0 = lds128(src + 4 * i * kD), r1 = lds128(src + 4 * i * kD + 4 * kD);
+            write(r0, i);
+            write(r1, i + 1);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_RAW_EMPTY) + 8u * kv);
+        } else {
+          uint4 r[8];
+          const int8_t* base = (kv ? p.v : p.k) + head + cl * 16;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            r[i] = load_once(base + (int64_t)__shfl_sync(0xffffffffu, rows, 4 * i + rl) * row_stride);
+          ok = warp_wait(bar(B_K_EMPTY) + 8u * (s + (B_V_EMPTY - B_K_EMPTY) * kv), par, lane, abort_flag, p.err);
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) write(r[i], i);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_K_FULL) + 8u * (s + (B_V_FULL - B_K_FULL) * kv));
+      }
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ softmax warps
@@ -682,27 +743,25 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
             }
             tmem_wait_st();
           }
-          // The row's maximum of the integer scores.  The loops over the columns stay rolled: the roles'
-          // code has to fit the instruction cache together.
-          uint32_t v0[32], v1[32];
+          // the row's maximum of the integer scores
+          uint32_t v0[16], v1[16];
           float mx = -CUDART_INF_F, mx1 = -CUDART_INF_F;
-          FA3_TMEM_LD32(scol, v0);
+          auto maxima = [&](const uint32_t (&w)[16]) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              mx = max3(mx, __uint_as_float(w[e]), __uint_as_float(w[e + 1]));
+              mx1 = max3(mx1, __uint_as_float(w[e + 2]), __uint_as_float(w[e + 3]));
+            }
+          };
+          FA3_TMEM_LD16(scol, v0);
 #pragma unroll 1
-          for (int c2 = 0; c2 < 2; ++c2) {
-            wait_ld32(v0);
-            FA3_TMEM_LD32(scol + c2 * 64 + 32, v1);
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              mx = max3(mx, __uint_as_float(v0[e]), __uint_as_float(v0[e + 1]));
-              mx1 = max3(mx1, __uint_as_float(v0[e + 2]), __uint_as_float(v0[e + 3]));
-            }
-            wait_ld32(v1);
-            FA3_TMEM_LD32(scol + (c2 ? 0 : 64), v0);           // the next half, then the first again
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              mx = max3(mx, __uint_as_float(v1[e]), __uint_as_float(v1[e + 1]));
-              mx1 = max3(mx1, __uint_as_float(v1[e + 2]), __uint_as_float(v1[e + 3]));
-            }
+          for (uint32_t k = 0; k < 128; k += 32) {
+            wait_ld16(v0);
+            FA3_TMEM_LD16(scol + k + 16, v1);
+            maxima(v0);
+            wait_ld16(v1);
+            FA3_TMEM_LD16(scol + ((k + 32) & 127), v0);        // the next, and the first again at the end
+            maxima(v1);
           }
           mx = fmaxf(mx, mx1);
           mx *= c;
@@ -735,10 +794,10 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
           // P = exp2(s c - m) as fp16 pairs over the S columns (keys 32 c4 .. 32 c4 + 31 go to columns
           // 16 c4 .. 16 c4 + 15); the row sum takes the weights before the rounding.
           float l0 = 0.f, l1 = 0.f;
-          auto weigh = [&](const uint32_t (&w)[32], uint32_t col) {
-            uint32_t pk[16];
+          auto weigh = [&](const uint32_t (&w)[16], uint32_t col) {
+            uint32_t pk[8];
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
+            for (int e = 0; e < 16; e += 2) {
               float p0, p1;
               fma2(p0, p1, __uint_as_float(w[e]), __uint_as_float(w[e + 1]), c, c, mc, mc);
               p0 = ex2_approx(p0);
@@ -746,16 +805,16 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
               add2(l0, l1, l0, l1, p0, p1);
               pk[e / 2] = pack_f16x2(p0, p1);
             }
-            FA3_TMEM_ST16(col, pk);
+            tmem_st8(col, pk);
           };
 #pragma unroll 1
-          for (int c2 = 0; c2 < 2; ++c2) {
-            wait_ld32(v0);
-            FA3_TMEM_LD32(scol + c2 * 64 + 32, v1);
-            weigh(v0, scol + c2 * 32);
-            wait_ld32(v1);
-            if (c2 == 0) FA3_TMEM_LD32(scol + 64, v0);
-            weigh(v1, scol + c2 * 32 + 16);
+          for (uint32_t k = 0; k < 128; k += 32) {
+            wait_ld16(v0);
+            FA3_TMEM_LD16(scol + k + 16, v1);
+            weigh(v0, scol + k / 2);
+            wait_ld16(v1);
+            if (k < 96) FA3_TMEM_LD16(scol + k + 32, v0);
+            weigh(v1, scol + k / 2 + 8);
           }
           l_run += l0 + l1;
           tmem_wait_st();
@@ -943,6 +1002,17 @@ FA3_API size_t fa3_chunk_workspace_size(int n, int B, int Hq, int Hkv, int D) {
 }
 
 namespace {
+// The cache as [rows][Hkv * 128] bytes in boxes of box rows of one KV head.
+bool cache_map(CUtensorMap* map, const int8_t* base, int Hkv, int64_t rows, int box) {
+  const auto encode = tensor_map_encoder();
+  if (!encode) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)Hkv * kD, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)Hkv * kD};
+  const cuuint32_t boxes[2] = {kD, (cuuint32_t)box}, step[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(base), dims, strides, boxes, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int chunk_attn(ChunkParams& p, int D, float softmax_scale, void* workspace, size_t workspace_bytes, void* stream) {
   if (!p.q || !p.k || !p.v || !p.q_scale || !p.k_scale || !p.v_scale || !p.q_start || !p.kv_lens || !p.out)
     return FA3_EINVAL;
@@ -963,6 +1033,11 @@ int chunk_attn(ChunkParams& p, int D, float softmax_scale, void* workspace, size
   p.part_o = static_cast<float4*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)2 * sms * (kD / 4) * p.rows_max);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int64_t cache_rows = p.block_table ? (int64_t)p.num_pages * p.page_size : (int64_t)p.B * p.T;
+  p.box = p.block_table ? std::min(kKeys, p.page_size & -p.page_size) : kKeys;
+  if (p.box < kLeastBox) p.box = 0;
+  if (p.box && (!cache_map(&p.map_k, p.k, p.Hkv, cache_rows, p.box) || !cache_map(&p.map_v, p.v, p.Hkv, cache_rows, p.box)))
+    return FA3_ECUDA;
   static std::atomic<bool> set[64];                          // the kernel's attribute, once a device
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return FA3_ECUDA;
