@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
           // O_x += P_x.V: P_x (fp16, over S_x: column k holds keys 2k, 2k + 1) is the A operand in
           // TMEM, V the MN-major B operand (128-byte swizzle: 8-key groups 1024 B apart, halves of d 16 KB).
           const uint32_t kt = kc + ((uint32_t)t >> per), s = kt & 1u, d = (x ? done1 : done0) + ((uint32_t)t >> 1);
-          ok = warp_all(wait_long(bar(B_V_FULL) + 8u * s, (kt >> 1) & 1u, abort_flag, p.err)) &&
+          ok = ((u.dual && x) || warp_all(wait_long(bar(B_V_FULL) + 8u * s, (kt >> 1) & 1u, abort_flag, p.err))) &&
                warp_all(wait_long(bar(B_P_FULL) + 8u * x, d & 1u, abort_flag, p.err));
           if (!ok) break;
           tc_fence_after();
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
           // apart, 8-wide d groups 2048 B apart), K the K-major B operand (128-byte swizzle: 8-key groups
           // 1024 B apart, 16 values of d 32 B apart within a half).  S_x holds the P of step t until its P.V is done.
           const uint32_t t2 = (uint32_t)(t + 2), kt = kc + (t2 >> per), s = kt & 1u;
-          ok = warp_all(wait_long(bar(B_K_FULL) + 8u * s, (kt >> 1) & 1u, abort_flag, p.err));
+          ok = (u.dual && x) || warp_all(wait_long(bar(B_K_FULL) + 8u * s, (kt >> 1) & 1u, abort_flag, p.err));
           if (ok && t >= 0)
             ok = warp_all(wait_long(bar(B_PV_DONE) + 8u * x, ((x ? done1 : done0) + ((uint32_t)t >> 1)) & 1u, abort_flag, p.err));
           if (!ok) break;
