@@ -49,10 +49,6 @@ constexpr int kD = 128;            // head dim
 constexpr int kKeys = 128;         // keys per tile
 constexpr int kRows = 128;         // rows (TMEM lanes) per row tile
 constexpr int kThreadsC = 512;     // warp 0: MMA; 1: TMA; 4-7 / 8-11: softmax of buffer 0 / 1; 12-15: converters
-// Registers a thread of each warpgroup (launched with 128 each, 512 in all).  Nothing in the loops may spill: local
-// memory goes to L2, since shared memory leaves no L1 to speak of.
-constexpr int kRegsIssue = 112, kRegsSoftmax = 152, kRegsConvert = 96;
-static_assert(kRegsIssue + 2 * kRegsSoftmax + kRegsConvert <= 512, "register file");
 constexpr uint32_t TM_O = 0, TM_S = 256;                   // O_x [128x, +128), S_x [256 + 128x, +128)
 constexpr uint32_t KV_TILE = kKeys * kD * 2;               // 32 KB of fp16
 constexpr uint32_t KV_HALF = KV_TILE / 2;                  // 64 values of d: 128 keys x 128 B, 128-byte swizzle
@@ -88,6 +84,13 @@ static_assert(SMEM_CHUNK <= 232448, "shared memory");
 // the least part of the line a CTA takes.
 constexpr int kUnitCost = 2, kLeastPart = 6;
 
+// What the combine kernel has to know of the cut before a CTA's part: nothing (owner < 0) unless it is the
+// first cut of its unit.
+struct Cut {
+  int row0, left, g, dual;      // first packed row of the row block, positions from there on, KV head, two row tiles
+  int owner, last, own, end;    // CTAs of the unit's begin and end; whether their parts hold any key tile
+};
+
 struct ChunkParams {
   const int8_t* q;              // [n][Hq][128]
   const int8_t* k;              // page pool [pool rows][Hkv][128], or [B][T][Hkv][128]
@@ -101,6 +104,7 @@ struct ChunkParams {
   uint16_t* out;                // bf16 [n][Hq][128]
   float4* part_o;               // [2 * CTAs][32][rows_max]: O of a cut unit's part, column group by row
   float2* part_ml;              // [2 * CTAs][rows_max]
+  struct Cut* cuts;             // [CTAs]
   int32_t* err;
   int n, B, T, Hq, Hkv, G, P, causal, ctas, rows_max;
   int page_size, max_pages, num_pages;
@@ -168,20 +172,50 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {     // inclu
   return v;
 }
 
-// Cost of the whole batch (the warp together).
-__device__ __forceinline__ int64_t total_cost(const ChunkParams& p, int lane, bool report) {
+// The line and its parts: CTA c takes [begin(c), begin(c + 1)).  Numbers that fit 32 bits are divided there (a
+// 64-bit division takes a hundred instructions, and the plan is on every call's way).
+__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
+  return ((uint64_t)a | (uint64_t)b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+struct Line {
+  int64_t total, each;
+  int parts, rest;
+  __device__ __forceinline__ int64_t begin(int c) const {
+    return c >= parts ? total : each * c + (int)((uint32_t)rest * (uint32_t)c / (uint32_t)parts);
+  }
+  // The part that position x lies in.
+  __device__ __forceinline__ int owner(int64_t x) const {
+    int c = (int)div64((x + 1) * parts - 1, total);
+    while (c > 0 && begin(c) > x) --c;
+    while (c + 1 < parts && begin(c + 1) <= x) ++c;
+    return c;
+  }
+};
+// The first 32 sequences, a lane each: the second pass over the lengths begins with them.
+struct Ahead {
+  Seq s;
+  int64_t cost;
+};
+// The warp together.
+__device__ __forceinline__ Line make_line(const ChunkParams& p, int lane, bool report, Ahead& a) {
+  a = Ahead{{0, 0, 0}, 0};
   int64_t sum = 0;
-  for (int b = lane; b < p.B; b += 32) sum += sequence_cost(p, sequence_of(p, b, report));
+  for (int b = lane; b < p.B; b += 32) {
+    const Seq s = sequence_of(p, b, report);
+    const int64_t c = sequence_cost(p, s);
+    if (b < 32) a = Ahead{s, c};
+    sum += c;
+  }
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return sum * p.Hkv;
+  Line l;
+  l.total = sum * p.Hkv;
+  const int64_t most = l.total / kLeastPart;
+  l.parts = (int)(most < 1 ? 1 : most < p.ctas ? most : p.ctas);
+  l.each = div64(l.total, l.parts);
+  l.rest = (int)(l.total - l.each * l.parts);
+  return l;
 }
-// CTAs that take part, and where CTA c's part of the line begins.
-__device__ __forceinline__ int parts_of(const ChunkParams& p, int64_t total) {
-  const int64_t most = total / kLeastPart;
-  return (int)(most < 1 ? 1 : most < p.ctas ? most : p.ctas);
-}
-__device__ __forceinline__ int64_t part_begin(int64_t total, int parts, int c) { return total * c / parts; }
 
 // A position on the line: unit (b, g, rb) and the offset into it.
 struct Cursor {
@@ -208,12 +242,17 @@ __device__ __forceinline__ void to_sequence(const ChunkParams& p, Cursor& c, int
   c.s = Seq{0, 0, 0};
 }
 // The unit that holds position x of the line (x < total).
-__device__ __forceinline__ Cursor seek(const ChunkParams& p, int64_t x, int lane) {
+__device__ __forceinline__ Cursor seek(const ChunkParams& p, int64_t x, const Ahead& first, int lane) {
   Cursor c = {p.B, 0, 0, {0, 0, 0}, 0};
   for (int base = 0; base < p.B; base += 32) {
-    Seq s = {0, 0, 0};
-    if (base + lane < p.B) s = sequence_of(p, base + lane, false);
-    const int64_t mine = sequence_cost(p, s), inc = warp_scan(mine * p.Hkv, lane);
+    Seq s = first.s;
+    int64_t mine = first.cost;
+    if (base > 0) {
+      s = Seq{0, 0, 0};
+      if (base + lane < p.B) s = sequence_of(p, base + lane, false);
+      mine = sequence_cost(p, s);
+    }
+    const int64_t inc = warp_scan(mine * p.Hkv, lane);
     const unsigned beyond = __ballot_sync(0xffffffffu, inc > x);
     if (beyond) {
       const int l = __ffs(beyond) - 1;
@@ -223,7 +262,7 @@ __device__ __forceinline__ Cursor seek(const ChunkParams& p, int64_t x, int lane
       c.s.q0 = __shfl_sync(0xffffffffu, s.q0, l);
       c.s.nq = __shfl_sync(0xffffffffu, s.nq, l);
       c.s.nkv = __shfl_sync(0xffffffffu, s.nkv, l);
-      c.g = (int)(x / per_head);
+      c.g = (int)div64(x, per_head);
       x -= c.g * per_head;
       break;
     }
@@ -250,6 +289,31 @@ __device__ __forceinline__ int tile_at(int64_t off, bool dual, int nt) {
   return (int)(t < nt ? t : nt);
 }
 
+// The record of the cut before CTA cta's part (the warp together).
+__device__ __noinline__ void record_cut(const ChunkParams& p, const Line& line, const Ahead& first, int cta, int lane) {
+  Cut cut = {0, 0, 0, 0, -1, 0, 0, 0};
+  const int64_t x = line.begin(cta);
+  if (cta > 0 && cta < line.parts && x < line.total) {
+    const Cursor c = seek(p, x, first, lane);
+    const int64_t begin = x - c.off;                         // of the unit
+    if (c.off > 0 && line.begin(cta - 1) <= begin) {         // its first cut
+      const int nt = tiles_of(p, c.s, c.rb);
+      const bool dual = is_dual(p, c.s, c.rb);
+      const int64_t end = begin + kUnitCost + (int64_t)nt * (dual ? 2 : 1);
+      cut.row0 = c.s.q0 + c.rb * 2 * p.P;
+      cut.left = c.s.nq - c.rb * 2 * p.P;
+      cut.g = c.g;
+      cut.dual = dual;
+      cut.owner = cta - 1;
+      cut.last = line.owner(end - 1);
+      // a CTA between the two has kLeastPart or more of the line, which is a key tile at least
+      cut.own = tile_at(c.off, dual, nt) > 0;
+      cut.end = tile_at(line.begin(cut.last) - begin, dual, nt) < nt;
+    }
+  }
+  if (lane == 0) p.cuts[cta] = cut;
+}
+
 // What a CTA does of a unit: key tiles [t0, t1) of nt, for row block rb.
 struct Part {
   int b, g, rb, q0, nq, nkv, t0, t1, nt;
@@ -266,11 +330,10 @@ struct Walk {
   Part u;
 };
 static_assert(sizeof(Walk) <= kWalkBytes, "walk area");
-__device__ __noinline__ void walk_begin(const ChunkParams& p, Walk* at, int64_t total, int parts, int cta, int lane) {
-  const int64_t x = part_begin(total, parts, cta);
-  const int64_t left = part_begin(total, parts, cta + 1) - x;
+__device__ __noinline__ void walk_begin(const ChunkParams& p, Walk* at, const Line& line, const Ahead& first, int cta, int lane) {
+  const int64_t x = line.begin(cta), left = line.begin(cta + 1) - x;
   Cursor c = {p.B, 0, 0, {0, 0, 0}, 0};
-  if (left > 0) c = seek(p, x, lane);
+  if (left > 0) c = seek(p, x, first, lane);
   if (lane == 0) {
     at->c = c;
     at->left = left;
@@ -362,11 +425,10 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8])
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
                ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
 }
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* tm) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
+}
 __device__ __forceinline__ void prefetch_line(const int8_t* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-template <int N>
-__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -410,15 +472,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + OFF_ABORT);
   auto bar = [&](int i) { return sbase + OFF_BAR + 8u * (uint32_t)i; };
-  pdl_wait();
-  pdl_launch_dependents();
-
-  const int64_t total = total_cost(p, lane, blockIdx.x == 0 && warp == 0);
-  const int parts = parts_of(p, total);
-  if ((int)blockIdx.x >= parts || total == 0) return;
-  Walk* walk = reinterpret_cast<Walk*>(smem + OFF_WALK + warp * kWalkBytes);
-  walk_begin(p, walk, total, parts, blockIdx.x, lane);
-
+  // Set-up that reads nothing another kernel writes goes before the wait for it.
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(B_K_FULL + s), 4);
@@ -437,6 +491,10 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
     mbar_init(bar(B_DRAIN), 1);
     *abort_flag = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (p.box) {
+      prefetch_map(&p.map_k);
+      prefetch_map(&p.map_v);
+    }
   }
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
@@ -447,6 +505,19 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TSLOT);
+  pdl_wait();
+  pdl_launch_dependents();
+
+  Walk* walk = reinterpret_cast<Walk*>(smem + OFF_WALK + warp * kWalkBytes);
+  if (warp != 3) {
+    Ahead first;
+    const Line line = make_line(p, lane, blockIdx.x == 0 && warp == 0, first);
+    if (warp != 2) {
+      walk_begin(p, walk, line, first, blockIdx.x, lane);
+    } else {
+      record_cut(p, line, first, blockIdx.x, lane);
+    }
+  }
 
   if (warp == 0) {
     // ------------------------------------------------------------ MMA issuer
@@ -906,56 +977,23 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
   }
 }
 
-// Merges the parts of cut units.  Block (c - 1, rows): the cut between CTAs c - 1 and c, if it is
-// the first in its unit; rows 32 blockIdx.y .. + 31.  A lane has a row, a warp 16 columns.
+// Merges the parts of cut units.  Block (c - 1, rows): the unit whose first cut lies before CTA c's part; rows
+// 32 blockIdx.y .. + 31.  A lane has a row, a warp 16 columns.
 __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constant__ ChunkParams p) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cut = blockIdx.x + 1;
-  // The lengths were written before the kernel that launched this one ahead of its end, so the
-  // plan need not wait for that kernel; its results do.
-  const int64_t total = total_cost(p, lane, false);
-  const int parts = parts_of(p, total);
-  bool work = cut < parts;
-  Cursor c;
-  int nt = 0, owner = 0;
-  int64_t cost = 0, begin = 0;
-  bool dual = false;
-  if (work) {
-    const int64_t x = part_begin(total, parts, cut);
-    c = seek(p, x, lane);
-    nt = tiles_of(p, c.s, c.rb);
-    dual = is_dual(p, c.s, c.rb);
-    cost = kUnitCost + (int64_t)nt * (dual ? 2 : 1);
-    begin = x - c.off;                                       // of the unit, on the line
-    owner = (int)(((begin + 1) * parts - 1) / total);        // CTA of the unit's begin
-    work = c.off > 0 && owner == cut - 1;
-  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int prow = blockIdx.y * 32 + lane;                   // row tile x 128 + row
+  const int r = prow & (kRows - 1), pl = r / p.G, i = (prow >= kRows ? p.P : 0) + pl;
   pdl_wait();
   pdl_launch_dependents();
-  if (!work) return;
-  const int prow = blockIdx.y * 32 + lane;                   // row tile x 128 + row
-  const int r = prow & (kRows - 1), pl = r / p.G, h = c.g * p.G + r - pl * p.G;
-  const int i = c.rb * 2 * p.P + (prow >= kRows ? p.P : 0) + pl;
-  if (prow >= kRows && !dual) return;
-  const bool active = pl < p.P && i < c.s.nq;
-  auto range = [&](int cta, int& t0, int& t1) {              // the key tiles of a CTA's part
-    const int64_t b = part_begin(total, parts, cta) - begin, e = part_begin(total, parts, cta + 1) - begin;
-    t0 = b <= 0 ? 0 : tile_at(b, dual, nt);
-    t1 = e >= cost ? nt : tile_at(e, dual, nt);
-    return t0 < t1;
-  };
-  int last = owner, have = 0, t0, t1;
-  for (int k = owner; k < parts && part_begin(total, parts, k) < begin + cost; ++k) {
-    last = k;
-    have += range(k, t0, t1) ? 1 : 0;
-  }
-  if (have < 2 || !active) return;                           // one CTA has all the keys after all
-  auto slot_of = [&](int cta) { return 2 * (int64_t)cta + (cta == owner ? 1 : 0); };
+  const Cut cut = p.cuts[blockIdx.x + 1];
+  if (cut.owner < 0 || cut.last - cut.owner - 1 + cut.own + cut.end < 2) return;   // no cut, or one CTA has all keys
+  if ((prow >= kRows && !cut.dual) || pl >= p.P || i >= cut.left) return;
+  const int k0 = cut.owner + (cut.own ? 0 : 1), k1 = cut.last - (cut.end ? 0 : 1);
+  auto slot_of = [&](int cta) { return 2 * (int64_t)cta + (cta == cut.owner ? 1 : 0); };
   float m = -CUDART_INF_F;
-  for (int k = owner; k <= last; ++k)
-    if (range(k, t0, t1)) m = fmaxf(m, p.part_ml[slot_of(k) * p.rows_max + prow].x);
+  for (int k = k0; k <= k1; ++k) m = fmaxf(m, p.part_ml[slot_of(k) * p.rows_max + prow].x);
   float l = 0.f, o[16] = {};
-  for (int k = owner; k <= last; ++k) {
-    if (!range(k, t0, t1)) continue;
+  for (int k = k0; k <= k1; ++k) {
     const float2 ml = p.part_ml[slot_of(k) * p.rows_max + prow];
     if (ml.x == -CUDART_INF_F) continue;
     const float f = ex2_approx(ml.x - m);
@@ -970,14 +1008,15 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constan
       o[4 * q4 + 3] = fmaf(a.w, f, o[4 * q4 + 3]);
     }
   }
-  const float inv = l > 0.f ? p.v_scale[c.g] / l : 0.f;
+  const float inv = l > 0.f ? p.v_scale[cut.g] / l : 0.f;
   uint32_t w[8];
 #pragma unroll
   for (int e = 0; e < 16; e += 2) {
     const __nv_bfloat162 bb = __floats2bfloat162_rn(o[e] * inv, o[e + 1] * inv);
     w[e / 2] = *reinterpret_cast<const uint32_t*>(&bb);
   }
-  uint4* out = reinterpret_cast<uint4*>(p.out + ((int64_t)(c.s.q0 + i) * p.Hq + h) * kD + warp * 16);
+  const int h = cut.g * p.G + r - pl * p.G;
+  uint4* out = reinterpret_cast<uint4*>(p.out + ((int64_t)(cut.row0 + i) * p.Hq + h) * kD + warp * 16);
   out[0] = make_uint4(w[0], w[1], w[2], w[3]);
   out[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }
@@ -986,7 +1025,7 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constan
 int rows_max_of(int n, int G) { return n > kRows / G ? 2 * kRows : kRows; }
 
 size_t workspace_bytes_of(int ctas, int rows_max) {
-  return (size_t)2 * ctas * rows_max * (kD * sizeof(float) + sizeof(float2));
+  return (size_t)2 * ctas * rows_max * (kD * sizeof(float) + sizeof(float2)) + (size_t)ctas * sizeof(Cut);
 }
 
 }  // namespace
@@ -1032,6 +1071,7 @@ int chunk_attn(ChunkParams& p, int D, float softmax_scale, void* workspace, size
   if (!workspace || workspace_bytes < workspace_bytes_of(sms, p.rows_max) || !aligned16(workspace)) return FA3_EWORKSPACE;
   p.part_o = static_cast<float4*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)2 * sms * (kD / 4) * p.rows_max);
+  p.cuts = reinterpret_cast<Cut*>(p.part_ml + (size_t)2 * sms * p.rows_max);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t cache_rows = p.block_table ? (int64_t)p.num_pages * p.page_size : (int64_t)p.B * p.T;
   p.box = p.block_table ? std::min(kKeys, p.page_size & -p.page_size) : kKeys;
