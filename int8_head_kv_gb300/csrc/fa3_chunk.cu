@@ -82,7 +82,7 @@ static_assert(SMEM_CHUNK <= 232448, "shared memory");
 
 // A unit's cost beside its steps (its query rows, pipeline fill and epilogue), in steps, and
 // the least part of the line a CTA takes.
-constexpr int kUnitCost = 2, kLeastPart = 6;
+constexpr int kUnitCost = 2, kLeastPart = 6, kLeastInner = 3;
 
 // What the combine kernel has to know of the cut before a CTA's part: nothing (owner < 0) unless it is the
 // first cut of its unit.
@@ -200,17 +200,23 @@ struct Ahead {
 __device__ __forceinline__ Line make_line(const ChunkParams& p, int lane, bool report, Ahead& a) {
   a = Ahead{{0, 0, 0}, 0};
   int64_t sum = 0;
+  int blocks = 0;
   for (int b = lane; b < p.B; b += 32) {
     const Seq s = sequence_of(p, b, report);
     const int64_t c = sequence_cost(p, s);
     if (b < 32) a = Ahead{s, c};
     sum += c;
+    blocks += blocks_of(p, s);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  blocks = __reduce_add_sync(0xffffffffu, blocks);
   Line l;
   l.total = sum * p.Hkv;
-  const int64_t most = l.total / kLeastPart;
+  // Parts of kLeastPart or more; short units go one to a CTA, though (parts of kLeastInner or more, so that a part
+  // inside a unit still holds a key tile).
+  const int64_t units = min((int64_t)blocks * p.Hkv, l.total / kLeastInner);
+  const int64_t most = max(l.total / kLeastPart, units);
   l.parts = (int)(most < 1 ? 1 : most < p.ctas ? most : p.ctas);
   l.each = div64(l.total, l.parts);
   l.rest = (int)(l.total - l.each * l.parts);
@@ -306,7 +312,7 @@ __device__ __noinline__ void record_cut(const ChunkParams& p, const Line& line, 
       cut.dual = dual;
       cut.owner = cta - 1;
       cut.last = line.owner(end - 1);
-      // a CTA between the two has kLeastPart or more of the line, which is a key tile at least
+      // a CTA between the two has kLeastInner or more of the line, which is a key tile at least
       cut.own = tile_at(c.off, dual, nt) > 0;
       cut.end = tile_at(line.begin(cut.last) - begin, dual, nt) < nt;
     }
