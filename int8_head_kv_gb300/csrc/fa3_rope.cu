@@ -43,8 +43,7 @@ struct HeadOut {
 struct RotArgs {
   const float* cos_sin;     // [table_len][rot], or nullptr: no rotation
   int table_len, rot, interleaved, D;
-  float eps, inv_D;
-  double inv_D64;
+  float eps, inv_D, inv_D_lo;                 // inv_D + inv_D_lo = 1 / D
 };
 
 // A lane's eight values of a row: two groups of four at o1 and o2.
@@ -324,11 +323,11 @@ __device__ __forceinline__ int find_sequence(const int32_t* q_start, int B, int 
 // nearer than 8 (20) u (|a| + |b|) max(|ac|, |bs|, |bc|, |as|) is decided again: one or
 // two values in 10^4 of normal data.
 //
-// Again, by the whole warp because the row's sum of squares is needed: sum and products
-// in float64, 1 / sqrt by one Newton step on rsqrtf (relative 1e-13), and the sign of
-// y - h s for the half step h next to t (h s is exact).  What float32 cannot carry (a scale
-// outside [2^-100, 2^100], a sum of squares outside [2^-100, 2^100], infinities and NaN)
-// ends there too.  The codes are those of float64 arithmetic.
+// Again, by the whole warp because the row's sum of squares is needed: everything as unevaluated pairs of
+// float32 (Dekker's products by fma, Knuth's sums; float64 runs at a small fraction of the float32 rate here),
+// 1 / sqrt by one correction of the hardware's, and the sign of y - h s for the half step h next to t.  What float32
+// cannot carry (a scale outside [2^-100, 2^100], a sum of squares outside [2^-100, 2^100], infinities and NaN) takes
+// float64.  The pairs hold 45 bits or more of y, so the codes are those of float64 arithmetic.
 constexpr float kTieNorm = 20.f / 16777216.f, kTiePlain = 8.f / 16777216.f;
 
 __device__ __forceinline__ int code64(double y, double s) {
@@ -336,69 +335,97 @@ __device__ __forceinline__ int code64(double y, double s) {
   return __double2int_rn(fmin(fmax(y / s, -127.0), 127.0));
 }
 
-// Value e of a lane's eight, decided in float64 (x: the values, w: the weights, c and sn
-// the angles of its four pairs).
+struct Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ Pair product(float a, float b) {          // exact
+  const float h = __fmul_rn(a, b);
+  return Pair{h, fmaf(a, b, -h)};
+}
+__device__ __forceinline__ Pair sum(float a, float b) {              // exact
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return Pair{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+
+// Value e of a lane's eight (x: the values, w: the weights or ones, c and sn the angles of its four pairs, r:
+// 1 / rms), decided as described above; t: y / scale in float32.
 template <bool INTER>
-__device__ __forceinline__ int decide64(const float (&x)[8], const float (&w)[8], const float (&c)[4],
-                                        const float (&sn)[4], int e, double rstd, bool norm, bool turn, bool exact,
-                                        float s, float rs) {
+__device__ __forceinline__ int decide(const float (&x)[8], const float (&w)[8], const float (&c)[4],
+                                      const float (&sn)[4], int e, Pair r, bool norm, bool turn, float s, float rs) {
   const int pe = INTER ? e / 2 : e % 4;
   const bool sec = INTER ? (e & 1) != 0 : e >= 4;
   const int o = sec ? first<INTER>(pe) : second<INTER>(pe);
-  const double mine = (double)x[e] * rstd * (norm ? (double)w[e] : 1.0);
-  double y = mine;
+  Pair y = {x[e] * w[e], 0.f};                                       // bf16 x bf16: exact
   if (turn) {
-    const double other = (double)x[o] * rstd * (norm ? (double)w[o] : 1.0);
-    y = sec ? mine * (double)c[pe] + other * (double)sn[pe] : mine * (double)c[pe] - other * (double)sn[pe];
+    const float other = x[o] * w[o];
+    const Pair p = product(y.hi, c[pe]), q = product(other, sec ? sn[pe] : -sn[pe]);
+    const Pair z = sum(p.hi, q.hi);
+    y = sum(z.hi, __fadd_rn(z.lo, __fadd_rn(p.lo, q.lo)));
   }
-  if (!exact) return code64(y, (double)s);
-  const float lo = floorf((float)y * rs), h = lo + 0.5f;       // the half step next to y / s
-  const double over = y - (double)h * (double)s;
-  const int code = (int)(over > 0.0 ? lo + 1.f : over < 0.0 ? lo : rintf(h));
+  if (norm) {
+    const Pair p = product(y.hi, r.hi);
+    y = Pair{p.hi, __fadd_rn(p.lo, fmaf(y.hi, r.lo, __fmul_rn(y.lo, r.hi)))};
+  }
+  const float lo = floorf(y.hi * rs), h = lo + 0.5f;                 // the half step next to y / s
+  const Pair g = product(h, s);
+  const float over = __fadd_rn(__fsub_rn(y.hi, g.hi), __fsub_rn(y.lo, g.lo));
+  const int code = (int)(over > 0.0f ? lo + 1.f : over < 0.0f ? lo : rintf(h));
   return max(-127, min(127, code));
 }
-
-// (hi, lo) += v with hi + lo exact but for lo's own roundings.
-__device__ __forceinline__ void add_exact(float& hi, float& lo, float v) {
-  const float s = __fadd_rn(hi, v), t = __fsub_rn(s, hi);
-  lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(v, t)));
-  hi = s;
+// The same in float64, for what float32 does not hold.
+template <bool INTER>
+__device__ __forceinline__ int decide64(const float (&x)[8], const float (&w)[8], const float (&c)[4],
+                                        const float (&sn)[4], int e, double rstd, bool turn, float s) {
+  const int pe = INTER ? e / 2 : e % 4;
+  const bool sec = INTER ? (e & 1) != 0 : e >= 4;
+  const int o = sec ? first<INTER>(pe) : second<INTER>(pe);
+  const double mine = (double)x[e] * rstd * (double)w[e];
+  double y = mine;
+  if (turn) {
+    const double other = (double)x[o] * rstd * (double)w[o];
+    y = sec ? mine * (double)c[pe] + other * (double)sn[pe] : mine * (double)c[pe] - other * (double)sn[pe];
+  }
+  return code64(y, (double)s);
 }
 
-// The lane's codes with those of `again` (a bit each) decided in float64; every lane of
-// the warp calls it.  Out of line: it is rare, and its registers are not the loop's.
+// The lane's codes with those of `again` (a bit each) decided again; every lane of the warp calls it.  Out of
+// line: it is rare, and its registers are not the loop's.
 template <int LANES, bool INTER>
 __device__ __noinline__ uint2 decide_row(const RotArgs& r, const uint16_t* weight, uint2 x1, uint2 x2, float s,
                                          uint2 codes, uint32_t again, bool sound, bool is_v, int pos, int i) {
   const Lane8 p = lane_place(i, r);
-  float x[8], w[8] = {}, c[4] = {}, sn[4] = {};
+  float x[8], w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f}, c[4] = {}, sn[4] = {};
   bf16x4(x1, x);
   bf16x4(x2, x + 4);
+  Pair rms = {1.f, 0.f};
   double rstd = 1.0;
   if (weight) {
-    // The sum of squares as an unevaluated pair of float32 (Knuth's exact sum of two numbers;
-    // the squares are exact): float64 arithmetic is 32 times slower here, so it starts at the
-    // row's one sum.
-    float hi = 0.f, lo = 0.f;
+    Pair ss = {0.f, 0.f};                                            // the squares are exact
+    auto add = [&](float v) {
+      const Pair z = sum(ss.hi, v);
+      ss = Pair{z.hi, __fadd_rn(ss.lo, z.lo)};
+    };
 #pragma unroll
-    for (int e = 0; e < 8; ++e) add_exact(hi, lo, x[e] * x[e]);
+    for (int e = 0; e < 8; ++e) add(x[e] * x[e]);
 #pragma unroll
     for (int o = LANES / 2; o; o >>= 1) {
-      const float h2 = __shfl_xor_sync(0xffffffffu, hi, o), l2 = __shfl_xor_sync(0xffffffffu, lo, o);
-      add_exact(hi, lo, h2);
-      lo = __fadd_rn(lo, l2);
+      const float h2 = __shfl_xor_sync(0xffffffffu, ss.hi, o), l2 = __shfl_xor_sync(0xffffffffu, ss.lo, o);
+      add(h2);
+      ss.lo = __fadd_rn(ss.lo, l2);
     }
-    double ms;
-    if (sound) {
-      ms = ((double)hi + (double)lo) * r.inv_D64 + (double)r.eps;
-      const double r0 = (double)rsqrtf((float)ms);
-      rstd = r0 * fma(-0.5 * ms * r0, r0, 1.5);
-    }
-    if (__any_sync(0xffffffffu, !sound)) {                   // squares that float32 does not hold
+    // m = ss / D + eps, then r0 + r0 (e / 2 + 3 e^2 / 8) with e = 1 - m r0^2
+    const Pair d = product(ss.hi, r.inv_D);
+    Pair m = sum(d.hi, r.eps);
+    m = sum(m.hi, __fadd_rn(m.lo, __fadd_rn(d.lo, fmaf(ss.hi, r.inv_D_lo, __fmul_rn(ss.lo, r.inv_D)))));
+    const float r0 = rsqrt_approx(m.hi);
+    const Pair t = product(r0, r0), u = product(m.hi, t.hi);
+    const float e = __fsub_rn(__fsub_rn(__fsub_rn(1.f, u.hi), u.lo), fmaf(m.hi, t.lo, __fmul_rn(m.lo, t.hi)));
+    rms = Pair{r0, r0 * (e * fmaf(0.375f, e, 0.5f))};
+    if (__any_sync(0xffffffffu, !sound)) {                           // squares that float32 does not hold
       double sd = 0.0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sd = fma((double)x[e], (double)x[e], sd);
-      ms = row_sum<LANES>(sd) / (double)r.D + (double)r.eps;
+      for (int k = 0; k < 8; ++k) sd = fma((double)x[k], (double)x[k], sd);
+      const double ms = row_sum<LANES>(sd) / (double)r.D + (double)r.eps;
       if (!sound) rstd = 1.0 / sqrt(ms);
     }
   }
@@ -413,11 +440,14 @@ __device__ __noinline__ uint2 decide_row(const RotArgs& r, const uint16_t* weigh
     c[0] = c4.x, c[1] = c4.y, c[2] = c4.z, c[3] = c4.w;
     sn[0] = s4.x, sn[1] = s4.y, sn[2] = s4.z, sn[3] = s4.w;
   }
+  const float rs = rcp_approx(s);
   uint32_t q[2] = {codes.x, codes.y};
 #pragma unroll
   for (int e = 0; e < 8; ++e)
     if (again >> e & 1u) {
-      const int code = is_v ? quant_code(x[e], s) : decide64<INTER>(x, w, c, sn, e, rstd, weight != nullptr, p.rotated, sound, s, rcp_approx(s));
+      const int code = is_v ? quant_code(x[e], s)
+                            : sound ? decide<INTER>(x, w, c, sn, e, rms, weight != nullptr, p.rotated, s, rs)
+                                    : decide64<INTER>(x, w, c, sn, e, rstd, p.rotated, s);
       q[e / 4] = (q[e / 4] & ~(0xffu << (8 * (e % 4)))) | (((uint32_t)code & 0xffu) << (8 * (e % 4)));
     }
   return make_uint2(q[0], q[1]);
@@ -563,13 +593,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
         const float lim = fmaf(-m * band, f, 0.5f);
         const float dm = max3(max3(fabsf(d[0]), fabsf(d[1]), fabsf(d[2])), max3(fabsf(d[3]), fabsf(d[4]), fabsf(d[5])),
                               fmaxf(fabsf(d[6]), fabsf(d[7])));
-        const bool sure = sound & (dm <= lim) & (lim >= lim_min);
+        sound = sound & (lim >= lim_min);                     // |t| below 2^15 and no infinity or NaN
+        const bool sure = sound & (dm <= lim);
         const bool live = h + u * rows < n_in;
         if (__any_sync(0xffffffffu, live & !sure)) {
           uint32_t again = 0;
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            if (live & (!sound | !(lim >= lim_min) | !(fabsf(d[e]) <= lim))) again |= 1u << e;
+            if (live & (!sound | !(fabsf(d[e]) <= lim))) again |= 1u << e;
           code = decide_row<LANES, INTER>(a.r, T.weight, cur[u][0], cur[u][1], s, code, again, sound, is_v, pl.pos, i);
         }
         if (live) {
@@ -607,7 +638,7 @@ int rot_args(const float* cos_sin, int table_len, int rot_dim, int interleaved, 
     rot_dim = 0;
     table_len = 0;
   }
-  *r = RotArgs{cos_sin, table_len, rot_dim, interleaved ? 1 : 0, D, eps, 1.f / (float)D, 1.0 / (double)D};
+  *r = RotArgs{cos_sin, table_len, rot_dim, interleaved ? 1 : 0, D, eps, 1.f / (float)D, (float)(1.0 / D - (double)(1.f / (float)D))};
   return FA3_OK;
 }
 
