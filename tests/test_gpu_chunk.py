@@ -43,10 +43,12 @@ def _run(F, c, err=None, out=None, **kw):
     if out is None:
         out = torch.full(c["q"].shape, KEEP, dtype=torch.bfloat16, device="cuda")
     a = [_t(c[k]) for k in ("q", "k", "v", "qs", "ks", "vs", "q_start", "lens")]
+    table = None if c["page"] is None else _t(c["table"])
+    torch.cuda.synchronize()                                 # the call may be on another stream than the copies
     if c["page"] is None:
         o = F.cross_attn_gqa(*a, SM, out=out, dev_err=err, **kw)
     else:
-        o = F.prefill_attn_gqa_paged(*a, _t(c["table"]), SM, out=out, dev_err=err, **kw)
+        o = F.prefill_attn_gqa_paged(*a, table, SM, out=out, dev_err=err, **kw)
     torch.cuda.synchronize()
     return o.float().cpu().numpy()
 
