@@ -714,18 +714,22 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
           sts128(dst + 4 * i * 128 + (at ^ 16u), o1);
         };
         if (p.box) {
-          ok = warp_wait(bar(B_RAW_FULL) + 8u * kv, kc & 1u, lane, abort_flag, p.err) &&
-               warp_wait(bar(B_K_EMPTY) + 8u * (s + (B_V_EMPTY - B_K_EMPTY) * kv), par, lane, abort_flag, p.err);
+          ok = warp_wait(bar(B_RAW_FULL) + 8u * kv, kc & 1u, lane, abort_flag, p.err);
           if (!ok) break;
+          // The int8 tile is given back as soon as it is in registers, before the wait for the fp16 tile's place (chunk
+          // of 16 x 4096 keys, one token each: 63 -> 57.5 us).  The fence holds the TMA's next writes behind these
+          // reads: without it one warp in some thousands read its part of the next tile.
           const uint32_t src = src0 + kv * RAW_TILE;
-#pragma unroll 1
-          for (int i = 0; i < 8; i += 2) {
-            const uint4 r0 = lds128(src + 4 * i * kD), r1 = lds128(src + 4 * i * kD + 4 * kD);
-            write(r0, i);
-            write(r1, i + 1);
-          }
+          uint4 r[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) r[i] = lds128(src + 4 * i * kD);
+          fence_proxy_async();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(B_RAW_EMPTY) + 8u * kv);
+          ok = warp_wait(bar(B_K_EMPTY) + 8u * (s + (B_V_EMPTY - B_K_EMPTY) * kv), par, lane, abort_flag, p.err);
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) write(r[i], i);
         } else {
           uint4 r[8];
           const int8_t* base = (kv ? p.v : p.k) + head + cl * 16;
