@@ -481,9 +481,9 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
   // Set-up that reads nothing another kernel writes goes before the wait for it.
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(bar(B_K_FULL + s), 4);
+      mbar_init(bar(B_K_FULL + s), 2);
       mbar_init(bar(B_K_EMPTY + s), 1);
-      mbar_init(bar(B_V_FULL + s), 4);
+      mbar_init(bar(B_V_FULL + s), 2);
       mbar_init(bar(B_V_EMPTY + s), 1);
       mbar_init(bar(B_S_FULL + s), 1);
       mbar_init(bar(B_P_FULL + s), 4);
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
       mbar_init(bar(B_ML + s), 4);
       mbar_init(bar(B_READ + s), 4);
       mbar_init(bar(B_RAW_FULL + s), 1);
-      mbar_init(bar(B_RAW_EMPTY + s), 4);
+      mbar_init(bar(B_RAW_EMPTY + s), 2);
     }
     mbar_init(bar(B_Q_READY), 8);
     mbar_init(bar(B_DRAIN), 1);
@@ -656,19 +656,21 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
     }
   } else if (warp >= 12) {
     // ------------------------------------------------------ int8 -> fp16 converters
-    // A warp has 32 keys of a tile, a lane 16 bytes of eight of them: bytes 16 (l % 8) .. of row l / 8, lanes
-    // l % 8 >= 4 of the row's neighbour (l / 8) ^ 1.  The two 16-byte fp16 chunks they become go to chunks 2c and
-    // 2c + 1 of the key's swizzled row; the neighbour's row has the other parity, so the eight lanes of a
-    // store hit different banks.  Without boxes the bytes come from the cache itself: a lane looks one key up, the
-    // others get its row by shuffles, and the rows of the next tile are asked of HBM into L2 a tile ahead.
-    const int cw = warp - 12, cl = lane & 7, rl = (lane >> 3) ^ (cl >> 2);
-    const uint32_t src0 = sbase + OFF_RAW + (uint32_t)(32 * cw + rl) * kD + cl * 16;
+    // Warps 12 and 13 have K, 14 and 15 V (each in a chain of its own: 16 x 4096 keys, one token each, 57.5 -> 53.6 us
+    // against all four on K and then V).  A warp has 64 keys of a tile, a lane 16 bytes of sixteen of them: bytes
+    // 16 (l % 8) .. of row l / 8, lanes l % 8 >= 4 of the row's neighbour (l / 8) ^ 1.  The two 16-byte fp16 chunks they
+    // become go to chunks 2c and 2c + 1 of the key's swizzled row; the neighbour's row has the other parity, so
+    // the eight lanes of a store hit different banks.  Without boxes the bytes come from the cache itself: a lane
+    // looks two keys up, the others get their rows by shuffles, and the rows of the next tile are asked of HBM into
+    // L2 a tile ahead.
+    const int cw = warp & 1, kv = (warp - 12) >> 1, cl = lane & 7, rl = (lane >> 3) ^ (cl >> 2);
+    const uint32_t src = sbase + OFF_RAW + kv * RAW_TILE + (uint32_t)(64 * cw + rl) * kD + cl * 16;
     // chunk 2 cl (and 2 cl + 1) of key n: half cl / 4, row n, chunk ((2 cl) % 8) ^ (n % 8)
-    const uint32_t dst0 = sbase + (uint32_t)(cl >> 2) * KV_HALF + (uint32_t)(32 * cw + rl) * 128;
+    const uint32_t dst0 = sbase + (uint32_t)(cl >> 2) * KV_HALF + (uint32_t)(64 * cw + rl) * 128;
     const uint32_t at0 = ((uint32_t)(2 * cl & 7) ^ (uint32_t)rl) * 16;   // n % 8 = rl, or rl + 4 for odd i
     const int row_stride = p.Hkv * kD;
     int j = 0, t_end = 0, n_keys = 0, b = 0, g = 0;          // the tile to look up next
-    int mine = 0, head = 0, head_next = 0;                   // the tile looked up: this lane's row, offset of the KV head
+    int mine[2] = {0, 0}, head = 0, head_next = 0;                   // the tile looked up: this lane's row, offset of the KV head
     auto look_up = [&]() {                                   // false: nothing left
       while (j >= t_end) {
         if (!walk_next(p, walk, lane)) return false;
@@ -680,16 +682,18 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
         n_keys = p.causal ? u.nkv - u.nq + min(u.nq, (u.rb + 1) * 2 * p.P) : u.nkv;
       }
       if (!p.box) {
-        const uint32_t t = (uint32_t)min(j * kKeys + 32 * cw + lane, n_keys - 1), pi = divu32(t, p.div_ps);
-        int pg = __ldg(p.block_table + (int64_t)b * p.max_pages + pi);
-        if ((uint32_t)pg >= (uint32_t)p.num_pages) {         // outside the pool: any page of it
-          set_dev_err(p.err, FA3_DEVERR_PAGE);
-          pg = 0;
-        }
-        mine = pg * p.page_size + (int)(t - pi * (uint32_t)p.page_size);
         head_next = g * kD;
-        prefetch_line(p.k + (int64_t)mine * row_stride + head_next);
-        prefetch_line(p.v + (int64_t)mine * row_stride + head_next);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t t = (uint32_t)min(j * kKeys + 64 * cw + 32 * h + lane, n_keys - 1), pi = divu32(t, p.div_ps);
+          int pg = __ldg(p.block_table + (int64_t)b * p.max_pages + pi);
+          if ((uint32_t)pg >= (uint32_t)p.num_pages) {         // outside the pool: any page of it
+            set_dev_err(p.err, FA3_DEVERR_PAGE);
+            pg = 0;
+          }
+          mine[h] = pg * p.page_size + (int)(t - pi * (uint32_t)p.page_size);
+          prefetch_line((kv ? p.v : p.k) + (int64_t)mine[h] * row_stride + head_next);
+        }
       }
       ++j;
       return true;
@@ -697,54 +701,44 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
     bool more = look_up(), ok = true;
     for (uint32_t kc = 0; more && ok; ++kc) {
       const uint32_t s = kc & 1u, par = ((kc >> 1) & 1u) ^ 1u;
-      const int rows = mine;                                 // of this tile
+      const int rows[2] = {mine[0], mine[1]};                // of this tile
       head = head_next;
       more = look_up();
-#pragma unroll 1
-      for (uint32_t kv = 0; kv < 2 && ok; ++kv) {
-        const uint32_t dst = dst0 + OFF_K + (OFF_V - OFF_K) * kv + s * KV_TILE;
-        auto write = [&](const uint4& r, int i) {
-          uint4 o0, o1;
-          i8x4_to_f16x4(r.x, o0.x, o0.y);
-          i8x4_to_f16x4(r.y, o0.z, o0.w);
-          i8x4_to_f16x4(r.z, o1.x, o1.y);
-          i8x4_to_f16x4(r.w, o1.z, o1.w);
-          const uint32_t at = at0 ^ ((uint32_t)(i & 1) << 6);
-          sts128(dst + 4 * i * 128 + at, o0);
-          sts128(dst + 4 * i * 128 + (at ^ 16u), o1);
-        };
-        if (p.box) {
-          ok = warp_wait(bar(B_RAW_FULL) + 8u * kv, kc & 1u, lane, abort_flag, p.err);
-          if (!ok) break;
-          // The int8 tile is given back as soon as it is in registers, before the wait for the fp16 tile's place (chunk
-          // of 16 x 4096 keys, one token each: 63 -> 57.5 us).  The fence holds the TMA's next writes behind these
-          // reads: without it one warp in some thousands read its part of the next tile.
-          const uint32_t src = src0 + kv * RAW_TILE;
-          uint4 r[8];
+      const uint32_t dst = dst0 + OFF_K + (OFF_V - OFF_K) * kv + s * KV_TILE;
+      uint4 r[16];
+      if (p.box) {
+        // The int8 tile is given back as soon as it is in registers, before the wait for the fp16 tile's place (the same
+        // workload: 63 -> 57.5 us).  The fence holds the TMA's next writes behind these reads: without it
+        // one warp in some thousands read its part of the next tile.
+        ok = warp_wait(bar(B_RAW_FULL) + 8u * kv, kc & 1u, lane, abort_flag, p.err);
+        if (!ok) break;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) r[i] = lds128(src + 4 * i * kD);
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(B_RAW_EMPTY) + 8u * kv);
-          ok = warp_wait(bar(B_K_EMPTY) + 8u * (s + (B_V_EMPTY - B_K_EMPTY) * kv), par, lane, abort_flag, p.err);
-          if (!ok) break;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) write(r[i], i);
-        } else {
-          uint4 r[8];
-          const int8_t* base = (kv ? p.v : p.k) + head + cl * 16;
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            r[i] = load_once(base + (int64_t)__shfl_sync(0xffffffffu, rows, 4 * i + rl) * row_stride);
-          ok = warp_wait(bar(B_K_EMPTY) + 8u * (s + (B_V_EMPTY - B_K_EMPTY) * kv), par, lane, abort_flag, p.err);
-          if (!ok) break;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) write(r[i], i);
-        }
+        for (int i = 0; i < 16; ++i) r[i] = lds128(src + 4 * i * kD);
         fence_proxy_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_K_FULL) + 8u * (s + (B_V_FULL - B_K_FULL) * kv));
+        if (lane == 0) mbar_arrive(bar(B_RAW_EMPTY) + 8u * kv);
+      } else {
+        const int8_t* base = (kv ? p.v : p.k) + head + cl * 16;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          r[i] = load_once(base + (int64_t)__shfl_sync(0xffffffffu, rows[i >> 3], (4 * i & 31) + rl) * row_stride);
       }
+      ok = warp_wait(bar(B_K_EMPTY) + 8u * (s + (B_V_EMPTY - B_K_EMPTY) * kv), par, lane, abort_flag, p.err);
+      if (!ok) break;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        uint4 o0, o1;
+        i8x4_to_f16x4(r[i].x, o0.x, o0.y);
+        i8x4_to_f16x4(r[i].y, o0.z, o0.w);
+        i8x4_to_f16x4(r[i].z, o1.x, o1.y);
+        i8x4_to_f16x4(r[i].w, o1.z, o1.w);
+        const uint32_t at = at0 ^ ((uint32_t)(i & 1) << 6);
+        sts128(dst + 4 * i * 128 + at, o0);
+        sts128(dst + 4 * i * 128 + (at ^ 16u), o1);
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_K_FULL) + 8u * (s + (B_V_FULL - B_K_FULL) * kv));
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ softmax warps
