@@ -82,7 +82,7 @@ static_assert(SMEM_CHUNK <= 232448, "shared memory");
 
 // A unit's cost beside its steps (its query rows, pipeline fill and epilogue), in steps, and
 // the least part of the line a CTA takes.
-constexpr int kUnitCost = 2, kLeastPart = 6, kLeastInner = 3;
+constexpr int kUnitCost = 4, kLeastPart = 8, kLeastInner = 5;
 
 // What the combine kernel has to know of the cut before a CTA's part: nothing (owner < 0) unless it is the
 // first cut of its unit.
