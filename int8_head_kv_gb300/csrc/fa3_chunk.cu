@@ -60,9 +60,9 @@ constexpr uint32_t OFF_RAW = OFF_V + 2 * KV_TILE;          // int8 K and V tile 
 constexpr uint32_t RAW_TILE = kKeys * kD;
 constexpr uint32_t OFF_ML = OFF_Q + Q_TILE;                // [2][128] float2: (m, l) of a single row tile's halves,
                                                            // in the second row tile's place
-constexpr uint32_t kWalkBytes = 96;
-constexpr uint32_t OFF_WALK = OFF_RAW + 2 * RAW_TILE;      // a Walk a warp
-constexpr uint32_t OFF_BAR = OFF_WALK + 16 * kWalkBytes;
+constexpr uint32_t OFF_PARTS = OFF_RAW + 2 * RAW_TILE;     // the ring of parts
+constexpr uint32_t kRing = 4, kPartBytes = 48;
+constexpr uint32_t OFF_BAR = OFF_PARTS + kRing * kPartBytes;
 enum {
   B_K_FULL = 0, B_K_EMPTY = 2, B_V_FULL = 4, B_V_EMPTY = 6,
   B_S_FULL = 8,                    // [2]: buffer x's scores of its next step
@@ -72,17 +72,19 @@ enum {
   B_READ = 16,                     // [2]: warps of buffer x have read both O of a single row tile
   B_RAW_FULL = 18,                 // [2]: int8 K, V tile arrived
   B_RAW_EMPTY = 20,                // [2]: int8 K, V tile taken into registers
-  B_Q_READY = 22, B_DRAIN, B_N
+  B_Q_READY = 22, B_DRAIN = 23,
+  B_PART_FULL = 24, B_PART_EMPTY = 28,   // [4]: part of the ring written, read by all
+  B_N = 32
 };
+__constant__ const uint8_t kArrivals[B_N] = {2, 2, 1, 1, 2, 2, 1, 1, 1, 1, 4, 4, 1, 1, 4, 4, 4, 4, 1, 1, 2, 2, 8, 1, 1, 1, 1, 1, 14, 14, 14, 14};
 constexpr uint32_t OFF_TSLOT = OFF_BAR + 8 * B_N;
 constexpr uint32_t OFF_ABORT = OFF_TSLOT + 4;
-constexpr uint32_t SMEM_CHUNK = OFF_BAR + 256 + 1024;      // + alignment slack
-static_assert(OFF_ABORT + 4 <= OFF_BAR + 256, "barrier area");
+constexpr uint32_t SMEM_CHUNK = OFF_ABORT + 4 + 1024;      // + alignment slack
 static_assert(SMEM_CHUNK <= 232448, "shared memory");
 
 // A unit's cost beside its steps (its query rows, pipeline fill and epilogue), in steps, and
 // the least part of the line a CTA takes.
-constexpr int kUnitCost = 4, kLeastPart = 8, kLeastInner = 5;
+constexpr int kUnitCost = 3, kLeastPart = 8, kLeastInner = 4;
 
 // What the combine kernel has to know of the cut before a CTA's part: nothing (owner < 0) unless it is the
 // first cut of its unit.
@@ -108,7 +110,8 @@ struct ChunkParams {
   int32_t* err;
   int n, B, T, Hq, Hkv, G, P, causal, ctas, rows_max;
   int page_size, max_pages, num_pages;
-  DivU32 div_ps;                // / page_size
+  DivU32 div_ps, div_2p;        // / page_size, / (2 P)
+  int narrow;                   // the line's numbers fit 24 bits
   float sm_log2;                // softmax_scale * log2(e)
   int box;                      // rows of a TMA box; 0: pages too ragged for boxes, loads through registers
   CUtensorMap map_k, map_v;     // [cache rows][Hkv * 128] in boxes of [box][128]
@@ -137,110 +140,141 @@ __device__ __forceinline__ Seq sequence_of(const ChunkParams& p, int b, bool rep
   }
   return s;
 }
-__device__ __forceinline__ int blocks_of(const ChunkParams& p, const Seq& s) { return (s.nq + 2 * p.P - 1) / (2 * p.P); }
+__device__ __forceinline__ int blocks_of(const ChunkParams& p, const Seq& s) {
+  return (int)divu32((uint32_t)(s.nq + 2 * p.P - 1), p.div_2p);
+}
 // Key tiles of row block rb, and its cost.
 __device__ __forceinline__ int tiles_of(const ChunkParams& p, const Seq& s, int rb) {
   const int keys = p.causal ? s.nkv - s.nq + min(s.nq, (rb + 1) * 2 * p.P) : s.nkv;
-  return (keys + kKeys - 1) / kKeys;
+  return (int)(((uint32_t)keys + kKeys - 1) / kKeys);
 }
 __device__ __forceinline__ bool is_dual(const ChunkParams& p, const Seq& s, int rb) { return s.nq - rb * 2 * p.P > p.P; }
 __device__ __forceinline__ int cost_of(const ChunkParams& p, const Seq& s, int rb) {
   return kUnitCost + tiles_of(p, s, rb) * (is_dual(p, s, rb) ? 2 : 1);
 }
+
+// The line's numbers are I: uint32_t where they fit 24 bits (the host's bound), int64_t otherwise.  The plan is on
+// every call's way, and 64-bit divisions and scans take several times as long.
+
+// Sum over r < n of floor((at + r step) / mod): whole multiples come out, then the roles of step and mod change
+// (the lattice points under a line, counted along the other axis).
+template <class I>
+__device__ __forceinline__ I floor_sum(I n, I mod, I step, I at) {
+  I total = 0;
+#pragma unroll 1
+  for (;;) {
+    total += n * (n - 1) / 2 * (step / mod) + n * (at / mod);
+    step %= mod;
+    at %= mod;
+    const I top = step * n + at;
+    if (top < mod) return total;
+    n = top / mod;
+    at = top % mod;
+    const I t = mod;
+    mod = step;
+    step = t;
+  }
+}
 // Cost of all row blocks of one KV head of the sequence.
-__device__ __forceinline__ int64_t sequence_cost(const ChunkParams& p, const Seq& s) {
+template <class I>
+__device__ __forceinline__ I sequence_cost(const ChunkParams& p, const Seq& s) {
   const int nb = blocks_of(p, s);
   if (nb == 0) return 0;
-  int64_t c = cost_of(p, s, nb - 1) + (int64_t)(nb - 1) * kUnitCost;
-  if (p.causal) {
-    int64_t t = 0;
-    int keys = s.nkv - s.nq + 2 * p.P + kKeys - 1;
-    for (int rb = 0; rb < nb - 1; ++rb, keys += 2 * p.P) t += keys / kKeys;
-    c += 2 * t;
-  } else {
-    c += 2 * (int64_t)(nb - 1) * ((s.nkv + kKeys - 1) / kKeys);
-  }
+  I c = (I)cost_of(p, s, nb - 1) + (I)(nb - 1) * kUnitCost;
+  if (nb > 1)
+    c += 2 * (p.causal ? floor_sum<I>((I)(nb - 1), kKeys, (I)(2 * p.P), (I)(s.nkv - s.nq) + 2 * p.P + kKeys - 1)
+                       : (I)(nb - 1) * (I)tiles_of(p, s, 0));
   return c;
 }
 
-__device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {     // inclusive
+template <class I>
+__device__ __forceinline__ I warp_scan(I v, int lane) {     // inclusive
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+    const I y = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += y;
   }
   return v;
 }
 
-// The line and its parts: CTA c takes [begin(c), begin(c + 1)).  Numbers that fit 32 bits are divided there (a
-// 64-bit division takes a hundred instructions, and the plan is on every call's way).
-__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
-  return ((uint64_t)a | (uint64_t)b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
-}
+// The line and its parts: CTA c takes [begin(c), begin(c + 1)).
+template <class I>
 struct Line {
-  int64_t total, each;
+  I total, each;
   int parts, rest;
-  __device__ __forceinline__ int64_t begin(int c) const {
-    return c >= parts ? total : each * c + (int)((uint32_t)rest * (uint32_t)c / (uint32_t)parts);
+  __device__ __forceinline__ I begin(int c) const {
+    return c >= parts ? total : each * (I)c + (I)((uint32_t)rest * (uint32_t)c / (uint32_t)parts);
   }
   // The part that position x lies in.
-  __device__ __forceinline__ int owner(int64_t x) const {
-    int c = (int)div64((x + 1) * parts - 1, total);
+  __device__ __forceinline__ int owner(I x) const {
+    int c = (int)(((x + 1) * (I)parts - 1) / total);
     while (c > 0 && begin(c) > x) --c;
     while (c + 1 < parts && begin(c + 1) <= x) ++c;
     return c;
   }
 };
-// The first 32 sequences, a lane each: the second pass over the lengths begins with them.
+// The first 32 sequences, a lane each: cost of a KV head and, summed over all heads, up to and with this one.
+template <class I>
 struct Ahead {
   Seq s;
-  int64_t cost;
+  I per_head, upto;
 };
-// The warp together.
-__device__ __forceinline__ Line make_line(const ChunkParams& p, int lane, bool report, Ahead& a) {
-  a = Ahead{{0, 0, 0}, 0};
-  int64_t sum = 0;
-  int blocks = 0;
-  for (int b = lane; b < p.B; b += 32) {
-    const Seq s = sequence_of(p, b, report);
-    const int64_t c = sequence_cost(p, s);
-    if (b < 32) a = Ahead{s, c};
-    sum += c;
-    blocks += blocks_of(p, s);
-  }
+// The warp together; s0: sequence `lane`.
+template <class I>
+__device__ __forceinline__ Line<I> make_line(const ChunkParams& p, int lane, bool report, const Seq& s0, Ahead<I>& a) {
+  a.s = s0;
+  a.per_head = sequence_cost<I>(p, s0);
+  a.upto = warp_scan<I>(a.per_head * (I)p.Hkv, lane);
+  int blocks = blocks_of(p, s0);
+  Line<I> l;
+  l.total = __shfl_sync(0xffffffffu, a.upto, 31);
+  if (p.B > 32) {
+    I sum = 0;
+#pragma unroll 1
+    for (int b = 32 + lane; b < p.B; b += 32) {
+      const Seq s = sequence_of(p, b, report);
+      sum += sequence_cost<I>(p, s);
+      blocks += blocks_of(p, s);
+    }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    l.total += sum * (I)p.Hkv;
+  }
   blocks = __reduce_add_sync(0xffffffffu, blocks);
-  Line l;
-  l.total = sum * p.Hkv;
   // Parts of kLeastPart or more; short units go one to a CTA, though (parts of kLeastInner or more, so that a part
   // inside a unit still holds a key tile).
-  const int64_t units = min((int64_t)blocks * p.Hkv, l.total / kLeastInner);
-  const int64_t most = max(l.total / kLeastPart, units);
-  l.parts = (int)(most < 1 ? 1 : most < p.ctas ? most : p.ctas);
-  l.each = div64(l.total, l.parts);
-  l.rest = (int)(l.total - l.each * l.parts);
+  const I units = min((I)blocks * (I)p.Hkv, l.total / kLeastInner), most = max(l.total / kLeastPart, units);
+  l.parts = most < 1 ? 1 : most < (I)p.ctas ? (int)most : p.ctas;
+  l.each = l.total / (I)l.parts;
+  l.rest = (int)(l.total - l.each * (I)l.parts);
   return l;
 }
 
 // A position on the line: unit (b, g, rb) and the offset into it.
+template <class I>
 struct Cursor {
   int b, g, rb;
   Seq s;
-  int64_t off;
+  I off;
 };
+__device__ __forceinline__ Seq lane_of(const Seq& s, int l) {
+  return Seq{__shfl_sync(0xffffffffu, s.q0, l), __shfl_sync(0xffffffffu, s.nq, l), __shfl_sync(0xffffffffu, s.nkv, l)};
+}
 // First sequence from b on with new rows (the warp together); b = B when there is none.
-__device__ __forceinline__ void to_sequence(const ChunkParams& p, Cursor& c, int b, int lane) {
-  for (; b < p.B; b += 32) {
-    Seq s = {0, 0, 0};
-    if (b + lane < p.B) s = sequence_of(p, b + lane, false);
-    const unsigned have = __ballot_sync(0xffffffffu, s.nq > 0);
+template <class I>
+__device__ __forceinline__ void to_sequence(const ChunkParams& p, Cursor<I>& c, int b, const Seq& s0, int lane) {
+#pragma unroll 1
+  for (int base = b & ~31; base < p.B; base += 32) {
+    Seq s = s0;
+    if (base > 0) {
+      s = Seq{0, 0, 0};
+      if (base + lane < p.B) s = sequence_of(p, base + lane, false);
+    }
+    const unsigned have = __ballot_sync(0xffffffffu, s.nq > 0 && base + lane >= b);
     if (have) {
       const int l = __ffs(have) - 1;
-      c.b = b + l;
-      c.s.q0 = __shfl_sync(0xffffffffu, s.q0, l);
-      c.s.nq = __shfl_sync(0xffffffffu, s.nq, l);
-      c.s.nkv = __shfl_sync(0xffffffffu, s.nkv, l);
+      c.b = base + l;
+      c.s = lane_of(s, l);
       return;
     }
   }
@@ -248,64 +282,70 @@ __device__ __forceinline__ void to_sequence(const ChunkParams& p, Cursor& c, int
   c.s = Seq{0, 0, 0};
 }
 // The unit that holds position x of the line (x < total).
-__device__ __forceinline__ Cursor seek(const ChunkParams& p, int64_t x, const Ahead& first, int lane) {
-  Cursor c = {p.B, 0, 0, {0, 0, 0}, 0};
+template <class I>
+__device__ __forceinline__ Cursor<I> seek(const ChunkParams& p, I x, const Ahead<I>& first, int lane) {
+  Cursor<I> c = {p.B, 0, 0, {0, 0, 0}, 0};
+#pragma unroll 1
   for (int base = 0; base < p.B; base += 32) {
     Seq s = first.s;
-    int64_t mine = first.cost;
+    I mine = first.per_head, upto = first.upto;
     if (base > 0) {
       s = Seq{0, 0, 0};
       if (base + lane < p.B) s = sequence_of(p, base + lane, false);
-      mine = sequence_cost(p, s);
+      mine = sequence_cost<I>(p, s);
+      upto = warp_scan<I>(mine * (I)p.Hkv, lane);
     }
-    const int64_t inc = warp_scan(mine * p.Hkv, lane);
-    const unsigned beyond = __ballot_sync(0xffffffffu, inc > x);
+    const unsigned beyond = __ballot_sync(0xffffffffu, upto > x);
     if (beyond) {
       const int l = __ffs(beyond) - 1;
-      const int64_t per_head = __shfl_sync(0xffffffffu, mine, l);
-      x -= __shfl_sync(0xffffffffu, inc, l) - per_head * p.Hkv;
+      const I per_head = __shfl_sync(0xffffffffu, mine, l);
+      x -= __shfl_sync(0xffffffffu, upto, l) - per_head * (I)p.Hkv;
       c.b = base + l;
-      c.s.q0 = __shfl_sync(0xffffffffu, s.q0, l);
-      c.s.nq = __shfl_sync(0xffffffffu, s.nq, l);
-      c.s.nkv = __shfl_sync(0xffffffffu, s.nkv, l);
-      c.g = (int)div64(x, per_head);
-      x -= c.g * per_head;
+      c.s = lane_of(s, l);
+      c.g = (int)(x / per_head);
+      x -= (I)c.g * per_head;
       break;
     }
-    x -= __shfl_sync(0xffffffffu, inc, 31);
+    x -= __shfl_sync(0xffffffffu, upto, 31);
   }
   const int nb = blocks_of(p, c.s);
-  for (int base = 0; base < nb; base += 32) {
-    const int64_t mine = base + lane < nb ? cost_of(p, c.s, base + lane) : 0, inc = warp_scan(mine, lane);
-    const unsigned beyond = __ballot_sync(0xffffffffu, inc > x);
+  c.off = x;
+#pragma unroll 1
+  for (int base = 0; base < nb && nb > 1; base += 32) {
+    const I mine = base + lane < nb ? (I)cost_of(p, c.s, base + lane) : 0, upto = warp_scan<I>(mine, lane);
+    const unsigned beyond = __ballot_sync(0xffffffffu, upto > x);
     if (beyond) {
       const int l = __ffs(beyond) - 1;
       c.rb = base + l;
-      c.off = x - __shfl_sync(0xffffffffu, inc - mine, l);
+      c.off = x - __shfl_sync(0xffffffffu, upto - mine, l);
       break;
     }
-    x -= __shfl_sync(0xffffffffu, inc, 31);
+    x -= __shfl_sync(0xffffffffu, upto, 31);
   }
   return c;
 }
 
 // Key tile at which a part that begins `off` into a unit begins.
-__device__ __forceinline__ int tile_at(int64_t off, bool dual, int nt) {
-  const int64_t t = off <= kUnitCost ? 0 : (off - kUnitCost) >> (dual ? 1 : 0);
-  return (int)(t < nt ? t : nt);
+template <class I>
+__device__ __forceinline__ int tile_at(I off, bool dual, int nt) {
+  const I t = off <= kUnitCost ? 0 : (off - kUnitCost) >> (dual ? 1 : 0);
+  return t < (I)nt ? (int)t : nt;
 }
 
 // The record of the cut before CTA cta's part (the warp together).
-__device__ __noinline__ void record_cut(const ChunkParams& p, const Line& line, const Ahead& first, int cta, int lane) {
+template <class I>
+__device__ __forceinline__ void record_cut(const ChunkParams& p, const Seq& s0, int cta, int lane) {
+  Ahead<I> first;
+  const Line<I> line = make_line<I>(p, lane, false, s0, first);
   Cut cut = {0, 0, 0, 0, -1, 0, 0, 0};
-  const int64_t x = line.begin(cta);
+  const I x = line.begin(cta);
   if (cta > 0 && cta < line.parts && x < line.total) {
-    const Cursor c = seek(p, x, first, lane);
-    const int64_t begin = x - c.off;                         // of the unit
+    const Cursor<I> c = seek<I>(p, x, first, lane);
+    const I begin = x - c.off;                               // of the unit
     if (c.off > 0 && line.begin(cta - 1) <= begin) {         // its first cut
       const int nt = tiles_of(p, c.s, c.rb);
       const bool dual = is_dual(p, c.s, c.rb);
-      const int64_t end = begin + kUnitCost + (int64_t)nt * (dual ? 2 : 1);
+      const I end = begin + (I)cost_of(p, c.s, c.rb);
       cut.row0 = c.s.q0 + c.rb * 2 * p.P;
       cut.left = c.s.nq - c.rb * 2 * p.P;
       cut.g = c.g;
@@ -313,8 +353,8 @@ __device__ __noinline__ void record_cut(const ChunkParams& p, const Line& line, 
       cut.owner = cta - 1;
       cut.last = line.owner(end - 1);
       // a CTA between the two has kLeastInner or more of the line, which is a key tile at least
-      cut.own = tile_at(c.off, dual, nt) > 0;
-      cut.end = tile_at(line.begin(cut.last) - begin, dual, nt) < nt;
+      cut.own = tile_at<I>(c.off, dual, nt) > 0;
+      cut.end = tile_at<I>(line.begin(cut.last) - begin, dual, nt) < nt;
     }
   }
   if (lane == 0) p.cuts[cta] = cut;
@@ -327,58 +367,49 @@ struct Part {
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == nt; }
 };
 
-// A CTA's parts in order.  Every warp walks them by itself; its place and the part it is at lie in shared
-// memory: they are looked at once a part, their registers are wanted elsewhere, and local memory is far away
-// (shared memory leaves no L1 to speak of).
-struct Walk {
-  Cursor c;
-  int64_t left;
-  Part u;
-};
-static_assert(sizeof(Walk) <= kWalkBytes, "walk area");
-__device__ __noinline__ void walk_begin(const ChunkParams& p, Walk* at, const Line& line, const Ahead& first, int cta, int lane) {
-  const int64_t x = line.begin(cta), left = line.begin(cta + 1) - x;
-  Cursor c = {p.B, 0, 0, {0, 0, 0}, 0};
-  if (left > 0) c = seek(p, x, first, lane);
-  if (lane == 0) {
-    at->c = c;
-    at->left = left;
+static_assert(sizeof(Part) <= kPartBytes, "ring of parts");
+
+// Rows of queries without a key (the warp together).
+__device__ __forceinline__ void zero_rows(const ChunkParams& p, int row0, int count, int g, int lane) {
+#pragma unroll 1
+  for (int i = lane >> 4; i < count * p.G; i += 2) {
+    const int at = i / p.G;
+    reinterpret_cast<uint4*>(p.out + ((int64_t)(row0 + at) * p.Hq + g * p.G + i - at * p.G) * kD)[lane & 15] = make_uint4(0u, 0u, 0u, 0u);
   }
-  __syncwarp();
 }
-// Moves to the next part, at->u; false: there is none.
-__device__ __noinline__ bool walk_next(const ChunkParams& p, Walk* at, int lane) {
-  Cursor c = at->c;
-  int64_t left = at->left;
-  Part u = {};
-  bool got = false;
-  while (left > 0 && !got) {
+// A CTA's parts in order (the warp together), each given to `put`.  The roles look a key tile ahead, so a part
+// in the ring has one at least: rows without a key are written here.
+template <class I, class Put>
+__device__ __forceinline__ void walk_parts(const ChunkParams& p, const Seq& s0, int cta, int lane, Put put) {
+  Ahead<I> first;
+  const Line<I> line = make_line<I>(p, lane, cta == 0, s0, first);
+  const I x = line.begin(cta);
+  I left = line.begin(cta + 1) - x;
+  if (left == 0) return;
+  Cursor<I> c = seek<I>(p, x, first, lane);
+#pragma unroll 1
+  while (left > 0) {
     const int nt = tiles_of(p, c.s, c.rb);
     const bool dual = is_dual(p, c.s, c.rb);
-    const int64_t cost = kUnitCost + (int64_t)nt * (dual ? 2 : 1);
-    const int64_t take = cost - c.off < left ? cost - c.off : left;
-    u = Part{c.b, c.g, c.rb, c.s.q0, c.s.nq, c.s.nkv, tile_at(c.off, dual, nt), tile_at(c.off + take, dual, nt), nt,
-             dual, c.off == 0};
-    if (c.off + take == cost) u.t1 = nt;
+    const I cost = (I)cost_of(p, c.s, c.rb), take = min(cost - c.off, left);
+    const bool first_part = c.off == 0;
+    const Part u = {c.b, c.g, c.rb, c.s.q0, c.s.nq, c.s.nkv, tile_at<I>(c.off, dual, nt),
+                    c.off + take == cost ? nt : tile_at<I>(c.off + take, dual, nt), nt, dual, first_part};
+    if (nt == 0) {
+      if (first_part) zero_rows(p, c.s.q0 + c.rb * 2 * p.P, min(c.s.nq - c.rb * 2 * p.P, 2 * p.P), c.g, lane);
+    } else if (u.t0 < u.t1 && !put(u)) {
+      return;
+    }
     left -= take;
     c.off = 0;
     if (++c.rb == blocks_of(p, c.s)) {
       c.rb = 0;
       if (++c.g == p.Hkv) {
         c.g = 0;
-        if (left > 0) to_sequence(p, c, c.b + 1, lane);
+        if (left > 0) to_sequence<I>(p, c, c.b + 1, s0, lane);
       }
     }
-    got = u.t0 < u.t1 || (nt == 0 && u.first);
   }
-  __syncwarp();
-  if (lane == 0) {
-    at->c = c;
-    at->left = left;
-    at->u = u;
-  }
-  __syncwarp();
-  return got;
 }
 
 // wait_bar for short waits.  Reading the global timer takes longer than most of them last, so the limit is a
@@ -479,62 +510,75 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + OFF_ABORT);
   auto bar = [&](int i) { return sbase + OFF_BAR + 8u * (uint32_t)i; };
   // Set-up that reads nothing another kernel writes goes before the wait for it.
-  if (tid == 0) {
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(bar(B_K_FULL + s), 2);
-      mbar_init(bar(B_K_EMPTY + s), 1);
-      mbar_init(bar(B_V_FULL + s), 2);
-      mbar_init(bar(B_V_EMPTY + s), 1);
-      mbar_init(bar(B_S_FULL + s), 1);
-      mbar_init(bar(B_P_FULL + s), 4);
-      mbar_init(bar(B_PV_DONE + s), 1);
-      mbar_init(bar(B_ML + s), 4);
-      mbar_init(bar(B_READ + s), 4);
-      mbar_init(bar(B_RAW_FULL + s), 1);
-      mbar_init(bar(B_RAW_EMPTY + s), 2);
-    }
-    mbar_init(bar(B_Q_READY), 8);
-    mbar_init(bar(B_DRAIN), 1);
-    *abort_flag = 0u;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    if (p.box) {
-      prefetch_map(&p.map_k);
-      prefetch_map(&p.map_v);
-    }
-  }
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                  ::"r"(sbase + OFF_TSLOT), "r"(512) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  } else if (warp == 1) {
+    static_assert(B_N == 32, "a lane a barrier");
+    mbar_init(bar(lane), lane >= B_PART_EMPTY && !p.box ? 13 : kArrivals[lane]);   // without boxes warp 1 has nothing to do
+    if (lane == 0) *abort_flag = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (lane == 0 && p.box) {
+      prefetch_map(&p.map_k);
+      prefetch_map(&p.map_v);
+    }
   }
+  pdl_wait();
+  Seq s0 = {0, 0, 0};                                         // of warps 2 and 3: on its way while the others set up
+  if ((warp & ~1) == 2 && lane < p.B) s0 = sequence_of(p, lane, blockIdx.x == 0 && warp == 3);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TSLOT);
-  pdl_wait();
   pdl_launch_dependents();
 
-  Walk* walk = reinterpret_cast<Walk*>(smem + OFF_WALK + warp * kWalkBytes);
-  if (warp != 3) {
-    Ahead first;
-    const Line line = make_line(p, lane, blockIdx.x == 0 && warp == 0, first);
-    if (warp != 2) {
-      walk_begin(p, walk, line, first, blockIdx.x, lane);
-    } else {
-      record_cut(p, line, first, blockIdx.x, lane);
-    }
-  }
+  // The CTA's parts come from warp 3 through a ring; a part with nt < 0 is the end.
+  Part* const ring = reinterpret_cast<Part*>(smem + OFF_PARTS);
+  uint32_t parts = 0;                                         // taken (by warp 3: written)
+  auto next_part = [&]() {                                    // false: none left; otherwise the part is ring[parts % kRing]
+    return warp_wait(bar(B_PART_FULL) + 8u * (parts % kRing), (parts / kRing) & 1u, lane, abort_flag, p.err) &&
+           ring[parts % kRing].nt >= 0;
+  };
+  auto part_read = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(B_PART_EMPTY) + 8u * (parts % kRing));
+    ++parts;
+  };
 
-  if (warp == 0) {
+  if (warp == 3) {
+    auto put = [&](const Part& u) {
+      if (!warp_wait(bar(B_PART_EMPTY) + 8u * (parts % kRing), ((parts / kRing) & 1u) ^ 1u, lane, abort_flag, p.err)) return false;
+      if (lane == 0) {
+        ring[parts % kRing] = u;
+        mbar_arrive(bar(B_PART_FULL) + 8u * (parts % kRing));
+      }
+      ++parts;
+      return true;
+    };
+    if (p.narrow)
+      walk_parts<uint32_t>(p, s0, blockIdx.x, lane, put);
+    else
+      walk_parts<int64_t>(p, s0, blockIdx.x, lane, put);
+    Part end = {};
+    end.nt = -1;
+    put(end);
+  } else if (warp == 2) {
+    if (p.narrow)
+      record_cut<uint32_t>(p, s0, blockIdx.x, lane);
+    else
+      record_cut<int64_t>(p, s0, blockIdx.x, lane);
+  } else if (warp == 0) {
     // ------------------------------------------------------------ MMA issuer
     const uint32_t id_qk = idesc_f16(kRows, kKeys, false, false);
     const uint32_t id_pv = idesc_f16(kRows, kD, false, true);
     uint32_t kc = 0, done0 = 0, done1 = 0, units = 0;         // key tiles, steps of each buffer, units so far
     bool ok = true;
     const uint32_t lead = elect_one();
-    while (ok && walk_next(p, walk, lane)) {
-      struct { int t0, t1, nt; bool dual; } u = {walk->u.t0, walk->u.t1, walk->u.nt, walk->u.dual};
-      if (u.nt == 0) continue;
+    while (ok && next_part()) {
+      const Part& now = ring[parts % kRing];
+      const struct { int t0, t1; bool dual; } u = {now.t0, now.t1, now.dual};
+      part_read();
       const int nk = u.t1 - u.t0, steps = u.dual ? 2 * nk : nk;
       ok = warp_all(wait_long(bar(B_Q_READY), units & 1u, abort_flag, p.err));
       // Step t: buffer t & 1, key tile t (or t / 2 with two row tiles).  P.V of step t, then Q.K^T of step t + 2.
@@ -606,13 +650,14 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
       int pg = 0, at = 0, g_at = 0;                          // the tile looked up
       auto look_up = [&]() {                                 // false: nothing left
         while (j >= t_end) {
-          if (!walk_next(p, walk, lane)) return false;
-          const Part& u = walk->u;
+          if (!next_part()) return false;
+          const Part& u = ring[parts % kRing];
           j = u.t0;
           t_end = u.t1;
           b = u.b;
           g = u.g;
           n_keys = p.causal ? u.nkv - u.nq + min(u.nq, (u.rb + 1) * 2 * p.P) : u.nkv;
+          part_read();
         }
         const uint32_t t = (uint32_t)min(j * kKeys + i * p.box, (n_keys - 1) & ~(p.box - 1));
         if (p.block_table) {
@@ -673,13 +718,14 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
     int mine[2] = {0, 0}, head = 0, head_next = 0;                   // the tile looked up: this lane's row, offset of the KV head
     auto look_up = [&]() {                                   // false: nothing left
       while (j >= t_end) {
-        if (!walk_next(p, walk, lane)) return false;
-        const Part& u = walk->u;
+        if (!next_part()) return false;
+        const Part& u = ring[parts % kRing];
         j = u.t0;
         t_end = u.t1;
         b = u.b;
         g = u.g;
         n_keys = p.causal ? u.nkv - u.nq + min(u.nq, (u.rb + 1) * 2 * p.P) : u.nkv;
+        part_read();
       }
       if (!p.box) {
         head_next = g * kD;
@@ -754,22 +800,15 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
     };
     uint32_t done = 0, done_other = 0, merges = 0;          // steps of this buffer and the other, merged units
     bool ok = true;
-    while (ok && walk_next(p, walk, lane)) {
-      const Part u = walk->u;
+    while (ok && next_part()) {
+      const Part u = ring[parts % kRing];
+      part_read();
       const int nk = u.t1 - u.t0, steps = u.dual ? 2 * nk : nk, mine = (steps + 1 - x) / 2;
       const int pl = r / p.G, hh = u.g * p.G + r - pl * p.G;  // position in the row tile, query head
       const int i = u.rb * 2 * p.P + (u.dual ? x * p.P : 0) + pl;
       const bool active = pl < p.P && i < u.nq;
       const bool warp_active = __any_sync(0xffffffffu, active);
       const int64_t orow = (int64_t)(u.q0 + (active ? i : 0)) * p.Hq + hh;   // row of q and out
-      if (u.nt == 0) {                                        // no key at all: zero rows
-        if (active && (u.dual || x == 0)) {
-          uint4* o = reinterpret_cast<uint4*>(p.out + orow * kD);
-#pragma unroll
-          for (int c8 = 0; c8 < kD / 8; ++c8) o[c8] = make_uint4(0u, 0u, 0u, 0u);
-        }
-        continue;                                             // the MMA warp passes over it as well
-      }
       // The row's query codes as fp16 into the row tile's K-major A operand (chunk of 8 d at
       // (d / 8) * 2048 + row * 16).
       if (u.dual || x == 0) {
@@ -1066,6 +1105,8 @@ int chunk_attn(ChunkParams& p, int D, float softmax_scale, void* workspace, size
   if ((p.block_table ? (int64_t)p.num_pages * p.page_size : (int64_t)p.B * p.T) >= ((int64_t)1 << 31)) return FA3_ERANGE;
   if (!aligned16(p.q) || !aligned16(p.k) || !aligned16(p.v) || !aligned16(p.out)) return FA3_ERANGE;
   p.P = kRows / p.G;
+  p.div_2p = make_divu32((uint32_t)(2 * p.P));
+  p.narrow = ((double)p.n / (2 * p.P) + p.B) * p.Hkv * (kUnitCost + 2.0 * (p.T / kKeys + 1.0)) < 16777216.0;
   p.sm_log2 = softmax_scale * 1.4426950408889634f;
   int sms = 0;
   const int st = check_device(&sms);

@@ -231,6 +231,39 @@ def test_cross_many_empty_between_full():
     _check(F, c, "many empty states")
 
 
+def test_cross_long_runs_of_empty_states():
+    # dozens of units without keys in one CTA's share, behind units with several key tiles
+    F = fa3()
+    rng = np.random.default_rng(19)
+    lens = np.zeros(2000, int)
+    lens[rng.choice(2000, 60, replace=False)] = rng.integers(1, 700, 60)
+    c = _case(rng, 8, 2, [1] * 2000, list(lens), None)
+    _check(F, c, "runs of empty states")
+
+
+def test_more_sequences_than_a_warp_has_lanes():
+    F = fa3()
+    rng = np.random.default_rng(20)
+    rows = list(rng.choice([0, 1, 1, 1, 3, 50], 1300))
+    c = _case(rng, 8, 2, rows, [r + int(x) for r, x in zip(rows, rng.integers(0, 200, 1300))], 16)
+    _check(F, c, "1300 sequences")
+
+
+def test_table_of_a_very_long_context():
+    # a table wide enough that the plan is made in 64 bits: the same cuts, the same bits
+    F = fa3()
+    rng = np.random.default_rng(21)
+    c = _case(rng, 16, 2, [1, 70], [3000, 1900], 256)
+    want = _run(F, c)
+    _gate(want, _ref(c), c, "narrow table")
+    wide = torch.full((2, 1 << 20), -1, dtype=torch.int32, device="cuda")
+    wide[:, :c["table"].shape[1]] = _t(c["table"])
+    out = torch.full(c["q"].shape, KEEP, dtype=torch.bfloat16, device="cuda")
+    a = [_t(c[k]) for k in ("q", "k", "v", "qs", "ks", "vs", "q_start", "lens")]
+    F.prefill_attn_gqa_paged(*a, wide, SM, out=out)
+    assert np.array_equal(out.float().cpu().numpy(), want)
+
+
 def test_agrees_with_the_decode_and_prefill_calls():
     # the same cache through the calls that were there: all within the gate of one oracle
     F = fa3()
