@@ -443,7 +443,8 @@ int fa3_norm_rope(const uint16_t* q, const uint16_t* k, const uint16_t* q_weight
  * q_start  int32 [B+1], non-decreasing, within [0, n];  kv_lens  int32 [B], n_b <=
  *          kv_lens[b] <= max_pages * page_size; otherwise FA3_DEVERR_LENS is set
  *          and the sequence is skipped.  Rows outside [q_start[0], q_start[B])
- *          are not read and their q_out is left as it was.
+ *          belong to no sequence: their values do not matter, and their q_out is
+ *          left as it was.
  * A position past the table sets FA3_DEVERR_POS and skips the row; a block-table
  * entry outside the pool sets FA3_DEVERR_PAGE and skips its k and v (q_out is
  * written).  Supported: any page_size >= 1; q_out, k_cache, v_cache 8-byte aligned. */
@@ -469,8 +470,9 @@ int fa3_rope_append_gqa_paged(const uint16_t* q, const uint16_t* k, const uint16
  *          (FA3_DEVERR_LENS) are left as they were.
  * Supported: D = 128, Hq / Hkv <= 128; q, k, v, out 16-byte aligned.
  * workspace  fa3_chunk_workspace_size(n, B, Hq, Hkv, D) bytes, 16-byte aligned
- *          (partial results of row blocks whose keys are shared out); its
- *          contents need no initialisation.
+ *          (partial results of row blocks whose keys are shared out, 20 or 40 MB);
+ *          its contents need no initialisation.  Calls that may run at the same
+ *          time need one each.
  * ------------------------------------------------------------------------ */
 size_t fa3_chunk_workspace_size(int n, int B, int Hq, int Hkv, int D);
 
@@ -489,8 +491,8 @@ int fa3_prefill_attn_gqa_paged(const int8_t* q, const int8_t* k, const int8_t* v
 /* Cross attention to an encoder's states of another length: every row of sequence b
  * attends to all of t < enc_lens[b], 0 <= enc_lens[b] <= T (else FA3_DEVERR_LENS);
  * no states at all gives zero rows.
- * k, v     int8 [B][T][Hkv][D] (rows t >= enc_lens[b] are not read), as
- *          fa3_quantize_append writes them; B * T < 2^31. */
+ * k, v     int8 [B][T][Hkv][D], as fa3_quantize_append writes them; what rows
+ *          t >= enc_lens[b] hold does not matter; B * T < 2^31. */
 int fa3_cross_attn_gqa(const int8_t* q, const int8_t* k, const int8_t* v,
                        const float* q_scale, const float* k_scale, const float* v_scale,
                        const int32_t* q_start, const int32_t* enc_lens, uint16_t* out,

@@ -22,15 +22,33 @@
 // end.  A cut unit's parts leave unnormalised O, maximum and sum in the workspace, and
 // chunk_combine_kernel merges them, so one long sequence and a ragged batch both fill the GPU.
 //
-// Roles in the CTA (512 threads): warp 0 issues the MMAs; warp 1 looks pages up in the block
-// table and brings int8 K and V tiles to shared memory by TMA; warps 12-15 write them as fp16
-// into one of two stages; warps 4-7 and 8-11 (a row a lane) run the softmax of buffers 0 and 1.  int8 codes are exact in fp16 and a 128-term sum of their products
-// stays below 2^24, so kind::f16 MMAs with fp32 accumulation give the exact integer
-// score (sm_103a has no integer tcgen05 kind).  P (fp16, relative to a lazily moved row
-// maximum) is written over its scores in TMEM and is the A operand of P.V; the row sum is
-// float32 over the unrounded weights.  TMEM: O_0, O_1, S_0, S_1, 128 columns each.
-// Every wait is bounded; on time-out the kernel sets FA3_DEVERR_TIMEOUT, drains its
-// MMAs, frees its TMEM and returns.
+// Roles in the CTA (512 threads).  Warp 0 issues the MMAs.  Warp 1 looks pages up in the
+// block table and brings int8 K and V tiles to shared memory by TMA.  Warp 2 records the
+// cut before the CTA's part for the combine kernel.  Warp 3 finds the CTA's parts of the
+// line and hands them to the others through a ring.  Warps 4-7 and 8-11 (a row a lane)
+// run the softmax of buffers 0 and 1.  Warps 12, 13 (K) and 14, 15 (V) write the int8
+// tiles as fp16 into one of two stages.
+//
+// Numbers.  int8 codes are exact in fp16 and a 128-term sum of their products stays
+// below 2^24, so kind::f16 MMAs with float32 accumulation give the exact integer score
+// (the integer tensor rate of sm_103a is far below it).  P is rounded to fp16 relative to a lazily
+// moved row maximum (off by 2^-11 of a weight at most, and the result is rounded to bf16,
+// 2^-8); the row sum is float32 over the unrounded weights, and O, partial results and
+// their merging are float32.  P is written over its scores in TMEM and is the A operand of
+// P.V.  TMEM: O_0, O_1, S_0, S_1, 128 columns each.
+//
+// What bounds it (64 query and 8 KV heads, one GB300).  4096 new rows on a context of
+// 8192: 777 us, 1060 TFLOP/s; a step takes 2250 cycles, of which the tensor pipe works
+// about 1200: the chain scores, softmax, P.V, scores of each of the two buffers, a
+// barrier at every arrow, and shared memory, which moves 640 KB a key tile (int8 tile in
+// and out, fp16 tile in, Q, K and V into the MMAs).  16 one-token rows of 4096 keys: 52
+// us, 2.6 TB/s; a key tile takes 2600 cycles, the way of an int8 tile from HBM to fp16,
+// one tile of K and one of V in flight because 224 KB of shared memory are full.  About
+// 8 us of a small call are the launch, the plan (2.5 us), the first tiles' way (3 us)
+// and the combine kernel (3 us).
+//
+// Every wait is bounded; on time-out the kernel sets FA3_DEVERR_TIMEOUT, waits for its
+// copies and MMAs, frees its TMEM and returns.
 #include "fa3_common.cuh"
 #include "fa3_tc.cuh"
 
@@ -82,9 +100,12 @@ constexpr uint32_t OFF_ABORT = OFF_TSLOT + 4;
 constexpr uint32_t SMEM_CHUNK = OFF_ABORT + 4 + 1024;      // + alignment slack
 static_assert(SMEM_CHUNK <= 232448, "shared memory");
 
-// A unit's cost beside its steps (its query rows, pipeline fill and epilogue), in steps, and
-// the least part of the line a CTA takes.
+// A unit's cost beside its steps (its query rows, pipeline fill and epilogue), in steps: fitted over the CTAs of ragged
+// batches it is about 7000 cycles against 1950 to 2200 a step (counted as two steps, a batch of eight sequences of up
+// to 512 new rows took 113 us, as three or four 101).  And the least part of the line a CTA takes, and the
+// least where short units go one to a CTA (16 one-token units of 128 keys: 17 us in parts of kLeastPart, 13 us).
 constexpr int kUnitCost = 3, kLeastPart = 8, kLeastInner = 4;
+static_assert(kLeastInner > kUnitCost, "a part inside a unit holds a key tile");
 
 // What the combine kernel has to know of the cut before a CTA's part: nothing (owner < 0) unless it is the
 // first cut of its unit.
@@ -106,7 +127,7 @@ struct ChunkParams {
   uint16_t* out;                // bf16 [n][Hq][128]
   float4* part_o;               // [2 * CTAs][32][rows_max]: O of a cut unit's part, column group by row
   float2* part_ml;              // [2 * CTAs][rows_max]
-  struct Cut* cuts;             // [CTAs]
+  Cut* cuts;                    // [CTAs]
   int32_t* err;
   int n, B, T, Hq, Hkv, G, P, causal, ctas, rows_max;
   int page_size, max_pages, num_pages;
@@ -117,10 +138,10 @@ struct ChunkParams {
   CUtensorMap map_k, map_v;     // [cache rows][Hkv * 128] in boxes of [box][128]
 };
 
-// Keys come in boxes of consecutive cache rows, the largest power of two that divides the page size
-// (and the tile), from 8 rows on.  A box of 8 rows or more keeps the TMA unit fast enough (one row a copy took 31
-// cycles a row, 126 us for the 16 x 4096-key decode against 67 through registers); smaller powers go through
-// registers.
+// Keys come in boxes of consecutive cache rows, the largest power of two that divides the page size (and the
+// tile), from 8 rows on: a tile's 16 boxes are then a half warp's.  Other page sizes go through registers.  The TMA unit
+// takes some 31 cycles a box: with a row a box, 16 one-token rows of 4096 keys took 126 us, through registers 67
+// and in boxes of 64 rows 63 at that time; 2 x 16 boxes of 8 rows hide behind a tile's 2600 cycles.
 constexpr int kLeastBox = 8;
 
 // ------------------------------------------------------------------ the line of steps
@@ -154,7 +175,8 @@ __device__ __forceinline__ int cost_of(const ChunkParams& p, const Seq& s, int r
 }
 
 // The line's numbers are I: uint32_t where they fit 24 bits (the host's bound), int64_t otherwise.  The plan is on
-// every call's way, and 64-bit divisions and scans take several times as long.
+// every call's way, and 64-bit divisions and scans take several times as long (16 sequences: 6600 cycles with int64_t,
+// 3200 with uint32_t).
 
 // Sum over r < n of floor((at + r step) / mod): whole multiples come out, then the roles of step and mod change
 // (the lattice points under a line, counted along the other axis).
@@ -1021,7 +1043,9 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
 }
 
 // Merges the parts of cut units.  Block (c - 1, rows): the unit whose first cut lies before CTA c's part; rows
-// 32 blockIdx.y .. + 31.  A lane has a row, a warp 16 columns.
+// 32 blockIdx.y .. + 31.  A lane has a row, a warp 16 columns.  It is launched while the main kernel runs and takes
+// about 3 us behind its end, for a few MB at most; the cuts come from the main kernel, because finding them
+// here again took 2 us more.
 __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constant__ ChunkParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int prow = blockIdx.y * 32 + lane;                   // row tile x 128 + row

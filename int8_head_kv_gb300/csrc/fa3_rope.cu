@@ -14,7 +14,8 @@
 // rot/2 + 4i .. rot/2 + 4i+3 (or 8i .. 8i+7 for neighbouring pairs and for values that
 // pass), which needs no exchange between lanes, reads each table value once and lets
 // the floating-point call work in place.  A row takes 8, 16 or 32 lanes (D up to 256),
-// a warp 4, 2 or 1 rows at a time.
+// a warp 4, 2 or 1 rows at a time.  Numbers are float32 throughout and rounded once, to
+// the output's type or to a code.
 #include "fa3_common.cuh"
 
 #include <cuda_bf16.h>
@@ -205,6 +206,11 @@ __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* dst, const 
 // Tasks of a token: chunks of per_chunk heads that lie within q or within k, so that
 // pointers, strides and weights are the warp's.  Two passes (32 / LANES rows each) are
 // loaded while the two before them are worked on.
+//
+// Bounded by HBM where there is enough of it: 8192 tokens of 64 + 8 heads of 128 (302 MB
+// in and out) take 53 us, 5.8 TB/s of the 6.7 that a copy reaches.  Packed arithmetic on
+// pairs of values and 64 registers (8 blocks an SM) brought that from 68; up to some
+// hundred tokens it is the launch, 2 to 5 us.
 template <typename OUT, int LANES, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads, 8) norm_rope_kernel(const NormRopeArgs a) {
   constexpr int rows = 32 / LANES;
@@ -483,6 +489,15 @@ __device__ __forceinline__ Place place_row(const RopeAppendArgs& a, int row, int
   return pl;
 }
 
+// The same walk over chunks of heads of q, k or v, of which each row ends as codes: q's
+// in q_out, k's and v's in the token's place in the pages.
+//
+// Bounded by instructions, about 190 for the 256 values of a warp's pass (a code and the
+// test of its neighbourhood take six a value): 3080 tokens of 64 + 8 + 8 heads of 128
+// (95 MB) take 37 us, 2.6 TB/s; half of it is HBM's.  A token's look-ups (sequence,
+// lengths, page) are loads that wait for one another, so the first rows are asked for
+// before them: 16 one-token sequences take 4 us.  Left to 116 registers: with 96 (5
+// blocks an SM) or 80 (6) the rows spill, 43 and 50 us.
 template <int LANES, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeAppendArgs a) {
   constexpr int rows = 32 / LANES;
@@ -644,8 +659,10 @@ int rot_args(const float* cos_sin, int table_len, int rot_dim, int interleaved, 
 
 int lanes_per_row(int D) { return D <= 64 ? 8 : D <= 128 ? 16 : 32; }
 
-// Head rows a warp takes of one token: enough warps to fill the GPU come first, then
-// longer tasks, which read a token's table row and place once for more heads.
+// Head rows a warp takes of one token: enough warps to fill the GPU come first (24 an SM),
+// then longer tasks, which read a token's table row and place once for more heads.  With
+// 64 warps an SM first, 999 tokens of 20 + 5 heads of 80 took 6.9 us instead of 4.8, and a
+// ragged append of as many heads 13 instead of 10; large calls are the same with either.
 int heads_per_task(int64_t tokens, int heads, int rows, int sms) {
   const int64_t passes = tokens * ((heads + rows - 1) / rows);
   const int64_t per = std::max<int64_t>(1, std::min<int64_t>(8, passes / ((int64_t)sms * 24)));
