@@ -39,9 +39,9 @@
 //
 // What bounds it (64 query and 8 KV heads, one GB300).  4096 new rows on a context of
 // 8192: 777 us, 1060 TFLOP/s; a step takes 2250 cycles, of which the tensor pipe works
-// about 1200: the chain scores, softmax, P.V, scores of each of the two buffers, a
-// barrier at every arrow, and shared memory, which moves 640 KB a key tile (int8 tile in
-// and out, fp16 tile in, Q, K and V into the MMAs).  16 one-token rows of 4096 keys: 52
+// 45 %: the chain scores, softmax, P.V, scores of each of the two buffers, a
+// barrier at every arrow, and shared memory, which moves some 320 KB a key tile (int8 tile
+// in and out, fp16 tile in, Q, K and V into the MMAs: 2500 cycles at 128 bytes each).  16 one-token rows of 4096 keys: 52
 // us, 2.6 TB/s; a key tile takes 2600 cycles, the way of an int8 tile from HBM to fp16,
 // one tile of K and one of V in flight because 224 KB of shared memory are full.  About
 // 8 us of a small call are the launch, the plan (2.5 us), the first tiles' way (3 us)
