@@ -467,8 +467,10 @@ int fa3_rope_append_gqa_paged(const uint16_t* q, const uint16_t* k, const uint16
  *   out[row, h, :] = bf16( v_scale[g] * sum_t softmax(s)_t * v[t, g, :] )
  * q        int8 [n][Hq][D];  out  bf16 [n][Hq][D].  Rows outside
  *          [q_start[0], q_start[B]) and those of a sequence with bad lengths
- *          (FA3_DEVERR_LENS) are left as they were.
- * Supported: D = 128, Hq / Hkv <= 128; q, k, v, out 16-byte aligned.
+ *          (FA3_DEVERR_LENS) are left as they were; all are, if q_start falls
+ *          and rises again so that sequences share rows.
+ * scales   finite; q_scale, k_scale >= 0 (a softmax scale of 0 or below is refused).
+ * Supported: D = 128, Hq / Hkv <= 128, n < 2^27 - 1; q, k, v, out 16-byte aligned.
  * workspace  fa3_chunk_workspace_size(n, B, Hq, Hkv, D) bytes, 16-byte aligned
  *          (partial results of row blocks whose keys are shared out, 20 or 40 MB);
  *          its contents need no initialisation.  Calls that may run at the same

@@ -248,6 +248,7 @@ __device__ __forceinline__ Line<I> make_line(const ChunkParams& p, int lane, boo
   a.per_head = sequence_cost<I>(p, s0);
   a.upto = warp_scan<I>(a.per_head * (I)p.Hkv, lane);
   int blocks = blocks_of(p, s0);
+  int64_t rows = s0.nq;
   Line<I> l;
   l.total = __shfl_sync(0xffffffffu, a.upto, 31);
   if (p.B > 32) {
@@ -257,12 +258,21 @@ __device__ __forceinline__ Line<I> make_line(const ChunkParams& p, int lane, boo
       const Seq s = sequence_of(p, b, report);
       sum += sequence_cost<I>(p, s);
       blocks += blocks_of(p, s);
+      rows += s.nq;
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     l.total += sum * (I)p.Hkv;
   }
   blocks = __reduce_add_sync(0xffffffffu, blocks);
+  // More rows than there are (a q_start that falls and rises again): the bounds of I do not hold, there is no plan.
+  // A lane's rows are counted up to 2^27 - 1, so that 32 of them fit 32 bits and one lane's are beyond any n < 2^27.
+  const uint32_t most_rows = (1u << 27) - 1, all = __reduce_add_sync(0xffffffffu, (uint32_t)min(rows, (int64_t)most_rows));
+  if (all > (uint32_t)p.n) {
+    if (report && lane == 0) set_dev_err(p.err, FA3_DEVERR_LENS);
+    l.total = 0;
+    blocks = 0;
+  }
   // Parts of kLeastPart or more; short units go one to a CTA, though (parts of kLeastInner or more, so that a part
   // inside a unit still holds a key tile).
   const I units = min((I)blocks * (I)p.Hkv, l.total / kLeastInner), most = max(l.total / kLeastPart, units);
@@ -435,12 +445,14 @@ __device__ __forceinline__ void walk_parts(const ChunkParams& p, const Seq& s0, 
 }
 
 // wait_bar for short waits.  Reading the global timer takes longer than most of them last, so the limit is a
-// number of tests (2^25, about a second: a test suspends the thread for a while by itself), and the abort flag is
-// looked at every 256.
-constexpr uint32_t kMostTests = 1u << 25;
+// number of tests: one that fails suspends the thread for 3.94 us, 2^18 of them are a second.  The abort flag is
+// looked at every 256.  A wait for a part of the ring may last as long as a unit of the longest context takes (0.3 s
+// for 16 million keys), and has four seconds.
+constexpr uint32_t kMostTests = 1u << 18, kMostTestsPart = 1u << 20;
+template <uint32_t MOST = kMostTests>
 __device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, int32_t* err) {
 #pragma unroll 1
-  for (uint32_t i = 0; i < kMostTests; ++i) {
+  for (uint32_t i = 0; i < MOST; ++i) {
     if (mbar_try(bar, parity)) return true;
     if ((i & 255u) == 255u && *abort_flag) return false;
   }
@@ -449,9 +461,10 @@ __device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, volatil
   return false;
 }
 // The same for a warp, whose lanes have to agree.
+template <uint32_t MOST = kMostTests>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int lane, volatile uint32_t* abort_flag,
                                           int32_t* err) {
-  return warp_all(wait_long(bar, parity, abort_flag, err));
+  return warp_all(wait_long<MOST>(bar, parity, abort_flag, err));
 }
 
 // The wait for this thread's TMEM loads, which also orders the uses of v behind it.
@@ -559,7 +572,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
   Part* const ring = reinterpret_cast<Part*>(smem + OFF_PARTS);
   uint32_t parts = 0;                                         // taken (by warp 3: written)
   auto next_part = [&]() {                                    // false: none left; otherwise the part is ring[parts % kRing]
-    return warp_wait(bar(B_PART_FULL) + 8u * (parts % kRing), (parts / kRing) & 1u, lane, abort_flag, p.err) &&
+    return warp_wait<kMostTestsPart>(bar(B_PART_FULL) + 8u * (parts % kRing), (parts / kRing) & 1u, lane, abort_flag,
+                                     p.err) &&
            ring[parts % kRing].nt >= 0;
   };
   auto part_read = [&]() {
@@ -570,7 +584,9 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
 
   if (warp == 3) {
     auto put = [&](const Part& u) {
-      if (!warp_wait(bar(B_PART_EMPTY) + 8u * (parts % kRing), ((parts / kRing) & 1u) ^ 1u, lane, abort_flag, p.err)) return false;
+      if (!warp_wait<kMostTestsPart>(bar(B_PART_EMPTY) + 8u * (parts % kRing), ((parts / kRing) & 1u) ^ 1u, lane,
+                                     abort_flag, p.err))
+        return false;
       if (lane == 0) {
         ring[parts % kRing] = u;
         mbar_arrive(bar(B_PART_FULL) + 8u * (parts % kRing));
@@ -1125,7 +1141,7 @@ int chunk_attn(ChunkParams& p, int D, float softmax_scale, void* workspace, size
   if (p.n <= 0 || p.B <= 0 || p.T <= 0 || p.Hq <= 0 || p.Hkv <= 0 || D <= 0 || p.Hq % p.Hkv != 0) return FA3_EINVAL;
   if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale)) return FA3_EINVAL;
   p.G = p.Hq / p.Hkv;
-  if (D != kD || p.G > kRows || p.Hkv > 65535) return FA3_ERANGE;
+  if (D != kD || p.G > kRows || p.Hkv > 65535 || p.n >= (1 << 27) - 1) return FA3_ERANGE;
   if ((p.block_table ? (int64_t)p.num_pages * p.page_size : (int64_t)p.B * p.T) >= ((int64_t)1 << 31)) return FA3_ERANGE;
   if (!aligned16(p.q) || !aligned16(p.k) || !aligned16(p.v) || !aligned16(p.out)) return FA3_ERANGE;
   p.P = kRows / p.G;

@@ -421,3 +421,67 @@ def test_a_layer_as_it_is_served():
     ref = O.packed_attention(rq, *kv, *sc, q_start, enc, SM, False, np.zeros(rq.shape))
     case = dict(q=rq, k=ck.cpu().numpy(), qs=sc[0], ks=sc[1], vs=sc[2], lens=enc)
     _gate(out.float().cpu().numpy(), ref, case, "cross step")
+
+
+def test_rows_shared_by_a_falling_q_start():
+    # every second sequence would have all rows: more rows than there are, so no plan and no row written
+    F = fa3()
+    for B in (4, 80):
+        c = _case(np.random.default_rng(22), 8, 2, [30] + [0] * (B - 1), [50] * B, 16)
+        c["q_start"] = np.asarray(([0, 30] * B)[:B + 1], np.int32)
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = _run(F, c, err)
+        assert int(err.item()) == F.FA3_DEVERR_LENS
+        assert np.all(got == KEEP)
+
+
+def test_two_calls_in_one_graph():
+    # their workspaces come from one pool, one after the other
+    F = fa3()
+    rng = np.random.default_rng(23)
+    c, d = _case(rng, 16, 2, [1, 20], [1800, 400], 64), _case(rng, 8, 4, [5, 1], [900, 2500], None)
+    want = [_run(F, c), _run(F, d)]
+    a, b = ([_t(x[k]) for k in ("q", "k", "v", "qs", "ks", "vs", "q_start", "lens")] for x in (c, d))
+    table = _t(c["table"])
+    outs = [torch.full(x["q"].shape, KEEP, dtype=torch.bfloat16, device="cuda") for x in (c, d)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        F.prefill_attn_gqa_paged(*a, table, SM, out=outs[0])
+        F.cross_attn_gqa(*b, SM, out=outs[1])
+    for _ in range(3):
+        for o in outs:
+            o.fill_(KEEP)
+        graph.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert np.array_equal(o.float().cpu().numpy(), w)
+
+
+def test_calls_that_are_refused():
+    F = fa3()
+    c = _case(np.random.default_rng(24), 8, 2, [3, 2], [20, 30], 16, behind=0)
+    q, k, v, qs, ks, vs, start, lens = (_t(c[x]) for x in ("q", "k", "v", "qs", "ks", "vs", "q_start", "lens"))
+    good = dict(q=q, k=k, v=v, q_scale=qs, k_scale=ks, v_scale=vs, q_start=start, kv_lens=lens, block_table=_t(c["table"]),
+                softmax_scale=SM)
+    F.prefill_attn_gqa_paged(**good)
+    need = F.chunk_workspace_size(5, 2, 8, 2, 128)
+    bads = [(dict(q=q.float()), TypeError), (dict(q=q[:, :, :64]), ValueError), (dict(q=q[:, :7].contiguous(), q_scale=qs[:7]), F.FA3Error),
+            (dict(q=q[:, ::2]), ValueError), (dict(v=v[:1]), ValueError), (dict(k=k.cpu()), TypeError), (dict(q_scale=qs[:2]), ValueError),
+            (dict(k_scale=ks.double()), TypeError), (dict(q_start=start[:2]), ValueError), (dict(kv_lens=lens[:0]), ValueError),
+            (dict(block_table=_t(c["table"])[:1]), ValueError), (dict(softmax_scale=0.0), F.FA3Error),
+            (dict(softmax_scale=float("nan")), F.FA3Error), (dict(out=torch.zeros(5, 8, 128, device="cuda")), TypeError),
+            (dict(out=torch.zeros(4, 8, 128, dtype=torch.bfloat16, device="cuda")), ValueError),
+            (dict(workspace=torch.zeros(need - 1, dtype=torch.uint8, device="cuda")), F.FA3Error),
+            (dict(workspace=torch.zeros(need + 1, dtype=torch.uint8, device="cuda")[1:]), F.FA3Error),
+            (dict(workspace=torch.zeros(need, dtype=torch.uint8)), ValueError)]
+    for bad, error in bads:
+        with pytest.raises(error):
+            F.prefill_attn_gqa_paged(**{**good, **bad})
+    half = dict(k=k[..., :64].contiguous(), v=v[..., :64].contiguous(), q=q[..., :64].contiguous())
+    with pytest.raises(F.FA3Error):                                           # head size 128 alone
+        F.prefill_attn_gqa_paged(**{**good, **half})
+    e = torch.zeros(2, 7, 2, 128, dtype=torch.int8, device="cuda")
+    F.cross_attn_gqa(q, e, e, qs, ks, vs, start, lens * 0, SM)
+    for k2, v2 in ((e[:1], e[:1]), (e, e[:, :6]), (e[:, :0], e[:, :0])):
+        with pytest.raises((ValueError, F.FA3Error)):
+            F.cross_attn_gqa(q, k2, v2, qs, ks, vs, start, lens * 0, SM)

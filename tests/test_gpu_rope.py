@@ -316,3 +316,84 @@ def test_append_past_32_bit_offsets():
     for p in (kp, vp):
         assert np.array_equal(p[num - 1, page - 2:].cpu().numpy(), ref)
         assert not p[:num - 1].any() and not p[num - 1, :page - 2].any()
+
+
+def test_streams_and_graphs():
+    # a side stream, and captured calls replayed on changed contents: the codes of the plain calls
+    F = fa3()
+    rng = np.random.default_rng(30)
+    cs = [_append_case(rng, 8, 2, 128, 128, 16, [1, 20, 3], kv, True) for kv in ([40, 33, 3], [25, 60, 60])]
+    cs[1]["table"] = cs[0]["table"] = np.arange(3 * 6, dtype=np.int32).reshape(3, 6)
+    cs[1]["cs"] = cs[0]["cs"] = _table(64, 128)
+    cs[1]["pools"] = [np.zeros((24, 16, 2, 128), np.int8) for _ in range(2)]
+    cs[0]["pools"] = cs[1]["pools"]
+    want = [_ref_append(c, False) for c in cs]
+    names = ("x", "q_start", "kv_lens", "sc")
+    buf = {n: (bf16_dev if n == "x" else _t)(cs[0][n]) for n in names}
+    table, tab = _t(cs[0]["table"]), _t(cs[0]["cs"])
+    pools = [_t(p) for p in cs[0]["pools"]]
+    w = [bf16_dev(a) for a in cs[0]["w"]]
+    cs[1]["w"] = cs[0]["w"]
+    want[1] = _ref_append(cs[1], False)
+    q_out = torch.full((cs[0]["n"], 8, 128), 77, dtype=torch.int8, device="cuda")
+    rows = torch.zeros(cs[0]["n"], 8, 128, dtype=torch.bfloat16, device="cuda")
+    pos = torch.arange(cs[0]["n"], dtype=torch.int32, device="cuda")
+
+    def calls(stream=None):
+        x, sc = buf["x"], buf["sc"]
+        F.rope_append_gqa_paged(x[:, :8], x[:, 8:10], x[:, 10:], tab, sc[:8], sc[8:10], sc[10:], *pools, table,
+                                buf["q_start"], buf["kv_lens"], *w, EPS, q_out=q_out, stream=stream)
+        F.norm_rope(x[:, :8], None, tab, pos, w[0], eps=EPS, q_out=rows, stream=stream)
+
+    def check(i):
+        torch.cuda.synchronize()
+        _same([t.cpu().numpy() for t in (q_out, *pools)], want[i])
+        y, m = O.norm_rope(cs[i]["x"][:, :8], cs[0]["w"][0], EPS, cs[0]["cs"], np.arange(cs[0]["n"]), False)
+        _check(rows, y, m, False)
+        for t in (rows, *pools):
+            t.zero_()
+        q_out.fill_(77)
+        torch.cuda.synchronize()
+
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    calls(side)
+    check(0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for i in (1, 0, 1):
+        for n in names:
+            buf[n].copy_((bf16_dev if n == "x" else _t)(cs[i][n]))
+        graph.replay()
+        check(i)
+
+
+def test_calls_that_are_refused():
+    F = fa3()
+    rng = np.random.default_rng(31)
+    x = bf16_dev(_values(rng, (6, 4, 128)))
+    tab, pos = _t(_table(8, 128)), torch.zeros(6, dtype=torch.int32, device="cuda")
+    w = bf16_dev(np.ones(128, np.float32))
+    for bad, error in ((dict(q=x.float()), TypeError), (dict(cos_sin=tab.double()), TypeError), (dict(pos=None), ValueError),
+                       (dict(pos=pos[:5]), ValueError), (dict(pos=pos.long()), TypeError), (dict(q_weight=w[:64]), ValueError),
+                       (dict(k_weight=w), ValueError), (dict(k=x[:5]), ValueError), (dict(k=x, k_weight=w), ValueError),
+                       (dict(q_out=x[:, :2]), ValueError), (dict(q_out=torch.zeros_like(x, dtype=torch.float16)), TypeError),
+                       (dict(q_out=x[:, :1].expand(6, 4, 128)), ValueError), (dict(q=x[..., ::2]), ValueError),
+                       (dict(q=x[..., :4]), ValueError), (dict(q=x[..., :12], cos_sin=None, pos=None), F.FA3Error), (dict(eps=-1.0), F.FA3Error), (dict(cos_sin=tab.cpu()), TypeError),
+                       (dict(q=x[..., 2:122], cos_sin=tab[:, :120].contiguous()), F.FA3Error)):   # rows off 8 bytes
+        with pytest.raises(error):
+            F.norm_rope(**{**dict(q=x, k=None, cos_sin=tab, pos=pos), **bad})
+    pool = torch.zeros(4, 8, 2, 128, dtype=torch.int8, device="cuda")
+    sc, i32 = torch.ones(2, device="cuda"), lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    good = dict(q=x[:, :2], k=x[:, 2:], v=x[:, 2:], cos_sin=tab, q_scale=sc, k_scale=sc, v_scale=sc, k_cache=pool,
+                v_cache=pool.clone(), block_table=i32(0, 1)[None], q_start=i32(0, 6), kv_lens=i32(6))
+    F.rope_append_gqa_paged(**good)
+    for bad, error in ((dict(k=x[:, 1:]), ValueError), (dict(v=x[:5, 2:]), ValueError), (dict(q=x[:, ::2]), ValueError),
+                       (dict(q_scale=None), F.FA3Error), (dict(k_scale=sc[:1]), ValueError), (dict(q_start=i32(0)), ValueError),
+                       (dict(kv_lens=i32(6).long()), TypeError), (dict(block_table=i32(0, 1)), ValueError),
+                       (dict(v_cache=pool[:2]), ValueError), (dict(v_cache=pool.transpose(0, 1)), ValueError),
+                       (dict(q_out=torch.zeros(6, 2, 64, dtype=torch.int8, device="cuda")), ValueError),
+                       (dict(q=None, q_weight=w), ValueError), (dict(dev_err=i32(0).cpu()), TypeError)):
+        with pytest.raises(error):
+            F.rope_append_gqa_paged(**{**good, **bad})
