@@ -475,6 +475,15 @@ __device__ __forceinline__ void wait_ld16(uint32_t* v) {
                :: "memory");
 }
 
+// 32 columns' maximum, by the load itself; the columns go to v all the same.
+__device__ __forceinline__ void tmem_ld_max32(uint32_t taddr, uint32_t (&v)[32], float& m) {
+  asm volatile("tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]), "=f"(m) : "r"(taddr));
+}
+__device__ __forceinline__ void wait_max(float& a) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(a) :: "memory");
+}
+
 // 16 bytes that this SM reads once: the L1 (what shared memory leaves of it) is passed by.
 __device__ __forceinline__ uint4 load_once(const int8_t* p) {
   uint4 v;
@@ -897,25 +906,16 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
           }
           // the row's maximum of the integer scores
           uint32_t v0[16], v1[16];
-          float mx = -CUDART_INF_F, mx1 = -CUDART_INF_F;
-          auto maxima = [&](const uint32_t (&w)[16]) {
-#pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              mx = max3(mx, __uint_as_float(w[e]), __uint_as_float(w[e + 1]));
-              mx1 = max3(mx1, __uint_as_float(w[e + 2]), __uint_as_float(w[e + 3]));
-            }
-          };
-          FA3_TMEM_LD16(scol, v0);
+          float mx = -CUDART_INF_F;
 #pragma unroll 1
           for (uint32_t k = 0; k < 128; k += 32) {
-            wait_ld16(v0);
-            FA3_TMEM_LD16(scol + k + 16, v1);
-            maxima(v0);
-            wait_ld16(v1);
-            FA3_TMEM_LD16(scol + ((k + 32) & 127), v0);        // the next, and the first again at the end
-            maxima(v1);
+            uint32_t w[32];
+            float m;
+            tmem_ld_max32(scol + k, w, m);
+            wait_max(m);
+            mx = fmaxf(mx, m);
           }
-          mx = fmaxf(mx, mx1);
+          FA3_TMEM_LD16(scol, v0);
           mx *= c;
           // Lazy rescale: the reference maximum moves only when the row maximum grew by more than 8
           // (log2 units); then O (P.V up to this buffer's step before) is scaled in place.
@@ -946,8 +946,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
           // P = exp2(s c - m) as fp16 pairs over the S columns (keys 32 c4 .. 32 c4 + 31 go to columns
           // 16 c4 .. 16 c4 + 15); the row sum takes the weights before the rounding.
           float l0 = 0.f, l1 = 0.f;
-          auto weigh = [&](const uint32_t (&w)[16], uint32_t col) {
-            uint32_t pk[8];
+          auto weigh = [&](const uint32_t (&w)[16], uint32_t (&pk)[8]) {
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
               float p0, p1;
@@ -957,17 +956,26 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
               add2(l0, l1, l0, l1, p0, p1);
               pk[e / 2] = pack_f16x2(p0, p1);
             }
-            tmem_st8(col, pk);
           };
+          uint32_t pa[8], pb[8];
+          wait_ld16(v0);
+          FA3_TMEM_LD16(scol + 16, v1);
+          weigh(v0, pa);
 #pragma unroll 1
-          for (uint32_t k = 0; k < 128; k += 32) {
-            wait_ld16(v0);
-            FA3_TMEM_LD16(scol + k + 16, v1);
-            weigh(v0, scol + k / 2);
+          for (uint32_t k = 0; k < 96; k += 32) {
             wait_ld16(v1);
-            if (k < 96) FA3_TMEM_LD16(scol + k + 32, v0);
-            weigh(v1, scol + k / 2 + 8);
+            FA3_TMEM_LD16(scol + k + 32, v0);
+            weigh(v1, pb);
+            tmem_st8(scol + k / 2, pa);
+            wait_ld16(v0);
+            FA3_TMEM_LD16(scol + k + 48, v1);
+            weigh(v0, pa);
+            tmem_st8(scol + k / 2 + 8, pb);
           }
+          wait_ld16(v1);
+          weigh(v1, pb);
+          tmem_st8(scol + 48, pa);
+          tmem_st8(scol + 56, pb);
           l_run += l0 + l1;
           tmem_wait_st();
           tc_fence_before();
