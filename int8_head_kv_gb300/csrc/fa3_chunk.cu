@@ -31,21 +31,22 @@
 //
 // Numbers.  int8 codes are exact in fp16 and a 128-term sum of their products stays
 // below 2^24, so kind::f16 MMAs with float32 accumulation give the exact integer score
-// (the integer tensor rate of sm_103a is far below it).  P is rounded to fp16 relative to a lazily
-// moved row maximum (off by 2^-11 of a weight at most, and the result is rounded to bf16,
-// 2^-8); the row sum is float32 over the unrounded weights, and O, partial results and
-// their merging are float32.  P is written over its scores in TMEM and is the A operand of
-// P.V.  TMEM: O_0, O_1, S_0, S_1, 128 columns each.
+// (the integer tensor rate of sm_103a is far below it).  P is rounded to fp16 relative to
+// a lazily moved row maximum (off by 2^-11 of a weight at most, where the result is rounded
+// to bf16, 2^-8); the row sum is float32 over the unrounded weights, and O, partial results
+// and their merging are float32.  P is written over its scores in TMEM and is the A operand
+// of P.V.  TMEM: O_0, O_1, S_0, S_1, 128 columns each.
 //
 // What bounds it (64 query and 8 KV heads, one GB300).  4096 new rows on a context of
-// 8192: 777 us, 1060 TFLOP/s; a step takes 2250 cycles, of which the tensor pipe works
-// 45 %: the chain scores, softmax, P.V, scores of each of the two buffers, a
-// barrier at every arrow, and shared memory, which moves some 320 KB a key tile (int8 tile
-// in and out, fp16 tile in, Q, K and V into the MMAs: 2500 cycles at 128 bytes each).  16 one-token rows of 4096 keys: 52
-// us, 2.6 TB/s; a key tile takes 2600 cycles, the way of an int8 tile from HBM to fp16,
-// one tile of K and one of V in flight because 224 KB of shared memory are full.  About
-// 8 us of a small call are the launch, the plan (2.5 us), the first tiles' way (3 us)
-// and the combine kernel (3 us).
+// 8192: 738 us, 1117 TFLOP/s.  A step takes 2150 cycles, of which the tensor pipe works
+// half: the rest is the chain scores, softmax, P.V, scores of each of the two buffers with
+// a barrier at every arrow, and shared memory, which moves 320 KB a key tile (int8 tile in
+// and out, fp16 tile in, Q, K and V into the MMAs: 2500 cycles at 128 bytes each).
+// 16 one-token rows of 4096 keys: 51 us, 2.6 TB/s.  A key tile takes 2500 cycles of the
+// same chain, for 8 rows of 128; neither a second int8 tile on its way (53.7 us) nor four
+// warps on a tile's softmax (55.1 us) shortened it, and more code costs every case: the
+// roles' loops share the SM's instruction cache.  About 8 us of a small call are the
+// launch, the plan (2 us), the first tiles' way (3 us) and the combine kernel (3 us).
 //
 // Every wait is bounded; on time-out the kernel sets FA3_DEVERR_TIMEOUT, waits for its
 // copies and MMAs, frees its TMEM and returns.
@@ -630,7 +631,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
       ok = warp_all(wait_long(bar(B_Q_READY), units & 1u, abort_flag, p.err));
       // Step t: buffer t & 1, key tile t (or t / 2 with two row tiles).  P.V of step t, then Q.K^T of step t + 2.
       // All roles' loops are kept rolled: together they have to stay in the SM's instruction cache, and an MMA lasts
-      // longer than an iteration.
+      // longer than an iteration (4096 rows on 8192 keys, the MMA loops unrolled by 1, 2, 4, 8: 743, 738, 756, 763 us).
       const uint32_t per = u.dual ? 1u : 0u;
 #pragma unroll 1
       for (int t = -2; t < steps && ok; ++t) {
@@ -645,7 +646,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
           tc_fence_after();
           uint32_t bd = desc_lo(sbase + OFF_V + s * KV_TILE, KV_HALF), ap = tmem + TM_S + x * 128;
           uint32_t acc = t >= 2 ? 1u : 0u;
-#pragma unroll 1
+#pragma unroll 2
           for (int kk = 0; kk < kKeys / 16; ++kk) {
             mma_ts<desc_hi(1024, true)>(lead, tmem + TM_O + x * 128, ap, bd, id_pv, acc);
             bd += 2048 >> 4;
@@ -667,7 +668,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
           tc_fence_after();
           uint32_t a = desc_lo(sbase + OFF_Q + (u.dual ? x : 0u) * Q_TILE, 2048), bd = desc_lo(sbase + OFF_K + s * KV_TILE, 16);
           uint32_t acc = 0u;
-#pragma unroll 1
+#pragma unroll 2
           for (int kk = 0; kk < kD / 16; ++kk) {
             mma_ss<desc_hi(128, false), desc_hi(1024, true)>(lead, tmem + TM_S + x * 128, a, bd, id_qk, acc);
             a += 4096 >> 4;
