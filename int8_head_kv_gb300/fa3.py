@@ -604,13 +604,15 @@ def _here(dev: int, stream):
         if stream.device_index != dev:
             raise ValueError("stream must be on the tensors' device")
         return stream.cuda_stream, torch.cuda.stream(stream)
-    ctx = torch.cuda.device(dev) if torch.cuda.current_device() != dev else None
+    ctx = torch.cuda.device(dev) if torch._C._cuda_getDevice() != dev else None
     return torch._C._cuda_getCurrentRawStream(dev), ctx
 
 
 def _rows4(t: torch.Tensor, name: str, out: bool = False):
     """Strides (b, s, h) of head rows [B][S][H][D] or [n][H][D]; 0 where there is one index."""
     st = t.stride()
+    if len(st) == 4 and st[3] == 1 and st[0] and st[1] and st[2] and not (st[0] | st[1] | st[2]) & 3:
+        return st[:3]                                        # nothing below would change or refuse it
     sh = t.shape
     if len(sh) == 3:
         st, sh = (0,) + st, (1,) + tuple(sh)
@@ -644,11 +646,13 @@ def norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], cos_sin: Optional[torc
     dev = q.get_device()
     Hkv, ks, kos, kp, kop = 0, (0, 0, 0), (0, 0, 0), None, None
     if k is not None:
-        _need(k, _BF16, "k")
+        if not (isinstance(k, torch.Tensor) and k.dtype is _BF16 and k.get_device() == dev):
+            _need(k, _BF16, "k")
+            raise ValueError("all tensors must be on one device")
         ks = _rows4(k, "k")
         ksh = k.shape
         Hkv = ksh[-2]
-        if len(ksh) != len(sh) or ksh[:-2] != sh[:-2] or ksh[-1] != D:
+        if len(ksh) != len(sh) or ksh[0] != sh[0] or ksh[-1] != D or ksh[:-2] != sh[:-2]:
             raise ValueError("k must have q's tokens and head size")
         if (q_weight is None) != (k_weight is None):
             raise ValueError("q_weight and k_weight go together")
@@ -665,10 +669,9 @@ def norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], cos_sin: Optional[torc
         if pos.numel() != B * S:
             raise ValueError("pos must hold one position for each token")
         pp = pos.data_ptr()
-    qw, kw = _vector(q_weight, D, _BF16, "q_weight", dev), _vector(k_weight, D, _BF16, "k_weight", dev)
-    ep = _error_word(dev_err, dev)
-    if k is not None and k.get_device() != dev:
-        raise ValueError("all tensors must be on one device")
+    qw = None if q_weight is None else _vector(q_weight, D, _BF16, "q_weight", dev)
+    kw = None if k_weight is None else _vector(k_weight, D, _BF16, "k_weight", dev)
+    ep = None if dev_err is None else _error_word(dev_err, dev)
     raw, ctx = _here(dev, stream)
     if ctx is not None:
         ctx.__enter__()
