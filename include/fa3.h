@@ -501,6 +501,19 @@ int fa3_cross_attn_gqa(const int8_t* q, const int8_t* k, const int8_t* v,
                        int n, int B, int T, int Hq, int Hkv, int D, float softmax_scale,
                        void* workspace, size_t workspace_bytes, int32_t* dev_err, void* stream);
 
+/* The four packed-row calls above with their arguments in one block, in their order, for
+ * callers behind a foreign-function interface: args[i] is a pointer's or an integer's
+ * value, or the bits of a double in place of a float; args is 8-byte aligned, count its
+ * length.  FA3_EINVAL: another call or number; FA3_ERANGE: a value beyond its
+ * argument's type; otherwise the call's own status. */
+enum {
+  FA3_CALL_NORM_ROPE = 0,
+  FA3_CALL_ROPE_APPEND_GQA_PAGED = 1,
+  FA3_CALL_PREFILL_ATTN_GQA_PAGED = 2,
+  FA3_CALL_CROSS_ATTN_GQA = 3
+};
+int fa3_call(int which, const int64_t* args, int count);
+
 #ifdef __cplusplus
 }
 #endif

@@ -9,6 +9,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 from collections import OrderedDict
 from typing import Optional
 
@@ -70,7 +71,15 @@ _SIGS = {
     "fa3_chunk_workspace_size": (_SZ, [_I] * 5),
     "fa3_prefill_attn_gqa_paged": (_I, [_P] * 10 + [_I] * 8 + [_F, _P, _SZ, _P, _P]),
     "fa3_cross_attn_gqa": (_I, [_P] * 9 + [_I] * 6 + [_F, _P, _SZ, _P, _P]),
+    "fa3_call": (_I, [_I, ctypes.c_char_p, _I]),
 }
+
+# fa3_call: number of the call, packer of its arguments, their number.  ctypes converts one by one what this
+# packs at once.
+_CALLS = {name: (i, struct.Struct("=" + "".join("d" if a is _F else "q" for a in _SIGS[name][1])).pack,
+                 len(_SIGS[name][1]))
+          for i, name in enumerate(("fa3_norm_rope", "fa3_rope_append_gqa_paged", "fa3_prefill_attn_gqa_paged",
+                                    "fa3_cross_attn_gqa"))}
 
 
 def library_path() -> str:
@@ -644,7 +653,7 @@ def norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], cos_sin: Optional[torc
     qs = _rows4(q, "q")
     B, S, Hq, D = sh if len(sh) == 4 else (1,) + tuple(sh)
     dev = q.get_device()
-    Hkv, ks, kos, kp, kop = 0, (0, 0, 0), (0, 0, 0), None, None
+    Hkv, ks, kos, kp, kop = 0, (0, 0, 0), (0, 0, 0), 0, 0
     if k is not None:
         if not (isinstance(k, torch.Tensor) and k.dtype is _BF16 and k.get_device() == dev):
             _need(k, _BF16, "k")
@@ -659,7 +668,7 @@ def norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], cos_sin: Optional[torc
         kp = k.data_ptr()
     elif k_out is not None or k_weight is not None:
         raise ValueError("k_out and k_weight need k")
-    table_len, rot, cp, pp = 0, 0, None, None
+    table_len, rot, cp, pp = 0, 0, 0, 0
     if cos_sin is not None:
         table_len, rot, cp = _table(cos_sin, D, dev)
         if pos is None:
@@ -669,9 +678,9 @@ def norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], cos_sin: Optional[torc
         if pos.numel() != B * S:
             raise ValueError("pos must hold one position for each token")
         pp = pos.data_ptr()
-    qw = None if q_weight is None else _vector(q_weight, D, _BF16, "q_weight", dev)
-    kw = None if k_weight is None else _vector(k_weight, D, _BF16, "k_weight", dev)
-    ep = None if dev_err is None else _error_word(dev_err, dev)
+    qw = 0 if q_weight is None else _vector(q_weight, D, _BF16, "q_weight", dev)
+    kw = 0 if k_weight is None else _vector(k_weight, D, _BF16, "k_weight", dev)
+    ep = 0 if dev_err is None else _error_word(dev_err, dev)
     raw, ctx = _here(dev, stream)
     if ctx is not None:
         ctx.__enter__()
@@ -691,8 +700,10 @@ def norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], cos_sin: Optional[torc
                 raise ValueError("k_out must have the input's shape and device and q_out's type")
             kos, kop = _rows4(k_out, "k_out", True), k_out.data_ptr()
         if B * S and Hq and D:
-            st = lib().fa3_norm_rope(q.data_ptr(), kp, qw, kw, eps, cp, table_len, rot, interleaved, pp,
-                                     q_out.data_ptr(), kop, t is _F32, B, S, Hq, Hkv, D, *qs, *ks, *qos, *kos, ep, raw)
+            i, pack, count = _CALLS["fa3_norm_rope"]
+            st = lib().fa3_call(i, pack(q.data_ptr(), kp, qw, kw, eps, cp, table_len, rot, bool(interleaved), pp,
+                                        q_out.data_ptr(), kop, t is _F32, B, S, Hq, Hkv, D, *qs, *ks, *qos, *kos, ep,
+                                        raw), count)
             if st:
                 raise FA3Error("fa3_norm_rope", st)
     finally:
@@ -711,9 +722,9 @@ def _table(cos_sin: torch.Tensor, D: int, dev: int):
 
 
 def _vector(t: Optional[torch.Tensor], n: int, dtype, name: str, dev: int):
-    """The address of n contiguous values, or None."""
+    """The address of n contiguous values, or 0."""
     if t is None:
-        return None
+        return 0
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()):
         _wrong(t, dtype, name)
     if t.numel() != n:
@@ -723,7 +734,7 @@ def _vector(t: Optional[torch.Tensor], n: int, dtype, name: str, dev: int):
 
 def _error_word(t: Optional[torch.Tensor], dev: int):
     if t is None:
-        return None
+        return 0
     if not (t.dtype is _I32 and t.get_device() == dev and t.numel() >= 1):
         _need(t, _I32, "dev_err")
         raise ValueError("dev_err must hold one value on the tensors' device")
@@ -797,10 +808,10 @@ def rope_append_gqa_paged(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.T
     ks, vs = _packed_rows(k, Hkv, D, n, "k", dev), _packed_rows(v, Hkv, D, n, "v", dev)
     ksc, vsc = _vector(k_scale, Hkv, _F32, "k_scale", dev), _vector(v_scale, Hkv, _F32, "v_scale", dev)
     qw, kw = _vector(q_weight, D, _BF16, "q_weight", dev), _vector(k_weight, D, _BF16, "k_weight", dev)
-    table_len, rot, cp = _table(cos_sin, D, dev) if cos_sin is not None else (0, 0, None)
+    table_len, rot, cp = _table(cos_sin, D, dev) if cos_sin is not None else (0, 0, 0)
     max_pages = _pages(block_table, B, dev)
     ep = _error_word(dev_err, dev)
-    Hq, qs, qsc, qp, qop = 0, 0, None, None, None
+    Hq, qs, qsc, qp, qop = 0, 0, 0, 0, 0
     if q is not None:
         if q.dim() != 3:
             raise ValueError("q must be [n][H][D]")
@@ -821,10 +832,11 @@ def rope_append_gqa_paged(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.T
                 raise ValueError("q_out must be [n][Hq][D]")
             qop = q_out.data_ptr()
         if n:
-            st = lib().fa3_rope_append_gqa_paged(
-                qp, k.data_ptr(), v.data_ptr(), qw, kw, eps, cp, table_len, rot, interleaved, qsc, ksc, vsc, qop,
+            i, pack, count = _CALLS["fa3_rope_append_gqa_paged"]
+            st = lib().fa3_call(i, pack(
+                qp, k.data_ptr(), v.data_ptr(), qw, kw, eps, cp, table_len, rot, bool(interleaved), qsc, ksc, vsc, qop,
                 k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), q_start.data_ptr(),
-                kv_lens.data_ptr(), n, B, Hq, Hkv, D, qs, ks, vs, num_pages, page_size, max_pages, ep, raw)
+                kv_lens.data_ptr(), n, B, Hq, Hkv, D, qs, ks, vs, num_pages, page_size, max_pages, ep, raw), count)
             if st:
                 raise FA3Error("fa3_rope_append_gqa_paged", st)
     finally:
@@ -874,11 +886,12 @@ def _packed_attn(name, q, k, v, q_scale, k_scale, v_scale, q_start, lens, B, Hkv
                 workspace = _chunk_workspace(nbytes, q.device, stream) if nbytes else None
             elif workspace.get_device() != dev or not workspace.is_contiguous():
                 raise ValueError("workspace must be contiguous and on the tensors' device")
-            wp, wn = (None, 0) if workspace is None else (workspace.data_ptr(),
-                                                          workspace.numel() * workspace.element_size())
-            st = getattr(L, name)(q.data_ptr(), k.data_ptr(), v.data_ptr(), qsc, ksc, vsc, q_start.data_ptr(),
-                                  lens.data_ptr(), *table, out.data_ptr(), n, B, *sizes(Hq), softmax_scale, wp, wn, ep,
-                                  raw)
+            wp, wn = (0, 0) if workspace is None else (workspace.data_ptr(),
+                                                       workspace.numel() * workspace.element_size())
+            i, pack, count = _CALLS[name]
+            st = L.fa3_call(i, pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), qsc, ksc, vsc, q_start.data_ptr(),
+                                    lens.data_ptr(), *table, out.data_ptr(), n, B, *sizes(Hq), softmax_scale, wp, wn, ep,
+                                    raw), count)
             if st:
                 raise FA3Error(name, st)
     finally:

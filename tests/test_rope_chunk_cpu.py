@@ -176,3 +176,23 @@ def test_rope_table_checks_and_far_positions():
     t = F.rope_table(100001, 4, device="cpu").numpy()
     ang = 100000 * np.array([1.0, 0.01])
     np.testing.assert_allclose(t[100000], np.concatenate([np.cos(ang), np.sin(ang)]), atol=2.0 ** -24)
+
+
+def test_calls_in_one_block(L):
+    from int8_head_kv_gb300 import fa3 as F
+    for name, (i, pack, count) in F._CALLS.items():
+        kinds = F._SIGS[name][1]
+        zero = [0.0 if k is F._F else 0 for k in kinds]
+        assert len(kinds) == count and L.fa3_call(i, pack(*zero), count) == EINVAL          # the call's own check
+        assert L.fa3_call(i, pack(*zero), count - 1) == EINVAL
+        assert L.fa3_call(i, None, count) == EINVAL
+        for at, k in enumerate(kinds):                                                      # beyond an int
+            for v in (1 << 31, -(1 << 31) - 1) if k is F._I else (-1,) if k is F._SZ else ():
+                assert L.fa3_call(i, pack(*zero[:at], v, *zero[at + 1:]), count) == ERANGE, (name, at)
+    assert L.fa3_call(len(F._CALLS), b"", 0) == EINVAL
+    # the same answer as the call itself where the arguments are looked at one by one: a head size of 12
+    args = [1 << 20, 0, 0, 0, 1e-6, 0, 0, 0, 0, 0, 1 << 20, 0, 0, 1, 1, 1, 0, 12] + [0] * 14
+    i, pack, count = F._CALLS["fa3_norm_rope"]
+    assert L.fa3_call(i, pack(*args), count) == L.fa3_norm_rope(*args) == ERANGE
+    args[4] = float("nan")
+    assert L.fa3_call(i, pack(*args), count) == L.fa3_norm_rope(*args) == EINVAL
