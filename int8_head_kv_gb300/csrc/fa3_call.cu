@@ -1,6 +1,6 @@
 // The packed-row calls with their arguments in one block: host code alone.  Each of these calls takes a few
 // microseconds of a GPU in a decode step, and behind a foreign-function interface every argument has a price: from
-// Python, fa3_norm_rope's 32 one by one make a call of 21 us, in one block of 17; the append's 34 of 25 and 21.
+// Python, fa3_norm_rope's 32 one by one make a call of 21 us, in one block of 17; the append's 32 of 25 and 21.
 #include "fa3_common.cuh"
 
 #include <cstring>

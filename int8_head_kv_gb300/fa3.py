@@ -849,11 +849,16 @@ def chunk_workspace_size(n: int, B: int, Hq: int, Hkv: int, D: int) -> int:
     return int(lib().fa3_chunk_workspace_size(n, B, Hq, Hkv, D))
 
 
-def _chunk_workspace(nbytes: int, device, stream):
+def _chunk_workspace(nbytes: int, device, stream, dev: int, raw: int):
     # A captured call takes its buffer from the graph's own pool: replays of two graphs
     # (or of a graph and eager calls) then never share one.
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    key = ("chunk", dev, raw)                                # _ws_key's, without asking for the stream again
+    ws = _ws_cache.get(key)
+    if ws is not None and ws.numel() >= nbytes:
+        _ws_cache.move_to_end(key)
+        return ws
     return _workspace("chunk", nbytes, device, stream=stream)
 
 
@@ -883,7 +888,7 @@ def _packed_attn(name, q, k, v, q_scale, k_scale, v_scale, q_start, lens, B, Hkv
             L = lib()
             if workspace is None:
                 nbytes = L.fa3_chunk_workspace_size(n, B, Hq, Hkv, D)
-                workspace = _chunk_workspace(nbytes, q.device, stream) if nbytes else None
+                workspace = _chunk_workspace(nbytes, q.device, stream, dev, raw) if nbytes else None
             elif workspace.get_device() != dev or not workspace.is_contiguous():
                 raise ValueError("workspace must be contiguous and on the tensors' device")
             wp, wn = (0, 0) if workspace is None else (workspace.data_ptr(),
