@@ -101,12 +101,14 @@ constexpr uint32_t OFF_ABORT = OFF_TSLOT + 4;
 constexpr uint32_t SMEM_CHUNK = OFF_ABORT + 4 + 1024;      // + alignment slack
 static_assert(SMEM_CHUNK <= 232448, "shared memory");
 
-// A unit's cost beside its steps (its query rows, pipeline fill and epilogue), in steps: fitted over the CTAs of ragged
-// batches it is about 7000 cycles against 1950 to 2200 a step (counted as two steps, a batch of eight sequences of up
-// to 512 new rows took 113 us, as three or four 101).  And the least part of the line a CTA takes, and the
-// least where short units go one to a CTA (16 one-token units of 128 keys: 17 us in parts of kLeastPart, 13 us).
-constexpr int kUnitCost = 3, kLeastPart = 8, kLeastInner = 4;
-static_assert(kLeastInner > kUnitCost, "a part inside a unit holds a key tile");
+// The line's unit is an eighth of a step with two row tiles: what a key tile costs with two row tiles and with one, a
+// unit's cost beside its steps (its query rows, pipeline fill and epilogue), the least part of the line a CTA takes,
+// and the least where short units go one to a CTA (16 one-token units of 128 keys: 17 us in parts of kLeastPart, 13
+// us).  Fitted over the CTAs of ragged batches: 1950 cycles a step with two row tiles, 2200 with one, 7000 to 8000 a
+// unit.  Eight sequences of up to 512 new rows took 113 us with a unit counted as 2 steps, 98.6 as 3 and every step
+// alike, 92.3 so.
+constexpr int kTileDual = 16, kTileSingle = 9, kUnitCost = 30, kLeastPart = 64, kLeastInner = 32;
+static_assert(kLeastInner >= kTileDual, "a part inside a unit, behind its fixed cost, holds a key tile");
 
 // What the combine kernel has to know of the cut before a CTA's part: nothing (owner < 0) unless it is the
 // first cut of its unit.
@@ -172,7 +174,7 @@ __device__ __forceinline__ int tiles_of(const ChunkParams& p, const Seq& s, int 
 }
 __device__ __forceinline__ bool is_dual(const ChunkParams& p, const Seq& s, int rb) { return s.nq - rb * 2 * p.P > p.P; }
 __device__ __forceinline__ int cost_of(const ChunkParams& p, const Seq& s, int rb) {
-  return kUnitCost + tiles_of(p, s, rb) * (is_dual(p, s, rb) ? 2 : 1);
+  return kUnitCost + tiles_of(p, s, rb) * (is_dual(p, s, rb) ? kTileDual : kTileSingle);
 }
 
 // The line's numbers are I: uint32_t where they fit 24 bits (the host's bound), int64_t otherwise.  The plan is on
@@ -205,7 +207,7 @@ __device__ __forceinline__ I sequence_cost(const ChunkParams& p, const Seq& s) {
   if (nb == 0) return 0;
   I c = (I)cost_of(p, s, nb - 1) + (I)(nb - 1) * kUnitCost;
   if (nb > 1)
-    c += 2 * (p.causal ? floor_sum<I>((I)(nb - 1), kKeys, (I)(2 * p.P), (I)(s.nkv - s.nq) + 2 * p.P + kKeys - 1)
+    c += kTileDual * (p.causal ? floor_sum<I>((I)(nb - 1), kKeys, (I)(2 * p.P), (I)(s.nkv - s.nq) + 2 * p.P + kKeys - 1)
                        : (I)(nb - 1) * (I)tiles_of(p, s, 0));
   return c;
 }
@@ -361,7 +363,7 @@ __device__ __forceinline__ Cursor<I> seek(const ChunkParams& p, I x, const Ahead
 // Key tile at which a part that begins `off` into a unit begins.
 template <class I>
 __device__ __forceinline__ int tile_at(I off, bool dual, int nt) {
-  const I t = off <= kUnitCost ? 0 : (off - kUnitCost) >> (dual ? 1 : 0);
+  const I at = off <= kUnitCost ? 0 : off - kUnitCost, t = dual ? at / kTileDual : at / kTileSingle;
   return t < (I)nt ? (int)t : nt;
 }
 
@@ -385,8 +387,10 @@ __device__ __forceinline__ void record_cut(const ChunkParams& p, const Seq& s0, 
       cut.dual = dual;
       cut.owner = cta - 1;
       cut.last = line.owner(end - 1);
-      // a CTA between the two has kLeastInner or more of the line, which is a key tile at least
+      // a CTA between the two has kLeastInner or more of the line, which is a key tile at least; only this one,
+      // right behind the unit's begin, may have none
       cut.own = tile_at<I>(c.off, dual, nt) > 0;
+      if (cta < cut.last && tile_at<I>(line.begin(cta + 1) - begin, dual, nt) == 0) cut.owner = cta;
       cut.end = tile_at<I>(line.begin(cut.last) - begin, dual, nt) < nt;
     }
   }
@@ -1155,7 +1159,7 @@ int chunk_attn(ChunkParams& p, int D, float softmax_scale, void* workspace, size
   if (!aligned16(p.q) || !aligned16(p.k) || !aligned16(p.v) || !aligned16(p.out)) return FA3_ERANGE;
   p.P = kRows / p.G;
   p.div_2p = make_divu32((uint32_t)(2 * p.P));
-  p.narrow = ((double)p.n / (2 * p.P) + p.B) * p.Hkv * (kUnitCost + 2.0 * (p.T / kKeys + 1.0)) < 16777216.0;
+  p.narrow = ((double)p.n / (2 * p.P) + p.B) * p.Hkv * (kUnitCost + kTileDual * (p.T / kKeys + 1.0)) < 16777216.0;
   p.sm_log2 = softmax_scale * 1.4426950408889634f;
   int sms = 0;
   const int st = check_device(&sms);

@@ -249,6 +249,16 @@ def test_more_sequences_than_a_warp_has_lanes():
     _check(F, c, "1300 sequences")
 
 
+@pytest.mark.parametrize("seed", range(8))
+def test_short_units_beside_longer_ones(seed):
+    # parts of the line shorter than a unit's fixed cost and a key tile: cuts right behind a unit's begin
+    F = fa3()
+    rng = np.random.default_rng([25, seed])
+    rows = list(rng.choice([1, 1, 1, 1, 1, 1, 20, 40], 6 * (seed + 1)))
+    c = _case(rng, 8, 1 + seed % 2 * 3, rows, [r + int(x) for r, x in zip(rows, rng.choice([3, 60, 90, 500, 900], len(rows)))], 32)
+    _check(F, c, "short units")
+
+
 def test_table_of_a_very_long_context():
     # a table wide enough that the plan is made in 64 bits: the same cuts, the same bits
     F = fa3()
