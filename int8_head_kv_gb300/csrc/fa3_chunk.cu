@@ -103,11 +103,12 @@ static_assert(SMEM_CHUNK <= 232448, "shared memory");
 
 // The line's unit is an eighth of a step with two row tiles: what a key tile costs with two row tiles and with one, a
 // unit's cost beside its steps (its query rows, pipeline fill and epilogue), the least part of the line a CTA takes,
-// and the least where short units go one to a CTA (16 one-token units of 128 keys: 17 us in parts of kLeastPart, 13
-// us).  Fitted over the CTAs of ragged batches: 1950 cycles a step with two row tiles, 2200 with one, 7000 to 8000 a
+// and the least where short units go one to a CTA (16 one-token units of 128 keys: 17 us in parts of two such units, 12
+// so).  A part of 40 is a short unit of one key tile: one token of 1024 keys takes 19.5 us in parts of 64, 17.9 of 40
+// and 16.6 of 32, which cut short units (one token of 64 keys 10.4 instead of 10.0).  Fitted over the CTAs of ragged batches: 1950 cycles a step with two row tiles, 2200 with one, 7000 to 8000 a
 // unit.  Eight sequences of up to 512 new rows took 113 us with a unit counted as 2 steps, 98.6 as 3 and every step
 // alike, 92.3 so.
-constexpr int kTileDual = 16, kTileSingle = 9, kUnitCost = 30, kLeastPart = 64, kLeastInner = 32;
+constexpr int kTileDual = 16, kTileSingle = 9, kUnitCost = 30, kLeastPart = 40, kLeastInner = 32;
 static_assert(kLeastInner >= kTileDual, "a part inside a unit, behind its fixed cost, holds a key tile");
 
 // What the combine kernel has to know of the cut before a CTA's part: nothing (owner < 0) unless it is the
