@@ -661,7 +661,7 @@ def norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], cos_sin: Optional[torc
         ks = _rows4(k, "k")
         ksh = k.shape
         Hkv = ksh[-2]
-        if len(ksh) != len(sh) or ksh[0] != sh[0] or ksh[-1] != D or ksh[:-2] != sh[:-2]:
+        if len(ksh) != len(sh) or ksh[0] != sh[0] or ksh[-1] != D or (len(sh) == 4 and ksh[1] != S):
             raise ValueError("k must have q's tokens and head size")
         if (q_weight is None) != (k_weight is None):
             raise ValueError("q_weight and k_weight go together")
