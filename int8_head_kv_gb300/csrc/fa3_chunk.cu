@@ -17,7 +17,7 @@
 //     alternate between the two score and accumulator buffers, and the two results are
 //     merged in the CTA.  Either way step t works on buffer t & 1, and while a buffer's
 //     softmax runs the tensor pipe has the other buffer's step.
-// All steps of all units, plus a unit's fixed cost in steps, lie on one line that is cut into equal
+// All units lie on one line, as long as their measured costs, that is cut into equal
 // parts, one per SM: a CTA takes whole units and at most one part of a unit at either
 // end.  A cut unit's parts leave unnormalised O, maximum and sum in the workspace, and
 // chunk_combine_kernel merges them, so one long sequence and a ragged batch both fill the GPU.
@@ -103,11 +103,11 @@ static_assert(SMEM_CHUNK <= 232448, "shared memory");
 
 // The line's unit is an eighth of a step with two row tiles: what a key tile costs with two row tiles and with one, a
 // unit's cost beside its steps (its query rows, pipeline fill and epilogue), the least part of the line a CTA takes,
-// and the least where short units go one to a CTA (16 one-token units of 128 keys: 17 us in parts of two such units, 12
-// so).  A part of 40 is a short unit of one key tile: one token of 1024 keys takes 19.5 us in parts of 64, 17.9 of 40
-// and 16.6 of 32, which cut short units (one token of 64 keys 10.4 instead of 10.0).  Fitted over the CTAs of ragged batches: 1950 cycles a step with two row tiles, 2200 with one, 7000 to 8000 a
-// unit.  Eight sequences of up to 512 new rows took 113 us with a unit counted as 2 steps, 98.6 as 3 and every step
-// alike, 92.3 so.
+// and the least where short units go one to a CTA (16 one-token units of 128 keys: 17 us in parts of two such units,
+// 12 so).  A part of 40 is a short unit of one key tile: one token of 1024 keys takes 19.5 us in parts of 64, 17.9 of
+// 40 and 16.6 of 32, which cut short units (one token of 64 keys 10.4 instead of 10.0).  Fitted over the CTAs of
+// ragged batches: 1950 cycles a step with two row tiles, 2200 with one, 7000 to 8000 a unit.  Eight sequences of up
+// to 512 new rows took 113 us with a unit counted as 2 steps, 98.6 as 3 and every step alike, 92.3 so.
 constexpr int kTileDual = 16, kTileSingle = 9, kUnitCost = 30, kLeastPart = 40, kLeastInner = 32;
 static_assert(kLeastInner >= kTileDual, "a part inside a unit, behind its fixed cost, holds a key tile");
 
@@ -483,8 +483,15 @@ __device__ __forceinline__ void wait_ld16(uint32_t* v) {
 
 // 32 columns' maximum, by the load itself; the columns go to v all the same.
 __device__ __forceinline__ void tmem_ld_max32(uint32_t taddr, uint32_t (&v)[32], float& m) {
-  asm volatile("tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]), "=f"(m) : "r"(taddr));
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+        "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+        "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]),
+        "=f"(m)
+      : "r"(taddr));
 }
 __device__ __forceinline__ void wait_max(float& a) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(a) :: "memory");
