@@ -470,7 +470,9 @@ __device__ __forceinline__ Place place_row(const RopeAppendArgs& a, int row, int
   const int b = find_sequence(a.q_start, a.B, row, lane);
   if (b < 0 || b >= a.B) return pl;                        // behind the last sequence
   const int q0 = a.q_start[b], q1 = a.q_start[b + 1], kv = a.kv_lens[b];
-  if (q0 < 0 || q1 <= row || q1 > a.n || kv < q1 - q0 || kv > a.T_max) {
+  // In a q_start that falls and rises the search may end at a sequence that begins behind the row: its position would
+  // be below 0, and the reads of the table and of the pages outside both.
+  if (q0 < 0 || q0 > row || q1 <= row || q1 > a.n || kv < q1 - q0 || kv > a.T_max) {
     if (lane == 0) set_dev_err(a.err, FA3_DEVERR_LENS);
     return pl;
   }

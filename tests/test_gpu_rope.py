@@ -397,3 +397,42 @@ def test_calls_that_are_refused():
                        (dict(q=None, q_weight=w), ValueError), (dict(dev_err=i32(0).cpu()), TypeError)):
         with pytest.raises(error):
             F.rope_append_gqa_paged(**{**good, **bad})
+
+
+@pytest.mark.parametrize("start", [[0, 9, 12, 4, 39], [0, 9, 4, 39, 39], [-3, 4, 9, 39, 39], [0, 4, 9, 4000, 39], [30, 20, 10, 5, 0]])
+@pytest.mark.parametrize("empty", [0, 40])
+def test_append_q_start_that_falls(start, empty):
+    # A row's sequence is searched for, and a start that falls may lead the search to one that begins behind the
+    # row: such a row is skipped.  Rows that are written are right for a sequence that holds them, nothing else is written.
+    F = fa3()
+    rng = np.random.default_rng([36, empty])
+    c = _append_case(rng, 2, 1, 64, 64, 8, [9, 3, 1, 26], [9, 3, 1, 40], False, behind=1)
+    assert c["n"] == 40
+    B = 4 + empty                                                           # sequences without rows in front: the search takes two steps
+    c["q_start"] = np.concatenate([np.zeros(empty, np.int32), np.asarray(start, np.int32)])
+    c["kv_lens"] = np.concatenate([np.zeros(empty, np.int32), np.array([9, 3, 1, 40], np.int32)])
+    c["table"] = np.arange(B * 6, dtype=np.int32).reshape(B, 6)
+    c["pools"] = [rng.integers(-127, 128, (B * 6, 8, 1, 64)).astype(np.int8) for _ in range(2)]
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q, k, v = _run_append(F, c, False, err)
+    assert int(err.item()) in (0, F.FA3_DEVERR_LENS)
+    may = [p.reshape(-1, 64).copy() for p in c["pools"]]
+    codes = lambda x, sc: O.quantize64(x, sc)  # noqa: E731
+    seen = np.zeros(c["n"], bool)
+    for b in range(B):
+        q0, q1, kv = int(c["q_start"][b]), int(c["q_start"][b + 1]), int(c["kv_lens"][b])
+        if not 0 <= q0 < q1 <= c["n"] or not q1 - q0 <= kv <= 48:
+            continue
+        for row in range(q0, q1):
+            at = np.array([kv - (q1 - row)])
+            x = c["x"][row:row + 1]
+            y = codes(O.norm_rope(x[:, :2], None, EPS, c["cs"], at, False)[0], c["sc"][:2])[0]
+            seen[row] |= np.array_equal(q[row], y)
+            k8 = codes(O.norm_rope(x[:, 2:3], None, EPS, c["cs"], at, False)[0], c["sc"][2:3])[0, 0]
+            v8 = O.quantize(x[:, 3:], c["sc"][3:][None, :, None])[0, 0]
+            place = b * 48 + int(at[0])
+            for got, new, keep in ((k, k8, may[0]), (v, v8, may[1])):
+                if np.array_equal(got.reshape(-1, 64)[place], new):
+                    keep[place] = new
+    assert np.all(seen | np.all(q == 77, axis=(1, 2)))
+    assert np.array_equal(k.reshape(-1, 64), may[0]) and np.array_equal(v.reshape(-1, 64), may[1])
