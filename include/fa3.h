@@ -441,10 +441,11 @@ int fa3_norm_rope(const uint16_t* q, const uint16_t* k, const uint16_t* q_weight
  *          (with q_out and q_weight NULL); k, v  bf16 [n][Hkv][D], row strides k_stride, v_stride.
  * q_out    int8 [n][Hq][D];  k_cache, v_cache  int8 [num_pages][page_size][Hkv][D].
  * q_start  int32 [B+1], non-decreasing, within [0, n];  kv_lens  int32 [B], n_b <=
- *          kv_lens[b] <= max_pages * page_size; otherwise FA3_DEVERR_LENS is set
- *          and the sequence is skipped.  Rows outside [q_start[0], q_start[B])
- *          belong to no sequence: their values do not matter, and their q_out is
- *          left as it was.
+ *          kv_lens[b] <= max_pages * page_size where n_b > 0; otherwise
+ *          FA3_DEVERR_LENS is set and the sequence is skipped (if q_start falls and
+ *          rises, its rows go to one of the sequences that hold them or to none).  Rows outside
+ *          [q_start[0], q_start[B]) belong to no sequence: their values do not matter,
+ *          and their q_out is left as it was.
  * A position past the table sets FA3_DEVERR_POS and skips the row; a block-table
  * entry outside the pool sets FA3_DEVERR_PAGE and skips its k and v (q_out is
  * written).  Supported: any page_size >= 1; q_out, k_cache, v_cache 8-byte aligned. */

@@ -472,10 +472,7 @@ __device__ __forceinline__ Place place_row(const RopeAppendArgs& a, int row, int
   const int q0 = a.q_start[b], q1 = a.q_start[b + 1], kv = a.kv_lens[b];
   // In a q_start that falls and rises the search may end at a sequence that begins behind the row: its position would
   // be below 0, and the reads of the table and of the pages outside both.
-  if (q0 < 0 || q0 > row || q1 <= row || q1 > a.n || kv < q1 - q0 || kv > a.T_max) {
-    if (lane == 0) set_dev_err(a.err, FA3_DEVERR_LENS);
-    return pl;
-  }
+  if (q0 < 0 || q0 > row || q1 <= row || q1 > a.n || kv < q1 - q0 || kv > a.T_max) return pl;   // check_lengths reports it
   pl.pos = kv - (q1 - row);
   if (a.r.cos_sin && pl.pos >= a.r.table_len) {
     if (lane == 0) set_dev_err(a.err, FA3_DEVERR_POS);
@@ -489,6 +486,15 @@ __device__ __forceinline__ Place place_row(const RopeAppendArgs& a, int row, int
   else if (lane == 0)
     set_dev_err(a.err, FA3_DEVERR_PAGE);
   return pl;
+}
+
+// Reports bad lengths of any sequence.  The rows cannot: a sequence that ends before it begins has none, and in a
+// q_start that falls a row may find another sequence that holds it.  A block of its own, so that no row waits for it.
+__device__ __forceinline__ void check_lengths(const RopeAppendArgs& a) {
+  for (int b = threadIdx.x; b < a.B; b += kRopeThreads) {
+    const int q0 = a.q_start[b], q1 = a.q_start[b + 1], kv = a.kv_lens[b];
+    if (q0 < 0 || q1 < q0 || q1 > a.n || (q1 > q0 && (kv < q1 - q0 || kv > a.T_max))) set_dev_err(a.err, FA3_DEVERR_LENS);
+  }
 }
 
 // The same walk over chunks of heads of q, k or v, of which each row ends as codes: q's
@@ -509,7 +515,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
   const uint32_t nt = (uint32_t)a.n * a.chunks;
   pdl_wait();
   pdl_launch_dependents();
-  for (uint32_t t = blockIdx.x * kRopeWarps + (threadIdx.x >> 5); t < nt; t += gridDim.x * kRopeWarps) {
+  if (blockIdx.x == 0) {
+    check_lengths(a);
+    return;
+  }
+  for (uint32_t t = (blockIdx.x - 1) * kRopeWarps + (threadIdx.x >> 5); t < nt; t += (gridDim.x - 1) * kRopeWarps) {
     const int row = (int)divu32(t, a.div_chunks);
     uint32_t chunk = t - (uint32_t)row * a.chunks;
     const bool is_q = chunk < a.q_chunks;
@@ -770,5 +780,5 @@ FA3_API int fa3_rope_append_gqa_paged(const uint16_t* q, const uint16_t* k, cons
   const bool inter = a.r.interleaved != 0;
   auto* kernel = lanes == 8 ? append_kernel<8>(inter) : lanes == 16 ? append_kernel<16>(inter)
                                                                     : append_kernel<32>(inter);
-  return cuda_status(launch_pdl(kernel, dim3((unsigned)blocks), dim3(kRopeThreads), 0, s, a));
+  return cuda_status(launch_pdl(kernel, dim3((unsigned)blocks + 1), dim3(kRopeThreads), 0, s, a));
 }

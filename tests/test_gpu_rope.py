@@ -436,3 +436,19 @@ def test_append_q_start_that_falls(start, empty):
                     keep[place] = new
     assert np.all(seen | np.all(q == 77, axis=(1, 2)))
     assert np.array_equal(k.reshape(-1, 64), may[0]) and np.array_equal(v.reshape(-1, 64), may[1])
+
+
+@pytest.mark.parametrize("start", [[0, 9, 12, 4, 39], [0, 9, 4, 39, 39], [0, 0, -1, 0, 39], [0, 41, 41, 41, 41]])
+@pytest.mark.parametrize("empty", [0, 1, 40, 300])
+def test_append_reports_every_bad_start(start, empty):
+    # also where every row finds a sequence that holds it, or no row looks at the bad one
+    F = fa3()
+    c = _append_case(np.random.default_rng(37), 2, 1, 64, 64, 8, [9, 3, 1, 26], [9, 3, 1, 40], False, behind=1)
+    B = 4 + empty
+    c["q_start"] = np.concatenate([np.zeros(empty, np.int32), np.asarray(start, np.int32)])
+    c["kv_lens"] = np.concatenate([np.zeros(empty, np.int32), np.full(4, 40, np.int32)])
+    c["table"] = np.arange(B * 6, dtype=np.int32).reshape(B, 6)
+    c["pools"] = [np.zeros((B * 6, 8, 1, 64), np.int8) for _ in range(2)]
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    _run_append(F, c, False, err)
+    assert int(err.item()) == F.FA3_DEVERR_LENS
