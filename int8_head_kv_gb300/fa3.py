@@ -10,6 +10,7 @@ import contextlib
 import ctypes
 import os
 import struct
+import threading
 from collections import OrderedDict
 from typing import Optional
 
@@ -130,8 +131,13 @@ def _need_contig(t: torch.Tensor, dtype, name: str):
 # Cached scratch buffers, one per (call kind, device, stream), at most
 # _WS_PER_KIND streams per (call kind, device): the least recently used entry is
 # dropped when another stream needs one.  Callers that manage memory themselves
-# pass workspace= explicitly and the cache is never touched.
+# pass workspace= explicitly and the cache is never touched.  Host threads may call
+# at once, also on one stream (their calls then share a buffer, and the library
+# enqueues the kernels of a call together): the cache is looked up under a lock.  A
+# buffer dropped while another thread still enqueues work on it goes back to
+# the stream it was allocated on, behind that work.
 _ws_cache: "OrderedDict" = OrderedDict()
+_ws_lock = threading.RLock()
 _WS_PER_KIND = 4
 
 
@@ -148,21 +154,23 @@ def _workspace(key, nbytes: int, device, zero: bool = False, stream=None) -> Opt
     if nbytes == 0:
         return None
     k, s = _ws_key(key, device, stream)
-    ws = _ws_cache.get(k)
-    if ws is None or ws.numel() < nbytes:
-        with torch.cuda.stream(s):
-            ws = (torch.zeros if zero else torch.empty)(nbytes, dtype=torch.uint8, device=device)
-        _ws_cache[k] = ws
-        same = [c for c in _ws_cache if c[:2] == k[:2]]
-        for old in same[:-_WS_PER_KIND]:
-            if old != k:
-                del _ws_cache[old]
-    _ws_cache.move_to_end(k)
+    with _ws_lock:
+        ws = _ws_cache.get(k)
+        if ws is None or ws.numel() < nbytes:
+            with torch.cuda.stream(s):
+                ws = (torch.zeros if zero else torch.empty)(nbytes, dtype=torch.uint8, device=device)
+            _ws_cache[k] = ws
+            same = [c for c in _ws_cache if c[:2] == k[:2]]
+            for old in same[:-_WS_PER_KIND]:
+                if old != k:
+                    del _ws_cache[old]
+        _ws_cache.move_to_end(k)
     return ws
 
 
 def _forget_workspace(key, device, stream=None) -> None:
-    _ws_cache.pop(_ws_key(key, device, stream)[0], None)
+    with _ws_lock:
+        _ws_cache.pop(_ws_key(key, device, stream)[0], None)
 
 
 # --------------------------------------------------------------------- calls
@@ -855,11 +863,12 @@ def _chunk_workspace(nbytes: int, device, stream, dev: int, raw: int):
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
     key = ("chunk", dev, raw)                                # _ws_key's, without asking for the stream again
-    ws = _ws_cache.get(key)
-    if ws is not None and ws.numel() >= nbytes:
-        _ws_cache.move_to_end(key)
-        return ws
-    return _workspace("chunk", nbytes, device, stream=stream)
+    with _ws_lock:
+        ws = _ws_cache.get(key)
+        if ws is not None and ws.numel() >= nbytes:
+            _ws_cache.move_to_end(key)
+            return ws
+        return _workspace("chunk", nbytes, device, stream=stream)
 
 
 def _packed_attn(name, q, k, v, q_scale, k_scale, v_scale, q_start, lens, B, Hkv, sizes, table, softmax_scale, out,

@@ -1,6 +1,9 @@
 """CPU checks of the attention-input and packed-attention calls: the oracle's own pins, the host-side
 refusals of the C ABI and those of the binding."""
 import ctypes
+import threading
+import types
+from collections import OrderedDict
 
 import numpy as np
 import pytest
@@ -196,3 +199,26 @@ def test_calls_in_one_block(L):
     assert L.fa3_call(i, pack(*args), count) == L.fa3_norm_rope(*args) == ERANGE
     args[4] = float("nan")
     assert L.fa3_call(i, pack(*args), count) == L.fa3_norm_rope(*args) == EINVAL
+
+
+def test_workspace_cache_is_looked_up_as_one_step(monkeypatch):
+    # another host thread drops the entry between the look-up and what follows it
+    from int8_head_kv_gb300 import fa3 as F
+    stream, device, threads = types.SimpleNamespace(cuda_stream=77), torch.device("cuda", 0), []
+
+    class Cache(OrderedDict):
+        def get(self, key, default=None):
+            found = super().get(key, default)
+            threads.append(threading.Thread(target=F._forget_workspace, args=("chunk", device, stream)))
+            threads[-1].start()
+            threads[-1].join(0.3)
+            return found
+
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    for look_up in (lambda: F._chunk_workspace(100, device, stream, 0, 77), lambda: F._workspace("chunk", 100, device, stream=stream)):
+        have = torch.empty(100, dtype=torch.uint8)
+        monkeypatch.setattr(F, "_ws_cache", Cache({("chunk", 0, 77): have}))
+        assert look_up() is have
+        for t in threads:
+            t.join()
+        assert not F._ws_cache
