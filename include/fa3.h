@@ -25,7 +25,8 @@
  *     into the optional caller-owned device word `dev_err` (int32, may be
  *     NULL) and skip the offending row; the caller reads the word when it
  *     likes.  Kernels never trap and every wait inside them is bounded.
- *   - Calls on the same stream are ordered; calls that share a workspace
+ *   - Calls on the same stream are ordered, whichever host threads make them: the
+ *     kernels of one call are enqueued together.  Calls that share a workspace
  *     must not run concurrently on different streams.  The library's kernels
  *     are launched as programmatic dependents of the work before them on the
  *     stream (their launch overlaps its tail), and each waits for that work to

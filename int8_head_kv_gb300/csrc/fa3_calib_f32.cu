@@ -367,6 +367,7 @@ FA3_API int fa3_calibrate_perhead_f32(const float* x, int64_t B, int H, int64_t 
   const unsigned chunks = (unsigned)((N + kF32Chunk - 1) / kF32Chunk);
   const unsigned stream_blocks = (unsigned)std::max<int64_t>(1, std::min<int64_t>((N + kF32Threads - 1) / kF32Threads,
                                                                                   (int64_t)sms * 4 / H + 1));
+  const LaunchTogether together(s);
   if (launch_pdl(f32_hist_hi_kernel, dim3(chunks, H), dim3(kF32Threads), smem, s, p) != cudaSuccess ||
       launch_pdl(f32_select_hi_kernel, dim3(H), dim3(kF32Threads), 0, s, p) != cudaSuccess ||
       launch_pdl(f32_hist_lo_kernel, dim3(stream_blocks, H), dim3(kF32Threads), 0, s, p) != cudaSuccess ||

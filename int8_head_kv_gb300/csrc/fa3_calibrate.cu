@@ -950,6 +950,7 @@ FA3_API int fa3_calibrate_perhead(const uint16_t* x, int64_t B, int H, int64_t L
   constexpr double kS = 8.0 * kSampleGroups;
   const double r_want = 3.0 * kS * (double)span / (double)N + 4.0;
   const uint32_t rank = r_want >= kS ? (uint32_t)kS : (uint32_t)r_want;
+  const LaunchTogether together(s);
   const bool use_lists = vec && rank <= (uint32_t)kMaxRank && (double)N * rank / kS <= 0.5 * kListCap;
   const int64_t pieces = (2 * L + kStageBytes - 1) / kStageBytes;
   const int64_t total_items = pieces * B * H;

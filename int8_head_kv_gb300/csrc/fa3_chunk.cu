@@ -1192,6 +1192,7 @@ int chunk_attn(ChunkParams& p, int D, float softmax_scale, void* workspace, size
       return FA3_ECUDA;
     if (dev < 64) set[dev].store(true, std::memory_order_release);
   }
+  const LaunchTogether together(s);
   if (launch_pdl(gqa_chunk_kernel, dim3((unsigned)sms), dim3(kThreadsC), SMEM_CHUNK, s, p) != cudaSuccess)
     return FA3_ECUDA;
   if (sms > 1 && launch_pdl(chunk_combine_kernel, dim3((unsigned)(sms - 1), (unsigned)(p.rows_max / 32)), dim3(256), 0, s,

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
 #include <utility>
 
 #include "fa3.h"
@@ -18,6 +19,15 @@ int check_device(int* num_sms);
 // Optional caller events recorded around the main kernel of a call (fa3_set_kernel_timing).
 void timing_begin(cudaStream_t s);
 void timing_end(cudaStream_t s);
+
+// Held over the launches of a call whose kernels hand data on through a workspace: host threads that share a stream share
+// the binding's workspace of that stream, and between a call's kernels no other call's may come.  (Threads on different
+// streams do not wait for one another, but for streams of the same slot.)
+std::mutex& launch_mutex(cudaStream_t s);
+struct LaunchTogether {
+  std::lock_guard<std::mutex> held;
+  explicit LaunchTogether(cudaStream_t s) : held(launch_mutex(s)) {}
+};
 
 inline int cuda_status(cudaError_t e) { return e == cudaSuccess ? FA3_OK : FA3_ECUDA; }
 

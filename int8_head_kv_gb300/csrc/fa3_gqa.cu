@@ -563,6 +563,7 @@ int gqa_decode(const int8_t* q, const int8_t* k, const int8_t* v, const float* q
                          : block_table ? gqa_decode_kernel<true, false> : gqa_decode_kernel<false, false>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess)
     return FA3_ECUDA;
+  const LaunchTogether together(s);
   timing_begin(s);
   const cudaError_t le = launch_pdl(kernel, dim3(splits, Hkv, B), dim3(kThreads), kSmemBytes, s, a);
   timing_end(s);

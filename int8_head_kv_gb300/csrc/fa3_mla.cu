@@ -1118,6 +1118,7 @@ int mla_decode(const uint16_t* q, const int8_t* ckv, const uint16_t* krope, cons
   prm.sm_log2 = softmax_scale * 1.4426950408889634f;
 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const LaunchTogether together(s);
   {
     const int per_seq = kRows * ((Dl + Dr) / 8);
     if (launch_pdl(mla_prepare_q_kernel, dim3((unsigned)((per_seq + 255) / 256), (unsigned)B), dim3(256), 0, s,

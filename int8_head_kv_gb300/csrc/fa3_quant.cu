@@ -23,6 +23,12 @@ void timing_end(cudaStream_t s) {
   if (g_timing_start && g_timing_stop) cudaEventRecord(g_timing_stop, s);
 }
 
+std::mutex& launch_mutex(cudaStream_t s) {
+  static std::mutex slots[64];
+  const uintptr_t a = reinterpret_cast<uintptr_t>(s);
+  return slots[(a ^ (a >> 6) ^ (a >> 12)) & 63u];
+}
+
 // The attributes of a device do not change: looked up once each (atomic slots: two host threads may both look
 // them up, and both store the same value).  Value: SM count, or -status.
 int check_device(int* num_sms) {

@@ -1,5 +1,8 @@
 """GPU parity of attention over packed new rows (chunks over a paged cache, cross attention) against the
 float64 oracle."""
+import sys
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -495,3 +498,45 @@ def test_calls_that_are_refused():
     for k2, v2 in ((e[:1], e[:1]), (e, e[:, :6]), (e[:, :0], e[:, :0])):
         with pytest.raises((ValueError, F.FA3Error)):
             F.cross_attn_gqa(q, k2, v2, qs, ks, vs, start, lens * 0, SM)
+
+
+def test_host_threads_on_one_stream():
+    # All threads have the same current stream, so their calls share a workspace: the kernels of one call, which hand their
+    # partial results on through it, stay together.  Batches of different sizes, and the decode call's own split.
+    F = fa3()
+    rng = np.random.default_rng(28)
+    cs = [_case(rng, 16, 2, [1, 20], [3000, 900], 64), _case(rng, 8, 4, [5, 1, 70], [900, 2500, 300], 16), _case(rng, 8, 2, [3, 1], [2000, 64], None),
+          _case(rng, 16, 2, [1, 1], [3000, 900], 64, behind=0), _case(rng, 8, 8, [1, 1, 1], [1200, 2, 2900], 32, behind=0)]
+    args = [[_t(c[k]) for k in ("q", "k", "v", "qs", "ks", "vs", "q_start", "lens")] for c in cs]
+    tables = [None if c["page"] is None else _t(c["table"]) for c in cs]
+
+    def call(i):
+        if cs[i]["page"] is None:
+            return F.cross_attn_gqa(*args[i], SM)
+        if i < 3:
+            return F.prefill_attn_gqa_paged(*args[i], tables[i], SM)
+        return F.decode_attn_gqa_paged(*args[i][:6], args[i][7], tables[i], SM)
+    want = [call(i) for i in range(len(cs))]
+    torch.cuda.synchronize()
+    got, failed = [[] for _ in cs], []
+
+    def run(i):
+        try:
+            for _ in range(150):
+                got[i].append(call(i))
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+    interval = sys.getswitchinterval()
+    sys.setswitchinterval(1e-6)
+    try:
+        threads = [threading.Thread(target=run, args=(i,)) for i in range(len(cs))]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    finally:
+        sys.setswitchinterval(interval)
+    torch.cuda.synchronize()
+    assert not failed, failed
+    for i, w in enumerate(want):
+        assert all(torch.equal(o, w) for o in got[i]), f"batch {i}: {sum(not torch.equal(o, w) for o in got[i])} of 150 differ"
