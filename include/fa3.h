@@ -437,7 +437,8 @@ int fa3_norm_rope(const uint16_t* q, const uint16_t* k, const uint16_t* q_weight
  * kv_lens[b] tokens: row q_start[b] + i has position kv_lens[b] - n_b + i, in the
  * cache and in cos_sin, n_b = q_start[b+1] - q_start[b].
  *   code = clamp(round_half_even(y / scale[h]), -127, 127)      (scale 0 -> 0)
- * of q and k is decided as if y and y / scale were computed in float64.
+ * of q and k is that of float64 arithmetic, operation by operation as written above
+ * (x / sqrt(mean + eps), times the weight, the two products of the rotation, the quotient).
  * q        bf16 [n][Hq][D], row stride q_stride elements (heads contiguous), or NULL
  *          (with q_out and q_weight NULL); k, v  bf16 [n][Hkv][D], row strides k_stride, v_stride.
  * q_out    int8 [n][Hq][D];  k_cache, v_cache  int8 [num_pages][page_size][Hkv][D].

@@ -331,9 +331,11 @@ __device__ __forceinline__ int find_sequence(const int32_t* q_start, int B, int 
 //
 // Again, by the whole warp because the row's sum of squares is needed: everything as unevaluated pairs of
 // float32 (Dekker's products by fma, Knuth's sums; float64 runs at a small fraction of the float32 rate here),
-// 1 / sqrt by one correction of the hardware's, and the sign of y - h s for the half step h next to t.  What float32
-// cannot carry (a scale outside [2^-100, 2^100], a sum of squares outside [2^-100, 2^100], infinities and NaN) takes
-// float64.  The pairs hold 45 bits or more of y, so the codes are those of float64 arithmetic.
+// 1 / sqrt by one correction of the hardware's, and the sign of y - h s for the half step h next to t.  The pairs are off
+// by up to 2^-44.7 of the terms |a c| + |b s| (the worst of 60,000 rows of three head sizes), so where y - h s is within
+// 2^-40 of them the pairs cannot tell a value on the half step from one beside it.  There, and for what float32 cannot
+// carry (a scale outside [2^-100, 2^100], a sum of squares outside [2^-100, 2^100], infinities and NaN), float64 decides, in
+// the order of the definition: x / rms, times the weight, the two products, their sum, the quotient.
 constexpr float kTieNorm = 20.f / 16777216.f, kTiePlain = 8.f / 16777216.f;
 
 __device__ __forceinline__ int code64(double y, double s) {
@@ -354,42 +356,43 @@ __device__ __forceinline__ Pair sum(float a, float b) {              // exact
 }
 
 // Value e of a lane's eight (x: the values, w: the weights or ones, c and sn the angles of its four pairs, r:
-// 1 / rms), decided as described above; t: y / scale in float32.
+// 1 / rms), decided as described above; near: the pairs cannot tell.
+constexpr float kPairBand = 9.094947017729282e-13f;                  // 2^-40
 template <bool INTER>
 __device__ __forceinline__ int decide(const float (&x)[8], const float (&w)[8], const float (&c)[4],
-                                      const float (&sn)[4], int e, Pair r, bool norm, bool turn, float s, float rs) {
+                                      const float (&sn)[4], int e, Pair r, bool norm, bool turn, float s, float rs, bool& near) {
   const int pe = INTER ? e / 2 : e % 4;
   const bool sec = INTER ? (e & 1) != 0 : e >= 4;
   const int o = sec ? first<INTER>(pe) : second<INTER>(pe);
   Pair y = {x[e] * w[e], 0.f};                                       // bf16 x bf16: exact
+  float terms = fabsf(y.hi);
   if (turn) {
     const float other = x[o] * w[o];
     const Pair p = product(y.hi, c[pe]), q = product(other, sec ? sn[pe] : -sn[pe]);
     const Pair z = sum(p.hi, q.hi);
+    terms = fabsf(p.hi) + fabsf(q.hi);
     y = sum(z.hi, __fadd_rn(z.lo, __fadd_rn(p.lo, q.lo)));
   }
   if (norm) {
     const Pair p = product(y.hi, r.hi);
+    terms *= r.hi;
     y = Pair{p.hi, __fadd_rn(p.lo, fmaf(y.hi, r.lo, __fmul_rn(y.lo, r.hi)))};
   }
   const float lo = floorf(y.hi * rs), h = lo + 0.5f;                 // the half step next to y / s
   const Pair g = product(h, s);
   const float over = __fadd_rn(__fsub_rn(y.hi, g.hi), __fsub_rn(y.lo, g.lo));
+  near = (norm || turn) && fabsf(over) <= terms * kPairBand;          // x alone is exact
   const int code = (int)(over > 0.0f ? lo + 1.f : over < 0.0f ? lo : rintf(h));
   return max(-127, min(127, code));
 }
-// The same in float64, for what float32 does not hold.
-template <bool INTER>
-__device__ __forceinline__ int decide64(const float (&x)[8], const float (&w)[8], const float (&c)[4],
-                                        const float (&sn)[4], int e, double rstd, bool turn, float s) {
-  const int pe = INTER ? e / 2 : e % 4;
-  const bool sec = INTER ? (e & 1) != 0 : e >= 4;
-  const int o = sec ? first<INTER>(pe) : second<INTER>(pe);
-  const double mine = (double)x[e] * rstd * (double)w[e];
-  double y = mine;
+// The same in float64, one rounding an operation: value x with weight w and angle c, its partner xo, wo and, with the
+// sign of their product, so.
+__device__ __noinline__ int decide64(float x, float w, float c, float xo, float wo, float so, double rms, bool norm,
+                                     bool turn, float s) {
+  double y = norm ? __dmul_rn((double)x / rms, (double)w) : (double)x;
   if (turn) {
-    const double other = (double)x[o] * rstd * (double)w[o];
-    y = sec ? mine * (double)c[pe] + other * (double)sn[pe] : mine * (double)c[pe] - other * (double)sn[pe];
+    const double other = norm ? __dmul_rn((double)xo / rms, (double)wo) : (double)xo;
+    y = __dadd_rn(__dmul_rn(y, (double)c), __dmul_rn(other, (double)so));
   }
   return code64(y, (double)s);
 }
@@ -403,8 +406,7 @@ __device__ __noinline__ uint2 decide_row(const RotArgs& r, const uint16_t* weigh
   float x[8], w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f}, c[4] = {}, sn[4] = {};
   bf16x4(x1, x);
   bf16x4(x2, x + 4);
-  Pair rms = {1.f, 0.f};
-  double rstd = 1.0;
+  Pair rms = {1.f, 0.f};                                             // 1 / rms
   if (weight) {
     Pair ss = {0.f, 0.f};                                            // the squares are exact
     auto add = [&](float v) {
@@ -427,20 +429,12 @@ __device__ __noinline__ uint2 decide_row(const RotArgs& r, const uint16_t* weigh
     const Pair t = product(r0, r0), u = product(m.hi, t.hi);
     const float e = __fsub_rn(__fsub_rn(__fsub_rn(1.f, u.hi), u.lo), fmaf(m.hi, t.lo, __fmul_rn(m.lo, t.hi)));
     rms = Pair{r0, r0 * (e * fmaf(0.375f, e, 0.5f))};
-    if (__any_sync(0xffffffffu, !sound)) {                           // squares that float32 does not hold
-      double sd = 0.0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) sd = fma((double)x[k], (double)x[k], sd);
-      const double ms = row_sum<LANES>(sd) / (double)r.D + (double)r.eps;
-      if (!sound) rstd = 1.0 / sqrt(ms);
-    }
   }
-  if (!again) return codes;
-  if (weight) {
+  if (weight && again) {
     bf16x4(load4(weight + p.o1), w);
     bf16x4(load4(weight + p.o2), w + 4);
   }
-  if (p.rotated) {
+  if (p.rotated && again) {
     const float* tr = r.cos_sin + (int64_t)pos * r.rot + 4 * i;
     const float4 c4 = *reinterpret_cast<const float4*>(tr), s4 = *reinterpret_cast<const float4*>(tr + r.rot / 2);
     c[0] = c4.x, c[1] = c4.y, c[2] = c4.z, c[3] = c4.w;
@@ -448,14 +442,34 @@ __device__ __noinline__ uint2 decide_row(const RotArgs& r, const uint16_t* weigh
   }
   const float rs = rcp_approx(s);
   uint32_t q[2] = {codes.x, codes.y};
+  auto set = [&](int e, int code) {
+    q[e / 4] = (q[e / 4] & ~(0xffu << (8 * (e % 4)))) | (((uint32_t)code & 0xffu) << (8 * (e % 4)));
+  };
+  uint32_t left = is_v || sound ? 0u : again;                        // for float64
 #pragma unroll
   for (int e = 0; e < 8; ++e)
-    if (again >> e & 1u) {
-      const int code = is_v ? quant_code(x[e], s)
-                            : sound ? decide<INTER>(x, w, c, sn, e, rms, weight != nullptr, p.rotated, s, rs)
-                                    : decide64<INTER>(x, w, c, sn, e, rstd, p.rotated, s);
-      q[e / 4] = (q[e / 4] & ~(0xffu << (8 * (e % 4)))) | (((uint32_t)code & 0xffu) << (8 * (e % 4)));
+    if ((again & ~left) >> e & 1u) {
+      bool near = false;
+      set(e, is_v ? quant_code(x[e], s) : decide<INTER>(x, w, c, sn, e, rms, weight != nullptr, p.rotated, s, rs, near));
+      if (near) left |= 1u << e;
     }
+  if (__any_sync(0xffffffffu, left != 0u)) {
+    double root = 1.0;
+    if (weight) {
+      double sd = 0.0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sd = fma((double)x[k], (double)x[k], sd);
+      root = sqrt(row_sum<LANES>(sd) / (double)r.D + (double)r.eps);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (left >> e & 1u) {
+        const int pe = INTER ? e / 2 : e % 4;
+        const bool sec = INTER ? (e & 1) != 0 : e >= 4;
+        const int o = sec ? first<INTER>(pe) : second<INTER>(pe);
+        set(e, decide64(x[e], w[e], c[pe], x[o], w[o], sec ? sn[pe] : -sn[pe], root, weight != nullptr, p.rotated, s));
+      }
+  }
   return make_uint2(q[0], q[1]);
 }
 
@@ -504,7 +518,7 @@ __device__ __forceinline__ void check_lengths(const RopeAppendArgs& a) {
 // test of its neighbourhood take six a value): 3080 tokens of 64 + 8 + 8 heads of 128
 // (95 MB) take 37 us, 2.6 TB/s; half of it is HBM's.  A token's look-ups (sequence,
 // lengths, page) are loads that wait for one another, so the first rows are asked for
-// before them: 16 one-token sequences take 4 us.  Left to 116 registers: with 96 (5
+// before them: 16 one-token sequences take 4 us.  Left to 124 registers: with 96 (5
 // blocks an SM) or 80 (6) the rows spill, 43 and 50 us.
 template <int LANES, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeAppendArgs a) {

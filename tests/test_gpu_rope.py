@@ -1,5 +1,7 @@
 """GPU parity of the attention-input calls: norm_rope (bf16 / float32 results) and rope_append_gqa_paged
 (INT8 codes into the paged cache), against the float64 oracle."""
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -452,3 +454,30 @@ def test_append_reports_every_bad_start(start, empty):
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
     _run_append(F, c, False, err)
     assert int(err.item()) == F.FA3_DEVERR_LENS
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+@pytest.mark.parametrize("D", [64, 80, 128, 192, 256])
+def test_append_ties_after_the_norm(D, eps, monkeypatch):
+    # Rows of one magnitude, and rows of one value beside zeros: the norm leaves +-w, or +-sqrt(D) w, exactly or (with
+    # eps) by a relative eps / (2 x^2) less, which float64 still tells from a half step.  Weights (k + 1/2), and
+    # for the rows of one value (k + 1/2) / sqrt(D) where that is a bf16 number, put them on half steps.  The codes are those of
+    # float64 arithmetic, with rotation by 0 (position 0) and by the table's angles, and without rotation.
+    monkeypatch.setattr(sys.modules[__name__], "EPS", eps)
+    F = fa3()
+    rng = np.random.default_rng([33, D])
+    n, Hq, Hkv = 300, 6, 2
+    for rot in (0, 32):
+        c = _append_case(rng, Hq, Hkv, D, rot, 16, [n, 1, 1], [n, 1, 3], True)
+        H = Hq + 2 * Hkv
+        mag = W.bf16_round(np.exp(rng.uniform(np.log(1e-3 if eps == 0 else 300.0), np.log(3e6), (c["n"], H, 1))).astype(np.float32))
+        c["x"] = mag * rng.choice([-1.0, 1.0], (c["n"], H, D)).astype(np.float32)
+        c["sc"][:] = np.float32(1.0)
+        c["sc"][2] = np.float32(4.0)
+        c["w"] = [W.bf16_round((rng.integers(0, 60, D) + 0.5).astype(np.float32)) for _ in range(2)]
+        if D in (64, 256):
+            lone = rng.random((c["n"], H)) < 0.3
+            at = rng.integers(0, D, (c["n"], H))
+            c["x"][lone] *= (np.arange(D) == at[lone][:, None])
+            c["w"] = [W.bf16_round(w / np.where(rng.random(D) < 0.5, 1.0, D ** 0.5).astype(np.float32)) for w in c["w"]]
+        _same(_run_append(F, c, rot == 32), _ref_append(c, rot == 32))
