@@ -707,7 +707,7 @@ def norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], cos_sin: Optional[torc
             elif k_out.dtype is not t or k_out.shape != ksh or k_out.get_device() != dev:
                 raise ValueError("k_out must have the input's shape and device and q_out's type")
             kos, kop = _rows4(k_out, "k_out", True), k_out.data_ptr()
-        if B * S and Hq and D:
+        if B * S and D:                                      # a q without heads is refused by the call
             i, pack, count = _CALLS["fa3_norm_rope"]
             st = lib().fa3_call(i, pack(q.data_ptr(), kp, qw, kw, eps, cp, table_len, rot, bool(interleaved), pp,
                                         q_out.data_ptr(), kop, t is _F32, B, S, Hq, Hkv, D, *qs, *ks, *qos, *kos, ep,

@@ -481,3 +481,14 @@ def test_append_ties_after_the_norm(D, eps, monkeypatch):
             c["x"][lone] *= (np.arange(D) == at[lone][:, None])
             c["w"] = [W.bf16_round(w / np.where(rng.random(D) < 0.5, 1.0, D ** 0.5).astype(np.float32)) for w in c["w"]]
         _same(_run_append(F, c, rot == 32), _ref_append(c, rot == 32))
+
+
+def test_k_without_heads_of_q_is_refused():
+    # the C call refuses a q without heads; a k_out that nothing writes must not come back
+    F = fa3()
+    x = bf16_dev(_values(np.random.default_rng(32), (6, 4, 128)))
+    for shape in (x, x.reshape(2, 3, 4, 128)):
+        with pytest.raises(F.FA3Error):
+            F.norm_rope(shape[..., :0, :], shape, None, None)
+    q, k = F.norm_rope(x[:0], x[:0, :2], None, None)                        # no tokens: nothing to write
+    assert q.shape == (0, 4, 128) and k.shape == (0, 2, 128)
