@@ -472,7 +472,8 @@ int fa3_rope_append_gqa_paged(const uint16_t* q, const uint16_t* k, const uint16
  *          [q_start[0], q_start[B]) and those of a sequence with bad lengths
  *          (FA3_DEVERR_LENS) are left as they were; all are, if q_start falls
  *          and rises again so that sequences share rows.
- * scales   finite; q_scale, k_scale >= 0 (a softmax scale of 0 or below is refused).
+ * scales   finite; q_scale, k_scale >= 0 (a softmax scale of 0 or below is refused); scores
+ *          |s[t]| below 2^26.
  * Supported: D = 128, Hq / Hkv <= 128, n < 2^27 - 1; q, k, v, out 16-byte aligned.
  * workspace  fa3_chunk_workspace_size(n, B, Hq, Hkv, D) bytes, 16-byte aligned
  *          (partial results of row blocks whose keys are shared out, 20 or 40 MB);

@@ -32,8 +32,11 @@
 // Numbers.  int8 codes are exact in fp16 and a 128-term sum of their products stays
 // below 2^24, so kind::f16 MMAs with float32 accumulation give the exact integer score
 // (the integer tensor rate of sm_103a is far below it).  P is rounded to fp16 relative to
-// a lazily moved row maximum (off by 2^-11 of a weight at most, where the result is rounded
-// to bf16, 2^-8); the row sum is float32 over the unrounded weights, and O, partial results
+// a reference that the row's maximum lies 2^7 to 2^15 above (it moves lazily): a weight is off by
+// 2^-11 of itself, or by 2^-32 of the row's largest where fp16 is subnormal, so T keys are off by
+// T 2^-32 of max|v| beside the bf16 rounding of the result, 2^-8 of it.  (With the maximum at 1
+// the weights below 2^-25 were lost, but counted in the row sum: 131072 keys off by 2^-8 of max|v|.)
+// The row sum is float32 over the unrounded weights, and O, partial results
 // and their merging are float32.  P is written over its scores in TMEM and is the A operand
 // of P.V.  TMEM: O_0, O_1, S_0, S_1, 128 columns each.
 //
@@ -929,10 +932,12 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
             mx = fmaxf(mx, m);
           }
           FA3_TMEM_LD16(scol, v0);
-          mx *= c;
-          // Lazy rescale: the reference maximum moves only when the row maximum grew by more than 8
-          // (log2 units); then O (P.V up to this buffer's step before) is scaled in place.
-          const bool grow = mx > m_run + 8.f || (m_run == -CUDART_INF_F && mx != -CUDART_INF_F);
+          // The reference, 7 (log2 units) below the row's maximum.  Rounded up, and the difference below is exact where
+          // it matters: P stays below 2^15 whatever the size of the scores.
+          mx = __fadd_ru(__fmul_ru(mx, c), -7.f);
+          // Lazy rescale: the reference moves only when it would by more than 8; then O (P.V up to this buffer's
+          // step before) is scaled in place.  No key yet: -inf - (-inf) is no difference.
+          const bool grow = mx - m_run > 8.f;
           const bool scale_o = grow && m_run != -CUDART_INF_F;
           if (__any_sync(0xffffffffu, scale_o)) {
             if (!warp_wait(bar(B_PV_DONE + x), (ph - 1u) & 1u, lane, abort_flag, p.err)) {

@@ -540,3 +540,78 @@ def test_host_threads_on_one_stream():
     assert not failed, failed
     for i, w in enumerate(want):
         assert all(torch.equal(o, w) for o in got[i]), f"batch {i}: {sum(not torch.equal(o, w) for o in got[i])} of 150 differ"
+
+
+def _exact(c, values=None):
+    """The packed attention of the case in float64, a sequence and KV head at a time; values in place of c's v."""
+    out = np.full(c["q"].shape, KEEP)
+    Hkv = c["k"].shape[2]
+    G = c["q"].shape[1] // Hkv
+    v_all = c["v"] if values is None else values
+    for b, kv in enumerate(c["lens"]):
+        s, e = int(c["q_start"][b]), int(c["q_start"][b + 1])
+        t = np.arange(kv)
+        at = (b, t) if c["page"] is None else (c["table"][b, t // c["page"]], t % c["page"])
+        for g in range(Hkv if e > s else 0):
+            q = c["q"][s:e, g * G:(g + 1) * G].reshape(-1, 128).astype(np.float64)
+            x = q @ c["k"][at][:, g].T.astype(np.float64)
+            x *= (np.tile(c["qs"][g * G:(g + 1) * G], e - s).astype(np.float64) * float(c["ks"][g]) * SM)[:, None]
+            if c["page"] is not None:
+                x[t[None] > (kv - (e - s) + np.repeat(np.arange(e - s), G))[:, None]] = -np.inf
+            x = np.exp(x - x.max(1, keepdims=True))
+            y = (x @ v_all[at][:, g].astype(np.float64)) / x.sum(1, keepdims=True) * float(c["vs"][g])
+            out[s:e, g * G:(g + 1) * G] = y.reshape(e - s, G, 128)
+    return out
+
+
+def _tail_case(T, rows, weight, page, Hq, B):
+    """B sequences over the same pages: one key that takes the weight 1 and T - 1 of weight 2^-weight each; values 0 and
+    +-100 or so.  (With a unit to each SM no key is shared out, so one running maximum sees them all.)"""
+    rng = np.random.default_rng([26, T, rows])
+    mp = -(-T // page)
+    c = dict(q=np.full((B * rows, Hq, 128), 64, np.int8), q_start=np.arange(0, B * rows + 1, rows, dtype=np.int32),
+             lens=np.full(B, T, np.int32), page=page, k=np.zeros((mp, page, 1, 128), np.int8),
+             table=np.broadcast_to(rng.permutation(mp).astype(np.int32), (B, mp)), qs=np.full(Hq, 0.01, np.float32),
+             ks=np.full(1, weight / (128 * 64 * 100 * 0.01 * SM * 1.4426950408889634), np.float32),
+             vs=np.full(1, 0.02, np.float32))
+    value = rng.integers(90, 110, 128).astype(np.int8) * rng.choice([-1, 1], 128).astype(np.int8)
+    c["v"] = np.broadcast_to(value, c["k"].shape).copy()
+    sink = (c["table"][0, 70 // page], 70 % page)
+    c["k"][sink], c["v"][sink] = 100, 0
+    return c
+
+
+@pytest.mark.parametrize("T,rows,weight,page,Hq,units", [
+    (131072, 1, 25.2, 64, 8, 1), (131072, 1, 24.6, 64, 8, 1), (131072, 1, 26.9, 7, 2, 1), (100001, 20, 24.6, 64, 8, 1),
+    (131072, 3, 28.0, 128, 128, 2), (20001, 1, 22.0, 48, 5, 1), (1 << 20, 1, 27.5, 64, 2, 1)])
+def test_long_tails_of_small_weights(T, rows, weight, page, Hq, units):
+    """A weight is off by 2^-11 of itself (fp16), or by 2^-32 of the largest (fp16's subnormals, half of 2^-24 against a
+    largest of 2^7 or more), by the float32 score, |s| log2 units, 2^-22 |s|, and by the exponential, 2^-22; the sum of
+    the weights counts them before the rounding.  So the output is off by those shares of the weighted mean of |v|, by
+    T 2^-32 of max|v|, and by half a bf16 step."""
+    F = fa3()
+    B = torch.cuda.get_device_properties(0).multi_processor_count // units
+    c = _tail_case(T, rows, weight, page, Hq, B)
+    one = dict(c, q=c["q"][:rows], q_start=c["q_start"][:2], lens=c["lens"][:1])
+    got, ref, mean = _run(F, c), _exact(one), np.abs(_exact(one, np.abs(c["v"])))
+    tol = 2.0 ** -8 * np.abs(ref) * (1 + 2.0 ** -8) + (2.0 ** -11 + 2.0 ** -22 * (weight + 2) + 2.0 ** -22) * mean \
+        + T * 2.0 ** -32 * 127 * float(c["vs"].max())
+    d = np.abs(got.reshape((B,) + ref.shape) - ref)
+    print(f"{T} keys of 2^-{weight}: {float((d / tol).max()):.3f} of the tolerance, largest output {float(np.abs(ref).max()):.2e}, "
+          f"error {float(d.max()):.2e}")
+    assert np.all(d <= tol)
+
+
+@pytest.mark.parametrize("scale", [1.0, 30.0, 100.0])
+@pytest.mark.parametrize("page", [64, 7, None])
+def test_very_large_scores(scale, page):
+    """Scores of up to 2^17 code products times 0.013 to 127 log2 units, 2^24 in all: the largest weights stay within fp16's
+    range.  The reference of the weights is rounded up twice, by 2 units at most, so the largest is 2^3 or more and the others
+    are off by 2^-28 of it, beside 2^-11 and, for five roundings of the factor, 2^-21 of their distance x from the largest,
+    x 2^-x < 1 of it."""
+    F = fa3()
+    c = _case(np.random.default_rng(29), 8, 2, [1, 40, 3], [500, 300, 700], page, behind=0)
+    c["qs"][:], c["ks"][:] = np.float32(0.1 * scale), np.float32(scale)
+    got, ref, mean = _run(F, c), _exact(c), np.abs(_exact(c, np.abs(c["v"])))
+    tol = 2.0 ** -8 * np.abs(ref) * (1 + 2.0 ** -8) + (2.0 ** -11 + 2.0 ** -21) * mean + 700 * 2.0 ** -28 * 127 * float(c["vs"].max())
+    assert np.all(np.isfinite(got)) and np.all(np.abs(got - ref) <= tol), float((np.abs(got - ref) / tol).max())
