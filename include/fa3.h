@@ -471,7 +471,7 @@ int fa3_rope_append_gqa_paged(const uint16_t* q, const uint16_t* k, const uint16
  * q        int8 [n][Hq][D];  out  bf16 [n][Hq][D].  Rows outside
  *          [q_start[0], q_start[B]) and those of a sequence with bad lengths
  *          (FA3_DEVERR_LENS) are left as they were; all are, if q_start falls
- *          and rises again so that sequences share rows.
+ *          (sequences might share rows).
  * scales   finite; q_scale, k_scale >= 0 (a softmax scale of 0 or below is refused); scores
  *          |s[t]| below 2^26.
  * Supported: D = 128, Hq / Hkv <= 128, n < 2^27 - 1; q, k, v, out 16-byte aligned.

@@ -155,7 +155,7 @@ constexpr int kLeastBox = 8;
 struct Seq {
   int q0, nq, nkv;
 };
-// The new rows and keys of sequence b; nq = 0 for an empty or invalid sequence.
+// The new rows and keys of sequence b; nq = 0 for an empty or invalid sequence, -1 for one that ends before it begins.
 __device__ __forceinline__ Seq sequence_of(const ChunkParams& p, int b, bool report) {
   Seq s;
   s.q0 = p.q_start[b];
@@ -164,7 +164,7 @@ __device__ __forceinline__ Seq sequence_of(const ChunkParams& p, int b, bool rep
   s.nq = q1 - s.q0;
   if (s.q0 < 0 || q1 < s.q0 || q1 > p.n || (s.nq > 0 && (s.nkv < (p.causal ? s.nq : 0) || s.nkv > p.T))) {
     if (report) set_dev_err(p.err, FA3_DEVERR_LENS);
-    s.nq = 0;
+    s.nq = q1 < s.q0 ? -1 : 0;
   }
   return s;
 }
@@ -255,7 +255,7 @@ __device__ __forceinline__ Line<I> make_line(const ChunkParams& p, int lane, boo
   a.per_head = sequence_cost<I>(p, s0);
   a.upto = warp_scan<I>(a.per_head * (I)p.Hkv, lane);
   int blocks = blocks_of(p, s0);
-  int64_t rows = s0.nq;
+  bool falls = s0.nq < 0;
   Line<I> l;
   l.total = __shfl_sync(0xffffffffu, a.upto, 31);
   if (p.B > 32) {
@@ -265,18 +265,16 @@ __device__ __forceinline__ Line<I> make_line(const ChunkParams& p, int lane, boo
       const Seq s = sequence_of(p, b, report);
       sum += sequence_cost<I>(p, s);
       blocks += blocks_of(p, s);
-      rows += s.nq;
+      falls |= s.nq < 0;
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     l.total += sum * (I)p.Hkv;
   }
   blocks = __reduce_add_sync(0xffffffffu, blocks);
-  // More rows than there are (a q_start that falls and rises again): the bounds of I do not hold, there is no plan.
-  // A lane's rows are counted up to 2^27 - 1, so that 32 of them fit 32 bits and one lane's are beyond any n < 2^27.
-  const uint32_t most_rows = (1u << 27) - 1, all = __reduce_add_sync(0xffffffffu, (uint32_t)min(rows, (int64_t)most_rows));
-  if (all > (uint32_t)p.n) {
-    if (report && lane == 0) set_dev_err(p.err, FA3_DEVERR_LENS);
+  // A q_start that falls: where it rises again sequences may share rows, which two units would write, and the rows may be more
+  // than n, which the bounds of I rest on.  There is no plan, then.
+  if (__any_sync(0xffffffffu, falls)) {
     l.total = 0;
     blocks = 0;
   }

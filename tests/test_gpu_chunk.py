@@ -615,3 +615,19 @@ def test_very_large_scores(scale, page):
     got, ref, mean = _run(F, c), _exact(c), np.abs(_exact(c, np.abs(c["v"])))
     tol = 2.0 ** -8 * np.abs(ref) * (1 + 2.0 ** -8) + (2.0 ** -11 + 2.0 ** -21) * mean + 700 * 2.0 ** -28 * 127 * float(c["vs"].max())
     assert np.all(np.isfinite(got)) and np.all(np.abs(got - ref) <= tol), float((np.abs(got - ref) / tol).max())
+
+
+@pytest.mark.parametrize("start", [[0, 9, 4, 39], [0, 4000, 9, 39], [5, 0, 9, 39], [0, 20, 39, 30]])
+@pytest.mark.parametrize("empty", [0, 31, 40])
+@pytest.mark.parametrize("page", [16, None])
+def test_falling_q_start_with_room_behind(start, empty, page):
+    # sequences that share rows though all their rows together are fewer than n: no row is written, also where the fall is beyond
+    # the sequences that a warp looks at first, or at their edge
+    F = fa3()
+    c = _case(np.random.default_rng(38), 8, 2, [4, 5, 30] + [0] * empty, [50, 60, 70] + [1] * empty, page, behind=25)
+    c["q_start"] = np.concatenate([np.full(empty, start[0], np.int32), np.asarray(start, np.int32)])
+    c["lens"] = np.concatenate([np.ones(empty, np.int32), np.array([50, 60, 70], np.int32)])
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = _run(F, c, err)
+    assert c["q"].shape[0] == 64 and int(err.item()) == F.FA3_DEVERR_LENS
+    assert np.all(got == KEEP)
