@@ -451,27 +451,25 @@ __device__ __forceinline__ void walk_parts(const ChunkParams& p, const Seq& s0, 
   }
 }
 
-// wait_bar for short waits.  Reading the global timer takes longer than most of them last, so the limit is a
-// number of tests: one that fails suspends the thread for 3.94 us, 2^18 of them are a second.  The abort flag is
-// looked at every 256.  A wait for a part of the ring may last as long as a unit of the longest context takes (0.3 s
-// for 16 million keys), and has four seconds.
-constexpr uint32_t kMostTests = 1u << 18, kMostTestsPart = 1u << 20;
-template <uint32_t MOST = kMostTests>
-__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, int32_t* err) {
-#pragma unroll 1
-  for (uint32_t i = 0; i < MOST; ++i) {
-    if (mbar_try(bar, parity)) return true;
-    if ((i & 255u) == 255u && *abort_flag) return false;
+// wait_bar for short waits, with bounded_wait's rare look at the clock, in ticks of 2^20 ns (1.05 ms).  A second for a wait
+// within a unit; a wait for a part of the ring may last as long as a unit of the longest context takes (2.3 us a key
+// tile), and has four seconds and 8 us a key tile.
+constexpr uint32_t kWaitTicks = 954;
+__device__ __forceinline__ uint32_t part_ticks(const ChunkParams& p) { return 4 * kWaitTicks + ((uint32_t)p.T >> 14); }
+__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, int32_t* err,
+                                          uint32_t limit = kWaitTicks) {
+  const Waited w = bounded_wait([&] { return mbar_try(bar, parity); }, [&] { return *abort_flag != 0u; },
+                                [] { return (uint32_t)(global_ns() >> 20); }, limit);
+  if (w == Waited::kLate) {
+    *abort_flag = 1u;
+    set_dev_err(err, FA3_DEVERR_TIMEOUT);
   }
-  *abort_flag = 1u;
-  set_dev_err(err, FA3_DEVERR_TIMEOUT);
-  return false;
+  return w == Waited::kDone;
 }
 // The same for a warp, whose lanes have to agree.
-template <uint32_t MOST = kMostTests>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int lane, volatile uint32_t* abort_flag,
-                                          int32_t* err) {
-  return warp_all(wait_long<MOST>(bar, parity, abort_flag, err));
+                                          int32_t* err, uint32_t limit = kWaitTicks) {
+  return warp_all(wait_long(bar, parity, abort_flag, err, limit));
 }
 
 // The wait for this thread's TMEM loads, which also orders the uses of v behind it.
@@ -595,8 +593,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
   Part* const ring = reinterpret_cast<Part*>(smem + OFF_PARTS);
   uint32_t parts = 0;                                         // taken (by warp 3: written)
   auto next_part = [&]() {                                    // false: none left; otherwise the part is ring[parts % kRing]
-    return warp_wait<kMostTestsPart>(bar(B_PART_FULL) + 8u * (parts % kRing), (parts / kRing) & 1u, lane, abort_flag,
-                                     p.err) &&
+    return warp_wait(bar(B_PART_FULL) + 8u * (parts % kRing), (parts / kRing) & 1u, lane, abort_flag, p.err, part_ticks(p)) &&
            ring[parts % kRing].nt >= 0;
   };
   auto part_read = [&]() {
@@ -607,8 +604,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
 
   if (warp == 3) {
     auto put = [&](const Part& u) {
-      if (!warp_wait<kMostTestsPart>(bar(B_PART_EMPTY) + 8u * (parts % kRing), ((parts / kRing) & 1u) ^ 1u, lane,
-                                     abort_flag, p.err))
+      if (!warp_wait(bar(B_PART_EMPTY) + 8u * (parts % kRing), ((parts / kRing) & 1u) ^ 1u, lane, abort_flag, p.err,
+                     part_ticks(p)))
         return false;
       if (lane == 0) {
         ring[parts % kRing] = u;

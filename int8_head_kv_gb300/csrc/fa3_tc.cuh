@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "fa3_common.cuh"
+#include "fa3_wait.cuh"
 
 namespace fa3 {
 namespace {
