@@ -578,16 +578,16 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
     Lane8 pt = p;
     pt.rotated = p.rotated && !is_v;                        // v: multiplied by 1 and 0
     const Turn w = make_turn<INTER>(pt, a.r, pl.pos, T.weight, i);
-    float band = 0.f;                                       // the largest factor, times the tie band
+    float band = 0.f;                                       // the largest factor (NaN if one is), times the tie band
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       float g0, g1, g2, g3;
       f32x2_unpack(w.ac[j], g0, g1);
       f32x2_unpack(w.nbs[j], g2, g3);
-      band = fmaxf(band, fmaxf(fmaxf(fabsf(g0), fabsf(g1)), fmaxf(fabsf(g2), fabsf(g3))));
+      band = max3_nan(max3_nan(band, fabsf(g0), fabsf(g1)), fabsf(g2), fabsf(g3));
       f32x2_unpack(w.bc[j], g0, g1);
       f32x2_unpack(w.as[j], g2, g3);
-      band = fmaxf(band, fmaxf(fmaxf(fabsf(g0), fabsf(g1)), fmaxf(fabsf(g2), fabsf(g3))));
+      band = max3_nan(max3_nan(band, fabsf(g0), fabsf(g1)), fabsf(g2), fabsf(g3));
     }
     band *= norm ? kTieNorm : kTiePlain;
     const float lim_min = 0.5f - 32768.f * (norm ? kTieNorm : kTiePlain);

@@ -492,3 +492,30 @@ def test_k_without_heads_of_q_is_refused():
             F.norm_rope(shape[..., :0, :], shape, None, None)
     q, k = F.norm_rope(x[:0], x[:0, :2], None, None)                        # no tokens: nothing to write
     assert q.shape == (0, 4, 128) and k.shape == (0, 2, 128)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_codes_of_nan(interleaved, monkeypatch):
+    monkeypatch.setattr(sys.modules[__name__], "bf16_dev", lambda a: torch.from_numpy(a).to(torch.bfloat16).cuda())   # NaN too
+    # NaN in a weight or an angle, among finite ones: the code of those values is the one that quantize_append gives NaN
+    F = fa3()
+    rng = np.random.default_rng(39)
+    c = _append_case(rng, 4, 2, 128, 64, 16, [30, 1], [30, 9], True)
+    c["sc"][0] = c["sc"][1]
+    ref = [a.copy() for a in _ref_append(c, interleaved)]
+    pool, one = (torch.zeros(1, 1, 1, 8, dtype=torch.int8, device="cuda"), torch.ones(1, device="cuda"))
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    F.quantize_append(torch.full((1, 1, 1, 8), float("nan"), dtype=torch.bfloat16, device="cuda"), one, pool, zero)
+    nan = int(pool[0, 0, 0, 0])
+    c["w"] = [w.copy() for w in c["w"]]
+    c["w"][0][100], c["w"][1][101] = np.nan, np.nan                         # beyond the rotated values: these alone
+    c["cs"][5, 3] = np.nan                                                  # position 5: both members of pair 3
+    ref[0][:31, :, 100] = nan
+    row, pair = (5, (6, 7) if interleaved else (3, 35))                     # sequence 0's token at position 5
+    for d in pair:
+        ref[0][row, :, d] = nan
+        ref[1][c["table"][0, 0], 5, :, d] = nan
+    for b, n, kv in ((0, 30, 30), (1, 1, 9)):
+        for p in range(kv - n, kv):
+            ref[1][c["table"][b, p // 16], p % 16, :, 101] = nan
+    _same(_run_append(F, c, interleaved), ref)
