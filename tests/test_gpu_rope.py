@@ -519,3 +519,44 @@ def test_append_codes_of_nan(interleaved, monkeypatch):
         for p in range(kv - n, kv):
             ref[1][c["table"][b, p // 16], p % 16, :, 101] = nan
     _same(_run_append(F, c, interleaved), ref)
+
+
+def _passes_a_task(tokens, heads, D):
+    # heads_per_task of the kernels: passes of 32 / lanes rows that a warp takes of one token
+    rows = 4 if D <= 64 else 2 if D <= 128 else 1
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    return max(1, min(8, tokens * -(-heads // rows) // (sms * 24)))
+
+
+# tokens enough for tasks of several passes: 20 + 5 and 35 + 7 heads leave a part of a task and of a pass at the end
+@pytest.mark.parametrize("tokens,Hq,Hkv,D,rot,interleaved,norm,passes", [
+    (2400, 20, 5, 128, 128, False, True, 8), (2700, 35, 7, 64, 64, True, True, 8), (1300, 20, 5, 256, 128, False, False, 8),
+    (1100, 20, 5, 128, 64, True, False, 3), (1700, 35, 7, 80, 32, False, True, 8), (700, 35, 7, 192, 192, True, True, 7)])
+def test_norm_rope_tasks_of_several_passes(tokens, Hq, Hkv, D, rot, interleaved, norm, passes):
+    F = fa3()
+    assert _passes_a_task(tokens, Hq + Hkv, D) >= passes
+    rng = np.random.default_rng([34, tokens, D])
+    x = _values(rng, (tokens, Hq + Hkv, D))
+    w = [W.bf16_round(1 + 0.3 * rng.standard_normal(D).astype(np.float32)) if norm else None for _ in range(2)]
+    pos, cs = rng.integers(0, 300, tokens).astype(np.int32), _table(300, rot)
+    xd, wd, tab, at = bf16_dev(x), [None if a is None else bf16_dev(a) for a in w], _t(cs), _t(pos)
+    want = [O.norm_rope(x[:, sl], a, EPS, cs, pos, interleaved) for sl, a in ((slice(0, Hq), w[0]), (slice(Hq, None), w[1]))]
+    for dt in (torch.bfloat16, torch.float32):
+        for got, ref in zip(F.norm_rope(xd[:, :Hq], xd[:, Hq:], tab, at, *wd, EPS, interleaved, out_dtype=dt), want):
+            _check(got, *ref, dt is torch.float32)
+    plain = F.norm_rope(xd[:, :Hq], xd[:, Hq:], tab, at, *wd, EPS, interleaved)
+    F.norm_rope(xd[:, :Hq], xd[:, Hq:], tab, at, *wd, EPS, interleaved, q_out=xd[:, :Hq], k_out=xd[:, Hq:])   # in place
+    assert torch.equal(xd[:, :Hq], plain[0]) and torch.equal(xd[:, Hq:], plain[1])
+
+
+@pytest.mark.parametrize("tokens,Hq,Hkv,D,rot,page,interleaved,norm,passes", [
+    (2000, 20, 5, 128, 128, 64, False, True, 8), (2300, 35, 7, 64, 64, 16, True, True, 8), (1000, 20, 5, 256, 128, 7, False, False, 8),
+    (900, 20, 5, 128, 64, 24, True, False, 3), (1400, 35, 7, 80, 32, 64, False, True, 8), (700, 35, 7, 192, 192, 16, True, True, 8)])
+def test_append_tasks_of_several_passes(tokens, Hq, Hkv, D, rot, page, interleaved, norm, passes):
+    F = fa3()
+    assert _passes_a_task(tokens, Hq + 2 * Hkv, D) >= passes
+    rng = np.random.default_rng([35, tokens, D])
+    c = _append_case(rng, Hq, Hkv, D, rot, page, [tokens - 44, 1, 0, 43], [tokens, 77, 3, 43], norm)
+    c["sc"][[0, 9, Hq - 1, Hq + 3]] = np.float32(0.0)                       # heads of later passes
+    c["sc"][[11, Hq + 4]] = np.float32(2.0 ** -120)                         # decided in float64
+    _same(_run_append(F, c, interleaved), _ref_append(c, interleaved))
