@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import workloads as W
-from helpers import bf16_dev, fa3
+from helpers import assert_attn_close, attn_errors, bf16_dev, fa3
 from oracle import fa3_oracle as O
 
 pytestmark = pytest.mark.gpu
@@ -631,3 +631,23 @@ def test_falling_q_start_with_room_behind(start, empty, page):
     got = _run(F, c, err)
     assert c["q"].shape[0] == 64 and int(err.item()) == F.FA3_DEVERR_LENS
     assert np.all(got == KEEP)
+
+
+@pytest.mark.parametrize("Hq,Hkv,q_lens,kv_lens,page", [
+    (16, 2, [1], [9001], 48), (16, 2, [5], [9001], 48), (16, 2, [20], [9001], 7), (8, 8, [1, 1, 1], [4096, 777, 64], 64),
+    (16, 2, [1, 260, 1, 1], [3000, 1300, 100, 700], 64), (35, 7, [5, 1, 3], [6001, 900, 64], 48), (32, 8, [448, 60], [2048, 300], None),
+    (16, 16, [1, 1, 1], [1500, 64, 900], None)])
+def test_relative_rms_of_long_contexts(Hq, Hkv, q_lens, kv_lens, page):
+    # outputs that are means over many keys are small beside max|v|: the project's bar on the relative RMS
+    F = fa3()
+    rng = np.random.default_rng([27, Hq, q_lens[0], kv_lens[0]])
+    c = _case(rng, Hq, Hkv, q_lens, kv_lens, page, behind=0)
+    got, ref = _run(F, c), _exact(c)
+    for b in range(len(q_lens)):
+        s, e = c["q_start"][b], c["q_start"][b + 1]
+        assert_attn_close(got[s:e], ref[s:e], True, f"{kv_lens[b]} keys, {e - s} rows")
+        # A head alone: the rounding of the output is up to 2^-8 of each value (and 2^-8 / sqrt 3 on average where
+        # all lie just above powers of two, which is beyond the bar), the weights' 2^-11 in product and sum.
+        for h in range(Hq):
+            _, rms = attn_errors(got[s:e, h], ref[s:e, h])
+            assert rms <= 2.0 ** -8 + 2.0 ** -10, f"{kv_lens[b]} keys, {e - s} rows, head {h}: relative RMS {rms:.3e}"
