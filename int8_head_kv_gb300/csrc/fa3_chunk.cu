@@ -41,15 +41,16 @@
 // of P.V.  TMEM: O_0, O_1, S_0, S_1, 128 columns each.
 //
 // What bounds it (64 query and 8 KV heads, one GB300).  4096 new rows on a context of
-// 8192: 738 us, 1117 TFLOP/s.  A step takes 2150 cycles, of which the tensor pipe works
-// half: the rest is the chain scores, softmax, P.V, scores of each of the two buffers with
-// a barrier at every arrow, and shared memory, which moves 320 KB a key tile (int8 tile in
-// and out, fp16 tile in, Q, K and V into the MMAs: 2500 cycles at 128 bytes each).
-// 16 one-token rows of 4096 keys: 51 us, 2.6 TB/s.  A key tile takes 2500 cycles of the
-// same chain, for 8 rows of 128; neither a second int8 tile on its way (53.7 us) nor four
-// warps on a tile's softmax (55.1 us) shortened it, and more code costs every case: the
-// roles' loops share the SM's instruction cache.  About 8 us of a small call are the
-// launch, the plan (2 us), the first tiles' way (3 us) and the combine kernel (3 us).
+// 8192: 682 us, 1209 TFLOP/s.  The tensor pipe works half of the time: the rest is the chain
+// scores, softmax, P.V, scores of each of the two buffers with a barrier at every arrow
+// (the softmax reads every score from TMEM twice, for the maximum and for the weight), and
+// shared memory, which moves 320 KB a key tile (int8 tile in and out, fp16 tile in, Q, K and V
+// into the MMAs: 2500 cycles at 128 bytes each).  16 one-token rows of 4096 keys: 50 us,
+// 2.7 TB/s.  A key tile takes 2500 cycles of the same chain, for 8 rows of 128; neither a second
+// int8 tile on its way nor four warps on a tile's softmax shortened it (53.7 and 55.1 us where
+// it took 51.4 and 53.6), and more code costs every case: the roles' loops share the SM's
+// instruction cache.  About 8 us of a small call are the launch, the plan (2 us), the first
+// tiles' way (3 us) and the combine kernel (3 us).
 //
 // Every wait is bounded; on time-out the kernel sets FA3_DEVERR_TIMEOUT, waits for its
 // copies and MMAs, frees its TMEM and returns.
@@ -107,10 +108,11 @@ static_assert(SMEM_CHUNK <= 232448, "shared memory");
 // The line's unit is an eighth of a step with two row tiles: what a key tile costs with two row tiles and with one, a
 // unit's cost beside its steps (its query rows, pipeline fill and epilogue), the least part of the line a CTA takes,
 // and the least where short units go one to a CTA (16 one-token units of 128 keys: 17 us in parts of two such units,
-// 12 so).  A part of 40 is a short unit of one key tile: one token of 1024 keys takes 19.5 us in parts of 64, 17.9 of
-// 40 and 16.6 of 32, which cut short units (one token of 64 keys 10.4 instead of 10.0).  Fitted over the CTAs of
-// ragged batches: 1950 cycles a step with two row tiles, 2200 with one, 7000 to 8000 a unit.  Eight sequences of up
-// to 512 new rows took 113 us with a unit counted as 2 steps, 98.6 as 3 and every step alike, 92.3 so.
+// 12 so).  A part of 40 is a short unit of one key tile: one token of 1024 keys takes 18.8 us in parts of 64, 16.7 of
+// 40 and 15.8 of 32, which cut short units (one token of 64 keys 10.2 instead of 10.0, of 4096 keys 22.5 instead of
+// 21.4).  Fitted over the CTAs of ragged batches: 1950 cycles a step with two row tiles, 2200 with one, 7000 to 8000 a
+// unit.  Eight sequences of up to 512 new rows took 113 us with a unit counted as 2 steps, 98.6 as 3 and every step
+// alike, 92.3 so (87 now).
 constexpr int kTileDual = 16, kTileSingle = 9, kUnitCost = 30, kLeastPart = 40, kLeastInner = 32;
 static_assert(kLeastInner >= kTileDual, "a part inside a unit, behind its fixed cost, holds a key tile");
 
@@ -186,7 +188,8 @@ __device__ __forceinline__ int cost_of(const ChunkParams& p, const Seq& s, int r
 // 3200 with uint32_t).
 
 // Sum over r < n of floor((at + r step) / mod): whole multiples come out, then the roles of step and mod change
-// (the lattice points under a line, counted along the other axis).
+// (the lattice points under a line, counted along the other axis: Graham, Knuth and Patashnik, "Concrete Mathematics",
+// section 3.5, with Euclid's steps).
 template <class I>
 __device__ __forceinline__ I floor_sum(I n, I mod, I step, I at) {
   I total = 0;
@@ -641,7 +644,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
       ok = warp_all(wait_long(bar(B_Q_READY), units & 1u, abort_flag, p.err));
       // Step t: buffer t & 1, key tile t (or t / 2 with two row tiles).  P.V of step t, then Q.K^T of step t + 2.
       // All roles' loops are kept rolled: together they have to stay in the SM's instruction cache, and an MMA lasts
-      // longer than an iteration (4096 rows on 8192 keys, the MMA loops unrolled by 1, 2, 4, 8: 743, 738, 756, 763 us).
+      // longer than an iteration (4096 rows on 8192 keys, the MMA loops unrolled by 1, 2, 4, 8: 691, 682, 700, 702 us).
       const uint32_t per = u.dual ? 1u : 0u;
 #pragma unroll 1
       for (int t = -2; t < steps && ok; ++t) {

@@ -514,12 +514,14 @@ __device__ __forceinline__ void check_lengths(const RopeAppendArgs& a) {
 // The same walk over chunks of heads of q, k or v, of which each row ends as codes: q's
 // in q_out, k's and v's in the token's place in the pages.
 //
-// Bounded by instructions, about 190 for the 256 values of a warp's pass (a code and the
-// test of its neighbourhood take six a value): 3080 tokens of 64 + 8 + 8 heads of 128
-// (95 MB) take 37 us, 2.6 TB/s; half of it is HBM's.  A token's look-ups (sequence,
-// lengths, page) are loads that wait for one another, so the first rows are asked for
-// before them: 16 one-token sequences take 4 us.  Left to 124 registers: with 96 (5
-// blocks an SM) or 80 (6) the rows spill, 43 and 50 us.
+// 3080 tokens of 64 + 8 + 8 heads of 128 (95 MB) take 37 us, 2.6 TB/s.  Bounded by latency at
+// low occupancy: about 190 instructions for the 256 values of a warp's pass (a code and the
+// test of its neighbourhood take six a value) fill 59 % of the issue slots, and 16 warps an
+// SM at 124 registers do not cover the rest (instructions wait for results before them,
+// shared-memory exchanges and loads, in this order).  With 96 registers (5 blocks an SM) or 80
+// (6) the rows spill, 45 and 51 us.  A token's look-ups (sequence, lengths, page) are loads
+// that wait for one another, so the first rows are asked for before them: 16 one-token
+// sequences take 4 us.
 template <int LANES, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeAppendArgs a) {
   constexpr int rows = 32 / LANES;
