@@ -450,7 +450,7 @@ int fa3_norm_rope(const uint16_t* q, const uint16_t* k, const uint16_t* q_weight
  *          and their q_out is left as it was.
  * A position past the table sets FA3_DEVERR_POS and skips the row; a block-table
  * entry outside the pool sets FA3_DEVERR_PAGE and skips its k and v (q_out is
- * written).  Supported: any page_size >= 1; q_out, k_cache, v_cache 8-byte aligned. */
+ * written).  Supported: any page_size >= 1, B <= 2^30; q_out, k_cache, v_cache 8-byte aligned. */
 int fa3_rope_append_gqa_paged(const uint16_t* q, const uint16_t* k, const uint16_t* v,
                               const uint16_t* q_weight, const uint16_t* k_weight, float eps,
                               const float* cos_sin, int table_len, int rot_dim, int interleaved,
@@ -474,7 +474,7 @@ int fa3_rope_append_gqa_paged(const uint16_t* q, const uint16_t* k, const uint16
  *          (sequences might share rows).
  * scales   finite; q_scale, k_scale >= 0 (a softmax scale of 0 or below is refused); scores
  *          |s[t]| below 2^26.
- * Supported: D = 128, Hq / Hkv <= 128, n < 2^27 - 1; q, k, v, out 16-byte aligned.
+ * Supported: D = 128, Hq / Hkv <= 128, n < 2^27 - 1, B <= 2^30; q, k, v, out 16-byte aligned.
  * workspace  fa3_chunk_workspace_size(n, B, Hq, Hkv, D) bytes, 16-byte aligned
  *          (partial results of row blocks whose keys are shared out, 20 or 40 MB);
  *          its contents need no initialisation.  Calls that may run at the same

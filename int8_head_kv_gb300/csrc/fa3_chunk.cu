@@ -1165,7 +1165,7 @@ int chunk_attn(ChunkParams& p, int D, float softmax_scale, void* workspace, size
   if (p.n <= 0 || p.B <= 0 || p.T <= 0 || p.Hq <= 0 || p.Hkv <= 0 || D <= 0 || p.Hq % p.Hkv != 0) return FA3_EINVAL;
   if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale)) return FA3_EINVAL;
   p.G = p.Hq / p.Hkv;
-  if (D != kD || p.G > kRows || p.Hkv > 65535 || p.n >= (1 << 27) - 1) return FA3_ERANGE;
+  if (D != kD || p.G > kRows || p.Hkv > 65535 || p.n >= (1 << 27) - 1 || p.B > kMostSequences) return FA3_ERANGE;
   if ((p.block_table ? (int64_t)p.num_pages * p.page_size : (int64_t)p.B * p.T) >= ((int64_t)1 << 31)) return FA3_ERANGE;
   if (!aligned16(p.q) || !aligned16(p.k) || !aligned16(p.v) || !aligned16(p.out)) return FA3_ERANGE;
   p.P = kRows / p.G;

@@ -33,6 +33,9 @@ inline int cuda_status(cudaError_t e) { return e == cudaSuccess ? FA3_OK : FA3_E
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Sequences of a packed-row call: kernels step through them in 32-bit numbers, some hundred at a time.
+constexpr int kMostSequences = 1 << 30;
+
 // bf16 bit pattern -> float (exact).
 __device__ __forceinline__ float bf16_to_float(uint32_t bits16) { return __uint_as_float(bits16 << 16); }
 

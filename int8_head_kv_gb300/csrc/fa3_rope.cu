@@ -764,7 +764,7 @@ FA3_API int fa3_rope_append_gqa_paged(const uint16_t* q, const uint16_t* k, cons
   RopeAppendArgs a;
   int st = rot_args(cos_sin, table_len, rot_dim, interleaved, eps, D, &a.r);
   if (st != FA3_OK) return st;
-  if ((int64_t)max_pages * page_size >= ((int64_t)1 << 31)) return FA3_ERANGE;
+  if ((int64_t)max_pages * page_size >= ((int64_t)1 << 31) || B > kMostSequences) return FA3_ERANGE;
   if (q_stride < 0 || k_stride < 0 || v_stride < 0 || q_stride % 4 != 0 || k_stride % 4 != 0 || v_stride % 4 != 0)
     return FA3_ERANGE;
   if (!aligned8(q) || !aligned8(k) || !aligned8(v) || !aligned8(q_weight) || !aligned8(k_weight) || !aligned8(q_out) ||

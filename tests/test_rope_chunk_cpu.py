@@ -222,3 +222,11 @@ def test_workspace_cache_is_looked_up_as_one_step(monkeypatch):
         for t in threads:
             t.join()
         assert not F._ws_cache
+
+
+def test_more_sequences_than_the_kernels_count_are_refused(L):
+    for B in ((1 << 30) + 1, (1 << 31) - 1):
+        assert L.fa3_rope_append_gqa_paged(None, FAKE, FAKE, None, None, 1e-6, None, 0, 0, 0, None, FAKE, FAKE, None, FAKE, FAKE, FAKE, FAKE, FAKE, 4,
+                                           B, 0, 2, 128, 0, 1024, 1024, 8, 16, 4, None, None) == ERANGE
+        assert L.fa3_prefill_attn_gqa_paged(*[FAKE] * 10, 4, B, 16, 2, 128, 8, 16, 4, 0.09, FAKE, 1 << 40, None, None) == ERANGE
+        assert L.fa3_cross_attn_gqa(*[FAKE] * 9, 4, B, 1, 16, 2, 128, 0.09, FAKE, 1 << 40, None, None) == ERANGE
