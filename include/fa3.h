@@ -505,7 +505,102 @@ int fa3_cross_attn_gqa(const int8_t* q, const int8_t* k, const int8_t* v,
                        int n, int B, int T, int Hq, int Hkv, int D, float softmax_scale,
                        void* workspace, size_t workspace_bytes, int32_t* dev_err, void* stream);
 
-/* The four packed-row calls above with their arguments in one block, in their order, for
+/* ------------------------------------------------------------------------
+ * Block-scaled paged INT8 cache: no calibration.  Every `block` consecutive tokens
+ * of a sequence share, for each KV head, one scale of their keys and one of
+ * their values, made from the tokens themselves; the query stays bf16.  The pages quantize with parameters that are fixed
+ * after calibration (msModelSlim FA3量化, 适用要求); these calls are for programs
+ * that have no calibration set, or whose caches are cut down as they grow.
+ * k_cache, v_cache  int8 [num_pages][page_size][Hkv][D], pages as above.
+ * k_scale, v_scale  float [num_pages][page_size / block][Hkv]: token t of a sequence has
+ *          the scale of its page's block (t % page_size) / block.  A token's values
+ *          are code * scale; scales are finite and not negative.  Scales of blocks
+ *          without a token are not read.
+ * weights  float [num_pages][Hkv][page_size]: attention weight gathered by each token.
+ * Rows are packed by q_start and kv_lens as for fa3_rope_append_gqa_paged.
+ * Supported: block a multiple of 16 up to 4096 that divides page_size; num_pages * page_size and
+ *          max_pages * page_size < 2^31; B <= 2^30, Hkv <= 65535.
+ * A sequence with a bad length, or rows outside [0, n), sets FA3_DEVERR_LENS and is left out;
+ * if q_start falls anywhere, nothing is written.
+ * ------------------------------------------------------------------------ */
+
+/* New rows into the cache.  With a the greatest magnitude among the finite values of a head's new
+ * rows in one block, s = a / 127; if the block holds tokens already, s becomes the greater of that and
+ * their scale s0, and their codes c become round_half_even(c * fl(s0 / s)), the product unrounded.
+ *   code = clamp(round_half_even(x / s), -127, 127)     (float32 quotient; s = 0 -> 0; NaN -> -127)
+ * so a token's value is within half a step of its block's scale when written, and moves by
+ * at most as much again each time that a later token makes the scale grow.
+ * k, v     bf16 [n][Hkv][D], row strides k_stride, v_stride elements, heads contiguous.
+ * A block whose block-table entry is outside the pool sets FA3_DEVERR_PAGE and is
+ * skipped.  A page that is written belongs to one sequence.
+ * Supported: D % 8 == 0, D <= 256; strides multiples of 4; all 8-byte aligned (scales 4). */
+int fa3_append_gqa_block_paged(const uint16_t* k, const uint16_t* v, int8_t* k_cache, int8_t* v_cache,
+                               float* k_scale, float* v_scale, const int32_t* block_table,
+                               const int32_t* q_start, const int32_t* kv_lens, int n, int B, int Hkv, int D,
+                               int64_t k_stride, int64_t v_stride, int num_pages, int page_size, int max_pages,
+                               int block, int32_t* dev_err, void* stream);
+
+/* Causal attention of packed new rows over the cache, which holds them already:
+ *   s[t] = (q[row, h] . k[t, g]) * softmax_scale,  t <= kv_lens[b] - n_b + i
+ *   out[row, h, :] = bf16( sum_t softmax(s)_t * v[t, g, :] ),  lse[row, h] = ln sum_t exp(s[t])
+ * q        bf16 [n][Hq][128], row stride q_stride elements; values of rows outside the sequences do
+ *          not matter.  out  bf16 [n][Hq][128].  lse  float [n][Hq], or NULL.
+ * Rows outside the sequences and those of a sequence with bad lengths are left as they were.
+ * An entry outside the pool sets FA3_DEVERR_PAGE and reads another page (that
+ * sequence's output is not valid).  A value scale below 2^-80 counts as 2^-80.
+ * Supported: D = 128, Hq / Hkv <= 128, n < 2^27 - 1; q_stride a multiple of 8; q, out and the caches 16-byte aligned.
+ * workspace  fa3_attn_block_workspace_size(n, B, Hq, Hkv, D) bytes, 16-byte aligned, not
+ *          initialised; calls that may run at the same time need one each. */
+size_t fa3_attn_block_workspace_size(int n, int B, int Hq, int Hkv, int D);
+
+int fa3_attn_gqa_block_paged(const uint16_t* q, const int8_t* k_cache, const int8_t* v_cache, const float* k_scale,
+                             const float* v_scale, const int32_t* q_start, const int32_t* kv_lens,
+                             const int32_t* block_table, uint16_t* out, float* lse, int n, int B, int Hq, int Hkv,
+                             int D, int64_t q_stride, int num_pages, int page_size, int max_pages, int block,
+                             float softmax_scale, void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                             void* stream);
+
+/* Adds up the attention weight of every cached token: for token t of sequence b and KV head g
+ *   sum over rows q_start[b] + i of b with t <= kv_lens[b] - n_b + i and heads h of g of exp(s[t] - lse[row, h])
+ * is added to its weight; a token of this call's new rows begins with nothing.  q, k_cache, k_scale
+ * and softmax_scale as for the attention call, whose lse it takes: a row then gives every head's
+ * tokens 1 in all.  Sequences without new rows keep their weights.  The sums are the same on
+ * every run; a page that sequences share gets both their sums, in either order.
+ * An entry outside the pool sets FA3_DEVERR_PAGE; its tokens get nothing.
+ * Supported: as fa3_attn_gqa_block_paged; q_stride >= Hq * D.
+ * workspace  fa3_attn_weights_workspace_size() bytes, 16-byte aligned, not initialised;
+ *          calls that may run at the same time need one each. */
+size_t fa3_attn_weights_workspace_size(void);
+
+int fa3_attn_weights_gqa_block_paged(const uint16_t* q, const int8_t* k_cache, const float* k_scale, const float* lse,
+                                     float* weights, const int32_t* q_start, const int32_t* kv_lens,
+                                     const int32_t* block_table, int n, int B, int Hq, int Hkv, int D,
+                                     int64_t q_stride, int num_pages, int page_size, int max_pages, int block,
+                                     float softmax_scale, void* workspace, size_t workspace_bytes,
+                                     int32_t* dev_err, void* stream);
+
+/* Cuts caches down.  Of each sequence and KV head the first `sinks` tokens stay, the last `recent`,
+ * and of the others the budget - sinks - recent with the greatest weights, the earliest of equal
+ * ones (-0 equals 0, NaN is greatest); a context of at most `budget` tokens stays whole.
+ * The kept tokens are copied, in their order, to slots 0, 1, .. of the pages in new_table.  A new
+ * block's scale is the greatest of its tokens' scales; codes c become
+ * round_half_even(c * fl(old scale / new scale)), the product unrounded.  Weights move along.
+ * kv_lens  int32 [B], 0 <= kv_lens[b] <= max_pages * page_size, otherwise FA3_DEVERR_LENS is set and the
+ *          sequence is left out (its kept and new_lens are left as they were).
+ * new_table  int32 [B][new_pages]: pages that block_table does not use for this call's
+ *          tokens, each of one sequence (the copies of one head would meet the
+ *          other's reads); budget <= new_pages * page_size.  An entry outside the pool
+ *          sets FA3_DEVERR_PAGE and its tokens are lost; one of block_table outside it reads another page.
+ * kept     int32 [B][Hkv][budget]: positions of the kept tokens, -1 behind them.
+ * new_lens int32 [B]: min(kv_lens[b], budget).
+ * Supported: D % 8 == 0, D <= 256, B <= 65535; caches 8-byte aligned. */
+int fa3_evict_gqa_block_paged(int8_t* k_cache, int8_t* v_cache, float* k_scale, float* v_scale, float* weights,
+                              const int32_t* block_table, const int32_t* kv_lens, const int32_t* new_table,
+                              int32_t* kept, int32_t* new_lens, int B, int Hkv, int D, int num_pages,
+                              int page_size, int max_pages, int block, int new_pages, int budget, int sinks,
+                              int recent, int32_t* dev_err, void* stream);
+
+/* The packed-row and block-scaled calls above with their arguments in one block, in their order, for
  * callers behind a foreign-function interface: args[i] is a pointer's or an integer's
  * value, or the bits of a double in place of a float; args is 8-byte aligned, count its
  * length.  FA3_EINVAL: another call or number; FA3_ERANGE: a value beyond its
@@ -514,7 +609,11 @@ enum {
   FA3_CALL_NORM_ROPE = 0,
   FA3_CALL_ROPE_APPEND_GQA_PAGED = 1,
   FA3_CALL_PREFILL_ATTN_GQA_PAGED = 2,
-  FA3_CALL_CROSS_ATTN_GQA = 3
+  FA3_CALL_CROSS_ATTN_GQA = 3,
+  FA3_CALL_APPEND_GQA_BLOCK_PAGED = 4,
+  FA3_CALL_ATTN_GQA_BLOCK_PAGED = 5,
+  FA3_CALL_ATTN_WEIGHTS_GQA_BLOCK_PAGED = 6,
+  FA3_CALL_EVICT_GQA_BLOCK_PAGED = 7
 };
 int fa3_call(int which, const int64_t* args, int count);
 

@@ -1,4 +1,4 @@
-// The packed-row calls with their arguments in one block: host code alone.  Each of these calls takes a few
+// The packed-row and block-scaled calls with their arguments in one block: host code alone.  Each of these calls takes a few
 // microseconds of a GPU in a decode step, and behind a foreign-function interface every argument has a price: from
 // Python, fa3_norm_rope's 32 one by one make a call of 21 us, in one block of 17; the append's 32 of 25 and 21.
 #include "fa3_common.cuh"
@@ -51,6 +51,10 @@ FA3_API int fa3_call(int which, const int64_t* args, int count) {
     case FA3_CALL_ROPE_APPEND_GQA_PAGED: return fa3::call(fa3_rope_append_gqa_paged, args, count);
     case FA3_CALL_PREFILL_ATTN_GQA_PAGED: return fa3::call(fa3_prefill_attn_gqa_paged, args, count);
     case FA3_CALL_CROSS_ATTN_GQA: return fa3::call(fa3_cross_attn_gqa, args, count);
+    case FA3_CALL_APPEND_GQA_BLOCK_PAGED: return fa3::call(fa3_append_gqa_block_paged, args, count);
+    case FA3_CALL_ATTN_GQA_BLOCK_PAGED: return fa3::call(fa3_attn_gqa_block_paged, args, count);
+    case FA3_CALL_ATTN_WEIGHTS_GQA_BLOCK_PAGED: return fa3::call(fa3_attn_weights_gqa_block_paged, args, count);
+    case FA3_CALL_EVICT_GQA_BLOCK_PAGED: return fa3::call(fa3_evict_gqa_block_paged, args, count);
     default: return FA3_EINVAL;
   }
 }

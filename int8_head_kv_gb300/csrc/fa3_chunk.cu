@@ -55,6 +55,8 @@
 // Every wait is bounded; on time-out the kernel sets FA3_DEVERR_TIMEOUT, waits for its
 // copies and MMAs, frees its TMEM and returns.
 #include "fa3_common.cuh"
+#include "fa3_packed.cuh"
+#include "fa3_pipe.cuh"
 #include "fa3_tc.cuh"
 
 #include <cuda_bf16.h>
@@ -145,6 +147,14 @@ struct ChunkParams {
   float sm_log2;                // softmax_scale * log2(e)
   int box;                      // rows of a TMA box; 0: pages too ragged for boxes, loads through registers
   CUtensorMap map_k, map_v;     // [cache rows][Hkv * 128] in boxes of [box][128]
+  // a block-scaled cache, instead of q, q_scale, k_scale and v_scale
+  const uint16_t* qf;           // bf16 [n][Hq][128], rows q_stride values apart
+  const float* ks;              // [num_pages][per_page][Hkv]
+  const float* vs;
+  float* lse;                   // [n][Hq], or nullptr
+  int64_t q_stride;
+  int per_page;
+  DivU32 div_block;
 };
 
 // Keys come in boxes of consecutive cache rows, the largest power of two that divides the page size (and the
@@ -187,26 +197,6 @@ __device__ __forceinline__ int cost_of(const ChunkParams& p, const Seq& s, int r
 // every call's way, and 64-bit divisions and scans take several times as long (16 sequences: 6600 cycles with int64_t,
 // 3200 with uint32_t).
 
-// Sum over r < n of floor((at + r step) / mod): whole multiples come out, then the roles of step and mod change
-// (the lattice points under a line, counted along the other axis: Graham, Knuth and Patashnik, "Concrete Mathematics",
-// section 3.5, with Euclid's steps).
-template <class I>
-__device__ __forceinline__ I floor_sum(I n, I mod, I step, I at) {
-  I total = 0;
-#pragma unroll 1
-  for (;;) {
-    total += n * (n - 1) / 2 * (step / mod) + n * (at / mod);
-    step %= mod;
-    at %= mod;
-    const I top = step * n + at;
-    if (top < mod) return total;
-    n = top / mod;
-    at = top % mod;
-    const I t = mod;
-    mod = step;
-    step = t;
-  }
-}
 // Cost of all row blocks of one KV head of the sequence.
 template <class I>
 __device__ __forceinline__ I sequence_cost(const ChunkParams& p, const Seq& s) {
@@ -219,32 +209,6 @@ __device__ __forceinline__ I sequence_cost(const ChunkParams& p, const Seq& s) {
   return c;
 }
 
-template <class I>
-__device__ __forceinline__ I warp_scan(I v, int lane) {     // inclusive
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const I y = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += y;
-  }
-  return v;
-}
-
-// The line and its parts: CTA c takes [begin(c), begin(c + 1)).
-template <class I>
-struct Line {
-  I total, each;
-  int parts, rest;
-  __device__ __forceinline__ I begin(int c) const {
-    return c >= parts ? total : each * (I)c + (I)((uint32_t)rest * (uint32_t)c / (uint32_t)parts);
-  }
-  // The part that position x lies in.
-  __device__ __forceinline__ int owner(I x) const {
-    int c = (int)(((x + 1) * (I)parts - 1) / total);
-    while (c > 0 && begin(c) > x) --c;
-    while (c + 1 < parts && begin(c + 1) <= x) ++c;
-    return c;
-  }
-};
 // The first 32 sequences, a lane each: cost of a KV head and, summed over all heads, up to and with this one.
 template <class I>
 struct Ahead {
@@ -454,34 +418,9 @@ __device__ __forceinline__ void walk_parts(const ChunkParams& p, const Seq& s0, 
   }
 }
 
-// wait_bar for short waits, with bounded_wait's rare look at the clock, in ticks of 2^20 ns (1.05 ms).  A second for a wait
-// within a unit; a wait for a part of the ring may last as long as a unit of the longest context takes (2.3 us a key
+// A wait for a part of the ring may last as long as a unit of the longest context takes (2.3 us a key
 // tile), and has four seconds and 8 us a key tile.
-constexpr uint32_t kWaitTicks = 954;
 __device__ __forceinline__ uint32_t part_ticks(const ChunkParams& p) { return 4 * kWaitTicks + ((uint32_t)p.T >> 14); }
-__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, int32_t* err,
-                                          uint32_t limit = kWaitTicks) {
-  const Waited w = bounded_wait([&] { return mbar_try(bar, parity); }, [&] { return *abort_flag != 0u; },
-                                [] { return (uint32_t)(global_ns() >> 20); }, limit);
-  if (w == Waited::kLate) {
-    *abort_flag = 1u;
-    set_dev_err(err, FA3_DEVERR_TIMEOUT);
-  }
-  return w == Waited::kDone;
-}
-// The same for a warp, whose lanes have to agree.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int lane, volatile uint32_t* abort_flag,
-                                          int32_t* err, uint32_t limit = kWaitTicks) {
-  return warp_all(wait_long(bar, parity, abort_flag, err, limit));
-}
-
-// The wait for this thread's TMEM loads, which also orders the uses of v behind it.
-__device__ __forceinline__ void wait_ld16(uint32_t* v) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
-                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
-               :: "memory");
-}
 
 // 32 columns' maximum, by the load itself; the columns go to v all the same.
 __device__ __forceinline__ void tmem_ld_max32(uint32_t taddr, uint32_t (&v)[32], float& m) {
@@ -498,54 +437,65 @@ __device__ __forceinline__ void tmem_ld_max32(uint32_t taddr, uint32_t (&v)[32],
 __device__ __forceinline__ void wait_max(float& a) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(a) :: "memory");
 }
-
-// 16 bytes that this SM reads once: the L1 (what shared memory leaves of it) is passed by.
-__device__ __forceinline__ uint4 load_once(const int8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* tm, int c0, int c1, uint32_t bar) {
+__device__ __forceinline__ void tmem_ld_max16(uint32_t taddr, uint32_t (&v)[16], float& m) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(bar) : "memory");
+      "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, %16, [%17];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+        "=f"(m)
+      : "r"(taddr));
 }
+__device__ __forceinline__ void wait_max(float& a, float& b) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(a), "+f"(b) :: "memory");
+}
+
+// Natural logarithm of a row's sum of exponentials: the sum of 2^(.. - m) is l.
+__device__ __forceinline__ float log_sum(float m, float l) { return l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F; }
+
+// A row of 128 bf16 values as fp16, times a power of two that brings the largest to [2^14, 2^15): exact, but for values
+// below 2^-38 of it.  Writes the chunks of 8 values 2048 bytes apart; returns the inverse of the power.
+__device__ __forceinline__ float put_query_row(const uint16_t* row, bool active, uint8_t* dst) {
+  uint4 v[16];
+  uint32_t top = 0;
+#pragma unroll
+  for (int c = 0; c < 16; ++c) v[c] = active ? __ldg(reinterpret_cast<const uint4*>(row) + c) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+  for (int c = 0; c < 16; ++c)
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[c].x & 0x7fff7fffu, v[c].y & 0x7fff7fffu),
+                                 __vmaxu2(v[c].z & 0x7fff7fffu, v[c].w & 0x7fff7fffu)));
+  const uint32_t e = max(max(top & 0xffffu, top >> 16) >> 7, 15u);     // the largest's exponent: 2^(e - 127)
+  const float f = __uint_as_float((268u - e) << 23);
+  auto two = [&](uint32_t w) { return pack_f16x2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f); };
+#pragma unroll
+  for (int c = 0; c < 16; ++c) *reinterpret_cast<uint4*>(dst + c * 2048) = make_uint4(two(v[c].x), two(v[c].y), two(v[c].z), two(v[c].w));
+  return __uint_as_float((e - 14u) << 23);
+}
+
+// The scales of a key tile's eight groups of 16 keys (a block's keys lie in whole groups), a lane each: lanes 0 .. 7 the
+// keys', 8 .. 15 the values'.  Looked up ahead: the page two tiles, the scale one.
+constexpr float kLeastScale = 8.271806125530277e-25f;        // 2^-80: a smaller value scale counts as this
+struct TileScales {
+  const int32_t* table;           // the sequence's pages
+  const float* pool;
+  int n_keys, g;
+  int page;                       // of the tile after the next
+  float next;                     // of the next tile
+};
+__device__ __forceinline__ int scale_token(const TileScales& t, int tile, int lane) {
+  return min(tile * kKeys + (lane & 7) * 16, t.n_keys - 1);
+}
+__device__ __forceinline__ int scale_page(const ChunkParams& p, const TileScales& t, int tile, int lane) {
+  int pg = __ldg(t.table + divu32((uint32_t)scale_token(t, tile, lane), p.div_ps));
+  return (uint32_t)pg < (uint32_t)p.num_pages ? pg : 0;      // outside the pool: the loader of the tile reports it
+}
+__device__ __forceinline__ float scale_of(const ChunkParams& p, const TileScales& t, int page, int tile, int lane) {
+  const uint32_t tok = (uint32_t)scale_token(t, tile, lane), at = tok - divu32(tok, p.div_ps) * (uint32_t)p.page_size;
+  return __ldg(t.pool + ((int64_t)page * p.per_page + divu32(at, p.div_block)) * p.Hkv + t.g);
+}
+
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
                ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
-}
-__device__ __forceinline__ void prefetch_map(const CUtensorMap* tm) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
-}
-__device__ __forceinline__ void prefetch_line(const int8_t* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-
-// MMAs on descriptors given by their low words (address and leading stride; the step along the contraction
-// is one 32-bit addition).  The whole warp runs the issuing code, converged, so that its addresses stay in
-// uniform registers, and the elected lane's predicate guards the instruction itself.
-__host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo, bool swizzle) { return (sbo >> 4) | (1u << 14) | (swizzle ? 2u << 29 : 0u); }
-__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4) | ((lbo >> 4) << 16); }
-__device__ __forceinline__ uint32_t elect_one() {
-  uint32_t e;
-  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
-  return e;
-}
-template <uint32_t HI_A, uint32_t HI_B>
-__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n.reg .pred p, e;\n.reg .b64 a, b;\nsetp.ne.b32 e, %0, 0;\nsetp.ne.b32 p, %5, 0;\n"
-      "mov.b64 a, {%2, %6};\nmov.b64 b, {%3, %7};\n"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%1], a, b, %4, p;\n}\n"
-      ::"r"(lead), "r"(d), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "n"(HI_A), "n"(HI_B) : "memory");
 }
 template <uint32_t HI>
 __device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
@@ -554,13 +504,11 @@ __device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a_tme
       "@e tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], b, %4, p;\n}\n"
       ::"r"(lead), "r"(d), "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(acc), "n"(HI) : "memory");
 }
-__device__ __forceinline__ void commit_if(uint32_t lead, uint32_t bar) {
-  asm volatile(
-      "{\n.reg .pred e;\nsetp.ne.b32 e, %1, 0;\n"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar), "r"(lead)
-      : "memory");
-}
-
+// BLOCK: bf16 queries, and scales of keys and values by blocks of tokens.  With l[t] = log2 of token t's value scale, the
+// softmax takes x[t] = s[t] log2(e) + l[t] in place of the score: P = 2^(x - m) are then the weights of V's bare codes, with
+// a maximum of their own, so that P.V needs no scale whatever sizes the blocks' values have, and the row sum, which is
+// of 2^(s log2(e) - m), takes P over the value scale, group by group of 16 keys.
+template <bool BLOCK>
 __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_constant__ ChunkParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -870,9 +818,28 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
       const bool active = pl < p.P && i < u.nq;
       const bool warp_active = __any_sync(0xffffffffu, active);
       const int64_t orow = (int64_t)(u.q0 + (active ? i : 0)) * p.Hq + hh;   // row of q and out
+      auto tile_of = [&](int st) { return u.t0 + (u.dual ? st : 2 * st + x); };
+      TileScales ts;
+      float q_inv = 1.f;                                     // BLOCK: a power of two that the row is divided by
+      if constexpr (BLOCK) {
+        ts.table = p.block_table + (int64_t)u.b * p.max_pages;
+        ts.pool = lane & 8 ? p.vs : p.ks;
+        ts.n_keys = p.causal ? u.nkv - u.nq + min(u.nq, (u.rb + 1) * 2 * p.P) : u.nkv;
+        ts.g = u.g;
+        if (mine > 0) {
+          ts.page = scale_page(p, ts, tile_of(0), lane);
+          ts.next = scale_of(p, ts, ts.page, tile_of(0), lane);
+          ts.page = scale_page(p, ts, tile_of(1), lane);
+        }
+      }
       // The row's query codes as fp16 into the row tile's K-major A operand (chunk of 8 d at
       // (d / 8) * 2048 + row * 16).
-      if (u.dual || x == 0) {
+      if constexpr (BLOCK) {
+        // a single row tile's second warpgroup needs the power and writes what the first does
+        q_inv = put_query_row(p.qf + (int64_t)(u.q0 + (active ? i : 0)) * p.q_stride + hh * kD, active,
+                              smem + OFF_Q + (u.dual ? x : 0) * Q_TILE + r * 16);
+        fence_proxy_async();
+      } else if (u.dual || x == 0) {
         const int8_t* qrow = p.q + orow * kD;
         uint8_t* qdst = smem + OFF_Q + (u.dual ? x : 0) * Q_TILE + r * 16;
 #pragma unroll
@@ -893,7 +860,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
       const int pos = !active ? -1 : p.causal ? u.nkv - u.nq + i : u.nkv - 1;   // last key this row sees
       const int pos_min = __reduce_min_sync(0xffffffffu, active ? pos : 0x7fffffff);
       // positive, so that -inf * c stays -inf; with a scale of zero every score still rounds to weight 1
-      const float c = active ? fmaxf(p.q_scale[hh] * p.k_scale[u.g] * p.sm_log2, 1e-37f) : 1.f;
+      const float c = BLOCK ? q_inv * p.sm_log2 : active ? fmaxf(p.q_scale[hh] * p.k_scale[u.g] * p.sm_log2, 1e-37f) : 1.f;
       float m_run = -CUDART_INF_F, l_run = 0.f;
       for (int st = 0; st < mine && ok; ++st) {
         const uint32_t ph = done + (uint32_t)st;
@@ -903,7 +870,23 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
         }
         if (warp_active) {
           tc_fence_after();
-          const int t0 = (u.t0 + (u.dual ? st : 2 * st + x)) * kKeys;   // the tile's first key
+          const int t0 = tile_of(st) * kKeys;                 // the tile's first key
+          float sc = 0.f, sc_inv = 0.f;                      // lanes 0 .. 7: key scale; 8 .. 15: log2 and inverse of the value scale
+          if constexpr (BLOCK) {
+            sc = ts.next;
+            if (st + 1 < mine) {
+              ts.next = scale_of(p, ts, ts.page, tile_of(st + 1), lane);
+              ts.page = scale_page(p, ts, tile_of(st + 2), lane);
+            }
+            if (lane & 8) {
+              sc = fmaxf(sc, kLeastScale);
+              sc_inv = __fdividef(1.f, sc);
+              sc = log2f(sc);
+            }
+          }
+          // factor and summand of group k's scores
+          auto factor = [&](int k) { return fmaxf(__shfl_sync(0xffffffffu, sc, k) * c, 1e-37f); };
+          auto summand = [&](int k) { return __shfl_sync(0xffffffffu, sc, 8 + k); };
           if (t0 + kKeys - 1 > pos_min) {
             // some active row of the warp does not see all keys: their scores become -inf
             const int last = pos - t0;
@@ -921,18 +904,31 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
           // the row's maximum of the integer scores
           uint32_t v0[16], v1[16];
           float mx = -CUDART_INF_F;
+          if constexpr (BLOCK) {
 #pragma unroll 1
-          for (uint32_t k = 0; k < 128; k += 32) {
-            uint32_t w[32];
-            float m;
-            tmem_ld_max32(scol + k, w, m);
-            wait_max(m);
-            mx = fmaxf(mx, m);
+            for (uint32_t k = 0; k < 8; k += 2) {
+              uint32_t w[16];
+              float m, m2;
+              tmem_ld_max16(scol + 16 * k, w, m);
+              tmem_ld_max16(scol + 16 * k + 16, w, m2);
+              const float f = factor(k), f2 = factor(k + 1), a = summand(k), a2 = summand(k + 1);
+              wait_max(m, m2);
+              mx = max3(mx, __fmaf_ru(m, f, a), __fmaf_ru(m2, f2, a2));
+            }
+          } else {
+#pragma unroll 1
+            for (uint32_t k = 0; k < 128; k += 32) {
+              uint32_t w[32];
+              float m;
+              tmem_ld_max32(scol + k, w, m);
+              wait_max(m);
+              mx = fmaxf(mx, m);
+            }
           }
           FA3_TMEM_LD16(scol, v0);
           // The reference, 7 (log2 units) below the row's maximum.  Rounded up, and the difference below is exact where
           // it matters: P stays below 2^15 whatever the size of the scores.
-          mx = __fadd_ru(__fmul_ru(mx, c), -7.f);
+          mx = __fadd_ru(BLOCK ? mx : __fmul_ru(mx, c), -7.f);
           // Lazy rescale: the reference moves only when it would by more than 8; then O (P.V up to this buffer's
           // step before) is scaled in place.  No key yet: -inf - (-inf) is no difference.
           const bool grow = mx - m_run > 8.f;
@@ -962,34 +958,40 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
           // P = exp2(s c - m) as fp16 pairs over the S columns (keys 32 c4 .. 32 c4 + 31 go to columns
           // 16 c4 .. 16 c4 + 15); the row sum takes the weights before the rounding.
           float l0 = 0.f, l1 = 0.f;
-          auto weigh = [&](const uint32_t (&w)[16], uint32_t (&pk)[8]) {
+          auto weigh = [&](const uint32_t (&w)[16], uint32_t (&pk)[8], int k) {   // the 16 keys of group k
+            const float f = BLOCK ? factor(k) : c, a = BLOCK ? summand(k) + mc : mc;
+            float g0 = 0.f, g1 = 0.f;
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
               float p0, p1;
-              fma2(p0, p1, __uint_as_float(w[e]), __uint_as_float(w[e + 1]), c, c, mc, mc);
+              fma2(p0, p1, __uint_as_float(w[e]), __uint_as_float(w[e + 1]), f, f, a, a);
               p0 = ex2_approx(p0);
               p1 = ex2_approx(p1);
-              add2(l0, l1, l0, l1, p0, p1);
+              if constexpr (BLOCK)
+                add2(g0, g1, g0, g1, p0, p1);
+              else
+                add2(l0, l1, l0, l1, p0, p1);
               pk[e / 2] = pack_f16x2(p0, p1);
             }
+            if constexpr (BLOCK) l0 = fmaf(g0 + g1, __shfl_sync(0xffffffffu, sc_inv, 8 + k), l0);
           };
           uint32_t pa[8], pb[8];
           wait_ld16(v0);
           FA3_TMEM_LD16(scol + 16, v1);
-          weigh(v0, pa);
+          weigh(v0, pa, 0);
 #pragma unroll 1
           for (uint32_t k = 0; k < 96; k += 32) {
             wait_ld16(v1);
             FA3_TMEM_LD16(scol + k + 32, v0);
-            weigh(v1, pb);
+            weigh(v1, pb, k / 16 + 1);
             tmem_st8(scol + k / 2, pa);
             wait_ld16(v0);
             FA3_TMEM_LD16(scol + k + 48, v1);
-            weigh(v0, pa);
+            weigh(v0, pa, k / 16 + 2);
             tmem_st8(scol + k / 2 + 8, pb);
           }
           wait_ld16(v1);
-          weigh(v1, pb);
+          weigh(v1, pb, 7);
           tmem_st8(scol + 48, pa);
           tmem_st8(scol + 56, pb);
           l_run += l0 + l1;
@@ -1026,7 +1028,9 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
       tc_fence_after();
       if (warp_active) {
         const bool whole = u.whole();
-        const float inv = !whole ? 1.f : l_run > 0.f ? p.v_scale[u.g] / l_run : 0.f;
+        const float inv = !whole ? 1.f : l_run > 0.f ? (BLOCK ? 1.f : p.v_scale[u.g]) / l_run : 0.f;
+        if constexpr (BLOCK)
+          if (whole && active && (u.dual || x == 0) && p.lse) p.lse[orow] = log_sum(m_run, l_run);
         f_mine *= inv;
         f_other *= inv;
         const int slot = 2 * (int)blockIdx.x + (u.first ? 1 : 0);
@@ -1086,6 +1090,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
 // 32 blockIdx.y .. + 31.  A lane has a row, a warp 16 columns.  It is launched while the main kernel runs and takes
 // about 3 us behind its end, for a few MB at most; the cuts come from the main kernel, because finding them
 // here again took 2 us more.
+template <bool BLOCK>
 __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constant__ ChunkParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int prow = blockIdx.y * 32 + lane;                   // row tile x 128 + row
@@ -1115,7 +1120,7 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constan
       o[4 * q4 + 3] = fmaf(a.w, f, o[4 * q4 + 3]);
     }
   }
-  const float inv = l > 0.f ? p.v_scale[cut.g] / l : 0.f;
+  const float inv = l > 0.f ? (BLOCK ? 1.f : p.v_scale[cut.g]) / l : 0.f;
   uint32_t w[8];
 #pragma unroll
   for (int e = 0; e < 16; e += 2) {
@@ -1123,6 +1128,8 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constan
     w[e / 2] = *reinterpret_cast<const uint32_t*>(&bb);
   }
   const int h = cut.g * p.G + r - pl * p.G;
+  if constexpr (BLOCK)
+    if (warp == 0 && p.lse) p.lse[(int64_t)(cut.row0 + i) * p.Hq + h] = log_sum(m, l);
   uint4* out = reinterpret_cast<uint4*>(p.out + ((int64_t)(cut.row0 + i) * p.Hq + h) * kD + warp * 16);
   out[0] = make_uint4(w[0], w[1], w[2], w[3]);
   out[1] = make_uint4(w[4], w[5], w[6], w[7]);
@@ -1159,15 +1166,16 @@ bool cache_map(CUtensorMap* map, const int8_t* base, int Hkv, int64_t rows, int 
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <bool BLOCK>
 int chunk_attn(ChunkParams& p, int D, float softmax_scale, void* workspace, size_t workspace_bytes, void* stream) {
-  if (!p.q || !p.k || !p.v || !p.q_scale || !p.k_scale || !p.v_scale || !p.q_start || !p.kv_lens || !p.out)
-    return FA3_EINVAL;
+  if (!(BLOCK ? (const void*)p.qf : (const void*)p.q) || !p.k || !p.v || !p.q_start || !p.kv_lens || !p.out) return FA3_EINVAL;
+  if (BLOCK ? !p.ks || !p.vs : !p.q_scale || !p.k_scale || !p.v_scale) return FA3_EINVAL;
   if (p.n <= 0 || p.B <= 0 || p.T <= 0 || p.Hq <= 0 || p.Hkv <= 0 || D <= 0 || p.Hq % p.Hkv != 0) return FA3_EINVAL;
   if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale)) return FA3_EINVAL;
   p.G = p.Hq / p.Hkv;
   if (D != kD || p.G > kRows || p.Hkv > 65535 || p.n >= (1 << 27) - 1 || p.B > kMostSequences) return FA3_ERANGE;
   if ((p.block_table ? (int64_t)p.num_pages * p.page_size : (int64_t)p.B * p.T) >= ((int64_t)1 << 31)) return FA3_ERANGE;
-  if (!aligned16(p.q) || !aligned16(p.k) || !aligned16(p.v) || !aligned16(p.out)) return FA3_ERANGE;
+  if (!aligned16(BLOCK ? (const void*)p.qf : (const void*)p.q) || !aligned16(p.k) || !aligned16(p.v) || !aligned16(p.out)) return FA3_ERANGE;
   p.P = kRows / p.G;
   p.div_2p = make_divu32((uint32_t)(2 * p.P));
   p.narrow = ((double)p.n / (2 * p.P) + p.B) * p.Hkv * (kUnitCost + kTileDual * (p.T / kKeys + 1.0)) < 16777216.0;
@@ -1191,14 +1199,14 @@ int chunk_attn(ChunkParams& p, int D, float softmax_scale, void* workspace, size
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return FA3_ECUDA;
   if (dev >= 64 || !set[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(gqa_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_CHUNK) != cudaSuccess)
+    if (cudaFuncSetAttribute(gqa_chunk_kernel<BLOCK>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_CHUNK) != cudaSuccess)
       return FA3_ECUDA;
     if (dev < 64) set[dev].store(true, std::memory_order_release);
   }
   const LaunchTogether together(s);
-  if (launch_pdl(gqa_chunk_kernel, dim3((unsigned)sms), dim3(kThreadsC), SMEM_CHUNK, s, p) != cudaSuccess)
+  if (launch_pdl(gqa_chunk_kernel<BLOCK>, dim3((unsigned)sms), dim3(kThreadsC), SMEM_CHUNK, s, p) != cudaSuccess)
     return FA3_ECUDA;
-  if (sms > 1 && launch_pdl(chunk_combine_kernel, dim3((unsigned)(sms - 1), (unsigned)(p.rows_max / 32)), dim3(256), 0, s,
+  if (sms > 1 && launch_pdl(chunk_combine_kernel<BLOCK>, dim3((unsigned)(sms - 1), (unsigned)(p.rows_max / 32)), dim3(256), 0, s,
                             p) != cudaSuccess)
     return FA3_ECUDA;
   return FA3_OK;
@@ -1219,7 +1227,7 @@ FA3_API int fa3_prefill_attn_gqa_paged(const int8_t* q, const int8_t* k, const i
   p.n = n; p.B = B; p.T = max_pages * page_size; p.Hq = Hq; p.Hkv = Hkv; p.causal = 1;
   p.page_size = page_size; p.max_pages = max_pages; p.num_pages = num_pages;
   p.div_ps = make_divu32((uint32_t)page_size);
-  return chunk_attn(p, D, softmax_scale, workspace, workspace_bytes, stream);
+  return chunk_attn<false>(p, D, softmax_scale, workspace, workspace_bytes, stream);
 }
 
 FA3_API int fa3_cross_attn_gqa(const int8_t* q, const int8_t* k, const int8_t* v, const float* q_scale,
@@ -1231,5 +1239,28 @@ FA3_API int fa3_cross_attn_gqa(const int8_t* q, const int8_t* k, const int8_t* v
   p.q = q; p.k = k; p.v = v; p.q_scale = q_scale; p.k_scale = k_scale; p.v_scale = v_scale; p.q_start = q_start;
   p.kv_lens = enc_lens; p.out = out; p.err = dev_err;
   p.n = n; p.B = B; p.T = T; p.Hq = Hq; p.Hkv = Hkv; p.causal = 0;
-  return chunk_attn(p, D, softmax_scale, workspace, workspace_bytes, stream);
+  return chunk_attn<false>(p, D, softmax_scale, workspace, workspace_bytes, stream);
+}
+
+FA3_API size_t fa3_attn_block_workspace_size(int n, int B, int Hq, int Hkv, int D) {
+  return fa3_chunk_workspace_size(n, B, Hq, Hkv, D);
+}
+
+FA3_API int fa3_attn_gqa_block_paged(const uint16_t* q, const int8_t* k_cache, const int8_t* v_cache, const float* k_scale,
+                                     const float* v_scale, const int32_t* q_start, const int32_t* kv_lens,
+                                     const int32_t* block_table, uint16_t* out, float* lse, int n, int B, int Hq, int Hkv,
+                                     int D, int64_t q_stride, int num_pages, int page_size, int max_pages, int block,
+                                     float softmax_scale, void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                                     void* stream) {
+  Pages pg;
+  const int st = pages_of(block_table, B, Hkv, num_pages, page_size, max_pages, block, &pg);
+  if (st != FA3_OK) return st;
+  if (q_stride < 0 || q_stride % 8 != 0) return FA3_ERANGE;
+  ChunkParams p = {};
+  p.qf = q; p.k = k_cache; p.v = v_cache; p.ks = k_scale; p.vs = v_scale; p.q_start = q_start; p.kv_lens = kv_lens;
+  p.block_table = block_table; p.out = out; p.lse = lse; p.err = dev_err;
+  p.n = n; p.B = B; p.T = pg.T_max; p.Hq = Hq; p.Hkv = Hkv; p.causal = 1; p.q_stride = q_stride;
+  p.page_size = page_size; p.max_pages = max_pages; p.num_pages = num_pages; p.per_page = pg.per_page;
+  p.div_ps = pg.div_ps; p.div_block = pg.div_block;
+  return chunk_attn<true>(p, D, softmax_scale, workspace, workspace_bytes, stream);
 }

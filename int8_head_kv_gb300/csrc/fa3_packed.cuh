@@ -1,0 +1,81 @@
+// What the calls on packed rows over a block-scaled paged cache share: which sequence a piece of work belongs to, and
+// where a block of tokens and its scales lie.
+#pragma once
+
+#include <stdint.h>
+
+#include "fa3_common.cuh"
+
+namespace fa3 {
+namespace {
+
+constexpr int kLeastBlock = 16, kMostBlock = 4096;   // tokens that share a scale: a multiple of the one, up to the other
+
+// The pages: token t of sequence b lies in row t % page_size of page block_table[b][t / page_size].
+struct Pages {
+  const int32_t* table;            // [B][max_pages]
+  int max_pages, num_pages, page_size, T_max;
+  int block, per_page, Hkv;        // tokens a scale, scales a page and head
+  DivU32 div_ps, div_block;
+};
+
+// Checks of what every call on such a cache is given; fills *p.
+inline int pages_of(const int32_t* table, int B, int Hkv, int num_pages, int page_size, int max_pages, int block, Pages* p) {
+  if (!table || B <= 0 || Hkv <= 0 || num_pages <= 0 || page_size <= 0 || max_pages <= 0 || block <= 0) return FA3_EINVAL;
+  if (page_size % block != 0) return FA3_EINVAL;
+  if (block % kLeastBlock != 0 || block > kMostBlock || B > kMostSequences || Hkv > 65535) return FA3_ERANGE;
+  if ((int64_t)max_pages * page_size >= ((int64_t)1 << 31) || (int64_t)num_pages * page_size >= ((int64_t)1 << 31)) return FA3_ERANGE;
+  *p = Pages{table, max_pages, num_pages, page_size, max_pages * page_size, block, page_size / block, Hkv,
+             make_divu32((uint32_t)page_size), make_divu32((uint32_t)block)};
+  return FA3_OK;
+}
+
+// A piece of work of a packed call: `index` counts the pieces of sequence b; q0 .. q0 + nq its rows, nkv its context.
+struct Piece {
+  int b, index, q0, nq, nkv;
+};
+
+// Pieces of `step` rows: sequence b has the numbers from q_start[b] / step + extra * b on, up to those of the next.  That is
+// no fewer than ceil(n_b / step) + extra - 1, whatever q_start[b] is, and the whole call has n / step + extra * B.
+inline int64_t pieces_of(int64_t n, int64_t B, int64_t step, int64_t extra) { return n / step + extra * B; }
+
+// Finds piece x (the block together; `found` is shared).  b < 0: there is none, or the sequence's lengths are bad, or
+// q_start falls somewhere (two sequences might share rows then: the call does nothing).  All threads read q_start at
+// once, one load's latency for B up to the block's threads.  With `report`, bad lengths set FA3_DEVERR_LENS.
+__device__ __forceinline__ Piece find_piece(const int32_t* __restrict__ q_start, const int32_t* __restrict__ kv_lens, int B, int n,
+                                            int T_max, DivU32 div_step, int extra, int64_t x, bool report, int32_t* err,
+                                            Piece* found) {
+  if (threadIdx.x == 0) found->b = -1;
+  __syncthreads();
+  bool falls = false, bad = false;
+  for (int b = threadIdx.x; b < B; b += blockDim.x) {
+    const int q0 = q_start[b], q1 = q_start[b + 1];
+    const int nkv = kv_lens[b];
+    falls |= q1 < q0;
+    const bool wrong = q0 < 0 || q1 > n || (q1 > q0 && (nkv < q1 - q0 || nkv > T_max));
+    bad |= wrong;
+    if (wrong || q1 <= q0) continue;
+    const int64_t first = (int64_t)divu32((uint32_t)q0, div_step) + (int64_t)extra * b;
+    const int64_t next = (int64_t)divu32((uint32_t)q1, div_step) + (int64_t)extra * (b + 1);
+    if (x >= first && x < next) *found = Piece{b, (int)(x - first), q0, q1 - q0, nkv};
+  }
+  if (report && (falls || bad)) set_dev_err(err, FA3_DEVERR_LENS);
+  falls = __syncthreads_or(falls);
+  Piece p = *found;
+  if (falls) p.b = -1;
+  return p;
+}
+
+// RNE(code * ratio), exactly: one fused operation rounds the exact product to a whole number (|code * ratio| <= 127).
+__device__ __forceinline__ uint32_t rescaled(uint32_t codes4, float ratio) {
+  uint32_t out = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float c = (float)(int)(int8_t)(codes4 >> (8 * e));
+    out |= (__float_as_uint(fmaf(c, ratio, kCodeMagic)) & 0xffu) << (8 * e);
+  }
+  return out;
+}
+
+}  // namespace
+}  // namespace fa3

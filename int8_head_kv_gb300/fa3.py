@@ -72,6 +72,12 @@ _SIGS = {
     "fa3_chunk_workspace_size": (_SZ, [_I] * 5),
     "fa3_prefill_attn_gqa_paged": (_I, [_P] * 10 + [_I] * 8 + [_F, _P, _SZ, _P, _P]),
     "fa3_cross_attn_gqa": (_I, [_P] * 9 + [_I] * 6 + [_F, _P, _SZ, _P, _P]),
+    "fa3_append_gqa_block_paged": (_I, [_P] * 9 + [_I] * 4 + [_I64] * 2 + [_I] * 4 + [_P, _P]),
+    "fa3_attn_block_workspace_size": (_SZ, [_I] * 5),
+    "fa3_attn_gqa_block_paged": (_I, [_P] * 10 + [_I] * 5 + [_I64] + [_I] * 4 + [_F, _P, _SZ, _P, _P]),
+    "fa3_attn_weights_workspace_size": (_SZ, []),
+    "fa3_attn_weights_gqa_block_paged": (_I, [_P] * 8 + [_I] * 5 + [_I64] + [_I] * 4 + [_F, _P, _SZ, _P, _P]),
+    "fa3_evict_gqa_block_paged": (_I, [_P] * 10 + [_I] * 11 + [_P, _P]),
     "fa3_call": (_I, [_I, ctypes.c_char_p, _I]),
 }
 
@@ -80,7 +86,8 @@ _SIGS = {
 _CALLS = {name: (i, struct.Struct("=" + "".join("d" if a is _F else "q" for a in _SIGS[name][1])).pack,
                  len(_SIGS[name][1]))
           for i, name in enumerate(("fa3_norm_rope", "fa3_rope_append_gqa_paged", "fa3_prefill_attn_gqa_paged",
-                                    "fa3_cross_attn_gqa"))}
+                                    "fa3_cross_attn_gqa", "fa3_append_gqa_block_paged", "fa3_attn_gqa_block_paged",
+                                    "fa3_attn_weights_gqa_block_paged", "fa3_evict_gqa_block_paged"))}
 
 
 def library_path() -> str:
@@ -857,18 +864,18 @@ def chunk_workspace_size(n: int, B: int, Hq: int, Hkv: int, D: int) -> int:
     return int(lib().fa3_chunk_workspace_size(n, B, Hq, Hkv, D))
 
 
-def _chunk_workspace(nbytes: int, device, stream, dev: int, raw: int):
+def _chunk_workspace(nbytes: int, device, stream, dev: int, raw: int, kind: str = "chunk"):
     # A captured call takes its buffer from the graph's own pool: replays of two graphs
     # (or of a graph and eager calls) then never share one.
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    key = ("chunk", dev, raw)                                # _ws_key's, without asking for the stream again
+    key = (kind, dev, raw)                                   # _ws_key's, without asking for the stream again
     with _ws_lock:
         ws = _ws_cache.get(key)
         if ws is not None and ws.numel() >= nbytes:
             _ws_cache.move_to_end(key)
             return ws
-        return _workspace("chunk", nbytes, device, stream=stream)
+        return _workspace(kind, nbytes, device, stream=stream)
 
 
 def _packed_attn(name, q, k, v, q_scale, k_scale, v_scale, q_start, lens, B, Hkv, sizes, table, softmax_scale, out,
@@ -950,3 +957,259 @@ def cross_attn_gqa(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_scale: t
     T, Hkv, D = sh[1], sh[2], sh[3]
     return _packed_attn("fa3_cross_attn_gqa", q, k, v, q_scale, k_scale, v_scale, q_start, enc_lens, B, Hkv,
                         lambda Hq: (T, Hq, Hkv, D), (), softmax_scale, out, workspace, dev_err, stream, dev)
+
+
+# ---------------------------------------------- block-scaled paged cache
+def block_scale_pool(cache: torch.Tensor, block: int) -> torch.Tensor:
+    """Scales for a pool int8 [num_pages][page_size][Hkv][D] with one for `block` tokens of a head:
+    float32 [num_pages][page_size / block][Hkv], zero."""
+    if cache.dim() != 4:
+        raise ValueError("cache must be [num_pages][page_size][Hkv][D]")
+    if block <= 0 or cache.shape[1] % block:
+        raise ValueError("block must divide the page size")
+    return torch.zeros(cache.shape[0], cache.shape[1] // block, cache.shape[2], dtype=_F32, device=cache.device)
+
+
+def attn_weight_pool(cache: torch.Tensor) -> torch.Tensor:
+    """Attention weights of a pool's tokens: float32 [num_pages][Hkv][page_size], zero."""
+    if cache.dim() != 4:
+        raise ValueError("cache must be [num_pages][page_size][Hkv][D]")
+    return torch.zeros(cache.shape[0], cache.shape[2], cache.shape[1], dtype=_F32, device=cache.device)
+
+
+def _block_scale(t: torch.Tensor, num_pages: int, page_size: int, Hkv: int, name: str, dev: int) -> int:
+    """Tokens that share one of the scales t [num_pages][page_size / block][Hkv]."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is _F32 and t.get_device() == dev and t.is_contiguous()):
+        _wrong(t, _F32, name)
+    sh = t.shape
+    if len(sh) != 3 or sh[0] != num_pages or sh[2] != Hkv or sh[1] == 0 or page_size % sh[1]:
+        raise ValueError(f"{name} must be [num_pages][page_size / block][Hkv]")
+    return page_size // sh[1]
+
+
+def _block_scales(k_scale, v_scale, num_pages: int, page_size: int, Hkv: int, dev: int) -> int:
+    block = _block_scale(k_scale, num_pages, page_size, Hkv, "k_scale", dev)
+    if _block_scale(v_scale, num_pages, page_size, Hkv, "v_scale", dev) != block:
+        raise ValueError("k_scale and v_scale must have blocks of one size")
+    return block
+
+
+def _weights_pool(t: torch.Tensor, num_pages: int, page_size: int, Hkv: int, dev: int) -> int:
+    if not (isinstance(t, torch.Tensor) and t.dtype is _F32 and t.get_device() == dev and t.is_contiguous()):
+        _wrong(t, _F32, "weights")
+    if t.shape != (num_pages, Hkv, page_size):
+        raise ValueError("weights must be [num_pages][Hkv][page_size]")
+    return t.data_ptr()
+
+
+def _queries(q: torch.Tensor, D: int, dev: int):
+    """n, Hq and the row stride of bf16 queries [n][Hq][D] with contiguous rows of heads."""
+    if not (isinstance(q, torch.Tensor) and q.dtype is _BF16 and q.get_device() == dev):
+        _need(q, _BF16, "q")
+        raise ValueError("all tensors must be on one device")
+    sh = q.shape
+    if len(sh) != 3 or sh[2] != D:
+        raise ValueError("q must be [n][Hq][D] with the cache's head size")
+    return sh[0], sh[1], _packed_rows(q, sh[1], D, sh[0], "q", dev) or sh[1] * D
+
+
+def _row_values(t: torch.Tensor, n: int, Hq: int, name: str, dev: int) -> int:
+    if not (isinstance(t, torch.Tensor) and t.dtype is _F32 and t.get_device() == dev and t.is_contiguous()):
+        _wrong(t, _F32, name)
+    if t.shape != (n, Hq):
+        raise ValueError(f"{name} must be [n][Hq]")
+    return t.data_ptr()
+
+
+def _given_workspace(workspace: torch.Tensor, dev: int):
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the tensors' device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def append_gqa_block_paged(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                           k_scale: torch.Tensor, v_scale: torch.Tensor, block_table: torch.Tensor,
+                           q_start: torch.Tensor, kv_lens: torch.Tensor, dev_err: Optional[torch.Tensor] = None,
+                           stream=None) -> None:
+    """New keys and values into a paged INT8 cache with a scale for each block of tokens and head (in place).
+
+    k, v bf16 [n][Hkv][D] with any row stride (slices of one projection): rows q_start[b] ..
+    q_start[b+1] - 1 are the last tokens of sequence b's kv_lens[b]-token context.  k_cache, v_cache int8
+    [num_pages][page_size][Hkv][D], k_scale, v_scale float32 [num_pages][page_size / block][Hkv]
+    (block_scale_pool).  A block's scale is its greatest magnitude / 127; where new tokens make it grow,
+    the codes of those that were there are rounded again."""
+    _need(k, _BF16, "k")
+    dev = k.get_device()
+    num_pages, page_size, Hkv, D = _pool_shape(k_cache, v_cache, dev)
+    block = _block_scales(k_scale, v_scale, num_pages, page_size, Hkv, dev)
+    B = _lens(q_start, kv_lens, "kv_lens", dev)
+    n = k.shape[0]
+    ks, vs = _packed_rows(k, Hkv, D, n, "k", dev), _packed_rows(v, Hkv, D, n, "v", dev)
+    max_pages = _pages(block_table, B, dev)
+    ep = _error_word(dev_err, dev)
+    raw, ctx = _here(dev, stream)
+    if not n:
+        return
+    if ctx is not None:
+        ctx.__enter__()
+    try:
+        i, pack, count = _CALLS["fa3_append_gqa_block_paged"]
+        st = lib().fa3_call(i, pack(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                    k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(),
+                                    q_start.data_ptr(), kv_lens.data_ptr(), n, B, Hkv, D, ks, vs, num_pages, page_size,
+                                    max_pages, block, ep, raw), count)
+        if st:
+            raise FA3Error("fa3_append_gqa_block_paged", st)
+    finally:
+        if ctx is not None:
+            ctx.__exit__(None, None, None)
+
+
+def attn_gqa_block_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor,
+                         v_scale: torch.Tensor, q_start: torch.Tensor, kv_lens: torch.Tensor,
+                         block_table: torch.Tensor, softmax_scale: float, out: Optional[torch.Tensor] = None,
+                         lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                         dev_err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Causal attention of packed new rows (single tokens to whole prompts) over a block-scaled paged cache that
+    holds them already: q bf16 [n][Hq][128] with any row stride, packed by q_start -> bf16 [n][Hq][128].
+
+    lse float32 [n][Hq], if given, takes the natural logarithm of every row's sum of exponentials (for
+    attn_weights_gqa_block_paged).  Rows outside the sequences are left as they were (zero when ``out`` is
+    allocated here)."""
+    _need(k, _I8, "k")
+    dev = k.get_device()
+    num_pages, page_size, Hkv, D = _pool_shape(k, v, dev)
+    block = _block_scales(k_scale, v_scale, num_pages, page_size, Hkv, dev)
+    B = _lens(q_start, kv_lens, "kv_lens", dev)
+    max_pages = _pages(block_table, B, dev)
+    n, Hq, qs = _queries(q, D, dev)
+    lp = 0 if lse is None else _row_values(lse, n, Hq, "lse", dev)
+    ep = _error_word(dev_err, dev)
+    raw, ctx = _here(dev, stream)
+    if ctx is not None:
+        ctx.__enter__()
+    try:
+        if out is None:
+            out = torch.zeros(q.shape, dtype=_BF16, device=q.device)
+        elif not (out.dtype is _BF16 and out.get_device() == dev and out.is_contiguous()):
+            _wrong(out, _BF16, "out")
+        elif out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+        if n:
+            L = lib()
+            if workspace is None:
+                nbytes = L.fa3_attn_block_workspace_size(n, B, Hq, Hkv, D)
+                workspace = _chunk_workspace(nbytes, q.device, stream, dev, raw) if nbytes else None
+            wp, wn = (0, 0) if workspace is None else _given_workspace(workspace, dev)
+            i, pack, count = _CALLS["fa3_attn_gqa_block_paged"]
+            st = L.fa3_call(i, pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                    q_start.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), out.data_ptr(), lp,
+                                    n, B, Hq, Hkv, D, qs, num_pages, page_size, max_pages, block, softmax_scale, wp, wn,
+                                    ep, raw), count)
+            if st:
+                raise FA3Error("fa3_attn_gqa_block_paged", st)
+    finally:
+        if ctx is not None:
+            ctx.__exit__(None, None, None)
+    return out
+
+
+def attn_weights_gqa_block_paged(q: torch.Tensor, k: torch.Tensor, k_scale: torch.Tensor, lse: torch.Tensor,
+                                 weights: torch.Tensor, q_start: torch.Tensor, kv_lens: torch.Tensor,
+                                 block_table: torch.Tensor, softmax_scale: float,
+                                 workspace: Optional[torch.Tensor] = None, dev_err: Optional[torch.Tensor] = None,
+                                 stream=None) -> None:
+    """Adds to ``weights`` float32 [num_pages][Hkv][page_size] (attn_weight_pool), for every token of each sequence with
+    new rows and each KV head, the attention weight that the rows give it (in place); the new rows' own tokens
+    begin with nothing.
+
+    q, k, k_scale, q_start, kv_lens, block_table and softmax_scale as for attn_gqa_block_paged, and the lse that it wrote."""
+    _need_contig(k, _I8, "k")
+    dev = k.get_device()
+    num_pages, page_size, Hkv, D = _pool_shape(k, k, dev)
+    block = _block_scale(k_scale, num_pages, page_size, Hkv, "k_scale", dev)
+    B = _lens(q_start, kv_lens, "kv_lens", dev)
+    max_pages = _pages(block_table, B, dev)
+    n, Hq, qs = _queries(q, D, dev)
+    lp = _row_values(lse, n, Hq, "lse", dev)
+    gp = _weights_pool(weights, num_pages, page_size, Hkv, dev)
+    ep = _error_word(dev_err, dev)
+    raw, ctx = _here(dev, stream)
+    if not n:
+        return
+    if ctx is not None:
+        ctx.__enter__()
+    try:
+        L = lib()
+        if workspace is None:
+            workspace = _chunk_workspace(L.fa3_attn_weights_workspace_size(), q.device, stream, dev, raw, "weights")
+        wp, wn = _given_workspace(workspace, dev)
+        i, pack, count = _CALLS["fa3_attn_weights_gqa_block_paged"]
+        st = L.fa3_call(i, pack(q.data_ptr(), k.data_ptr(), k_scale.data_ptr(), lp, gp, q_start.data_ptr(),
+                                kv_lens.data_ptr(), block_table.data_ptr(), n, B, Hq, Hkv, D, qs, num_pages, page_size,
+                                max_pages, block, softmax_scale, wp, wn, ep, raw), count)
+        if st:
+            raise FA3Error("fa3_attn_weights_gqa_block_paged", st)
+    finally:
+        if ctx is not None:
+            ctx.__exit__(None, None, None)
+
+
+def evict_gqa_block_paged(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                          weights: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                          new_table: torch.Tensor, budget: int, sinks: int = 0, recent: int = 0,
+                          kept: Optional[torch.Tensor] = None, new_lens: Optional[torch.Tensor] = None,
+                          dev_err: Optional[torch.Tensor] = None, stream=None):
+    """Cuts the sequences' caches down to ``budget`` tokens, for each KV head by itself: the first ``sinks``, the last
+    ``recent`` and, of the others, those with the greatest weights (the earliest of equal ones).
+
+    The kept tokens are copied in order, with their scales and weights, to the pages in new_table int32
+    [B][new_pages], which must not be among those that block_table uses.  Returns (kept int32 [B][Hkv][budget]: their positions, -1 behind
+    them; new_lens int32 [B]: min(kv_lens, budget)); of a sequence with a bad length both are left as they were
+    (-1 and 0 when allocated here)."""
+    _need(k_cache, _I8, "k_cache")
+    dev = k_cache.get_device()
+    num_pages, page_size, Hkv, D = _pool_shape(k_cache, v_cache, dev)
+    block = _block_scales(k_scale, v_scale, num_pages, page_size, Hkv, dev)
+    gp = _weights_pool(weights, num_pages, page_size, Hkv, dev)
+    if not (kv_lens.dtype is _I32 and kv_lens.get_device() == dev and kv_lens.is_contiguous()):
+        _wrong(kv_lens, _I32, "kv_lens")
+    B = kv_lens.numel()
+    if B == 0:
+        raise ValueError("kv_lens must not be empty")
+    max_pages = _pages(block_table, B, dev)
+    if not (new_table.dtype is _I32 and new_table.get_device() == dev and new_table.is_contiguous()):
+        _wrong(new_table, _I32, "new_table")
+    if new_table.dim() != 2 or new_table.shape[0] != B:
+        raise ValueError("new_table must be [B][new_pages]")
+    new_pages = new_table.shape[1]
+    if budget <= 0 or sinks < 0 or recent < 0 or sinks + recent > budget or budget > new_pages * page_size:
+        raise ValueError("budget must be positive, hold sinks and recent, and fit new_table's pages")
+    ep = _error_word(dev_err, dev)
+    raw, ctx = _here(dev, stream)
+    if ctx is not None:
+        ctx.__enter__()
+    try:
+        if kept is None:
+            kept = torch.full((B, Hkv, budget), -1, dtype=_I32, device=k_cache.device)
+        elif not (kept.dtype is _I32 and kept.get_device() == dev and kept.is_contiguous()):
+            _wrong(kept, _I32, "kept")
+        elif kept.shape != (B, Hkv, budget):
+            raise ValueError("kept must be [B][Hkv][budget]")
+        if new_lens is None:
+            new_lens = torch.zeros(B, dtype=_I32, device=k_cache.device)
+        elif not (new_lens.dtype is _I32 and new_lens.get_device() == dev and new_lens.is_contiguous()):
+            _wrong(new_lens, _I32, "new_lens")
+        elif new_lens.numel() != B:
+            raise ValueError("new_lens must hold one value for each sequence")
+        i, pack, count = _CALLS["fa3_evict_gqa_block_paged"]
+        st = lib().fa3_call(i, pack(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), gp,
+                                    block_table.data_ptr(), kv_lens.data_ptr(), new_table.data_ptr(), kept.data_ptr(),
+                                    new_lens.data_ptr(), B, Hkv, D, num_pages, page_size, max_pages, block, new_pages,
+                                    budget, sinks, recent, ep, raw), count)
+        if st:
+            raise FA3Error("fa3_evict_gqa_block_paged", st)
+    finally:
+        if ctx is not None:
+            ctx.__exit__(None, None, None)
+    return kept, new_lens

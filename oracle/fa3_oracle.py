@@ -629,3 +629,133 @@ def packed_attention(q8, keys, values, q_scale, k_scale, v_scale, q_start, lens,
                 w = np.exp(s - s.max())
                 out[row, h] = float(v_scale[g]) * (w @ values[b][:T_i, g].astype(np.float64)) / w.sum()
     return out
+
+
+# ---------------------------------------------------------------------------
+# A paged cache with a scale for each block of tokens and head (no counterpart in
+# the pages, whose scales are calibrated; symmetric codes as FA3量化 算法流程 step 4)
+# ---------------------------------------------------------------------------
+def block_row(table: np.ndarray, b: int, t: int, page_size: int):
+    """Page and row in the page of token t of sequence b."""
+    return int(table[b, t // page_size]), t % page_size
+
+
+def rescale_codes(codes: np.ndarray, old, new) -> np.ndarray:
+    """round_half_even(code * fl(old / new)); the product of 8 and 24 bits is exact in float64."""
+    if np.float32(new) == 0 or np.float32(old) == np.float32(new):
+        return codes.copy()
+    ratio = np.float32(old) / np.float32(new)
+    return np.rint(codes.astype(np.float64) * np.float64(ratio)).astype(np.int8)
+
+
+def append_block_paged(k, v, k_pool, v_pool, k_scale, v_scale, table, q_start, kv_lens):
+    """New rows into block-scaled pools; returns copies of (k_pool, v_pool, k_scale, v_scale)."""
+    out = [x.copy() for x in (k_pool, v_pool, k_scale, v_scale)]
+    ps, block = k_pool.shape[1], k_pool.shape[1] // k_scale.shape[1]
+    for b, end in enumerate(kv_lens):
+        n = int(q_start[b + 1] - q_start[b])
+        start = int(end) - n
+        for lo in range(start // block * block, int(end) if n else 0, block):
+            old, new = range(lo, max(lo, start)), range(max(lo, start), min(lo + block, int(end)))
+            page, at = block_row(table, b, lo, ps)
+            rows = [int(q_start[b]) + t - start for t in new]
+            for x, pool, scale in ((k, out[0], out[2]), (v, out[1], out[3])):
+                for h in range(pool.shape[2]):
+                    val = x[rows, h].astype(np.float32)
+                    fine = np.abs(val[np.isfinite(val)])
+                    s = np.float32(fine.max() if fine.size else 0) / np.float32(127)
+                    s0 = scale[page, at // block, h]
+                    if len(old) and not s > s0:
+                        s = s0
+                    for t in old:
+                        pool[page, t % ps, h] = rescale_codes(pool[page, t % ps, h], s0, s)
+                    scale[page, at // block, h] = s
+                    for t, y in zip(new, val):                # NaN: -127, the quantizer's lowest code
+                        pool[page, t % ps, h] = quantize(np.where(np.isnan(y), np.float32(-np.inf), y), s)
+    return out
+
+
+def cached_block_values(pool, scale, table, b, end):
+    """float64 [end][Hkv][D]: what sequence b's first `end` tokens stand for."""
+    ps, block = pool.shape[1], pool.shape[1] // scale.shape[1]
+    at = [block_row(table, b, t, ps) for t in range(int(end))]
+    page, row = np.array([a[0] for a in at], int), np.array([a[1] for a in at], int)
+    return pool[page, row].astype(np.float64) * scale[page, row // block].astype(np.float64)[..., None]
+
+
+def block_scores(q, k_pool, k_scale, table, q_start, kv_lens, sm):
+    """Yields (sequence, rows, query head, scores float64 [rows][T], -inf where a row does not see a token)."""
+    Hq, Hkv = q.shape[1], k_pool.shape[2]
+    for b, end in enumerate(kv_lens):
+        r0, r1 = int(q_start[b]), int(q_start[b + 1])
+        if r1 == r0:
+            continue
+        keys = cached_block_values(k_pool, k_scale, table, b, end)
+        last = int(end) - (r1 - r0) + np.arange(r1 - r0)
+        for h in range(Hq):
+            s = q[r0:r1, h].astype(np.float64) @ keys[:, h // (Hq // Hkv)].T * float(sm)
+            yield b, slice(r0, r1), h, np.where(np.arange(int(end))[None] > last[:, None], -np.inf, s)
+
+
+def attention_block(q, k_pool, v_pool, k_scale, v_scale, table, q_start, kv_lens, sm, out, lse):
+    """Causal attention of packed rows; returns (out, lse) as float64 copies with the rows of sequences filled in."""
+    out, lse = out.astype(np.float64), lse.astype(np.float64)
+    g = q.shape[1] // k_pool.shape[2]
+    values = {}
+    for b, rows, h, s in block_scores(q, k_pool, k_scale, table, q_start, kv_lens, sm):
+        if b not in values:
+            values = {b: cached_block_values(v_pool, v_scale, table, b, kv_lens[b])}
+        m = s.max(1, keepdims=True)
+        p = np.exp(s - m)
+        out[rows, h] = p @ values[b][:, h // g] / p.sum(1, keepdims=True)
+        lse[rows, h] = m[:, 0] + np.log(p.sum(1))
+    return out, lse
+
+
+def attention_weights_block(q, k_pool, k_scale, lse, weights, table, q_start, kv_lens, sm):
+    """Returns the weights pool [num_pages][Hkv][page_size] in float64 with the rows' attention weights added."""
+    out, ps = weights.astype(np.float64), k_pool.shape[1]
+    g = q.shape[1] // k_pool.shape[2]
+    for b, rows, h, s in block_scores(q, k_pool, k_scale, table, q_start, kv_lens, sm):
+        w = np.exp(s - lse[rows, h].astype(np.float64)[:, None]).sum(0)
+        for t in range(int(kv_lens[b])):
+            page, at = block_row(table, b, t, ps)
+            if h % g == 0 and t >= int(kv_lens[b]) - (rows.stop - rows.start):
+                out[page, h // g, at] = 0
+            out[page, h // g, at] += w[t]
+    return out
+
+
+def kept_tokens(w, budget: int, sinks: int, recent: int):
+    """Positions of the tokens that stay of a context with weights w, in order."""
+    T = len(w)
+    if T <= budget:
+        return list(range(T))
+    middle = list(range(sinks, T - recent))
+    # greatest first (NaN above all, -0 as 0), the earliest of equal ones
+    middle.sort(key=lambda t: (0 if np.isnan(w[t]) else 1, 0.0 if np.isnan(w[t]) else -float(w[t]) + 0.0, t))
+    return sorted(list(range(sinks)) + middle[:budget - sinks - recent] + list(range(T - recent, T)))
+
+
+def evict_block_paged(k_pool, v_pool, k_scale, v_scale, weights, table, kv_lens, new_table, budget, sinks, recent):
+    """Returns (kept, new_lens, k_pool, v_pool, k_scale, v_scale, weights) after the eviction."""
+    pools, scales, weights = [k_pool.copy(), v_pool.copy()], [k_scale.copy(), v_scale.copy()], weights.copy()
+    ps, block, Hkv = k_pool.shape[1], k_pool.shape[1] // k_scale.shape[1], k_pool.shape[2]
+    B = len(kv_lens)
+    kept, new_lens = np.full((B, Hkv, budget), -1, np.int32), np.zeros(B, np.int32)
+    for b in range(B):
+        new_lens[b] = min(int(kv_lens[b]), budget)
+        where = [block_row(table, b, t, ps) for t in range(int(kv_lens[b]))]
+        for h in range(Hkv):
+            keep = kept_tokens([weights[p, h, r] for p, r in where], budget, sinks, recent)
+            kept[b, h, :len(keep)] = keep
+            for lo in range(0, len(keep), block):
+                part = keep[lo:lo + block]
+                for pool, scale, old_pool, old_scale in zip(pools, scales, (k_pool, v_pool), (k_scale, v_scale)):
+                    s = [old_scale[where[t][0], where[t][1] // block, h] for t in part]
+                    page, at = block_row(new_table, b, lo, ps)
+                    scale[page, at // block, h] = max(s)
+                    for i, (t, si) in enumerate(zip(part, s)):
+                        pool[page, at + i, h] = rescale_codes(old_pool[where[t][0], where[t][1], h], si, max(s))
+                        weights[page, h, at + i] = weights[where[t][0], h, where[t][1]]
+    return (kept, new_lens, *pools, *scales, weights)
