@@ -55,6 +55,7 @@
 // Every wait is bounded; on time-out the kernel sets FA3_DEVERR_TIMEOUT, waits for its
 // copies and MMAs, frees its TMEM and returns.
 #include "fa3_common.cuh"
+#include "fa3_few.cuh"
 #include "fa3_packed.cuh"
 #include "fa3_pipe.cuh"
 #include "fa3_tc.cuh"
@@ -449,9 +450,6 @@ __device__ __forceinline__ void wait_max(float& a, float& b) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(a), "+f"(b) :: "memory");
 }
 
-// Natural logarithm of a row's sum of exponentials: the sum of 2^(.. - m) is l.
-__device__ __forceinline__ float log_sum(float m, float l) { return l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F; }
-
 // A row of 128 bf16 values as fp16, times a power of two that brings the largest to [2^14, 2^15): exact, but for values
 // below 2^-38 of it.  Writes the chunks of 8 values 2048 bytes apart; returns the inverse of the power.
 __device__ __forceinline__ float put_query_row(const uint16_t* row, bool active, uint8_t* dst) {
@@ -473,7 +471,6 @@ __device__ __forceinline__ float put_query_row(const uint16_t* row, bool active,
 
 // The scales of a key tile's eight groups of 16 keys (a block's keys lie in whole groups), a lane each: lanes 0 .. 7 the
 // keys', 8 .. 15 the values'.  Looked up ahead: the page two tiles, the scale one.
-constexpr float kLeastScale = 8.271806125530277e-25f;        // 2^-80: a smaller value scale counts as this
 struct TileScales {
   const int32_t* table;           // the sequence's pages
   const float* pool;
@@ -1186,6 +1183,15 @@ int chunk_attn(ChunkParams& p, int D, float softmax_scale, void* workspace, size
   p.ctas = sms;
   p.rows_max = rows_max_of(p.n, p.G);
   if (!workspace || workspace_bytes < workspace_bytes_of(sms, p.rows_max) || !aligned16(workspace)) return FA3_EWORKSPACE;
+  if constexpr (BLOCK) {
+    if (few_rows(p.n, p.B, p.Hkv, p.G, p.T)) {
+      if (workspace_bytes < few_rows_workspace(p.n, p.B, p.G, sms)) return FA3_EWORKSPACE;
+      const FewCall c = {p.qf, p.k, p.v, p.ks, p.vs, p.q_start, p.kv_lens, p.out, p.lse, p.q_stride, p.n, p.B, p.Hq, p.G, sms,
+                         p.sm_log2, p.err};
+      return cuda_status(few_rows_attn(c, p.block_table, p.num_pages, p.page_size, p.max_pages, p.page_size / p.per_page, p.Hkv,
+                                       workspace, static_cast<cudaStream_t>(stream)));
+    }
+  }
   p.part_o = static_cast<float4*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)2 * sms * (kD / 4) * p.rows_max);
   p.cuts = reinterpret_cast<Cut*>(p.part_ml + (size_t)2 * sms * p.rows_max);
@@ -1243,7 +1249,11 @@ FA3_API int fa3_cross_attn_gqa(const int8_t* q, const int8_t* k, const int8_t* v
 }
 
 FA3_API size_t fa3_attn_block_workspace_size(int n, int B, int Hq, int Hkv, int D) {
-  return fa3_chunk_workspace_size(n, B, Hq, Hkv, D);
+  const size_t chunk = fa3_chunk_workspace_size(n, B, Hq, Hkv, D);
+  if (chunk == 0) return 0;
+  int sms = 0;
+  if (check_device(&sms) != FA3_OK) sms = 152;
+  return std::max(chunk, few_rows_workspace(n, B, Hq / Hkv, sms));
 }
 
 FA3_API int fa3_attn_gqa_block_paged(const uint16_t* q, const int8_t* k_cache, const int8_t* v_cache, const float* k_scale,

@@ -1,0 +1,535 @@
+// Attention of few packed rows a sequence (decode steps, drafts) over a block-scaled paged INT8 cache.
+//
+// The call's arithmetic is fa3_chunk.cu's (block-scaled variant); here it is HBM-bound: each KV byte meets a handful of
+// query columns, too few for the 128 rows of tcgen05.mma.  A column is a new row's query head; a column tile is RT rows x the
+// group's G heads, up to 8 NT columns, as the N side of warp-level MMAs with 16 tokens as the M side:
+//   * scores  S^T[16 tokens x 8 columns] = K . Q^T by m16n8k16 f16, int8 codes exact in fp16, bf16 queries exact after a
+//     power of two by column; the contraction order is permuted so that a thread's K and Q words are the bytes it holds;
+//   * x = s log2(e) + log2(value scale), P = 2^(x - m) as fp16, O^T += V^T . P^T on V's bare codes, and the row sum takes P
+//     over the value scale: a step of 16 tokens lies in one block of the cache, so its scales are one number each;
+//   * P lies 2^7 to 2^15 above fp16's normal range's end for the row's largest, which moves lazily.
+//
+// Work.  A unit is a column tile of one sequence and KV head; its steps of 16 tokens and all others lie on one line that is
+// cut into equal parts, one per resident CTA, so ragged batches and one long context fill the GPU alike.  A CTA's four
+// warps take a unit's steps in turn, each through its own cp.async ring, and merge at its end; a cut unit's parts meet in
+// few_combine_kernel.
+#include "fa3_few.cuh"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math_constants.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+
+namespace fa3 {
+namespace {
+
+constexpr int kD = 128;
+constexpr int kStep = 16;          // tokens of a warp's step
+constexpr int kWarps = 4, kThreadsF = 32 * kWarps;
+constexpr int kStages = 2;
+constexpr int kStageBytes = 2 * kStep * kD;                // K, then V rows
+constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+
+// What a unit costs beside its steps, and the least part of the line a CTA takes (enough for a part inside a unit to hold a
+// step), in steps of a CTA's warp.
+constexpr int kUnitSteps = 12, kLeastSteps = 16;
+static_assert(kLeastSteps > kUnitSteps, "a part inside a unit, behind its fixed cost, holds a step");
+
+struct CutF {
+  int b, tile, g, first, last;     // unit, CTAs that have parts of it; first < 0: none begins here
+};
+
+struct FewParams {
+  const uint16_t* q;
+  const int8_t* k;
+  const int8_t* v;
+  const float* ks;
+  const float* vs;
+  const int32_t* q_start;
+  const int32_t* kv_lens;
+  __nv_bfloat16* out;
+  float* lse;
+  float* part_o;                   // [2 * CTAs][columns][128]
+  float2* part_ml;                 // [2 * CTAs][columns]
+  CutF* cuts;                      // [CTAs]
+  int32_t* err;
+  int64_t q_stride;
+  Pages pg;
+  int n, B, Hq, G, RT, ctas;
+  DivU32 div_RT, div_G;
+  float sm_log2;
+};
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Four signed int8 codes -> two f16x2 (exact).
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  lo = __byte_perm(u, 0x64646464u, 0x4140);
+  hi = __byte_perm(u, 0x64646464u, 0x4342);
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(0x64806480u));
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(0x64806480u));
+}
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// Row values 4 lane .. 4 lane + 3 of a row whose weighted sum is a and whose weights' is l.
+__device__ __forceinline__ void put_row(__nv_bfloat16* row, int lane, const float (&a)[4], float l) {
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const __nv_bfloat162 x = __floats2bfloat162_rn(a[0] * inv, a[1] * inv), y = __floats2bfloat162_rn(a[2] * inv, a[3] * inv);
+  *reinterpret_cast<uint2*>(row + 4 * lane) = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+}
+
+struct SeqF {
+  int q0, nq, nkv;
+};
+// nq = 0: nothing to do; -1: q_start falls.
+__device__ __forceinline__ SeqF sequence_of(const FewParams& p, int b, bool report) {
+  SeqF s;
+  s.q0 = p.q_start[b];
+  const int q1 = p.q_start[b + 1];
+  s.nkv = p.kv_lens[b];
+  s.nq = q1 - s.q0;
+  if (s.q0 < 0 || q1 < s.q0 || q1 > p.n || (s.nq > 0 && (s.nkv < s.nq || s.nkv > p.pg.T_max))) {
+    if (report) set_dev_err(p.err, FA3_DEVERR_LENS);
+    s.nq = q1 < s.q0 ? -1 : 0;
+  }
+  return s;
+}
+// Column tiles, and the cost of one (all of a sequence's count as its last).
+__device__ __forceinline__ int tiles_of(const FewParams& p, const SeqF& s) {
+  return s.nq > 0 ? (int)divu32((uint32_t)(s.nq + p.RT - 1), p.div_RT) : 0;
+}
+__device__ __forceinline__ int cost_of(const SeqF& s) { return kUnitSteps + (int)(((uint32_t)s.nkv + kStep - 1) / kStep); }
+__device__ __forceinline__ int64_t sequence_cost(const FewParams& p, const SeqF& s) {
+  return s.nq > 0 ? (int64_t)tiles_of(p, s) * p.pg.Hkv * cost_of(s) : 0;
+}
+
+struct Where {
+  int64_t total;                   // of the line
+  int64_t off;                     // of the CTA's begin in sequence b
+  int b;
+};
+
+// The line's length, and the sequence that holds its position of CTA `cta` (the block together).
+__device__ __forceinline__ Where find_begin(const FewParams& p, int cta, int64_t* warp_sum, Where* found) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.B + kThreadsF - 1) / kThreadsF, b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+  int64_t sum = 0;
+  bool falls = false;
+  for (int b = b0; b < b1; ++b) {
+    const SeqF s = sequence_of(p, b, cta == 0);
+    falls |= s.nq < 0;
+    sum += sequence_cost(p, s);
+  }
+  int64_t upto = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  if (lane == 31) warp_sum[warp] = upto;
+  falls = __syncthreads_or(falls);
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) upto += warp_sum[w];
+    total += warp_sum[w];
+  }
+  if (falls) total = 0;
+  const int64_t most = total / kLeastSteps, parts = most < 1 ? 1 : min(most, (int64_t)p.ctas);
+  const int64_t x = cta >= parts ? total : total * cta / parts;
+  if (x < total && upto > x && upto - sum <= x) {
+    int64_t off = x - (upto - sum);
+    int b = b0;
+    for (; b < b1; ++b) {
+      const int64_t c = sequence_cost(p, sequence_of(p, b, false));
+      if (off < c) break;
+      off -= c;
+    }
+    *found = Where{total, off, b};
+  }
+  __syncthreads();
+  return x < total ? *found : Where{total, 0, p.B};
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kThreadsF, NT == 1 ? 4 : 3) few_rows_kernel(const __grid_constant__ FewParams p) {
+  // A 128-byte row stores its 16-byte chunk c at position c ^ f(row & 7), f(r) = (r & 6) ^ 4 (r & 1): every 8-lane
+  // phase of the K and V fragment loads below then touches 8 distinct 16-byte bank groups.
+  extern __shared__ __align__(128) uint8_t fsm[];
+  constexpr int kCols = 8 * NT;
+  float (*sm_o)[kCols][kD] = reinterpret_cast<float (*)[kCols][kD]>(fsm);   // at a unit's end, in the rings' place
+  static_assert(kWarps * kCols * kD * 4 <= kRingBytes, "partial O fits in the rings");
+  __shared__ float sm_m[kWarps][kCols], sm_l[kWarps][kCols];
+  __shared__ int64_t warp_sum[kWarps];
+  __shared__ Where found;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+  const int r = lane >> 2, qd = lane & 3;
+  Where w = find_begin(p, cta, warp_sum, &found);
+  const int64_t parts = max((int64_t)1, min(w.total / kLeastSteps, (int64_t)p.ctas));
+  auto begin = [&](int64_t c) { return c >= parts ? w.total : w.total * c / parts; };
+  int64_t x = begin(cta), left = begin(cta + 1) - x;
+  CutF cut = {0, 0, 0, -1, -1};
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(fsm) + (uint32_t)(warp * kStages * kStageBytes);
+  auto swz = [](int row) { return (row & 6) ^ ((row & 1) << 2); };
+  auto chunk_addr = [&](uint32_t base, int row, int col) { return base + row * 128 + ((col ^ swz(row)) << 4); };
+  const int64_t tok_stride = (int64_t)p.pg.Hkv * kD;
+
+  SeqF s = {0, 0, 0};
+  int tile = 0, g = 0, off = 0;
+  if (left > 0) {
+    s = sequence_of(p, w.b, false);
+    const int64_t u = w.off / cost_of(s);
+    off = (int)(w.off - u * cost_of(s));
+    tile = (int)(u / p.pg.Hkv);
+    g = (int)(u - (int64_t)tile * p.pg.Hkv);
+  }
+  while (left > 0) {
+    const int cost = cost_of(s), take = (int)min((int64_t)(cost - off), left);
+    // the unit's rows, columns, keys and steps
+    const int i0 = tile * p.RT, cols = min(p.RT, s.nq - i0) * p.G;
+    const int c0 = s.nkv - s.nq, keys = c0 + min(s.nq, i0 + p.RT), steps = (keys + kStep - 1) / kStep;
+    auto step_at = [&](int o) { return min(max(o - kUnitSteps, 0), steps); };
+    const int s0 = step_at(off), s1 = off + take == cost ? steps : step_at(off + take);
+    if (s0 < s1) {
+      const bool whole = s0 == 0 && s1 == steps;
+      // A part that begins the unit records the cut; the costs count some steps that only the last tile has, so the last CTA
+      // with any is the one that holds the last step.
+      if (s0 == 0 && !whole) {
+        const int64_t end = x + (kUnitSteps + steps - off) - 1;
+        int64_t c = ((end + 1) * parts - 1) / w.total;
+        while (c > 0 && begin(c) > end) --c;
+        while (c + 1 < parts && begin(c + 1) <= end) ++c;
+        cut = CutF{w.b, tile, g, cta, (int)c};
+      }
+      const int32_t* table = p.pg.table + (int64_t)w.b * p.pg.max_pages;
+      const int8_t* kbase = p.k + (int64_t)g * kD;
+      const int8_t* vbase = p.v + (int64_t)g * kD;
+      const int n_my = s1 - s0 > warp ? (s1 - s0 - warp + kWarps - 1) / kWarps : 0;   // steps s0 + warp, + 4, ...
+      // A step's page is looked up two steps ahead and its scales one step ahead of their use.
+      auto entry_of = [&](int m) {
+        return __ldg(table + divu32((uint32_t)((s0 + warp + kWarps * m) * kStep), p.pg.div_ps));
+      };
+      int pg_next = n_my > 0 ? entry_of(0) : 0;
+      float ks_next = 0.f, vs_next = 0.f;
+      auto issue = [&](int m, int stage) {
+        const int t0 = (s0 + warp + kWarps * m) * kStep;
+        int page = pg_next;
+        if (m + 1 < n_my) pg_next = entry_of(m + 1);
+        if ((uint32_t)page >= (uint32_t)p.pg.num_pages) {          // outside the pool: any page of it
+          if (lane == 0) set_dev_err(p.err, FA3_DEVERR_PAGE);
+          page = 0;
+        }
+        const int at = t0 - (int)divu32((uint32_t)t0, p.pg.div_ps) * p.pg.page_size;
+        const int64_t row0 = (int64_t)page * p.pg.page_size + at;
+        const int64_t sc = ((int64_t)page * p.pg.per_page + (int)divu32((uint32_t)at, p.pg.div_block)) * p.pg.Hkv + g;
+        ks_next = __ldg(p.ks + sc);
+        vs_next = __ldg(p.vs + sc);
+#pragma unroll
+        for (int i8 = 0; i8 < 8; ++i8) {
+          const int i = lane + 32 * i8, kv = i >> 7, row = (i >> 3) & 15, col = i & 7;
+          // rows behind the context are read as they are (they lie in the same page) and masked
+          cp_async16(ring + stage * kStageBytes + kv * 2048 + row * 128 + ((col ^ swz(row)) << 4),
+                     (kv ? vbase : kbase) + (row0 + row) * tok_stride + col * 16);
+        }
+      };
+      if (n_my > 0) issue(0, 0);
+      cp_async_commit();
+      // Q^T fragments: thread (r, qd) holds column 8 nt + r's values [16 qd, +16) and [64 + 16 qd, +16) as fp16, times a
+      // power of two that brings the column's largest to [2^14, 2^15).
+      uint32_t qh[NT][8][2];
+      float f0[NT], f1[NT];
+      int lim0[NT], lim1[NT];                                   // last key of columns 8 nt + 2 qd, + 1; -1: no column
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int col = 8 * nt + r, ri = (int)divu32((uint32_t)col, p.div_G);
+        uint4 v[4];
+        const uint16_t* row = p.q + (int64_t)(s.q0 + i0 + ri) * p.q_stride + (int64_t)(g * p.G + col - ri * p.G) * kD;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[i] = col < cols ? __ldg(reinterpret_cast<const uint4*>(row + (i >> 1) * 64 + 16 * qd + 8 * (i & 1)))
+                            : make_uint4(0u, 0u, 0u, 0u);
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
+                                       __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu)));
+        top = max(top & 0xffffu, top >> 16);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const uint32_t e = max(top >> 7, 15u);                  // the largest's exponent: 2^(e - 127)
+        const float f = __uint_as_float((268u - e) << 23);
+        auto two = [&](uint32_t y) { return pack_f16x2(__uint_as_float(y << 16) * f, __uint_as_float(y & 0xffff0000u) * f); };
+#pragma unroll
+        for (int st = 0; st < 8; ++st) {
+          qh[nt][st][0] = two(word(v[st >> 1], 2 * (st & 1)));
+          qh[nt][st][1] = two(word(v[st >> 1], 2 * (st & 1) + 1));
+        }
+        const float inv = __uint_as_float((e - 14u) << 23) * p.sm_log2;
+        f0[nt] = __shfl_sync(0xffffffffu, inv, 4 * (2 * qd));
+        f1[nt] = __shfl_sync(0xffffffffu, inv, 4 * (2 * qd + 1));
+        const int ca = 8 * nt + 2 * qd;
+        lim0[nt] = ca < cols ? c0 + i0 + (int)divu32((uint32_t)ca, p.div_G) : -1;
+        lim1[nt] = ca + 1 < cols ? c0 + i0 + (int)divu32((uint32_t)(ca + 1), p.div_G) : -1;
+      }
+      float m0[NT], m1[NT], l0[NT], l1[NT], o[NT][8][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        m0[nt] = m1[nt] = -CUDART_INF_F;
+        l0[nt] = l1[nt] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+      }
+      for (int m = 0; m < n_my; ++m) {
+        const int t0 = (s0 + warp + kWarps * m) * kStep;
+        const float ks = ks_next, vs = fmaxf(vs_next, kLeastScale);
+        if (m + 1 < n_my) issue(m + 1, (m + 1) % kStages);
+        cp_async_commit();
+        cp_async_wait<1>();
+        __syncwarp();
+        const uint32_t kst = ring + (m % kStages) * kStageBytes, vst = kst + 2048;
+        uint4 kr[4], vr[4];
+        kr[0] = lds128(chunk_addr(kst, r, qd));
+        kr[1] = lds128(chunk_addr(kst, r, 4 + qd));
+        kr[2] = lds128(chunk_addr(kst, r + 8, qd));
+        kr[3] = lds128(chunk_addr(kst, r + 8, 4 + qd));
+        vr[0] = lds128(chunk_addr(vst, 2 * qd, r));
+        vr[1] = lds128(chunk_addr(vst, 2 * qd + 1, r));
+        vr[2] = lds128(chunk_addr(vst, 2 * qd + 8, r));
+        vr[3] = lds128(chunk_addr(vst, 2 * qd + 9, r));
+        __syncwarp();                                           // every lane has its fragments: the stage may be refilled
+        float cf[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) cf[nt][0] = cf[nt][1] = cf[nt][2] = cf[nt][3] = 0.f;
+#pragma unroll
+        for (int st = 0; st < 8; ++st) {
+          uint32_t a0, a1, a2, a3;
+          codes_to_f16(word(kr[st >> 2], st & 3), a0, a2);       // row r: the thread's values 4 st .. 4 st + 3
+          codes_to_f16(word(kr[2 + (st >> 2)], st & 3), a1, a3);  // row r + 8
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816(cf[nt], a0, a1, a2, a3, qh[nt][st][0], qh[nt][st][1]);
+        }
+        const float lv = __log2f(vs), rv = __fdividef(1.f, vs);
+        uint32_t b0[NT], b1[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float e0 = f0[nt] * ks, e1 = f1[nt] * ks;
+          const int ta = t0 + r, tb = ta + 8;
+          const float x0 = ta <= lim0[nt] ? fmaf(cf[nt][0], e0, lv) : -CUDART_INF_F;
+          const float x1 = ta <= lim1[nt] ? fmaf(cf[nt][1], e1, lv) : -CUDART_INF_F;
+          const float x2 = tb <= lim0[nt] ? fmaf(cf[nt][2], e0, lv) : -CUDART_INF_F;
+          const float x3 = tb <= lim1[nt] ? fmaf(cf[nt][3], e1, lv) : -CUDART_INF_F;
+          float mx0 = fmaxf(x0, x2), mx1 = fmaxf(x1, x3);
+#pragma unroll
+          for (int o_ = 4; o_ < 32; o_ <<= 1) {
+            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o_));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o_));
+          }
+          // The reference lies 7 below the largest when it is set and moves only when that has grown by more than 8.
+          const bool g0 = mx0 - 7.f > m0[nt] + 8.f, g1 = mx1 - 7.f > m1[nt] + 8.f;
+          if (__any_sync(0xffffffffu, g0 || g1)) {
+            const float n0 = g0 ? mx0 - 7.f : m0[nt], n1 = g1 ? mx1 - 7.f : m1[nt];
+            const float al0 = g0 ? (m0[nt] == -CUDART_INF_F ? 0.f : ex2_approx(m0[nt] - n0)) : 1.f;
+            const float al1 = g1 ? (m1[nt] == -CUDART_INF_F ? 0.f : ex2_approx(m1[nt] - n1)) : 1.f;
+            l0[nt] *= al0;
+            l1[nt] *= al1;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              o[nt][i][0] *= al0; o[nt][i][1] *= al1; o[nt][i][2] *= al0; o[nt][i][3] *= al1;
+            }
+            m0[nt] = n0;
+            m1[nt] = n1;
+          }
+          const float ref0 = m0[nt] == -CUDART_INF_F ? 0.f : m0[nt], ref1 = m1[nt] == -CUDART_INF_F ? 0.f : m1[nt];
+          const float p0 = ex2_approx(x0 - ref0), p1 = ex2_approx(x1 - ref1), p2 = ex2_approx(x2 - ref0),
+                      p3 = ex2_approx(x3 - ref1);
+          l0[nt] = fmaf(p0 + p2, rv, l0[nt]);
+          l1[nt] = fmaf(p1 + p3, rv, l1[nt]);
+          b0[nt] = movmatrix_trans(pack_f16x2(p0, p1));
+          b1[nt] = movmatrix_trans(pack_f16x2(p2, p3));
+        }
+        // O^T += V^T . P^T; m-tile i covers values 16 r + 2 i (row r) and 16 r + 2 i + 1 (row r + 8)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
+          uint32_t a0, a1, a2, a3;
+          codes_to_f16(__byte_perm(word(vr[0], i >> 1), word(vr[1], i >> 1), sel), a0, a1);
+          codes_to_f16(__byte_perm(word(vr[2], i >> 1), word(vr[3], i >> 1), sel), a2, a3);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][i], a0, a1, a2, a3, b0[nt], b1[nt]);
+        }
+      }
+      cp_async_wait<0>();
+      // ---- merge the warps (the rings become the partial-O buffer)
+      __syncthreads();
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int o_ = 4; o_ < 32; o_ <<= 1) {
+          l0[nt] += __shfl_xor_sync(0xffffffffu, l0[nt], o_);
+          l1[nt] += __shfl_xor_sync(0xffffffffu, l1[nt], o_);
+        }
+        const int ca = 8 * nt + 2 * qd;
+        if (r == 0) {
+          sm_m[warp][ca] = m0[nt]; sm_m[warp][ca + 1] = m1[nt];
+          sm_l[warp][ca] = l0[nt]; sm_l[warp][ca + 1] = l1[nt];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          *reinterpret_cast<float2*>(&sm_o[warp][ca][16 * r + 2 * i]) = make_float2(o[nt][i][0], o[nt][i][2]);
+          *reinterpret_cast<float2*>(&sm_o[warp][ca + 1][16 * r + 2 * i]) = make_float2(o[nt][i][1], o[nt][i][3]);
+        }
+      }
+      __syncthreads();
+      // a warp has every fourth column, a lane four values
+      for (int col = warp; col < cols; col += kWarps) {
+        float M = -CUDART_INF_F;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) M = fmaxf(M, sm_m[k][col]);
+        float L = 0.f, a[4] = {};
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+          const float fk = M == -CUDART_INF_F ? 0.f : ex2_approx(sm_m[k][col] - M);
+          const float4 ok = *reinterpret_cast<const float4*>(&sm_o[k][col][4 * lane]);
+          L = fmaf(sm_l[k][col], fk, L);
+          a[0] = fmaf(ok.x, fk, a[0]); a[1] = fmaf(ok.y, fk, a[1]); a[2] = fmaf(ok.z, fk, a[2]); a[3] = fmaf(ok.w, fk, a[3]);
+        }
+        const int ri = (int)divu32((uint32_t)col, p.div_G);
+        const int64_t orow = (int64_t)(s.q0 + i0 + ri) * p.Hq + g * p.G + col - ri * p.G;
+        if (whole) {
+          put_row(p.out + orow * kD, lane, a, L);
+          if (lane == 0 && p.lse) p.lse[orow] = log_sum(M, L);
+        } else {
+          const int64_t slot = (int64_t)(2 * cta + (s0 == 0 ? 1 : 0)) * kCols + col;
+          *reinterpret_cast<float4*>(p.part_o + slot * kD + 4 * lane) = make_float4(a[0], a[1], a[2], a[3]);
+          if (lane == 0) p.part_ml[slot] = make_float2(M, L);
+        }
+      }
+      __syncthreads();                                          // the rings are the next unit's
+    }
+    left -= take;
+    x += take;
+    off = 0;
+    if (++g == p.pg.Hkv) {
+      g = 0;
+      if (++tile == tiles_of(p, s) && left > 0) {
+        tile = 0;
+        do {
+          s = ++w.b < p.B ? sequence_of(p, w.b, false) : SeqF{0, 1, 0};
+        } while (s.nq <= 0);
+      }
+    }
+  }
+  if (tid == 0) p.cuts[cta] = cut;
+}
+
+// Merges the parts of the unit whose first cut lies behind CTA blockIdx.x's part: a warp a column.
+template <int NT>
+__global__ void __launch_bounds__(kThreadsF) few_combine_kernel(const __grid_constant__ FewParams p) {
+  constexpr int kCols = 8 * NT;
+  pdl_wait();
+  pdl_launch_dependents();
+  const CutF u = p.cuts[blockIdx.x];
+  if (u.first < 0) return;
+  const int lane = threadIdx.x & 31, col = blockIdx.y * kWarps + (threadIdx.x >> 5);
+  const int q0 = p.q_start[u.b], nq = p.q_start[u.b + 1] - q0, i0 = u.tile * p.RT, cols = min(p.RT, nq - i0) * p.G;
+  if (col >= cols) return;
+  auto slot = [&](int c) { return (int64_t)(2 * c + (c == u.first ? 1 : 0)) * kCols + col; };
+  float M = -CUDART_INF_F;
+  for (int c = u.first; c <= u.last; ++c) M = fmaxf(M, p.part_ml[slot(c)].x);
+  float L = 0.f, a[4] = {};
+#pragma unroll 4
+  for (int c = u.first; c <= u.last; ++c) {
+    const float2 ml = p.part_ml[slot(c)];
+    const float4 o = *reinterpret_cast<const float4*>(p.part_o + slot(c) * kD + 4 * lane);
+    const float f = M == -CUDART_INF_F ? 0.f : ex2_approx(ml.x - M);
+    L = fmaf(ml.y, f, L);
+    a[0] = fmaf(o.x, f, a[0]); a[1] = fmaf(o.y, f, a[1]); a[2] = fmaf(o.z, f, a[2]); a[3] = fmaf(o.w, f, a[3]);
+  }
+  const int ri = (int)divu32((uint32_t)col, p.div_G);
+  const int64_t orow = (int64_t)(q0 + i0 + ri) * p.Hq + u.g * p.G + col - ri * p.G;
+  put_row(p.out + orow * kD, lane, a, L);
+  if (lane == 0 && p.lse) p.lse[orow] = log_sum(M, L);
+}
+
+// Column tiles of 8 where sequences have 8 columns or fewer on average, of 16 otherwise.
+int n_tiles(int n, int B, int G) { return (int64_t)std::max(1, n / B) * G <= 8 ? 1 : 2; }
+int ctas_of(int nt, int sms) { return sms * (nt == 1 ? 4 : 3); }
+size_t bytes_of(int nt, int ctas) {
+  return (size_t)ctas * (2 * 8 * nt * (kD * sizeof(float) + sizeof(float2)) + sizeof(CutF));
+}
+
+template <int NT>
+cudaError_t launch(FewParams& p, void* workspace, cudaStream_t s) {
+  p.RT = 8 * NT / p.G;
+  p.div_RT = make_divu32((uint32_t)p.RT);
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)2 * p.ctas * 8 * NT * kD);
+  p.cuts = reinterpret_cast<CutF*>(p.part_ml + (size_t)2 * p.ctas * 8 * NT);
+  const LaunchTogether together(s);
+  cudaError_t e = launch_pdl(few_rows_kernel<NT>, dim3((unsigned)p.ctas), dim3(kThreadsF), kRingBytes, s, p);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(few_combine_kernel<NT>, dim3((unsigned)p.ctas, 2 * NT), dim3(kThreadsF), 0, s, p);
+}
+
+}  // namespace
+
+bool few_rows(int n, int B, int Hkv, int G, int T_max) {
+  const double units = (double)n + B;
+  return G <= 16 && (int64_t)n * G <= (int64_t)48 * B && units * Hkv * (T_max / kStep + kUnitSteps + 1.0) * 1024.0 < 4503599627370496.0;
+}
+size_t few_rows_workspace(int n, int B, int G, int sms) {
+  if (G > 16) return 0;
+  const int nt = n_tiles(n, B, G);
+  return bytes_of(nt, ctas_of(nt, sms));
+}
+cudaError_t few_rows_attn(const FewCall& c, const int32_t* table, int num_pages, int page_size, int max_pages, int block,
+                          int Hkv, void* workspace, cudaStream_t s) {
+  FewParams p;
+  if (pages_of(table, c.B, Hkv, num_pages, page_size, max_pages, block, &p.pg) != FA3_OK) return cudaErrorInvalidValue;
+  p.q = c.q; p.k = c.k; p.v = c.v; p.ks = c.ks; p.vs = c.vs; p.q_start = c.q_start; p.kv_lens = c.kv_lens;
+  p.out = reinterpret_cast<__nv_bfloat16*>(c.out); p.lse = c.lse; p.err = c.err; p.q_stride = c.q_stride;
+  p.n = c.n; p.B = c.B; p.Hq = c.Hq; p.G = c.G; p.sm_log2 = c.sm_log2;
+  p.div_G = make_divu32((uint32_t)c.G);
+  const int nt = n_tiles(c.n, c.B, c.G);
+  p.ctas = ctas_of(nt, c.sms);
+  return nt == 1 ? launch<1>(p, workspace, s) : launch<2>(p, workspace, s);
+}
+
+}  // namespace fa3

@@ -2,6 +2,7 @@
 // where a block of tokens and its scales lie.
 #pragma once
 
+#include <math_constants.h>
 #include <stdint.h>
 
 #include "fa3_common.cuh"
@@ -76,6 +77,11 @@ __device__ __forceinline__ uint32_t rescaled(uint32_t codes4, float ratio) {
   }
   return out;
 }
+
+constexpr float kLeastScale = 8.271806125530277e-25f;      // 2^-80: attention takes a smaller value scale as this
+
+// Natural logarithm of a row's sum of exponentials: the sum of 2^(.. - m) is l.
+__device__ __forceinline__ float log_sum(float m, float l) { return l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F; }
 
 }  // namespace
 }  // namespace fa3

@@ -103,23 +103,23 @@ def _score_error(c, sm=SM):
     return d
 
 
-def _check_attention(c, out, lse, sm=SM, keep=3.0):
+def _check_attention(c, out, lse, sm=SM, keep=3.0, rows=None):
     ref, rl = O.attention_block(np.nan_to_num(c["q"]), c["k"], c["v"], c["ks"], c["vs"], c["table"], c["q_start"], c["kv_lens"],
                                 sm, np.full(c["q"].shape, keep), np.full(c["q"].shape[:2], keep))
     mean, _ = O.attention_block(np.nan_to_num(c["q"]), c["k"], np.abs(c["v"]), c["ks"], c["vs"], c["table"], c["q_start"],
                                 c["kv_lens"], sm, np.full(c["q"].shape, keep), np.full(c["q"].shape[:2], keep))
-    d, used = _score_error(c, sm), c["used"]
+    d, used = _score_error(c, sm), c["used"] if rows is None else rows
     T = int(c["kv_lens"].max())
     most = 127 * float(np.nanmax(c["vs"]))
     tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 2 * d[..., None] + 2 * (np.abs(rl) * 2 * U)[..., None]) * mean + T * 2.0 ** -32 * most
     bad = np.abs(out - ref) > tol
     assert np.all(np.isfinite(out[used])) and not bad[used].any(), (np.argwhere(bad & used[:, None, None])[:4],
                                                                     np.abs(out - ref)[bad][:4], tol[bad][:4])
-    assert np.all(out[~used] == keep)
+    assert np.all(out[~used] == keep) or rows is not None
     if lse is not None:
         tl = d + (T / 16 + 64) * U + np.abs(rl) * 8 * U
         assert not (np.abs(lse - rl) > tl)[used].any(), (np.abs(lse - rl) / tl)[used].max()
-        assert np.all(lse[~used] == keep)
+        assert np.all(lse[~used] == keep) or rows is not None
     return ref, rl
 
 
@@ -306,7 +306,7 @@ def test_attention_values_all_zero():
 def test_attention_bad_lengths_pages_and_starts():
     F, rng = fa3(), np.random.default_rng(14)
     c = _rows(rng, _cache(rng, [100, 130, 64], 32, 16, 2), [1, 2, 20], 4, behind=0)
-    whole, wl = _attend(F, c)
+    _check_attention(c, *_attend(F, c))
     for lens, start in (([100, 1, 64], None), ([100, 1000, 64], None), (None, [0, 4, 3, 23]), (None, [0, 1, 3, 24]),
                         (None, [-1, 1, 3, 23])):
         d = dict(c)
@@ -324,7 +324,8 @@ def test_attention_bad_lengths_pages_and_starts():
             rows[1:] = True
         elif start[-1] > 23:
             rows[:3] = True
-        assert np.array_equal(out[rows], whole[rows]) and np.array_equal(lse[rows], wl[rows])
+        # within the bounds, not the same bits: the work may be cut at other keys
+        _check_attention(c, out, lse, rows=rows)
         assert np.all(out[~rows] == 3.0) and np.all(lse[~rows] == 3.0)
     for bad in (-1, 10 ** 6):
         d = dict(c, table=c["table"].copy())
@@ -332,7 +333,9 @@ def test_attention_bad_lengths_pages_and_starts():
         err = torch.zeros(1, dtype=torch.int32, device="cuda")
         out, lse = _attend(F, d, err)
         assert err.item() == F.FA3_DEVERR_PAGE
-        assert np.array_equal(out[[0, *range(3, 23)]], whole[[0, *range(3, 23)]])
+        rows = np.ones(23, bool)
+        rows[1:3] = False
+        _check_attention(c, out, lse, rows=rows)
 
 
 # --------------------------------------------------------------------- weights
