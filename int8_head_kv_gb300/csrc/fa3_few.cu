@@ -29,17 +29,24 @@ namespace {
 constexpr int kD = 128;
 constexpr int kStep = 16;          // tokens of a warp's step
 constexpr int kWarps = 4, kThreadsF = 32 * kWarps;
-constexpr int kStages = 2;
+#ifndef CT2
+#define CT2 3
+#endif
+#ifndef KST
+#define KST 2
+#endif
+constexpr int kStages = KST;
 constexpr int kStageBytes = 2 * kStep * kD;                // K, then V rows
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 
 // What a unit costs beside its steps, and the least part of the line a CTA takes (enough for a part inside a unit to hold a
 // step), in steps of a CTA's warp.
+constexpr float kNone = -1e30f;                            // the reference of a column that has seen no key
 constexpr int kUnitSteps = 12, kLeastSteps = 16;
 static_assert(kLeastSteps > kUnitSteps, "a part inside a unit, behind its fixed cost, holds a step");
 
 struct CutF {
-  int b, tile, g, first, last;     // unit, CTAs that have parts of it; first < 0: none begins here
+  int row0, cols, g, first, last;  // the unit's first row, columns and KV head, CTAs that have parts of it; first < 0: none begins here
 };
 
 struct FewParams {
@@ -134,60 +141,86 @@ __device__ __forceinline__ int tiles_of(const FewParams& p, const SeqF& s) {
   return s.nq > 0 ? (int)divu32((uint32_t)(s.nq + p.RT - 1), p.div_RT) : 0;
 }
 __device__ __forceinline__ int cost_of(const SeqF& s) { return kUnitSteps + (int)(((uint32_t)s.nkv + kStep - 1) / kStep); }
-__device__ __forceinline__ int64_t sequence_cost(const FewParams& p, const SeqF& s) {
-  return s.nq > 0 ? (int64_t)tiles_of(p, s) * p.pg.Hkv * cost_of(s) : 0;
+__device__ __forceinline__ uint32_t sequence_cost(const FewParams& p, const SeqF& s) {
+  return s.nq > 0 ? (uint32_t)(tiles_of(p, s) * p.pg.Hkv * cost_of(s)) : 0u;
 }
 
-struct Where {
-  int64_t total;                   // of the line
-  int64_t off;                     // of the CTA's begin in sequence b
-  int b;
-};
-
-// The line's length, and the sequence that holds its position of CTA `cta` (the block together).
-__device__ __forceinline__ Where find_begin(const FewParams& p, int cta, int64_t* warp_sum, Where* found) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (p.B + kThreadsF - 1) / kThreadsF, b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-  int64_t sum = 0;
-  bool falls = false;
-  for (int b = b0; b < b1; ++b) {
-    const SeqF s = sequence_of(p, b, cta == 0);
-    falls |= s.nq < 0;
-    sum += sequence_cost(p, s);
+// The line's parts: CTA c takes [begin(c), begin(c + 1)).  Its numbers fit 31 bits (few_rows), and it is planned by every warp
+// for itself, in registers: with 64-bit numbers, shared memory and barriers, the way to the first key took some 2 us more.
+struct LineF {
+  uint32_t total, each, rest;
+  int parts;
+  __device__ __forceinline__ uint32_t begin(int c) const {
+    return c >= parts ? total : each * (uint32_t)c + rest * (uint32_t)c / (uint32_t)parts;
   }
-  int64_t upto = sum;
+  __device__ __forceinline__ int owner(uint32_t x) const {
+    int c = min((int)(x / each), parts - 1);
+    while (c > 0 && begin(c) > x) --c;
+    while (c + 1 < parts && begin(c + 1) <= x) ++c;
+    return c;
+  }
+};
+struct Begin {
+  SeqF s;
+  int b;
+  uint32_t off;                    // of the CTA's begin in sequence b
+};
+// The line, and the sequence that holds the begin of CTA `cta`'s part (the warp together; none if the part is empty).
+__device__ __forceinline__ LineF find_begin(const FewParams& p, int cta, int lane, Begin* at) {
+  // a lane has `per` sequences that follow one another
+  const int per = (p.B + 31) >> 5, b0 = lane * per;
+  SeqF s = {0, 0, 0};
+  uint32_t mine = 0;
+  bool falls = false;
+#pragma unroll 4
+  for (int i = 0; i < per; ++i) {
+    if (b0 + i < p.B) {
+      s = sequence_of(p, b0 + i, cta == 0 && threadIdx.x < 32);
+      falls |= s.nq < 0;
+      mine += sequence_cost(p, s);
+    }
+  }
+  uint32_t upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+    const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += y;
   }
-  if (lane == 31) warp_sum[warp] = upto;
-  falls = __syncthreads_or(falls);
-  int64_t total = 0;
+  LineF l;
+  l.total = __any_sync(0xffffffffu, falls) ? 0u : __shfl_sync(0xffffffffu, upto, 31);
+  l.parts = (int)max(1u, min(l.total / kLeastSteps, (uint32_t)p.ctas));
+  l.each = l.total / (uint32_t)l.parts;
+  l.rest = l.total - l.each * (uint32_t)l.parts;
+  const uint32_t x = l.begin(cta);
+  if (x >= l.total) return l;
+  int k = __ffs(__ballot_sync(0xffffffffu, upto > x)) - 1;
+  at->off = x - __shfl_sync(0xffffffffu, upto - mine, k);
+  at->b = k * per;
+#pragma unroll 1
+  for (int base = 0; per > 1; base += 32) {                  // which of that lane's
+    s = base + lane < per && at->b + base + lane < p.B ? sequence_of(p, at->b + base + lane, false) : SeqF{0, 0, 0};
+    const uint32_t c = sequence_cost(p, s);
+    uint32_t u = c;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) upto += warp_sum[w];
-    total += warp_sum[w];
-  }
-  if (falls) total = 0;
-  const int64_t most = total / kLeastSteps, parts = most < 1 ? 1 : min(most, (int64_t)p.ctas);
-  const int64_t x = cta >= parts ? total : total * cta / parts;
-  if (x < total && upto > x && upto - sum <= x) {
-    int64_t off = x - (upto - sum);
-    int b = b0;
-    for (; b < b1; ++b) {
-      const int64_t c = sequence_cost(p, sequence_of(p, b, false));
-      if (off < c) break;
-      off -= c;
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, u, o);
+      if (lane >= o) u += y;
     }
-    *found = Where{total, off, b};
+    const unsigned beyond = __ballot_sync(0xffffffffu, u > at->off);
+    if (beyond) {
+      k = __ffs(beyond) - 1;
+      at->off -= __shfl_sync(0xffffffffu, u - c, k);
+      at->b += base + k;
+      break;
+    }
+    at->off -= __shfl_sync(0xffffffffu, u, 31);
   }
-  __syncthreads();
-  return x < total ? *found : Where{total, 0, p.B};
+  at->s = SeqF{__shfl_sync(0xffffffffu, s.q0, k), __shfl_sync(0xffffffffu, s.nq, k), __shfl_sync(0xffffffffu, s.nkv, k)};
+  return l;
 }
 
 template <int NT>
-__global__ void __launch_bounds__(kThreadsF, NT == 1 ? 4 : 3) few_rows_kernel(const __grid_constant__ FewParams p) {
+__global__ void __launch_bounds__(kThreadsF, NT == 1 ? 4 : CT2) few_rows_kernel(const __grid_constant__ FewParams p) {
   // A 128-byte row stores its 16-byte chunk c at position c ^ f(row & 7), f(r) = (r & 6) ^ 4 (r & 1): every 8-lane
   // phase of the K and V fragment loads below then touches 8 distinct 16-byte bank groups.
   extern __shared__ __align__(128) uint8_t fsm[];
@@ -195,33 +228,29 @@ __global__ void __launch_bounds__(kThreadsF, NT == 1 ? 4 : 3) few_rows_kernel(co
   float (*sm_o)[kCols][kD] = reinterpret_cast<float (*)[kCols][kD]>(fsm);   // at a unit's end, in the rings' place
   static_assert(kWarps * kCols * kD * 4 <= kRingBytes, "partial O fits in the rings");
   __shared__ float sm_m[kWarps][kCols], sm_l[kWarps][kCols];
-  __shared__ int64_t warp_sum[kWarps];
-  __shared__ Where found;
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
   const int r = lane >> 2, qd = lane & 3;
-  Where w = find_begin(p, cta, warp_sum, &found);
-  const int64_t parts = max((int64_t)1, min(w.total / kLeastSteps, (int64_t)p.ctas));
-  auto begin = [&](int64_t c) { return c >= parts ? w.total : w.total * c / parts; };
-  int64_t x = begin(cta), left = begin(cta + 1) - x;
+  Begin w = {{0, 0, 0}, p.B, 0u};
+  const LineF line = find_begin(p, cta, lane, &w);
+  uint32_t x = line.begin(cta), left = line.begin(cta + 1) - x;
   CutF cut = {0, 0, 0, -1, -1};
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(fsm) + (uint32_t)(warp * kStages * kStageBytes);
   auto swz = [](int row) { return (row & 6) ^ ((row & 1) << 2); };
   auto chunk_addr = [&](uint32_t base, int row, int col) { return base + row * 128 + ((col ^ swz(row)) << 4); };
   const int64_t tok_stride = (int64_t)p.pg.Hkv * kD;
 
-  SeqF s = {0, 0, 0};
+  SeqF s = w.s;
   int tile = 0, g = 0, off = 0;
   if (left > 0) {
-    s = sequence_of(p, w.b, false);
-    const int64_t u = w.off / cost_of(s);
-    off = (int)(w.off - u * cost_of(s));
-    tile = (int)(u / p.pg.Hkv);
-    g = (int)(u - (int64_t)tile * p.pg.Hkv);
+    const uint32_t u = w.off / (uint32_t)cost_of(s);
+    off = (int)(w.off - u * (uint32_t)cost_of(s));
+    tile = (int)(u / (uint32_t)p.pg.Hkv);
+    g = (int)u - tile * p.pg.Hkv;
   }
   while (left > 0) {
-    const int cost = cost_of(s), take = (int)min((int64_t)(cost - off), left);
+    const int cost = cost_of(s), take = (int)min((uint32_t)(cost - off), left);
     // the unit's rows, columns, keys and steps
     const int i0 = tile * p.RT, cols = min(p.RT, s.nq - i0) * p.G;
     const int c0 = s.nkv - s.nq, keys = c0 + min(s.nq, i0 + p.RT), steps = (keys + kStep - 1) / kStep;
@@ -229,62 +258,62 @@ __global__ void __launch_bounds__(kThreadsF, NT == 1 ? 4 : 3) few_rows_kernel(co
     const int s0 = step_at(off), s1 = off + take == cost ? steps : step_at(off + take);
     if (s0 < s1) {
       const bool whole = s0 == 0 && s1 == steps;
-      // A part that begins the unit records the cut; the costs count some steps that only the last tile has, so the last CTA
-      // with any is the one that holds the last step.
-      if (s0 == 0 && !whole) {
-        const int64_t end = x + (kUnitSteps + steps - off) - 1;
-        int64_t c = ((end + 1) * parts - 1) / w.total;
-        while (c > 0 && begin(c) > end) --c;
-        while (c + 1 < parts && begin(c + 1) <= end) ++c;
-        cut = CutF{w.b, tile, g, cta, (int)c};
+      // Q^T fragments: thread (r, qd) holds column 8 nt + r's values [16 qd, +16) and [64 + 16 qd, +16) as fp16, times a
+      // power of two that brings the column's largest to [2^14, 2^15).  The values are asked for before all else.
+      uint4 qv[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int col = 8 * nt + r, ri = (int)divu32((uint32_t)col, p.div_G);
+        const uint16_t* row = p.q + (int64_t)(s.q0 + i0 + ri) * p.q_stride + (int64_t)(g * p.G + col - ri * p.G) * kD;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          qv[nt][i] = col < cols ? __ldg(reinterpret_cast<const uint4*>(row + (i >> 1) * 64 + 16 * qd + 8 * (i & 1)))
+                                 : make_uint4(0u, 0u, 0u, 0u);
       }
-      const int32_t* table = p.pg.table + (int64_t)w.b * p.pg.max_pages;
-      const int8_t* kbase = p.k + (int64_t)g * kD;
-      const int8_t* vbase = p.v + (int64_t)g * kD;
       const int n_my = s1 - s0 > warp ? (s1 - s0 - warp + kWarps - 1) / kWarps : 0;   // steps s0 + warp, + 4, ...
-      // A step's page is looked up two steps ahead and its scales one step ahead of their use.
-      auto entry_of = [&](int m) {
-        return __ldg(table + divu32((uint32_t)((s0 + warp + kWarps * m) * kStep), p.pg.div_ps));
-      };
-      int pg_next = n_my > 0 ? entry_of(0) : 0;
-      float ks_next = 0.f, vs_next = 0.f;
-      auto issue = [&](int m, int stage) {
-        const int t0 = (s0 + warp + kWarps * m) * kStep;
-        int page = pg_next;
-        if (m + 1 < n_my) pg_next = entry_of(m + 1);
-        if ((uint32_t)page >= (uint32_t)p.pg.num_pages) {          // outside the pool: any page of it
-          if (lane == 0) set_dev_err(p.err, FA3_DEVERR_PAGE);
+      // A lane looks one of the next 32 steps up: its first row in the pool, and its scales.
+      int row_of = 0;
+      float ks_of = 0.f, lv_of = 0.f, rv_of = 0.f, ks_next = 0.f, vs_next = 0.f;
+      auto look_up = [&](int m) {
+        const uint32_t t = (uint32_t)((s0 + warp + kWarps * min(m + lane, n_my - 1)) * kStep), pi = divu32(t, p.pg.div_ps);
+        int page = __ldg(p.pg.table + (int64_t)w.b * p.pg.max_pages + pi);
+        if ((uint32_t)page >= (uint32_t)p.pg.num_pages) {           // outside the pool: any page of it
+          set_dev_err(p.err, FA3_DEVERR_PAGE);
           page = 0;
         }
-        const int at = t0 - (int)divu32((uint32_t)t0, p.pg.div_ps) * p.pg.page_size;
-        const int64_t row0 = (int64_t)page * p.pg.page_size + at;
+        const int at = (int)(t - pi * (uint32_t)p.pg.page_size);
+        row_of = page * p.pg.page_size + at;
         const int64_t sc = ((int64_t)page * p.pg.per_page + (int)divu32((uint32_t)at, p.pg.div_block)) * p.pg.Hkv + g;
         ks_next = __ldg(p.ks + sc);
         vs_next = __ldg(p.vs + sc);
+      };
+      // A step's 16 rows of K and of V: a lane has 16 bytes of rows l / 8, l / 8 + 4, ..  Rows behind the context are read as
+      // they are (they lie in the same page) and masked.
+      const int64_t lane_off = (int64_t)(lane >> 3) * tok_stride + g * kD + (lane & 7) * 16;
+      const uint32_t lane_dst = ring + (uint32_t)(lane >> 3) * 128;
+      const uint32_t dst_even = ((lane & 7) ^ swz(lane >> 3)) << 4, dst_odd = ((lane & 7) ^ swz((lane >> 3) + 4)) << 4;
+      auto issue = [&](int m, int stage) {
+        const int64_t at = (int64_t)__shfl_sync(0xffffffffu, row_of, m & 31) * tok_stride + lane_off;
+        const int8_t *ka = p.k + at, *va = p.v + at;
+        const uint32_t dst = lane_dst + stage * kStageBytes;
 #pragma unroll
-        for (int i8 = 0; i8 < 8; ++i8) {
-          const int i = lane + 32 * i8, kv = i >> 7, row = (i >> 3) & 15, col = i & 7;
-          // rows behind the context are read as they are (they lie in the same page) and masked
-          cp_async16(ring + stage * kStageBytes + kv * 2048 + row * 128 + ((col ^ swz(row)) << 4),
-                     (kv ? vbase : kbase) + (row0 + row) * tok_stride + col * 16);
+        for (int i = 0; i < 4; ++i) {
+          cp_async16(dst + 512 * i + (i & 1 ? dst_odd : dst_even), ka + 4 * i * tok_stride);
+          cp_async16(dst + 2048 + 512 * i + (i & 1 ? dst_odd : dst_even), va + 4 * i * tok_stride);
         }
       };
-      if (n_my > 0) issue(0, 0);
-      cp_async_commit();
-      // Q^T fragments: thread (r, qd) holds column 8 nt + r's values [16 qd, +16) and [64 + 16 qd, +16) as fp16, times a
-      // power of two that brings the column's largest to [2^14, 2^15).
+      if (n_my > 0) look_up(0);
+#pragma unroll
+      for (int m = 0; m < kStages - 1; ++m) {
+        if (m < n_my) issue(m, m);
+        cp_async_commit();
+      }
       uint32_t qh[NT][8][2];
       float f0[NT], f1[NT];
       int lim0[NT], lim1[NT];                                   // last key of columns 8 nt + 2 qd, + 1; -1: no column
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const int col = 8 * nt + r, ri = (int)divu32((uint32_t)col, p.div_G);
-        uint4 v[4];
-        const uint16_t* row = p.q + (int64_t)(s.q0 + i0 + ri) * p.q_stride + (int64_t)(g * p.G + col - ri * p.G) * kD;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          v[i] = col < cols ? __ldg(reinterpret_cast<const uint4*>(row + (i >> 1) * 64 + 16 * qd + 8 * (i & 1)))
-                            : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 (&v)[4] = qv[nt];
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -308,65 +337,86 @@ __global__ void __launch_bounds__(kThreadsF, NT == 1 ? 4 : 3) few_rows_kernel(co
         lim0[nt] = ca < cols ? c0 + i0 + (int)divu32((uint32_t)ca, p.div_G) : -1;
         lim1[nt] = ca + 1 < cols ? c0 + i0 + (int)divu32((uint32_t)(ca + 1), p.div_G) : -1;
       }
+      // kNone in place of -infinity: differences of references stay numbers
       float m0[NT], m1[NT], l0[NT], l1[NT], o[NT][8][4];
+      int lim = 0x7fffffff;                                     // the last key that all columns see
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        m0[nt] = m1[nt] = -CUDART_INF_F;
+        m0[nt] = m1[nt] = kNone;
         l0[nt] = l1[nt] = 0.f;
+        lim = min(lim, min(lim0[nt], lim1[nt]));
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
       }
       for (int m = 0; m < n_my; ++m) {
         const int t0 = (s0 + warp + kWarps * m) * kStep;
-        const float ks = ks_next, vs = fmaxf(vs_next, kLeastScale);
-        if (m + 1 < n_my) issue(m + 1, (m + 1) % kStages);
+        if ((m & 31) == 0) {
+          const float vs = fmaxf(vs_next, kLeastScale);
+          ks_of = ks_next;
+          lv_of = __log2f(vs);
+          rv_of = __fdividef(1.f, vs);
+        }
+        const float ks = __shfl_sync(0xffffffffu, ks_of, m & 31), lv = __shfl_sync(0xffffffffu, lv_of, m & 31),
+                    rv = __shfl_sync(0xffffffffu, rv_of, m & 31);
+        if (m + kStages - 1 < n_my) {
+          if (((m + kStages - 1) & 31) == 0) look_up(m + kStages - 1);
+          issue(m + kStages - 1, (m + kStages - 1) % kStages);
+        }
         cp_async_commit();
-        cp_async_wait<1>();
+        cp_async_wait<kStages - 1>();
         __syncwarp();
         const uint32_t kst = ring + (m % kStages) * kStageBytes, vst = kst + 2048;
-        uint4 kr[4], vr[4];
-        kr[0] = lds128(chunk_addr(kst, r, qd));
-        kr[1] = lds128(chunk_addr(kst, r, 4 + qd));
-        kr[2] = lds128(chunk_addr(kst, r + 8, qd));
-        kr[3] = lds128(chunk_addr(kst, r + 8, 4 + qd));
-        vr[0] = lds128(chunk_addr(vst, 2 * qd, r));
-        vr[1] = lds128(chunk_addr(vst, 2 * qd + 1, r));
-        vr[2] = lds128(chunk_addr(vst, 2 * qd + 8, r));
-        vr[3] = lds128(chunk_addr(vst, 2 * qd + 9, r));
-        __syncwarp();                                           // every lane has its fragments: the stage may be refilled
         float cf[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) cf[nt][0] = cf[nt][1] = cf[nt][2] = cf[nt][3] = 0.f;
+        {
+          const uint4 k0 = lds128(chunk_addr(kst, r, qd)), k1 = lds128(chunk_addr(kst, r, 4 + qd)),
+                      k2 = lds128(chunk_addr(kst, r + 8, qd)), k3 = lds128(chunk_addr(kst, r + 8, 4 + qd));
 #pragma unroll
-        for (int st = 0; st < 8; ++st) {
-          uint32_t a0, a1, a2, a3;
-          codes_to_f16(word(kr[st >> 2], st & 3), a0, a2);       // row r: the thread's values 4 st .. 4 st + 3
-          codes_to_f16(word(kr[2 + (st >> 2)], st & 3), a1, a3);  // row r + 8
+          for (int st = 0; st < 8; ++st) {
+            uint32_t a0, a1, a2, a3;
+            codes_to_f16(word(st < 4 ? k0 : k1, st & 3), a0, a2);  // row r: the thread's values 4 st .. 4 st + 3
+            codes_to_f16(word(st < 4 ? k2 : k3, st & 3), a1, a3);  // row r + 8
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816(cf[nt], a0, a1, a2, a3, qh[nt][st][0], qh[nt][st][1]);
+            for (int nt = 0; nt < NT; ++nt) mma16816(cf[nt], a0, a1, a2, a3, qh[nt][st][0], qh[nt][st][1]);
+          }
         }
-        const float lv = __log2f(vs), rv = __fdividef(1.f, vs);
+        const uint4 v0 = lds128(chunk_addr(vst, 2 * qd, r)), v1 = lds128(chunk_addr(vst, 2 * qd + 1, r)),
+                    v2 = lds128(chunk_addr(vst, 2 * qd + 8, r)), v3 = lds128(chunk_addr(vst, 2 * qd + 9, r));
+        __syncwarp();                                           // every lane has its fragments: the stage may be refilled
+        const bool masked = __any_sync(0xffffffffu, t0 + kStep - 1 > lim);
         uint32_t b0[NT], b1[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const float e0 = f0[nt] * ks, e1 = f1[nt] * ks;
-          const int ta = t0 + r, tb = ta + 8;
-          const float x0 = ta <= lim0[nt] ? fmaf(cf[nt][0], e0, lv) : -CUDART_INF_F;
-          const float x1 = ta <= lim1[nt] ? fmaf(cf[nt][1], e1, lv) : -CUDART_INF_F;
-          const float x2 = tb <= lim0[nt] ? fmaf(cf[nt][2], e0, lv) : -CUDART_INF_F;
-          const float x3 = tb <= lim1[nt] ? fmaf(cf[nt][3], e1, lv) : -CUDART_INF_F;
-          float mx0 = fmaxf(x0, x2), mx1 = fmaxf(x1, x3);
+          float y[4];
+          auto exponents = [&]() {                              // of tokens r, r + 8 and columns 2 qd, 2 qd + 1
+            const float a0 = lv - m0[nt], a1 = lv - m1[nt];
+            y[0] = fmaf(cf[nt][0], e0, a0);
+            y[1] = fmaf(cf[nt][1], e1, a1);
+            y[2] = fmaf(cf[nt][2], e0, a0);
+            y[3] = fmaf(cf[nt][3], e1, a1);
+            if (masked) {
+              const int ta = t0 + r, tb = ta + 8;
+              y[0] = ta <= lim0[nt] ? y[0] : -CUDART_INF_F;
+              y[1] = ta <= lim1[nt] ? y[1] : -CUDART_INF_F;
+              y[2] = tb <= lim0[nt] ? y[2] : -CUDART_INF_F;
+              y[3] = tb <= lim1[nt] ? y[3] : -CUDART_INF_F;
+            }
+          };
+          exponents();
+          // The reference lies 7 below the column's largest when it is set, and moves when one is 15 or more above it:
+          // P stays below 2^15 (a little above, by the rounding of y), which is below fp16's end.
+          if (__any_sync(0xffffffffu, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) > 15.f)) {
+            auto x_of = [&](int e) { return y[e] == -CUDART_INF_F ? y[e] : fmaf(cf[nt][e], e & 1 ? e1 : e0, lv); };
+            float x0 = fmaxf(x_of(0), x_of(2)), x1 = fmaxf(x_of(1), x_of(3));
 #pragma unroll
-          for (int o_ = 4; o_ < 32; o_ <<= 1) {
-            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o_));
-            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o_));
-          }
-          // The reference lies 7 below the largest when it is set and moves only when that has grown by more than 8.
-          const bool g0 = mx0 - 7.f > m0[nt] + 8.f, g1 = mx1 - 7.f > m1[nt] + 8.f;
-          if (__any_sync(0xffffffffu, g0 || g1)) {
-            const float n0 = g0 ? mx0 - 7.f : m0[nt], n1 = g1 ? mx1 - 7.f : m1[nt];
-            const float al0 = g0 ? (m0[nt] == -CUDART_INF_F ? 0.f : ex2_approx(m0[nt] - n0)) : 1.f;
-            const float al1 = g1 ? (m1[nt] == -CUDART_INF_F ? 0.f : ex2_approx(m1[nt] - n1)) : 1.f;
+            for (int k = 4; k < 32; k <<= 1) {
+              x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, k));
+              x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, k));
+            }
+            const float n0 = x0 - 7.f > m0[nt] + 8.f ? x0 - 7.f : m0[nt], n1 = x1 - 7.f > m1[nt] + 8.f ? x1 - 7.f : m1[nt];
+            const float al0 = ex2_approx(m0[nt] - n0), al1 = ex2_approx(m1[nt] - n1);
             l0[nt] *= al0;
             l1[nt] *= al1;
 #pragma unroll
@@ -375,10 +425,9 @@ __global__ void __launch_bounds__(kThreadsF, NT == 1 ? 4 : 3) few_rows_kernel(co
             }
             m0[nt] = n0;
             m1[nt] = n1;
+            exponents();
           }
-          const float ref0 = m0[nt] == -CUDART_INF_F ? 0.f : m0[nt], ref1 = m1[nt] == -CUDART_INF_F ? 0.f : m1[nt];
-          const float p0 = ex2_approx(x0 - ref0), p1 = ex2_approx(x1 - ref1), p2 = ex2_approx(x2 - ref0),
-                      p3 = ex2_approx(x3 - ref1);
+          const float p0 = ex2_approx(y[0]), p1 = ex2_approx(y[1]), p2 = ex2_approx(y[2]), p3 = ex2_approx(y[3]);
           l0[nt] = fmaf(p0 + p2, rv, l0[nt]);
           l1[nt] = fmaf(p1 + p3, rv, l1[nt]);
           b0[nt] = movmatrix_trans(pack_f16x2(p0, p1));
@@ -389,8 +438,8 @@ __global__ void __launch_bounds__(kThreadsF, NT == 1 ? 4 : 3) few_rows_kernel(co
         for (int i = 0; i < 8; ++i) {
           const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
           uint32_t a0, a1, a2, a3;
-          codes_to_f16(__byte_perm(word(vr[0], i >> 1), word(vr[1], i >> 1), sel), a0, a1);
-          codes_to_f16(__byte_perm(word(vr[2], i >> 1), word(vr[3], i >> 1), sel), a2, a3);
+          codes_to_f16(__byte_perm(word(v0, i >> 1), word(v1, i >> 1), sel), a0, a1);
+          codes_to_f16(__byte_perm(word(v2, i >> 1), word(v3, i >> 1), sel), a2, a3);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][i], a0, a1, a2, a3, b0[nt], b1[nt]);
         }
@@ -419,13 +468,13 @@ __global__ void __launch_bounds__(kThreadsF, NT == 1 ? 4 : 3) few_rows_kernel(co
       __syncthreads();
       // a warp has every fourth column, a lane four values
       for (int col = warp; col < cols; col += kWarps) {
-        float M = -CUDART_INF_F;
+        float M = kNone;
 #pragma unroll
         for (int k = 0; k < kWarps; ++k) M = fmaxf(M, sm_m[k][col]);
         float L = 0.f, a[4] = {};
 #pragma unroll
         for (int k = 0; k < kWarps; ++k) {
-          const float fk = M == -CUDART_INF_F ? 0.f : ex2_approx(sm_m[k][col] - M);
+          const float fk = ex2_approx(sm_m[k][col] - M);
           const float4 ok = *reinterpret_cast<const float4*>(&sm_o[k][col][4 * lane]);
           L = fmaf(sm_l[k][col], fk, L);
           a[0] = fmaf(ok.x, fk, a[0]); a[1] = fmaf(ok.y, fk, a[1]); a[2] = fmaf(ok.z, fk, a[2]); a[3] = fmaf(ok.w, fk, a[3]);
@@ -441,6 +490,9 @@ __global__ void __launch_bounds__(kThreadsF, NT == 1 ? 4 : 3) few_rows_kernel(co
           if (lane == 0) p.part_ml[slot] = make_float2(M, L);
         }
       }
+      // The part that begins a unit records its cut; the costs count some steps that only the last tile has, so the last CTA
+      // with any is the one that holds the last step.
+      if (s0 == 0 && !whole) cut = CutF{s.q0 + i0, cols, g, cta, line.owner(x + (uint32_t)(kUnitSteps + steps - off) - 1u)};
       __syncthreads();                                          // the rings are the next unit's
     }
     left -= take;
@@ -463,40 +515,64 @@ __global__ void __launch_bounds__(kThreadsF, NT == 1 ? 4 : 3) few_rows_kernel(co
 template <int NT>
 __global__ void __launch_bounds__(kThreadsF) few_combine_kernel(const __grid_constant__ FewParams p) {
   constexpr int kCols = 8 * NT;
+  // No early start of what follows: its blocks would be placed around these, and the next attention call's, which fill the GPU
+  // exactly, unevenly (16 one-token rows of 4096 keys 36.2 us a call instead of 32.0, of 16384 keys 107 instead of 89).
   pdl_wait();
-  pdl_launch_dependents();
   const CutF u = p.cuts[blockIdx.x];
   if (u.first < 0) return;
   const int lane = threadIdx.x & 31, col = blockIdx.y * kWarps + (threadIdx.x >> 5);
-  const int q0 = p.q_start[u.b], nq = p.q_start[u.b + 1] - q0, i0 = u.tile * p.RT, cols = min(p.RT, nq - i0) * p.G;
-  if (col >= cols) return;
+  if (col >= u.cols) return;
   auto slot = [&](int c) { return (int64_t)(2 * c + (c == u.first ? 1 : 0)) * kCols + col; };
-  float M = -CUDART_INF_F;
-  for (int c = u.first; c <= u.last; ++c) M = fmaxf(M, p.part_ml[slot(c)].x);
-  float L = 0.f, a[4] = {};
-#pragma unroll 4
-  for (int c = u.first; c <= u.last; ++c) {
-    const float2 ml = p.part_ml[slot(c)];
-    const float4 o = *reinterpret_cast<const float4*>(p.part_o + slot(c) * kD + 4 * lane);
-    const float f = M == -CUDART_INF_F ? 0.f : ex2_approx(ml.x - M);
-    L = fmaf(ml.y, f, L);
-    a[0] = fmaf(o.x, f, a[0]); a[1] = fmaf(o.y, f, a[1]); a[2] = fmaf(o.z, f, a[2]); a[3] = fmaf(o.w, f, a[3]);
+  // four parts' loads at once; the reference moves from four to four
+  float M = kNone, L = 0.f, a[4] = {};
+#pragma unroll 1
+  for (int c = u.first; c <= u.last; c += 4) {
+    float2 ml[4];
+    float4 o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t at = slot(min(c + k, u.last));
+      ml[k] = p.part_ml[at];
+      o[k] = *reinterpret_cast<const float4*>(p.part_o + at * kD + 4 * lane);
+    }
+    float top = M;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = fmaxf(top, ml[k].x);
+    const float f = ex2_approx(M - top);
+    L *= f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a[e] *= f;
+    M = top;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float fk = c + k <= u.last ? ex2_approx(ml[k].x - M) : 0.f;
+      L = fmaf(ml[k].y, fk, L);
+      a[0] = fmaf(o[k].x, fk, a[0]); a[1] = fmaf(o[k].y, fk, a[1]); a[2] = fmaf(o[k].z, fk, a[2]); a[3] = fmaf(o[k].w, fk, a[3]);
+    }
   }
   const int ri = (int)divu32((uint32_t)col, p.div_G);
-  const int64_t orow = (int64_t)(q0 + i0 + ri) * p.Hq + u.g * p.G + col - ri * p.G;
+  const int64_t orow = (int64_t)(u.row0 + ri) * p.Hq + u.g * p.G + col - ri * p.G;
   put_row(p.out + orow * kD, lane, a, L);
   if (lane == 0 && p.lse) p.lse[orow] = log_sum(M, L);
 }
 
 // Column tiles of 8 where sequences have 8 columns or fewer on average, of 16 otherwise.
 int n_tiles(int n, int B, int G) { return (int64_t)std::max(1, n / B) * G <= 8 ? 1 : 2; }
-int ctas_of(int nt, int sms) { return sms * (nt == 1 ? 4 : 3); }
+int ctas_of(int nt, int sms) { return sms * (nt == 1 ? 4 : CT2); }
 size_t bytes_of(int nt, int ctas) {
   return (size_t)ctas * (2 * 8 * nt * (kD * sizeof(float) + sizeof(float2)) + sizeof(CutF));
 }
 
 template <int NT>
 cudaError_t launch(FewParams& p, void* workspace, cudaStream_t s) {
+  static std::atomic<bool> set[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return cudaErrorInvalidDevice;
+  if (dev >= 64 || !set[dev].load(std::memory_order_acquire)) {
+    const cudaError_t e = cudaFuncSetAttribute(few_rows_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) set[dev].store(true, std::memory_order_release);
+  }
   p.RT = 8 * NT / p.G;
   p.div_RT = make_divu32((uint32_t)p.RT);
   p.part_o = static_cast<float*>(workspace);
@@ -512,7 +588,7 @@ cudaError_t launch(FewParams& p, void* workspace, cudaStream_t s) {
 
 bool few_rows(int n, int B, int Hkv, int G, int T_max) {
   const double units = (double)n + B;
-  return G <= 16 && (int64_t)n * G <= (int64_t)48 * B && units * Hkv * (T_max / kStep + kUnitSteps + 1.0) * 1024.0 < 4503599627370496.0;
+  return G <= 16 && (int64_t)n * G <= (int64_t)48 * B && units * Hkv * (T_max / kStep + kUnitSteps + 1.0) < 2147483648.0;
 }
 size_t few_rows_workspace(int n, int B, int G, int sms) {
   if (G > 16) return 0;
