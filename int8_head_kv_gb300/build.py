@@ -38,7 +38,7 @@ def _stale() -> bool:
 
 def _compile(src: str, verbose: bool) -> str:
     obj = os.path.join(OBJDIR, os.path.basename(src)[:-3] + ".o")
-    cmd = [NVCC] + FLAGS + os.environ.get("XF", "").split() + ["-c", src, "-o", obj]
+    cmd = [NVCC] + FLAGS + ["-c", src, "-o", obj]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)

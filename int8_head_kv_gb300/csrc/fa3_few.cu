@@ -29,20 +29,14 @@ namespace {
 constexpr int kD = 128;
 constexpr int kStep = 16;          // tokens of a warp's step
 constexpr int kWarps = 4, kThreadsF = 32 * kWarps;
-#ifndef CT2
-#define CT2 3
-#endif
-#ifndef KST
-#define KST 2
-#endif
-constexpr int kStages = KST;
+constexpr int kStages = 2;
 constexpr int kStageBytes = 2 * kStep * kD;                // K, then V rows
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 
 // What a unit costs beside its steps, and the least part of the line a CTA takes (enough for a part inside a unit to hold a
 // step), in steps of a CTA's warp.
 constexpr float kNone = -1e30f;                            // the reference of a column that has seen no key
-constexpr int kUnitSteps = 12, kLeastSteps = 16;
+constexpr int kUnitSteps = 16, kLeastSteps = 20;
 static_assert(kLeastSteps > kUnitSteps, "a part inside a unit, behind its fixed cost, holds a step");
 
 struct CutF {
@@ -220,7 +214,7 @@ __device__ __forceinline__ LineF find_begin(const FewParams& p, int cta, int lan
 }
 
 template <int NT>
-__global__ void __launch_bounds__(kThreadsF, NT == 1 ? 4 : CT2) few_rows_kernel(const __grid_constant__ FewParams p) {
+__global__ void __launch_bounds__(kThreadsF, NT == 1 ? 4 : 3) few_rows_kernel(const __grid_constant__ FewParams p) {
   // A 128-byte row stores its 16-byte chunk c at position c ^ f(row & 7), f(r) = (r & 6) ^ 4 (r & 1): every 8-lane
   // phase of the K and V fragment loads below then touches 8 distinct 16-byte bank groups.
   extern __shared__ __align__(128) uint8_t fsm[];
@@ -511,45 +505,69 @@ __global__ void __launch_bounds__(kThreadsF, NT == 1 ? 4 : CT2) few_rows_kernel(
   if (tid == 0) p.cuts[cta] = cut;
 }
 
-// Merges the parts of the unit whose first cut lies behind CTA blockIdx.x's part: a warp a column.
-template <int NT>
-__global__ void __launch_bounds__(kThreadsF) few_combine_kernel(const __grid_constant__ FewParams p) {
+// Merges the parts of the unit whose first cut lies behind CTA blockIdx.x's part.  MW warps have a column, each every MW-th
+// part, eight at once.
+constexpr int kMergeCols = 4, kMergeLoads = 8;
+template <int NT, int MW>
+__global__ void __launch_bounds__(32 * MW * kMergeCols) few_combine_kernel(const __grid_constant__ FewParams p) {
   constexpr int kCols = 8 * NT;
+  __shared__ float4 sm_a[kMergeCols][MW][32];
+  __shared__ float2 sm_ml[kMergeCols][MW];
   // No early start of what follows: its blocks would be placed around these, and the next attention call's, which fill the GPU
   // exactly, unevenly (16 one-token rows of 4096 keys 36.2 us a call instead of 32.0, of 16384 keys 107 instead of 89).
   pdl_wait();
   const CutF u = p.cuts[blockIdx.x];
   if (u.first < 0) return;
-  const int lane = threadIdx.x & 31, col = blockIdx.y * kWarps + (threadIdx.x >> 5);
-  if (col >= u.cols) return;
-  auto slot = [&](int c) { return (int64_t)(2 * c + (c == u.first ? 1 : 0)) * kCols + col; };
-  // four parts' loads at once; the reference moves from four to four
+  const int lane = threadIdx.x & 31, part = (threadIdx.x >> 5) % MW, mine = threadIdx.x / (32 * MW);
+  const int col = blockIdx.y * kMergeCols + mine;
   float M = kNone, L = 0.f, a[4] = {};
+  if (col < u.cols) {
+    auto slot = [&](int c) { return (int64_t)(2 * c + (c == u.first ? 1 : 0)) * kCols + col; };
 #pragma unroll 1
-  for (int c = u.first; c <= u.last; c += 4) {
-    float2 ml[4];
-    float4 o[4];
+    for (int c = u.first + part; c <= u.last; c += kMergeLoads * MW) {
+      float2 ml[kMergeLoads];
+      float4 o[kMergeLoads];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int64_t at = slot(min(c + k, u.last));
-      ml[k] = p.part_ml[at];
-      o[k] = *reinterpret_cast<const float4*>(p.part_o + at * kD + 4 * lane);
-    }
-    float top = M;
+      for (int k = 0; k < kMergeLoads; ++k) {
+        const int64_t at = slot(min(c + k * MW, u.last));
+        ml[k] = p.part_ml[at];
+        o[k] = *reinterpret_cast<const float4*>(p.part_o + at * kD + 4 * lane);
+      }
+      float top = M;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) top = fmaxf(top, ml[k].x);
-    const float f = ex2_approx(M - top);
-    L *= f;
+      for (int k = 0; k < kMergeLoads; ++k) top = fmaxf(top, ml[k].x);
+      const float f = ex2_approx(M - top);
+      L *= f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) a[e] *= f;
-    M = top;
+      for (int e = 0; e < 4; ++e) a[e] *= f;
+      M = top;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float fk = c + k <= u.last ? ex2_approx(ml[k].x - M) : 0.f;
-      L = fmaf(ml[k].y, fk, L);
-      a[0] = fmaf(o[k].x, fk, a[0]); a[1] = fmaf(o[k].y, fk, a[1]); a[2] = fmaf(o[k].z, fk, a[2]); a[3] = fmaf(o[k].w, fk, a[3]);
+      for (int k = 0; k < kMergeLoads; ++k) {
+        const float fk = c + k * MW <= u.last ? ex2_approx(ml[k].x - M) : 0.f;
+        L = fmaf(ml[k].y, fk, L);
+        a[0] = fmaf(o[k].x, fk, a[0]); a[1] = fmaf(o[k].y, fk, a[1]); a[2] = fmaf(o[k].z, fk, a[2]); a[3] = fmaf(o[k].w, fk, a[3]);
+      }
     }
   }
+  if constexpr (MW > 1) {
+    sm_a[mine][part][lane] = make_float4(a[0], a[1], a[2], a[3]);
+    if (lane == 0) sm_ml[mine][part] = make_float2(M, L);
+    __syncthreads();
+    if (part) return;
+    M = kNone;
+#pragma unroll
+    for (int k = 0; k < MW; ++k) M = fmaxf(M, sm_ml[mine][k].x);
+    L = a[0] = a[1] = a[2] = a[3] = 0.f;
+#pragma unroll
+    for (int k = 0; k < MW; ++k) {
+      const float2 ml = sm_ml[mine][k];
+      const float4 o = sm_a[mine][k][lane];
+      const float f = ex2_approx(ml.x - M);
+      L = fmaf(ml.y, f, L);
+      a[0] = fmaf(o.x, f, a[0]); a[1] = fmaf(o.y, f, a[1]); a[2] = fmaf(o.z, f, a[2]); a[3] = fmaf(o.w, f, a[3]);
+    }
+  }
+  if (col >= u.cols) return;
   const int ri = (int)divu32((uint32_t)col, p.div_G);
   const int64_t orow = (int64_t)(u.row0 + ri) * p.Hq + u.g * p.G + col - ri * p.G;
   put_row(p.out + orow * kD, lane, a, L);
@@ -558,7 +576,7 @@ __global__ void __launch_bounds__(kThreadsF) few_combine_kernel(const __grid_con
 
 // Column tiles of 8 where sequences have 8 columns or fewer on average, of 16 otherwise.
 int n_tiles(int n, int B, int G) { return (int64_t)std::max(1, n / B) * G <= 8 ? 1 : 2; }
-int ctas_of(int nt, int sms) { return sms * (nt == 1 ? 4 : CT2); }
+int ctas_of(int nt, int sms) { return sms * (nt == 1 ? 4 : 3); }
 size_t bytes_of(int nt, int ctas) {
   return (size_t)ctas * (2 * 8 * nt * (kD * sizeof(float) + sizeof(float2)) + sizeof(CutF));
 }
@@ -581,7 +599,11 @@ cudaError_t launch(FewParams& p, void* workspace, cudaStream_t s) {
   const LaunchTogether together(s);
   cudaError_t e = launch_pdl(few_rows_kernel<NT>, dim3((unsigned)p.ctas), dim3(kThreadsF), kRingBytes, s, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(few_combine_kernel<NT>, dim3((unsigned)p.ctas, 2 * NT), dim3(kThreadsF), 0, s, p);
+  // Four warps a column where units may have many parts; one token of 32768 keys (76 parts a unit): 25.5 us with one warp,
+  // 22.5 with four; but 16 of 1024 keys: 14.4 and 17.0, for its more blocks.
+  const dim3 grid((unsigned)p.ctas, 8 * NT / kMergeCols);
+  if (p.ctas > 16 * (int64_t)p.B * p.pg.Hkv) return launch_pdl(few_combine_kernel<NT, 4>, grid, dim3(128 * kMergeCols), 0, s, p);
+  return launch_pdl(few_combine_kernel<NT, 1>, grid, dim3(32 * kMergeCols), 0, s, p);
 }
 
 }  // namespace
