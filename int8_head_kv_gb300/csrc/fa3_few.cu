@@ -118,7 +118,8 @@ struct SeqF {
   int q0, nq, nkv;
 };
 // nq = 0: nothing to do; -1: q_start falls.
-__device__ __forceinline__ SeqF sequence_of(const FewParams& p, int b, bool report) {
+template <class P>
+__device__ __forceinline__ SeqF sequence_of(const P& p, int b, bool report) {
   SeqF s;
   s.q0 = p.q_start[b];
   const int q1 = p.q_start[b + 1];
@@ -160,7 +161,8 @@ struct Begin {
   uint32_t off;                    // of the CTA's begin in sequence b
 };
 // The line, and the sequence that holds the begin of CTA `cta`'s part (the warp together; none if the part is empty).
-__device__ __forceinline__ LineF find_begin(const FewParams& p, int cta, int lane, Begin* at) {
+template <class P>
+__device__ __forceinline__ LineF find_begin(const P& p, int cta, int lane, Begin* at) {
   // a lane has `per` sequences that follow one another
   const int per = (p.B + 31) >> 5, b0 = lane * per;
   SeqF s = {0, 0, 0};
@@ -574,6 +576,217 @@ __global__ void __launch_bounds__(32 * MW * kMergeCols) few_combine_kernel(const
   if (lane == 0 && p.lse) p.lse[orow] = log_sum(M, L);
 }
 
+// ------------------------------------------------------------------ attention weights of few rows
+// fa3_weights.cu's sums where few columns meet each key: only keys are read, once for every 64 columns of a sequence, and the
+// scores are those above, with the sum over columns (2 a thread, then the four threads of a token) in place of the softmax.
+// Tokens have nothing to do with one another, so a part of the line is a run of tokens and there is nothing to merge.
+constexpr int kChunkCols = 64, kWStages = 3;
+constexpr uint32_t kWRing = kWarps * kWStages * kStep * kD;                    // int8 rows of K
+constexpr uint32_t OFF_WQ = kWRing;                                            // [tile][4][32] uint4: fragments of Q^T
+constexpr uint32_t OFF_WC = OFF_WQ + kChunkCols / 8 * 4 * 32 * 16;             // [tile][4] float4: two columns' factors and -lse
+constexpr uint32_t OFF_WL = OFF_WC + kChunkCols / 8 * 4 * 16;                  // [tile][4] int2: the last key that sees them
+constexpr uint32_t SMEM_FEW_WEIGHTS = OFF_WL + kChunkCols / 8 * 4 * 8;
+constexpr int kWUnit = 16;         // what a unit costs beside its steps
+
+struct FewWeightParams {
+  const uint16_t* q;
+  const int8_t* k;
+  const float* ks;
+  const float* lse;
+  float* weights;
+  const int32_t* q_start;
+  const int32_t* kv_lens;
+  int32_t* err;
+  int64_t q_stride;
+  Pages pg;
+  int n, B, Hq, G, RC, ctas;       // RC: rows of a chunk
+  DivU32 div_RC, div_G;
+  float sm_log2;
+};
+__device__ __forceinline__ int chunks_of(const FewWeightParams& p, const SeqF& s) { return (int)divu32((uint32_t)(s.nq + p.RC - 1), p.div_RC); }
+__device__ __forceinline__ uint32_t unit_cost(const FewWeightParams& p, const SeqF& s) {
+  return kWUnit + (uint32_t)(((uint32_t)s.nkv + kStep - 1) / kStep) * (uint32_t)chunks_of(p, s);
+}
+__device__ __forceinline__ uint32_t sequence_cost(const FewWeightParams& p, const SeqF& s) {
+  return s.nq > 0 ? (uint32_t)p.pg.Hkv * unit_cost(p, s) : 0u;
+}
+
+__global__ void __launch_bounds__(kThreadsF, 4) few_weights_kernel(const __grid_constant__ FewWeightParams p) {
+  extern __shared__ __align__(128) uint8_t fsm[];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+  const int r = lane >> 2, qd = lane & 3;
+  Begin w = {{0, 0, 0}, p.B, 0u};
+  const LineF line = find_begin(p, cta, lane, &w);
+  uint32_t left = line.begin(cta + 1) - line.begin(cta);
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(fsm) + (uint32_t)(warp * kWStages * kStep * kD);
+  auto swz = [](int row) { return (row & 6) ^ ((row & 1) << 2); };
+  auto chunk_addr = [&](uint32_t base, int row, int col) { return base + row * 128 + ((col ^ swz(row)) << 4); };
+  const int64_t tok_stride = (int64_t)p.pg.Hkv * kD;
+  uint4* const sm_q = reinterpret_cast<uint4*>(fsm + OFF_WQ);
+  float4* const sm_c = reinterpret_cast<float4*>(fsm + OFF_WC);
+  int2* const sm_lim = reinterpret_cast<int2*>(fsm + OFF_WL);
+  SeqF s = w.s;
+  int g = 0;
+  uint32_t off = 0;
+  if (left > 0) {
+    g = (int)(w.off / unit_cost(p, s));
+    off = w.off - (uint32_t)g * unit_cost(p, s);
+  }
+  while (left > 0) {
+    const uint32_t cost = unit_cost(p, s), take = min(cost - off, left);
+    const int chunks = chunks_of(p, s), c0 = s.nkv - s.nq;
+    // a part begins with the first step that begins behind its begin
+    auto step_at = [&](uint32_t o) { return o <= kWUnit ? 0 : (int)((o - kWUnit + (uint32_t)chunks - 1u) / (uint32_t)chunks); };
+    const int s0 = step_at(off), s1 = step_at(off + take);
+    const int n_my = s1 - s0 > warp ? (s1 - s0 - warp + kWarps - 1) / kWarps : 0;   // steps s0 + warp, + 4, ...
+    for (int chunk = 0; chunk < chunks && s0 < s1; ++chunk) {
+      const int i0 = chunk * p.RC, cols = min(p.RC, s.nq - i0) * p.G, tiles = (cols + 7) >> 3;
+      // A lane looks one of the next 32 steps up: its page and row there, and its scale.
+      int page_of = 0, at_of = 0;
+      float ks_of = 0.f, ks_next = 0.f;
+      int page_next = 0, at_next = 0;
+      auto look_up = [&](int m) {
+        const uint32_t t = (uint32_t)((s0 + warp + kWarps * min(m + lane, n_my - 1)) * kStep), pi = divu32(t, p.pg.div_ps);
+        page_next = __ldg(p.pg.table + (int64_t)w.b * p.pg.max_pages + pi);
+        at_next = (int)(t - pi * (uint32_t)p.pg.page_size);
+        if ((uint32_t)page_next >= (uint32_t)p.pg.num_pages) {      // outside the pool: its tokens get nothing
+          set_dev_err(p.err, FA3_DEVERR_PAGE);
+          page_next = -1;
+        }
+        ks_next = __ldg(p.ks + ((int64_t)max(page_next, 0) * p.pg.per_page + (int)divu32((uint32_t)at_next, p.pg.div_block)) * p.pg.Hkv + g);
+      };
+      const int64_t lane_off = (int64_t)(lane >> 3) * tok_stride + g * kD + (lane & 7) * 16;
+      const uint32_t lane_dst = ring + (uint32_t)(lane >> 3) * 128;
+      const uint32_t dst_even = ((lane & 7) ^ swz(lane >> 3)) << 4, dst_odd = ((lane & 7) ^ swz((lane >> 3) + 4)) << 4;
+      auto issue = [&](int m) {
+        const int pg = __shfl_sync(0xffffffffu, page_next, m & 31), at = __shfl_sync(0xffffffffu, at_next, m & 31);
+        const int8_t* ka = p.k + ((int64_t)max(pg, 0) * p.pg.page_size + at) * tok_stride + lane_off;
+        const uint32_t dst = lane_dst + (m % kWStages) * (kStep * kD);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cp_async16(dst + 512 * i + (i & 1 ? dst_odd : dst_even), ka + 4 * i * tok_stride);
+      };
+      if (n_my > 0) look_up(0);
+#pragma unroll
+      for (int m = 0; m < kWStages - 1; ++m) {
+        if (m < n_my) issue(m);
+        cp_async_commit();
+      }
+      // Q^T fragments as above, a tile of 8 columns a warp
+      for (int tile = warp; tile < tiles; tile += kWarps) {
+        const int col = 8 * tile + r, ri = (int)divu32((uint32_t)col, p.div_G), h = g * p.G + col - ri * p.G;
+        const int64_t row = s.q0 + i0 + ri;
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[i] = col < cols ? __ldg(reinterpret_cast<const uint4*>(p.q + row * p.q_stride + (int64_t)h * kD + (i >> 1) * 64 +
+                                                                   16 * qd + 8 * (i & 1)))
+                            : make_uint4(0u, 0u, 0u, 0u);
+        const float lse = col < cols ? __ldg(p.lse + row * p.Hq + h) * -1.4426950408889634f : 0.f;
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
+                                       __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu)));
+        top = max(top & 0xffffu, top >> 16);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const uint32_t e = max(top >> 7, 15u);
+        const float f = __uint_as_float((268u - e) << 23), inv = __uint_as_float((e - 14u) << 23) * p.sm_log2;
+        auto two = [&](uint32_t y) { return pack_f16x2(__uint_as_float(y << 16) * f, __uint_as_float(y & 0xffff0000u) * f); };
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          sm_q[(tile * 4 + i) * 32 + lane] = make_uint4(two(v[i].x), two(v[i].y), two(v[i].z), two(v[i].w));
+        const int lim = col < cols ? c0 + i0 + ri : -1;
+        const float f0 = __shfl_sync(0xffffffffu, inv, 8 * qd), f1 = __shfl_sync(0xffffffffu, inv, 8 * qd + 4);
+        const float l0 = __shfl_sync(0xffffffffu, lse, 8 * qd), l1 = __shfl_sync(0xffffffffu, lse, 8 * qd + 4);
+        const int m0 = __shfl_sync(0xffffffffu, lim, 8 * qd), m1 = __shfl_sync(0xffffffffu, lim, 8 * qd + 4);
+        if (r == 0) {
+          sm_c[tile * 4 + qd] = make_float4(f0, f1, l0, l1);
+          sm_lim[tile * 4 + qd] = make_int2(m0, m1);
+        }
+      }
+      __syncthreads();
+      const int lim_min = (cols & 7) ? -1 : c0 + i0;             // the last key that all of the chunk's columns see
+      for (int m = 0; m < n_my; ++m) {
+        const int t0 = (s0 + warp + kWarps * m) * kStep;
+        if ((m & 31) == 0) page_of = page_next, at_of = at_next, ks_of = ks_next;
+        const float ks = __shfl_sync(0xffffffffu, ks_of, m & 31);
+        const int page = __shfl_sync(0xffffffffu, page_of, m & 31), at = __shfl_sync(0xffffffffu, at_of, m & 31);
+        if (m + kWStages - 1 < n_my) {
+          if (((m + kWStages - 1) & 31) == 0) look_up(m + kWStages - 1);
+          issue(m + kWStages - 1);
+        }
+        cp_async_commit();
+        cp_async_wait<kWStages - 1>();
+        __syncwarp();
+        const uint32_t kst = ring + (m % kWStages) * (kStep * kD);
+        uint32_t a[8][4];
+        {
+          const uint4 k0 = lds128(chunk_addr(kst, r, qd)), k1 = lds128(chunk_addr(kst, r, 4 + qd)),
+                      k2 = lds128(chunk_addr(kst, r + 8, qd)), k3 = lds128(chunk_addr(kst, r + 8, 4 + qd));
+#pragma unroll
+          for (int st = 0; st < 8; ++st) {
+            codes_to_f16(word(st < 4 ? k0 : k1, st & 3), a[st][0], a[st][2]);
+            codes_to_f16(word(st < 4 ? k2 : k3, st & 3), a[st][1], a[st][3]);
+          }
+        }
+        __syncwarp();                                            // every lane has its fragments: the stage may be refilled
+        const bool masked = t0 + kStep - 1 > lim_min;
+        const int ta = t0 + r, tb = ta + 8;
+        float sa = 0.f, sb = 0.f;
+#pragma unroll 1
+        for (int tile = 0; tile < tiles; ++tile) {
+          float cf[4] = {};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 b = sm_q[(tile * 4 + i) * 32 + lane];
+            mma16816(cf, a[2 * i][0], a[2 * i][1], a[2 * i][2], a[2 * i][3], b.x, b.y);
+            mma16816(cf, a[2 * i + 1][0], a[2 * i + 1][1], a[2 * i + 1][2], a[2 * i + 1][3], b.z, b.w);
+          }
+          const float4 c = sm_c[tile * 4 + qd];
+          const float e0 = c.x * ks, e1 = c.y * ks;
+          float y0 = ex2_approx(fmaf(cf[0], e0, c.z)), y1 = ex2_approx(fmaf(cf[1], e1, c.w)),
+                y2 = ex2_approx(fmaf(cf[2], e0, c.z)), y3 = ex2_approx(fmaf(cf[3], e1, c.w));
+          if (masked) {
+            const int2 lim = sm_lim[tile * 4 + qd];
+            y0 = ta <= lim.x ? y0 : 0.f;
+            y1 = ta <= lim.y ? y1 : 0.f;
+            y2 = tb <= lim.x ? y2 : 0.f;
+            y3 = tb <= lim.y ? y3 : 0.f;
+          }
+          sa += y0 + y1;
+          sb += y2 + y3;
+        }
+        sa += __shfl_xor_sync(0xffffffffu, sa, 1);
+        sb += __shfl_xor_sync(0xffffffffu, sb, 1);
+        sa += __shfl_xor_sync(0xffffffffu, sa, 2);
+        sb += __shfl_xor_sync(0xffffffffu, sb, 2);
+        const int t = qd ? tb : ta;
+        if (qd < 2 && page >= 0 && t < s.nkv) {
+          float* to = p.weights + ((int64_t)page * p.pg.Hkv + g) * p.pg.page_size + at + r + 8 * qd;
+          // a new token begins with nothing; old ones may lie in pages that sequences share
+          if (t >= c0 && chunk == 0)
+            *to = qd ? sb : sa;
+          else
+            atomicAdd(to, qd ? sb : sa);
+        }
+      }
+      cp_async_wait<0>();
+      __syncthreads();                                           // the fragments are the next chunk's
+    }
+    left -= take;
+    off = 0;
+    if (++g == p.pg.Hkv && left > 0) {
+      g = 0;
+      do {
+        s = ++w.b < p.B ? sequence_of(p, w.b, false) : SeqF{0, 1, 0};
+      } while (s.nq <= 0);
+    }
+  }
+}
+
 // Column tiles of 8 where sequences have 8 columns or fewer on average, of 16 otherwise.
 int n_tiles(int n, int B, int G) { return (int64_t)std::max(1, n / B) * G <= 8 ? 1 : 2; }
 int ctas_of(int nt, int sms) { return sms * (nt == 1 ? 4 : 3); }
@@ -628,6 +841,35 @@ cudaError_t few_rows_attn(const FewCall& c, const int32_t* table, int num_pages,
   const int nt = n_tiles(c.n, c.B, c.G);
   p.ctas = ctas_of(nt, c.sms);
   return nt == 1 ? launch<1>(p, workspace, s) : launch<2>(p, workspace, s);
+}
+
+
+bool few_rows_weights(int n, int B, int Hkv, int G, int T_max) {
+  const double chunks = (double)n / (kChunkCols / std::min(G, kChunkCols)) + B;
+  // Up to some 64 columns a sequence: 16 sequences of 4096 keys, 64 query and 8 KV heads, with 1, 4, 8 and 16 rows each take
+  // 18.3, 26.0, 37.8 and 72.6 us here and 45.5, 45.3, 43.3 and 54.0 in fa3_weights.cu's kernel.
+  return G <= kChunkCols && (int64_t)n * G <= (int64_t)72 * B &&
+         Hkv * ((double)B * kWUnit + chunks * (T_max / kStep + 1.0)) < 2147483648.0;
+}
+cudaError_t few_rows_weights_attn(const FewCall& c, float* weights, const int32_t* table, int num_pages, int page_size,
+                                  int max_pages, int block, int Hkv, cudaStream_t s) {
+  FewWeightParams p;
+  if (pages_of(table, c.B, Hkv, num_pages, page_size, max_pages, block, &p.pg) != FA3_OK) return cudaErrorInvalidValue;
+  static std::atomic<bool> set[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return cudaErrorInvalidDevice;
+  if (dev >= 64 || !set[dev].load(std::memory_order_acquire)) {
+    const cudaError_t e = cudaFuncSetAttribute(few_weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_FEW_WEIGHTS);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) set[dev].store(true, std::memory_order_release);
+  }
+  p.q = c.q; p.k = c.k; p.ks = c.ks; p.lse = c.lse; p.weights = weights; p.q_start = c.q_start; p.kv_lens = c.kv_lens;
+  p.err = c.err; p.q_stride = c.q_stride; p.n = c.n; p.B = c.B; p.Hq = c.Hq; p.G = c.G; p.sm_log2 = c.sm_log2;
+  p.RC = kChunkCols / c.G;
+  p.div_RC = make_divu32((uint32_t)p.RC);
+  p.div_G = make_divu32((uint32_t)c.G);
+  p.ctas = 4 * c.sms;
+  return launch_pdl(few_weights_kernel, dim3((unsigned)p.ctas), dim3(kThreadsF), SMEM_FEW_WEIGHTS, s, p);
 }
 
 }  // namespace fa3

@@ -17,7 +17,7 @@ struct FewCall {
   const int32_t* q_start;
   const int32_t* kv_lens;
   uint16_t* out;
-  float* lse;
+  float* lse;                      // written (read by the weights)
   int64_t q_stride;
   int n, B, Hq, G, sms;
   float sm_log2;
@@ -29,5 +29,10 @@ bool few_rows(int n, int B, int Hkv, int G, int T_max);
 size_t few_rows_workspace(int n, int B, int G, int sms);
 cudaError_t few_rows_attn(const FewCall& c, const int32_t* table, int num_pages, int page_size, int max_pages, int block,
                           int Hkv, void* workspace, cudaStream_t s);
+
+// The same of fa3_attn_weights_gqa_block_paged (v, vs and out unused; lse is read).
+bool few_rows_weights(int n, int B, int Hkv, int G, int T_max);
+cudaError_t few_rows_weights_attn(const FewCall& c, float* weights, const int32_t* table, int num_pages, int page_size,
+                                  int max_pages, int block, int Hkv, cudaStream_t s);
 
 }  // namespace fa3

@@ -19,6 +19,7 @@
 //
 // Every wait is bounded; on time-out the kernel sets FA3_DEVERR_TIMEOUT, waits for its
 // copies and MMAs, frees its TMEM and returns.
+#include "fa3_few.cuh"
 #include "fa3_packed.cuh"
 #include "fa3_pipe.cuh"
 
@@ -593,6 +594,12 @@ FA3_API int fa3_attn_weights_gqa_block_paged(const uint16_t* q, const int8_t* k_
   st = check_device(&sms);
   if (st != FA3_OK) return st;
   if (!workspace || workspace_bytes < weights_bytes_of(sms) || !aligned16(workspace)) return FA3_EWORKSPACE;
+  if (few_rows_weights(n, B, Hkv, p.G, p.pg.T_max)) {
+    const FewCall c = {q, k_cache, nullptr, k_scale, nullptr, q_start, kv_lens, nullptr, const_cast<float*>(lse), q_stride, n, B,
+                       Hq, p.G, sms, softmax_scale * 1.4426950408889634f, dev_err};
+    return cuda_status(few_rows_weights_attn(c, weights, block_table, num_pages, page_size, max_pages, block, Hkv,
+                                             static_cast<cudaStream_t>(stream)));
+  }
   p.k = k_cache; p.ks = k_scale; p.lse = lse; p.weights = weights; p.q_start = q_start; p.kv_lens = kv_lens;
   p.part = static_cast<float*>(workspace);
   p.cuts = reinterpret_cast<CutW*>(p.part + (size_t)2 * sms * kKeysW);
