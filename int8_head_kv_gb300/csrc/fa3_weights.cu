@@ -13,9 +13,9 @@
 // parts leave their sums in the workspace, and weights_combine_kernel adds them up in order, so results do not
 // depend on which CTA is first.
 //
-// Roles in the CTA (512 threads).  Warp 0 issues the MMAs, warp 1 brings the query tiles by TMA, warp 2 plans, warp 3 brings
-// the rows' log-sum-exps.  Warps 4-7 and 8-11 (a key a lane) sum up the scores of the first and second row tile.
-// Warps 12-15 bring the int8 keys and write them as bf16.
+// Roles in the CTA (768 threads).  Warp 0 issues the MMAs, warp 1 brings the query tiles by TMA, warp 2 plans, warp 3 brings
+// the rows' log-sum-exps.  Warps 4-7 and 8-11 (a key a lane) sum up the first 64 columns of the first and second row
+// tile, warps 12-19 the others.  Warps 20-23 bring the int8 keys and write them as bf16.
 //
 // Every wait is bounded; on time-out the kernel sets FA3_DEVERR_TIMEOUT, waits for its
 // copies and MMAs, frees its TMEM and returns.
@@ -35,7 +35,7 @@ namespace {
 constexpr int kD = 128;
 constexpr int kKeysW = 256;        // keys of a unit: two row tiles of the MMA
 constexpr int kCols = 128;         // columns of a step, at most
-constexpr int kThreadsW = 512;
+constexpr int kThreadsW = 768;
 constexpr uint32_t kHalfTile = 128 * 128;                  // 128 rows of 64 values of d, 128-byte swizzle
 constexpr uint32_t kTile = 2 * kHalfTile;                  // 128 rows of 128 values
 constexpr uint32_t kQStages = 3;
@@ -52,12 +52,15 @@ enum {
   W_DRAIN = 10,
   W_Q_FULL = 11, W_Q_EMPTY = 14,   // [3]: a step's queries
   W_PART_FULL = 17, W_PART_EMPTY = 21,   // [4]
-  W_N = 25
+  W_SUM_FULL = 25, W_SUM_EMPTY = 27,     // [2]: the sums over a row tile's other columns written; read
+  W_N = 29
 };
-__constant__ const uint8_t kArrivalsW[W_N] = {4, 4, 1, 1, 1, 1, 8, 8, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 15, 15, 15, 15};
-constexpr uint32_t OFF_TSLOTW = OFF_BARW + 8 * W_N;
+__constant__ const uint8_t kArrivalsW[W_N] = {4, 4, 1, 1, 1, 1, 16, 16, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 23, 23, 23, 23,
+                                                4, 4, 4, 4};
+constexpr uint32_t OFF_SUMW = (OFF_BARW + 8 * W_N + 15) / 16 * 16;   // [2][128] float
+constexpr uint32_t OFF_TSLOTW = OFF_SUMW + kKeysW * 4;
 constexpr uint32_t OFF_ABORTW = OFF_TSLOTW + 4;
-constexpr uint32_t SMEM_WEIGHTS = OFF_ABORTW + 4 + 1024;   // + alignment slack
+constexpr uint32_t SMEM_WEIGHTS = OFF_ABORTW + 4;          // aligned by its declaration: there is no room for slack
 static_assert(SMEM_WEIGHTS <= 232448, "shared memory");
 
 // The line's unit is a step.  kUnitSteps: what a unit costs beside its steps (its keys' way to shared memory); kLeastSteps: the
@@ -250,6 +253,12 @@ __device__ __forceinline__ void i8x4_to_bf16x4(uint32_t w, uint32_t& lo, uint32_
   hi = two(__byte_perm(w, 0x43434343u, 0x4342));
 }
 
+__device__ __forceinline__ void wait_ld32(uint32_t* v) {
+  wait_ld16(v);
+  asm volatile("" : "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                    "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+               :: "memory");
+}
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* tm, int c0, int c1, int c2, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
@@ -257,8 +266,7 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* tm, int 
 }
 
 __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_constant__ WeightParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + OFF_ABORTW);
@@ -413,12 +421,12 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
         ++steps;
       }
     }
-  } else if (warp >= 12) {
+  } else if (warp >= 20) {
     // ------------------------------------------------------ int8 keys -> bf16
     // A warp has 64 keys, a lane 16 bytes of sixteen of them: bytes 16 (l % 8) .. of row l / 8, lanes l % 8 >= 4 of the row's
     // neighbour (l / 8) ^ 1, so that the eight lanes of a store hit different banks of the swizzled rows.  A lane looks
     // two keys up, the others get their rows by shuffles.
-    const int cw = warp - 12, cl = lane & 7, rl = (lane >> 3) ^ (cl >> 2);
+    const int cw = warp - 20, cl = lane & 7, rl = (lane >> 3) ^ (cl >> 2);
     const uint32_t dst0 = sbase + OFF_KW + (uint32_t)(cw >> 1) * kTile + (uint32_t)(cl >> 2) * kHalfTile +
                           (uint32_t)(64 * (cw & 1) + rl) * 128;
     const uint32_t at0 = ((uint32_t)(2 * cl & 7) ^ (uint32_t)rl) * 16;   // n % 8 = rl, or rl + 4 for odd i
@@ -439,34 +447,41 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
         }
         rows[h] = page * p.pg.page_size + (int)(t - pi * (uint32_t)p.pg.page_size);
       }
-      uint4 r[16];
       const int8_t* base = p.k + u.g * kD + cl * 16;
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        r[i] = load_once(base + (int64_t)__shfl_sync(0xffffffffu, rows[i >> 3], (4 * i & 31) + rl) * row_stride);
       const uint32_t kb = units & 1u, dst = dst0 + 2 * kb * kTile;
-      ok = warp_wait(bar(W_K_EMPTY) + 8u * kb, ((units >> 1) & 1u) ^ 1u, lane, abort_flag, p.err, p.wait_ticks);
-      if (!ok) break;
+#pragma unroll 1
+      for (int half = 0; half < 2 && ok; ++half) {
+        uint4 r[8];
+        const int row = half ? rows[1] : rows[0];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        uint4 o0, o1;
-        i8x4_to_bf16x4(r[i].x, o0.x, o0.y);
-        i8x4_to_bf16x4(r[i].y, o0.z, o0.w);
-        i8x4_to_bf16x4(r[i].z, o1.x, o1.y);
-        i8x4_to_bf16x4(r[i].w, o1.z, o1.w);
-        const uint32_t at = at0 ^ ((uint32_t)(i & 1) << 6);
-        sts128(dst + 4 * i * 128 + at, o0);
-        sts128(dst + 4 * i * 128 + (at ^ 16u), o1);
+        for (int i = 0; i < 8; ++i)
+          r[i] = load_once(base + (int64_t)__shfl_sync(0xffffffffu, row, 4 * i + rl) * row_stride);
+        if (half == 0) ok = warp_wait(bar(W_K_EMPTY) + 8u * kb, ((units >> 1) & 1u) ^ 1u, lane, abort_flag, p.err, p.wait_ticks);
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          uint4 o0, o1;
+          i8x4_to_bf16x4(r[i].x, o0.x, o0.y);
+          i8x4_to_bf16x4(r[i].y, o0.z, o0.w);
+          i8x4_to_bf16x4(r[i].z, o1.x, o1.y);
+          i8x4_to_bf16x4(r[i].w, o1.z, o1.w);
+          const uint32_t at = at0 ^ ((uint32_t)(i & 1) << 6);
+          sts128(dst + (32 * half + 4 * i) * 128 + at, o0);
+          sts128(dst + (32 * half + 4 * i) * 128 + (at ^ 16u), o1);
+        }
       }
+      if (!ok) break;
       fence_proxy_async();
       warp_arrive(W_K_FULL + (int)kb);
       ++units;
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------ sums of exponentials, a key a lane
-    const int h = (warp - 4) >> 2;
+    const int h = ((warp - 4) >> 2) & 1, side = (warp - 4) >> 3;   // row tile, half of the columns
     const int r = ((warp - 4) & 3) * 32 + lane;
     const uint32_t lane_base = (uint32_t)(((warp - 4) & 3) * 32) << 16;
+    float* const other = reinterpret_cast<float*>(smem + OFF_SUMW) + h * 128 + r;
+    uint32_t units = 0;
     uint32_t steps = 0;
     bool ok = true;
     while (ok && next_part()) {
@@ -493,31 +508,35 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
         const int i0 = (rt0 + s) * p.P, cols = min(p.P, u.nq - i0) * p.G;
         const int from = valid ? min(max(t - c - i0, 0), kCols) * p.G : kCols;   // the first column that sees this key
         const uint32_t scol = tmem + lane_base + st * 256 + (uint32_t)h * 128, ls = sbase + OFF_LSE + st * kCols * 4;
-        const bool cut = __any_sync(0xffffffffu, from > 0) || (cols & 15);
+        const int clear = __reduce_max_sync(0xffffffffu, from);              // from here on all of the warp's keys are seen
         float a0 = 0.f, a1 = 0.f;
 #pragma unroll 1
-        for (int k = 0; k < cols; k += 16) {
-          uint32_t w[16];
-          FA3_TMEM_LD16(scol + k, w);
-          float l[16];
+        for (int k = 64 * side; k < min(cols, 64 * side + 64); k += 32) {
+          uint32_t w[32];
+          FA3_TMEM_LD32(scol + k, w);
+          wait_ld32(w);
+          if (k >= clear && k + 32 <= cols) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint4 v = lds128(ls + 4 * (k + 4 * e));
-            l[4 * e] = __uint_as_float(v.x), l[4 * e + 1] = __uint_as_float(v.y);
-            l[4 * e + 2] = __uint_as_float(v.z), l[4 * e + 3] = __uint_as_float(v.w);
-          }
-          wait_ld16(w);
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            float x0, x1;
-            fma2(x0, x1, __uint_as_float(w[e]), __uint_as_float(w[e + 1]), f, f, l[e], l[e + 1]);
-            x0 = ex2_approx(x0);
-            x1 = ex2_approx(x1);
-            if (cut) {                                        // also drops what columns without a row hold
-              x0 = k + e >= from && k + e < cols ? x0 : 0.f;
-              x1 = k + e + 1 >= from && k + e + 1 < cols ? x1 : 0.f;
+            for (int e = 0; e < 32; e += 4) {
+              const uint4 v = lds128(ls + 4 * (k + e));
+              float x0, x1, x2, x3;
+              fma2(x0, x1, __uint_as_float(w[e]), __uint_as_float(w[e + 1]), f, f, __uint_as_float(v.x), __uint_as_float(v.y));
+              fma2(x2, x3, __uint_as_float(w[e + 2]), __uint_as_float(w[e + 3]), f, f, __uint_as_float(v.z), __uint_as_float(v.w));
+              add2(a0, a1, a0, a1, ex2_approx(x0), ex2_approx(x1));
+              add2(a0, a1, a0, a1, ex2_approx(x2), ex2_approx(x3));
             }
-            add2(a0, a1, a0, a1, x0, x1);
+          } else {
+            // the mask also drops what columns without a row hold
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const uint4 v = lds128(ls + 4 * (k + e));
+              const float l[4] = {__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float y = ex2_approx(fmaf(__uint_as_float(w[e + i]), f, l[i]));
+                a0 += k + e + i >= from && k + e + i < cols ? y : 0.f;
+              }
+            }
           }
         }
         tc_fence_before();
@@ -528,6 +547,20 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
         total = z;
       }
       if (!ok) break;
+      // the two warps of a key meet in shared memory
+      const uint32_t par = units & 1u;
+      ++units;
+      if (side) {
+        ok = warp_wait(bar(W_SUM_EMPTY + h), par ^ 1u, lane, abort_flag, p.err);
+        if (!ok) break;
+        *other = total;
+        warp_arrive(W_SUM_FULL + h);
+        continue;
+      }
+      ok = warp_wait(bar(W_SUM_FULL + h), par, lane, abort_flag, p.err);
+      if (!ok) break;
+      total += *other;
+      warp_arrive(W_SUM_EMPTY + h);
       if (u.s0 == 0 && u.s1 == u.n) {
         if (valid) add_weight(p, u.b, u.g, t, t >= c, total);
       } else {
