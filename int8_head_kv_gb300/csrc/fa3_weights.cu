@@ -8,14 +8,20 @@
 // a thread has a key and sums along its own TMEM lane.  bf16 queries go in as they are, and an int8 code is exact
 // in bf16, so the products are exact and the sums float32.
 //
-// Work.  A unit is 256 keys of one sequence and KV head, as two row tiles; a step is the scores of P new tokens x G heads
-// (up to 128 columns) with both.  All units lie on one line that is cut into equal parts, one per SM; a cut unit's
+// The row's log-sum-exp goes into the product as well: with f the key's factor (its scale, softmax_scale and log2(e)), the exponent
+// is f (S - lse / f), and lse / f is a product of a number of the key's and one of the column's.  Both are split into
+// three bf16 parts, exactly, and the eight products of parts that count (what is left out is below 2^-31 of it) are one more
+// slice of the contraction.  A thread then reads nothing but its scores: with the log-sum-exps in shared memory, each warp reading
+// them anew, that memory was the bound (4460 cycles for 512 keys x 128 columns; the MMAs alone take 2048).
+//
+// Work.  A unit is 512 keys of one sequence and KV head, as four row tiles; a step is the scores of P new tokens x G heads
+// (up to 128 columns) with all four.  All units lie on one line that is cut into equal parts, one per SM; a cut unit's
 // parts leave their sums in the workspace, and weights_combine_kernel adds them up in order, so results do not
 // depend on which CTA is first.
 //
-// Roles in the CTA (768 threads).  Warp 0 issues the MMAs, warp 1 brings the query tiles by TMA, warp 2 plans, warp 3 brings
-// the rows' log-sum-exps.  Warps 4-7 and 8-11 (a key a lane) sum up the first 64 columns of the first and second row
-// tile, warps 12-19 the others.  Warps 20-23 bring the int8 keys and write them as bf16.
+// Roles in the CTA (768 threads).  Warp 0 issues the MMAs, warp 1 brings the query tiles by TMA, warp 2 plans, warp 3 writes the
+// columns' parts of the log-sum-exps.  Warps 4-7, 8-11, 12-15 and 16-19 (a key a lane) sum up the four row tiles' scores, each in a
+// quarter of TMEM.  Warps 20-23 bring the int8 keys and write them as bf16, and the keys' parts of the log-sum-exps.
 //
 // Every wait is bounded; on time-out the kernel sets FA3_DEVERR_TIMEOUT, waits for its
 // copies and MMAs, frees its TMEM and returns.
@@ -33,39 +39,40 @@ namespace fa3 {
 namespace {
 
 constexpr int kD = 128;
-constexpr int kKeysW = 256;        // keys of a unit: two row tiles of the MMA
+constexpr int kTilesW = 4, kKeysW = 128 * kTilesW;         // row tiles of the MMA and keys of a unit
 constexpr int kCols = 128;         // columns of a step, at most
 constexpr int kThreadsW = 768;
 constexpr uint32_t kHalfTile = 128 * 128;                  // 128 rows of 64 values of d, 128-byte swizzle
 constexpr uint32_t kTile = 2 * kHalfTile;                  // 128 rows of 128 values
-constexpr uint32_t kQStages = 3;
-constexpr uint32_t OFF_KW = 0;                             // 2 buffers of two row tiles
+constexpr uint32_t kQStages = 2;
+constexpr uint32_t kSlice = 128 * 32;                      // 128 rows of 16 values, in two chunks of 8
+constexpr uint32_t OFF_KW = 0;                             // four row tiles
 constexpr uint32_t OFF_QW = OFF_KW + 4 * kTile;
-constexpr uint32_t OFF_LSE = OFF_QW + kQStages * kTile;    // [2][128] float
+constexpr uint32_t OFF_KX = OFF_QW + kQStages * kTile;     // the row tiles' slices of the log-sum-exp
+constexpr uint32_t OFF_QX = OFF_KX + kTilesW * kSlice;     // the columns', a stage each
 constexpr uint32_t kRingW = 4, kPartBytesW = 48;
-constexpr uint32_t OFF_PARTSW = OFF_LSE + 2 * kCols * 4;
+constexpr uint32_t OFF_PARTSW = OFF_QX + kQStages * kSlice;
 constexpr uint32_t OFF_BARW = OFF_PARTSW + kRingW * kPartBytesW;
 enum {
-  W_K_FULL = 0, W_K_EMPTY = 2,     // [2]: a unit's keys written; all its MMAs done
-  W_S_FULL = 4, W_S_EMPTY = 6,     // [2]: a step's scores; read
-  W_L_FULL = 8,                    // [2]: a step's log-sum-exps (free again with S_EMPTY)
-  W_DRAIN = 10,
-  W_Q_FULL = 11, W_Q_EMPTY = 14,   // [3]: a step's queries
-  W_PART_FULL = 17, W_PART_EMPTY = 21,   // [4]
-  W_SUM_FULL = 25, W_SUM_EMPTY = 27,     // [2]: the sums over a row tile's other columns written; read
-  W_N = 29
+  W_K_FULL = 0, W_K_EMPTY = 1,     // a unit's keys written; all its MMAs done
+  W_S_FULL = 2, W_S_EMPTY = 6,     // [4]: a row tile's scores of a step; read
+  W_Q_FULL = 10, W_Q_EMPTY = 12,   // [2]: a step's queries and log-sum-exps
+  W_DRAIN = 14,
+  W_PART_FULL = 15, W_PART_EMPTY = 19,   // [4]
+  W_N = 23
 };
-__constant__ const uint8_t kArrivalsW[W_N] = {4, 4, 1, 1, 1, 1, 16, 16, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 23, 23, 23, 23,
-                                                4, 4, 4, 4};
-constexpr uint32_t OFF_SUMW = (OFF_BARW + 8 * W_N + 15) / 16 * 16;   // [2][128] float
-constexpr uint32_t OFF_TSLOTW = OFF_SUMW + kKeysW * 4;
+__constant__ const uint8_t kArrivalsW[W_N] = {4, 1, 1, 1, 1, 1, 4, 4, 4, 4, 2, 2, 1, 1, 1, 1, 1, 1, 1, 23, 23, 23, 23};
+constexpr uint32_t OFF_TSLOTW = OFF_BARW + 8 * W_N;
 constexpr uint32_t OFF_ABORTW = OFF_TSLOTW + 4;
-constexpr uint32_t SMEM_WEIGHTS = OFF_ABORTW + 4;          // aligned by its declaration: there is no room for slack
+constexpr uint32_t SMEM_WEIGHTS = OFF_ABORTW + 4 + 1024;   // + alignment slack
 static_assert(SMEM_WEIGHTS <= 232448, "shared memory");
 
 // The line's unit is a step.  kUnitSteps: what a unit costs beside its steps (its keys' way to shared memory); kLeastSteps: the
 // least part of the line a CTA takes, enough for a part inside a unit to hold a step.
-constexpr int kUnitSteps = 2, kLeastSteps = 4;
+#ifndef KU
+#define KU 2
+#endif
+constexpr int kUnitSteps = KU, kLeastSteps = KU + 2;
 static_assert(kLeastSteps > kUnitSteps, "a part inside a unit, behind its fixed cost, holds a step");
 
 struct CutW {
@@ -79,7 +86,7 @@ struct WeightParams {
   float* weights;                  // [num_pages][Hkv][page_size]
   const int32_t* q_start;
   const int32_t* kv_lens;
-  float* part;                     // [2 * CTAs][256]: sums of a cut unit's parts
+  float* part;                     // [2 * CTAs][512]: sums of a cut unit's parts
   CutW* cuts;                      // [CTAs]
   int32_t* err;
   Pages pg;
@@ -114,6 +121,10 @@ __device__ __forceinline__ int col_tiles(const WeightParams& p, const SeqW& s) {
 __device__ __forceinline__ int first_col_tile(const WeightParams& p, const SeqW& s, int j) {
   const int i0 = j * kKeysW - (s.nkv - s.nq);
   return i0 <= 0 ? 0 : (int)divu32((uint32_t)i0, p.div_P);
+}
+// The first column tile that sees a key of row tile x of key tile j, as all behind it do (col_tiles: none does).
+__device__ __forceinline__ int first_of_tile(const WeightParams& p, const SeqW& s, int j, int x) {
+  return j * kKeysW + 128 * x < s.nkv ? first_col_tile(p, SeqW{s.q0, s.nq, s.nkv - 128 * x}, j) : col_tiles(p, s);
 }
 __device__ __forceinline__ int steps_of(const WeightParams& p, const SeqW& s, int j) { return col_tiles(p, s) - first_col_tile(p, s, j); }
 // Cost of all units of one KV head.
@@ -259,6 +270,33 @@ __device__ __forceinline__ void wait_ld32(uint32_t* v) {
                     "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
                :: "memory");
 }
+
+// A number as the sum of three bf16 numbers, exactly (24 bits are three times 8; each is the rest's upper half).
+__device__ __forceinline__ void three_parts(float x, uint32_t (&p)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    p[i] = __float_as_uint(x) >> 16;
+    x -= __uint_as_float(p[i] << 16);
+  }
+}
+// The factor of a key's scores: not so small that its inverse leaves float32's range (a smaller one gives every score 0 as well).
+__device__ __forceinline__ float key_factor(const WeightParams& p, int page, int at, int g) {
+  const float ks = (uint32_t)page < (uint32_t)p.pg.num_pages
+                       ? __ldg(p.ks + ((int64_t)page * p.pg.per_page + divu32((uint32_t)at, p.pg.div_block)) * p.pg.Hkv + g)
+                       : 0.f;                                 // outside the pool: the keys' loader reports it
+  return fmaxf(ks * p.sm_log2, 8.673617379884035e-19f);      // 2^-60
+}
+
+#ifndef CH
+#define CH 16
+#endif
+#if CH == 16
+#define LDCH FA3_TMEM_LD16
+#define WCH wait_ld16
+#else
+#define LDCH FA3_TMEM_LD32
+#define WCH wait_ld32
+#endif
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* tm, int c0, int c1, int c2, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
@@ -266,7 +304,8 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* tm, int 
 }
 
 __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_constant__ WeightParams p) {
-  extern __shared__ __align__(1024) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + OFF_ABORTW);
@@ -281,6 +320,10 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     if (lane == 0) prefetch_map(&p.map_q);
   }
+  // the slices' second chunks are zero
+  for (int i = tid; i < (int)((kTilesW + kQStages) * 128); i += kThreadsW)
+    sts128(sbase + OFF_KX + (uint32_t)(i >> 7) * kSlice + 2048u + (uint32_t)(i & 127) * 16u, make_uint4(0u, 0u, 0u, 0u));
+  fence_proxy_async();
   pdl_wait();
   tc_fence_before();
   __syncthreads();
@@ -324,44 +367,49 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
     put(end);
   } else if (warp == 0) {
     // ------------------------------------------------------------ MMA issuer
-    uint32_t units = 0, steps = 0, qs = 0, q_par = 0;
+    uint32_t units = 0, qs = 0, q_par = 0, done = 0;          // done: parities of the row tiles' steps, a bit each
     bool ok = true;
     const uint32_t lead = elect_one();
     while (ok && next_part()) {
       const PartW u = ring[parts % kRingW];
       part_read();
-      const uint32_t kb = units & 1u;
-      ok = warp_all(wait_long(bar(W_K_FULL) + 8u * kb, (units >> 1) & 1u, abort_flag, p.err, p.wait_ticks));
-      const int rt0 = first_col_tile(p, SeqW{u.q0, u.nq, u.nkv}, u.tile);
+      ok = warp_all(wait_long(bar(W_K_FULL), units & 1u, abort_flag, p.err, p.wait_ticks));
+      const SeqW sq = {u.q0, u.nq, u.nkv};
+      const int rt0 = first_col_tile(p, sq, u.tile);
+      int seen[kTilesW];                                      // the first step that sees a row tile
+#pragma unroll
+      for (int x = 0; x < kTilesW; ++x) seen[x] = first_of_tile(p, sq, u.tile, x) - rt0;
 #pragma unroll 1
       for (int s = u.s0; s < u.s1 && ok; ++s) {
-        const uint32_t st = steps & 1u;
-        ok = warp_all(wait_long(bar(W_Q_FULL) + 8u * qs, q_par, abort_flag, p.err)) &&
-             warp_all(wait_long(bar(W_S_EMPTY) + 8u * st, ((steps >> 1) & 1u) ^ 1u, abort_flag, p.err));
-        if (!ok) break;
-        tc_fence_after();
+        ok = warp_all(wait_long(bar(W_Q_FULL) + 8u * qs, q_par, abort_flag, p.err));
         const int cols = min(p.P, u.nq - (rt0 + s) * p.P) * p.G;
         const uint32_t id = idesc_f16(128, (cols + 15) & ~15, true, false);
-        // S = K.Q^T: both K-major, 128-byte swizzle: 8-row groups 1024 B apart, 16 values of d 32 B apart within a half
-#pragma unroll 1
-        for (uint32_t h = 0; h < 2; ++h) {
-          uint32_t a = desc_lo(sbase + OFF_KW + (2 * kb + h) * kTile, 16), bd = desc_lo(sbase + OFF_QW + qs * kTile, 16);
-          uint32_t acc = 0u;
+#pragma unroll
+        for (uint32_t x = 0; x < kTilesW; ++x) {
+          if (!ok || s < seen[x]) continue;
+          ok = warp_all(wait_long(bar(W_S_EMPTY) + 8u * x, ((done >> x) & 1u) ^ 1u, abort_flag, p.err));
+          if (!ok) continue;
+          tc_fence_after();
+          // S = K.Q^T: both K-major, 128-byte swizzle: 8-row groups 1024 B apart, 16 values of d 32 B apart within a half; the
+          // slice of the log-sum-exp without swizzle, as 8-row groups 128 B and chunks of 8 values 2048 B apart
+          uint32_t a = desc_lo(sbase + OFF_KW + x * kTile, 16), bd = desc_lo(sbase + OFF_QW + qs * kTile, 16);
+          mma_ss<desc_hi(128, false), desc_hi(128, false)>(lead, tmem + x * 128, desc_lo(sbase + OFF_KX + x * kSlice, 2048),
+                                                           desc_lo(sbase + OFF_QX + qs * kSlice, 2048), id, 0u);
 #pragma unroll 2
           for (int kk = 0; kk < kD / 16; ++kk) {
-            mma_ss<desc_hi(1024, true), desc_hi(1024, true)>(lead, tmem + st * 256 + h * 128, a, bd, id, acc);
+            mma_ss<desc_hi(1024, true), desc_hi(1024, true)>(lead, tmem + x * 128, a, bd, id, 1u);
             const uint32_t next = kk == 3 ? (kHalfTile >> 4) - 3 * (32 >> 4) : 32 >> 4;
             a += next;
             bd += next;
-            acc = 1u;
           }
+          commit_if(lead, bar(W_S_FULL) + 8u * x);
+          done ^= 1u << x;
         }
-        commit_if(lead, bar(W_S_FULL) + 8u * st);
+        if (!ok) break;
         commit_if(lead, bar(W_Q_EMPTY) + 8u * qs);
-        ++steps;
         if (++qs == kQStages) qs = 0, q_par ^= 1u;
       }
-      if (ok) commit_if(lead, bar(W_K_EMPTY) + 8u * kb);
+      if (ok) commit_if(lead, bar(W_K_EMPTY));
       ++units;
     }
     commit_if(lead, bar(W_DRAIN));                            // every MMA issued has completed before TMEM is freed
@@ -395,40 +443,56 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
       while (!mbar_try(bar(W_Q_FULL) + 8u * t, par) && global_ns() - t0 < kWaitNs / 50) {}
     }
   } else if (warp == 3) {
-    // ------------------------------------------------------ log-sum-exps of a step's columns, in log2 units
-    uint32_t steps = 0;
+    // ------------------------------------------------------ log-sum-exps of a step's columns
+    // -lse log2(e) in parts b1, b2, b3 meets the keys' a1, a2, a3 as a1 b1, a1 b2, a2 b1, a1 b3, a2 b2, a3 b1, a2 b3, a3 b2.  A step's
+    // values are asked for two steps ahead: their way is longer than a step.
+    uint32_t qs = 0, q_par = 1;
     bool ok = true;
     while (ok && next_part()) {
       const PartW u = ring[parts % kRingW];
       part_read();
       const int rt0 = first_col_tile(p, SeqW{u.q0, u.nq, u.nkv}, u.tile);
-#pragma unroll 1
-      for (int s = u.s0; s < u.s1 && ok; ++s) {
-        const int i0 = (rt0 + s) * p.P, cols = min(p.P, u.nq - i0) * p.G;
-        float v[4];
+      float v[3][4];
+      auto ask = [&](int s, float (&to)[4]) {
+        const int i0 = (rt0 + s) * p.P, cols = s < u.s1 ? min(p.P, u.nq - i0) * p.G : 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int c = lane + 32 * k, i = (int)divu32((uint32_t)c, p.div_G);
-          v[k] = c < cols ? p.lse[(int64_t)(u.q0 + i0 + i) * p.Hq + u.g * p.G + c - i * p.G] : 0.f;
+          to[k] = c < cols ? __ldg(p.lse + (int64_t)(u.q0 + i0 + i) * p.Hq + u.g * p.G + c - i * p.G) : 0.f;
         }
-        const uint32_t st = steps & 1u;
-        ok = warp_wait(bar(W_S_EMPTY) + 8u * st, ((steps >> 1) & 1u) ^ 1u, lane, abort_flag, p.err);
-        if (!ok) break;
-        float* to = reinterpret_cast<float*>(smem + OFF_LSE) + st * kCols;
+      };
+      ask(u.s0, v[0]);
+      ask(u.s0 + 1, v[1]);
+#pragma unroll 1
+      for (int s = u.s0; s < u.s1 && ok; s += 3) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) to[lane + 32 * k] = v[k] * -1.4426950408889634f;
-        warp_arrive(W_L_FULL + (int)st);
-        ++steps;
+        for (int x = 0; x < 3; ++x) {
+          if (s + x < u.s1 && ok) {
+            ask(s + x + 2, v[(x + 2) % 3]);
+            ok = warp_wait(bar(W_Q_EMPTY) + 8u * qs, q_par, lane, abort_flag, p.err);
+            if (ok) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                uint32_t b[3];                               // an infinite lse: weights of nothing
+                three_parts(fminf(fmaxf(v[x][k] * -1.4426950408889634f, -1e6f), 1e6f), b);
+                sts128(sbase + OFF_QX + qs * kSlice + (uint32_t)(lane + 32 * k) * 16u,
+                       make_uint4(b[0] | b[1] << 16, b[0] | b[2] << 16, b[1] | b[0] << 16, b[2] | b[1] << 16));
+              }
+              fence_proxy_async();
+              warp_arrive(W_Q_FULL + (int)qs);
+              if (++qs == kQStages) qs = 0, q_par ^= 1u;
+            }
+          }
+        }
       }
     }
   } else if (warp >= 20) {
     // ------------------------------------------------------ int8 keys -> bf16
-    // A warp has 64 keys, a lane 16 bytes of sixteen of them: bytes 16 (l % 8) .. of row l / 8, lanes l % 8 >= 4 of the row's
-    // neighbour (l / 8) ^ 1, so that the eight lanes of a store hit different banks of the swizzled rows.  A lane looks
-    // two keys up, the others get their rows by shuffles.
+    // A warp has a row tile, in four times 32 keys, a lane 16 bytes of eight of them: bytes 16 (l % 8) .. of row l / 8, lanes
+    // l % 8 >= 4 of the row's neighbour (l / 8) ^ 1, so that the eight lanes of a store hit different banks of the swizzled
+    // rows.  A lane looks four keys up, the others get their rows by shuffles.
     const int cw = warp - 20, cl = lane & 7, rl = (lane >> 3) ^ (cl >> 2);
-    const uint32_t dst0 = sbase + OFF_KW + (uint32_t)(cw >> 1) * kTile + (uint32_t)(cl >> 2) * kHalfTile +
-                          (uint32_t)(64 * (cw & 1) + rl) * 128;
+    const uint32_t dst = sbase + OFF_KW + (uint32_t)cw * kTile + (uint32_t)(cl >> 2) * kHalfTile + (uint32_t)rl * 128;
     const uint32_t at0 = ((uint32_t)(2 * cl & 7) ^ (uint32_t)rl) * 16;   // n % 8 = rl, or rl + 4 for odd i
     const int row_stride = p.pg.Hkv * kD;
     uint32_t units = 0;
@@ -436,27 +500,29 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
     while (ok && next_part()) {
       const PartW u = ring[parts % kRingW];
       part_read();
-      int rows[2];
+      const int8_t* base = p.k + u.g * kD + cl * 16;
+      int rows[4];
+      float factor[4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t t = (uint32_t)min(u.tile * kKeysW + 64 * cw + 32 * h + lane, u.nkv - 1), pi = divu32(t, p.pg.div_ps);
+      for (int h = 0; h < 4; ++h) {
+        const uint32_t t = (uint32_t)min(u.tile * kKeysW + 128 * cw + 32 * h + lane, u.nkv - 1), pi = divu32(t, p.pg.div_ps);
         int page = __ldg(p.pg.table + (int64_t)u.b * p.pg.max_pages + pi);
         if ((uint32_t)page >= (uint32_t)p.pg.num_pages) {      // outside the pool: any page of it
           set_dev_err(p.err, FA3_DEVERR_PAGE);
           page = 0;
         }
-        rows[h] = page * p.pg.page_size + (int)(t - pi * (uint32_t)p.pg.page_size);
+        const int at = (int)(t - pi * (uint32_t)p.pg.page_size);
+        rows[h] = page * p.pg.page_size + at;
+        factor[h] = key_factor(p, page, at, u.g);
+        prefetch_line(p.k + u.g * kD + (int64_t)rows[h] * row_stride);
       }
-      const int8_t* base = p.k + u.g * kD + cl * 16;
-      const uint32_t kb = units & 1u, dst = dst0 + 2 * kb * kTile;
-#pragma unroll 1
-      for (int half = 0; half < 2 && ok; ++half) {
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
         uint4 r[8];
-        const int row = half ? rows[1] : rows[0];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          r[i] = load_once(base + (int64_t)__shfl_sync(0xffffffffu, row, 4 * i + rl) * row_stride);
-        if (half == 0) ok = warp_wait(bar(W_K_EMPTY) + 8u * kb, ((units >> 1) & 1u) ^ 1u, lane, abort_flag, p.err, p.wait_ticks);
+          r[i] = load_once(base + (int64_t)__shfl_sync(0xffffffffu, rows[h], 4 * i + rl) * row_stride);
+        if (h == 0) ok = warp_wait(bar(W_K_EMPTY), (units & 1u) ^ 1u, lane, abort_flag, p.err, p.wait_ticks);
         if (!ok) break;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -466,105 +532,99 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
           i8x4_to_bf16x4(r[i].z, o1.x, o1.y);
           i8x4_to_bf16x4(r[i].w, o1.z, o1.w);
           const uint32_t at = at0 ^ ((uint32_t)(i & 1) << 6);
-          sts128(dst + (32 * half + 4 * i) * 128 + at, o0);
-          sts128(dst + (32 * half + 4 * i) * 128 + (at ^ 16u), o1);
+          sts128(dst + (32 * h + 4 * i) * 128 + at, o0);
+          sts128(dst + (32 * h + 4 * i) * 128 + (at ^ 16u), o1);
         }
+        uint32_t a[3];
+        three_parts(__fdiv_rn(1.f, factor[h]), a);
+        sts128(sbase + OFF_KX + (uint32_t)cw * kSlice + (uint32_t)(32 * h + lane) * 16u,
+               make_uint4(a[0] | a[0] << 16, a[1] | a[0] << 16, a[1] | a[2] << 16, a[1] | a[2] << 16));
       }
       if (!ok) break;
       fence_proxy_async();
-      warp_arrive(W_K_FULL + (int)kb);
+      warp_arrive(W_K_FULL);
       ++units;
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------ sums of exponentials, a key a lane
-    const int h = ((warp - 4) >> 2) & 1, side = (warp - 4) >> 3;   // row tile, half of the columns
-    const int r = ((warp - 4) & 3) * 32 + lane;
-    const uint32_t lane_base = (uint32_t)(((warp - 4) & 3) * 32) << 16;
-    float* const other = reinterpret_cast<float*>(smem + OFF_SUMW) + h * 128 + r;
-    uint32_t units = 0;
-    uint32_t steps = 0;
+    const int x = (warp - 4) >> 2, quarter = (warp - 4) & 3;  // row tile, quarter of its lanes
+    const int r = 128 * x + quarter * 32 + lane;
+    const uint32_t scol = tmem + ((uint32_t)(quarter * 32) << 16) + x * 128;
+    uint32_t done = 0;                                        // steps of this row tile
     bool ok = true;
     while (ok && next_part()) {
       const PartW u = ring[parts % kRingW];
       part_read();
-      const int t = u.tile * kKeysW + h * 128 + r, c = u.nkv - u.nq;
-      const bool valid = t < u.nkv;
-      float f = 0.f;
+      const int t = u.tile * kKeysW + r, c = u.nkv - u.nq;
+      float f;
       {
-        const uint32_t tv = (uint32_t)min(t, u.nkv - 1), pi = divu32(tv, p.pg.div_ps), at = tv - pi * (uint32_t)p.pg.page_size;
+        const uint32_t tv = (uint32_t)min(t, u.nkv - 1), pi = divu32(tv, p.pg.div_ps);
         const int page = __ldg(p.pg.table + (int64_t)u.b * p.pg.max_pages + pi);
-        if ((uint32_t)page < (uint32_t)p.pg.num_pages)         // outside the pool: the keys' loader reports it
-          f = __ldg(p.ks + ((int64_t)page * p.pg.per_page + divu32(at, p.pg.div_block)) * p.pg.Hkv + u.g) * p.sm_log2;
+        f = key_factor(p, page, (int)(tv - pi * (uint32_t)p.pg.page_size), u.g);
       }
-      const int rt0 = first_col_tile(p, SeqW{u.q0, u.nq, u.nkv}, u.tile);
+      const SeqW sq = {u.q0, u.nq, u.nkv};
+      const int rt0 = first_col_tile(p, sq, u.tile), seen = first_of_tile(p, sq, u.tile, x) - rt0;
+      // From step `clear` on all rows see all of the row tile's keys (what lanes behind the context hold is not used); before step
+      // `full` all 128 columns are rows.
+      const int clear = (max(min(u.tile * kKeysW + 128 * x + 128, u.nkv) - 1 - c, 0) + p.P - 1) / p.P - rt0;
+      const int full = p.P * p.G == kCols ? u.nq / p.P - rt0 : 0;
       float total = 0.f, lost = 0.f;                          // the sum, and what its roundings lost (Kahan)
 #pragma unroll 1
-      for (int s = u.s0; s < u.s1; ++s) {
-        const uint32_t st = steps & 1u, par = (steps >> 1) & 1u;
-        ok = warp_wait(bar(W_L_FULL) + 8u * st, par, lane, abort_flag, p.err) &&
-             warp_wait(bar(W_S_FULL) + 8u * st, par, lane, abort_flag, p.err);
+      for (int s = max(u.s0, seen); s < u.s1; ++s) {
+        ok = warp_wait(bar(W_S_FULL) + 8u * x, done & 1u, lane, abort_flag, p.err);
         if (!ok) break;
+        ++done;
         tc_fence_after();
-        const int i0 = (rt0 + s) * p.P, cols = min(p.P, u.nq - i0) * p.G;
-        const int from = valid ? min(max(t - c - i0, 0), kCols) * p.G : kCols;   // the first column that sees this key
-        const uint32_t scol = tmem + lane_base + st * 256 + (uint32_t)h * 128, ls = sbase + OFF_LSE + st * kCols * 4;
-        const int clear = __reduce_max_sync(0xffffffffu, from);              // from here on all of the warp's keys are seen
-        float a0 = 0.f, a1 = 0.f;
+        float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
+        if (s >= clear && s < full) {
+          uint32_t v[CH];
+          LDCH(scol, v);
 #pragma unroll 1
-        for (int k = 64 * side; k < min(cols, 64 * side + 64); k += 32) {
-          uint32_t w[32];
-          FA3_TMEM_LD32(scol + k, w);
-          wait_ld32(w);
-          if (k >= clear && k + 32 <= cols) {
+          for (uint32_t k = CH;; k += CH) {
+            WCH(v);
+            float y[CH];
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const uint4 v = lds128(ls + 4 * (k + e));
-              float x0, x1, x2, x3;
-              fma2(x0, x1, __uint_as_float(w[e]), __uint_as_float(w[e + 1]), f, f, __uint_as_float(v.x), __uint_as_float(v.y));
-              fma2(x2, x3, __uint_as_float(w[e + 2]), __uint_as_float(w[e + 3]), f, f, __uint_as_float(v.z), __uint_as_float(v.w));
-              add2(a0, a1, a0, a1, ex2_approx(x0), ex2_approx(x1));
-              add2(a0, a1, a0, a1, ex2_approx(x2), ex2_approx(x3));
+            for (int e = 0; e < CH; e += 2) mul2(y[e], y[e + 1], __uint_as_float(v[e]), __uint_as_float(v[e + 1]), f, f);
+            if (k < kCols) {
+              LDCH(scol + k, v);
+            } else {
+              tc_fence_before();                              // the scores are all in registers
+              warp_arrive(W_S_EMPTY + x);
             }
-          } else {
-            // the mask also drops what columns without a row hold
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const uint4 v = lds128(ls + 4 * (k + e));
-              const float l[4] = {__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)};
+            for (int e = 0; e < CH; e += 4) {
+              add2(a0, a1, a0, a1, ex2_approx(y[e]), ex2_approx(y[e + 1]));
+              add2(b0, b1, b0, b1, ex2_approx(y[e + 2]), ex2_approx(y[e + 3]));
+            }
+            if (k == kCols) break;
+          }
+        } else {
+          // the first column that sees the key; the mask also drops what columns without a row hold
+          const int i0 = (rt0 + s) * p.P, cols = min(p.P, u.nq - i0) * p.G, from = min(max(t - c - i0, 0), kCols) * p.G;
+#pragma unroll 1
+          for (int k = 0; k < cols; k += 16) {
+            uint32_t v[16];
+            FA3_TMEM_LD16(scol + k, v);
+            wait_ld16(v);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float y = ex2_approx(fmaf(__uint_as_float(w[e + i]), f, l[i]));
-                a0 += k + e + i >= from && k + e + i < cols ? y : 0.f;
-              }
+            for (int e = 0; e < 16; e += 2) {
+              const float y = ex2_approx(__uint_as_float(v[e]) * f), z = ex2_approx(__uint_as_float(v[e + 1]) * f);
+              a0 += k + e >= from && k + e < cols ? y : 0.f;
+              a1 += k + e + 1 >= from && k + e + 1 < cols ? z : 0.f;
             }
           }
+          tc_fence_before();
+          warp_arrive(W_S_EMPTY + x);
         }
-        tc_fence_before();
-        warp_arrive(W_S_EMPTY + (int)st);
-        ++steps;
-        const float y = a0 + a1 - lost, z = total + y;
-        lost = (z - total) - y;
+        const float d = (a0 + a1) + (b0 + b1) - lost, z = total + d;
+        lost = (z - total) - d;
         total = z;
       }
       if (!ok) break;
-      // the two warps of a key meet in shared memory
-      const uint32_t par = units & 1u;
-      ++units;
-      if (side) {
-        ok = warp_wait(bar(W_SUM_EMPTY + h), par ^ 1u, lane, abort_flag, p.err);
-        if (!ok) break;
-        *other = total;
-        warp_arrive(W_SUM_FULL + h);
-        continue;
-      }
-      ok = warp_wait(bar(W_SUM_FULL + h), par, lane, abort_flag, p.err);
-      if (!ok) break;
-      total += *other;
-      warp_arrive(W_SUM_EMPTY + h);
       if (u.s0 == 0 && u.s1 == u.n) {
-        if (valid) add_weight(p, u.b, u.g, t, t >= c, total);
+        if (t < u.nkv) add_weight(p, u.b, u.g, t, t >= c, total);
       } else {
-        p.part[(int64_t)(2 * (int)blockIdx.x + (u.s0 == 0 ? 1 : 0)) * kKeysW + h * 128 + r] = total;
+        p.part[(int64_t)(2 * (int)blockIdx.x + (u.s0 == 0 ? 1 : 0)) * kKeysW + r] = total;
       }
     }
   }
