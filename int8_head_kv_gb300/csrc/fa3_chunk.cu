@@ -88,7 +88,8 @@ constexpr uint32_t OFF_ML = OFF_Q + Q_TILE;                // [2][128] float2: (
                                                            // in the second row tile's place
 constexpr uint32_t OFF_PARTS = OFF_RAW + 2 * RAW_TILE;     // the ring of parts
 constexpr uint32_t kRing = 4, kPartBytes = 48;
-constexpr uint32_t OFF_BAR = OFF_PARTS + kRing * kPartBytes;
+constexpr uint32_t OFF_SCALES = OFF_PARTS + kRing * kPartBytes;   // [2][2][8] float4: a step's scales by groups of 16 keys
+constexpr uint32_t OFF_BAR = OFF_SCALES + 2 * 2 * 8 * 16;
 enum {
   B_K_FULL = 0, B_K_EMPTY = 2, B_V_FULL = 4, B_V_EMPTY = 6,
   B_S_FULL = 8,                    // [2]: buffer x's scores of its next step
@@ -100,9 +101,11 @@ enum {
   B_RAW_EMPTY = 20,                // [2]: int8 K, V tile taken into registers
   B_Q_READY = 22, B_DRAIN = 23,
   B_PART_FULL = 24, B_PART_EMPTY = 28,   // [4]: part of the ring written, read by all
-  B_N = 32
+  B_SC_FULL = 32, B_SC_EMPTY = 36,       // [2][2]: scales of a step of buffer x written, read (block-scaled cache)
+  B_N = 40
 };
-__constant__ const uint8_t kArrivals[B_N] = {2, 2, 1, 1, 2, 2, 1, 1, 1, 1, 4, 4, 1, 1, 4, 4, 4, 4, 1, 1, 2, 2, 8, 1, 1, 1, 1, 1, 14, 14, 14, 14};
+__constant__ const uint8_t kArrivals[B_N] = {2, 2, 1, 1, 2, 2, 1, 1, 1, 1, 4, 4, 1, 1, 4, 4, 4, 4, 1, 1, 2, 2, 8, 1, 1, 1, 1, 1, 14, 14, 14, 14,
+                                             1, 1, 1, 1, 4, 4, 4, 4};
 constexpr uint32_t OFF_TSLOT = OFF_BAR + 8 * B_N;
 constexpr uint32_t OFF_ABORT = OFF_TSLOT + 4;
 constexpr uint32_t SMEM_CHUNK = OFF_ABORT + 4 + 1024;      // + alignment slack
@@ -450,33 +453,36 @@ __device__ __forceinline__ void wait_max(float& a, float& b) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(a), "+f"(b) :: "memory");
 }
 
-// A row of 128 bf16 values as fp16, times a power of two that brings the largest to [2^14, 2^15): exact, but for values
-// below 2^-38 of it.  Writes the chunks of 8 values 2048 bytes apart; returns the inverse of the power.
+// A row of 128 bf16 values as fp16, times a power of two; writes the chunks of 8 values 2048 bytes apart, and returns the power's
+// inverse.  2^6 does for rows whose largest value lies in [2^-6, 2^9): what is rounded is below 2^-25 of it.  Others are read
+// again, times what brings their largest to [2^14, 2^15).  (The row is not held in registers: the softmax loop spilled then, and
+// 4096 rows on 8192 keys took 842 us, and 800 with two readings for all.)
 __device__ __forceinline__ float put_query_row(const uint16_t* row, bool active, uint8_t* dst) {
-  uint4 v[16];
-  uint32_t top = 0;
-#pragma unroll
-  for (int c = 0; c < 16; ++c) v[c] = active ? __ldg(reinterpret_cast<const uint4*>(row) + c) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-  for (int c = 0; c < 16; ++c)
-    top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[c].x & 0x7fff7fffu, v[c].y & 0x7fff7fffu),
-                                 __vmaxu2(v[c].z & 0x7fff7fffu, v[c].w & 0x7fff7fffu)));
-  const uint32_t e = max(max(top & 0xffffu, top >> 16) >> 7, 15u);     // the largest's exponent: 2^(e - 127)
-  const float f = __uint_as_float((268u - e) << 23);
-  auto two = [&](uint32_t w) { return pack_f16x2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f); };
-#pragma unroll
-  for (int c = 0; c < 16; ++c) *reinterpret_cast<uint4*>(dst + c * 2048) = make_uint4(two(v[c].x), two(v[c].y), two(v[c].z), two(v[c].w));
-  return __uint_as_float((e - 14u) << 23);
+  float f = 64.f, inv = 0.015625f;
+#pragma unroll 1
+  for (int pass = 0;; ++pass) {
+    uint32_t top = 0;
+#pragma unroll 4
+    for (int c = 0; c < 16; ++c) {
+      const uint4 v = active ? __ldg(reinterpret_cast<const uint4*>(row) + c) : make_uint4(0u, 0u, 0u, 0u);
+      top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+      auto two = [&](uint32_t w) { return pack_f16x2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f); };
+      *reinterpret_cast<uint4*>(dst + c * 2048) = make_uint4(two(v.x), two(v.y), two(v.z), two(v.w));
+    }
+    const uint32_t e = max(top & 0xffffu, top >> 16) >> 7;   // the largest's exponent: 2^(e - 127)
+    if (pass || !active || (e >= 121u && e < 136u)) return inv;
+    const uint32_t k = max(e, 75u);                          // (a row below 2^-52 counts as that: its scores are nothing either way)
+    f = __uint_as_float((268u - k) << 23);
+    inv = __uint_as_float((k - 14u) << 23);
+  }
 }
 
 // The scales of a key tile's eight groups of 16 keys (a block's keys lie in whole groups), a lane each: lanes 0 .. 7 the
-// keys', 8 .. 15 the values'.  Looked up ahead: the page two tiles, the scale one.
+// keys', 8 .. 15 the values'.
 struct TileScales {
   const int32_t* table;           // the sequence's pages
   const float* pool;
   int n_keys, g;
-  int page;                       // of the tile after the next
-  float next;                     // of the next tile
 };
 __device__ __forceinline__ int scale_token(const TileScales& t, int tile, int lane) {
   return min(tile * kKeys + (lane & 7) * 16, t.n_keys - 1);
@@ -501,12 +507,13 @@ __device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a_tme
       "@e tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], b, %4, p;\n}\n"
       ::"r"(lead), "r"(d), "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(acc), "n"(HI) : "memory");
 }
-// BLOCK: bf16 queries, and scales of keys and values by blocks of tokens.  With l[t] = log2 of token t's value scale, the
+// GROUP > 0: bf16 queries, and scales of keys and values by blocks of tokens.  With l[t] = log2 of token t's value scale, the
 // softmax takes x[t] = s[t] log2(e) + l[t] in place of the score: P = 2^(x - m) are then the weights of V's bare codes, with
 // a maximum of their own, so that P.V needs no scale whatever sizes the blocks' values have, and the row sum, which is
-// of 2^(s log2(e) - m), takes P over the value scale, group by group of 16 keys.
-template <bool BLOCK>
+// of 2^(s log2(e) - m), takes P over the value scale, group by group of GROUP keys (GROUP 0: not such a cache).
+template <int GROUP>
 __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_constant__ ChunkParams p) {
+  constexpr bool BLOCK = GROUP != 0;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -519,8 +526,10 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
                  ::"r"(sbase + OFF_TSLOT), "r"(512) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   } else if (warp == 1) {
-    static_assert(B_N == 32, "a lane a barrier");
-    mbar_init(bar(lane), lane >= B_PART_EMPTY && !p.box ? 13 : kArrivals[lane]);   // without boxes warp 1 has nothing to do
+    static_assert(B_PART_EMPTY + (int)kRing == 32 && B_N == 40, "a lane a barrier, and eight more");
+    // without boxes warp 1 has nothing to do; scales are warp 2's business
+    mbar_init(bar(lane), lane >= B_PART_EMPTY ? (p.box ? 14 : 13) + (BLOCK ? 1 : 0) : kArrivals[lane]);
+    if (BLOCK && lane < B_N - 32) mbar_init(bar(32 + lane), kArrivals[32 + lane]);
     if (lane == 0) *abort_flag = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     if (lane == 0 && p.box) {
@@ -570,6 +579,40 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
     end.nt = -1;
     put(end);
   } else if (warp == 2) {
+    if constexpr (BLOCK) {
+      // ------------------------------------------------------ scales of keys and values, step by step
+      // A group's (key scale, log2 and inverse of the value scale).  A tile's page is looked up two tiles ahead, its scales one.
+      uint32_t done[2] = {0, 0};
+      bool ok = true;
+      while (ok && next_part()) {
+        const Part u = ring[parts % kRing];
+        part_read();
+        const TileScales ts = {p.block_table + (int64_t)u.b * p.max_pages, lane & 8 ? p.vs : p.ks,
+                               p.causal ? u.nkv - u.nq + min(u.nq, (u.rb + 1) * 2 * p.P) : u.nkv, u.g};
+        float next = scale_of(p, ts, scale_page(p, ts, u.t0, lane), u.t0, lane);
+        int page = scale_page(p, ts, u.t0 + 1, lane);
+#pragma unroll 1
+        for (int j = u.t0; j < u.t1 && ok; ++j) {
+          float sc = next;
+          next = scale_of(p, ts, page, j + 1, lane);
+          page = scale_page(p, ts, j + 2, lane);
+          // (a key scale of zero: 2^-60, so that -inf times it, and c, stays -inf)
+          sc = fmaxf(sc, lane & 8 ? kLeastScale : 8.673617379884035e-19f);
+          const float lv = __shfl_down_sync(0xffffffffu, log2f(sc), 8), rv = __shfl_down_sync(0xffffffffu, 1.f / sc, 8);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (!ok || (!u.dual && ((j - u.t0) & 1) != x)) continue;
+            const uint32_t st = done[x] & 1u;
+            ok = warp_wait(bar(B_SC_EMPTY) + 8u * (2 * x + st), ((done[x] >> 1) & 1u) ^ 1u, lane, abort_flag, p.err);
+            if (!ok) continue;
+            if (lane < 8) reinterpret_cast<float4*>(smem + OFF_SCALES)[(2 * x + st) * 8 + lane] = make_float4(sc, lv, rv, 0.f);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_SC_FULL) + 8u * (2 * x + st));
+            ++done[x];
+          }
+        }
+      }
+    }
     if (p.narrow)
       record_cut<uint32_t>(p, s0, blockIdx.x, lane);
     else
@@ -816,19 +859,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
       const bool warp_active = __any_sync(0xffffffffu, active);
       const int64_t orow = (int64_t)(u.q0 + (active ? i : 0)) * p.Hq + hh;   // row of q and out
       auto tile_of = [&](int st) { return u.t0 + (u.dual ? st : 2 * st + x); };
-      TileScales ts;
       float q_inv = 1.f;                                     // BLOCK: a power of two that the row is divided by
-      if constexpr (BLOCK) {
-        ts.table = p.block_table + (int64_t)u.b * p.max_pages;
-        ts.pool = lane & 8 ? p.vs : p.ks;
-        ts.n_keys = p.causal ? u.nkv - u.nq + min(u.nq, (u.rb + 1) * 2 * p.P) : u.nkv;
-        ts.g = u.g;
-        if (mine > 0) {
-          ts.page = scale_page(p, ts, tile_of(0), lane);
-          ts.next = scale_of(p, ts, ts.page, tile_of(0), lane);
-          ts.page = scale_page(p, ts, tile_of(1), lane);
-        }
-      }
       // The row's query codes as fp16 into the row tile's K-major A operand (chunk of 8 d at
       // (d / 8) * 2048 + row * 16).
       if constexpr (BLOCK) {
@@ -857,33 +888,25 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
       const int pos = !active ? -1 : p.causal ? u.nkv - u.nq + i : u.nkv - 1;   // last key this row sees
       const int pos_min = __reduce_min_sync(0xffffffffu, active ? pos : 0x7fffffff);
       // positive, so that -inf * c stays -inf; with a scale of zero every score still rounds to weight 1
-      const float c = BLOCK ? q_inv * p.sm_log2 : active ? fmaxf(p.q_scale[hh] * p.k_scale[u.g] * p.sm_log2, 1e-37f) : 1.f;
+      const float c = BLOCK ? fmaxf(q_inv * p.sm_log2, 8.673617379884035e-19f) : active ? fmaxf(p.q_scale[hh] * p.k_scale[u.g] * p.sm_log2, 1e-37f) : 1.f;
       float m_run = -CUDART_INF_F, l_run = 0.f;
       for (int st = 0; st < mine && ok; ++st) {
         const uint32_t ph = done + (uint32_t)st;
-        if (!warp_wait(bar(B_S_FULL + x), ph & 1u, lane, abort_flag, p.err)) {
+        // (the scales are there long before the scores)
+        if ((BLOCK && !warp_wait(bar(B_SC_FULL) + 8u * (2 * x + (ph & 1u)), (ph >> 1) & 1u, lane, abort_flag, p.err)) ||
+            !warp_wait(bar(B_S_FULL + x), ph & 1u, lane, abort_flag, p.err)) {
           ok = false;
           break;
         }
         if (warp_active) {
           tc_fence_after();
           const int t0 = tile_of(st) * kKeys;                 // the tile's first key
-          float sc = 0.f, sc_inv = 0.f;                      // lanes 0 .. 7: key scale; 8 .. 15: log2 and inverse of the value scale
-          if constexpr (BLOCK) {
-            sc = ts.next;
-            if (st + 1 < mine) {
-              ts.next = scale_of(p, ts, ts.page, tile_of(st + 1), lane);
-              ts.page = scale_page(p, ts, tile_of(st + 2), lane);
-            }
-            if (lane & 8) {
-              sc = fmaxf(sc, kLeastScale);
-              sc_inv = __fdividef(1.f, sc);
-              sc = log2f(sc);
-            }
-          }
-          // factor and summand of group k's scores
-          auto factor = [&](int k) { return fmaxf(__shfl_sync(0xffffffffu, sc, k) * c, 1e-37f); };
-          auto summand = [&](int k) { return __shfl_sync(0xffffffffu, sc, 8 + k); };
+          // factor and summand of group k's scores, and the inverse of its value scale
+          const uint32_t scales = sbase + OFF_SCALES + (2 * x + (ph & 1u)) * 128u;
+          auto group = [&](uint32_t k) {
+            const uint4 v = lds128(scales + 16 * k);
+            return make_float3(__uint_as_float(v.x) * c, __uint_as_float(v.y), __uint_as_float(v.z));
+          };
           if (t0 + kKeys - 1 > pos_min) {
             // some active row of the warp does not see all keys: their scores become -inf
             const int last = pos - t0;
@@ -901,16 +924,26 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
           // the row's maximum of the integer scores
           uint32_t v0[16], v1[16];
           float mx = -CUDART_INF_F;
-          if constexpr (BLOCK) {
+          if constexpr (GROUP == 32) {
+#pragma unroll 1
+            for (uint32_t k = 0; k < 8; k += 2) {
+              uint32_t w[32];
+              float m;
+              tmem_ld_max32(scol + 16 * k, w, m);
+              const float3 f = group(k);
+              wait_max(m);
+              mx = fmaxf(mx, __fmaf_ru(m, f.x, f.y));
+            }
+          } else if constexpr (GROUP == 16) {
 #pragma unroll 1
             for (uint32_t k = 0; k < 8; k += 2) {
               uint32_t w[16];
               float m, m2;
               tmem_ld_max16(scol + 16 * k, w, m);
               tmem_ld_max16(scol + 16 * k + 16, w, m2);
-              const float f = factor(k), f2 = factor(k + 1), a = summand(k), a2 = summand(k + 1);
+              const float3 f = group(k), f2 = group(k + 1);
               wait_max(m, m2);
-              mx = max3(mx, __fmaf_ru(m, f, a), __fmaf_ru(m2, f2, a2));
+              mx = max3(mx, __fmaf_ru(m, f.x, f.y), __fmaf_ru(m2, f2.x, f2.y));
             }
           } else {
 #pragma unroll 1
@@ -955,9 +988,12 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
           // P = exp2(s c - m) as fp16 pairs over the S columns (keys 32 c4 .. 32 c4 + 31 go to columns
           // 16 c4 .. 16 c4 + 15); the row sum takes the weights before the rounding.
           float l0 = 0.f, l1 = 0.f;
-          auto weigh = [&](const uint32_t (&w)[16], uint32_t (&pk)[8], int k) {   // the 16 keys of group k
-            const float f = BLOCK ? factor(k) : c, a = BLOCK ? summand(k) + mc : mc;
-            float g0 = 0.f, g1 = 0.f;
+          // 16 keys of one group; a group's numbers are asked for before the wait for its scores
+          auto ask = [&](int k) { return BLOCK ? group(k) : make_float3(c, 0.f, 0.f); };
+          float g0 = 0.f, g1 = 0.f;
+          auto weigh = [&](const uint32_t (&w)[16], uint32_t (&pk)[8], const float3& s, bool second) {
+            const float f = BLOCK ? s.x : c, a = BLOCK ? s.y + mc : mc, inv = s.z;
+            if (GROUP != 32 || !second) g0 = g1 = 0.f;
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
               float p0, p1;
@@ -970,31 +1006,37 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
                 add2(l0, l1, l0, l1, p0, p1);
               pk[e / 2] = pack_f16x2(p0, p1);
             }
-            if constexpr (BLOCK) l0 = fmaf(g0 + g1, __shfl_sync(0xffffffffu, sc_inv, 8 + k), l0);
+            if (GROUP == 16 || (GROUP == 32 && second)) l0 = fmaf(g0 + g1, inv, l0);
           };
           uint32_t pa[8], pb[8];
+          float3 sa = ask(0), sb = sa;
           wait_ld16(v0);
           FA3_TMEM_LD16(scol + 16, v1);
-          weigh(v0, pa, 0);
+          if (GROUP == 16) sb = ask(1);
+          weigh(v0, pa, sa, false);
 #pragma unroll 1
           for (uint32_t k = 0; k < 96; k += 32) {
             wait_ld16(v1);
             FA3_TMEM_LD16(scol + k + 32, v0);
-            weigh(v1, pb, k / 16 + 1);
+            if (GROUP == 16) sa = ask(k / 16 + 2);
+            weigh(v1, pb, sb, true);
             tmem_st8(scol + k / 2, pa);
+            if (GROUP == 32) sa = sb = ask(k / 16 + 2);
             wait_ld16(v0);
             FA3_TMEM_LD16(scol + k + 48, v1);
-            weigh(v0, pa, k / 16 + 2);
+            if (GROUP == 16) sb = ask(k / 16 + 3);
+            weigh(v0, pa, sa, false);
             tmem_st8(scol + k / 2 + 8, pb);
           }
           wait_ld16(v1);
-          weigh(v1, pb, 7);
+          weigh(v1, pb, sb, true);
           tmem_st8(scol + 48, pa);
           tmem_st8(scol + 56, pb);
           l_run += l0 + l1;
           tmem_wait_st();
           tc_fence_before();
         }
+        if constexpr (BLOCK) warp_arrive(B_SC_EMPTY + 2 * x + (int)(ph & 1u));
         warp_arrive(B_P_FULL + x);
       }
       if (!ok) break;
@@ -1163,6 +1205,19 @@ bool cache_map(CUtensorMap* map, const int8_t* base, int Hkv, int64_t rows, int 
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <int GROUP>
+int launch_chunk(const ChunkParams& p, int sms, cudaStream_t s) {
+  static std::atomic<bool> set[64];                          // the kernel's attribute, once a device
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return FA3_ECUDA;
+  if (dev >= 64 || !set[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(gqa_chunk_kernel<GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_CHUNK) != cudaSuccess)
+      return FA3_ECUDA;
+    if (dev < 64) set[dev].store(true, std::memory_order_release);
+  }
+  return cuda_status(launch_pdl(gqa_chunk_kernel<GROUP>, dim3((unsigned)sms), dim3(kThreadsC), SMEM_CHUNK, s, p));
+}
+
 template <bool BLOCK>
 int chunk_attn(ChunkParams& p, int D, float softmax_scale, void* workspace, size_t workspace_bytes, void* stream) {
   if (!(BLOCK ? (const void*)p.qf : (const void*)p.q) || !p.k || !p.v || !p.q_start || !p.kv_lens || !p.out) return FA3_EINVAL;
@@ -1201,17 +1256,11 @@ int chunk_attn(ChunkParams& p, int D, float softmax_scale, void* workspace, size
   if (p.box < kLeastBox) p.box = 0;
   if (p.box && (!cache_map(&p.map_k, p.k, p.Hkv, cache_rows, p.box) || !cache_map(&p.map_v, p.v, p.Hkv, cache_rows, p.box)))
     return FA3_ECUDA;
-  static std::atomic<bool> set[64];                          // the kernel's attribute, once a device
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return FA3_ECUDA;
-  if (dev >= 64 || !set[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(gqa_chunk_kernel<BLOCK>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_CHUNK) != cudaSuccess)
-      return FA3_ECUDA;
-    if (dev < 64) set[dev].store(true, std::memory_order_release);
-  }
   const LaunchTogether together(s);
-  if (launch_pdl(gqa_chunk_kernel<BLOCK>, dim3((unsigned)sms), dim3(kThreadsC), SMEM_CHUNK, s, p) != cudaSuccess)
-    return FA3_ECUDA;
+  // a block's keys in groups of 32 where its size allows it, of 16 otherwise (4096 rows on 8192 keys, blocks of 128: G32 and G16 us)
+  const int st_main = !BLOCK ? launch_chunk<0>(p, sms, s) : p.page_size / p.per_page % 32 == 0 ? launch_chunk<32>(p, sms, s)
+                                                                                              : launch_chunk<16>(p, sms, s);
+  if (st_main != FA3_OK) return st_main;
   if (sms > 1 && launch_pdl(chunk_combine_kernel<BLOCK>, dim3((unsigned)(sms - 1), (unsigned)(p.rows_max / 32)), dim3(256), 0, s,
                             p) != cudaSuccess)
     return FA3_ECUDA;

@@ -69,10 +69,7 @@ static_assert(SMEM_WEIGHTS <= 232448, "shared memory");
 
 // The line's unit is a step.  kUnitSteps: what a unit costs beside its steps (its keys' way to shared memory); kLeastSteps: the
 // least part of the line a CTA takes, enough for a part inside a unit to hold a step.
-#ifndef KU
-#define KU 2
-#endif
-constexpr int kUnitSteps = KU, kLeastSteps = KU + 2;
+constexpr int kUnitSteps = 2, kLeastSteps = 4;
 static_assert(kLeastSteps > kUnitSteps, "a part inside a unit, behind its fixed cost, holds a step");
 
 struct CutW {
@@ -264,13 +261,6 @@ __device__ __forceinline__ void i8x4_to_bf16x4(uint32_t w, uint32_t& lo, uint32_
   hi = two(__byte_perm(w, 0x43434343u, 0x4342));
 }
 
-__device__ __forceinline__ void wait_ld32(uint32_t* v) {
-  wait_ld16(v);
-  asm volatile("" : "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
-                    "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
-               :: "memory");
-}
-
 // A number as the sum of three bf16 numbers, exactly (24 bits are three times 8; each is the rest's upper half).
 __device__ __forceinline__ void three_parts(float x, uint32_t (&p)[3]) {
 #pragma unroll
@@ -287,16 +277,6 @@ __device__ __forceinline__ float key_factor(const WeightParams& p, int page, int
   return fmaxf(ks * p.sm_log2, 8.673617379884035e-19f);      // 2^-60
 }
 
-#ifndef CH
-#define CH 16
-#endif
-#if CH == 16
-#define LDCH FA3_TMEM_LD16
-#define WCH wait_ld16
-#else
-#define LDCH FA3_TMEM_LD32
-#define WCH wait_ld32
-#endif
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* tm, int c0, int c1, int c2, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
@@ -577,22 +557,22 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
         tc_fence_after();
         float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
         if (s >= clear && s < full) {
-          uint32_t v[CH];
-          LDCH(scol, v);
+          uint32_t v[16];
+          FA3_TMEM_LD16(scol, v);
 #pragma unroll 1
-          for (uint32_t k = CH;; k += CH) {
-            WCH(v);
-            float y[CH];
+          for (uint32_t k = 16;; k += 16) {
+            wait_ld16(v);
+            float y[16];
 #pragma unroll
-            for (int e = 0; e < CH; e += 2) mul2(y[e], y[e + 1], __uint_as_float(v[e]), __uint_as_float(v[e + 1]), f, f);
+            for (int e = 0; e < 16; e += 2) mul2(y[e], y[e + 1], __uint_as_float(v[e]), __uint_as_float(v[e + 1]), f, f);
             if (k < kCols) {
-              LDCH(scol + k, v);
+              FA3_TMEM_LD16(scol + k, v);
             } else {
               tc_fence_before();                              // the scores are all in registers
               warp_arrive(W_S_EMPTY + x);
             }
 #pragma unroll
-            for (int e = 0; e < CH; e += 4) {
+            for (int e = 0; e < 16; e += 4) {
               add2(a0, a1, a0, a1, ex2_approx(y[e]), ex2_approx(y[e + 1]));
               add2(b0, b1, b0, b1, ex2_approx(y[e + 2]), ex2_approx(y[e + 3]));
             }
