@@ -589,6 +589,13 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
         part_read();
         const TileScales ts = {p.block_table + (int64_t)u.b * p.max_pages, lane & 8 ? p.vs : p.ks,
                                p.causal ? u.nkv - u.nq + min(u.nq, (u.rb + 1) * 2 * p.P) : u.nkv, u.g};
+        // The unit's queries into L2: this warp is a few tiles ahead of those that read them.
+        const int i0 = u.rb * 2 * p.P, lines = min(2 * p.P, u.nq - i0) * p.G * 2;
+        for (int k = lane; k < lines; k += 32) {
+          const int at = k / (2 * p.G);
+          prefetch_line(reinterpret_cast<const int8_t*>(p.qf + (int64_t)(u.q0 + i0 + at) * p.q_stride + (int64_t)u.g * p.G * kD) +
+                        (k - at * 2 * p.G) * 128);
+        }
         float next = scale_of(p, ts, scale_page(p, ts, u.t0, lane), u.t0, lane);
         int page = scale_page(p, ts, u.t0 + 1, lane);
 #pragma unroll 1
