@@ -518,8 +518,8 @@ int fa3_cross_attn_gqa(const int8_t* q, const int8_t* k, const int8_t* v,
  *          without a token are not read.
  * weights  float [num_pages][Hkv][page_size]: attention weight gathered by each token.
  * Rows are packed by q_start and kv_lens as for fa3_rope_append_gqa_paged.
- * Supported: block a multiple of 16 up to 4096 that divides page_size; num_pages * page_size and
- *          max_pages * page_size < 2^31; B <= 2^30, Hkv <= 65535.
+ * Supported: block a multiple of 16 up to 4096 that divides page_size; num_pages * page_size < 2^31,
+ *          max_pages * page_size <= 2^31 - 2^16; B <= 2^30, Hkv <= 65535.
  * A sequence with a bad length, or rows outside [0, n), sets FA3_DEVERR_LENS and is left out;
  * if q_start falls anywhere, nothing is written.
  * ------------------------------------------------------------------------ */

@@ -33,8 +33,11 @@ __device__ __forceinline__ uint4 load8(const uint16_t* p, bool wide) {
   const uint2 a = reinterpret_cast<const uint2*>(p)[0], b = reinterpret_cast<const uint2*>(p)[1];
   return make_uint4(a.x, a.y, b.x, b.y);
 }
-// The largest magnitude of 8 bf16 values that are finite, as its 15 bits (their order is the magnitudes').
+// The largest magnitude of 8 bf16 values, as its 15 bits (their order is the magnitudes'); of those that are finite.
 __device__ __forceinline__ uint32_t amax8(uint4 v, uint32_t m) {
+  return __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+}
+__device__ __forceinline__ uint32_t amax8_finite(uint4 v, uint32_t m) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -43,61 +46,144 @@ __device__ __forceinline__ uint32_t amax8(uint4 v, uint32_t m) {
   }
   return m;
 }
+// Codes of eight bf16 values, quant_code's.
+__device__ __noinline__ uint2 codes8_divided(uint4 v, float s) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t c[2] = {0u, 0u};
+#pragma unroll 1
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t x = (e & 4 ? (e & 2 ? w[3] : w[2]) : (e & 2 ? w[1] : w[0])) >> (16 * (e & 1));
+    c[e >> 2] |= ((uint32_t)quant_code(bf16_to_float(x & 0xffffu), s) & 0xffu) << (8 * (e & 3));
+  }
+  return make_uint2(c[0], c[1]);
+}
+// The same where `plain`: s in [2^-100, 2^100], every value finite and at most 127 s in magnitude.  Values next to half
+// steps are no rare case here: with a the block's greatest, x / s = 127 x / a is a half step, but for s's rounding, whenever the
+// eight bits of x and a are such, which a warp's 256 values meet two times in three.  So the float32 quotient itself decides: two
+// corrections of x rs by its residual, which one fused operation gives exactly, round it correctly (Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990; rs is 1 / s rounded correctly), and adding 1.5 2^23
+// rounds it to a whole number, half to even.
+__device__ __forceinline__ uint2 codes8(uint4 v, float s, float rs, bool plain) {
+  if (!plain) return codes8_divided(v, s);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const unsigned long long rs2 = f32x2_pack(rs, rs), s2 = f32x2_pack(-s, -s), one2 = f32x2_pack(1.f, 1.f),
+                           zero2 = f32x2_pack(0.f, 0.f), magic2 = f32x2_pack(kCodeMagic, kCodeMagic);
+  uint32_t q[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const unsigned long long x = f32x2_pack(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+    unsigned long long y = f32x2_fma(x, rs2, zero2);
+    y = f32x2_fma(f32x2_fma(y, s2, x), rs2, y);
+    y = f32x2_fma(f32x2_fma(y, s2, x), rs2, y);
+    float t0, t1;
+    f32x2_unpack(f32x2_fma(y, one2, magic2), t0, t1);
+    q[2 * k] = __float_as_uint(t0);
+    q[2 * k + 1] = __float_as_uint(t1);
+  }
+  return make_uint2(__byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410),
+                    __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410));
+}
 
-// Block (piece, head, k or v).
+// Block (piece, heads, k or v): W warps have a block of tokens of one head.  A thread keeps up to 8 groups of 8 values, in shared
+// memory, so that they are read once where W warps hold a block; larger blocks are read again (from L2).  The loops stay
+// short: with 16 groups in registers and all their code in a row, instructions were what the warps waited for (a ragged batch
+// of 6168 new tokens, 8 heads, blocks of 32: 54 us; 13.1 so).
+constexpr int kHeld = 8, kAsk = 8;
+constexpr int kAppendSmem = kAppendThreads * kHeld * 16;
+template <int W>
 __global__ void __launch_bounds__(kAppendThreads) block_append_kernel(const __grid_constant__ AppendArgs a) {
+  constexpr int kHeads = kAppendThreads / 32 / W;
   __shared__ Piece found;
   __shared__ uint32_t warp_max[kAppendThreads / 32];
+  extern __shared__ uint4 kept[];
   pdl_wait();
   pdl_launch_dependents();
-  const int tid = threadIdx.x, h = blockIdx.y, kv = blockIdx.z;
+  const int warp = threadIdx.x >> 5, kv = blockIdx.z, h = blockIdx.y * kHeads + warp / W;
+  const int tid = threadIdx.x % (32 * W);                    // in the block of tokens
   const Piece p = find_piece(a.q_start, a.kv_lens, a.B, a.n, a.pg.T_max, a.pg.div_block, 2, blockIdx.x,
                              (blockIdx.x | blockIdx.y | blockIdx.z) == 0, a.err, &found);
   if (p.b < 0) return;
-  // Tokens [lo, hi) of the block are new, [blk * block, lo) were there.
+  // Tokens [lo, hi) of the block are new, [base, lo) were there.
   const int start = p.nkv - p.nq, blk = (int)divu32((uint32_t)start, a.pg.div_block) + p.index;
   const int base = blk * a.pg.block, lo = max(base, start), hi = min(base + a.pg.block, p.nkv);
   if (base >= p.nkv) return;
+  const bool mine = h < a.pg.Hkv;
+  const int items = mine ? (hi - lo) * a.chunks : 0;
   const int pi = (int)divu32((uint32_t)base, a.pg.div_ps), page = a.pg.table[(int64_t)p.b * a.pg.max_pages + pi];
+  const uint16_t* x = a.x[kv] + (int64_t)(p.q0 + lo - start) * a.stride[kv] + (int64_t)h * a.D;
+  // A thread's groups are 32 W apart: their offsets go on from one to the next.
+  const int rows_on = (int)divu32(32u * W, a.div_chunks), chunks_on = 32 * W - rows_on * a.chunks;
+  const int row0 = (int)divu32((uint32_t)tid, a.div_chunks), c0 = tid - row0 * a.chunks;
+  struct Walk {
+    int c;
+    int64_t off;
+  };
+  auto begin = [&](int64_t stride) { return Walk{c0, row0 * stride + c0 * 8}; };
+  auto next = [&](Walk& w, int64_t stride) {
+    w.c += chunks_on;
+    w.off += rows_on * stride + chunks_on * 8;
+    if (w.c >= a.chunks) {
+      w.c -= a.chunks;
+      w.off += stride - a.chunks * 8;
+    }
+  };
+  const int64_t x_step = a.stride[kv];
+  const bool wide = a.wide;
+  uint32_t m = 0;
+  Walk in = begin(x_step);
+  int i = tid;
+#pragma unroll 1
+  for (int k = 0; k < kHeld && i < items; k += kAsk) {
+    uint4 v[kAsk];
+#pragma unroll
+    for (int e = 0; e < kAsk; ++e, i += 32 * W) {
+      v[e] = make_uint4(0u, 0u, 0u, 0u);
+      if (i < items) v[e] = load8(x + in.off, wide);
+      next(in, x_step);
+    }
+#pragma unroll
+    for (int e = 0; e < kAsk; ++e) {
+      m = amax8(v[e], m);
+      kept[(k + e) * kAppendThreads + threadIdx.x] = v[e];
+    }
+  }
   if ((uint32_t)page >= (uint32_t)a.pg.num_pages) {
-    if (tid == 0 && h == 0 && kv == 0) set_dev_err(a.err, FA3_DEVERR_PAGE);
+    if (threadIdx.x == 0) set_dev_err(a.err, FA3_DEVERR_PAGE);
     return;
   }
   const int at = base - pi * a.pg.page_size;                 // of the block in its page
-  const int rows = hi - lo, items = rows * a.chunks;
-  const uint16_t* x = a.x[kv] + (int64_t)(p.q0 + lo - start) * a.stride[kv] + (int64_t)h * a.D;
-  constexpr int kHeld = 4;                                   // groups of 8 values that a thread keeps
-  uint4 held[kHeld];
-  uint32_t m = 0;
-#pragma unroll
-  for (int k = 0; k < kHeld; ++k) {
-    const int i = tid + k * kAppendThreads;
-    held[k] = make_uint4(0u, 0u, 0u, 0u);
-    if (i < items) {
-      const int row = (int)divu32((uint32_t)i, a.div_chunks);
-      held[k] = load8(x + row * a.stride[kv] + (i - row * a.chunks) * 8, a.wide);
+  float* scale = a.scale[kv] + ((int64_t)page * a.pg.per_page + (int)divu32((uint32_t)at, a.pg.div_block)) * a.pg.Hkv + (mine ? h : 0);
+  const float before = lo > base ? *scale : 0.f;
+  for (; i < items; i += 32 * W) {
+    m = amax8(load8(x + in.off, wide), m);
+    next(in, x_step);
+  }
+  bool plain = max(m & 0xffffu, m >> 16) < 0x7f80u;
+  if (!plain) {                                              // some value is not finite: again, without those
+    m = 0;
+    in = begin(x_step);
+    for (i = tid; i < items; i += 32 * W) {
+      m = amax8_finite(load8(x + in.off, wide), m);
+      next(in, x_step);
     }
   }
-#pragma unroll
-  for (int k = 0; k < kHeld; ++k) m = amax8(held[k], m);
-  for (int i = tid + kHeld * kAppendThreads; i < items; i += kAppendThreads) {
-    const int row = (int)divu32((uint32_t)i, a.div_chunks);
-    m = amax8(load8(x + row * a.stride[kv] + (i - row * a.chunks) * 8, a.wide), m);
-  }
   m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
-  if ((tid & 31) == 0) warp_max[tid >> 5] = m;
-  float* scale = a.scale[kv] + ((int64_t)page * a.pg.per_page + (int)divu32((uint32_t)at, a.pg.div_block)) * a.pg.Hkv + h;
-  const float before = lo > base ? *scale : 0.f;
-  __syncthreads();
+  if constexpr (W > 1) {
+    if ((threadIdx.x & 31) == 0) warp_max[warp] = m;
+    __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kAppendThreads / 32; ++w) m = max(m, warp_max[w]);
+    for (int w = 0; w < W; ++w) m = max(m, warp_max[warp / W * W + w]);
+  } else {
+    __syncwarp();
+  }
+  if (!mine) return;
   float s = __fdiv_rn(bf16_to_float(m), 127.f);
   int8_t* rows0 = a.cache[kv] + ((int64_t)page * a.pg.page_size + at) * a.pg.Hkv * a.D + (int64_t)h * a.D;   // token `base`
   const int64_t step = (int64_t)a.pg.Hkv * a.D;
   if (lo > base) {
     if (s > before) {
       const float ratio = __fdiv_rn(before, s);
-      for (int i = tid; i < (lo - base) * a.chunks; i += kAppendThreads) {
+      for (int i = tid; i < (lo - base) * a.chunks; i += 32 * W) {
         const int row = (int)divu32((uint32_t)i, a.div_chunks);
         uint2* c = reinterpret_cast<uint2*>(rows0 + row * step + (i - row * a.chunks) * 8);
         const uint2 w = *c;
@@ -107,22 +193,23 @@ __global__ void __launch_bounds__(kAppendThreads) block_append_kernel(const __gr
       s = before;
     }
   }
-  if (tid == 0) *scale = s;                                  // every thread has read it: the barrier above
-  const float rs = rcp_approx(s);
-  const bool exact = exact_scale(s);
+  if (tid == 0) *scale = s;                                  // all have read it: the barrier above
+  const float rs = __fdiv_rn(1.f, s);
+  plain = plain && exact_scale(s);
   int8_t* out = rows0 + (lo - base) * step;
-#pragma unroll
-  for (int k = 0; k < kHeld; ++k) {
-    const int i = tid + k * kAppendThreads;
-    if (i < items) {
-      const int row = (int)divu32((uint32_t)i, a.div_chunks);
-      *reinterpret_cast<uint2*>(out + row * step + (i - row * a.chunks) * 8) = quant_group8(held[k], s, rs, exact);
-    }
+  in = begin(x_step);
+  Walk to = begin(step);
+  i = tid;
+#pragma unroll 2
+  for (int k = 0; k < kHeld; ++k, i += 32 * W) {
+    if (i < items) *reinterpret_cast<uint2*>(out + to.off) = codes8(kept[k * kAppendThreads + threadIdx.x], s, rs, plain);
+    next(in, x_step);
+    next(to, step);
   }
-  for (int i = tid + kHeld * kAppendThreads; i < items; i += kAppendThreads) {
-    const int row = (int)divu32((uint32_t)i, a.div_chunks);
-    const uint4 v = load8(x + row * a.stride[kv] + (i - row * a.chunks) * 8, a.wide);
-    *reinterpret_cast<uint2*>(out + row * step + (i - row * a.chunks) * 8) = quant_group8(v, s, rs, exact);
+  for (; i < items; i += 32 * W) {
+    *reinterpret_cast<uint2*>(out + to.off) = codes8(load8(x + in.off, wide), s, rs, plain);
+    next(in, x_step);
+    next(to, step);
   }
 }
 
@@ -142,7 +229,8 @@ struct EvictArgs {
   int32_t* new_lens;               // [B]
   int32_t* err;
   Pages pg;
-  int B, D, new_pages, budget, sinks, recent, chunks, cached;
+  int B, D, new_pages, budget, sinks, recent, cached;
+  int rows, unit, chunks;          // tokens of a block of evict_move_kernel; bytes it moves at once, how many times a row
   DivU32 div_chunks;
 };
 
@@ -202,20 +290,56 @@ __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_c
     return;
   }
   const int c0 = a.sinks, c1 = T - a.recent, want = a.budget - a.sinks - a.recent;   // want < c1 - c0
-  auto load = [&](int t) -> uint32_t {
-    const uint32_t pi = divu32((uint32_t)t, a.pg.div_ps);
-    int page = a.pg.table[(int64_t)b * a.pg.max_pages + pi];
-    if ((uint32_t)page >= (uint32_t)a.pg.num_pages) {        // outside the pool: any page of it
-      set_dev_err(a.err, FA3_DEVERR_PAGE);
-      page = 0;
+  // kLoads keys a thread on their way at once: a token's page, then its weight
+  constexpr int kLoads = 8;
+  const int32_t* table = a.pg.table + (int64_t)b * a.pg.max_pages;
+  auto load = [&](int t0, int stride, uint32_t (&k)[kLoads]) {
+    int page[kLoads], at[kLoads];
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const uint32_t t = (uint32_t)min(t0 + i * stride, c1 - 1), pi = divu32(t, a.pg.div_ps);
+      page[i] = __ldg(table + pi);
+      at[i] = (int)(t - pi * (uint32_t)a.pg.page_size);
     }
-    return weight_key(a.weights[((int64_t)page * a.pg.Hkv + g) * a.pg.page_size + (t - (int)pi * a.pg.page_size)]);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      if ((uint32_t)page[i] >= (uint32_t)a.pg.num_pages) {   // outside the pool: any page of it
+        bad = true;
+        page[i] = 0;
+      }
+      k[i] = __float_as_uint(a.weights[((int64_t)page[i] * a.pg.Hkv + g) * a.pg.page_size + at[i]]);
+    }
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) k[i] = weight_key(__uint_as_float(k[i]));
+    if (bad) set_dev_err(a.err, FA3_DEVERR_PAGE);
   };
   const bool cached = c1 - c0 <= a.cached;
   if (cached) {
-    for (int t = c0 + tid; t < c1; t += kPickThreads) keys[t - c0] = load(t);
+    for (int t = c0 + tid; t < c1; t += kLoads * kPickThreads) {
+      uint32_t k[kLoads];
+      load(t, kPickThreads, k);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        if (t + i * kPickThreads < c1) keys[t + i * kPickThreads - c0] = k[i];
+    }
+    __syncthreads();
   }
-  auto key = [&](int t) { return cached ? keys[t - c0] : load(t); };
+  // calls use(position, key) for all of this thread's tokens t0, t0 + stride, .. below t1; the warp's lanes have as many
+  auto each = [&](int t0, int stride, int t1, auto use) {
+    for (int t = t0; t - lane < t1; t += kLoads * stride) {
+      uint32_t k[kLoads];
+      if (cached) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) k[i] = keys[min(t + i * stride, c1 - 1) - c0];
+      } else {
+        load(t, stride, k);
+      }
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        if (t - lane + i * stride < t1) use(t + i * stride, t + i * stride < t1, k[i]);
+    }
+  };
   // The want-th greatest key, digit by digit from the top: `above` keys are greater than every one with these digits.
   uint32_t prefix = 0, need = (uint32_t)want;
   int shift = 32;
@@ -223,10 +347,18 @@ __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_c
     const int bits = min(kDigitBits, shift), rest = shift - bits;
     for (int i = tid; i < kBins; i += kPickThreads) bins[i] = 0;
     __syncthreads();
-    for (int t = c0 + tid; t < c1; t += kPickThreads) {
-      const uint32_t k = key(t);
-      if (shift == 32 || k >> shift == prefix) atomicAdd(&bins[(k >> rest) & ((1u << bits) - 1u)], 1u);
-    }
+    each(c0 + tid, kPickThreads, c1, [&](int, bool in, uint32_t k) {
+      const bool counts = in && (shift == 32 || k >> shift == prefix);
+      const uint32_t bin = (k >> rest) & ((1u << bits) - 1u);
+      // tokens that nothing looked at, or equally little, are many: lanes with the first one's bin are counted at once
+      const uint32_t all = __ballot_sync(0xffffffffu, counts);
+      if (all) {
+        const uint32_t first = __shfl_sync(0xffffffffu, bin, __ffs(all) - 1);
+        const uint32_t same = __ballot_sync(0xffffffffu, counts && bin == first);
+        if (counts && bin != first) atomicAdd(&bins[bin], 1u);
+        if (lane == 0) atomicAdd(&bins[first], (uint32_t)__popc(same));
+      }
+    });
     __syncthreads();
     // a thread has two bins, the greatest first
     const int hi = kBins - 1 - 2 * tid;
@@ -247,100 +379,124 @@ __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_c
   const int count = c1 - c0, per = ((count + kPickThreads - 1) / kPickThreads) * 32;
   const int w0 = c0 + (int)min((int64_t)count, (int64_t)warp * per), w1 = c0 + (int)min((int64_t)count, (int64_t)(warp + 1) * per);
   uint32_t more = 0, same = 0;
-  for (int t0 = w0; t0 < w1; t0 += 32) {
-    const uint32_t k = t0 + lane < w1 ? key(t0 + lane) : 0u;
-    more += __popc(__ballot_sync(0xffffffffu, t0 + lane < w1 && want > 0 && k > prefix));
-    same += __popc(__ballot_sync(0xffffffffu, t0 + lane < w1 && want > 0 && k == prefix));
-  }
+  each(w0 + lane, 32, w1, [&](int, bool in, uint32_t k) {
+    more += __popc(__ballot_sync(0xffffffffu, in && want > 0 && k > prefix));
+    same += __popc(__ballot_sync(0xffffffffu, in && want > 0 && k == prefix));
+  });
   uint32_t total;
   const uint32_t same_before = __shfl_sync(0xffffffffu, block_scan(lane == 0 ? same : 0u, tmp, &total), 0);
   const uint32_t take = same_before >= need ? 0u : min(same, need - same_before);
   const uint32_t before = __shfl_sync(0xffffffffu, block_scan(lane == 0 ? more + take : 0u, tmp, &total), 0);
   uint32_t at = before, seen = same_before;
-  for (int t0 = w0; t0 < w1; t0 += 32) {
-    const bool in = t0 + lane < w1 && want > 0;
-    const uint32_t k = in ? key(t0 + lane) : 0u;
+  each(w0 + lane, 32, w1, [&](int t, bool in, uint32_t k) {
+    in = in && want > 0;
     const uint32_t eq = __ballot_sync(0xffffffffu, in && k == prefix), below = (1u << lane) - 1u;
     const bool stays = in && (k > prefix || (k == prefix && seen + __popc(eq & below) < need));
     const uint32_t all = __ballot_sync(0xffffffffu, stays);
-    if (stays) kept[a.sinks + at + __popc(all & below)] = t0 + lane;
+    if (stays) kept[a.sinks + at + __popc(all & below)] = t;
     at += __popc(all);
     seen += __popc(eq);
-  }
+  });
   for (int i = tid; i < a.sinks; i += kPickThreads) kept[i] = i;
   for (int i = tid; i < a.recent; i += kPickThreads) kept[a.budget - a.recent + i] = c1 + i;
 }
 
-constexpr int kMoveThreads = 128;
+constexpr int kMoveThreads = 256;
 
-// Block (destination block, head, sequence): its tokens' codes, at the greatest of their scales, and weights.
+// Block (rows, head, sequence): `rows` tokens of the new context, whole blocks of it, as codes at the greatest of their block's
+// scales, and their weights.  A thread's pieces, of 16 bytes where rows allow it, are on their way at once and while the
+// scales are found.
+template <class V>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs a) {
-  extern __shared__ int64_t src_row[];                       // [block], then float ratio[2][block]
-  float* ratio = reinterpret_cast<float*>(src_row + a.pg.block);
-  __shared__ float warp_max[2][kMoveThreads / 32];
+  // per token: row in the old pages and in the new ones (head rows; -1: no such page), scales of k and v; per block: their greatest
+  extern __shared__ int64_t src_row[];
+  int64_t* const dst_row = src_row + a.rows;
+  float* const scale = reinterpret_cast<float*>(dst_row + a.rows);
+  int* const most = reinterpret_cast<int*>(scale + 2 * a.rows);
   pdl_wait();
   pdl_launch_dependents();
-  const int tid = threadIdx.x, g = blockIdx.y, b = blockIdx.z, bs = a.pg.block;
+  const int tid = threadIdx.x, g = blockIdx.y, b = blockIdx.z, blocks = a.rows / a.pg.block;
   const int T = a.kv_lens[b];
   if (T < 0 || T > a.pg.T_max) return;
-  const int left = min(T, a.budget), base = blockIdx.x * bs, rows = min(bs, left - base);
+  const int base = blockIdx.x * a.rows, rows = min(a.rows, min(T, a.budget) - base);
   if (rows <= 0) return;
-  const int pi = (int)divu32((uint32_t)base, a.pg.div_ps), page = a.new_table[(int64_t)b * a.new_pages + pi];
-  if ((uint32_t)page >= (uint32_t)a.pg.num_pages) {
-    if (tid == 0) set_dev_err(a.err, FA3_DEVERR_PAGE);
-    return;
-  }
-  const int at = base - pi * a.pg.page_size;
   const int32_t* kept = a.kept + ((int64_t)b * a.pg.Hkv + g) * a.budget + base;
-  const int64_t to = ((int64_t)page * a.pg.page_size + at) * a.pg.Hkv + g;             // in head rows
-  float m[2] = {0.f, 0.f};
+  for (int i = tid; i < 2 * blocks; i += kMoveThreads) most[i] = 0;
+  float s[2] = {0.f, 0.f};
   for (int i = tid; i < rows; i += kMoveThreads) {
     const int t = kept[i];
-    const uint32_t sp = divu32((uint32_t)t, a.pg.div_ps);
-    int from = a.pg.table[(int64_t)b * a.pg.max_pages + sp];
-    if ((uint32_t)from >= (uint32_t)a.pg.num_pages) {
+    const uint32_t sp = divu32((uint32_t)t, a.pg.div_ps), dp = divu32((uint32_t)(base + i), a.pg.div_ps);
+    int from = __ldg(a.pg.table + (int64_t)b * a.pg.max_pages + sp);
+    const int to = __ldg(a.new_table + (int64_t)b * a.new_pages + dp);
+    if ((uint32_t)from >= (uint32_t)a.pg.num_pages) {        // outside the pool: any page of it
       set_dev_err(a.err, FA3_DEVERR_PAGE);
       from = 0;
     }
-    const int in = t - (int)sp * a.pg.page_size;
+    const bool lost = (uint32_t)to >= (uint32_t)a.pg.num_pages;
+    if (lost) set_dev_err(a.err, FA3_DEVERR_PAGE);
+    const int in = t - (int)sp * a.pg.page_size, at = base + i - (int)dp * a.pg.page_size;
     src_row[i] = ((int64_t)from * a.pg.page_size + in) * a.pg.Hkv + g;
-    a.weights[((int64_t)page * a.pg.Hkv + g) * a.pg.page_size + at + i] =
-        a.weights[((int64_t)from * a.pg.Hkv + g) * a.pg.page_size + in];
+    dst_row[i] = lost ? -1 : ((int64_t)to * a.pg.page_size + at) * a.pg.Hkv + g;
+    const float w = a.weights[((int64_t)from * a.pg.Hkv + g) * a.pg.page_size + in];
     const int64_t sc = ((int64_t)from * a.pg.per_page + (int)divu32((uint32_t)in, a.pg.div_block)) * a.pg.Hkv + g;
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      const float s = a.scale[kv][sc];
-      ratio[kv * bs + i] = s;
-      m[kv] = fmaxf(m[kv], s);
-    }
-  }
-#pragma unroll
-  for (int kv = 0; kv < 2; ++kv) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m[kv] = fmaxf(m[kv], __shfl_xor_sync(0xffffffffu, m[kv], o));
-    if ((tid & 31) == 0) warp_max[kv][tid >> 5] = m[kv];
+    s[0] = a.scale[0][sc];
+    s[1] = a.scale[1][sc];
+    scale[i] = s[0];
+    scale[a.rows + i] = s[1];
+    if (!lost) a.weights[((int64_t)to * a.pg.Hkv + g) * a.pg.page_size + at] = w;
   }
   __syncthreads();
-#pragma unroll
-  for (int kv = 0; kv < 2; ++kv) {
-#pragma unroll
-    for (int w = 0; w < kMoveThreads / 32; ++w) m[kv] = fmaxf(m[kv], warp_max[kv][w]);
-    if (tid == 0)
-      a.scale[kv][((int64_t)page * a.pg.per_page + (int)divu32((uint32_t)at, a.pg.div_block)) * a.pg.Hkv + g] = m[kv];
-    for (int i = tid; i < rows; i += kMoveThreads) {
-      const float s = ratio[kv * bs + i];
-      ratio[kv * bs + i] = s == m[kv] ? 1.f : __fdiv_rn(s, m[kv]);   // 0 / 0 with it
-    }
-  }
-  __syncthreads();
+  // the first pieces are asked for; scales are not negative, so their bits are in their order
+  constexpr int kLoads = 4;
   const int items = rows * a.chunks;
-  for (int j = tid; j < 2 * items; j += kMoveThreads) {
-    const int kv = j >= items, i = j - kv * items;
-    const int row = (int)divu32((uint32_t)i, a.div_chunks), c = (i - row * a.chunks) * 8;
-    uint2 w = *reinterpret_cast<const uint2*>(a.cache[kv] + src_row[row] * a.D + c);
-    const float r = ratio[kv * bs + row];
-    if (r != 1.f) w = make_uint2(rescaled(w.x, r), rescaled(w.y, r));
-    *reinterpret_cast<uint2*>(a.cache[kv] + (to + (int64_t)row * a.pg.Hkv) * a.D + c) = w;
+  auto where = [&](int j, int& kv, int& row, int& c) {
+    kv = j >= items;
+    const int i = j - kv * items;
+    row = (int)divu32((uint32_t)i, a.div_chunks);
+    c = (i - row * a.chunks) * (int)sizeof(V);
+  };
+  auto load = [&](int j, V (&v)[kLoads]) {
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+      int kv, row, c;
+      where(min(j + k * kMoveThreads, 2 * items - 1), kv, row, c);
+      v[k] = __ldcs(reinterpret_cast<const V*>(a.cache[kv] + src_row[row] * a.D + c));
+    }
+  };
+  V v[kLoads];
+  load(tid, v);
+  for (int i = tid; i < rows; i += kMoveThreads) {
+    const int blk = (int)divu32((uint32_t)i, a.pg.div_block);
+    atomicMax(&most[blk], __float_as_int(scale[i]));
+    atomicMax(&most[blocks + blk], __float_as_int(scale[a.rows + i]));
+  }
+  __syncthreads();
+  for (int i = tid; i < 2 * rows; i += kMoveThreads) {
+    const int kv = i >= rows, row = i - kv * rows, blk = (int)divu32((uint32_t)row, a.pg.div_block);
+    const float old = scale[kv * a.rows + row], now = __int_as_float(most[kv * blocks + blk]);
+    scale[kv * a.rows + row] = old == now ? 1.f : __fdiv_rn(old, now);   // 0 / 0 with it
+    if (row == blk * a.pg.block && dst_row[row] >= 0) {
+      const uint32_t dp = divu32((uint32_t)(base + row), a.pg.div_ps);
+      const int at = base + row - (int)dp * a.pg.page_size, to = a.new_table[(int64_t)b * a.new_pages + dp];
+      a.scale[kv][((int64_t)to * a.pg.per_page + (int)divu32((uint32_t)at, a.pg.div_block)) * a.pg.Hkv + g] = now;
+    }
+  }
+  __syncthreads();
+  for (int j = tid; j < 2 * items; j += kLoads * kMoveThreads) {
+    if (j != tid) load(j, v);
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+      if (j + k * kMoveThreads >= 2 * items) break;
+      int kv, row, c;
+      where(j + k * kMoveThreads, kv, row, c);
+      const float r = scale[kv * a.rows + row];
+      uint32_t* w = reinterpret_cast<uint32_t*>(&v[k]);
+      if (r != 1.f) {
+#pragma unroll
+        for (int e = 0; e < (int)sizeof(V) / 4; ++e) w[e] = rescaled(w[e], r);
+      }
+      if (dst_row[row] >= 0) *reinterpret_cast<V*>(a.cache[kv] + dst_row[row] * a.D + c) = v[k];
+    }
   }
 }
 
@@ -374,7 +530,14 @@ FA3_API int fa3_append_gqa_block_paged(const uint16_t* k, const uint16_t* v, int
   a.q_start = q_start; a.kv_lens = kv_lens; a.err = dev_err; a.n = n; a.B = B; a.D = D; a.chunks = D / 8;
   a.wide = aligned16(k) && aligned16(v) && k_stride % 8 == 0 && v_stride % 8 == 0;
   a.div_chunks = make_divu32((uint32_t)a.chunks);
-  return cuda_status(launch_pdl(block_append_kernel, dim3((unsigned)pieces, (unsigned)Hkv, 2), dim3(kAppendThreads), 0,
+  // as many warps a block of tokens as hold it
+  const int warps = kAppendThreads / 32, need = (block * a.chunks + 32 * kHeld - 1) / (32 * kHeld);
+  const int W = need <= 1 ? 1 : need <= 2 ? 2 : need <= 4 ? 4 : 8;
+  auto* kernel = W == 1 ? block_append_kernel<1> : W == 2 ? block_append_kernel<2> : W == 4 ? block_append_kernel<4>
+                                                                                            : block_append_kernel<8>;
+  const int heads = warps / W;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAppendSmem) != cudaSuccess) return FA3_ECUDA;
+  return cuda_status(launch_pdl(kernel, dim3((unsigned)pieces, (unsigned)((Hkv + heads - 1) / heads), 2), dim3(kAppendThreads), kAppendSmem,
                                 static_cast<cudaStream_t>(stream), a));
 }
 
@@ -397,18 +560,23 @@ FA3_API int fa3_evict_gqa_block_paged(int8_t* k_cache, int8_t* v_cache, float* k
   if (st != FA3_OK) return st;
   a.cache[0] = k_cache; a.cache[1] = v_cache; a.scale[0] = k_scale; a.scale[1] = v_scale; a.weights = weights;
   a.kv_lens = kv_lens; a.new_table = new_table; a.kept = kept; a.new_lens = new_lens; a.err = dev_err;
-  a.B = B; a.D = D; a.new_pages = new_pages; a.budget = budget; a.sinks = sinks; a.recent = recent; a.chunks = D / 8;
+  a.B = B; a.D = D; a.new_pages = new_pages; a.budget = budget; a.sinks = sinks; a.recent = recent;
+  const bool wide = D % 16 == 0 && aligned16(k_cache) && aligned16(v_cache);
+  a.unit = wide ? 16 : 8;
+  a.chunks = D / a.unit;
   a.div_chunks = make_divu32((uint32_t)a.chunks);
+  a.rows = block * std::max(1, 64 / block);                  // 64 tokens or one block
   a.cached = std::min(a.pg.T_max, 48 * 1024);
   const int smem = a.cached * 4;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const auto move = wide ? evict_move_kernel<uint4> : evict_move_kernel<uint2>;
+  const int move_smem = a.rows * 24 + a.rows / block * 8;
   if (cudaFuncSetAttribute(evict_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 48 * 1024 * 4) != cudaSuccess ||
-      cudaFuncSetAttribute(evict_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4096 * 16) != cudaSuccess)
+      cudaFuncSetAttribute(move, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostBlock * 24 + 8) != cudaSuccess)
     return FA3_ECUDA;
   const LaunchTogether together(s);
   if (launch_pdl(evict_pick_kernel, dim3((unsigned)Hkv, (unsigned)B), dim3(kPickThreads), (size_t)smem, s, a) != cudaSuccess)
     return FA3_ECUDA;
-  const unsigned blocks = (unsigned)((budget + block - 1) / block);
-  return cuda_status(launch_pdl(evict_move_kernel, dim3(blocks, (unsigned)Hkv, (unsigned)B), dim3(kMoveThreads),
-                                (size_t)block * 16, s, a));
+  const unsigned blocks = (unsigned)((budget + a.rows - 1) / a.rows);
+  return cuda_status(launch_pdl(move, dim3(blocks, (unsigned)Hkv, (unsigned)B), dim3(kMoveThreads), (size_t)move_smem, s, a));
 }

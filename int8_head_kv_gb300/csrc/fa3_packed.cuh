@@ -25,7 +25,9 @@ inline int pages_of(const int32_t* table, int B, int Hkv, int num_pages, int pag
   if (!table || B <= 0 || Hkv <= 0 || num_pages <= 0 || page_size <= 0 || max_pages <= 0 || block <= 0) return FA3_EINVAL;
   if (page_size % block != 0) return FA3_EINVAL;
   if (block % kLeastBlock != 0 || block > kMostBlock || B > kMostSequences || Hkv > 65535) return FA3_ERANGE;
-  if ((int64_t)max_pages * page_size >= ((int64_t)1 << 31) || (int64_t)num_pages * page_size >= ((int64_t)1 << 31)) return FA3_ERANGE;
+  // (kernels look some tokens behind a context's last in 32-bit numbers)
+  if ((int64_t)max_pages * page_size > ((int64_t)1 << 31) - 65536 || (int64_t)num_pages * page_size >= ((int64_t)1 << 31))
+    return FA3_ERANGE;
   *p = Pages{table, max_pages, num_pages, page_size, max_pages * page_size, block, page_size / block, Hkv,
              make_divu32((uint32_t)page_size), make_divu32((uint32_t)block)};
   return FA3_OK;

@@ -178,6 +178,27 @@ def test_append_token_by_token_and_values_at_half_steps():
     assert _same(got, state)
 
 
+def test_append_codes_of_every_pair_of_mantissas():
+    """Eight-bit mantissas against a block's eight-bit greatest: 127 x / a is a half step for many, and what the rounding
+    of the scale makes of it decides."""
+    F = fa3()
+    c = _cache(np.random.default_rng(8), [5], 16, 16, 128, 256)
+    m = np.arange(128, 256) / 128.0
+    val = np.concatenate([m * 2.0 ** -e for e in range(10)])          # 1280 values a head, 5 tokens of 256
+    x = np.broadcast_to(val, (128, 1280)).copy()
+    x[np.broadcast_to(x[:, :128] > m[:, None], (128, 128)).nonzero()] /= 2   # none above the head's greatest
+    x[:, ::3] *= -1
+    x[np.arange(128), np.arange(128)] = m
+    k = x.reshape(128, 5, 256).transpose(1, 0, 2).astype(np.float32)
+    assert np.array_equal(_f(_bf(k)), k)
+    for up in (1.0, 2.0 ** 20, 2.0 ** -40):
+        ref = O.append_block_paged(k * np.float32(up), k[::-1] * np.float32(up), c["k"], c["v"], c["ks"], c["vs"], c["table"], [0, 5], [5])
+        got = [_t(c[y]) for y in ("k", "v", "ks", "vs")]
+        F.append_gqa_block_paged(_bf(k * up).cuda(), _bf(k[::-1] * up).cuda(), *got, _t(c["table"]), _t(np.array([0, 5], np.int32)),
+                                 _t(c["kv_lens"]))
+        assert _same(got, ref)
+
+
 @pytest.mark.parametrize("old", [False, True])
 def test_append_zero_tiny_and_not_finite_values(old):
     F, rng = fa3(), np.random.default_rng(6)
