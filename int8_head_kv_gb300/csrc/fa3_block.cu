@@ -218,6 +218,7 @@ __global__ void __launch_bounds__(kAppendThreads) block_append_kernel(const __gr
 // greatest weights, the earliest of equal ones, up to `budget` in all; a context that fits the budget stays whole.
 constexpr int kPickThreads = 1024;
 constexpr int kDigitBits = 11, kBins = 1 << kDigitBits;
+constexpr int kMostKeys = 48 * 1024;                       // of a context that shared memory holds
 
 struct EvictArgs {
   int8_t* cache[2];
@@ -270,12 +271,13 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* tmp, uint32
 }
 
 // Block (head, sequence): the tokens that stay, in order, to `kept`.
+constexpr int kFewKeys = 4096;
 __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_constant__ EvictArgs a) {
-  extern __shared__ uint32_t keys[];                         // of the whole context, where they fit
-  __shared__ uint32_t bins[kBins], tmp[33], found[2];
+  extern __shared__ __align__(16) uint32_t keys[];           // of all tokens that are chosen from, where they fit
+  __shared__ uint32_t bins[kBins], tmp[33], found[2], few[kFewKeys], n_few;
   pdl_wait();
   pdl_launch_dependents();
-  const int tid = threadIdx.x, g = blockIdx.x, b = blockIdx.y, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, g = blockIdx.x, b = blockIdx.y;
   const int T = a.kv_lens[b];
   int32_t* kept = a.kept + ((int64_t)b * a.pg.Hkv + g) * a.budget;
   if (T < 0 || T > a.pg.T_max) {
@@ -289,76 +291,118 @@ __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_c
     for (int i = tid; i < T; i += kPickThreads) kept[i] = i;
     return;
   }
+  for (int i = tid; i < a.sinks; i += kPickThreads) kept[i] = i;
+  for (int i = tid; i < a.recent; i += kPickThreads) kept[a.budget - a.recent + i] = T - a.recent + i;
   const int c0 = a.sinks, c1 = T - a.recent, want = a.budget - a.sinks - a.recent;   // want < c1 - c0
-  // kLoads keys a thread on their way at once: a token's page, then its weight
-  constexpr int kLoads = 8;
+  if (want == 0) return;
+  // Tokens go by fours, which lie in one page: group q holds tokens base + 4 q .. + 3, with key 0, which no weight has, outside
+  // [c0, c1).  kLoads groups a thread are on their way at once.
+  constexpr int kLoads = 4;
+  const int base = c0 & ~3, groups = (c1 - base + 3) >> 2;
   const int32_t* table = a.pg.table + (int64_t)b * a.pg.max_pages;
-  auto load = [&](int t0, int stride, uint32_t (&k)[kLoads]) {
-    int page[kLoads], at[kLoads];
+  auto load = [&](int q0, int stride, uint4 (&k)[kLoads]) {
+    int page[kLoads];
+    uint32_t t[kLoads];
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const uint32_t t = (uint32_t)min(t0 + i * stride, c1 - 1), pi = divu32(t, a.pg.div_ps);
-      page[i] = __ldg(table + pi);
-      at[i] = (int)(t - pi * (uint32_t)a.pg.page_size);
+      t[i] = (uint32_t)(base + 4 * min(q0 + i * stride, groups - 1));
+      page[i] = __ldg(table + divu32(t[i], a.pg.div_ps));
     }
+    float4 w[kLoads];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       if ((uint32_t)page[i] >= (uint32_t)a.pg.num_pages) {   // outside the pool: any page of it
         bad = true;
         page[i] = 0;
       }
-      k[i] = __float_as_uint(a.weights[((int64_t)page[i] * a.pg.Hkv + g) * a.pg.page_size + at[i]]);
+      const int at = (int)(t[i] - divu32(t[i], a.pg.div_ps) * (uint32_t)a.pg.page_size);
+      w[i] = *reinterpret_cast<const float4*>(a.weights + ((int64_t)page[i] * a.pg.Hkv + g) * a.pg.page_size + at);
     }
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) k[i] = weight_key(__uint_as_float(k[i]));
+    for (int i = 0; i < kLoads; ++i) {
+      auto in = [&](int e, float x) {
+        const int u = (int)t[i] + e;
+        return u >= c0 && u < c1 ? weight_key(x) : 0u;
+      };
+      k[i] = make_uint4(in(0, w[i].x), in(1, w[i].y), in(2, w[i].z), in(3, w[i].w));
+    }
     if (bad) set_dev_err(a.err, FA3_DEVERR_PAGE);
   };
-  const bool cached = c1 - c0 <= a.cached;
-  if (cached) {
-    for (int t = c0 + tid; t < c1; t += kLoads * kPickThreads) {
-      uint32_t k[kLoads];
-      load(t, kPickThreads, k);
+  const bool cached = 4 * groups <= a.cached;
+  uint4* const keys4 = reinterpret_cast<uint4*>(keys);
+  // A thread's run of groups (an odd number of them: eight threads' groups then lie in different banks).
+  const int per = ((groups + kPickThreads - 1) / kPickThreads) | 1;
+  const int g0 = (int)min((int64_t)groups, (int64_t)tid * per), g1 = (int)min((int64_t)groups, (int64_t)tid * per + per);
+  // calls use(group, its keys) for this thread's run, in order
+  auto run = [&](auto use) {
+    if (cached) {
+      for (int q = g0; q < g1; ++q) use(q, keys4[q]);
+    } else {
+      for (int q = g0; q < g1; q += kLoads) {
+        uint4 k[kLoads];
+        load(q, 1, k);
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i)
-        if (t + i * kPickThreads < c1) keys[t + i * kPickThreads - c0] = k[i];
-    }
-    __syncthreads();
-  }
-  // calls use(position, key) for all of this thread's tokens t0, t0 + stride, .. below t1; the warp's lanes have as many
-  auto each = [&](int t0, int stride, int t1, auto use) {
-    for (int t = t0; t - lane < t1; t += kLoads * stride) {
-      uint32_t k[kLoads];
-      if (cached) {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) k[i] = keys[min(t + i * stride, c1 - 1) - c0];
-      } else {
-        load(t, stride, k);
+        for (int i = 0; i < kLoads; ++i)
+          if (q + i < g1) use(q + i, k[i]);
       }
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i)
-        if (t - lane + i * stride < t1) use(t + i * stride, t + i * stride < t1, k[i]);
     }
   };
-  // The want-th greatest key, digit by digit from the top: `above` keys are greater than every one with these digits.
+  auto four = [](uint4 k, auto use) {
+    use(0, k.x);
+    use(1, k.y);
+    use(2, k.z);
+    use(3, k.w);
+  };
+  // The want-th greatest key, digit by digit from the top.  Behind the first digit few keys are left as a rule, which are put aside.
   uint32_t prefix = 0, need = (uint32_t)want;
-  int shift = 32;
-  while (shift > 0 && want > 0) {
+  bool aside = false;
+  if (tid == 0) n_few = 0;
+#pragma unroll 1
+  for (int shift = 32; shift > 0;) {
     const int bits = min(kDigitBits, shift), rest = shift - bits;
+    const uint32_t mask = (1u << bits) - 1u;
     for (int i = tid; i < kBins; i += kPickThreads) bins[i] = 0;
     __syncthreads();
-    each(c0 + tid, kPickThreads, c1, [&](int, bool in, uint32_t k) {
-      const bool counts = in && (shift == 32 || k >> shift == prefix);
-      const uint32_t bin = (k >> rest) & ((1u << bits) - 1u);
-      // tokens that nothing looked at, or equally little, are many: lanes with the first one's bin are counted at once
-      const uint32_t all = __ballot_sync(0xffffffffu, counts);
-      if (all) {
-        const uint32_t first = __shfl_sync(0xffffffffu, bin, __ffs(all) - 1);
-        const uint32_t same = __ballot_sync(0xffffffffu, counts && bin == first);
-        if (counts && bin != first) atomicAdd(&bins[bin], 1u);
-        if (lane == 0) atomicAdd(&bins[first], (uint32_t)__popc(same));
+    if (shift == 32) {
+      // tokens that nothing looked at are many: counted by the thread
+      constexpr uint32_t kZero = 0x80000000u;
+      uint32_t zeros = 0;
+      for (int q = tid; q < groups; q += kLoads * kPickThreads) {
+        uint4 k[kLoads];
+        load(q, kPickThreads, k);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          if (q + i * kPickThreads < groups) {
+            if (cached) keys4[q + i * kPickThreads] = k[i];
+            four(k[i], [&](int, uint32_t x) {
+              if (x == kZero) ++zeros; else if (x) atomicAdd(&bins[x >> rest], 1u);
+            });
+          }
+        }
       }
-    });
+      zeros = __reduce_add_sync(0xffffffffu, zeros);
+      if (lane == 0 && zeros) atomicAdd(&bins[kZero >> rest], zeros);
+    } else if (aside) {
+      const int n = (int)n_few;
+      for (int i = tid; i < n; i += kPickThreads)
+        if (few[i] >> shift == prefix) atomicAdd(&bins[(few[i] >> rest) & mask], 1u);
+    } else {
+      // all keys again: many are equal then, and equal neighbours are counted by the thread
+      uint32_t last = 0, times = 0;
+      run([&](int, uint4 k) {
+        four(k, [&](int, uint32_t x) {
+          if (!x || x >> shift != prefix) return;
+          if (x != last) {
+            if (times) atomicAdd(&bins[(last >> rest) & mask], times);
+            last = x;
+            times = 0;
+          }
+          ++times;
+        });
+      });
+      if (times) atomicAdd(&bins[(last >> rest) & mask], times);
+    }
     __syncthreads();
     // a thread has two bins, the greatest first
     const int hi = kBins - 1 - 2 * tid;
@@ -373,32 +417,35 @@ __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_c
     __syncthreads();
     prefix = (shift == 32 ? 0u : prefix << bits) | found[0];
     need = found[1];
+    if (shift == 32 && bins[found[0]] <= kFewKeys) {
+      aside = true;
+      run([&](int, uint4 k) {
+        four(k, [&](int, uint32_t x) {
+          if (x && x >> rest == prefix) few[atomicAdd(&n_few, 1u)] = x;
+        });
+      });
+      __syncthreads();
+    }
     shift = rest;
   }
-  // Kept: greater than `prefix`, or equal to it and one of the first `need` such.  A warp has a run of tokens.
-  const int count = c1 - c0, per = ((count + kPickThreads - 1) / kPickThreads) * 32;
-  const int w0 = c0 + (int)min((int64_t)count, (int64_t)warp * per), w1 = c0 + (int)min((int64_t)count, (int64_t)(warp + 1) * per);
+  // Kept: greater than `prefix`, or equal to it and one of the first `need` such.
   uint32_t more = 0, same = 0;
-  each(w0 + lane, 32, w1, [&](int, bool in, uint32_t k) {
-    more += __popc(__ballot_sync(0xffffffffu, in && want > 0 && k > prefix));
-    same += __popc(__ballot_sync(0xffffffffu, in && want > 0 && k == prefix));
+  run([&](int, uint4 k) {
+    four(k, [&](int, uint32_t x) {
+      more += x > prefix;
+      same += x == prefix;
+    });
   });
   uint32_t total;
-  const uint32_t same_before = __shfl_sync(0xffffffffu, block_scan(lane == 0 ? same : 0u, tmp, &total), 0);
-  const uint32_t take = same_before >= need ? 0u : min(same, need - same_before);
-  const uint32_t before = __shfl_sync(0xffffffffu, block_scan(lane == 0 ? more + take : 0u, tmp, &total), 0);
-  uint32_t at = before, seen = same_before;
-  each(w0 + lane, 32, w1, [&](int t, bool in, uint32_t k) {
-    in = in && want > 0;
-    const uint32_t eq = __ballot_sync(0xffffffffu, in && k == prefix), below = (1u << lane) - 1u;
-    const bool stays = in && (k > prefix || (k == prefix && seen + __popc(eq & below) < need));
-    const uint32_t all = __ballot_sync(0xffffffffu, stays);
-    if (stays) kept[a.sinks + at + __popc(all & below)] = t;
-    at += __popc(all);
-    seen += __popc(eq);
+  uint32_t seen = block_scan(same, tmp, &total);
+  uint32_t at = block_scan(more, tmp, &total) + min(seen, need);
+  run([&](int q, uint4 k) {
+    four(k, [&](int e, uint32_t x) {
+      const bool stays = x > prefix || (x == prefix && seen < need);
+      seen += x == prefix;
+      if (stays) kept[a.sinks + at++] = base + 4 * q + e;
+    });
   });
-  for (int i = tid; i < a.sinks; i += kPickThreads) kept[i] = i;
-  for (int i = tid; i < a.recent; i += kPickThreads) kept[a.budget - a.recent + i] = c1 + i;
 }
 
 constexpr int kMoveThreads = 256;
@@ -554,7 +601,7 @@ FA3_API int fa3_evict_gqa_block_paged(int8_t* k_cache, int8_t* v_cache, float* k
   if (st != FA3_OK) return st;
   if ((int64_t)sinks + recent > budget || (int64_t)budget > (int64_t)new_pages * page_size) return FA3_EINVAL;
   if (D % 8 != 0 || D > 256 || B > 65535) return FA3_ERANGE;
-  if (!aligned8(k_cache) || !aligned8(v_cache) || !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(weights))
+  if (!aligned8(k_cache) || !aligned8(v_cache) || !aligned4(k_scale) || !aligned4(v_scale) || !aligned16(weights))
     return FA3_ERANGE;
   st = check_device(nullptr);
   if (st != FA3_OK) return st;
@@ -566,12 +613,12 @@ FA3_API int fa3_evict_gqa_block_paged(int8_t* k_cache, int8_t* v_cache, float* k
   a.chunks = D / a.unit;
   a.div_chunks = make_divu32((uint32_t)a.chunks);
   a.rows = block * std::max(1, 64 / block);                  // 64 tokens or one block
-  a.cached = std::min(a.pg.T_max, 48 * 1024);
+  a.cached = std::min(a.pg.T_max / 4 * 4 + 8, kMostKeys);   // (up to three tokens more, in front and behind)
   const int smem = a.cached * 4;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const auto move = wide ? evict_move_kernel<uint4> : evict_move_kernel<uint2>;
   const int move_smem = a.rows * 24 + a.rows / block * 8;
-  if (cudaFuncSetAttribute(evict_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 48 * 1024 * 4) != cudaSuccess ||
+  if (cudaFuncSetAttribute(evict_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostKeys * 4) != cudaSuccess ||
       cudaFuncSetAttribute(move, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostBlock * 24 + 8) != cudaSuccess)
     return FA3_ECUDA;
   const LaunchTogether together(s);
