@@ -1010,7 +1010,8 @@ def _queries(q: torch.Tensor, D: int, dev: int):
     sh = q.shape
     if len(sh) != 3 or sh[2] != D:
         raise ValueError("q must be [n][Hq][D] with the cache's head size")
-    return sh[0], sh[1], _packed_rows(q, sh[1], D, sh[0], "q", dev) or sh[1] * D
+    stride = _packed_rows(q, sh[1], D, sh[0], "q", dev)
+    return sh[0], sh[1], stride if sh[0] > 1 else sh[1] * D
 
 
 def _row_values(t: torch.Tensor, n: int, Hq: int, name: str, dev: int) -> int:

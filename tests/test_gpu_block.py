@@ -280,6 +280,23 @@ def test_attention(Hq, Hkv, page, block, q_lens, kv_lens):
     assert none is None and np.array_equal(out, out2)
 
 
+def test_attention_of_one_query_expanded_over_rows():
+    F, rng = fa3(), np.random.default_rng(10)
+    for q_lens in ([1, 1, 1], [60, 30, 40]):
+        c = _rows(rng, _cache(rng, [100, 130, 64], 32, 16, 2), q_lens, 4, behind=0)
+        c["q"][:] = c["q"][:1]
+        out, lse = _attend(F, c)
+        a = [_t(c[x]) for x in ("k", "v", "ks", "vs", "q_start", "kv_lens", "table")]
+        q = _bf(c["q"][:1]).cuda().expand(len(c["q"]), -1, -1)
+        l2 = torch.zeros(c["q"].shape[:2], device="cuda")
+        o2 = F.attn_gqa_block_paged(q, *a, SM, lse=l2)
+        assert np.array_equal(out, _f(o2)) and np.array_equal(lse, _f(l2))
+        if len(c["q"]) > 3:                                         # whole rows of heads may not overlap there
+            w = F.attn_weight_pool(a[0])
+            with pytest.raises(F.FA3Error):
+                F.attn_weights_gqa_block_paged(q, a[0], a[2], l2, w, *a[4:], SM)
+
+
 def test_attention_long_contexts_split_over_the_gpu():
     F, rng = fa3(), np.random.default_rng(11)
     for q_lens, kv_lens, Hq, Hkv in (([1], [20000], 8, 1), ([70, 1], [9000, 3000], 6, 2)):
