@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_c
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       t[i] = (uint32_t)(base + 4 * min(q0 + i * stride, groups - 1));
-      page[i] = __ldg(table + divu32(t[i], a.pg.div_ps));
+      page[i] = table[divu32(t[i], a.pg.div_ps)];
     }
     float4 w[kLoads];
 #pragma unroll
@@ -473,8 +473,8 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
   for (int i = tid; i < rows; i += kMoveThreads) {
     const int t = kept[i];
     const uint32_t sp = divu32((uint32_t)t, a.pg.div_ps), dp = divu32((uint32_t)(base + i), a.pg.div_ps);
-    int from = __ldg(a.pg.table + (int64_t)b * a.pg.max_pages + sp);
-    const int to = __ldg(a.new_table + (int64_t)b * a.new_pages + dp);
+    int from = a.pg.table[(int64_t)b * a.pg.max_pages + sp];
+    const int to = a.new_table[(int64_t)b * a.new_pages + dp];
     if ((uint32_t)from >= (uint32_t)a.pg.num_pages) {        // outside the pool: any page of it
       set_dev_err(a.err, FA3_DEVERR_PAGE);
       from = 0;

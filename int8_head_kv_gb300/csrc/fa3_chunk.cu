@@ -462,12 +462,18 @@ __device__ __forceinline__ float put_query_row(const uint16_t* row, bool active,
 #pragma unroll 1
   for (int pass = 0;; ++pass) {
     uint32_t top = 0;
-#pragma unroll 4
-    for (int c = 0; c < 16; ++c) {
-      const uint4 v = active ? __ldg(reinterpret_cast<const uint4*>(row) + c) : make_uint4(0u, 0u, 0u, 0u);
-      top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
-      auto two = [&](uint32_t w) { return pack_f16x2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f); };
-      *reinterpret_cast<uint4*>(dst + c * 2048) = make_uint4(two(v.x), two(v.y), two(v.z), two(v.w));
+#pragma unroll 1
+    for (int c = 0; c < 16; c += 4) {
+      uint4 w[4];                                            // (loads do not pass the stores by themselves)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = active ? reinterpret_cast<const uint4*>(row)[c + k] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint4 v = w[k];
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+        auto two = [&](uint32_t y) { return pack_f16x2(__uint_as_float(y << 16) * f, __uint_as_float(y & 0xffff0000u) * f); };
+        *reinterpret_cast<uint4*>(dst + (c + k) * 2048) = make_uint4(two(v.x), two(v.y), two(v.z), two(v.w));
+      }
     }
     const uint32_t e = max(top & 0xffffu, top >> 16) >> 7;   // the largest's exponent: 2^(e - 127)
     if (pass || !active || (e >= 121u && e < 136u)) return inv;
@@ -488,12 +494,12 @@ __device__ __forceinline__ int scale_token(const TileScales& t, int tile, int la
   return min(tile * kKeys + (lane & 7) * 16, t.n_keys - 1);
 }
 __device__ __forceinline__ int scale_page(const ChunkParams& p, const TileScales& t, int tile, int lane) {
-  int pg = __ldg(t.table + divu32((uint32_t)scale_token(t, tile, lane), p.div_ps));
+  const int pg = t.table[divu32((uint32_t)scale_token(t, tile, lane), p.div_ps)];
   return (uint32_t)pg < (uint32_t)p.num_pages ? pg : 0;      // outside the pool: the loader of the tile reports it
 }
 __device__ __forceinline__ float scale_of(const ChunkParams& p, const TileScales& t, int page, int tile, int lane) {
   const uint32_t tok = (uint32_t)scale_token(t, tile, lane), at = tok - divu32(tok, p.div_ps) * (uint32_t)p.page_size;
-  return __ldg(t.pool + ((int64_t)page * p.per_page + divu32(at, p.div_block)) * p.Hkv + t.g);
+  return t.pool[((int64_t)page * p.per_page + divu32(at, p.div_block)) * p.Hkv + t.g];
 }
 
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
@@ -718,7 +724,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
         const uint32_t t = (uint32_t)min(j * kKeys + i * p.box, (n_keys - 1) & ~(p.box - 1));
         if (p.block_table) {
           const uint32_t pi = divu32(t, p.div_ps);
-          pg = mine ? __ldg(p.block_table + (int64_t)b * p.max_pages + pi) : 0;
+          pg = mine ? p.block_table[(int64_t)b * p.max_pages + pi] : 0;
           at = (int)(t - pi * (uint32_t)p.page_size);
         } else {
           at = b * p.T + (int)t;
@@ -788,7 +794,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t t = (uint32_t)min(j * kKeys + 64 * cw + 32 * h + lane, n_keys - 1), pi = divu32(t, p.div_ps);
-          int pg = __ldg(p.block_table + (int64_t)b * p.max_pages + pi);
+          int pg = p.block_table[(int64_t)b * p.max_pages + pi];
           if ((uint32_t)pg >= (uint32_t)p.num_pages) {         // outside the pool: any page of it
             set_dev_err(p.err, FA3_DEVERR_PAGE);
             pg = 0;

@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kThreadsF, NT == 1 ? 4 : 3) few_rows_kernel(co
         const uint16_t* row = p.q + (int64_t)(s.q0 + i0 + ri) * p.q_stride + (int64_t)(g * p.G + col - ri * p.G) * kD;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          qv[nt][i] = col < cols ? __ldg(reinterpret_cast<const uint4*>(row + (i >> 1) * 64 + 16 * qd + 8 * (i & 1)))
+          qv[nt][i] = col < cols ? *reinterpret_cast<const uint4*>(row + (i >> 1) * 64 + 16 * qd + 8 * (i & 1))
                                  : make_uint4(0u, 0u, 0u, 0u);
       }
       const int n_my = s1 - s0 > warp ? (s1 - s0 - warp + kWarps - 1) / kWarps : 0;   // steps s0 + warp, + 4, ...
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreadsF, NT == 1 ? 4 : 3) few_rows_kernel(co
       float ks_of = 0.f, lv_of = 0.f, rv_of = 0.f, ks_next = 0.f, vs_next = 0.f;
       auto look_up = [&](int m) {
         const uint32_t t = (uint32_t)((s0 + warp + kWarps * min(m + lane, n_my - 1)) * kStep), pi = divu32(t, p.pg.div_ps);
-        int page = __ldg(p.pg.table + (int64_t)w.b * p.pg.max_pages + pi);
+        int page = p.pg.table[(int64_t)w.b * p.pg.max_pages + pi];
         if ((uint32_t)page >= (uint32_t)p.pg.num_pages) {           // outside the pool: any page of it
           set_dev_err(p.err, FA3_DEVERR_PAGE);
           page = 0;
@@ -280,8 +280,8 @@ __global__ void __launch_bounds__(kThreadsF, NT == 1 ? 4 : 3) few_rows_kernel(co
         const int at = (int)(t - pi * (uint32_t)p.pg.page_size);
         row_of = page * p.pg.page_size + at;
         const int64_t sc = ((int64_t)page * p.pg.per_page + (int)divu32((uint32_t)at, p.pg.div_block)) * p.pg.Hkv + g;
-        ks_next = __ldg(p.ks + sc);
-        vs_next = __ldg(p.vs + sc);
+        ks_next = p.ks[sc];
+        vs_next = p.vs[sc];
       };
       // A step's 16 rows of K and of V: a lane has 16 bytes of rows l / 8, l / 8 + 4, ..  Rows behind the context are read as
       // they are (they lie in the same page) and masked.
@@ -649,13 +649,13 @@ __global__ void __launch_bounds__(kThreadsF, 4) few_weights_kernel(const __grid_
       int page_next = 0, at_next = 0;
       auto look_up = [&](int m) {
         const uint32_t t = (uint32_t)((s0 + warp + kWarps * min(m + lane, n_my - 1)) * kStep), pi = divu32(t, p.pg.div_ps);
-        page_next = __ldg(p.pg.table + (int64_t)w.b * p.pg.max_pages + pi);
+        page_next = p.pg.table[(int64_t)w.b * p.pg.max_pages + pi];
         at_next = (int)(t - pi * (uint32_t)p.pg.page_size);
         if ((uint32_t)page_next >= (uint32_t)p.pg.num_pages) {      // outside the pool: its tokens get nothing
           set_dev_err(p.err, FA3_DEVERR_PAGE);
           page_next = -1;
         }
-        ks_next = __ldg(p.ks + ((int64_t)max(page_next, 0) * p.pg.per_page + (int)divu32((uint32_t)at_next, p.pg.div_block)) * p.pg.Hkv + g);
+        ks_next = p.ks[((int64_t)max(page_next, 0) * p.pg.per_page + (int)divu32((uint32_t)at_next, p.pg.div_block)) * p.pg.Hkv + g];
       };
       const int64_t lane_off = (int64_t)(lane >> 3) * tok_stride + g * kD + (lane & 7) * 16;
       const uint32_t lane_dst = ring + (uint32_t)(lane >> 3) * 128;
@@ -680,10 +680,10 @@ __global__ void __launch_bounds__(kThreadsF, 4) few_weights_kernel(const __grid_
         uint4 v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          v[i] = col < cols ? __ldg(reinterpret_cast<const uint4*>(p.q + row * p.q_stride + (int64_t)h * kD + (i >> 1) * 64 +
-                                                                   16 * qd + 8 * (i & 1)))
+          v[i] = col < cols ? *reinterpret_cast<const uint4*>(p.q + row * p.q_stride + (int64_t)h * kD + (i >> 1) * 64 +
+                                                                  16 * qd + 8 * (i & 1))
                             : make_uint4(0u, 0u, 0u, 0u);
-        const float lse = col < cols ? __ldg(p.lse + row * p.Hq + h) * -1.4426950408889634f : 0.f;
+        const float lse = col < cols ? p.lse[row * p.Hq + h] * -1.4426950408889634f : 0.f;
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i)

@@ -80,10 +80,11 @@ __device__ __forceinline__ void wait_ld16(uint32_t* v) {
                :: "memory");
 }
 
-// 16 bytes that this SM reads once: the L1 (what shared memory leaves of it) is passed by.
+// 16 bytes that this SM reads once: the L1 (what shared memory leaves of it) is passed by.  (Not as read-only data: the call
+// before may have written them after this kernel had begun.)
 __device__ __forceinline__ uint4 load_once(const int8_t* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }

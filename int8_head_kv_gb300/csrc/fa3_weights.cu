@@ -272,7 +272,7 @@ __device__ __forceinline__ void three_parts(float x, uint32_t (&p)[3]) {
 // The factor of a key's scores: not so small that its inverse leaves float32's range (a smaller one gives every score 0 as well).
 __device__ __forceinline__ float key_factor(const WeightParams& p, int page, int at, int g) {
   const float ks = (uint32_t)page < (uint32_t)p.pg.num_pages
-                       ? __ldg(p.ks + ((int64_t)page * p.pg.per_page + divu32((uint32_t)at, p.pg.div_block)) * p.pg.Hkv + g)
+                       ? p.ks[((int64_t)page * p.pg.per_page + divu32((uint32_t)at, p.pg.div_block)) * p.pg.Hkv + g]
                        : 0.f;                                 // outside the pool: the keys' loader reports it
   return fmaxf(ks * p.sm_log2, 8.673617379884035e-19f);      // 2^-60
 }
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int c = lane + 32 * k, i = (int)divu32((uint32_t)c, p.div_G);
-          to[k] = c < cols ? __ldg(p.lse + (int64_t)(u.q0 + i0 + i) * p.Hq + u.g * p.G + c - i * p.G) : 0.f;
+          to[k] = c < cols ? p.lse[(int64_t)(u.q0 + i0 + i) * p.Hq + u.g * p.G + c - i * p.G] : 0.f;
         }
       };
       ask(u.s0, v[0]);
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
         const uint32_t t = (uint32_t)min(u.tile * kKeysW + 128 * cw + 32 * h + lane, u.nkv - 1), pi = divu32(t, p.pg.div_ps);
-        int page = __ldg(p.pg.table + (int64_t)u.b * p.pg.max_pages + pi);
+        int page = p.pg.table[(int64_t)u.b * p.pg.max_pages + pi];
         if ((uint32_t)page >= (uint32_t)p.pg.num_pages) {      // outside the pool: any page of it
           set_dev_err(p.err, FA3_DEVERR_PAGE);
           page = 0;
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
       float f;
       {
         const uint32_t tv = (uint32_t)min(t, u.nkv - 1), pi = divu32(tv, p.pg.div_ps);
-        const int page = __ldg(p.pg.table + (int64_t)u.b * p.pg.max_pages + pi);
+        const int page = p.pg.table[(int64_t)u.b * p.pg.max_pages + pi];
         f = key_factor(p, page, (int)(tv - pi * (uint32_t)p.pg.page_size), u.g);
       }
       const SeqW sq = {u.q0, u.nq, u.nkv};
