@@ -846,9 +846,9 @@ cudaError_t few_rows_attn(const FewCall& c, const int32_t* table, int num_pages,
 
 bool few_rows_weights(int n, int B, int Hkv, int G, int T_max) {
   const double chunks = (double)n / (kChunkCols / std::min(G, kChunkCols)) + B;
-  // Up to some 64 columns a sequence: 16 sequences of 4096 keys, 64 query and 8 KV heads, with 1, 4, 8 and 16 rows each take
-  // 18.3, 26.0, 37.8 and 72.6 us here and 45.5, 45.3, 43.3 and 54.0 in fa3_weights.cu's kernel.
-  return G <= kChunkCols && (int64_t)n * G <= (int64_t)72 * B &&
+  // Up to some 96 columns a sequence: 16 sequences of 4096 keys, 64 query and 8 KV heads, with 1, 4, 8 and 16 rows each take
+  // 18.2, 26.5, 39.2 and 70.3 us here and 50, 51.2, 52.6 and 52.0 in fa3_weights.cu's kernel.
+  return G <= kChunkCols && (int64_t)n * G <= (int64_t)96 * B &&
          Hkv * ((double)B * kWUnit + chunks * (T_max / kStep + 1.0)) < 2147483648.0;
 }
 cudaError_t few_rows_weights_attn(const FewCall& c, float* weights, const int32_t* table, int num_pages, int page_size,
