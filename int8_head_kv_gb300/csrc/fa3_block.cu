@@ -274,7 +274,7 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* tmp, uint32
 constexpr int kFewKeys = 4096;
 __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_constant__ EvictArgs a) {
   extern __shared__ __align__(16) uint32_t keys[];           // of all tokens that are chosen from, where they fit
-  __shared__ uint32_t bins[kBins], tmp[33], found[2], few[kFewKeys], n_few;
+  __shared__ uint32_t bins[kBins], tmp[33], found[3], few[kFewKeys], n_few;
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, g = blockIdx.x, b = blockIdx.y;
@@ -413,11 +413,12 @@ __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_c
       const bool second = before + n0 < need;
       found[0] = (uint32_t)(second ? hi - 1 : hi);
       found[1] = need - before - (second ? n0 : 0u);
+      found[2] = second ? n1 : n0;                           // (the bins are cleared by whoever comes first)
     }
     __syncthreads();
     prefix = (shift == 32 ? 0u : prefix << bits) | found[0];
     need = found[1];
-    if (shift == 32 && bins[found[0]] <= kFewKeys) {
+    if (shift == 32 && found[2] <= kFewKeys) {
       aside = true;
       run([&](int, uint4 k) {
         four(k, [&](int, uint32_t x) {
