@@ -592,8 +592,8 @@ int fa3_attn_weights_gqa_block_paged(const uint16_t* q, const int8_t* k_cache, c
  *          other's reads); budget <= new_pages * page_size.  An entry outside the pool
  *          sets FA3_DEVERR_PAGE and its tokens are lost; one of block_table outside it reads another page.
  * kept     int32 [B][Hkv][budget]: positions of the kept tokens, -1 behind them.
- * new_lens int32 [B]: min(kv_lens[b], budget).
- * Supported: D % 8 == 0, D <= 256, B <= 65535; caches 8-byte aligned, weights 16-byte aligned. */
+ * new_lens int32 [B]: min(kv_lens[b], budget); apart from kv_lens.
+ * Supported: D % 8 == 0, D <= 256, B <= 65535, budget <= 2^31 - 2^16; caches 8-byte aligned, weights 16-byte aligned. */
 int fa3_evict_gqa_block_paged(int8_t* k_cache, int8_t* v_cache, float* k_scale, float* v_scale, float* weights,
                               const int32_t* block_table, const int32_t* kv_lens, const int32_t* new_table,
                               int32_t* kept, int32_t* new_lens, int B, int Hkv, int D, int num_pages,

@@ -601,9 +601,11 @@ FA3_API int fa3_evict_gqa_block_paged(int8_t* k_cache, int8_t* v_cache, float* k
   int st = pages_of(block_table, B, Hkv, num_pages, page_size, max_pages, block, &a.pg);
   if (st != FA3_OK) return st;
   if ((int64_t)sinks + recent > budget || (int64_t)budget > (int64_t)new_pages * page_size) return FA3_EINVAL;
-  if (D % 8 != 0 || D > 256 || B > 65535) return FA3_ERANGE;
+  if (D % 8 != 0 || D > 256 || B > 65535 || (int64_t)budget > ((int64_t)1 << 31) - 65536) return FA3_ERANGE;
   if (!aligned8(k_cache) || !aligned8(v_cache) || !aligned4(k_scale) || !aligned4(v_scale) || !aligned16(weights))
     return FA3_ERANGE;
+  // (the blocks of other heads would read the lengths that the first has written)
+  if (new_lens < kv_lens + B && kv_lens < new_lens + B) return FA3_EINVAL;
   st = check_device(nullptr);
   if (st != FA3_OK) return st;
   a.cache[0] = k_cache; a.cache[1] = v_cache; a.scale[0] = k_scale; a.scale[1] = v_scale; a.weights = weights;

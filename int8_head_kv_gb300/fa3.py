@@ -1165,9 +1165,9 @@ def evict_gqa_block_paged(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale:
     ``recent`` and, of the others, those with the greatest weights (the earliest of equal ones).
 
     The kept tokens are copied in order, with their scales and weights, to the pages in new_table int32
-    [B][new_pages], which must not be among those that block_table uses.  Returns (kept int32 [B][Hkv][budget]: their positions, -1 behind
-    them; new_lens int32 [B]: min(kv_lens, budget)); of a sequence with a bad length both are left as they were
-    (-1 and 0 when allocated here)."""
+    [B][new_pages], which must not be among those that block_table uses.  Returns (kept int32
+    [B][Hkv][budget]: their positions, -1 behind them; new_lens int32 [B], which may not be kv_lens itself:
+    min(kv_lens, budget)); of a sequence with a bad length both are left as they were (-1 and 0 when allocated here)."""
     _need(k_cache, _I8, "k_cache")
     dev = k_cache.get_device()
     num_pages, page_size, Hkv, D = _pool_shape(k_cache, v_cache, dev)

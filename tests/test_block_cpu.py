@@ -166,6 +166,16 @@ def test_eviction_validation(L):
         assert call(**bad) == ERANGE, bad
 
 
+def test_eviction_refuses_lengths_in_place_and_budgets_beyond_32_bits(L):
+    def call(kl, nl, budget=100, new=2):
+        return L.fa3_evict_gqa_block_paged(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, kl, FAKE, FAKE, nl, 4, 2, 128, 8, 64, 4, 32, new,
+                                           budget, 4, 10, None, None)
+    at = FAKE.value
+    for d in (0, 4, 12, -12):
+        assert call(FAKE, ctypes.c_void_p(at + d)) == EINVAL, d
+    assert call(FAKE, ctypes.c_void_p(at + 16), (1 << 31) - 65535, 1 << 25) == ERANGE
+
+
 def test_call_block_knows_the_calls(L):
     F = fa3()
     for name, count in (("fa3_append_gqa_block_paged", 21), ("fa3_attn_gqa_block_paged", 25),
