@@ -548,7 +548,8 @@ int fa3_append_gqa_block_paged(const uint16_t* k, const uint16_t* v, int8_t* k_c
  * Rows outside the sequences and those of a sequence with bad lengths are left as they were.
  * An entry outside the pool sets FA3_DEVERR_PAGE and reads another page (that
  * sequence's output is not valid).  A value scale below 2^-80 counts as 2^-80.
- * Supported: D = 128, Hq / Hkv <= 128, n < 2^27 - 1; q_stride a multiple of 8; q, out and the caches 16-byte aligned.
+ * Supported: D = 128, Hq / Hkv <= 128, n < 2^27 - 1; q_stride a multiple of 8; q, out and the caches 16-byte aligned,
+ *          scales and lse 4-byte.
  * workspace  fa3_attn_block_workspace_size(n, B, Hq, Hkv, D) bytes, 16-byte aligned, not
  *          initialised; calls that may run at the same time need one each. */
 size_t fa3_attn_block_workspace_size(int n, int B, int Hq, int Hkv, int D);
@@ -567,7 +568,7 @@ int fa3_attn_gqa_block_paged(const uint16_t* q, const int8_t* k_cache, const int
  * tokens 1 in all.  Sequences without new rows keep their weights.  The sums are the same on
  * every run; a page that sequences share gets both their sums, in either order.
  * An entry outside the pool sets FA3_DEVERR_PAGE; its tokens get nothing.
- * Supported: as fa3_attn_gqa_block_paged; q_stride >= Hq * D.
+ * Supported: as fa3_attn_gqa_block_paged; q_stride >= Hq * D; weights 4-byte aligned.
  * workspace  fa3_attn_weights_workspace_size() bytes, 16-byte aligned, not initialised;
  *          calls that may run at the same time need one each. */
 size_t fa3_attn_weights_workspace_size(void);

@@ -549,7 +549,6 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
 }
 
 inline bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
-inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 }  // namespace
 }  // namespace fa3

@@ -1327,7 +1327,7 @@ FA3_API int fa3_attn_gqa_block_paged(const uint16_t* q, const int8_t* k_cache, c
   Pages pg;
   const int st = pages_of(block_table, B, Hkv, num_pages, page_size, max_pages, block, &pg);
   if (st != FA3_OK) return st;
-  if (q_stride < 0 || q_stride % 8 != 0) return FA3_ERANGE;
+  if (q_stride < 0 || q_stride % 8 != 0 || !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(lse)) return FA3_ERANGE;
   ChunkParams p = {};
   p.qf = q; p.k = k_cache; p.v = v_cache; p.ks = k_scale; p.vs = v_scale; p.q_start = q_start; p.kv_lens = kv_lens;
   p.block_table = block_table; p.out = out; p.lse = lse; p.err = dev_err;

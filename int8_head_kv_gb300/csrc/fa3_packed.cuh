@@ -12,6 +12,8 @@ namespace {
 
 constexpr int kLeastBlock = 16, kMostBlock = 4096;   // tokens that share a scale: a multiple of the one, up to the other
 
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 // The pages: token t of sequence b lies in row t % page_size of page block_table[b][t / page_size].
 struct Pages {
   const int32_t* table;            // [B][max_pages]

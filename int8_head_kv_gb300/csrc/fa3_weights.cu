@@ -662,7 +662,7 @@ FA3_API int fa3_attn_weights_gqa_block_paged(const uint16_t* q, const int8_t* k_
   p.G = Hq / Hkv;
   if (D != kD || p.G > kCols || n >= (1 << 27) - 1 || q_stride < 0 || q_stride % 8 != 0) return FA3_ERANGE;
   if (n > 1 && q_stride < (int64_t)Hq * kD) return FA3_ERANGE;
-  if (!aligned16(q) || !aligned16(k_cache)) return FA3_ERANGE;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned4(k_scale) || !aligned4(lse) || !aligned4(weights)) return FA3_ERANGE;
   int sms = 0;
   st = check_device(&sms);
   if (st != FA3_OK) return st;

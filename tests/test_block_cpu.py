@@ -153,6 +153,18 @@ def test_weights_validation(L):
     assert L.fa3_attn_weights_workspace_size() > 0
 
 
+def test_values_of_four_bytes_are_aligned(L):
+    odd = ctypes.c_void_p(4098)
+    for at in (3, 4, 9):
+        a = [FAKE] * 10
+        a[at] = odd
+        assert L.fa3_attn_gqa_block_paged(*a, 4, 2, 16, 2, 128, 2048, 8, 64, 4, 32, 0.09, FAKE, 1 << 40, None, None) == ERANGE
+    for at in (2, 3, 4):
+        a = [FAKE] * 8
+        a[at] = odd
+        assert L.fa3_attn_weights_gqa_block_paged(*a, 4, 2, 16, 2, 128, 2048, 8, 64, 4, 32, 0.09, FAKE, 1 << 30, None, None) == ERANGE
+
+
 def test_eviction_validation(L):
     def call(k=FAKE, v=FAKE, ks=FAKE, w=FAKE, bt=FAKE, kl=FAKE, nt=FAKE, kept=FAKE, nl=FAKE, B=2, Hkv=2, D=128, npg=8, ps=64,
              mp=4, block=32, new=2, budget=100, sinks=4, recent=10):
