@@ -456,6 +456,53 @@ def test_weights_bad_lengths_pages_and_starts():
     assert err.item() == F.FA3_DEVERR_PAGE and np.array_equal(got, whole)
 
 
+def _both(F, c, seed):
+    """Attention and, with its log-sum-exps, attention weights."""
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = _attend(F, c, err)
+    _check_attention(c, out, lse)
+    before = np.random.default_rng(seed).random((c["num"], c["Hkv"], c["page"])).astype(np.float32)
+    _check_weights(c, lse, before, _weigh(F, c, lse, before, err))
+    assert err.item() == 0
+
+
+@pytest.mark.parametrize("most,long", [(1, 0), (3, 0), (3, 2), (40, 4)])
+def test_many_sequences_some_without_rows(most, long):
+    """More sequences than a warp or a block looks at in one go, also without rows and without a context."""
+    F, rng = fa3(), np.random.default_rng(61 + most + long)
+    B = 141
+    q_lens = rng.integers(0, most + 1, B)
+    q_lens[[0, 31, 32, 33, 70, 139, 140]] = 0
+    q_lens[rng.integers(34, 70, long)] = 90
+    kv_lens = q_lens + rng.integers(0, 150, B)
+    kv_lens[[0, 32, 140]] = 0
+    _both(F, _rows(rng, _cache(rng, kv_lens.tolist(), 32, 16, 2), q_lens.tolist(), 8, lead=2), 62)
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,Hq,Hkv", [([1, 1, 2, 1], [90, 300, 2, 45], 8, 2), ([70, 40], [200, 41], 8, 2),
+                                                  ([2, 1], [130, 40], 40, 1), ([30], [64], 100, 1)])
+def test_queries_of_very_different_sizes(q_lens, kv_lens, Hq, Hkv):
+    F, rng = fa3(), np.random.default_rng(63)
+    c = _rows(rng, _cache(rng, kv_lens, 64, 32, Hkv), q_lens, Hq)
+    n = c["q"].shape[0]
+    c["q"] *= np.exp2(np.resize([0, -40, 9, -7, 5, -70, -3], n * Hq)).reshape(n, Hq, 1).astype(np.float32)
+    c["q"][c["q_start"][0], 0] = 0
+    _both(F, c, 64)
+
+
+@pytest.mark.parametrize("q_lens", [[1, 2], [60, 30]])
+def test_weights_of_rows_whose_sum_is_infinite(q_lens):
+    F, rng = fa3(), np.random.default_rng(65)
+    c = _rows(rng, _cache(rng, [200, 150], 32, 16, 2), q_lens, 8)
+    before = rng.random((c["num"], 2, 32)).astype(np.float32)
+    got = _weigh(F, c, np.full(c["q"].shape[:2], np.inf, np.float32), before)
+    ref = before.copy()
+    for b, (new, kv) in enumerate(zip(q_lens, (200, 150))):
+        t = np.arange(kv - new, kv)
+        ref[c["table"][b, t // 32], :, t % 32] = 0
+    assert np.array_equal(got, ref)
+
+
 # -------------------------------------------------------------------- eviction
 EVICT = [                         # kv_lens, page, block, Hkv, D, budget, sinks, recent
     ([1], 16, 16, 1, 8, 1, 0, 0),
@@ -507,6 +554,22 @@ def test_eviction_longer_than_shared_memory():
         t = np.arange(T)
         ref = O.kept_tokens(w[c["table"][0, t // 64], 0, t % 64], budget, 3, 77)
         assert got[0][0, 0].tolist() == ref
+
+
+@pytest.mark.parametrize("T,page,values", [(30000, 48, 1), (30001, 64, 2), (9000, 16, 3)])
+def test_eviction_among_many_equal_weights(T, page, values):
+    """More equal weights than are put aside, which shared memory holds."""
+    F, rng = fa3(), np.random.default_rng(33)
+    B, Hkv, budget = 3, 4, 5000
+    pages = -(-budget // page)
+    c = _cache(rng, [T] * B, page, 16, Hkv, 8, extra=pages)
+    new = c["rest"][:B * pages].reshape(B, pages).copy()
+    w = (1 + rng.integers(0, values, (c["num"], Hkv, page)) / 64).astype(np.float32)
+    kept = _evict(F, c, w, new, budget, 5, 100)[0]
+    t = np.arange(T)
+    for b in range(B):
+        for g in range(Hkv):
+            assert kept[b, g].tolist() == O.kept_tokens(w[c["table"][b, t // page], g, t % page], budget, 5, 100)
 
 
 def test_eviction_bad_lengths_and_pages():
