@@ -245,8 +245,8 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Exclusive prefix sums over the block's threads, and the total (1024 threads; `tmp` holds 33 values).
-__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* tmp, uint32_t* total) {
+// Exclusive prefix sums over the block's 1024 threads (`tmp` holds 32 values).
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* tmp) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t s = v;
 #pragma unroll
@@ -266,10 +266,8 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* tmp, uint32
       if (lane >= o) t += y;
     }
     tmp[lane] = t - mine;
-    if (lane == 31) tmp[32] = t;
   }
   __syncthreads();
-  *total = tmp[32];
   return tmp[warp] + s - v;
 }
 
@@ -277,7 +275,7 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* tmp, uint32
 constexpr int kFewKeys = 4096;
 __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_constant__ EvictArgs a) {
   extern __shared__ __align__(16) uint32_t keys[];           // of all tokens that are chosen from, where they fit
-  __shared__ uint32_t bins[kBins], tmp[33], found[3], few[kFewKeys], n_few;
+  __shared__ uint32_t bins[2][kBins], sums[2][32], tmp[32], few[kFewKeys], n_few;
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, g = blockIdx.x, b = blockIdx.y;
@@ -367,13 +365,14 @@ __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_c
   };
   uint32_t prefix = 0, need = (uint32_t)want;
   bool aside = false;
+  for (int i = tid; i < kBins; i += kPickThreads) bins[0][i] = 0;
   if (tid == 0) n_few = 0;
+  __syncthreads();
 #pragma unroll 1
-  for (int shift = 32; shift > 0;) {
+  for (int shift = 32, buf = 0; shift > 0; buf ^= 1) {
     const int bits = min(kDigitBits, shift), rest = shift - bits;
     const uint32_t mask = (1u << bits) - 1u;
-    for (int i = tid; i < kBins; i += kPickThreads) bins[i] = 0;
-    __syncthreads();
+    uint32_t* const count = bins[buf];
     if (shift == 32) {
       // tokens that nothing looked at are many: counted by the thread
       constexpr uint32_t kZero = 0x80000000u;
@@ -386,17 +385,17 @@ __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_c
           if (q + i * kPickThreads < groups) {
             if (cached) keys4[q + i * kPickThreads] = k[i];
             four(k[i], [&](int, uint32_t x) {
-              if (x == kZero) ++zeros; else if (x) atomicAdd(&bins[x >> rest], 1u);
+              if (x == kZero) ++zeros; else if (x) atomicAdd(&count[x >> rest], 1u);
             });
           }
         }
       }
       zeros = __reduce_add_sync(0xffffffffu, zeros);
-      if (lane == 0 && zeros) atomicAdd(&bins[kZero >> rest], zeros);
+      if (lane == 0 && zeros) atomicAdd(&count[kZero >> rest], zeros);
     } else if (aside) {
       const int n = (int)n_few;
       for (int i = tid; i < n; i += kPickThreads)
-        if (few[i] >> shift == prefix) atomicAdd(&bins[(few[i] >> rest) & mask], 1u);
+        if (few[i] >> shift == prefix) atomicAdd(&count[(few[i] >> rest) & mask], 1u);
     } else {
       // all keys again: many are equal then, and equal neighbours are counted by the thread
       uint32_t last = 0, times = 0;
@@ -404,30 +403,41 @@ __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_c
         four(k, [&](int, uint32_t x) {
           if (!x || x >> shift != prefix) return;
           if (x != last) {
-            if (times) atomicAdd(&bins[(last >> rest) & mask], times);
+            if (times) atomicAdd(&count[(last >> rest) & mask], times);
             last = x;
             times = 0;
           }
           ++times;
         });
       });
-      if (times) atomicAdd(&bins[(last >> rest) & mask], times);
+      if (times) atomicAdd(&count[(last >> rest) & mask], times);
     }
     __syncthreads();
-    // a thread has two bins, the greatest first
-    const int hi = kBins - 1 - 2 * tid;
-    const uint32_t n0 = bins[hi], n1 = bins[hi - 1];
-    uint32_t total;
-    const uint32_t before = block_scan(n0 + n1, tmp, &total);
-    if (before < need && before + n0 + n1 >= need) {
-      const bool second = before + n0 < need;
-      found[0] = (uint32_t)(second ? hi - 1 : hi);
-      found[1] = need - before - (second ? n0 : 0u);
-      found[2] = second ? n1 : n0;                           // (the bins are cleared by whoever comes first)
-    }
+    // A thread has two bins, the greatest first, and a warp the sum of its 64; then every warp finds the digit for itself.  The other
+    // bins, which all have read, are cleared meanwhile.
+    const uint32_t mine = __reduce_add_sync(0xffffffffu, count[kBins - 1 - 2 * tid] + count[kBins - 2 - 2 * tid]);
+    if (lane == 0) sums[buf][tid >> 5] = mine;
+    for (int i = tid; i < kBins; i += kPickThreads) bins[buf ^ 1][i] = 0;
     __syncthreads();
-    prefix = (shift == 32 ? 0u : prefix << bits) | found[0];
-    need = found[1];
+    // the lane whose values, summed up from lane 0 on, reach `need`; what lies in front of them is taken off it
+    auto reach = [&](uint32_t v) {
+      uint32_t upto = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      const int l = __ffs(__ballot_sync(0xffffffffu, upto >= need)) - 1;
+      need -= __shfl_sync(0xffffffffu, upto - v, l);
+      return l;
+    };
+    const int w = reach(sums[buf][lane]), hi = kBins - 1 - 64 * w;
+    const uint32_t n0 = count[hi - 2 * lane], n1 = count[hi - 2 * lane - 1];
+    const int l = reach(n0 + n1);
+    const uint32_t f0 = __shfl_sync(0xffffffffu, n0, l), f1 = __shfl_sync(0xffffffffu, n1, l);
+    const bool second = f0 < need;
+    if (second) need -= f0;
+    prefix = (shift == 32 ? 0u : prefix << bits) | (uint32_t)(hi - 2 * l - second);
     if (shift == 32) {
       if (cached) {
         for (int q = g0; q < g1; ++q) {
@@ -441,7 +451,7 @@ __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_c
           among |= (unsigned long long)here << (4 * (q - g0));
         }
       }
-      if (found[2] <= kFewKeys) {
+      if ((second ? f1 : f0) <= kFewKeys) {
         aside = true;
         if (cached) {
           if (among) {
@@ -479,9 +489,17 @@ __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_c
       });
     });
   }
-  uint32_t total;
-  uint32_t seen = block_scan(same, tmp, &total);
-  uint32_t at = block_scan(more, tmp, &total) + min(seen, need);
+  uint32_t seen, at;
+  if (cached) {                                              // both counts at once: they stay below 2^16
+    static_assert(kMostKeys < 65536, "counts in 16 bits");
+    const uint32_t before = block_scan(more << 16 | same, tmp);
+    seen = before & 0xffffu;
+    at = before >> 16;
+  } else {
+    seen = block_scan(same, tmp);
+    at = block_scan(more, tmp);
+  }
+  at += min(seen, need);
   if (cached) {
     bits_of(above | equal, [&](int i) {
       const bool is_equal = equal >> i & 1;

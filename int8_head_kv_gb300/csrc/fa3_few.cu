@@ -13,6 +13,12 @@
 // cut into equal parts, one per resident CTA, so ragged batches and one long context fill the GPU alike.  A CTA's four
 // warps take a unit's steps in turn, each through its own cp.async ring, and merge at its end; a cut unit's parts meet in
 // few_combine_kernel.
+//
+// What bounds it (one GB300, 64 query and 8 KV heads).  16 one-token rows of 4096 keys: 29.5 us, of 16384 keys 89 us, and 14.5 us
+// of 1024: HBM at 6.8 TB/s behind some 10 us that every call pays (launch, plan, a chain of lengths, page, scales and first keys, the
+// combine kernel).  With two column tiles the MMAs, conversions and exponentials of a step count as well: two rows each
+// 33 us, four, whose 32 columns are two units that read the keys twice, 54 (half of the issue slots, three warps a
+// scheduler).  A merge by whoever comes last to a unit, in place of the second kernel, took 33.5 us for the first case.
 #include "fa3_few.cuh"
 
 #include <cuda_bf16.h>
@@ -34,9 +40,9 @@ constexpr int kStages = 2;
 constexpr int kStageBytes = 2 * kStep * kD;                // K, then V rows
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 
+constexpr float kNone = -1e30f;    // the reference of a column that has seen no key
 // What a unit costs beside its steps, and the least part of the line a CTA takes (enough for a part inside a unit to hold a
 // step), in steps of a CTA's warp.
-constexpr float kNone = -1e30f;                            // the reference of a column that has seen no key
 constexpr int kUnitSteps = 16, kLeastSteps = 20;
 static_assert(kLeastSteps > kUnitSteps, "a part inside a unit, behind its fixed cost, holds a step");
 
@@ -581,6 +587,8 @@ __global__ void __launch_bounds__(32 * MW * kMergeCols) few_combine_kernel(const
 // fa3_weights.cu's sums where few columns meet each key: only keys are read, once for every 64 columns of a sequence, and the
 // scores are those above, with the sum over columns (2 a thread, then the four threads of a token) in place of the softmax.
 // Tokens have nothing to do with one another, so a part of the line is a run of tokens and there is nothing to merge.
+// 16 one-token rows of 4096 keys, 64 query and 8 KV heads: 17.6 us, 10 of them HBM's; each 8 columns more take 2.6 us
+// (MMAs and exponentials).
 constexpr int kChunkCols = 64, kWStages = 3;
 constexpr uint32_t kWRing = kWarps * kWStages * kStep * kD;                    // int8 rows of K
 constexpr uint32_t OFF_WQ = kWRing;                                            // [tile][4][32] uint4: fragments of Q^T
@@ -855,7 +863,6 @@ cudaError_t few_rows_attn(const FewCall& c, const int32_t* table, int num_pages,
   p.ctas = ctas_of(nt, c.sms);
   return nt == 1 ? launch<1>(p, workspace, s) : launch<2>(p, workspace, s);
 }
-
 
 bool few_rows_weights(int n, int B, int Hkv, int G, int T_max) {
   const double chunks = (double)n / (kChunkCols / std::min(G, kChunkCols)) + B;

@@ -71,15 +71,24 @@ __device__ __forceinline__ Piece find_piece(const int32_t* __restrict__ q_start,
   return p;
 }
 
-// RNE(code * ratio), exactly: one fused operation rounds the exact product to a whole number (|code * ratio| <= 127).
+// RNE(code * ratio), exactly: one fused operation rounds the exact product to a whole number (|code * ratio| <= 127).  Codes
+// become float32 as the low byte of 2^23 (+ 128), by byte moves and packed sums: conversion instructions go at 16 a cycle, and were
+// what an eviction waited for.
 __device__ __forceinline__ uint32_t rescaled(uint32_t codes4, float ratio) {
-  uint32_t out = 0;
+  const uint32_t u = codes4 ^ 0x80808080u;
+  const unsigned long long less = f32x2_pack(-8388736.f, -8388736.f), by = f32x2_pack(ratio, ratio), one = f32x2_pack(1.f, 1.f),
+                           magic = f32x2_pack(kCodeMagic, kCodeMagic);
+  uint32_t q[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float c = (float)(int)(int8_t)(codes4 >> (8 * e));
-    out |= (__float_as_uint(fmaf(c, ratio, kCodeMagic)) & 0xffu) << (8 * e);
+  for (int e = 0; e < 4; e += 2) {
+    const unsigned long long x = f32x2_pack(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440 + e)),
+                                            __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7441 + e)));
+    float t0, t1;
+    f32x2_unpack(f32x2_fma(f32x2_fma(x, one, less), by, magic), t0, t1);
+    q[e] = __float_as_uint(t0);
+    q[e + 1] = __float_as_uint(t1);
   }
-  return out;
+  return __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
 }
 
 constexpr float kLeastScale = 8.271806125530277e-25f;      // 2^-80: attention takes a smaller value scale as this
