@@ -219,6 +219,9 @@ __global__ void __launch_bounds__(kAppendThreads) block_append_kernel(const __gr
 // ------------------------------------------------------------------ eviction
 // Of each sequence and KV head the first `sinks` tokens stay, the last `recent`, and of the others those with the
 // greatest weights, the earliest of equal ones, up to `budget` in all; a context that fits the budget stays whole.
+//
+// The choice is a radix selection by one block a head and sequence: 16 contexts of 4096 tokens and 8 heads take 8.8 us, three of
+// up to 20001 tokens and 5 heads 13.0 (15 blocks: latency, barriers and instructions, far from HBM).  A cluster of blocks a head was slower.
 constexpr int kPickThreads = 1024;
 constexpr int kDigitBits = 11, kBins = 1 << kDigitBits;
 constexpr int kMostKeys = 48 * 1024;                       // of a context that shared memory holds
@@ -523,7 +526,9 @@ constexpr int kMoveThreads = 128, kMoveTokens = 32;         // tokens of a block
 // scales, and their weights.  A thread's pieces, of 16 bytes where rows allow it, are on their way at once and while the
 // scales are found.  Its way is a chain of four loads (positions, pages, scales, codes), so many blocks an SM, and small
 // ones, are what hides it: 16 contexts of 4096 tokens cut to 1024 take 25.5 us a call so, 28.0 with 5 blocks an SM of 256
-// threads and 64 tokens, 25.5 with 7 (an odd batch of three long contexts 20.1, 19.9 and 20.4).
+// threads and 64 tokens, 25.5 with 7 (an odd batch of three long contexts alike).  17 of them are this kernel's, 4 TB/s: pieces of 128
+// bytes, a head's row of one token, from all over the pool.  Asking for the rows from evict_pick_kernel, into L2, was slower
+// (28.8 us; the odd batch 27.0 where it takes 18.4).
 template <class V>
 __global__ void __launch_bounds__(kMoveThreads, 12) evict_move_kernel(const __grid_constant__ EvictArgs a) {
   // per token: row in the old pages and in the new ones (head rows; -1: no such page), scales of k and v; per block: their greatest

@@ -23,11 +23,11 @@
 // columns' parts of the log-sum-exps.  Warps 4-7, 8-11, 12-15 and 16-19 (a key a lane) sum up the four row tiles' scores, each in a
 // quarter of TMEM.  Warps 20-23 bring the int8 keys and write them as bf16, and the keys' parts of the log-sum-exps.
 //
-// What bounds it (64 query and 8 KV heads, one GB300).  4096 new rows on a context of 8192: 308 us, 1340 TFLOP/s, the
-// exponentials included in no count.  The MMAs take 62 % of the time, their exponentials 55 % of that unit's; each row tile's four
-// warps wait for TMEM, multiply, exponentiate and add, and are busy for 80 %.  With few columns a unit's keys are what costs (their
-// way to shared memory as bf16, some 8 us a unit): 16 contexts of 4096 keys take 52 us with 1 to 128 columns each, so few
-// columns go to fa3_few.cu's kernel.
+// What bounds it (64 query and 8 KV heads, one GB300).  4096 new rows on a context of 8192: 308 us, 1340 TFLOP/s (exponentials
+// not counted).  The tensor pipe is active for 45 % of the time; the warps that sum, each row tile's four, wait for TMEM,
+// multiply, exponentiate and add, and are busy for 80 %.  With few columns a unit's keys are what costs (their way to shared
+// memory as bf16, some 8 us a unit): 16 contexts of 4096 keys take 51 us with 8 columns each as with 128, so few columns go to
+// fa3_few.cu's kernel.
 //
 // Every wait is bounded; on time-out the kernel sets FA3_DEVERR_TIMEOUT, waits for its
 // copies and MMAs, frees its TMEM and returns.
