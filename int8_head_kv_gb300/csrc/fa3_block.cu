@@ -12,6 +12,7 @@
 #include "fa3_packed.cuh"
 
 #include <algorithm>
+#include <atomic>
 
 namespace fa3 {
 namespace {
@@ -93,6 +94,7 @@ __device__ __forceinline__ uint2 codes8(uint4 v, float s, float rs, bool plain) 
 // of 6168 new tokens, 8 heads, blocks of 32: 54 us; 13.1 so).
 constexpr int kHeld = 8, kAsk = 8;
 constexpr int kAppendSmem = kAppendThreads * kHeld * 16;
+static_assert(kAppendSmem + 1024 <= 48 * 1024, "no attribute of the kernel's needed");
 template <int W>
 __global__ void __launch_bounds__(kAppendThreads) block_append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int kHeads = kAppendThreads / 32 / W;
@@ -658,7 +660,6 @@ FA3_API int fa3_append_gqa_block_paged(const uint16_t* k, const uint16_t* v, int
   auto* kernel = W == 1 ? block_append_kernel<1> : W == 2 ? block_append_kernel<2> : W == 4 ? block_append_kernel<4>
                                                                                             : block_append_kernel<8>;
   const int heads = warps / W;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAppendSmem) != cudaSuccess) return FA3_ECUDA;
   return cuda_status(launch_pdl(kernel, dim3((unsigned)pieces, (unsigned)((Hkv + heads - 1) / heads), 2), dim3(kAppendThreads), kAppendSmem,
                                 static_cast<cudaStream_t>(stream), a));
 }
@@ -695,9 +696,17 @@ FA3_API int fa3_evict_gqa_block_paged(int8_t* k_cache, int8_t* v_cache, float* k
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const auto move = wide ? evict_move_kernel<uint4> : evict_move_kernel<uint2>;
   const int move_smem = a.rows * 24 + a.rows / block * 8;
-  if (cudaFuncSetAttribute(evict_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostKeys * 4) != cudaSuccess ||
-      cudaFuncSetAttribute(move, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostBlock * 24 + 8) != cudaSuccess)
-    return FA3_ECUDA;
+  static std::atomic<bool> set[64];                          // the kernels' attributes, once a device
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return FA3_ECUDA;
+  if (dev >= 64 || !set[dev].load(std::memory_order_acquire)) {
+    constexpr auto kMost = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    if (cudaFuncSetAttribute(evict_pick_kernel, kMost, kMostKeys * 4) != cudaSuccess ||
+        cudaFuncSetAttribute(evict_move_kernel<uint4>, kMost, kMostBlock * 24 + 8) != cudaSuccess ||
+        cudaFuncSetAttribute(evict_move_kernel<uint2>, kMost, kMostBlock * 24 + 8) != cudaSuccess)
+      return FA3_ECUDA;
+    if (dev < 64) set[dev].store(true, std::memory_order_release);
+  }
   const LaunchTogether together(s);
   if (launch_pdl(evict_pick_kernel, dim3((unsigned)Hkv, (unsigned)B), dim3(kPickThreads), (size_t)smem, s, a) != cudaSuccess)
     return FA3_ECUDA;
