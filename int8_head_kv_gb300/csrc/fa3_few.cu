@@ -2,7 +2,7 @@
 //
 // The call's arithmetic is fa3_chunk.cu's (block-scaled variant); here it is HBM-bound: each KV byte meets a handful of
 // query columns, too few for the 128 rows of tcgen05.mma.  A column is a new row's query head; a column tile is RT rows x the
-// group's G heads, up to 8 NT columns, as the N side of warp-level MMAs with 16 tokens as the M side:
+// group's G heads, up to 8 NT columns (8, 16 or 32), as the N side of warp-level MMAs with 16 tokens as the M side:
 //   * scores  S^T[16 tokens x 8 columns] = K . Q^T by m16n8k16 f16, int8 codes exact in fp16, bf16 queries exact after a
 //     power of two by column; the contraction order is permuted so that a thread's K and Q words are the bytes it holds;
 //   * x = s log2(e) + log2(value scale), P = 2^(x - m) as fp16, O^T += V^T . P^T on V's bare codes, and the row sum takes P
@@ -16,9 +16,8 @@
 //
 // What bounds it (one GB300, 64 query and 8 KV heads).  16 one-token rows of 4096 keys: 29.5 us, of 16384 keys 89 us, and 14.5 us
 // of 1024: HBM at 6.8 TB/s behind some 10 us that every call pays (launch, plan, a chain of lengths, page, scales and first keys, the
-// combine kernel).  With two column tiles the MMAs, conversions and exponentials of a step count as well: two rows each
-// 33 us, four, whose 32 columns are two units that read the keys twice, 54 (half of the issue slots, three warps a
-// scheduler).  A merge by whoever comes last to a unit, in place of the second kernel, took 33.5 us for the first case.
+// combine kernel).  With more columns the MMAs, conversions and exponentials of a step count as well: two rows each
+// 33 us, four 46 (half of the issue slots, three and two warps a scheduler).  A merge by whoever comes last to a unit, in place of the second kernel, took 33.5 us for the first case.
 #include "fa3_few.cuh"
 
 #include <cuda_bf16.h>
@@ -36,9 +35,15 @@ namespace {
 constexpr int kD = 128;
 constexpr int kStep = 16;          // tokens of a warp's step
 constexpr int kWarps = 4, kThreadsF = 32 * kWarps;
-constexpr int kStages = 2;
 constexpr int kStageBytes = 2 * kStep * kD;                // K, then V rows
-constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+// The attention kernel's shared memory: rings, and where the columns are too many for registers their queries and constants.
+template <int NT>
+struct FewSmem {
+  static constexpr bool kQueries = NT > 2;
+  static constexpr int kStages = NT > 2 ? 4 : 2, kCtas = NT == 1 ? 4 : NT == 2 ? 3 : 2;   // of a ring; an SM
+  static constexpr int kRing = kWarps * kStages * kStageBytes;
+  static constexpr int kBytes = kRing + (kQueries ? NT * (4 * 32 + 4) * 16 : 0);
+};
 
 constexpr float kNone = -1e30f;    // the reference of a column that has seen no key
 // What a unit costs beside its steps, and the least part of the line a CTA takes (enough for a part inside a unit to hold a
@@ -223,13 +228,16 @@ __device__ __forceinline__ LineF find_begin(const P& p, int cta, int lane, Begin
 }
 
 template <int NT>
-__global__ void __launch_bounds__(kThreadsF, NT == 1 ? 4 : 3) few_rows_kernel(const __grid_constant__ FewParams p) {
+__global__ void __launch_bounds__(kThreadsF, FewSmem<NT>::kCtas) few_rows_kernel(const __grid_constant__ FewParams p) {
   // A 128-byte row stores its 16-byte chunk c at position c ^ f(row & 7), f(r) = (r & 6) ^ 4 (r & 1): every 8-lane
   // phase of the K and V fragment loads below then touches 8 distinct 16-byte bank groups.
   extern __shared__ __align__(128) uint8_t fsm[];
-  constexpr int kCols = 8 * NT;
+  constexpr int kCols = 8 * NT, kStages = FewSmem<NT>::kStages;
+  constexpr bool kShared = FewSmem<NT>::kQueries;
+  uint4* const sm_q = reinterpret_cast<uint4*>(fsm + FewSmem<NT>::kRing);   // [tile][4][32]: fragments of Q^T
+  float4* const sm_c = reinterpret_cast<float4*>(sm_q + NT * 4 * 32);       // [tile][4]: two columns' factors and last keys
   float (*sm_o)[kCols][kD] = reinterpret_cast<float (*)[kCols][kD]>(fsm);   // at a unit's end, in the rings' place
-  static_assert(kWarps * kCols * kD * 4 <= kRingBytes, "partial O fits in the rings");
+  static_assert(kWarps * kCols * kD * 4 <= FewSmem<NT>::kRing, "partial O fits in the rings");
   __shared__ float sm_m[kWarps][kCols], sm_l[kWarps][kCols];
   pdl_wait();
   pdl_launch_dependents();
@@ -263,10 +271,13 @@ __global__ void __launch_bounds__(kThreadsF, NT == 1 ? 4 : 3) few_rows_kernel(co
       const bool whole = s0 == 0 && s1 == steps;
       // Q^T fragments: thread (r, qd) holds column 8 nt + r's values [16 qd, +16) and [64 + 16 qd, +16) as fp16, times a
       // power of two that brings the column's largest to [2^14, 2^15).  The values are asked for before all else.
-      uint4 qv[NT][4];
+      // (Where they are shared, a warp makes one tile's.)
+      constexpr int NQ = kShared ? 1 : NT;
+      static_assert(!kShared || NT == kWarps, "a tile a warp");
+      uint4 qv[NQ][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int col = 8 * nt + r, ri = (int)divu32((uint32_t)col, p.div_G);
+      for (int nt = 0; nt < NQ; ++nt) {
+        const int col = 8 * (kShared ? warp : nt) + r, ri = (int)divu32((uint32_t)col, p.div_G);
         const uint16_t* row = p.q + (int64_t)(s.q0 + i0 + ri) * p.q_stride + (int64_t)(g * p.G + col - ri * p.G) * kD;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -311,11 +322,11 @@ __global__ void __launch_bounds__(kThreadsF, NT == 1 ? 4 : 3) few_rows_kernel(co
         if (m < n_my) issue(m, m);
         cp_async_commit();
       }
-      uint32_t qh[NT][8][2];
-      float f0[NT], f1[NT];
-      int lim0[NT], lim1[NT];                                   // last key of columns 8 nt + 2 qd, + 1; -1: no column
+      uint32_t qh[NQ][8][2];
+      float f0[NQ], f1[NQ];
+      int lim0[NQ], lim1[NQ];                                   // last key of columns 8 nt + 2 qd, + 1; -1: no column
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int nt = 0; nt < NQ; ++nt) {
         const uint4 (&v)[4] = qv[nt];
         uint32_t top = 0;
 #pragma unroll
@@ -336,18 +347,24 @@ __global__ void __launch_bounds__(kThreadsF, NT == 1 ? 4 : 3) few_rows_kernel(co
         const float inv = __uint_as_float((e - 14u) << 23) * p.sm_log2;
         f0[nt] = __shfl_sync(0xffffffffu, inv, 4 * (2 * qd));
         f1[nt] = __shfl_sync(0xffffffffu, inv, 4 * (2 * qd + 1));
-        const int ca = 8 * nt + 2 * qd;
+        const int ca = 8 * (kShared ? warp : nt) + 2 * qd;
         lim0[nt] = ca < cols ? c0 + i0 + (int)divu32((uint32_t)ca, p.div_G) : -1;
         lim1[nt] = ca + 1 < cols ? c0 + i0 + (int)divu32((uint32_t)(ca + 1), p.div_G) : -1;
       }
+      if constexpr (kShared) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          sm_q[(warp * 4 + i) * 32 + lane] = make_uint4(qh[0][2 * i][0], qh[0][2 * i][1], qh[0][2 * i + 1][0], qh[0][2 * i + 1][1]);
+        if (r == 0) sm_c[warp * 4 + qd] = make_float4(f0[0], f1[0], __int_as_float(lim0[0]), __int_as_float(lim1[0]));
+        __syncthreads();
+      }
       // kNone in place of -infinity: differences of references stay numbers
       float m0[NT], m1[NT], l0[NT], l1[NT], o[NT][8][4];
-      int lim = 0x7fffffff;                                     // the last key that all columns see
+      const int lim = cols == kCols ? c0 + i0 : -1;             // the last key that all columns see
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         m0[nt] = m1[nt] = kNone;
         l0[nt] = l1[nt] = 0.f;
-        lim = min(lim, min(lim0[nt], lim1[nt]));
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
       }
@@ -376,22 +393,40 @@ __global__ void __launch_bounds__(kThreadsF, NT == 1 ? 4 : 3) few_rows_kernel(co
           const uint4 k0 = lds128(chunk_addr(kst, r, qd)), k1 = lds128(chunk_addr(kst, r, 4 + qd)),
                       k2 = lds128(chunk_addr(kst, r + 8, qd)), k3 = lds128(chunk_addr(kst, r + 8, 4 + qd));
 #pragma unroll
-          for (int st = 0; st < 8; ++st) {
-            uint32_t a0, a1, a2, a3;
-            codes_to_f16(word(st < 4 ? k0 : k1, st & 3), a0, a2);  // row r: the thread's values 4 st .. 4 st + 3
-            codes_to_f16(word(st < 4 ? k2 : k3, st & 3), a1, a3);  // row r + 8
+          for (int i = 0; i < 4; ++i) {
+            uint32_t ka[2][4];                                  // row r: the thread's values 4 st .. 4 st + 3; row r + 8
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816(cf[nt], a0, a1, a2, a3, qh[nt][st][0], qh[nt][st][1]);
+            for (int e = 0; e < 2; ++e) {
+              const int st = 2 * i + e;
+              codes_to_f16(word(st < 4 ? k0 : k1, st & 3), ka[e][0], ka[e][2]);
+              codes_to_f16(word(st < 4 ? k2 : k3, st & 3), ka[e][1], ka[e][3]);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              uint4 b;
+              if constexpr (kShared) b = sm_q[(nt * 4 + i) * 32 + lane];
+              else b = make_uint4(qh[nt][2 * i][0], qh[nt][2 * i][1], qh[nt][2 * i + 1][0], qh[nt][2 * i + 1][1]);
+              mma16816(cf[nt], ka[0][0], ka[0][1], ka[0][2], ka[0][3], b.x, b.y);
+              mma16816(cf[nt], ka[1][0], ka[1][1], ka[1][2], ka[1][3], b.z, b.w);
+            }
           }
         }
         const uint4 v0 = lds128(chunk_addr(vst, 2 * qd, r)), v1 = lds128(chunk_addr(vst, 2 * qd + 1, r)),
                     v2 = lds128(chunk_addr(vst, 2 * qd + 8, r)), v3 = lds128(chunk_addr(vst, 2 * qd + 9, r));
         __syncwarp();                                           // every lane has its fragments: the stage may be refilled
-        const bool masked = __any_sync(0xffffffffu, t0 + kStep - 1 > lim);
+        const bool masked = t0 + kStep - 1 > lim;
         uint32_t b0[NT], b1[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const float e0 = f0[nt] * ks, e1 = f1[nt] * ks;
+          float fa, fb;
+          int la, lb;
+          if constexpr (kShared) {
+            const float4 c = sm_c[nt * 4 + qd];
+            fa = c.x, fb = c.y, la = __float_as_int(c.z), lb = __float_as_int(c.w);
+          } else {
+            fa = f0[nt], fb = f1[nt], la = lim0[nt], lb = lim1[nt];
+          }
+          const float e0 = fa * ks, e1 = fb * ks;
           float y[4];
           auto exponents = [&]() {                              // of tokens r, r + 8 and columns 2 qd, 2 qd + 1
             const float a0 = lv - m0[nt], a1 = lv - m1[nt];
@@ -401,10 +436,10 @@ __global__ void __launch_bounds__(kThreadsF, NT == 1 ? 4 : 3) few_rows_kernel(co
             y[3] = fmaf(cf[nt][3], e1, a1);
             if (masked) {
               const int ta = t0 + r, tb = ta + 8;
-              y[0] = ta <= lim0[nt] ? y[0] : -CUDART_INF_F;
-              y[1] = ta <= lim1[nt] ? y[1] : -CUDART_INF_F;
-              y[2] = tb <= lim0[nt] ? y[2] : -CUDART_INF_F;
-              y[3] = tb <= lim1[nt] ? y[3] : -CUDART_INF_F;
+              y[0] = ta <= la ? y[0] : -CUDART_INF_F;
+              y[1] = ta <= lb ? y[1] : -CUDART_INF_F;
+              y[2] = tb <= la ? y[2] : -CUDART_INF_F;
+              y[3] = tb <= lb ? y[3] : -CUDART_INF_F;
             }
           };
           exponents();
@@ -808,9 +843,16 @@ __global__ void __launch_bounds__(kThreadsF, 4) few_weights_kernel(const __grid_
   }
 }
 
-// Column tiles of 8 where sequences have 8 columns or fewer on average, of 16 otherwise.
-int n_tiles(int n, int B, int G) { return (int64_t)std::max(1, n / B) * G <= 8 ? 1 : 2; }
-int ctas_of(int nt, int sms) { return sms * (nt == 1 ? 4 : 3); }
+// Columns of a sequence on average (whole rows, for some of n may be nobody's).
+int64_t columns_of(int n, int B, int G) { return (int64_t)std::max(1, n / B) * G; }
+// Units of 8, 16 or 32 columns, as sequences have on average.  16 sequences of 4096 keys, 16 columns each: 33 us in units of 16,
+// 43 of 32; 32 columns: 54.5 in two units of 16, 46 in one of 32, whose keys are read and converted once (but half as many
+// warps are there to hide the waits, and its queries have to lie in shared memory).
+int n_tiles(int n, int B, int G) {
+  const int64_t cols = columns_of(n, B, G);
+  return cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
+}
+int ctas_of(int nt, int sms) { return sms * (nt == 1 ? FewSmem<1>::kCtas : nt == 2 ? FewSmem<2>::kCtas : FewSmem<4>::kCtas); }
 size_t bytes_of(int nt, int ctas) {
   return (size_t)ctas * (2 * 8 * nt * (kD * sizeof(float) + sizeof(float2)) + sizeof(CutF));
 }
@@ -821,7 +863,7 @@ cudaError_t launch(FewParams& p, void* workspace, cudaStream_t s) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return cudaErrorInvalidDevice;
   if (dev >= 64 || !set[dev].load(std::memory_order_acquire)) {
-    const cudaError_t e = cudaFuncSetAttribute(few_rows_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    const cudaError_t e = cudaFuncSetAttribute(few_rows_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, FewSmem<NT>::kBytes);
     if (e != cudaSuccess) return e;
     if (dev < 64) set[dev].store(true, std::memory_order_release);
   }
@@ -831,7 +873,7 @@ cudaError_t launch(FewParams& p, void* workspace, cudaStream_t s) {
   p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)2 * p.ctas * 8 * NT * kD);
   p.cuts = reinterpret_cast<CutF*>(p.part_ml + (size_t)2 * p.ctas * 8 * NT);
   const LaunchTogether together(s);
-  cudaError_t e = launch_pdl(few_rows_kernel<NT>, dim3((unsigned)p.ctas), dim3(kThreadsF), kRingBytes, s, p);
+  cudaError_t e = launch_pdl(few_rows_kernel<NT>, dim3((unsigned)p.ctas), dim3(kThreadsF), FewSmem<NT>::kBytes, s, p);
   if (e != cudaSuccess) return e;
   // Four warps a column where units may have many parts; one token of 32768 keys (76 parts a unit): 25.5 us with one warp,
   // 22.5 with four; but 16 of 1024 keys: 14.4 and 17.0, for its more blocks.
@@ -844,7 +886,9 @@ cudaError_t launch(FewParams& p, void* workspace, cudaStream_t s) {
 
 bool few_rows(int n, int B, int Hkv, int G, int T_max) {
   const double units = (double)n + B;
-  return G <= 16 && (int64_t)n * G <= (int64_t)48 * B && units * Hkv * (T_max / kStep + kUnitSteps + 1.0) < 2147483648.0;
+  // Up to 32 columns a sequence: 16 sequences of 4096 keys, 64 query and 8 KV heads, with 1, 2, 3, 4 and 5 rows each take 29.5, 33, 45,
+  // 46 and 78 us here, and 58 to 61 in fa3_chunk.cu's kernel.
+  return G <= 16 && columns_of(n, B, G) <= 32 && units * Hkv * (T_max / kStep + kUnitSteps + 1.0) < 2147483648.0;
 }
 size_t few_rows_workspace(int n, int B, int G, int sms) {
   if (G > 16) return 0;
@@ -861,7 +905,7 @@ cudaError_t few_rows_attn(const FewCall& c, const int32_t* table, int num_pages,
   p.div_G = make_divu32((uint32_t)c.G);
   const int nt = n_tiles(c.n, c.B, c.G);
   p.ctas = ctas_of(nt, c.sms);
-  return nt == 1 ? launch<1>(p, workspace, s) : launch<2>(p, workspace, s);
+  return nt == 1 ? launch<1>(p, workspace, s) : nt == 2 ? launch<2>(p, workspace, s) : launch<4>(p, workspace, s);
 }
 
 bool few_rows_weights(int n, int B, int Hkv, int G, int T_max) {

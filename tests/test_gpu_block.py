@@ -297,6 +297,19 @@ def test_attention_of_one_query_expanded_over_rows():
                 F.attn_weights_gqa_block_paged(q, a[0], a[2], l2, w, *a[4:], SM)
 
 
+@pytest.mark.parametrize("Hq,Hkv,q_lens,kv_lens", [
+    (8, 1, [4, 4], [900, 33]), (8, 1, [3, 4, 3], [3, 16, 17]), (16, 1, [2, 2, 2], [2, 700, 15]), (40, 8, [6, 5, 7], [6, 20, 400]),
+    (11, 1, [2, 2], [129, 64]), (13, 1, [2, 2, 1, 0, 4], [500, 2, 1, 0, 77]), (2, 2, [32, 30, 20], [1500, 30, 21]),
+    (8, 1, [20, 1, 1, 1, 1, 1], [3000, 1, 20, 300, 64, 5])])
+def test_attention_units_of_32_columns(Hq, Hkv, q_lens, kv_lens):
+    F, rng = fa3(), np.random.default_rng(9)
+    c = _rows(rng, _cache(rng, kv_lens, 48, 16, Hkv), q_lens, Hq, lead=1)
+    out, lse = _attend(F, c)
+    _check_attention(c, out, lse)
+    out2, _ = _attend(F, c, lse=False, strided=True)
+    assert np.array_equal(out, out2)
+
+
 def test_attention_long_contexts_split_over_the_gpu():
     F, rng = fa3(), np.random.default_rng(11)
     for q_lens, kv_lens, Hq, Hkv in (([1], [20000], 8, 1), ([70, 1], [9000, 3000], 6, 2)):
