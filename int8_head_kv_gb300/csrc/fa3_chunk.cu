@@ -58,8 +58,8 @@
 // of keys the key scale is a factor of the exponent, x = S k_scale softmax_scale log2(e) + log2(v_scale),
 // so that V's bare codes are the operand of P.V, and the row sum takes P / v_scale.  Warp 2
 // writes a step's scales, their logarithms and inverses, to shared memory, two steps ahead.  4096 rows on
-// 8192 keys: 751 us, 1099 TFLOP/s, 10 % more than with one scale a head: the softmax warps, the longest
-// link of the chain, read the scales and have a fused operation more a score.  Batches of few
+// 8192 keys: 736 us, 1121 TFLOP/s, 8 % more than with one scale a head (blocks of 32 or 64: 751 us): the softmax
+// warps, the longest link of the chain, wait for the scales, and read one for each group.  Batches of few
 // rows a sequence take fa3_few.cu's kernels (16 one-token rows of 4096 keys: 29.5 us there).
 //
 // Every wait is bounded; on time-out the kernel sets FA3_DEVERR_TIMEOUT, waits for its
@@ -981,6 +981,11 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
           FA3_TMEM_LD16(scol, v0);
           // The reference, 7 (log2 units) below the row's maximum.  Rounded up, and the difference below is exact where
           // it matters: P stays below 2^15 whatever the size of the scores.
+          float3 whole;                                       // a tile of one group
+          if constexpr (GROUP == kKeys) {
+            whole = group(0);
+            mx = __fmaf_ru(mx, whole.x, whole.y);
+          }
           mx = __fadd_ru(BLOCK ? mx : __fmul_ru(mx, c), -7.f);
           // Lazy rescale: the reference moves only when it would by more than 8; then O (P.V up to this buffer's
           // step before) is scaled in place.  No key yet: -inf - (-inf) is no difference.
@@ -1012,7 +1017,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
           // 16 c4 .. 16 c4 + 15); the row sum takes the weights before the rounding.
           float l0 = 0.f, l1 = 0.f;
           // 16 keys of one group; a group's numbers are asked for before the wait for its scores
-          auto ask = [&](int k) { return BLOCK ? group(k) : make_float3(c, 0.f, 0.f); };
+          auto ask = [&](int k) { return GROUP == kKeys ? whole : BLOCK ? group(k) : make_float3(c, 0.f, 0.f); };
           float g0 = 0.f, g1 = 0.f;
           auto weigh = [&](const uint32_t (&w)[16], uint32_t (&pk)[8], const float3& s, bool second) {
             const float f = BLOCK ? s.x : c, a = BLOCK ? s.y + mc : mc, inv = s.z;
@@ -1023,7 +1028,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
               fma2(p0, p1, __uint_as_float(w[e]), __uint_as_float(w[e + 1]), f, f, a, a);
               p0 = ex2_approx(p0);
               p1 = ex2_approx(p1);
-              if constexpr (BLOCK)
+              if constexpr (GROUP == 16 || GROUP == 32)
                 add2(g0, g1, g0, g1, p0, p1);
               else
                 add2(l0, l1, l0, l1, p0, p1);
@@ -1055,7 +1060,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
           weigh(v1, pb, sb, true);
           tmem_st8(scol + 48, pa);
           tmem_st8(scol + 56, pb);
-          l_run += l0 + l1;
+          l_run = GROUP == kKeys ? fmaf(l0 + l1, whole.z, l_run) : l_run + (l0 + l1);
           tmem_wait_st();
           tc_fence_before();
         }
@@ -1280,10 +1285,13 @@ int chunk_attn(ChunkParams& p, int D, float softmax_scale, void* workspace, size
   if (p.box && (!cache_map(&p.map_k, p.k, p.Hkv, cache_rows, p.box) || !cache_map(&p.map_v, p.v, p.Hkv, cache_rows, p.box)))
     return FA3_ECUDA;
   const LaunchTogether together(s);
-  // a block's keys in groups of 32 where its size allows it, of 16 otherwise (4096 rows on 8192 keys, blocks of 128:
-  // 751 us with groups of 32, 788 of 16)
-  const int st_main = !BLOCK ? launch_chunk<0>(p, sms, s) : p.page_size / p.per_page % 32 == 0 ? launch_chunk<32>(p, sms, s)
-                                                                                              : launch_chunk<16>(p, sms, s);
+  // a block's keys in groups of 128 or 32 where its size allows it, of 16 otherwise (4096 rows on 8192 keys, blocks of 128:
+  // 736 us with groups of 128, 751 of 32, 788 of 16)
+  const int block = BLOCK ? p.page_size / p.per_page : 0;
+  const int st_main = !BLOCK            ? launch_chunk<0>(p, sms, s)
+                      : block % kKeys == 0 ? launch_chunk<kKeys>(p, sms, s)
+                      : block % 32 == 0    ? launch_chunk<32>(p, sms, s)
+                                           : launch_chunk<16>(p, sms, s);
   if (st_main != FA3_OK) return st_main;
   if (sms > 1 && launch_pdl(chunk_combine_kernel<BLOCK>, dim3((unsigned)(sms - 1), (unsigned)(p.rows_max / 32)), dim3(256), 0, s,
                             p) != cudaSuccess)

@@ -280,6 +280,18 @@ def test_attention(Hq, Hkv, page, block, q_lens, kv_lens):
     assert none is None and np.array_equal(out, out2)
 
 
+@pytest.mark.parametrize("page,block,wide", [(128, 128, 2.0), (384, 128, 2.0 ** 20), (256, 256, 2.0 ** 20), (4096, 4096, 2.0)])
+def test_attention_of_blocks_that_hold_whole_key_tiles(page, block, wide):
+    F, rng = fa3(), np.random.default_rng(12)
+    for Hq, Hkv, q_lens, kv_lens in ((8, 2, [200, 1, 130], [700, 129, 130]), (4, 4, [300], [1100])):
+        c = _rows(rng, _cache(rng, kv_lens, page, block, Hkv), q_lens, Hq, lead=1)
+        c["vs"] *= np.exp2(rng.uniform(-np.log2(wide), 0, c["vs"].shape)).astype(np.float32)
+        out, lse = _attend(F, c)
+        _check_attention(c, out, lse)
+        out2, _ = _attend(F, c, lse=False, strided=True)
+        assert np.array_equal(out, out2)
+
+
 def test_attention_of_one_query_expanded_over_rows():
     F, rng = fa3(), np.random.default_rng(10)
     for q_lens in ([1, 1, 1], [60, 30, 40]):
