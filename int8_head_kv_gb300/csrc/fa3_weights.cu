@@ -11,7 +11,8 @@
 // The row's log-sum-exp goes into the product as well: with f the key's factor (its scale, softmax_scale and log2(e)), the exponent
 // is f (S - lse / f), and lse / f is a product of a number of the key's and one of the column's.  Both are split into
 // three bf16 parts, exactly, and the eight products of parts that count (what is left out is below 2^-31 of it) are one more
-// slice of the contraction.  A thread then reads nothing but its scores: with the log-sum-exps in shared memory, each warp reading
+// slice of the contraction, the last: the tensor pipe cuts its sums off relative to their largest term, which lse / f is as a
+// rule (weights of 4096 rows on 8192 keys were off by 1.5e-6 of them in the mean with the slice first, 6e-7 so).  A thread then reads nothing but its scores: with the log-sum-exps in shared memory, each warp reading
 // them anew, that memory was the bound (4460 cycles for 512 keys x 128 columns; the MMAs alone take 2048).
 //
 // Work.  A unit is 512 keys of one sequence and KV head, as four row tiles; a step is the scores of P new tokens x G heads
@@ -379,15 +380,15 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
           // S = K.Q^T: both K-major, 128-byte swizzle: 8-row groups 1024 B apart, 16 values of d 32 B apart within a half; the
           // slice of the log-sum-exp without swizzle, as 8-row groups 128 B and chunks of 8 values 2048 B apart
           uint32_t a = desc_lo(sbase + OFF_KW + x * kTile, 16), bd = desc_lo(sbase + OFF_QW + qs * kTile, 16);
-          mma_ss<desc_hi(128, false), desc_hi(128, false)>(lead, tmem + x * 128, desc_lo(sbase + OFF_KX + x * kSlice, 2048),
-                                                           desc_lo(sbase + OFF_QX + qs * kSlice, 2048), id, 0u);
 #pragma unroll 2
           for (int kk = 0; kk < kD / 16; ++kk) {
-            mma_ss<desc_hi(1024, true), desc_hi(1024, true)>(lead, tmem + x * 128, a, bd, id, 1u);
+            mma_ss<desc_hi(1024, true), desc_hi(1024, true)>(lead, tmem + x * 128, a, bd, id, (uint32_t)(kk > 0));
             const uint32_t next = kk == 3 ? (kHalfTile >> 4) - 3 * (32 >> 4) : 32 >> 4;
             a += next;
             bd += next;
           }
+          mma_ss<desc_hi(128, false), desc_hi(128, false)>(lead, tmem + x * 128, desc_lo(sbase + OFF_KX + x * kSlice, 2048),
+                                                           desc_lo(sbase + OFF_QX + qs * kSlice, 2048), id, 1u);
           commit_if(lead, bar(W_S_FULL) + 8u * x);
           done ^= 1u << x;
         }
