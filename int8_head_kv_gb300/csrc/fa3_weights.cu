@@ -11,8 +11,9 @@
 // The row's log-sum-exp goes into the product as well: with f the key's factor (its scale, softmax_scale and log2(e)), the exponent
 // is f (S - lse / f), and lse / f is a product of a number of the key's and one of the column's.  Both are split into
 // three bf16 parts, exactly, and the eight products of parts that count (what is left out is below 2^-31 of it) are one more
-// slice of the contraction, the last: the tensor pipe cuts its sums off relative to their largest term, which lse / f is as a
-// rule (weights of 4096 rows on 8192 keys were off by 1.5e-6 of them in the mean with the slice first, 6e-7 so).  A thread then reads nothing but its scores: with the log-sum-exps in shared memory, each warp reading
+// slice of the contraction, the last, and taken relative to the lse of the step's first column, which the exponent gets in float32:
+// the tensor pipe cuts its sums off relative to their largest term, which lse / f would be (weights of 4096 rows on 8192 keys
+// were off by 1.5e-6 of them in the mean with all of it as the first slice, 6e-7 as the last, 1.2e-7 so; 308, 309 and 312 us).  A thread then reads nothing but its scores: with the log-sum-exps in shared memory, each warp reading
 // them anew, that memory was the bound (4460 cycles for 512 keys x 128 columns; the MMAs alone take 2048).
 //
 // Work.  A unit is 512 keys of one sequence and KV head, as four row tiles; a step is the scores of P new tokens x G heads
@@ -24,7 +25,7 @@
 // columns' parts of the log-sum-exps.  Warps 4-7, 8-11, 12-15 and 16-19 (a key a lane) sum up the four row tiles' scores, each in a
 // quarter of TMEM.  Warps 20-23 bring the int8 keys and write them as bf16, and the keys' parts of the log-sum-exps.
 //
-// What bounds it (64 query and 8 KV heads, one GB300).  4096 new rows on a context of 8192: 308 us, 1340 TFLOP/s (exponentials
+// What bounds it (64 query and 8 KV heads, one GB300).  4096 new rows on a context of 8192: 312 us, 1320 TFLOP/s (exponentials
 // not counted).  The tensor pipe is active for 45 % of the time; the warps that sum, each row tile's four, wait for TMEM,
 // multiply, exponentiate and add, and are busy for 80 %.  With few columns a unit's keys are what costs (their way to shared
 // memory as bf16, some 8 us a unit): 16 contexts of 4096 keys take 51 us with 8 columns each as with 128, so few columns go to
@@ -268,6 +269,12 @@ __device__ __forceinline__ void i8x4_to_bf16x4(uint32_t w, uint32_t& lo, uint32_
   hi = two(__byte_perm(w, 0x43434343u, 0x4342));
 }
 
+// A step's exponents are taken relative to its first column's: -lse log2(e), or 0 where that is not a common number.
+__device__ __forceinline__ float center_of(float lse) {
+  const float c = lse * -1.4426950408889634f;
+  return fabsf(c) < 1e5f ? c : 0.f;
+}
+
 // A number as the sum of three bf16 numbers, exactly (24 bits are three times 8; each is the rest's upper half).
 __device__ __forceinline__ void three_parts(float x, uint32_t (&p)[3]) {
 #pragma unroll
@@ -458,10 +465,11 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
             ask(s + x + 2, v[(x + 2) % 3]);
             ok = warp_wait(bar(W_Q_EMPTY) + 8u * qs, q_par, lane, abort_flag, p.err);
             if (ok) {
+              const float center = center_of(__shfl_sync(0xffffffffu, v[x][0], 0));
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 uint32_t b[3];                               // an infinite lse: weights of nothing
-                three_parts(fminf(fmaxf(v[x][k] * -1.4426950408889634f, -1e6f), 1e6f), b);
+                three_parts(fminf(fmaxf(v[x][k] * -1.4426950408889634f - center, -1e6f), 1e6f), b);
                 sts128(sbase + OFF_QX + qs * kSlice + (uint32_t)(lane + 32 * k) * 16u,
                        make_uint4(b[0] | b[1] << 16, b[0] | b[2] << 16, b[1] | b[0] << 16, b[2] | b[1] << 16));
               }
@@ -556,8 +564,13 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
       const int clear = (max(min(u.tile * kKeysW + 128 * x + 128, u.nkv) - 1 - c, 0) + p.P - 1) / p.P - rt0;
       const int full = p.P * p.G == kCols ? u.nq / p.P - rt0 : 0;
       float total = 0.f, lost = 0.f;                          // the sum, and what its roundings lost (Kahan)
+      const int first = max(u.s0, seen);
+      const float* const lse = p.lse + (int64_t)(u.q0 + rt0 * p.P) * p.Hq + u.g * p.G;   // the first column's
+      float next = first < u.s1 ? lse[(int64_t)first * p.P * p.Hq] : 0.f;
 #pragma unroll 1
-      for (int s = max(u.s0, seen); s < u.s1; ++s) {
+      for (int s = first; s < u.s1; ++s) {
+        const float mu = center_of(next);
+        if (s + 1 < u.s1) next = lse[(int64_t)(s + 1) * p.P * p.Hq];
         ok = warp_wait(bar(W_S_FULL) + 8u * x, done & 1u, lane, abort_flag, p.err);
         if (!ok) break;
         ++done;
@@ -571,7 +584,7 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
             wait_ld16(v);
             float y[16];
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) mul2(y[e], y[e + 1], __uint_as_float(v[e]), __uint_as_float(v[e + 1]), f, f);
+            for (int e = 0; e < 16; e += 2) fma2(y[e], y[e + 1], __uint_as_float(v[e]), __uint_as_float(v[e + 1]), f, f, mu, mu);
             if (k < kCols) {
               FA3_TMEM_LD16(scol + k, v);
             } else {
@@ -595,7 +608,7 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
             wait_ld16(v);
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
-              const float y = ex2_approx(__uint_as_float(v[e]) * f), z = ex2_approx(__uint_as_float(v[e + 1]) * f);
+              const float y = ex2_approx(fmaf(__uint_as_float(v[e]), f, mu)), z = ex2_approx(fmaf(__uint_as_float(v[e + 1]), f, mu));
               a0 += k + e >= from && k + e < cols ? y : 0.f;
               a1 += k + e + 1 >= from && k + e + 1 < cols ? z : 0.f;
             }
