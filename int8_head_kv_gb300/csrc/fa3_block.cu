@@ -223,7 +223,8 @@ __global__ void __launch_bounds__(kAppendThreads) block_append_kernel(const __gr
 // greatest weights, the earliest of equal ones, up to `budget` in all; a context that fits the budget stays whole.
 //
 // The choice is a radix selection by one block a head and sequence: 16 contexts of 4096 tokens and 8 heads take 8.8 us, three of
-// up to 20001 tokens and 5 heads 13.0 (15 blocks: latency, barriers and instructions, far from HBM).  A cluster of blocks a head was slower.
+// up to 20001 tokens and 5 heads 13.0 (15 blocks: latency, barriers and instructions, far from HBM).  A cluster of blocks a head
+// was slower.
 constexpr int kPickThreads = 1024;
 constexpr int kDigitBits = 11, kBins = 1 << kDigitBits;
 constexpr int kMostKeys = 48 * 1024;                       // of a context that shared memory holds

@@ -14,10 +14,11 @@
 // warps take a unit's steps in turn, each through its own cp.async ring, and merge at its end; a cut unit's parts meet in
 // few_combine_kernel.
 //
-// What bounds it (one GB300, 64 query and 8 KV heads).  16 one-token rows of 4096 keys: 29.5 us, of 16384 keys 89 us, and 14.5 us
-// of 1024: HBM at 6.8 TB/s behind some 10 us that every call pays (launch, plan, a chain of lengths, page, scales and first keys, the
-// combine kernel).  With more columns the MMAs, conversions and exponentials of a step count as well: two rows each
-// 33 us, four 46 (half of the issue slots, three and two warps a scheduler).  A merge by whoever comes last to a unit, in place of the second kernel, took 33.5 us for the first case.
+// What bounds it (one GB300, 64 query and 8 KV heads).  16 one-token rows of 4096 keys take 29.5 us, of 16384 keys 89 to 93 us and
+// of 1024 14.5 us: HBM at 6.5 to 6.8 TB/s behind some 10 us that every call pays (launch, plan, a chain of lengths, page and first
+// keys, the combine kernel).  With more columns the MMAs, conversions and exponentials of a step count as well: two rows each
+// 33 us, four 46 (half of the issue slots, three and two warps a scheduler).  A merge by whoever comes last to a unit, in place
+// of the second kernel, took 33.5 us for the first case.
 #include "fa3_few.cuh"
 
 #include <cuda_bf16.h>
