@@ -741,6 +741,37 @@ def test_other_streams_and_graphs(q_lens, kv_lens):
     assert same(a) and same(b)
 
 
+@pytest.mark.parametrize("q_lens", [[1, 2], [150, 40]])
+def test_pages_beyond_32_bit_offsets(q_lens):
+    """The same calls on the first and on the last pages of pools of 4.6 GB give the same."""
+    F, rng = fa3(), np.random.default_rng(71)
+    num, page, block, Hkv, Hq, budget = 70000, 64, 32, 8, 16, 70
+    lens = np.array([400, 130], np.int32)
+    n, fill = sum(q_lens), int(lens.sum())
+    k, v, _ = _kv(rng, fill, Hkv, 128)
+    k, v, q = _bf(k).cuda(), _bf(v).cuda(), _bf(rng.standard_normal((n, Hq, 128))).cuda()
+    pools = [torch.empty(num, page, Hkv, 128, dtype=torch.int8, device="cuda") for _ in range(2)]
+    scales = [F.block_scale_pool(pools[0], block) for _ in range(2)]
+    w = F.attn_weight_pool(pools[0])
+    start = np.concatenate([[0], np.cumsum(q_lens)]).astype(np.int32)
+    results = []
+    for first in (0, num - 20):
+        table = first + np.arange(14, dtype=np.int32).reshape(2, 7)
+        new = first + np.arange(14, 18, dtype=np.int32).reshape(2, 2)
+        tt, tl, ts = _t(table), _t(lens), _t(start)
+        F.append_gqa_block_paged(k, v, *pools, *scales, tt, _t(np.array([0, 400, 530], np.int32)), tl)
+        lse = torch.zeros(n, Hq, device="cuda")
+        out = F.attn_gqa_block_paged(q, *pools, *scales, ts, tl, tt, SM, lse=lse)
+        F.attn_weights_gqa_block_paged(q, pools[0], scales[0], lse, w, ts, tl, tt, SM)
+        kept, nl = F.evict_gqa_block_paged(*pools, *scales, w, tt, tl, _t(new), budget, sinks=1, recent=5)
+        at = [(first + 14 + 2 * b + t // page, t % page) for b in range(2) for t in range(budget)]
+        pg, row = (torch.tensor(x, device="cuda") for x in zip(*at))
+        results.append([out, lse, kept, nl, pools[0][pg, row], pools[1][pg, row], scales[0][pg, row // block],
+                        scales[1][pg, row // block], w[pg, :, row]])
+    assert all(torch.equal(x, y) for x, y in zip(*results))
+    assert results[0][8].sum() > 0 and results[0][3].tolist() == [budget, budget]
+
+
 def test_refusals_on_the_gpu():
     F = fa3()
     pool = torch.zeros(4, 32, 2, 128, dtype=torch.int8, device="cuda")
