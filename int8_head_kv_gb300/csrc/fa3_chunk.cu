@@ -1095,7 +1095,9 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
       tc_fence_after();
       if (warp_active) {
         const bool whole = u.whole();
-        const float inv = !whole ? 1.f : l_run > 0.f ? (BLOCK ? 1.f : p.v_scale[u.g]) / l_run : 0.f;
+        // (block-scaled: rows see a key at least, and scores that are not finite make l_run NaN, or 0 with all at -inf, and the
+        // row NaN; an int8 row's scores are finite)
+        const float inv = !whole ? 1.f : BLOCK ? 1.f / l_run : l_run > 0.f ? p.v_scale[u.g] / l_run : 0.f;
         if constexpr (BLOCK)
           if (whole && active && (u.dual || x == 0) && p.lse) p.lse[orow] = log_sum(m_run, l_run);
         f_mine *= inv;
@@ -1174,7 +1176,7 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constan
   float l = 0.f, o[16] = {};
   for (int k = k0; k <= k1; ++k) {
     const float2 ml = p.part_ml[slot_of(k) * p.rows_max + prow];
-    if (ml.x == -CUDART_INF_F) continue;
+    if (ml.x == -CUDART_INF_F && ml.y == 0.f) continue;      // no key (with NaN for all scores the sum is NaN)
     const float f = ex2_approx(ml.x - m);
     l = fmaf(ml.y, f, l);
     const float4* po = p.part_o + slot_of(k) * (kD / 4) * p.rows_max + prow;
@@ -1187,7 +1189,7 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constan
       o[4 * q4 + 3] = fmaf(a.w, f, o[4 * q4 + 3]);
     }
   }
-  const float inv = l > 0.f ? (BLOCK ? 1.f : p.v_scale[cut.g]) / l : 0.f;
+  const float inv = BLOCK ? 1.f / l : l > 0.f ? p.v_scale[cut.g] / l : 0.f;
   uint32_t w[8];
 #pragma unroll
   for (int e = 0; e < 16; e += 2) {

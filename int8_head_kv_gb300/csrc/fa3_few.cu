@@ -120,9 +120,10 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 }
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-// Row values 4 lane .. 4 lane + 3 of a row whose weighted sum is a and whose weights' is l.
+// Row values 4 lane .. 4 lane + 3 of a row whose weighted sum is a and whose weights' is l.  (A row sees a key at least, so l is
+// positive where its scores are finite; infinite or NaN scores make l NaN, or 0 with all at -inf, and the row NaN.)
 __device__ __forceinline__ void put_row(__nv_bfloat16* row, int lane, const float (&a)[4], float l) {
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = 1.f / l;
   const __nv_bfloat162 x = __floats2bfloat162_rn(a[0] * inv, a[1] * inv), y = __floats2bfloat162_rn(a[2] * inv, a[3] * inv);
   *reinterpret_cast<uint2*>(row + 4 * lane) = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
 }

@@ -1,0 +1,90 @@
+"""Block-scaled cache at the edges of its numbers: query rows and log-sum-exps that are not finite, scores of very different
+sizes side by side, scales far from one, and tables far wider than their contexts.
+
+Tolerances beside test_gpu_block.py's.  A token's weight is added up term by term: the row's term exp(s - lse) is off by its own
+d (a score's error) and by what its exponent's parts lose.  Those are f = fl(k_scale fl(sm log2 e)), two roundings of |s|;
+fl(lse log2 e) and, in the kernel that takes it through the product, fl(1 / f), two of |lse|; and there the tensor pipe's last
+sum of nine terms, each cut off below 2^-24 of the greatest, |lse|: 16 U (|s| + |lse| + 1) holds them, U = 2^-24, and 4 U for
+the exponential.  Where that is no small number e, the term lies within exp(+-e).  64 additions a step and the compensated
+sum of steps: 68 U of the sum.
+"""
+import numpy as np
+import pytest
+import torch
+
+from helpers import fa3
+from oracle import fa3_oracle as O
+from test_gpu_block import SM, U, _attend, _bf, _cache, _check_attention, _f, _rows, _score_error, _t, _weigh
+
+pytestmark = pytest.mark.gpu
+
+
+def _weight_bounds(c, lse, before, sm=SM):
+    """The weights pool in float64 and each weight's tolerance."""
+    lse = lse.astype(np.float32).astype(np.float64)
+    q, ps, g = np.nan_to_num(c["q"]), c["page"], c["q"].shape[1] // c["Hkv"]
+    d = _score_error(c, sm)
+    ref, tol = before.astype(np.float64), np.zeros(before.shape)
+    for b, rows, h, s in O.block_scores(q, c["k"], c["ks"], c["table"], c["q_start"], c["kv_lens"], sm):
+        le = lse[rows, h][:, None]
+        with np.errstate(invalid="ignore"):
+            term = np.where(s == -np.inf, 0.0, np.exp(s - le))
+            e = d[rows, h][:, None] + (np.abs(np.where(s == -np.inf, 0.0, s)) + np.abs(le) + 1) * 16 * U + 4 * U
+            off = np.where(term == 0, 0.0, term * np.expm1(e))
+        t = np.arange(int(c["kv_lens"][b]))
+        at = (c["table"][b, t // ps], h // g, t % ps)
+        if h % g == 0:
+            ref[at] = np.where(t >= len(t) - (rows.stop - rows.start), 0.0, ref[at])
+        ref[at] += term.sum(0)
+        tol[at] += off.sum(0) + 68 * U * term.sum(0)
+    return ref, tol + np.abs(ref) * 2 * U
+
+
+def _lse(c, sm=SM):
+    return O.attention_block(np.nan_to_num(c["q"]), c["k"], c["v"], c["ks"], c["vs"], c["table"], c["q_start"], c["kv_lens"], sm,
+                             np.zeros(c["q"].shape), np.zeros(c["q"].shape[:2]))[1]
+
+
+def _within(got, ref, tol):
+    bad = ~(np.abs(got - ref) <= tol)
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4].tolist(), got[bad][:4], ref[bad][:4], tol[bad][:4])
+
+
+# ------------------------------------------------- query rows that are not finite
+# Hq, Hkv, q_lens, kv_lens: units of 8, 16 and 32 columns, one long context, two row tiles, one row tile, cut units of both
+SHAPES = [(8, 2, [1, 1, 1], [300, 2, 129]), (16, 1, [1, 1], [500, 77]), (8, 1, [4, 4, 4, 4], [900, 33, 64, 5]),
+          (8, 1, [1], [20000]), (8, 2, [200, 40, 130], [700, 129, 130]), (8, 2, [30, 25], [400, 25]), (8, 1, [70], [9000]),
+          (8, 2, [20], [6000])]
+
+
+def _spoil(c, value, rng):
+    """Some rows' queries of one head get `value`; which (row, head) did."""
+    hit = np.zeros(c["q"].shape[:2], bool)
+    q = c["q"].copy()
+    starts = c["q_start"]
+    for b in range(len(starts) - 1):
+        row = int(rng.integers(starts[b], starts[b + 1]))
+        hit[row, rng.integers(0, q.shape[1])] = True
+    hit[starts[0], 0] = True
+    q[hit, 5] = value
+    return dict(c, q=q), hit
+
+
+@pytest.mark.parametrize("Hq,Hkv,q_lens,kv_lens", SHAPES)
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("block", [16, 32, 128])
+def test_a_query_that_is_not_finite_shows_in_its_row_alone(Hq, Hkv, q_lens, kv_lens, value, block):
+    F, rng = fa3(), np.random.default_rng(81)
+    c = _rows(rng, _cache(rng, kv_lens, 128, block, Hkv), q_lens, Hq)
+    out, _ = _attend(F, c)
+    _check_attention(c, out, None)
+    for code in (None, -77):                                       # any codes; all scores infinite and of one sign
+        d = c
+        if code is not None:
+            d = dict(c, k=c["k"].copy())
+            d["k"][..., 5] = code
+            out, _ = _attend(F, d)
+        spoiled, hit = _spoil(d, value, rng)
+        got, _ = _attend(F, spoiled)
+        assert np.all(np.isnan(got[hit]))
+        assert np.array_equal(got[~hit], out[~hit])
