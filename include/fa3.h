@@ -546,7 +546,7 @@ int fa3_append_gqa_block_paged(const uint16_t* k, const uint16_t* v, int8_t* k_c
  * q        bf16 [n][Hq][128], row stride q_stride elements; values of rows outside the sequences do
  *          not matter.  out  bf16 [n][Hq][128].  lse  float [n][Hq], or NULL.
  * Rows outside the sequences and those of a sequence with bad lengths are left as they were.
- * A row and head whose query holds a NaN or an infinity has NaN in out; no other is affected.
+ * A row and head whose query holds a NaN or an infinity has NaN in out and lse; no other is affected.
  * An entry outside the pool sets FA3_DEVERR_PAGE and reads another page (that
  * sequence's output is not valid).  A value scale below 2^-80 counts as 2^-80.
  * Supported: D = 128, Hq / Hkv <= 128, n < 2^27 - 1; q_stride a multiple of 8; q, out and the caches 16-byte aligned,

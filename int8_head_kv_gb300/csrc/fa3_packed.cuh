@@ -93,8 +93,9 @@ __device__ __forceinline__ uint32_t rescaled(uint32_t codes4, float ratio) {
 
 constexpr float kLeastScale = 8.271806125530277e-25f;      // 2^-80: attention takes a smaller value scale as this
 
-// Natural logarithm of a row's sum of exponentials: the sum of 2^(.. - m) is l.
-__device__ __forceinline__ float log_sum(float m, float l) { return l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F; }
+// Natural logarithm of a row's sum of exponentials: the sum of 2^(.. - m) is l.  Scores that are not finite make l NaN, or 0
+// with all at -inf: NaN, as the row is.
+__device__ __forceinline__ float log_sum(float m, float l) { return l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : CUDART_NAN_F; }
 
 }  // namespace
 }  // namespace fa3

@@ -88,3 +88,18 @@ def test_a_query_that_is_not_finite_shows_in_its_row_alone(Hq, Hkv, q_lens, kv_l
         got, _ = _attend(F, spoiled)
         assert np.all(np.isnan(got[hit]))
         assert np.array_equal(got[~hit], out[~hit])
+
+
+@pytest.mark.parametrize("Hq,Hkv,q_lens,kv_lens", SHAPES)
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_the_log_sum_exp_of_a_query_that_is_not_finite_is_not_a_number(Hq, Hkv, q_lens, kv_lens, value):
+    F, rng = fa3(), np.random.default_rng(82)
+    c = _rows(rng, _cache(rng, kv_lens, 64, 32, Hkv), q_lens, Hq)
+    for code in (None, -77):
+        if code is not None:
+            c["k"][..., 5] = code
+        _, lse = _attend(F, c)
+        spoiled, hit = _spoil(c, value, rng)
+        _, got = _attend(F, spoiled)
+        assert np.all(np.isnan(got[hit]))
+        assert np.array_equal(got[~hit], lse[~hit])
