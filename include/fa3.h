@@ -568,6 +568,7 @@ int fa3_attn_gqa_block_paged(const uint16_t* q, const int8_t* k_cache, const int
  * and softmax_scale as for the attention call, whose lse it takes: a row then gives every head's
  * tokens 1 in all.  Sequences without new rows keep their weights.  The sums are the same on
  * every run; a page that sequences share gets both their sums, in either order.
+ * A row with NaN in its query or its log-sum-exp gives NaN to the tokens that it sees.
  * An entry outside the pool sets FA3_DEVERR_PAGE; its tokens get nothing.
  * Supported: as fa3_attn_gqa_block_paged; q_stride >= Hq * D; weights 4-byte aligned.
  * workspace  fa3_attn_weights_workspace_size() bytes, 16-byte aligned, not initialised;

@@ -469,8 +469,9 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
               const float center = center_of(__shfl_sync(0xffffffffu, v[x][0], 0));
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                uint32_t b[3];                               // an infinite lse: weights of nothing
-                three_parts(fminf(fmaxf(v[x][k] * -1.4426950408889634f - center, -1e6f), 1e6f), b);
+                uint32_t b[3];                               // an infinite lse: weights of nothing; NaN passes
+                const float y = v[x][k] * -1.4426950408889634f - center;
+                three_parts(y < -1e6f ? -1e6f : y > 1e6f ? 1e6f : y, b);
                 sts128(sbase + OFF_QX + qs * kSlice + (uint32_t)(lane + 32 * k) * 16u,
                        make_uint4(b[0] | b[1] << 16, b[0] | b[2] << 16, b[1] | b[0] << 16, b[2] | b[1] << 16));
               }

@@ -103,3 +103,35 @@ def test_the_log_sum_exp_of_a_query_that_is_not_finite_is_not_a_number(Hq, Hkv, 
         _, got = _attend(F, spoiled)
         assert np.all(np.isnan(got[hit]))
         assert np.array_equal(got[~hit], lse[~hit])
+
+
+# ------------------------------------------------------------ log-sum-exps and weights
+# Hq, Hkv, q_lens, kv_lens: fa3_few.cu's kernel with one and with several chunks of columns, fa3_weights.cu's with units
+# whole and cut
+WEIGHT_SHAPES = [(8, 2, [1, 3], [300, 129]), (16, 1, [5, 1], [500, 77]), (8, 2, [70, 40], [200, 41]), (100, 1, [30], [64]),
+                 (8, 1, [400, 30], [5000, 31])]
+
+
+@pytest.mark.parametrize("Hq,Hkv,q_lens,kv_lens", WEIGHT_SHAPES)
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("query", [True, False])
+def test_a_log_sum_exp_or_query_that_is_not_a_number_shows_in_the_weights(Hq, Hkv, q_lens, kv_lens, first, query):
+    F, rng = fa3(), np.random.default_rng(83)
+    c = _rows(rng, _cache(rng, kv_lens, 64, 32, Hkv), q_lens, Hq)
+    before = rng.random((c["num"], Hkv, 64)).astype(np.float32)
+    lse = _lse(c)
+    row, h = int(c["q_start"][0]) + (0 if first else q_lens[0] - 1), 0 if first else Hq - 1
+    sees = kv_lens[0] - q_lens[0] + (row - int(c["q_start"][0])) + 1
+    without = lse.copy()
+    without[row, h] = 1e4                                          # a row that gives nothing
+    ref, tol = _weight_bounds(c, without, before)
+    if query:
+        c["q"][row, h, 77] = np.nan
+    else:
+        lse[row, h] = np.nan
+    got = _weigh(F, c, lse, before)
+    shown = np.zeros(got.shape, bool)
+    t = np.arange(sees)
+    shown[c["table"][0, t // 64], h // (Hq // Hkv), t % 64] = True
+    assert np.all(np.isnan(got[shown]))
+    _within(got[~shown], ref[~shown], tol[~shown])
