@@ -548,7 +548,7 @@ int fa3_append_gqa_block_paged(const uint16_t* k, const uint16_t* v, int8_t* k_c
  * Rows outside the sequences and those of a sequence with bad lengths are left as they were.
  * A row and head whose query holds a NaN or an infinity has NaN in out and lse; no other is affected.
  * An entry outside the pool sets FA3_DEVERR_PAGE and reads another page (that
- * sequence's output is not valid).  A value scale below 2^-80 counts as 2^-80.
+ * sequence's output is not valid).  A value scale below 2^-80 counts as 2^-80.  Scores |s[t]| below 2^26.
  * Supported: D = 128, Hq / Hkv <= 128, n < 2^27 - 1; q_stride a multiple of 8; q, out and the caches 16-byte aligned,
  *          scales and lse 4-byte.
  * workspace  fa3_attn_block_workspace_size(n, B, Hq, Hkv, D) bytes, 16-byte aligned, not

@@ -270,6 +270,8 @@ __device__ __forceinline__ void i8x4_to_bf16x4(uint32_t w, uint32_t& lo, uint32_
   hi = two(__byte_perm(w, 0x43434343u, 0x4342));
 }
 
+constexpr float kMostLse = 268435456.f;                      // 2^28: log-sum-exps relative to a step's, in log2 units
+
 // A step's exponents are taken relative to its first column's: -lse log2(e), or 0 where that is not a common number.
 __device__ __forceinline__ float center_of(float lse) {
   const float c = lse * -1.4426950408889634f;
@@ -469,9 +471,10 @@ __global__ void __launch_bounds__(kThreadsW, 1) weights_kernel(const __grid_cons
               const float center = center_of(__shfl_sync(0xffffffffu, v[x][0], 0));
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                uint32_t b[3];                               // an infinite lse: weights of nothing; NaN passes
+                // with scores below 2^26 only an infinite lse, whose row's weights are nothing, lies outside; NaN passes
+                uint32_t b[3];
                 const float y = v[x][k] * -1.4426950408889634f - center;
-                three_parts(y < -1e6f ? -1e6f : y > 1e6f ? 1e6f : y, b);
+                three_parts(y < -kMostLse ? -kMostLse : y > kMostLse ? kMostLse : y, b);
                 sts128(sbase + OFF_QX + qs * kSlice + (uint32_t)(lane + 32 * k) * 16u,
                        make_uint4(b[0] | b[1] << 16, b[0] | b[2] << 16, b[1] | b[0] << 16, b[2] | b[1] << 16));
               }

@@ -135,3 +135,32 @@ def test_a_log_sum_exp_or_query_that_is_not_a_number_shows_in_the_weights(Hq, Hk
     shown[c["table"][0, t // 64], h // (Hq // Hkv), t % 64] = True
     assert np.all(np.isnan(got[shown]))
     _within(got[~shown], ref[~shown], tol[~shown])
+
+
+@pytest.mark.parametrize("Hq,Hkv,q_lens,kv_lens", WEIGHT_SHAPES)
+@pytest.mark.parametrize("size", [2.0 ** 14, 2.0 ** 17])
+def test_weights_of_scores_of_a_million(Hq, Hkv, q_lens, kv_lens, size):
+    """Queries of one power of two, so that a score's sum is exact; one key far above the others, which the weights are of."""
+    F, rng = fa3(), np.random.default_rng(84)
+    c = _rows(rng, _cache(rng, kv_lens, 64, 32, Hkv), q_lens, Hq)
+    sign = np.where(rng.random(c["q"].shape) < 0.5, -1.0, 1.0)
+    c["q"] = np.where(c["used"][:, None, None], sign * size, np.nan).astype(np.float32)
+    c["ks"] = np.where(np.isfinite(c["ks"]), np.float32(0.5), np.float32(np.nan))
+    lse = _lse(c).astype(np.float32)
+    assert np.abs(lse[c["used"]]).max() > 4e5
+    before = np.zeros((c["num"], Hkv, 64), np.float32)
+    ps, g, ref = 64, Hq // Hkv, np.zeros(before.shape)
+    low, high = np.zeros(before.shape), np.zeros(before.shape)
+    for b, rows, h, s in O.block_scores(np.nan_to_num(c["q"]), c["k"], c["ks"], c["table"], c["q_start"], c["kv_lens"], SM):
+        le = lse[rows, h].astype(np.float64)[:, None]
+        seen = s > -np.inf
+        x = np.where(seen, s, 0) - le
+        e = (np.abs(np.where(seen, s, 0)) + np.abs(le) + 1) * 16 * U + 4 * U
+        t = np.arange(int(c["kv_lens"][b]))
+        at = (c["table"][b, t // ps], h // g, t % ps)
+        low[at] += np.where(seen, np.exp(np.minimum(x - e, 80)), 0).sum(0)
+        high[at] += np.where(seen, np.exp(np.minimum(x + e, 80)), 0).sum(0)
+    got = _weigh(F, c, lse, before)
+    assert np.all(np.isfinite(got))
+    bad = (got < low * (1 - 2.0 ** -16) - 1e-30) | (got > high * (1 + 2.0 ** -16) + 1e-30)
+    assert not bad.any(), (int(bad.sum()), got[bad][:4], low[bad][:4], high[bad][:4])
