@@ -11,8 +11,8 @@
 // The row's log-sum-exp goes into the product as well: with f the key's factor (its scale, softmax_scale and log2(e)), the exponent
 // is f (S - lse / f), and lse / f is a product of a number of the key's and one of the column's.  Both are split into
 // three bf16 parts, exactly, and the eight products of parts that count (what is left out is below 2^-31 of it) are one more
-// slice of the contraction.  It is the last, and taken relative to the lse of the step's first column, which the exponent gets
-// in float32: the tensor pipe cuts its sums off relative to their largest term, which lse / f would be (weights of 4096
+// slice of the contraction.  It is the last, and taken relative to the lse of the step's first column (a common one's: below 64),
+// which the exponent gets in float32: the tensor pipe cuts its sums off relative to their largest term, which lse / f would be (weights of 4096
 // rows on 8192 keys were off by 1.5e-6 of them in the mean with all of it as the first slice, 6e-7 as the last, 1.2e-7 so;
 // 308, 309 and 312 us).  A thread then reads little but its scores: with the log-sum-exps in shared memory, each warp reading
 // them anew, that memory was the bound (4460 cycles for 512 keys x 128 columns; the MMAs alone take 2048).
@@ -272,10 +272,12 @@ __device__ __forceinline__ void i8x4_to_bf16x4(uint32_t w, uint32_t& lo, uint32_
 
 constexpr float kMostLse = 268435456.f;                      // 2^28: log-sum-exps relative to a step's, in log2 units
 
-// A step's exponents are taken relative to its first column's: -lse log2(e), or 0 where that is not a common number.
+// A step's exponents are taken relative to its first column's: -lse log2(e), or 0 where that is 64 or more.  A column's weights
+// are off by the rounding of the centre's size as well as of its own log-sum-exp's, and rows of large scores stand beside rows
+// of small ones: with a centre of 1000 their weights were off by 1e-4.
 __device__ __forceinline__ float center_of(float lse) {
   const float c = lse * -1.4426950408889634f;
-  return fabsf(c) < 1e5f ? c : 0.f;
+  return fabsf(c) < 64.f ? c : 0.f;
 }
 
 // A number as the sum of three bf16 numbers, exactly (24 bits are three times 8; each is the rest's upper half).

@@ -164,3 +164,21 @@ def test_weights_of_scores_of_a_million(Hq, Hkv, q_lens, kv_lens, size):
     assert np.all(np.isfinite(got))
     bad = (got < low * (1 - 2.0 ** -16) - 1e-30) | (got > high * (1 + 2.0 ** -16) + 1e-30)
     assert not bad.any(), (int(bad.sum()), got[bad][:4], low[bad][:4], high[bad][:4])
+
+
+@pytest.mark.parametrize("Hq,Hkv,q_lens,kv_lens", WEIGHT_SHAPES)
+@pytest.mark.parametrize("large", [0.0, 2.0 ** 6, 2.0 ** 10])
+def test_weights_of_small_rows_beside_large_ones(Hq, Hkv, q_lens, kv_lens, large):
+    """Every token's bound is that of its own rows: the first row of a sequence has the largest scores, in its group's
+    first head, and another in the middle; they give their weight to few tokens."""
+    F, rng = fa3(), np.random.default_rng(85)
+    c = _rows(rng, _cache(rng, kv_lens, 64, 32, Hkv), q_lens, Hq)
+    g = Hq // Hkv
+    size = np.exp2(np.resize([0, -3, -40, -1, -7], c["q"].shape[0] * Hq)).reshape(-1, Hq)
+    for b, n in enumerate(q_lens):
+        for i in (0, n // 2):
+            size[c["q_start"][b] + i, ::g] = large
+    c["q"] *= size[..., None].astype(np.float32)
+    lse = _lse(c)
+    before = (rng.random((c["num"], Hkv, 64)) * 0.01).astype(np.float32)
+    _within(_weigh(F, c, lse, before), *_weight_bounds(c, lse, before))
