@@ -487,7 +487,7 @@ __device__ __forceinline__ float put_query_row(const uint16_t* row, bool active,
     }
     const uint32_t e = max(top & 0xffffu, top >> 16) >> 7;   // the largest's exponent: 2^(e - 127)
     if (pass || !active || (e >= 121u && e < 136u)) return inv;
-    const uint32_t k = max(e, 75u);                          // (a row below 2^-52 counts as that: its scores are nothing either way)
+    const uint32_t k = max(e, 15u);                          // (as far as the power stays a number)
     f = __uint_as_float((268u - k) << 23);
     inv = __uint_as_float((k - 14u) << 23);
   }
@@ -619,8 +619,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
           float sc = next;
           next = scale_of(p, ts, page, j + 1, lane);
           page = scale_page(p, ts, j + 2, lane);
-          // (a key scale of zero: 2^-60, so that -inf times it, and c, stays -inf)
-          sc = fmaxf(sc, lane & 8 ? kLeastScale : 8.673617379884035e-19f);
+          if (lane & 8) sc = fmaxf(sc, kLeastScale);
           const float lv = __shfl_down_sync(0xffffffffu, log2f(sc), 8), rv = __shfl_down_sync(0xffffffffu, 1.f / sc, 8);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
@@ -910,8 +909,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
       warp_arrive(B_Q_READY);
       const int pos = !active ? -1 : p.causal ? u.nkv - u.nq + i : u.nkv - 1;   // last key this row sees
       const int pos_min = __reduce_min_sync(0xffffffffu, active ? pos : 0x7fffffff);
-      // positive, so that -inf * c stays -inf; with a scale of zero every score still rounds to weight 1
-      const float c = BLOCK ? fmaxf(q_inv * p.sm_log2, 8.673617379884035e-19f) : active ? fmaxf(p.q_scale[hh] * p.k_scale[u.g] * p.sm_log2, 1e-37f) : 1.f;
+      // positive, so that -inf * c stays -inf; with a scale of zero every score still rounds to weight 1 (block-scaled: by group)
+      const float c = BLOCK ? q_inv * p.sm_log2 : active ? fmaxf(p.q_scale[hh] * p.k_scale[u.g] * p.sm_log2, 1e-37f) : 1.f;
       float m_run = -CUDART_INF_F, l_run = 0.f;
       for (int st = 0; st < mine && ok; ++st) {
         const uint32_t ph = done + (uint32_t)st;
@@ -924,11 +923,12 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
         if (warp_active) {
           tc_fence_after();
           const int t0 = tile_of(st) * kKeys;                 // the tile's first key
-          // factor and summand of group k's scores, and the inverse of its value scale
+          // factor and summand of group k's scores, and the inverse of its value scale.  The factor is positive, so that a
+          // masked score's -inf times it stays -inf: a row's scores before it are below 2^29, so 1e-37 of them is as good as 0.
           const uint32_t scales = sbase + OFF_SCALES + (2 * x + (ph & 1u)) * 128u;
           auto group = [&](uint32_t k) {
             const uint4 v = lds128(scales + 16 * k);
-            return make_float3(__uint_as_float(v.x) * c, __uint_as_float(v.y), __uint_as_float(v.z));
+            return make_float3(fmaxf(__uint_as_float(v.x) * c, 1e-37f), __uint_as_float(v.y), __uint_as_float(v.z));
           };
           if (t0 + kKeys - 1 > pos_min) {
             // some active row of the warp does not see all keys: their scores become -inf

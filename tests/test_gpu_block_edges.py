@@ -182,3 +182,25 @@ def test_weights_of_small_rows_beside_large_ones(Hq, Hkv, q_lens, kv_lens, large
     lse = _lse(c)
     before = (rng.random((c["num"], Hkv, 64)) * 0.01).astype(np.float32)
     _within(_weigh(F, c, lse, before), *_weight_bounds(c, lse, before))
+
+
+# ------------------------------------------------------------ scales far from one
+@pytest.mark.parametrize("Hq,Hkv,q_lens,kv_lens", [(8, 2, [1, 1, 1], [300, 2, 129]), (8, 1, [4, 4], [900, 33]),
+                                                   (8, 2, [200, 40, 130], [700, 129, 130]), (8, 2, [30, 25], [400, 25])])
+@pytest.mark.parametrize("block", [16, 32, 128])
+@pytest.mark.parametrize("exponent", [-95, -84, -60, 45, 75, 90])
+def test_attention_of_key_scales_and_queries_that_make_up_for_one_another(Hq, Hkv, q_lens, kv_lens, block, exponent):
+    """Queries 2^exponent as large and key scales 2^-exponent: the scores are ordinary, with half of the rows and the
+    blocks' scales (the last block's aside) as far the other way, whose scores are next to nothing."""
+    F, rng = fa3(), np.random.default_rng(86)
+    c = _rows(rng, _cache(rng, kv_lens, 128, block, Hkv), q_lens, Hq)
+    c["q"] = np.ldexp(c["q"], exponent).astype(np.float32)
+    c["ks"] = np.ldexp(c["ks"], -exponent).astype(np.float32)
+    out, lse = _attend(F, c)
+    _check_attention(c, out, lse)
+    some = rng.random(c["ks"].shape) < 0.3
+    c["ks"][some & np.isfinite(c["ks"])] *= np.float32(2.0 ** -20)
+    c["q"][::2] *= np.float32(2.0 ** -10)
+    c["q"] = _f(_bf(c["q"]))
+    out, lse = _attend(F, c)
+    _check_attention(c, out, lse)
