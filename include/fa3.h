@@ -570,6 +570,7 @@ int fa3_attn_gqa_block_paged(const uint16_t* q, const int8_t* k_cache, const int
  * every run; a page that sequences share gets both their sums, in either order.
  * A row with NaN in its query or its log-sum-exp gives NaN to the tokens that it sees.
  * An entry outside the pool sets FA3_DEVERR_PAGE; its tokens get nothing.
+ * k_scale * softmax_scale below 2^-98 may count as that (of no weight with queries below 2^60).
  * Supported: as fa3_attn_gqa_block_paged; q_stride >= Hq * D; weights 4-byte aligned.
  * workspace  fa3_attn_weights_workspace_size() bytes, 16-byte aligned, not initialised;
  *          calls that may run at the same time need one each. */

@@ -288,12 +288,14 @@ __device__ __forceinline__ void three_parts(float x, uint32_t (&p)[3]) {
     x -= __uint_as_float(p[i] << 16);
   }
 }
-// The factor of a key's scores: not so small that its inverse leaves float32's range (a smaller one gives every score 0 as well).
+// The factor of a key's scores: not so small that its inverse times kMostLse leaves float32's range (with queries below 2^60, a
+// smaller one gives every score 0 as well).
+constexpr float kLeastFactor = 3.1554436208840472e-30f;      // 2^-98
 __device__ __forceinline__ float key_factor(const WeightParams& p, int page, int at, int g) {
   const float ks = (uint32_t)page < (uint32_t)p.pg.num_pages
                        ? p.ks[((int64_t)page * p.pg.per_page + divu32((uint32_t)at, p.pg.div_block)) * p.pg.Hkv + g]
                        : 0.f;                                 // outside the pool: the keys' loader reports it
-  return fmaxf(ks * p.sm_log2, 8.673617379884035e-19f);      // 2^-60
+  return fmaxf(ks * p.sm_log2, kLeastFactor);
 }
 
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* tm, int c0, int c1, int c2, uint32_t bar) {

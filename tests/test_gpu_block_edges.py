@@ -204,3 +204,16 @@ def test_attention_of_key_scales_and_queries_that_make_up_for_one_another(Hq, Hk
     c["q"] = _f(_bf(c["q"]))
     out, lse = _attend(F, c)
     _check_attention(c, out, lse)
+
+
+@pytest.mark.parametrize("Hq,Hkv,q_lens,kv_lens", WEIGHT_SHAPES)
+@pytest.mark.parametrize("exponent", [-84, 45, 60])
+def test_weights_of_key_scales_and_queries_that_make_up_for_one_another(Hq, Hkv, q_lens, kv_lens, exponent):
+    F, rng = fa3(), np.random.default_rng(87)
+    c = _rows(rng, _cache(rng, kv_lens, 64, 32, Hkv), q_lens, Hq)
+    c["q"] = np.ldexp(c["q"], exponent).astype(np.float32)
+    c["ks"] = np.ldexp(c["ks"], -exponent).astype(np.float32)
+    c["ks"][(rng.random(c["ks"].shape) < 0.2) & np.isfinite(c["ks"])] = 0
+    lse = _lse(c)
+    before = (rng.random((c["num"], Hkv, 64)) * 0.01).astype(np.float32)
+    _within(_weigh(F, c, lse, before), *_weight_bounds(c, lse, before))
