@@ -6,7 +6,7 @@ d (a score's error) and by what its exponent's parts lose.  Those are f = fl(k_s
 fl(lse log2 e) and, in the kernel that takes it through the product, fl(1 / f), two of |lse|; and there the tensor pipe's last
 sum of nine terms, each cut off below 2^-24 of the greatest, |lse|: 16 U (|s| + |lse| + 1) holds them, U = 2^-24, and 4 U for
 the exponential.  Where that is no small number e, the term lies within exp(+-e).  64 additions a step and the compensated
-sum of steps: 68 U of the sum.
+sum of steps: 68 U of the sum.  A term below 2^-126, float32's smallest normal number, may be lost: 2^-126 for each.
 """
 import numpy as np
 import pytest
@@ -14,7 +14,7 @@ import torch
 
 from helpers import fa3
 from oracle import fa3_oracle as O
-from test_gpu_block import SM, U, _attend, _bf, _cache, _check_attention, _f, _rows, _score_error, _t, _weigh
+from test_gpu_block import ATTN, SM, U, _attend, _bf, _cache, _check_attention, _f, _rows, _score_error, _t, _weigh
 
 pytestmark = pytest.mark.gpu
 
@@ -36,7 +36,7 @@ def _weight_bounds(c, lse, before, sm=SM):
         if h % g == 0:
             ref[at] = np.where(t >= len(t) - (rows.stop - rows.start), 0.0, ref[at])
         ref[at] += term.sum(0)
-        tol[at] += off.sum(0) + 68 * U * term.sum(0)
+        tol[at] += off.sum(0) + 68 * U * term.sum(0) + len(term) * 2.0 ** -126
     return ref, tol + np.abs(ref) * 2 * U
 
 
@@ -216,4 +216,49 @@ def test_weights_of_key_scales_and_queries_that_make_up_for_one_another(Hq, Hkv,
     c["ks"][(rng.random(c["ks"].shape) < 0.2) & np.isfinite(c["ks"])] = 0
     lse = _lse(c)
     before = (rng.random((c["num"], Hkv, 64)) * 0.01).astype(np.float32)
+    _within(_weigh(F, c, lse, before), *_weight_bounds(c, lse, before))
+
+
+# ------------------------------------------------------------ shapes that no other test has
+@pytest.mark.parametrize("Hq,Hkv,q_lens,kv_lens", [(28, 4, [700, 1], [1900, 300]), (24, 2, [500], [2100]), (24, 8, [600], [600]),
+                                                   (40, 8, [300, 200], [900, 1300])])
+def test_weights_of_prompts_in_groups_that_do_not_divide_128(Hq, Hkv, q_lens, kv_lens):
+    F, rng = fa3(), np.random.default_rng(88)
+    c = _rows(rng, _cache(rng, kv_lens, 64, 64, Hkv), q_lens, Hq)
+    lse = _lse(c)
+    before = (rng.random((c["num"], Hkv, 64)) * 0.01).astype(np.float32)
+    got = _weigh(F, c, lse, before)
+    _within(got, *_weight_bounds(c, lse, before))
+    assert np.array_equal(got, _weigh(F, c, lse, before))
+
+
+@pytest.mark.parametrize("q_lens", [[1, 1], [60, 30], [300, 5]])
+def test_tables_far_wider_than_the_contexts(q_lens):
+    """A table for 2^30 tokens a sequence: plans in 64 bits, whichever kernel."""
+    F, rng = fa3(), np.random.default_rng(89)
+    page, wide = 16384, 65536
+    lens = [600, 320]
+    c = _rows(rng, _cache(rng, lens, page, 32, 1, spare=2, extra=1), q_lens, 8)
+    table = np.full((2, wide), -1, np.int32)
+    table[:, 0] = c["table"][:, 0]
+    c["table"] = table
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = _attend(F, c, err)
+    _check_attention(c, out, lse)
+    before = (rng.random((c["num"], 1, page)) * 0.01).astype(np.float32)
+    got = _weigh(F, c, lse, before, err)
+    _within(got, *_weight_bounds(c, lse, before))
+    assert err.item() == 0
+
+
+@pytest.mark.parametrize("Hq,Hkv,page,block,q_lens,kv_lens", ATTN)
+@pytest.mark.parametrize("mixed", [False, True])
+def test_weights_within_the_bounds_of_their_own_rows(Hq, Hkv, page, block, q_lens, kv_lens, mixed):
+    F, rng = fa3(), np.random.default_rng(90)
+    c = _rows(rng, _cache(rng, kv_lens, page, block, Hkv), q_lens, Hq, lead=1)
+    if mixed:
+        n = c["q"].shape[0]
+        c["q"] *= np.exp2(np.resize([0, -40, 9, -7, 5, -70, -3], n * Hq)).reshape(n, Hq, 1).astype(np.float32)
+    _, lse = _attend(F, c)
+    before = (rng.random((c["num"], Hkv, page)) * 0.01).astype(np.float32)
     _within(_weigh(F, c, lse, before), *_weight_bounds(c, lse, before))
