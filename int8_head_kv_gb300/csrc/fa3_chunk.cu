@@ -924,11 +924,11 @@ __global__ void __launch_bounds__(kThreadsC, 1) gqa_chunk_kernel(const __grid_co
           tc_fence_after();
           const int t0 = tile_of(st) * kKeys;                 // the tile's first key
           // factor and summand of group k's scores, and the inverse of its value scale.  The factor is positive, so that a
-          // masked score's -inf times it stays -inf: a row's scores before it are below 2^29, so 1e-37 of them is as good as 0.
+          // masked score's -inf times it stays -inf: 1e-37 is nothing beside one that counts (scores before it are below 2^29).
           const uint32_t scales = sbase + OFF_SCALES + (2 * x + (ph & 1u)) * 128u;
           auto group = [&](uint32_t k) {
             const uint4 v = lds128(scales + 16 * k);
-            return make_float3(fmaxf(__uint_as_float(v.x) * c, 1e-37f), __uint_as_float(v.y), __uint_as_float(v.z));
+            return make_float3(fmaf(__uint_as_float(v.x), c, 1e-37f), __uint_as_float(v.y), __uint_as_float(v.z));
           };
           if (t0 + kKeys - 1 > pos_min) {
             // some active row of the warp does not see all keys: their scores become -inf
