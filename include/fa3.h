@@ -566,7 +566,8 @@ int fa3_attn_gqa_block_paged(const uint16_t* q, const int8_t* k_cache, const int
  *   sum over rows q_start[b] + i of b with t <= kv_lens[b] - n_b + i and heads h of g of exp(s[t] - lse[row, h])
  * is added to its weight; a token of this call's new rows begins with nothing.  q, k_cache, k_scale
  * and softmax_scale as for the attention call, whose lse it takes: a row then gives every head's
- * tokens 1 in all.  Sequences without new rows keep their weights.  The sums are the same on
+ * tokens 1 in all.  Sequences without new rows keep their weights, and tokens that were never new
+ * rows of such a call have what their page held.  The sums are the same on
  * every run; a page that sequences share gets both their sums, in either order.
  * A row with NaN in its query or its log-sum-exp gives NaN to the tokens that it sees.
  * An entry outside the pool sets FA3_DEVERR_PAGE; its tokens get nothing.

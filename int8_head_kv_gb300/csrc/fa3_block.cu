@@ -224,7 +224,9 @@ __global__ void __launch_bounds__(kAppendThreads) block_append_kernel(const __gr
 //
 // The choice is a radix selection by one block a head and sequence: 16 contexts of 4096 tokens and 8 heads take 8.8 us, three of
 // up to 20001 tokens and 5 heads 13.0 (15 blocks: latency, barriers and instructions, far from HBM).  A cluster of blocks a head
-// was slower.
+// was slower.  Contexts beyond kMostKeys are read again for each digit (a whole call on one of 49000 tokens, 8 heads: 35 us, of 60000
+// 72, of 100000 110).  Shared memory goes by the table's width, the lengths being on the device: one block an SM instead of
+// two from 20000 tokens on (128 contexts of 2048 cut to 1024: 164 us, with a table for 131072 tokens 184).
 constexpr int kPickThreads = 1024;
 constexpr int kDigitBits = 11, kBins = 1 << kDigitBits;
 constexpr int kMostKeys = 48 * 1024;                       // of a context that shared memory holds

@@ -58,7 +58,7 @@
 // of keys the key scale is a factor of the exponent, x = S k_scale softmax_scale log2(e) + log2(v_scale),
 // so that V's bare codes are the operand of P.V, and the row sum takes P / v_scale.  Warp 2
 // writes a step's scales, their logarithms and inverses, to shared memory, two steps ahead.  4096 rows on
-// 8192 keys: 736 us, 1121 TFLOP/s, 8 % more than with one scale a head (blocks of 32 or 64: 751 us): the softmax
+// 8192 keys: 733 us, 1125 TFLOP/s, 7 % more than with one scale a head (blocks of 32 or 64: 757 us): the softmax
 // warps, the longest link of the chain, wait for the scales, and read one for each group.  Batches of few
 // rows a sequence take fa3_few.cu's kernels (16 one-token rows of 4096 keys: 29.5 us there).
 //
@@ -1288,7 +1288,7 @@ int chunk_attn(ChunkParams& p, int D, float softmax_scale, void* workspace, size
     return FA3_ECUDA;
   const LaunchTogether together(s);
   // a block's keys in groups of 128 or 32 where its size allows it, of 16 otherwise (4096 rows on 8192 keys, blocks of 128:
-  // 736 us with groups of 128, 751 of 32, 788 of 16)
+  // 733 us with groups of 128; blocks of 32 or 64: 757 of 32; blocks of 16: 797)
   const int block = BLOCK ? p.page_size / p.per_page : 0;
   const int st_main = !BLOCK            ? launch_chunk<0>(p, sms, s)
                       : block % kKeys == 0 ? launch_chunk<kKeys>(p, sms, s)

@@ -889,7 +889,10 @@ cudaError_t launch(FewParams& p, void* workspace, cudaStream_t s) {
 bool few_rows(int n, int B, int Hkv, int G, int T_max) {
   const double units = (double)n + B;
   // Up to 32 columns a sequence: 16 sequences of 4096 keys, 64 query and 8 KV heads, with 1, 2, 3, 4 and 5 rows each take 29.5, 33, 45,
-  // 46 and 78 us here, and 58 to 61 in fa3_chunk.cu's kernel.
+  // 46 and 78 us here, and 58 to 61 in fa3_chunk.cu's kernel.  The lengths are on the device, so the rule goes by the call's average,
+  // and was measured on calls of equal sequences.  A chunk beside many single tokens is the wrong way round for one of them: 512
+  // rows beside 128 tokens (4 rows on average, all here) take 517 us, the parts by themselves 82 (there) and 181 (here); beside 64
+  // (8 rows, all there) 248, by themselves 82 and 96.
   return G <= 16 && columns_of(n, B, G) <= 32 && units * Hkv * (T_max / kStep + kUnitSteps + 1.0) < 2147483648.0;
 }
 size_t few_rows_workspace(int n, int B, int G, int sms) {
@@ -913,7 +916,8 @@ cudaError_t few_rows_attn(const FewCall& c, const int32_t* table, int num_pages,
 bool few_rows_weights(int n, int B, int Hkv, int G, int T_max) {
   const double chunks = (double)n / (kChunkCols / std::min(G, kChunkCols)) + B;
   // Up to some 96 columns a sequence: 16 sequences of 4096 keys, 64 query and 8 KV heads, with 1, 4, 8 and 16 rows each take
-  // 17.6, 24.8, 36.0 and 64.7 us here and 50.7, 51.1, 52.5 and 51.6 in fa3_weights.cu's kernel.
+  // 17.6, 24.8, 36.0 and 64.7 us here and 50.7, 51.1, 52.5 and 51.6 in fa3_weights.cu's kernel.  By the call's average, as above:
+  // 512 rows beside 64 single tokens (9 rows on average, all here) take 473 us, by themselves 42 (there) and 53 (here).
   return G <= kChunkCols && (int64_t)n * G <= (int64_t)96 * B &&
          Hkv * ((double)B * kWUnit + chunks * (T_max / kStep + 1.0)) < 2147483648.0;
 }

@@ -28,7 +28,9 @@
 //
 // What bounds it (64 query and 8 KV heads, one GB300).  4096 new rows on a context of 8192: 312 us, 1320 TFLOP/s (exponentials
 // not counted).  The tensor pipe is active for 45 % of the time; the warps that sum, each row tile's four, wait for TMEM,
-// multiply, exponentiate and add, and are busy for 80 %.  With few columns a unit's keys are what costs (their way to shared
+// multiply, exponentiate and add, and are busy for 80 %.  Their fast loop is for steps of 128 columns, that is groups that divide
+// 128 and calls with rows enough on average; in other groups every step is read with its mask, 680 to 730 TFLOP/s (56 query
+// and 8 KV heads: 493 us, 24 and 8: 225, 28 and 4: 254).  With few columns a unit's keys are what costs (their way to shared
 // memory as bf16, some 8 us a unit): 16 contexts of 4096 keys take 51 us with 8 columns each as with 128, so few columns go to
 // fa3_few.cu's kernel.
 //
