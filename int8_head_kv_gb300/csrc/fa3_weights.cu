@@ -11,11 +11,11 @@
 // The row's log-sum-exp goes into the product as well: with f the key's factor (its scale, softmax_scale and log2(e)), the exponent
 // is f (S - lse / f), and lse / f is a product of a number of the key's and one of the column's.  Both are split into
 // three bf16 parts, exactly, and the eight products of parts that count (what is left out is below 2^-31 of it) are one more
-// slice of the contraction.  It is the last, and taken relative to the lse of the step's first column (a common one's: below 64),
-// which the exponent gets in float32: the tensor pipe cuts its sums off relative to their largest term, which lse / f would be (weights of 4096
-// rows on 8192 keys were off by 1.5e-6 of them in the mean with all of it as the first slice, 6e-7 as the last, 1.2e-7 so;
-// 308, 309 and 312 us).  A thread then reads little but its scores: with the log-sum-exps in shared memory, each warp reading
-// them anew, that memory was the bound (4460 cycles for 512 keys x 128 columns; the MMAs alone take 2048).
+// slice of the contraction.  It is the last, and taken relative to the lse of the step's first column, where that is a common
+// number, which the exponent gets in float32: the tensor pipe cuts its sums off relative to their largest term, which
+// lse / f would be (weights of 4096 rows on 8192 keys were off by 1.5e-6 of them in the mean with all of it as the first slice,
+// 6e-7 as the last, 1.2e-7 so; 308, 309 and 312 us).  A thread then reads little but its scores: with the log-sum-exps in shared
+// memory, each warp reading them anew, that memory was the bound (4460 cycles for 512 keys x 128 columns; the MMAs alone take 2048).
 //
 // Work.  A unit is 512 keys of one sequence and KV head, as four row tiles; a step is the scores of P new tokens x G heads
 // (up to 128 columns) with all four.  All units lie on one line that is cut into equal parts, one per SM; a cut unit's
